@@ -82,6 +82,8 @@ typedef void* pkv_stream_t;
 #define PKV_DEVERR_DUPLICATE_SLOT 0x80u /* checked append: a slot named twice; nothing written */
 #define PKV_DEVERR_PREFIX_MISMATCH 0x100u /* shared-prefix decode: a member's prefix is not its
                                              group's (or is out of range); decoded without it */
+#define PKV_DEVERR_BAD_POSITION 0x200u  /* position outside the rotation table: token skipped */
+#define PKV_DEVERR_BAD_TREE 0x400u      /* drafted tree's parent, or accepted path, out of order */
 
 /*
  * pkv_kv_append -- scatter new K/V rows into the paged pools.
@@ -615,6 +617,167 @@ PKV_API int pkv_paged_verify_attention_bf16out(const void* q, int num_seqs, int 
                                                float scale, void* out, void* workspace,
                                                size_t ws_bytes, int partition_blocks,
                                                pkv_stream_t stream);
+
+/*
+ * The speculative step with a tree of drafted tokens ("Cache KV, attention et
+ * optimisation de l'inference", section "Decodage speculatif": guess several
+ * next tokens cheaply, then check them all in one pass; here the guesses
+ * branch).  The n nodes of a sequence's tree are appended as the last n
+ * positions of its context, in the order they were drafted (a parent before
+ * its children), and checked in one pass:
+ *   pkv_bm_reserve_draft          slots for the nodes           (pagedkv_blocks.h)
+ *   pkv_draft_tree_layout         ancestor masks and positions
+ *   pkv_qk_norm_rope_append       each layer: q, k rotated, k and v appended
+ *   pkv_paged_tree_attention      each layer
+ *   pkv_kv_accept_rows            the accepted path's rows move up
+ *   pkv_bm_commit_draft           the accepted tokens join the sequence
+ * Ragged batches: sequence s's nodes are rows q_start[s] .. q_start[s+1] - 1
+ * of the packed arrays, 0 to 64 of them; a single node is a plain decode.
+ *
+ * pkv_qk_norm_rope_append -- per-head RMS norm and rotary embedding of new
+ * queries and keys, and the append of keys and values, in one pass (for any
+ * new tokens: prompt chunks, decodes or drafts).  For a head x of d elements
+ * of token t,
+ *   y = x * rsqrt(mean(x^2) + eps) * weight   (y = x when the weight is NULL)
+ * and the first rot_dim elements of y turn in pairs (a, b) -> (a c - b s,
+ * b c + a s) with c = rope_table[p][i], s = rope_table[p][rot_dim / 2 + i],
+ * p = positions[t]: pair i is elements (i, i + rot_dim / 2), or (2 i, 2 i + 1)
+ * when interleaved is nonzero.  All in float32 from the bf16 inputs, rounded
+ * once: q_out bf16, K as stored in the pool, V copied.
+ *   q            : [num_tokens][q_heads][d_head] bf16, token t at element
+ *                  t * q_tok_stride; k, v : [num_tokens][kv_heads][d_head]
+ *                  likewise -- views of one fused projection are accepted.
+ *                  Bases 16-byte aligned, strides multiples of 8 elements.
+ *   positions    : [num_tokens] int64 in [0, max_positions).  A token outside
+ *                  is skipped whole (q_out and caches keep what they held) and
+ *                  PKV_DEVERR_BAD_POSITION is set.
+ *   rope_table   : [max_positions][rot_dim] float32, 16-byte aligned: cosines,
+ *                  then sines.
+ *   rot_dim      : a multiple of 16, 16 .. d_head (PKV_EUNSUPPORTED otherwise);
+ *                  the other elements pass through.
+ *   q_weight, k_weight : [d_head] bf16, 16-byte aligned, or NULL (no norm).
+ *   slot_mapping : as in pkv_kv_append; a token with slot -1 gets its q_out
+ *                  row and no cache row.  Two tokens with one slot race.
+ *   q_out        : [num_tokens][q_heads][d_head] bf16, contiguous, 16-byte
+ *                  aligned; must not overlap q, k or v (PKV_EINVAL).
+ * d_head 64 or 128; any q_heads.  No workspace.
+ *
+ * pkv_qk_norm_rope_append_fp8 -- the same into FP8 pools: the float32 values
+ * of K and V times 1 / scale, rounded once to e4m3 (to nearest even, finite
+ * overflow to +-448), as pkv_kv_append_fp8 stores them.
+ */
+PKV_API int pkv_qk_norm_rope_append(const void* q, int64_t q_tok_stride, const void* k,
+                                    int64_t k_tok_stride, const void* v, int64_t v_tok_stride,
+                                    int64_t num_tokens, int q_heads, const int64_t* positions,
+                                    const float* rope_table, int64_t max_positions, int rot_dim,
+                                    int interleaved, const void* q_weight, const void* k_weight,
+                                    float eps, const int64_t* slot_mapping, void* q_out,
+                                    void* k_cache, void* v_cache, pkv_cache_desc cache,
+                                    pkv_stream_t stream);
+PKV_API int pkv_qk_norm_rope_append_fp8(const void* q, int64_t q_tok_stride, const void* k,
+                                        int64_t k_tok_stride, const void* v, int64_t v_tok_stride,
+                                        int64_t num_tokens, int q_heads, const int64_t* positions,
+                                        const float* rope_table, int64_t max_positions,
+                                        int rot_dim, int interleaved, const void* q_weight,
+                                        const void* k_weight, float eps,
+                                        const int64_t* slot_mapping, void* q_out, void* k_cache,
+                                        void* v_cache, pkv_cache_desc cache, float k_scale,
+                                        float v_scale, pkv_stream_t stream);
+
+/*
+ * pkv_draft_tree_layout -- the ancestor masks and positions of drafted trees.
+ *   parents      : [total_q] int32; parents[q_start[s] + t] is node t's parent
+ *                  in its own sequence's numbering, -1 <= parent < t (-1: a
+ *                  child of the last committed token).  Any other value counts
+ *                  as -1 and sets PKV_DEVERR_BAD_TREE.
+ *   context_lens : [num_seqs] int32, the tree included.
+ *   max_q_len    : host bound on a tree's nodes, at most 64 (PKV_EUNSUPPORTED).
+ *   tree_mask    : [total_q] uint64 out; bit u of node t's word: u is t or an
+ *                  ancestor of t.
+ *   positions    : [total_q] int64 out: context_len - n + depth, a root's depth
+ *                  being 0 (what pkv_qk_norm_rope_append takes).
+ * A sequence with a q_start that is not monotone or beyond total_q, more than
+ * max_q_len nodes or fewer context positions than nodes is left out (nothing of it is
+ * written; PKV_DEVERR_BAD_QUERY_RANGE).
+ */
+PKV_API int pkv_draft_tree_layout(const int32_t* parents, const int32_t* q_start, int num_seqs,
+                                  int total_q, int max_q_len, const int32_t* context_lens,
+                                  uint64_t* tree_mask, int64_t* positions, pkv_stream_t stream);
+
+/*
+ * pkv_paged_tree_attention -- each node of the drafted trees attends over the
+ * committed keys of its sequence and over the nodes of its mask:
+ *   out[r, h] = softmax over keys j < context_len - n, and keys
+ *               context_len - n + u with bit u of tree_mask[r]
+ * (softmax(q K^T * scale + mask) V, "Optimisation de l'inference", "Etape 2",
+ * the mask that of the tree).  Any mask is taken, not only a tree's; bits from
+ * n on are ignored, and a row that sees no key is zero.  A node that a row
+ * does not see never reaches it, whatever its K and V rows hold (NaN and
+ * infinities included).
+ *   q            : [total_q][q_heads][d_head] bf16, contiguous, 16-byte aligned.
+ *   q_start, max_q_len, context_lens : as in pkv_draft_tree_layout; a sequence
+ *                  outside those bounds, or with a context beyond the block
+ *                  table, is rejected: none of its rows is written and
+ *                  PKV_DEVERR_BAD_QUERY_RANGE is set.
+ *   out          : [total_q][q_heads][d_head] float32, 16-byte aligned; rows
+ *                  outside every tree are not written.
+ *   workspace    : >= pkv_tree_attention_workspace_bytes(...) device bytes,
+ *                  256-byte aligned (PKV_ENOMEM if NULL or smaller), contents
+ *                  need no initialisation; calls that share it must be ordered
+ *                  on the GPU.  Its size depends on the current device.
+ * Other arguments, shapes and errors are those of pkv_paged_prefill_attention.
+ * Context lengths are read on the device only: no host bound is needed, and a
+ * captured call may be replayed with other lengths, trees and tables.
+ * pkv_paged_tree_attention_bf16out rounds the float32 result once to bf16
+ * (ties to even), bit for bit; out is then 16-byte aligned bf16.
+ */
+PKV_API size_t pkv_tree_attention_workspace_bytes(int num_seqs, int max_q_len, int q_heads,
+                                                  int kv_heads, int d_head);
+PKV_API int pkv_paged_tree_attention(const void* q, const int32_t* q_start, int num_seqs,
+                                     int total_q, int max_q_len, int q_heads,
+                                     const uint64_t* tree_mask, const void* k_cache,
+                                     const void* v_cache, pkv_cache_desc cache,
+                                     const int32_t* block_tables, int max_blocks_per_seq,
+                                     const int32_t* context_lens, float scale, float* out,
+                                     void* workspace, size_t ws_bytes, pkv_stream_t stream);
+PKV_API int pkv_paged_tree_attention_bf16out(const void* q, const int32_t* q_start, int num_seqs,
+                                             int total_q, int max_q_len, int q_heads,
+                                             const uint64_t* tree_mask, const void* k_cache,
+                                             const void* v_cache, pkv_cache_desc cache,
+                                             const int32_t* block_tables, int max_blocks_per_seq,
+                                             const int32_t* context_lens, float scale, void* out,
+                                             void* workspace, size_t ws_bytes,
+                                             pkv_stream_t stream);
+
+/*
+ * pkv_kv_accept_rows -- after a path of each tree is accepted, its K and V
+ * rows move up behind the committed ones: in every layer's pools the row at
+ * position context_len - n + accepted[s][i] is copied to position
+ * context_len - n + i, for i < num_accepted[s], and new_context_lens[s] =
+ * context_len - n + num_accepted[s].  In place, bit for bit, as if every row
+ * were read before any is written; rows behind the accepted ones keep what
+ * they held.
+ *   k_cache, v_cache : the first layer's pools; layer l's start l *
+ *                  k_layer_stride (v_layer_stride) elements on (ignored for
+ *                  one layer; else at least a pool, a multiple of 16 bytes).
+ *   elem_bytes   : 2 (bf16 pools) or 1 (FP8).
+ *   accepted     : [num_seqs][max_accepted] int32, strictly increasing node
+ *                  numbers in [0, n) (a root-to-leaf path is).
+ *   num_accepted : [num_seqs] int32 in [0, min(max_accepted, n)].
+ *   new_context_lens : [num_seqs] int32 out; must not overlap an input.
+ * The pages that hold a tree belong to its sequence alone (as after
+ * pkv_bm_reserve_draft).  A path that breaks these rules, a tree of more than
+ * 64 nodes or a context beyond the block table leaves its sequence's rows and
+ * length as they were and sets PKV_DEVERR_BAD_TREE; a block id outside the
+ * pool skips the row and sets PKV_DEVERR_BAD_BLOCK_ID.
+ */
+PKV_API int pkv_kv_accept_rows(void* k_cache, int64_t k_layer_stride, void* v_cache,
+                               int64_t v_layer_stride, int num_layers, pkv_cache_desc cache,
+                               int32_t elem_bytes, const int32_t* block_tables,
+                               int max_blocks_per_seq, const int32_t* context_lens,
+                               const int32_t* q_start, int num_seqs, const int32_t* accepted,
+                               int max_accepted, const int32_t* num_accepted,
+                               int32_t* new_context_lens, pkv_stream_t stream);
 
 /*
  * FP8 KV cache.  The pages name FP8 KV caches as the way to halve decode's

@@ -78,10 +78,33 @@ PKV_API int pkv_bm_append_tokens(pkv_block_manager* bm, int64_t seq_id, const in
                                  int32_t num_tokens, int64_t* slots, int32_t* copy_pairs,
                                  int32_t max_copies, int32_t* num_copies);
 
+/* Reserves positions [len, len + num_nodes) of seq_id for the nodes of a tree
+ * of drafted tokens ("Cache KV, attention...", section "Decodage
+ * speculatif"): their slots go to slots[0 .. num_nodes), with the
+ * copy-on-write pair of pkv_bm_append_tokens if the last block is partly
+ * filled and shared.  The sequence's length and its hashed blocks stay as they
+ * were: most nodes will be rejected.  Until pkv_bm_commit_draft, the blocks
+ * belong to the sequence, pkv_bm_block_tables reports the length with the
+ * draft, and appending to, forking or reserving again for seq_id returns
+ * PKV_EINVAL.  PKV_EINVAL also for an unknown seq_id, a NULL pointer,
+ * num_nodes <= 0 or no room for the copy pair; PKV_ENOBLOCKS if the pool is
+ * short (nothing is changed then). */
+PKV_API int pkv_bm_reserve_draft(pkv_block_manager* bm, int64_t seq_id, int32_t num_nodes,
+                                 int64_t* slots, int32_t* copy_pairs, int32_t max_copies,
+                                 int32_t* num_copies);
+
+/* Ends a draft: the accepted path's tokens token_ids[0 .. num_tokens) join the
+ * sequence (their rows moved up by pkv_kv_accept_rows; 0 rejects the whole
+ * draft), blocks that became full are hashed, and the draft's other blocks go
+ * back to the free list, last block first.  PKV_EINVAL for an unknown seq_id,
+ * no reserved draft, num_tokens < 0 or more tokens than reserved positions. */
+PKV_API int pkv_bm_commit_draft(pkv_block_manager* bm, int64_t seq_id, const int32_t* token_ids,
+                                int32_t num_tokens);
+
 /* child becomes a copy of parent that shares all of its blocks (each block's
  * reference count goes up by one); no block is copied until one of them
  * appends into a shared partial block.  PKV_EINVAL if parent is unknown or
- * child already exists. */
+ * has a reserved draft, or child already exists. */
 PKV_API int pkv_bm_fork(pkv_block_manager* bm, int64_t parent, int64_t child);
 
 /* Drops seq_id; blocks whose count reaches zero go to the back of the free
@@ -104,7 +127,8 @@ PKV_API int pkv_bm_block_table(const pkv_block_manager* bm, int64_t seq_id, int3
 
 /* Batch export in the layout the attention calls take: row s of
  * block_tables[num_seqs][max_blocks_per_seq] (int32, row-major) receives the
- * blocks of seq_ids[s], padded with 0, and context_lens[s] its length.
+ * blocks of seq_ids[s], padded with 0, and context_lens[s] its length (a
+ * reserved draft included).
  * PKV_EINVAL for an unknown id, or a sequence with more blocks than
  * max_blocks_per_seq (nothing is written then). */
 PKV_API int pkv_bm_block_tables(const pkv_block_manager* bm, const int64_t* seq_ids,

@@ -46,3 +46,11 @@ from .block_manager import (  # noqa: F401,E402
     copy_blocks,
     num_blocks_for_budget,
 )
+
+from .draft_tree import (  # noqa: F401,E402
+    norm_rope,
+    rope_table,
+    tree_layout,
+    tree_attention,
+    accept_rows,
+)

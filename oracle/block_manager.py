@@ -171,6 +171,47 @@ class BlockManager:
             self._register(blocks[j], s["last_hash"], chunk)
         return slots, copies
 
+    def reserve_draft(self, seq_id: int, num_nodes: int):
+        """Slots for a drafted tree behind the sequence and the copies to make
+        first; the tokens and hashes stay as they were until the commit."""
+        s = self.seqs[seq_id]
+        if num_nodes <= 0 or s.get("draft", 0):
+            raise ValueError("bad draft")
+        bs, L, blocks = self.bs, len(s["tokens"]), s["blocks"]
+        cow = L % bs != 0 and self.ref[blocks[-1]] > 1
+        want = -(-(L + num_nodes) // bs)
+        need = int(cow) + want - (-(-L // bs))
+        if need > len(self.free):
+            raise NoFreeBlocks(need)
+        copies = []
+        if cow:
+            old, new = blocks[-1], self._take_free()
+            self.ref[old] -= 1
+            blocks[-1] = new
+            copies.append((old, new))
+        while len(blocks) < want:
+            blocks.append(self._take_free())
+        s["draft"] = num_nodes
+        return self.slots(seq_id, L, num_nodes), copies
+
+    def commit_draft(self, seq_id: int, token_ids) -> None:
+        """The accepted tokens join; blocks beyond them are freed, last first."""
+        s = self.seqs[seq_id]
+        ids, bs, L = list(token_ids), self.bs, len(s["tokens"])
+        if not 0 < s.get("draft", 0) >= len(ids):
+            raise ValueError("bad commit")
+        s["draft"] = 0
+        while len(s["blocks"]) > -(-(L + len(ids)) // bs):
+            b = s["blocks"].pop()
+            self.ref[b] -= 1
+            if self.ref[b] == 0:
+                self.free.append(b)
+        s["tokens"].extend(ids)
+        for j in range(L // bs, (L + len(ids)) // bs):
+            chunk = s["tokens"][j * bs:(j + 1) * bs]
+            s["last_hash"] = block_hash(s["last_hash"], chunk)
+            self._register(s["blocks"][j], s["last_hash"], chunk)
+
     def fork(self, parent: int, child: int) -> None:
         if child in self.seqs:
             raise KeyError(f"sequence {child} exists")

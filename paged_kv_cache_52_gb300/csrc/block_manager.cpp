@@ -39,6 +39,7 @@ struct Sequence {
   std::vector<int32_t> blocks;
   std::vector<int32_t> tokens;
   uint64_t last_hash = kFnvOffset;  // hash of the last full block (chain state)
+  int32_t draft = 0;                // positions reserved behind the tokens
 };
 
 }  // namespace
@@ -187,6 +188,7 @@ int pkv_bm_append_tokens(pkv_block_manager* bm, int64_t seq_id, const int32_t* t
   auto it = bm->seqs.find(seq_id);
   if (it == bm->seqs.end()) return PKV_EINVAL;
   Sequence& s = it->second;
+  if (s.draft > 0) return PKV_EINVAL;
   const int32_t bs = bm->bs;
   const int64_t L = int64_t(s.tokens.size());
   if (L + num_tokens > INT32_MAX) return PKV_EINVAL;
@@ -225,10 +227,81 @@ int pkv_bm_append_tokens(pkv_block_manager* bm, int64_t seq_id, const int32_t* t
   return PKV_OK;
 }
 
+// Draft positions: blocks are taken as for an append, but no token joins the
+// sequence and nothing is hashed until the commit says which were accepted.
+int pkv_bm_reserve_draft(pkv_block_manager* bm, int64_t seq_id, int32_t num_nodes, int64_t* slots,
+                         int32_t* copy_pairs, int32_t max_copies, int32_t* num_copies) {
+  if (!bm || num_nodes <= 0 || !slots || !num_copies) return PKV_EINVAL;
+  auto it = bm->seqs.find(seq_id);
+  if (it == bm->seqs.end()) return PKV_EINVAL;
+  Sequence& s = it->second;
+  if (s.draft > 0) return PKV_EINVAL;
+  const int32_t bs = bm->bs;
+  const int64_t L = int64_t(s.tokens.size());
+  if (L + num_nodes > INT32_MAX) return PKV_EINVAL;
+  const bool cow = L % bs != 0 && bm->ref[s.blocks.back()] > 1;
+  if (cow && (max_copies < 1 || !copy_pairs)) return PKV_EINVAL;
+  const int32_t blocks = pkv_block_manager::ceil_div(L + num_nodes, bs);
+  const int32_t need = int32_t(cow) + blocks - pkv_block_manager::ceil_div(L, bs);
+  if (need > bm->free_count) return PKV_ENOBLOCKS;
+  try {
+    s.blocks.reserve(size_t(blocks));
+  } catch (const std::bad_alloc&) {
+    return PKV_ENOMEM;
+  }
+  *num_copies = 0;
+  if (cow) {
+    const int32_t old = s.blocks.back();
+    const int32_t fresh = bm->take_free();
+    --bm->ref[old];
+    s.blocks.back() = fresh;
+    copy_pairs[0] = old;
+    copy_pairs[1] = fresh;
+    *num_copies = 1;
+  }
+  while (int32_t(s.blocks.size()) < blocks) s.blocks.push_back(bm->take_free());
+  for (int32_t i = 0; i < num_nodes; ++i) {
+    const int64_t pos = L + i;
+    slots[i] = int64_t(s.blocks[size_t(pos / bs)]) * bs + pos % bs;
+  }
+  s.draft = num_nodes;
+  return PKV_OK;
+}
+
+int pkv_bm_commit_draft(pkv_block_manager* bm, int64_t seq_id, const int32_t* token_ids,
+                        int32_t num_tokens) {
+  if (!bm || num_tokens < 0 || (num_tokens > 0 && !token_ids)) return PKV_EINVAL;
+  auto it = bm->seqs.find(seq_id);
+  if (it == bm->seqs.end()) return PKV_EINVAL;
+  Sequence& s = it->second;
+  if (s.draft <= 0 || num_tokens > s.draft) return PKV_EINVAL;
+  const int32_t bs = bm->bs;
+  const int64_t L = int64_t(s.tokens.size());
+  try {
+    s.tokens.reserve(size_t(L + num_tokens));
+  } catch (const std::bad_alloc&) {
+    return PKV_ENOMEM;
+  }
+  s.draft = 0;
+  const size_t keep = size_t(pkv_block_manager::ceil_div(L + num_tokens, bs));
+  while (s.blocks.size() > keep) {
+    const int32_t b = s.blocks.back();
+    s.blocks.pop_back();
+    if (--bm->ref[b] == 0) bm->push_back_free(b);
+  }
+  s.tokens.insert(s.tokens.end(), token_ids, token_ids + num_tokens);
+  for (int64_t j = L / bs; j < (L + num_tokens) / bs; ++j) {
+    const int32_t* chunk = s.tokens.data() + size_t(j) * bs;
+    s.last_hash = chain_hash(s.last_hash, chunk, bs);
+    bm->register_block(s.blocks[size_t(j)], s.last_hash, chunk);
+  }
+  return PKV_OK;
+}
+
 int pkv_bm_fork(pkv_block_manager* bm, int64_t parent, int64_t child) {
   if (!bm || bm->seqs.count(child)) return PKV_EINVAL;
   auto it = bm->seqs.find(parent);
-  if (it == bm->seqs.end()) return PKV_EINVAL;
+  if (it == bm->seqs.end() || it->second.draft > 0) return PKV_EINVAL;
   try {
     Sequence copy = it->second;
     for (int32_t b : copy.blocks) ++bm->ref[b];
@@ -304,7 +377,7 @@ int pkv_bm_block_tables(const pkv_block_manager* bm, const int64_t* seq_ids, int
     int32_t* row = block_tables + size_t(s) * size_t(max_blocks_per_seq);
     for (int32_t j = 0; j < max_blocks_per_seq; ++j)
       row[j] = j < int32_t(q.blocks.size()) ? q.blocks[size_t(j)] : 0;
-    context_lens[s] = int32_t(q.tokens.size());
+    context_lens[s] = int32_t(q.tokens.size()) + q.draft;
   }
   return PKV_OK;
 }

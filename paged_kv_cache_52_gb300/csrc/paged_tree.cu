@@ -1,0 +1,976 @@
+// Attention of trees of drafted tokens over the paged KV cache: the
+// verification step of speculative decoding when the draft branches, on the
+// 5th-generation tensor cores (tcgen05 + tensor memory).
+//
+// What is computed: sequence s has L = context_len cached positions, of which
+// the last n <= 64 are the nodes of its tree.  Node t with ancestor mask M_t
+// attends the committed keys j < L - n and the nodes u with bit u of M_t:
+//   out[t, h] = sum_j p_j v_j,  p = softmax_j(scale q[t, h] . k_j)
+// (the prefill's softmax(q K^T scale + mask) V with a tree in place of the
+// causal triangle), GQA head h reading KV head h / G.  A row that sees no key
+// is zero.
+//
+// Design (GB300):
+//  * rows of a (sequence, KV head) pair are its n x G (node, head) rows,
+//    node-major, in tiles of 128 = the MMA's M; every K/V byte is read once
+//    for a tile pair.  The keys stream by in tiles of 128 (8 pages).
+//  * the work is cut by key tiles, not by sequences: the tiles of all items
+//    (pair, row group) laid end to end are divided evenly over one CTA per
+//    SM, so a batch of ragged contexts, or one long one, loads every SM
+//    alike.  A CTA's range covers parts of one or more items; an item that
+//    lies in one CTA is finished there, the pieces of a cut item (at most two
+//    per CTA) go through the workspace and a merge kernel by log-sum-exp.
+//  * TILES = 1 (at most 128 rows a pair): bound by HBM.  The two softmax
+//    warpgroups take the key tiles in turn, each with its own running max,
+//    sum and tensor-memory accumulator, so one works on its scores while the
+//    other's products run; at the end of an item each row's two halves are
+//    combined, both warpgroups reading both accumulators (half the columns
+//    each).  TILES = 2: bound by the tensor cores; warpgroup t owns row tile
+//    t and K/V tiles serve both.
+//  * warps 0-3 and 4-7 softmax, correction and epilogue (thread = row =
+//    tensor-memory lane), warp 8 loads K, 9 issues the MMAs, 10 loads V, 11
+//    loads Q.  The rings run on across items; only Q and the accumulators
+//    change hands at an item's end.
+//  * S = Q K^T lands in tensor memory, the softmax overwrites it with P as
+//    bf16 hi + lo (two MMAs a step, error ~2^-17: a row may see very few
+//    keys, where P rounded to one bf16 would move the output by 2^-9), and
+//    P V reads P from tensor memory.
+//  * only tiles that reach the tree apply a mask: 128 bits a row, made from
+//    the 64-bit ancestor mask.  A masked key's P is 0, but 0 * NaN is not:
+//    in those tiles every non-finite element of V is replaced by 0 in shared
+//    memory and added, in the epilogue, to just the rows that see its node,
+//    so a sibling's (or a stale row's) NaN or infinity reaches nobody else.
+//  * every wait is bounded; a timeout sets the error word and an abort flag,
+//    copies and MMAs in flight are drained and tensor memory is freed.
+#include <algorithm>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+#include "pkv_tcgen05.cuh"
+
+namespace pkv {
+
+static __device__ unsigned g_tree_error = 0;
+
+constexpr int kTrRows = 128;     // rows (node x head) per tile
+constexpr int kTrKeys = 128;     // keys per K/V tile (8 pages)
+constexpr int kTrMaxNodes = 64;  // nodes of a tree (bits of a mask)
+constexpr int kTrThreads = 384;
+constexpr int kTrSoftmaxThreads = 256;
+constexpr int kTrKWarp = 8, kTrMmaWarp = 9, kTrVWarp = 10, kTrQWarp = 11;
+constexpr uint32_t kTrTmemCols = 512;  // warpgroup w: S/P at 256 w, O at 256 w + 128
+constexpr float kTrRescale = 8.0f;     // log2 units: move the running max when it grows by > x256
+constexpr int kTrMaxStages = 8;
+
+template <int D, int TILES>
+struct TreeSmem {
+  static constexpr int kHalf = 128 * 128;  // 128 rows x 64 bf16
+  static constexpr int kTileBytes = (D / 64) * kHalf;
+  static constexpr int kQBytes = TILES * kTileBytes;
+  // ring stages: what 227 KB hold beside Q.  A V tile waits for its softmax, a
+  // K tile only for its product, so V gets the odd stage only if K has three.
+  static constexpr int kKStages = D == 64 ? 5 : 3;
+  static constexpr int kVStages = D == 64 ? 5 : (TILES == 1 ? 3 : 2);
+  static constexpr int kKOff = kQBytes;
+  static constexpr int kVOff = kKOff + kKStages * kTileBytes;
+  static constexpr int kXchOff = kVOff + kVStages * kTileBytes;  // [2][128] (max, sum)
+  static constexpr int kBarOff = kXchOff + 2 * kTrRows * 8;
+  static constexpr int kNumBars = 2 + 4 * kTrMaxStages + 6 + 3;
+  static constexpr int kMiscOff = kBarOff + kNumBars * 8;
+  // tensor-memory base, abort flag, first sequence, pad; offset in it and
+  // tiles of this CTA (64 bit); non-finite nodes [2] (64 bit); scan [12] (64 bit)
+  static constexpr int kSmemBytes = kMiscOff + 16 + 16 + 16 + 96;
+  static_assert(kSmemBytes <= 232448, "tree tile does not fit in shared memory");
+  static_assert(kKStages <= kTrMaxStages && kVStages <= kTrMaxStages, "ring stages");
+};
+
+enum TrBar {
+  kTrQFull = 0, kTrQEmpty = 1,
+  kTrKFull = 2, kTrKEmpty = kTrKFull + kTrMaxStages,
+  kTrVFull = kTrKEmpty + kTrMaxStages, kTrVEmpty = kTrVFull + kTrMaxStages,
+  kTrSFull = kTrVEmpty + kTrMaxStages, kTrPFull = kTrSFull + 2, kTrODone = kTrPFull + 2,
+  kTrXch = kTrODone + 2, kTrEpi = kTrXch + 1, kTrDrain = kTrEpi + 1
+};
+
+// What a CTA's range starts in, for the merge: sequence (-1: no work), item
+// of the sequence, first key tile, unused.
+struct TreeStart {
+  int seq, item, tile, pad;
+};
+
+struct TreeParams {
+  const int32_t* q_start;
+  const unsigned long long* tree_mask;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const void* v_pool;
+  void* out;
+  int out_bf16;
+  float* part_o;    // [2 CTAs][TILES * 128][D], normalised
+  float* part_lse;  // [2 CTAs][TILES * 128], log2
+  TreeStart* start; // [CTAs]
+  int num_seqs, total_q, max_q_len, q_heads, kv_heads, num_blocks, max_blocks_per_seq;
+  float scale_log2;
+};
+
+// A sequence's share of the work: row groups and key tiles (0 groups: none).
+struct TreeSeq {
+  int qs, n, ctx, groups, tiles;
+  bool bad;
+  __device__ __forceinline__ long long total(int kv_heads) const {
+    return (long long)groups * tiles * kv_heads;
+  }
+};
+
+template <int G, int TILES>
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int s) {
+  TreeSeq r;
+  r.qs = __ldg(p.q_start + s);
+  const int qe = __ldg(p.q_start + s + 1);
+  r.ctx = __ldg(p.context_lens + s);
+  r.n = qe - r.qs;
+  r.bad = r.qs < 0 || r.n < 0 || qe > p.total_q || r.n > p.max_q_len || r.n > r.ctx ||
+          r.ctx > p.max_blocks_per_seq * 16;
+  constexpr int kTokens = TILES * kTrRows / G;
+  r.groups = r.bad ? 0 : (r.n + kTokens - 1) / kTokens;
+  r.tiles = (r.ctx + kTrKeys - 1) / kTrKeys;
+  return r;
+}
+
+// The pieces of items in one CTA's range, in order.
+template <int G, int TILES>
+struct TreeWalk {
+  const TreeParams& p;
+  int s;
+  long long off;   // tiles of sequence s before the next piece
+  int left;        // tiles of the range after the current piece
+  TreeSeq seq;
+  int item, first, tiles;  // current piece
+  bool loaded = false;
+  __device__ __forceinline__ TreeWalk(const TreeParams& pp, int s0, long long off0, int count)
+      : p(pp), s(s0), off(off0), left(count) {}
+  __device__ __forceinline__ bool next() {
+    if (left <= 0) return false;
+    if (!loaded) {
+      seq = tree_seq<G, TILES>(p, s);
+      loaded = true;
+    }
+    while (off >= seq.total(p.kv_heads)) {
+      if (++s >= p.num_seqs) return false;
+      off = 0;
+      seq = tree_seq<G, TILES>(p, s);
+    }
+    item = int(off / seq.tiles);
+    first = int(off - (long long)item * seq.tiles);
+    tiles = min(seq.tiles - first, left);
+    off += tiles;
+    left -= tiles;
+    return true;
+  }
+  __device__ __forceinline__ int kv_head() const { return item / seq.groups; }
+  __device__ __forceinline__ int group() const { return item % seq.groups; }
+  __device__ __forceinline__ bool whole() const { return first == 0 && tiles == seq.tiles; }
+};
+
+// Bounded wait that also gives up as soon as another role has aborted.
+__device__ __forceinline__ bool tr_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  for (uint32_t i = 0; i < kWaitPollLimit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 255u && *abort_flag) return false;
+  }
+  return false;
+}
+
+__device__ __forceinline__ void tr_abort(volatile int* abort_flag) {
+  *abort_flag = 1;
+  atomicOr(&g_tree_error, kErrWaitTimeout);
+}
+
+// 32 of a row's key bits: key0 + i - base is node i's distance into the tree.
+__device__ __forceinline__ uint32_t key_bits(unsigned long long mask, int off) {
+  if (off >= 64 || off <= -32) return off < 0 ? 0xffffffffu : 0u;
+  if (off >= 0) return uint32_t(mask >> off);
+  return ((1u << -off) - 1u) | uint32_t(mask << -off);
+}
+
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared_u4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w) : "memory");
+}
+
+// The bits 15 and 31 of the halves of a bf16 pair that are NaN or infinite.
+__device__ __forceinline__ uint32_t nonfinite_bf16x2(uint32_t w) {
+  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+__device__ __forceinline__ uint32_t keep_finite(uint32_t w) {
+  return w & ~((nonfinite_bf16x2(w) >> 15) * 0xffffu);
+}
+
+template <int D, int G, int TILES>
+__global__ void __launch_bounds__(kTrThreads, 1)
+paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                  const __grid_constant__ CUtensorMap tmap_k,
+                  const __grid_constant__ CUtensorMap tmap_v, const TreeParams p) {
+  using T = TreeSmem<D, TILES>;
+  constexpr int TPT = kTrRows / G;  // tree nodes per row tile
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bars = sbase + T::kBarOff;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::kMiscOff);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + T::kMiscOff + 4);
+  int* start_seq = reinterpret_cast<int*>(smem + T::kMiscOff + 8);
+  long long* start_off = reinterpret_cast<long long*>(smem + T::kMiscOff + 16);
+  unsigned long long* nonfinite = reinterpret_cast<unsigned long long*>(smem + T::kMiscOff + 32);
+  long long* scan = reinterpret_cast<long long*>(smem + T::kMiscOff + 48);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  griddep_wait();  // inputs may have been written by the previous kernel in the stream
+
+  // ---- this CTA's range of the key tiles of all items
+  const int per_thread = (p.num_seqs + kTrThreads - 1) / kTrThreads;
+  const int s_lo = min(int(threadIdx.x) * per_thread, p.num_seqs);
+  const int s_hi = min(s_lo + per_thread, p.num_seqs);
+  long long mine = 0;
+  for (int s = s_lo; s < s_hi; ++s) {
+    const TreeSeq q = tree_seq<G, TILES>(p, s);
+    if (q.bad && blockIdx.x == 0) atomicOr(&g_tree_error, kErrBadQueryRange);
+    mine += q.total(p.kv_heads);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  if (lane == 31) scan[warp] = incl;
+  if (threadIdx.x == 0) *abort_flag = 0, *start_seq = p.num_seqs, nonfinite[0] = nonfinite[1] = 0;
+  __syncthreads();
+  long long all = 0;
+#pragma unroll
+  for (int w = 0; w < kTrThreads / 32; ++w) {
+    if (w == warp) incl += all;
+    all += scan[w];
+  }
+  // with fewer tiles than CTAs the last CTAs have none, so that a cut item's
+  // pieces lie in consecutive CTAs
+  const long long active = min((long long)gridDim.x, all), c = blockIdx.x;
+  const long long lo = c < active ? all * c / active : all;
+  const int count = c < active ? int(all * (c + 1) / active - lo) : 0;
+  if (lo >= incl - mine && lo < incl) {  // the range starts in this thread's sequences
+    long long at = lo - (incl - mine);
+    for (int s = s_lo; s < s_hi; ++s) {
+      const long long w = tree_seq<G, TILES>(p, s).total(p.kv_heads);
+      if (at < w) {
+        *start_seq = s;
+        *start_off = at;
+        break;
+      }
+      at -= w;
+    }
+  }
+  if (count > 0 && warp == 0) {
+    tmem_alloc(smem_u32(tmem_slot), kTrTmemCols);
+    tmem_relinquish();
+  }
+  if (threadIdx.x == kTrKWarp * 32) {
+    mbar_init(bars + 8 * kTrQFull, 1);
+    mbar_init(bars + 8 * kTrQEmpty, 1);
+    for (int s = 0; s < kTrMaxStages; ++s) {
+      mbar_init(bars + 8 * (kTrKFull + s), 1);
+      mbar_init(bars + 8 * (kTrKEmpty + s), 1);
+      mbar_init(bars + 8 * (kTrVFull + s), 1);
+      mbar_init(bars + 8 * (kTrVEmpty + s), 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(bars + 8 * (kTrSFull + w), 1);
+      mbar_init(bars + 8 * (kTrPFull + w), 4);
+      mbar_init(bars + 8 * (kTrODone + w), 1);
+    }
+    mbar_init(bars + 8 * kTrXch, 8);
+    mbar_init(bars + 8 * kTrEpi, 8);
+    mbar_init(bars + 8 * kTrDrain, 1);
+    fence_barrier_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (threadIdx.x == 0) {
+    TreeStart st{-1, 0, 0, 0};
+    if (count > 0) {
+      const int tiles = tree_seq<G, TILES>(p, *start_seq).tiles;
+      st.seq = *start_seq;
+      st.item = int(*start_off / tiles);
+      st.tile = int(*start_off % tiles);
+    }
+    p.start[blockIdx.x] = st;
+  }
+  if (count == 0) return;  // uniform over the CTA; no tensor memory held
+  const uint32_t tmem = *tmem_slot;
+  TreeWalk<G, TILES> walk(p, *start_seq, *start_off, count);
+
+  if (warp == kTrKWarp || warp == kTrVWarp) {
+    // ================= K and V rings =================
+    const bool is_v = warp == kTrVWarp;
+    const int stages = is_v ? T::kVStages : T::kKStages;
+    const uint32_t ring = sbase + (is_v ? T::kVOff : T::kKOff);
+    const uint32_t full = bars + 8 * (is_v ? kTrVFull : kTrKFull);
+    const uint32_t empty = bars + 8 * (is_v ? kTrVEmpty : kTrKEmpty);
+    const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
+    constexpr int kLoads = 8 * (D / 64);  // pages x column halves
+    if (lane == 0) tma_prefetch_desc(map);
+    int i = 0;
+    bool ok = true;
+    while (ok && walk.next()) {
+      const int kvh = walk.kv_head();
+      const int32_t* table = p.block_tables + size_t(walk.s) * p.max_blocks_per_seq;
+      const int nblk = (walk.seq.ctx + 15) / 16;
+      for (int j = 0; j < walk.tiles; ++j, ++i) {
+        const int st = i % stages;
+        int id = -1;  // pages past the context: the box is out of bounds and reads zeros
+        const int blk = (walk.first + j) * 8 + lane / (D / 64);
+        if (lane < kLoads && blk < nblk) {
+          id = __ldg(table + blk);
+          if (id < 0 || id >= p.num_blocks) {
+            atomicOr(&g_tree_error, kErrBadBlockId);
+            id = -1;
+          }
+        }
+        if (i >= stages) {
+          ok = __all_sync(0xffffffffu, tr_wait(empty + 8 * st, (i / stages - 1) & 1, abort_flag));
+          if (!ok) break;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(full + 8 * st, T::kTileBytes);
+        __syncwarp();
+        if (lane < kLoads)
+          tma_load_4d(ring + st * T::kTileBytes + (lane % (D / 64)) * T::kHalf +
+                          (lane / (D / 64)) * 2048,
+                      map, full + 8 * st, (lane % (D / 64)) * 64, kvh, 0, id);
+      }
+    }
+    if (!ok) {
+      // no copy may land after the CTA exits: wait (bounded) for the last one
+      // of each slot
+      if (lane == 0) {
+        tr_abort(abort_flag);
+        for (int k = max(0, i - stages); k < i; ++k)
+          (void)mbar_wait_bounded(full + 8 * (k % stages), (k / stages) & 1);
+      }
+    } else if (lane == 0) {
+      // the last release of each slot has arrived before the CTA exits (or,
+      // after an abort elsewhere, the copies have)
+      for (int k = max(0, i - stages); k < i; ++k) {
+        if (!tr_wait(empty + 8 * (k % stages), (k / stages) & 1, abort_flag))
+          (void)mbar_wait_bounded(full + 8 * (k % stages), (k / stages) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kTrQWarp) {
+    // ================= Q =================
+    if (lane == 0) {
+      tma_prefetch_desc(&tmap_q);
+      int k = 0;
+      bool ok = true;
+      for (; walk.next(); ++k) {
+        if (k > 0) {
+          ok = tr_wait(bars + 8 * kTrQEmpty, (k - 1) & 1, abort_flag);
+          if (!ok) break;
+        }
+        mbar_arrive_expect_tx(bars + 8 * kTrQFull, T::kQBytes);
+        const int tok = walk.seq.qs + walk.group() * TILES * TPT;
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(sbase + t * T::kTileBytes + h * T::kHalf, &tmap_q, bars + 8 * kTrQFull,
+                        h * 64, walk.kv_head() * G, tok + t * TPT);
+      }
+      if (!ok) tr_abort(abort_flag);
+      if (k > 0 && !tr_wait(bars + 8 * kTrQEmpty, (k - 1) & 1, abort_flag))
+        (void)mbar_wait_bounded(bars + 8 * kTrQFull, (k - 1) & 1);
+    }
+    __syncwarp();
+  } else if (warp == kTrMmaWarp) {
+    // ================= MMA issuer (one thread) =================
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = idesc_bf16_f32(128, kTrKeys, 0, 0);
+      constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 0, 1);
+      auto mma_s = [&](int w, int t, int i) {  // S_w = Q_t K_i^T
+        const uint32_t q_smem = sbase + t * T::kTileBytes;
+        const uint32_t k_smem = sbase + T::kKOff + (i % T::kKStages) * T::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = (k >> 2) * T::kHalf + (k & 3) * 32;
+          umma_bf16(tmem + w * 256, smem_desc_sw128(q_smem + off, 16, 1024),
+                    smem_desc_sw128(k_smem + off, 16, 1024), kIdescS, k > 0);
+        }
+        umma_commit(bars + 8 * (kTrSFull + w));
+      };
+      auto mma_pv = [&](int w, int i, bool fresh) {  // O_w (+)= P_w V_i
+        const uint32_t v_smem = sbase + T::kVOff + (i % T::kVStages) * T::kTileBytes;
+#pragma unroll
+        for (int k = 0; k < kTrKeys / 16; ++k) {
+          const uint64_t vdesc = smem_desc_sw128(v_smem + k * 2048, T::kHalf, 1024);
+          const uint32_t a_hi = tmem + w * 256 + 64 * (k >> 2) + 8 * (k & 3);
+          umma_bf16_ts(tmem + w * 256 + 128, a_hi, vdesc, kIdescPV, (!fresh || k > 0) ? 1u : 0u);
+          umma_bf16_ts(tmem + w * 256 + 128, a_hi + 32, vdesc, kIdescPV, 1u);
+        }
+        umma_commit(bars + 8 * (kTrODone + w));
+      };
+      auto wait = [&](int bar, uint32_t parity) {
+        const bool r = tr_wait(bars + 8 * bar, parity, abort_flag);
+        if (r) tc_fence_after();
+        return r;
+      };
+      // the piece of the next S product (runs ahead) and of the next P V
+      TreeWalk<G, TILES> ahead = walk;
+      int sk = -1, s_end = 0;  // pieces begun by S, and the stream tile the current one ends at
+      auto ready_s = [&](int i) {  // operands of S(i) are in shared memory
+        if (i == s_end) {
+          if (!ahead.next()) return false;
+          s_end += ahead.tiles;
+          ++sk;
+          if (!wait(kTrQFull, sk & 1)) return false;
+        }
+        return wait(kTrKFull + i % T::kKStages, (i / T::kKStages) & 1);
+      };
+      auto done_s = [&](int i) {
+        umma_commit(bars + 8 * (kTrKEmpty + i % T::kKStages));
+        if (i + 1 == s_end) umma_commit(bars + 8 * kTrQEmpty);
+      };
+      bool ok = true;
+      int pk = -1, p_begin = 0, p_end = 0;
+      auto piece_of = [&](int i) {
+        if (i == p_end) {
+          (void)walk.next();
+          p_begin = p_end;
+          p_end += walk.tiles;
+          ++pk;
+        }
+      };
+      if constexpr (TILES == 1) {
+        for (int i = 0; ok && i < 2 && i < count; ++i) {
+          ok = ready_s(i);
+          if (ok) mma_s(i & 1, 0, i), done_s(i);
+        }
+        for (int i = 0; ok && i < count; ++i) {
+          const int w = i & 1;
+          piece_of(i);
+          const bool fresh = i - p_begin < 2;  // first tile of this accumulator in the piece
+          ok = wait(kTrPFull + w, (i >> 1) & 1) &&
+               wait(kTrVFull + i % T::kVStages, (i / T::kVStages) & 1) &&
+               (!fresh || pk == 0 || wait(kTrEpi, (pk - 1) & 1));
+          if (!ok) break;
+          mma_pv(w, i, fresh);
+          umma_commit(bars + 8 * (kTrVEmpty + i % T::kVStages));
+          if (i + 2 < count) {
+            ok = ready_s(i + 2);
+            if (ok) mma_s(w, 0, i + 2), done_s(i + 2);
+          }
+        }
+      } else {
+        ok = ready_s(0);
+        if (ok) {
+          mma_s(0, 0, 0);
+          mma_s(1, 1, 0);
+          done_s(0);
+        }
+        for (int i = 0; ok && i < count; ++i) {
+          piece_of(i);
+          const bool fresh = i == p_begin;
+          ok = wait(kTrPFull + 0, i & 1) &&
+               wait(kTrVFull + i % T::kVStages, (i / T::kVStages) & 1) &&
+               (!fresh || pk == 0 || wait(kTrEpi, (pk - 1) & 1));
+          if (!ok) break;
+          mma_pv(0, i, fresh);
+          const bool more = i + 1 < count;
+          if (more) {
+            ok = ready_s(i + 1);
+            if (!ok) break;
+            mma_s(0, 0, i + 1);
+          }
+          ok = wait(kTrPFull + 1, i & 1);
+          if (!ok) break;
+          mma_pv(1, i, fresh);
+          umma_commit(bars + 8 * (kTrVEmpty + i % T::kVStages));
+          if (more) mma_s(1, 1, i + 1), done_s(i + 1);
+        }
+      }
+      if (!ok) tr_abort(abort_flag);
+      // every MMA issued has completed before tensor memory is released
+      umma_commit(bars + 8 * kTrDrain);
+      (void)mbar_wait_bounded(bars + 8 * kTrDrain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ================= softmax, correction, epilogue =================
+    const int w = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;  // row of the tile = tensor-memory lane
+    const int node_in_tile = r / G, head = r - (r / G) * G;
+    const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16);
+    const uint32_t s_col = w * 256, o_col = w * 256 + 128;
+    float2* xch = reinterpret_cast<float2*>(smem + T::kXchOff);
+    const bool neg = p.scale_log2 < 0.f;  // uniform
+    const float mag = fabsf(p.scale_log2);
+    int i = 0;  // stream tile the current piece begins at
+    bool ok = true;
+    for (int k = 0; ok && walk.next(); ++k) {
+      const TreeSeq& q = walk.seq;
+      const int node = (walk.group() * TILES + (TILES == 2 ? w : 0)) * TPT + node_in_tile;
+      const bool valid = node < q.n;
+      const bool warp_valid = __any_sync(0xffffffffu, valid);
+      const int base = q.ctx - q.n;  // committed keys
+      unsigned long long mask = 0;
+      if (valid) {
+        mask = __ldg(p.tree_mask + q.qs + node);
+        if (q.n < 64) mask &= (1ull << q.n) - 1ull;
+      }
+      float m = -INFINITY, l = 0.f;
+      int seen = 0;  // tiles of the piece this warpgroup has taken
+      int last = -1;
+      for (int j = 0; j < walk.tiles; ++j) {
+        const int it = i + j;
+        if (TILES == 1 && (it & 1) != w) continue;
+        const int ph = TILES == 1 ? it >> 1 : it;
+        last = ph;
+        const int key0 = (walk.first + j) * kTrKeys;
+        const bool masked = key0 + kTrKeys > base;
+        ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * (kTrSFull + w), ph & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        if (warp_valid) {
+          uint32_t bits[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) bits[c] = masked ? key_bits(mask, key0 + 32 * c - base) : ~0u;
+          // the tile's max over the keys this row sees
+          float ex[8];
+#pragma unroll
+          for (int a = 0; a < 8; ++a) ex[a] = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; c += 2) {
+            float va[32], vb[32];
+            tmem_ld32(lane_base + s_col + c * 32, va);
+            tmem_ld32(lane_base + s_col + c * 32 + 32, vb);
+            tmem_wait_ld();
+            if (neg) {
+#pragma unroll
+              for (int u = 0; u < 32; ++u) va[u] = -va[u], vb[u] = -vb[u];
+            }
+            if (masked) {
+#pragma unroll
+              for (int u = 0; u < 32; ++u) {
+                va[u] = (bits[c] >> u) & 1u ? va[u] : -INFINITY;
+                vb[u] = (bits[c + 1] >> u) & 1u ? vb[u] : -INFINITY;
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < 32; ++u) ex[u & 7] = max3f(ex[u & 7], va[u], vb[u]);
+          }
+          const float top = fmaxf(fmaxf(fmaxf(ex[0], ex[1]), fmaxf(ex[2], ex[3])),
+                                  fmaxf(fmaxf(ex[4], ex[5]), fmaxf(ex[6], ex[7])));
+          const float mx = top == -INFINITY ? -INFINITY : top * mag;
+          const bool move = mx > m + kTrRescale || (m == -INFINITY && mx > m);
+          if (__any_sync(0xffffffffu, move)) {
+            const float alpha = move ? ex2(m - mx) : 1.f;  // 0 when m is -inf
+            if (seen > 0) {
+              // the accumulator's last product must be done before it is scaled
+              ok = __all_sync(0xffffffffu,
+                              tr_wait(bars + 8 * (kTrODone + w), (ph - 1) & 1, abort_flag));
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+                tmem_ld32(lane_base + o_col + c * 32, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int u = 0; u < 32; u += 2)
+                  f2_unpack(f2_mul(f2_pack(o[u], o[u + 1]), a2), o[u], o[u + 1]);
+                tmem_st32(lane_base + o_col + c * 32, o);
+              }
+            }
+            l *= alpha;
+            if (move) m = mx;
+          }
+          // P = 2^(x - m) as bf16 hi + lo over the columns of the scores:
+          // keys [64 g, 64 g + 64): hi at 64 g, lo at 64 g + 32, two keys a column
+          const float mref = m == -INFINITY ? 0.f : m;  // nothing seen yet: all P are 0
+          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+          const uint64_t nm2 = f2_pack(-mref, -mref);
+          uint64_t ls[2] = {0ull, 0ull};
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            float va[32], vb[32];
+            tmem_ld32(lane_base + s_col + 64 * g, va);
+            tmem_ld32(lane_base + s_col + 64 * g + 32, vb);
+            tmem_wait_ld();
+            uint32_t hi[32], lo[32];
+#pragma unroll
+            for (int u = 0; u < 32; ++u) {
+              const int kk = 2 * u;
+              const float s0 = kk < 32 ? va[kk] : vb[kk - 32];
+              const float s1 = kk < 32 ? va[kk + 1] : vb[kk - 31];
+              float x0, x1;
+              f2_unpack(f2_fma(f2_pack(s0, s1), sc2, nm2), x0, x1);
+              float e0 = ex2(x0), e1 = ex2(x1);
+              if (masked) {
+                const uint32_t b = bits[2 * g + (kk >> 5)];
+                e0 = (b >> (kk & 31)) & 1u ? e0 : 0.f;
+                e1 = (b >> ((kk & 31) + 1)) & 1u ? e1 : 0.f;
+              }
+              const uint64_t e = f2_pack(e0, e1);
+              ls[u & 1] = f2_add(ls[u & 1], e);
+              hi[u] = pack_bf16x2(e0, e1);
+              float r0, r1;
+              f2_unpack(f2_sub(e, f2_pack(bf16_lo_to_f32(hi[u]), bf16_hi_to_f32(hi[u]))), r0, r1);
+              lo[u] = pack_bf16x2(r0, r1);
+            }
+            tmem_st32u(lane_base + s_col + 64 * g, hi);
+            tmem_st32u(lane_base + s_col + 64 * g + 32, lo);
+          }
+          float a0, a1, b0, b1;
+          f2_unpack(ls[0], a0, a1);
+          f2_unpack(ls[1], b0, b1);
+          l += (a0 + a1) + (b0 + b1);
+        }
+        if (masked && (TILES == 1 || w == 0)) {
+          // thread r looks at key row r of V; the chunk order differs from
+          // row to row, so that a warp's reads spread over the banks
+          ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * (kTrVFull + it % T::kVStages),
+                                               (it / T::kVStages) & 1, abort_flag));
+          if (!ok) break;
+          const int key = key0 + r;
+          if (key >= base) {
+            const uint32_t row = sbase + T::kVOff + (it % T::kVStages) * T::kTileBytes + r * 128;
+            uint32_t any = 0;
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                const uint32_t at = row + h * T::kHalf + (((c + r) & 7) << 4);
+                const uint4 v = ld_shared_u4(at);
+                const uint32_t bad = nonfinite_bf16x2(v.x) | nonfinite_bf16x2(v.y) |
+                                     nonfinite_bf16x2(v.z) | nonfinite_bf16x2(v.w);
+                if (bad) {
+                  st_shared_u4(at, make_uint4(keep_finite(v.x), keep_finite(v.y),
+                                              keep_finite(v.z), keep_finite(v.w)));
+                  any = 1;
+                }
+              }
+            if (any) {
+              if (key < q.ctx) atomicOr(nonfinite + (k & 1), 1ull << (key - base));
+              fence_proxy_async_smem();
+            }
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + 8 * (kTrPFull + w));
+        ++seen;
+      }
+      if (!ok) break;
+
+      // ---- end of the piece: both warpgroups meet
+      if (k > 0) {  // the exchange of the piece before has been read
+        ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * kTrEpi, (k - 1) & 1, abort_flag));
+        if (!ok) break;
+      }
+      if (warp == 0 && lane == 0) nonfinite[(k + 1) & 1] = 0;
+      xch[w * kTrRows + r] = make_float2(m, l);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * kTrXch);
+      ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * kTrXch, k & 1, abort_flag));
+      if (!ok) break;
+      if (last >= 0) {
+        ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * (kTrODone + w), last & 1, abort_flag));
+        if (!ok) break;
+      }
+      const int begin = i, end = i + walk.tiles;  // stream tiles of the piece
+      i = end;
+      float fa = 0.f, fb = 0.f, lse = -INFINITY;  // factors of O_w and of the other O
+      if constexpr (TILES == 1) {
+        const float2 other = xch[(1 - w) * kTrRows + r];
+        const float big = fmaxf(m, other.x);
+        const float ref = big == -INFINITY ? 0.f : big;
+        const float wa = ex2(m - ref), wb = ex2(other.x - ref);
+        const float tot = l * wa + other.y * wb;
+        if (l != 0.f) fa = wa / tot;  // NaN scores included
+        if (other.y != 0.f) fb = wb / tot;
+        if (tot != 0.f) lse = ref + __log2f(tot);
+        // the other warpgroup's last tile of the piece, if it had one
+        const int ot = ((end - 1) & 1) != w ? end - 1 : end - 2;
+        if (ot >= begin) {
+          ok = __all_sync(0xffffffffu,
+                          tr_wait(bars + 8 * (kTrODone + 1 - w), (ot >> 1) & 1, abort_flag));
+          if (!ok) break;
+        } else {
+          fb = 0.f;
+        }
+      } else if (l != 0.f) {
+        fa = 1.f / l;
+        lse = (m == -INFINITY ? 0.f : m) + __log2f(l);
+      }
+      tc_fence_after();
+
+      if (warp_valid) {
+        const unsigned long long hit = mask & nonfinite[k & 1];
+        const int kvh = walk.kv_head();
+        const size_t orow = (size_t(q.qs) + node) * p.q_heads + size_t(kvh) * G + head;
+        const bool whole = walk.whole();
+        // slot 2c: the piece the CTA's range starts with, 2c + 1: the one it ends with
+        const size_t slot = size_t(blockIdx.x) * 2 + (k == 0 ? 0 : 1);
+        const size_t prow = (slot * TILES + (TILES == 2 ? w : 0)) * kTrRows + r;
+        // TILES 1: this warpgroup's half of the columns of both accumulators
+        constexpr int kCols = TILES == 1 ? D / 2 : D;
+        const int col0 = TILES == 1 ? w * kCols : 0;
+        const bool use_a = __any_sync(0xffffffffu, fa != 0.f);
+        const bool use_b = TILES == 1 && __any_sync(0xffffffffu, fb != 0.f);
+#pragma unroll 1
+        for (int c = 0; c < kCols; c += 32) {
+          float o[32];
+#pragma unroll
+          for (int u = 0; u < 32; ++u) o[u] = 0.f;
+          if (use_a) {
+            float a[32];
+            tmem_ld32(lane_base + o_col + col0 + c, a);
+            tmem_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 32; ++u) o[u] = fa != 0.f ? a[u] * fa : 0.f;
+          }
+          if (use_b) {
+            float b[32];
+            tmem_ld32(lane_base + (256 - s_col) + 128 + col0 + c, b);
+            tmem_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 32; ++u) o[u] += fb != 0.f ? b[u] * fb : 0.f;
+          }
+          // non-finite V elements of nodes this row sees (rare)
+          for (unsigned long long h = hit; h; h &= h - 1) {
+            const int at = base + __ffsll(h) - 1;
+            const int id = __ldg(p.block_tables + size_t(walk.s) * p.max_blocks_per_seq + at / 16);
+            const int64_t row = (int64_t(id) * 16 + at % 16) * p.kv_heads + kvh;
+            for (int u = 0; u < 32; ++u) {
+              const uint32_t x = reinterpret_cast<const uint16_t*>(p.v_pool)[row * D + col0 + c + u];
+              if ((x & 0x7f80u) == 0x7f80u) {
+                const float add = __uint_as_float(x << 16);
+#pragma unroll
+                for (int z = 0; z < 32; ++z) o[z] += z == u ? add : 0.f;
+              }
+            }
+          }
+          if (!valid) continue;
+          if (!whole) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + col0 + c);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          } else if (p.out_bf16) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D +
+                                                  col0 + c);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              dst[u] = make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]),
+                                  pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
+                                  pack_bf16x2(o[8 * u + 4], o[8 * u + 5]),
+                                  pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow * D + col0 + c);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          }
+        }
+        if (valid && !whole && col0 == 0) p.part_lse[prow] = lse;
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * kTrEpi);
+    }
+    if (!ok && lane == 0) tr_abort(abort_flag);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTrTmemCols);
+  }
+}
+
+// Joins the pieces of the items that were cut between CTAs.  Block (b, y):
+// the item in which CTA b's range starts, if the range of an earlier CTA does
+// not start inside the same item (each cut item then has one b); its pieces
+// are CTA b - 1's last one and the first ones of b, b + 1, ... while they are
+// of the item.  A warp takes a row; out = sum 2^(lse_i - lse) o_i.
+constexpr int kTrMergeWarps = 4;
+
+template <int D, int G, int TILES>
+__global__ void __launch_bounds__(kTrMergeWarps * 32)
+tree_merge_kernel(const TreeParams p, int ctas) {
+  griddep_wait();
+  const int b = blockIdx.x + 1;
+  const TreeStart here = p.start[b];
+  if (here.seq < 0 || here.tile == 0) return;
+  const TreeStart before = p.start[b - 1];
+  const bool same = before.seq == here.seq && before.item == here.item;
+  if (same && before.tile > 0) return;
+  const TreeSeq q = tree_seq<G, TILES>(p, here.seq);
+  const int kvh = here.item / q.groups, group = here.item % q.groups;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * kTrMergeWarps + warp;  // row of the group
+  const int node = group * TILES * (kTrRows / G) + r / G;
+  if (node >= q.n) return;
+  // CTAs b, b + 1, ... whose ranges start in the item, 32 looked at at a time
+  int parts = 1;
+  for (int c = b;; c += 32) {
+    bool mine = false;
+    if (c + lane < ctas) {
+      const TreeStart s = p.start[c + lane];
+      mine = s.seq == here.seq && s.item == here.item;
+    }
+    const unsigned vote = __ballot_sync(0xffffffffu, mine);
+    parts += vote == 0xffffffffu ? 32 : __ffs(~vote) - 1;
+    if (vote != 0xffffffffu) break;
+  }
+  auto row_of = [&](int i) {  // piece i's row in the workspace
+    const size_t slot = i == 0 ? size_t(b - 1) * 2 + (same ? 0 : 1) : size_t(b + i - 1) * 2;
+    return slot * (TILES * kTrRows) + r;
+  };
+  constexpr int V = D / 32;  // columns per lane
+  float acc[V];
+#pragma unroll
+  for (int u = 0; u < V; ++u) acc[u] = 0.f;
+  float big = -INFINITY, tot = 0.f;
+  for (int i0 = 0; i0 < parts; i0 += 32) {  // lane i weighs piece i0 + i
+    const float lse = i0 + lane < parts ? __ldg(p.part_lse + row_of(i0 + lane)) : -INFINITY;
+    float top = lse;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float now = fmaxf(big, top);
+    const float ref = now == -INFINITY ? 0.f : now;
+    const float fade = ex2(big - ref);
+    big = now;
+    const float wgt = ex2(lse - ref);
+    tot *= fade;
+#pragma unroll
+    for (int u = 0; u < V; ++u) acc[u] *= fade;
+    const int n = min(32, parts - i0);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float g = __shfl_sync(0xffffffffu, wgt, i);
+      const float* o = p.part_o + row_of(i0 + i) * D + lane * V;
+      float x[V];
+      if constexpr (V == 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(o));
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+      } else {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(o));
+        x[0] = v.x, x[1] = v.y;
+      }
+      tot += g;
+#pragma unroll
+      for (int u = 0; u < V; ++u) acc[u] = fmaf(x[u], g, acc[u]);
+    }
+  }
+  const float inv = tot != 0.f ? 1.f / tot : 0.f;
+  const size_t at = ((size_t(q.qs) + node) * p.q_heads + size_t(kvh) * G + r % G) * D + lane * V;
+#pragma unroll
+  for (int u = 0; u < V; u += 2) {
+    if (p.out_bf16)
+      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at + u) =
+          pack_bf16x2(acc[u] * inv, acc[u + 1] * inv);
+    else
+      *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at + u) =
+          make_float2(acc[u] * inv, acc[u + 1] * inv);
+  }
+}
+
+cudaError_t tree_error_word(unsigned** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_tree_error);
+}
+
+unsigned read_tree_error(bool clear) {
+  unsigned word = 0;
+  if (cudaMemcpyFromSymbol(&word, g_tree_error, sizeof(word)) != cudaSuccess) return ~0u;
+  if (clear) {
+    const unsigned zero = 0;
+    if (cudaMemcpyToSymbol(g_tree_error, &zero, sizeof(zero)) != cudaSuccess) return ~0u;
+  }
+  return word;
+}
+
+int tree_tile_rows() { return kTrRows; }
+
+template <int D, int G, int TILES>
+static cudaError_t launch_tree_t(const TreeParams& p, int ctas, const CUtensorMap* tq,
+                                 const CUtensorMap* tk, const CUtensorMap* tv,
+                                 cudaStream_t stream) {
+  using T = TreeSmem<D, TILES>;
+  static std::atomic<int> attr_done[kAttrMaxDevices];
+  cudaError_t e = set_smem_limit_once(paged_tree_kernel<D, G, TILES>, T::kSmemBytes, attr_done);
+  if (e != cudaSuccess) return e;
+  e = launch_after_previous(paged_tree_kernel<D, G, TILES>, dim3(ctas), dim3(kTrThreads),
+                            T::kSmemBytes, stream, *tq, *tk, *tv, p);
+  if (e != cudaSuccess || ctas < 2) return e;
+  const int rows = std::min(p.max_q_len * G, TILES * kTrRows);
+  return launch_after_previous(tree_merge_kernel<D, G, TILES>,
+                               dim3(ctas - 1, (rows + kTrMergeWarps - 1) / kTrMergeWarps),
+                               dim3(kTrMergeWarps * 32), 0, stream, p, ctas);
+}
+
+template <int D, int TILES>
+static cudaError_t launch_tree_g(const TreeParams& p, int ctas, int group, const CUtensorMap* tq,
+                                 const CUtensorMap* tk, const CUtensorMap* tv,
+                                 cudaStream_t stream) {
+  switch (group) {
+    case 1: return launch_tree_t<D, 1, TILES>(p, ctas, tq, tk, tv, stream);
+    case 2: return launch_tree_t<D, 2, TILES>(p, ctas, tq, tk, tv, stream);
+    case 4: return launch_tree_t<D, 4, TILES>(p, ctas, tq, tk, tv, stream);
+    case 8: return launch_tree_t<D, 8, TILES>(p, ctas, tq, tk, tv, stream);
+    case 16: return launch_tree_t<D, 16, TILES>(p, ctas, tq, tk, tv, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+int tree_tiles(int group, int max_q_len) { return group * max_q_len <= kTrRows ? 1 : 2; }
+
+cudaError_t launch_paged_tree(const TreeArgs& a, const CUtensorMap* tq, const CUtensorMap* tk,
+                              const CUtensorMap* tv, cudaStream_t stream) {
+  TreeParams p;
+  p.q_start = a.q_start;
+  p.tree_mask = reinterpret_cast<const unsigned long long*>(a.tree_mask);
+  p.block_tables = a.block_tables;
+  p.context_lens = a.context_lens;
+  p.v_pool = a.v_cache;
+  p.out = a.out;
+  p.out_bf16 = a.out_bf16 ? 1 : 0;
+  p.part_o = a.part_o;
+  p.part_lse = a.part_lse;
+  p.start = static_cast<TreeStart*>(a.start);
+  p.num_seqs = a.num_seqs;
+  p.total_q = a.total_q;
+  p.max_q_len = a.max_q_len;
+  p.q_heads = a.q_heads;
+  p.kv_heads = a.kv_heads;
+  p.num_blocks = a.num_blocks;
+  p.max_blocks_per_seq = a.max_blocks_per_seq;
+  p.scale_log2 = a.scale_log2;
+  const int group = a.q_heads / a.kv_heads;
+  const bool one = tree_tiles(group, a.max_q_len) == 1;
+  if (a.d_head == 128)
+    return one ? launch_tree_g<128, 1>(p, a.ctas, group, tq, tk, tv, stream)
+               : launch_tree_g<128, 2>(p, a.ctas, group, tq, tk, tv, stream);
+  if (a.d_head == 64)
+    return one ? launch_tree_g<64, 1>(p, a.ctas, group, tq, tk, tv, stream)
+               : launch_tree_g<64, 2>(p, a.ctas, group, tq, tk, tv, stream);
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace pkv

@@ -1697,7 +1697,7 @@ namespace {
 // atomic step, so a bit raised meanwhile by a kernel on another stream stays
 // for the next query instead of being lost -- and stores the OR.
 struct ErrorWordSet {
-  unsigned* word[9];
+  unsigned* word[12];
   int count;
   int clear;
 };
@@ -1715,13 +1715,14 @@ std::mutex g_collect_mutex;  // one collection in flight per process
 
 int collect_error_words(cudaStream_t stream, bool clear, unsigned* word) {
   ErrorWordSet s = {};
-  cudaError_t (*const getters[9])(unsigned**) = {
+  cudaError_t (*const getters[12])(unsigned**) = {
       pkv::append_error_word, pkv::decode_error_word, pkv::decode_fp8_error_word,
       pkv::prefill_error_word, pkv::verify_error_word, pkv::probe_error_word,
-      pkv::mixed_decode_error_word, pkv::mixed_prefill_error_word, pkv::decode_flat_error_word};
-  for (int i = 0; i < 9; ++i)
+      pkv::mixed_decode_error_word, pkv::mixed_prefill_error_word, pkv::decode_flat_error_word,
+      pkv::rope_error_word, pkv::draft_error_word, pkv::tree_error_word};
+  for (int i = 0; i < 12; ++i)
     if (getters[i](&s.word[i]) != cudaSuccess) return PKV_ECUDA;
-  s.count = 9;
+  s.count = 12;
   s.clear = clear ? 1 : 0;
   std::lock_guard<std::mutex> lock(g_collect_mutex);
   collect_error_words_kernel<<<1, 1, 0, stream>>>(s);
@@ -1763,10 +1764,13 @@ int pkv_get_device_error(unsigned int* word, int clear) {
   const unsigned w = pkv::read_probe_error(clear != 0);
   const unsigned m = pkv::read_mixed_error(clear != 0);
   const unsigned fl = pkv::read_decode_flat_error(clear != 0);
+  const unsigned r = pkv::read_rope_error(clear != 0);
+  const unsigned dr = pkv::read_draft_error(clear != 0);
+  const unsigned t = pkv::read_tree_error(clear != 0);
   if (a == ~0u || d == ~0u || f == ~0u || d8 == ~0u || v == ~0u || w == ~0u || m == ~0u ||
-      fl == ~0u)
+      fl == ~0u || r == ~0u || dr == ~0u || t == ~0u)
     return PKV_ECUDA;
-  *word = a | d | f | d8 | v | w | m | fl;
+  *word = a | d | f | d8 | v | w | m | fl | r | dr | t;
   return PKV_OK;
 }
 
@@ -1778,6 +1782,297 @@ int pkv_wait_timeout_probe(uint32_t polls, unsigned long long* cycles, pkv_strea
   const cudaError_t e =
       pkv::launch_wait_timeout_probe(polls, cycles, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The speculative step: norm + rotation + append, tree layout, tree attention,
+// accepted rows.
+// ---------------------------------------------------------------------------
+namespace {
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+int rope_append(const void* q, int64_t q_tok_stride, const void* k, int64_t k_tok_stride,
+                const void* v, int64_t v_tok_stride, int64_t num_tokens, int q_heads,
+                const int64_t* positions, const float* rope_table, int64_t max_positions,
+                int rot_dim, int interleaved, const void* q_weight, const void* k_weight,
+                float eps, const int64_t* slot_mapping, void* q_out, void* k_cache,
+                void* v_cache, const pkv_cache_desc& cache, bool fp8, float k_scale,
+                float v_scale, pkv_stream_t stream) {
+  int st = check_cache_desc(cache);
+  if (st != PKV_OK) return st;
+  if (num_tokens < 0 || q_heads <= 0 || max_positions <= 0) return PKV_EINVAL;
+  if (cache.d_head != 64 && cache.d_head != 128) return PKV_EUNSUPPORTED;
+  if (rot_dim <= 0 || rot_dim > cache.d_head || rot_dim % 16) return PKV_EUNSUPPORTED;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return PKV_EINVAL;
+  if (fp8 && (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) ||
+              !std::isfinite(v_scale)))
+    return PKV_EINVAL;
+  if (num_tokens == 0) return PKV_OK;
+  if (!q || !k || !v || !positions || !rope_table || !slot_mapping || !q_out || !k_cache ||
+      !v_cache)
+    return PKV_EINVAL;
+  const int64_t qrow = int64_t(q_heads) * cache.d_head;
+  const int64_t row = int64_t(cache.kv_heads) * cache.d_head;
+  if (int64_t(q_heads) + 2 * int64_t(cache.kv_heads) > (1 << 20)) return PKV_EUNSUPPORTED;
+  if (q_tok_stride < qrow || k_tok_stride < row || v_tok_stride < row || q_tok_stride % 8 ||
+      k_tok_stride % 8 || v_tok_stride % 8)
+    return PKV_EINVAL;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) ||
+      !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(rope_table, 16) ||
+      !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(positions, 8) ||
+      !aligned(slot_mapping, 8))
+    return PKV_EINVAL;
+  // a warp reads a head's partner elements before another warp's store only
+  // if no output lies over an input
+  const size_t out_bytes = size_t(num_tokens) * size_t(qrow) * 2;
+  auto span = [&](int64_t stride, int64_t r) {
+    return size_t((num_tokens - 1) * stride + r) * 2;
+  };
+  if (overlap(q_out, out_bytes, q, span(q_tok_stride, qrow)) ||
+      overlap(q_out, out_bytes, k, span(k_tok_stride, row)) ||
+      overlap(q_out, out_bytes, v, span(v_tok_stride, row)))
+    return PKV_EINVAL;
+  const int sms = current_device_sms();
+  if (sms <= 0) return PKV_ECUDA;
+  pkv::QkRopeArgs a;
+  a.q = static_cast<const uint4*>(q);
+  a.k = static_cast<const uint4*>(k);
+  a.v = static_cast<const uint4*>(v);
+  a.q_stride_vec = q_tok_stride / 8;
+  a.k_stride_vec = k_tok_stride / 8;
+  a.v_stride_vec = v_tok_stride / 8;
+  a.positions = positions;
+  a.table = rope_table;
+  a.max_positions = max_positions;
+  a.rot_dim = rot_dim;
+  a.q_weight = static_cast<const uint4*>(q_weight);
+  a.k_weight = static_cast<const uint4*>(k_weight);
+  a.eps = eps;
+  a.slot_mapping = slot_mapping;
+  a.num_tokens = num_tokens;
+  a.num_slots = int64_t(cache.num_blocks) * cache.block_size;
+  a.q_out = static_cast<uint4*>(q_out);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.q_heads = q_heads;
+  a.kv_heads = cache.kv_heads;
+  a.k_inv = fp8 ? 1.0f / k_scale : 1.f;
+  a.v_inv = fp8 ? 1.0f / v_scale : 1.f;
+  a.interleaved = interleaved != 0;
+  a.fp8 = fp8;
+  const cudaError_t e =
+      pkv::launch_qk_rope_append(a, cache.d_head, sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : (e == cudaErrorInvalidValue ? PKV_EUNSUPPORTED : PKV_ECUDA);
+}
+
+// Workspace of the tree attention: each CTA's start, then two slots of
+// partial rows per CTA (log-sum-exp, then outputs).
+struct TreeLayout {
+  int ctas = 0;
+  size_t lse_off = 0, o_off = 0, total = 0;
+};
+
+int tree_layout(int max_q_len, int q_heads, int kv_heads, int d_head, TreeLayout* w) {
+  if (max_q_len < 0 || q_heads <= 0 || kv_heads <= 0) return PKV_EINVAL;
+  if (q_heads % kv_heads || !supported_group(q_heads / kv_heads)) return PKV_EUNSUPPORTED;
+  if (d_head != 64 && d_head != 128) return PKV_EUNSUPPORTED;
+  if (max_q_len > pkv::tree_max_nodes()) return PKV_EUNSUPPORTED;
+  w->ctas = current_device_sms();
+  if (w->ctas <= 0) w->ctas = 152;  // no device: the size for a GB300
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t rows = size_t(w->ctas) * 2 * size_t(pkv::tree_tile_rows()) *
+                      size_t(pkv::tree_tiles(q_heads / kv_heads, max_q_len));
+  w->lse_off = up(size_t(w->ctas) * 16);
+  w->o_off = w->lse_off + up(rows * 4);
+  w->total = w->o_off + rows * size_t(d_head) * 4;
+  return PKV_OK;
+}
+
+int tree_attention(const void* q, const int32_t* q_start, int num_seqs, int total_q,
+                   int max_q_len, int q_heads, const uint64_t* tree_mask, const void* k_cache,
+                   const void* v_cache, const pkv_cache_desc& cache, const int32_t* block_tables,
+                   int max_blocks_per_seq, const int32_t* context_lens, float scale, void* out,
+                   bool out_bf16, void* workspace, size_t ws_bytes, pkv_stream_t stream) {
+  int st = check_prefill(q, q_start, num_seqs, total_q, max_q_len, q_heads, k_cache, v_cache,
+                         cache, block_tables, max_blocks_per_seq, context_lens, scale, out);
+  if (st != PKV_OK) return st;
+  TreeLayout w;
+  st = tree_layout(max_q_len, q_heads, cache.kv_heads, cache.d_head, &w);
+  if (st != PKV_OK) return st;
+  if (num_seqs == 0 || total_q == 0 || max_q_len == 0) return PKV_OK;
+  if (!tree_mask || !aligned(tree_mask, 8)) return PKV_EINVAL;
+  if (max_blocks_per_seq > INT32_MAX / kBlockSize) return PKV_EUNSUPPORTED;
+  if (!workspace || ws_bytes < w.total) return PKV_ENOMEM;
+  if (!aligned(workspace, 256)) return PKV_EINVAL;
+  if (current_device_sms() <= 0) return PKV_ECUDA;
+  const int group = q_heads / cache.kv_heads;
+  const int rows = pkv::tree_tile_rows();
+  CUtensorMap tq, tk, tv;
+  if (!encode_query_map(&tq, q, total_q, q_heads, cache.d_head, group, rows / group) ||
+      !encode_pool_map(&tk, k_cache, cache) || !encode_pool_map(&tv, v_cache, cache))
+    return PKV_ECUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  pkv::TreeArgs a;
+  a.q_start = q_start;
+  a.tree_mask = tree_mask;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.v_cache = v_cache;
+  a.out = out;
+  a.out_bf16 = out_bf16;
+  a.start = ws;
+  a.part_lse = reinterpret_cast<float*>(ws + w.lse_off);
+  a.part_o = reinterpret_cast<float*>(ws + w.o_off);
+  a.num_seqs = num_seqs;
+  a.total_q = total_q;
+  a.max_q_len = max_q_len;
+  a.q_heads = q_heads;
+  a.kv_heads = cache.kv_heads;
+  a.d_head = cache.d_head;
+  a.num_blocks = cache.num_blocks;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.ctas = w.ctas;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  const cudaError_t e =
+      pkv::launch_paged_tree(a, &tq, &tk, &tv, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkv_qk_norm_rope_append(const void* q, int64_t q_tok_stride, const void* k,
+                            int64_t k_tok_stride, const void* v, int64_t v_tok_stride,
+                            int64_t num_tokens, int q_heads, const int64_t* positions,
+                            const float* rope_table, int64_t max_positions, int rot_dim,
+                            int interleaved, const void* q_weight, const void* k_weight,
+                            float eps, const int64_t* slot_mapping, void* q_out, void* k_cache,
+                            void* v_cache, pkv_cache_desc cache, pkv_stream_t stream) {
+  return rope_append(q, q_tok_stride, k, k_tok_stride, v, v_tok_stride, num_tokens, q_heads,
+                     positions, rope_table, max_positions, rot_dim, interleaved, q_weight,
+                     k_weight, eps, slot_mapping, q_out, k_cache, v_cache, cache, false, 1.f, 1.f,
+                     stream);
+}
+
+int pkv_qk_norm_rope_append_fp8(const void* q, int64_t q_tok_stride, const void* k,
+                                int64_t k_tok_stride, const void* v, int64_t v_tok_stride,
+                                int64_t num_tokens, int q_heads, const int64_t* positions,
+                                const float* rope_table, int64_t max_positions, int rot_dim,
+                                int interleaved, const void* q_weight, const void* k_weight,
+                                float eps, const int64_t* slot_mapping, void* q_out,
+                                void* k_cache, void* v_cache, pkv_cache_desc cache,
+                                float k_scale, float v_scale, pkv_stream_t stream) {
+  return rope_append(q, q_tok_stride, k, k_tok_stride, v, v_tok_stride, num_tokens, q_heads,
+                     positions, rope_table, max_positions, rot_dim, interleaved, q_weight,
+                     k_weight, eps, slot_mapping, q_out, k_cache, v_cache, cache, true, k_scale,
+                     v_scale, stream);
+}
+
+int pkv_draft_tree_layout(const int32_t* parents, const int32_t* q_start, int num_seqs,
+                          int total_q, int max_q_len, const int32_t* context_lens,
+                          uint64_t* tree_mask, int64_t* positions, pkv_stream_t stream) {
+  if (num_seqs < 0 || total_q < 0 || max_q_len < 0) return PKV_EINVAL;
+  if (max_q_len > pkv::tree_max_nodes()) return PKV_EUNSUPPORTED;
+  if (num_seqs == 0 || total_q == 0 || max_q_len == 0) return PKV_OK;
+  if (!parents || !q_start || !context_lens || !tree_mask || !positions) return PKV_EINVAL;
+  if (!aligned(parents, 4) || !aligned(q_start, 4) || !aligned(context_lens, 4) ||
+      !aligned(tree_mask, 8) || !aligned(positions, 8))
+    return PKV_EINVAL;
+  const cudaError_t e =
+      pkv::launch_tree_layout(parents, q_start, num_seqs, total_q, max_q_len, context_lens,
+                              tree_mask, positions, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+size_t pkv_tree_attention_workspace_bytes(int num_seqs, int max_q_len, int q_heads, int kv_heads,
+                                          int d_head) {
+  TreeLayout w;
+  if (num_seqs < 0 || tree_layout(max_q_len, q_heads, kv_heads, d_head, &w) != PKV_OK) return 0;
+  return w.total;
+}
+
+int pkv_paged_tree_attention(const void* q, const int32_t* q_start, int num_seqs, int total_q,
+                             int max_q_len, int q_heads, const uint64_t* tree_mask,
+                             const void* k_cache, const void* v_cache, pkv_cache_desc cache,
+                             const int32_t* block_tables, int max_blocks_per_seq,
+                             const int32_t* context_lens, float scale, float* out,
+                             void* workspace, size_t ws_bytes, pkv_stream_t stream) {
+  return tree_attention(q, q_start, num_seqs, total_q, max_q_len, q_heads, tree_mask, k_cache,
+                        v_cache, cache, block_tables, max_blocks_per_seq, context_lens, scale,
+                        out, false, workspace, ws_bytes, stream);
+}
+
+int pkv_paged_tree_attention_bf16out(const void* q, const int32_t* q_start, int num_seqs,
+                                     int total_q, int max_q_len, int q_heads,
+                                     const uint64_t* tree_mask, const void* k_cache,
+                                     const void* v_cache, pkv_cache_desc cache,
+                                     const int32_t* block_tables, int max_blocks_per_seq,
+                                     const int32_t* context_lens, float scale, void* out,
+                                     void* workspace, size_t ws_bytes, pkv_stream_t stream) {
+  return tree_attention(q, q_start, num_seqs, total_q, max_q_len, q_heads, tree_mask, k_cache,
+                        v_cache, cache, block_tables, max_blocks_per_seq, context_lens, scale,
+                        out, true, workspace, ws_bytes, stream);
+}
+
+int pkv_kv_accept_rows(void* k_cache, int64_t k_layer_stride, void* v_cache,
+                       int64_t v_layer_stride, int num_layers, pkv_cache_desc cache,
+                       int32_t elem_bytes, const int32_t* block_tables, int max_blocks_per_seq,
+                       const int32_t* context_lens, const int32_t* q_start, int num_seqs,
+                       const int32_t* accepted, int max_accepted, const int32_t* num_accepted,
+                       int32_t* new_context_lens, pkv_stream_t stream) {
+  int st = check_cache_desc(cache);
+  if (st != PKV_OK) return st;
+  if (elem_bytes != 1 && elem_bytes != 2) return PKV_EINVAL;
+  if (num_layers < 0 || num_seqs < 0 || max_accepted < 0) return PKV_EINVAL;
+  const int64_t row_bytes = int64_t(cache.kv_heads) * cache.d_head * elem_bytes;
+  if (row_bytes % 16 || row_bytes > (1 << 24)) return PKV_EUNSUPPORTED;
+  if (num_layers == 0 || num_seqs == 0) return PKV_OK;
+  if (!k_cache || !v_cache || !block_tables || !context_lens || !q_start || !num_accepted ||
+      !new_context_lens || (max_accepted > 0 && !accepted) || max_blocks_per_seq <= 0)
+    return PKV_EINVAL;
+  const int64_t pool_bytes = int64_t(cache.num_blocks) * cache.block_size * row_bytes;
+  for (const int64_t s : {k_layer_stride, v_layer_stride})
+    if (num_layers > 1 &&
+        (s < pool_bytes / elem_bytes || (s * elem_bytes) % 16 || s > (int64_t(1) << 60)))
+      return PKV_EINVAL;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_tables, 4) ||
+      !aligned(context_lens, 4) || !aligned(q_start, 4) || !aligned(accepted, 4) ||
+      !aligned(num_accepted, 4) || !aligned(new_context_lens, 4))
+    return PKV_EINVAL;
+  // other CTAs of a sequence still read what one CTA would overwrite
+  const size_t n = size_t(num_seqs) * 4;
+  if (overlap(new_context_lens, n, context_lens, n) ||
+      overlap(new_context_lens, n, num_accepted, n) ||
+      overlap(new_context_lens, n, q_start, n + 4) ||
+      overlap(new_context_lens, n, accepted, n * size_t(max_accepted)))
+    return PKV_EINVAL;
+  pkv::AcceptArgs a;
+  a.k_cache = static_cast<uint4*>(k_cache);
+  a.v_cache = static_cast<uint4*>(v_cache);
+  a.k_layer_vec = num_layers > 1 ? k_layer_stride * elem_bytes / 16 : 0;
+  a.v_layer_vec = num_layers > 1 ? v_layer_stride * elem_bytes / 16 : 0;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.q_start = q_start;
+  a.accepted = accepted;
+  a.num_accepted = num_accepted;
+  a.new_context_lens = new_context_lens;
+  a.num_seqs = num_seqs;
+  a.max_accepted = max_accepted;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_blocks = cache.num_blocks;
+  a.row_vec = int(row_bytes / 16);
+  a.col_blocks = 0;
+  const cudaError_t e =
+      pkv::launch_accept_rows(a, num_layers, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : (e == cudaErrorInvalidValue ? PKV_EUNSUPPORTED : PKV_ECUDA);
 }
 
 }  // extern "C"

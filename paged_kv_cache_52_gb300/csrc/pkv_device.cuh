@@ -25,6 +25,8 @@ enum : unsigned {
   kErrTmemAlloc = 1u << 5,      // tensor-memory allocation failed
   kErrDuplicateSlot = 1u << 7,  // checked append: two tokens name one slot (nothing written)
   kErrPrefixMismatch = 1u << 8, // a prefix-group member's prefix is not its group's (not shared)
+  kErrBadPosition = 1u << 9,    // position outside the rotation table (token skipped)
+  kErrBadTree = 1u << 10,       // tree parent or accepted path out of order
 };
 
 // A bounded wait gives up after this many polls.  A poll of try_wait on a

@@ -21,6 +21,9 @@ cudaError_t probe_error_word(unsigned** word);
 cudaError_t mixed_decode_error_word(unsigned** word);
 cudaError_t mixed_prefill_error_word(unsigned** word);
 cudaError_t decode_flat_error_word(unsigned** word);
+cudaError_t rope_error_word(unsigned** word);
+cudaError_t draft_error_word(unsigned** word);
+cudaError_t tree_error_word(unsigned** word);
 
 // ---- kv_append.cu
 // reject (optional): a device flag set by launch_slot_duplicates; when it is
@@ -235,5 +238,66 @@ cudaError_t launch_mixed_step(const PrefillArgs& pa, const DecodeArgs& da, int* 
                               const CUtensorMap* tmap_qd = nullptr,
                               const CUtensorMap* tmap_o = nullptr);
 unsigned read_mixed_error(bool clear);
+
+// ---- qk_rope_append.cu: norm and rotation of queries and keys, and the append
+struct QkRopeArgs {
+  const uint4 *q, *k, *v;                       // 16-byte vectors of 8 bf16
+  int64_t q_stride_vec, k_stride_vec, v_stride_vec;  // per token
+  const int64_t* positions;
+  const float* table;                           // [max_positions][rot_dim]: cosines, sines
+  int64_t max_positions;
+  int rot_dim;
+  const uint4 *q_weight, *k_weight;             // [d_head] bf16, or null: no norm
+  float eps;
+  const int64_t* slot_mapping;
+  int64_t num_tokens, num_slots;
+  uint4* q_out;
+  void *k_cache, *v_cache;
+  int q_heads, kv_heads;
+  float k_inv, v_inv;                           // FP8 pools: 1 / scale
+  bool interleaved, fp8;
+};
+cudaError_t launch_qk_rope_append(const QkRopeArgs& a, int d_head, int num_sms,
+                                  cudaStream_t stream);
+unsigned read_rope_error(bool clear);
+
+// ---- draft_tree.cu: layout of drafted trees, and the accepted path's rows
+int tree_max_nodes();
+cudaError_t launch_tree_layout(const int32_t* parents, const int32_t* q_start, int num_seqs,
+                               int total_q, int max_q_len, const int32_t* context_lens,
+                               uint64_t* tree_mask, int64_t* positions, cudaStream_t stream);
+struct AcceptArgs {
+  uint4 *k_cache, *v_cache;
+  int64_t k_layer_vec, v_layer_vec;  // 16-byte vectors between layers
+  const int32_t *block_tables, *context_lens, *q_start, *accepted, *num_accepted;
+  int32_t* new_context_lens;
+  int num_seqs, max_accepted, max_blocks_per_seq, num_blocks;
+  int row_vec;     // 16-byte vectors per token row
+  int col_blocks;  // set by the launch
+};
+cudaError_t launch_accept_rows(const AcceptArgs& a, int num_layers, cudaStream_t stream);
+unsigned read_draft_error(bool clear);
+
+// ---- paged_tree.cu: attention of drafted trees
+struct TreeArgs {
+  const int32_t* q_start;
+  const uint64_t* tree_mask;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const void* v_cache;
+  void* out;
+  bool out_bf16;
+  float *part_o, *part_lse;  // 2 slots per CTA of tree_tiles() * tree_tile_rows() rows
+  void* start;               // 16 bytes per CTA
+  int num_seqs, total_q, max_q_len, q_heads, kv_heads, d_head, num_blocks, max_blocks_per_seq;
+  int ctas;
+  float scale_log2;
+};
+int tree_tile_rows();
+int tree_tiles(int group, int max_q_len);  // row tiles per CTA for these sizes
+cudaError_t launch_paged_tree(const TreeArgs& a, const CUtensorMap* tmap_q,
+                              const CUtensorMap* tmap_k, const CUtensorMap* tmap_v,
+                              cudaStream_t stream);
+unsigned read_tree_error(bool clear);
 
 }  // namespace pkv

@@ -34,6 +34,8 @@ DEVERR_BITS = {
     0x40: "query outside f16 range (fp8 decode)",
     0x80: "duplicate slot (checked append wrote nothing)",
     0x100: "prefix-group member without its group's prefix (decoded without it)",
+    0x200: "position outside the rotation table (token skipped)",
+    0x400: "drafted tree's parent or accepted path out of order",
 }
 
 
@@ -164,12 +166,34 @@ SIGNATURES = {
     "pkv_paged_verify_attention": ([_vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _vp,
                                     CacheDesc, _vp, ctypes.c_int, _vp, ctypes.c_int, _f32, _vp,
                                     _vp, _sz, ctypes.c_int, _vp], ctypes.c_int),
+    "pkv_qk_norm_rope_append": ([_vp, _i64, _vp, _i64, _vp, _i64, _i64, ctypes.c_int, _vp, _vp,
+                                 _i64, ctypes.c_int, ctypes.c_int, _vp, _vp, _f32, _vp, _vp, _vp,
+                                 _vp, CacheDesc, _vp], ctypes.c_int),
+    "pkv_qk_norm_rope_append_fp8": ([_vp, _i64, _vp, _i64, _vp, _i64, _i64, ctypes.c_int, _vp,
+                                     _vp, _i64, ctypes.c_int, ctypes.c_int, _vp, _vp, _f32, _vp,
+                                     _vp, _vp, _vp, CacheDesc, _f32, _f32, _vp], ctypes.c_int),
+    "pkv_draft_tree_layout": ([_vp, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp,
+                               _vp], ctypes.c_int),
+    "pkv_tree_attention_workspace_bytes": ([ctypes.c_int] * 5, _sz),
+    "pkv_paged_tree_attention": ([_vp, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                  ctypes.c_int, _vp, _vp, _vp, CacheDesc, _vp, ctypes.c_int, _vp,
+                                  _f32, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "pkv_paged_tree_attention_bf16out": ([_vp, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                          ctypes.c_int, _vp, _vp, _vp, CacheDesc, _vp,
+                                          ctypes.c_int, _vp, _f32, _vp, _vp, _sz, _vp],
+                                         ctypes.c_int),
+    "pkv_kv_accept_rows": ([_vp, _i64, _vp, _i64, ctypes.c_int, CacheDesc, _i32, _vp,
+                            ctypes.c_int, _vp, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp,
+                            _vp], ctypes.c_int),
     # host block manager (pagedkv_blocks.h); pointers are host memory
     "pkv_bm_create": ([_i32, _i32, ctypes.POINTER(_vp)], ctypes.c_int),
     "pkv_bm_destroy": ([_vp], None),
     "pkv_bm_add_sequence": ([_vp, _i64, _vp, _i32, ctypes.POINTER(_i32)], ctypes.c_int),
     "pkv_bm_append_tokens": ([_vp, _i64, _vp, _i32, _vp, _vp, _i32, ctypes.POINTER(_i32)],
                              ctypes.c_int),
+    "pkv_bm_reserve_draft": ([_vp, _i64, _i32, _vp, _vp, _i32, ctypes.POINTER(_i32)],
+                             ctypes.c_int),
+    "pkv_bm_commit_draft": ([_vp, _i64, _vp, _i32], ctypes.c_int),
     "pkv_bm_fork": ([_vp, _i64, _i64], ctypes.c_int),
     "pkv_bm_free_sequence": ([_vp, _i64], ctypes.c_int),
     "pkv_bm_slots": ([_vp, _i64, _i32, _i32, _vp], ctypes.c_int),
@@ -930,6 +954,229 @@ def describe_device_error(word: int) -> list[str]:
 
 
 # --------------------------------------------------------------------------
+# The speculative step with trees of drafted tokens.
+# --------------------------------------------------------------------------
+def _same_device(first: torch.Tensor, *others: Optional[torch.Tensor]):
+    """Every tensor on ``first``'s GPU; returns a context that makes it the
+    current device for the call (a launch goes to the current device)."""
+    for t in others:
+        _need(t is None or t.device == first.device, "all tensors must be on one GPU")
+    return torch.cuda.device(first.device)
+
+
+def _need_i32(t: torch.Tensor, name: str, *shape):
+    _need(t.is_cuda and t.dtype == torch.int32 and t.is_contiguous() and
+          tuple(t.shape) == shape, f"{name} must be a contiguous int32 CUDA tensor {list(shape)}")
+
+
+def _tree_batch(q_start: torch.Tensor, context_lens: torch.Tensor,
+                max_q_len: Optional[int]) -> tuple[int, int]:
+    _need(context_lens.dim() == 1, "context_lens must be [S]")
+    S = context_lens.shape[0]
+    _need_i32(context_lens, "context_lens", S)
+    _need_i32(q_start, "q_start", S + 1)
+    if max_q_len is None:
+        max_q_len = int((q_start[1:] - q_start[:-1]).max().item()) if S else 0
+    return S, int(max_q_len)
+
+
+def _rope_append(fn, name, pools, q, k, v, positions, rope_table, slot_mapping, k_cache, v_cache,
+                 scales, q_weight, k_weight, eps, interleaved, out):
+    pools(k_cache, v_cache)
+    hkv, d = k_cache.shape[2:]
+    _need(q.dim() == 3, "q must be [T, Hq, d]")
+    T, hq = q.shape[:2]
+    for x, n, heads in ((q, "q", hq), (k, "k", hkv), (v, "v", hkv)):
+        _need(x.is_cuda and x.dtype == torch.bfloat16 and tuple(x.shape) == (T, heads, d),
+              f"{n} must be a [T, heads, d] bf16 CUDA tensor")
+        _need(T == 0 or (x.stride(2) == 1 and (heads == 1 or x.stride(1) == d)),
+              f"each token row of {n} must be contiguous")
+    for x, n in ((positions, "positions"), (slot_mapping, "slot_mapping")):
+        _need(x.is_cuda and x.dtype == torch.int64 and x.is_contiguous() and x.shape == (T,),
+              f"{n} must be contiguous int64 [T] on the GPU")
+    _need(rope_table.is_cuda and rope_table.dtype == torch.float32 and rope_table.dim() == 2 and
+          rope_table.is_contiguous(), "rope_table must be contiguous float32 [positions, rot]")
+    for x, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        _need(x is None or (x.is_cuda and x.dtype == torch.bfloat16 and x.shape == (d,) and
+                            x.is_contiguous()), f"{n} must be contiguous bf16 [d]")
+    with _same_device(k_cache, q, k, v, v_cache, positions, rope_table, slot_mapping, q_weight,
+                      k_weight, out):
+        if out is None:
+            out = torch.empty(T, hq, d, dtype=torch.bfloat16, device=q.device)
+        _need(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == (T, hq, d),
+              "out must be contiguous bfloat16 [T, Hq, d]")
+        # a single token's stride is not used, but is checked: give its row
+        sq, sk, sv = (x.stride(0) if T > 1 else x.shape[1] * d for x in (q, k, v))
+        st = fn(_ptr(q), sq, _ptr(k), sk, _ptr(v), sv, T, hq, _ptr(positions), _ptr(rope_table),
+                rope_table.shape[0], rope_table.shape[1], int(bool(interleaved)), _ptr(q_weight),
+                _ptr(k_weight), float(eps), _ptr(slot_mapping), _ptr(out), _ptr(k_cache),
+                _ptr(v_cache), cache_desc(k_cache), *scales, _stream(k_cache))
+    _check(name, st)
+    return out
+
+
+def qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                        positions: torch.Tensor, rope_table: torch.Tensor,
+                        slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        q_weight: Optional[torch.Tensor] = None,
+                        k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                        interleaved: bool = False,
+                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Per-head RMS norm (with a weight ``[d]`` bf16) and rotary embedding of
+    ``q [T, Hq, d]`` and ``k [T, Hkv, d]``, and the append of the new keys and
+    ``v`` at ``slot_mapping`` (-1 skips), in one pass.  ``rope_table
+    [positions, rot]`` float32 holds cosines, then sines; pairs are ``(i, i +
+    rot/2)``, or ``(2i, 2i+1)`` when ``interleaved``.  Token rows may be
+    strided (views of a fused projection).  Returns the rotated queries, bf16
+    ``[T, Hq, d]``."""
+    return _rope_append(lib.pkv_qk_norm_rope_append, "pkv_qk_norm_rope_append", _check_cache, q, k,
+                        v, positions, rope_table, slot_mapping, k_cache, v_cache, (), q_weight,
+                        k_weight, eps, interleaved, out)
+
+
+def qk_norm_rope_append_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                            positions: torch.Tensor, rope_table: torch.Tensor,
+                            slot_mapping: torch.Tensor, k_cache: torch.Tensor,
+                            v_cache: torch.Tensor, k_scale: float, v_scale: float,
+                            q_weight: Optional[torch.Tensor] = None,
+                            k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                            interleaved: bool = False,
+                            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``qk_norm_rope_append`` into FP8 (e4m3) pools with per-pool scales: the
+    float32 keys and values are rounded once, to their codes."""
+    return _rope_append(lib.pkv_qk_norm_rope_append_fp8, "pkv_qk_norm_rope_append_fp8",
+                        _check_fp8_cache, q, k, v, positions, rope_table, slot_mapping, k_cache,
+                        v_cache, (float(k_scale), float(v_scale)), q_weight, k_weight, eps,
+                        interleaved, out)
+
+
+def draft_tree_layout(parents: torch.Tensor, q_start: torch.Tensor, context_lens: torch.Tensor,
+                      max_q_len: Optional[int] = None, tree_mask: Optional[torch.Tensor] = None,
+                      positions: Optional[torch.Tensor] = None):
+    """Ancestor masks and positions of drafted trees: ``parents [total]`` int32
+    (in each tree's own numbering, -1 = a child of the last committed token),
+    tree s being rows ``q_start[s]:q_start[s+1]`` (at most 64).  Returns
+    ``(tree_mask, positions)``, int64 ``[total]``: bit u of a node's word marks
+    node u as itself or an ancestor; its position is the committed length plus
+    its depth.  ``max_q_len`` (host int) bounds a tree's nodes; when omitted it
+    is read from ``q_start`` (a device sync)."""
+    _need(parents.dim() == 1, "parents must be [total]")
+    total = parents.shape[0]
+    _need_i32(parents, "parents", total)
+    S, max_q_len = _tree_batch(q_start, context_lens, max_q_len)
+    with _same_device(parents, q_start, context_lens, tree_mask, positions):
+        if tree_mask is None:
+            tree_mask = torch.empty(total, dtype=torch.int64, device=parents.device)
+        if positions is None:
+            positions = torch.empty(total, dtype=torch.int64, device=parents.device)
+        for t, n in ((tree_mask, "tree_mask"), (positions, "positions")):
+            _need(t.dtype == torch.int64 and t.is_contiguous() and t.shape == (total,),
+                  f"{n} must be contiguous int64 [total]")
+        st = lib.pkv_draft_tree_layout(_ptr(parents), _ptr(q_start), S, total, max_q_len,
+                                       _ptr(context_lens), _ptr(tree_mask), _ptr(positions),
+                                       _stream(parents))
+    _check("pkv_draft_tree_layout", st)
+    return tree_mask, positions
+
+
+def tree_attention_workspace(num_seqs: int, max_q_len: int, q_heads: int, kv_heads: int,
+                             d_head: int, device) -> torch.Tensor:
+    """Workspace for ``paged_tree_attention``: the pieces of trees whose keys
+    are divided between SMs (its size does not depend on the contexts)."""
+    with torch.cuda.device(device):
+        n = lib.pkv_tree_attention_workspace_bytes(int(num_seqs), int(max_q_len), int(q_heads),
+                                                   int(kv_heads), int(d_head))
+        _need(n > 0, "unsupported tree attention shape (more than 64 nodes?)")
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def paged_tree_attention(q: torch.Tensor, q_start: torch.Tensor, tree_mask: torch.Tensor,
+                         k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                         context_lens: torch.Tensor, scale: float,
+                         out: Optional[torch.Tensor] = None, max_q_len: Optional[int] = None,
+                         workspace: Optional[torch.Tensor] = None,
+                         out_dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """Attention of trees of drafted tokens: rows ``q_start[s]:q_start[s+1]``
+    (at most 64) of ``q [total, Hq, d]`` are the nodes of sequence s's tree,
+    already appended as the last positions of its context.  A node attends the
+    committed positions and the nodes of its ``tree_mask`` word (int64
+    ``[total]``, see ``draft_tree_layout``).  Returns ``out [total, Hq, d]``,
+    float32 unless ``out_dtype`` (or a given ``out``) is bfloat16.
+    ``max_q_len`` (host int) bounds a tree's nodes; when omitted it is read
+    from ``q_start`` (a device sync)."""
+    _check_cache(k_cache, v_cache)
+    _need(q.is_cuda and q.dtype == torch.bfloat16 and q.dim() == 3 and q.is_contiguous(),
+          "q must be a contiguous [total, Hq, d] bf16 CUDA tensor")
+    total, hq, d = q.shape
+    _need(d == k_cache.shape[3], "q and cache head dims differ")
+    S, max_q_len = _tree_batch(q_start, context_lens, max_q_len)
+    _need(tree_mask.is_cuda and tree_mask.dtype == torch.int64 and tree_mask.is_contiguous() and
+          tree_mask.shape == (total,), "tree_mask must be contiguous int64 [total] on the GPU")
+    _need(block_tables.dim() == 2, "block_tables must be [S, max_blocks]")
+    _need_i32(block_tables, "block_tables", S, block_tables.shape[1])
+    odt = _out_dtype(out, out_dtype)
+    with _same_device(q, q_start, tree_mask, k_cache, v_cache, block_tables, context_lens, out,
+                      workspace):
+        if out is None:
+            out = torch.empty(total, hq, d, dtype=odt, device=q.device)
+        _need(out.dtype == odt and out.is_contiguous() and out.shape == (total, hq, d),
+              "out must be contiguous float32 or bfloat16 [total, Hq, d]")
+        if workspace is None:
+            workspace = tree_attention_workspace(S, max_q_len, hq, k_cache.shape[2], d, q.device)
+        _need(workspace.is_cuda and workspace.dtype == torch.uint8 and workspace.is_contiguous(),
+              "workspace must be a contiguous uint8 CUDA tensor")
+        fn = (lib.pkv_paged_tree_attention_bf16out if odt == torch.bfloat16
+              else lib.pkv_paged_tree_attention)
+        st = fn(_ptr(q), _ptr(q_start), S, total, max_q_len, hq, _ptr(tree_mask), _ptr(k_cache),
+                _ptr(v_cache), cache_desc(k_cache), _ptr(block_tables), block_tables.shape[1],
+                _ptr(context_lens), float(scale), _ptr(out), _ptr(workspace), workspace.numel(),
+                _stream(q))
+    _check(fn.__name__, st)
+    return out
+
+
+def kv_accept_rows(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
+                   context_lens: torch.Tensor, q_start: torch.Tensor, accepted: torch.Tensor,
+                   num_accepted: torch.Tensor,
+                   new_context_lens: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Move each accepted path's K and V rows up behind the committed ones, in
+    place: position ``base + accepted[s, i]`` to ``base + i`` for ``i <
+    num_accepted[s]``, ``base`` being ``context_lens[s]`` minus its tree's
+    nodes.  The pools are one layer's ``[NB, 16, Hkv, d]`` or all layers'
+    ``[layers, NB, 16, Hkv, d]`` (bf16, or uint8 FP8 codes; each layer
+    contiguous).  Returns the new context lengths, int32 ``[S]``."""
+    for c in (k_cache, v_cache):
+        _need(c.is_cuda and c.dtype in (torch.bfloat16, torch.uint8) and c.dim() in (4, 5),
+              "pools must be [NB, 16, Hkv, d] or [layers, NB, 16, Hkv, d] bf16 or uint8 CUDA "
+              "tensors")
+    _need(k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype,
+          "k_cache and v_cache differ")
+    k5, v5 = ((c if c.dim() == 5 else c.unsqueeze(0)) for c in (k_cache, v_cache))
+    layers = k5.shape[0]
+    for c in (k5, v5):
+        _need(layers == 0 or c[0].is_contiguous(), "each layer's pool must be contiguous")
+    S, _ = _tree_batch(q_start, context_lens, 0)
+    _need(block_tables.dim() == 2, "block_tables must be [S, max_blocks]")
+    _need_i32(block_tables, "block_tables", S, block_tables.shape[1])
+    _need(accepted.dim() == 2, "accepted must be [S, max_accepted]")
+    _need_i32(accepted, "accepted", S, accepted.shape[1])
+    _need_i32(num_accepted, "num_accepted", S)
+    with _same_device(k_cache, v_cache, block_tables, context_lens, q_start, accepted,
+                      num_accepted, new_context_lens):
+        if new_context_lens is None:
+            new_context_lens = torch.empty(S, dtype=torch.int32, device=k_cache.device)
+        _need_i32(new_context_lens, "new_context_lens", S)
+        desc = CacheDesc(*k5.shape[1:])
+        st = lib.pkv_kv_accept_rows(_ptr(k_cache), k5.stride(0), _ptr(v_cache), v5.stride(0),
+                                    layers, desc, k_cache.element_size(), _ptr(block_tables),
+                                    block_tables.shape[1], _ptr(context_lens), _ptr(q_start), S,
+                                    _ptr(accepted), accepted.shape[1], _ptr(num_accepted),
+                                    _ptr(new_context_lens), _stream(k_cache))
+    _check("pkv_kv_accept_rows", st)
+    return new_context_lens
+
+
+# --------------------------------------------------------------------------
 # Host block manager (pagedkv_blocks.h) and the copy-on-write block copy.
 # --------------------------------------------------------------------------
 def _i32_host(values) -> "ctypes.Array":
@@ -979,6 +1226,23 @@ class BlockManager:
         _check("pkv_bm_append_tokens", lib.pkv_bm_append_tokens(
             self._h, int(seq_id), _i32_host(ids), len(ids), slots, pairs, 1, ctypes.byref(n)))
         return list(slots[:len(ids)]), [(pairs[0], pairs[1])] if n.value else []
+
+    def reserve_draft(self, seq_id: int, num_nodes: int):
+        """Slots for a tree of drafted tokens behind the sequence, and the (src,
+        dst) block copies to make first; ``commit_draft`` ends the draft."""
+        slots = (ctypes.c_int64 * max(1, num_nodes))()
+        pairs = (ctypes.c_int32 * 2)()
+        n = ctypes.c_int32()
+        _check("pkv_bm_reserve_draft", lib.pkv_bm_reserve_draft(
+            self._h, int(seq_id), int(num_nodes), slots, pairs, 1, ctypes.byref(n)))
+        return list(slots[:num_nodes]), [(pairs[0], pairs[1])] if n.value else []
+
+    def commit_draft(self, seq_id: int, token_ids) -> None:
+        """The accepted path's tokens join the sequence; the draft's other
+        blocks are freed."""
+        ids = list(token_ids)
+        _check("pkv_bm_commit_draft", lib.pkv_bm_commit_draft(self._h, int(seq_id),
+                                                              _i32_host(ids), len(ids)))
 
     def fork(self, parent: int, child: int) -> None:
         _check("pkv_bm_fork", lib.pkv_bm_fork(self._h, int(parent), int(child)))
