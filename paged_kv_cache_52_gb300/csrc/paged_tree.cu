@@ -54,9 +54,7 @@ static __device__ unsigned g_tree_error = 0;
 
 constexpr int kTrRows = 128;     // rows (node x head) per tile
 constexpr int kTrKeys = 128;     // keys per K/V tile (8 pages)
-constexpr int kTrMaxNodes = 64;  // nodes of a tree (bits of a mask)
 constexpr int kTrThreads = 384;
-constexpr int kTrSoftmaxThreads = 256;
 constexpr int kTrKWarp = 8, kTrMmaWarp = 9, kTrVWarp = 10, kTrQWarp = 11;
 constexpr uint32_t kTrTmemCols = 512;  // warpgroup w: S/P at 256 w, O at 256 w + 128
 constexpr float kTrRescale = 8.0f;     // log2 units: move the running max when it grows by > x256
@@ -77,9 +75,9 @@ struct TreeSmem {
   static constexpr int kBarOff = kXchOff + 2 * kTrRows * 8;
   static constexpr int kNumBars = 2 + 4 * kTrMaxStages + 6 + 3;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-  // tensor-memory base, abort flag, first sequence, pad; offset in it and
-  // tiles of this CTA (64 bit); non-finite nodes [2] (64 bit); scan [12] (64 bit)
-  static constexpr int kSmemBytes = kMiscOff + 16 + 16 + 16 + 96;
+  // tensor-memory base, abort flag; non-finite nodes [2] (64 bit); scan [12]
+  // (64 bit); the start of the range
+  static constexpr int kSmemBytes = kMiscOff + 16 + 16 + 96 + 48;
   static_assert(kSmemBytes <= 232448, "tree tile does not fit in shared memory");
   static_assert(kKStages <= kTrMaxStages && kVStages <= kTrMaxStages, "ring stages");
 };
@@ -92,10 +90,11 @@ enum TrBar {
   kTrXch = kTrODone + 2, kTrEpi = kTrXch + 1, kTrDrain = kTrEpi + 1
 };
 
-// What a CTA's range starts in, for the merge: sequence (-1: no work), item
-// of the sequence, first key tile, unused.
-struct TreeStart {
-  int seq, item, tile, pad;
+// Where a CTA's range starts, for the merge: sequence (-1: no work), item of
+// the sequence, first key tile, and the sequence's first row, nodes and row
+// groups.
+struct __align__(16) TreeStart {
+  int seq, item, tile, qs, n, groups, pad[2];
 };
 
 struct TreeParams {
@@ -146,15 +145,11 @@ struct TreeWalk {
   int left;        // tiles of the range after the current piece
   TreeSeq seq;
   int item, first, tiles;  // current piece
-  bool loaded = false;
-  __device__ __forceinline__ TreeWalk(const TreeParams& pp, int s0, long long off0, int count)
-      : p(pp), s(s0), off(off0), left(count) {}
+  __device__ __forceinline__ TreeWalk(const TreeParams& pp, const TreeSeq& q0, int s0,
+                                      long long off0, int count)
+      : p(pp), s(s0), off(off0), left(count), seq(q0) {}
   __device__ __forceinline__ bool next() {
     if (left <= 0) return false;
-    if (!loaded) {
-      seq = tree_seq<G, TILES>(p, s);
-      loaded = true;
-    }
     while (off >= seq.total(p.kv_heads)) {
       if (++s >= p.num_seqs) return false;
       off = 0;
@@ -224,63 +219,27 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
   const uint32_t bars = sbase + T::kBarOff;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + T::kMiscOff + 4);
-  int* start_seq = reinterpret_cast<int*>(smem + T::kMiscOff + 8);
-  long long* start_off = reinterpret_cast<long long*>(smem + T::kMiscOff + 16);
-  unsigned long long* nonfinite = reinterpret_cast<unsigned long long*>(smem + T::kMiscOff + 32);
-  long long* scan = reinterpret_cast<long long*>(smem + T::kMiscOff + 48);
+  unsigned long long* nonfinite = reinterpret_cast<unsigned long long*>(smem + T::kMiscOff + 16);
+  long long* scan = reinterpret_cast<long long*>(smem + T::kMiscOff + 32);
+  struct Begin {
+    long long off;
+    TreeSeq seq;
+    int s;
+  };
+  static_assert(sizeof(Begin) <= 48, "start of the range");
+  Begin* begin = reinterpret_cast<Begin*>(smem + T::kMiscOff + 128);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  griddep_wait();  // inputs may have been written by the previous kernel in the stream
-
-  // ---- this CTA's range of the key tiles of all items
-  const int per_thread = (p.num_seqs + kTrThreads - 1) / kTrThreads;
-  const int s_lo = min(int(threadIdx.x) * per_thread, p.num_seqs);
-  const int s_hi = min(s_lo + per_thread, p.num_seqs);
-  long long mine = 0;
-  for (int s = s_lo; s < s_hi; ++s) {
-    const TreeSeq q = tree_seq<G, TILES>(p, s);
-    if (q.bad && blockIdx.x == 0) atomicOr(&g_tree_error, kErrBadQueryRange);
-    mine += q.total(p.kv_heads);
-  }
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
-  }
-  if (lane == 31) scan[warp] = incl;
-  if (threadIdx.x == 0) *abort_flag = 0, *start_seq = p.num_seqs, nonfinite[0] = nonfinite[1] = 0;
-  __syncthreads();
-  long long all = 0;
-#pragma unroll
-  for (int w = 0; w < kTrThreads / 32; ++w) {
-    if (w == warp) incl += all;
-    all += scan[w];
-  }
-  // with fewer tiles than CTAs the last CTAs have none, so that a cut item's
-  // pieces lie in consecutive CTAs
-  const long long active = min((long long)gridDim.x, all), c = blockIdx.x;
-  const long long lo = c < active ? all * c / active : all;
-  const int count = c < active ? int(all * (c + 1) / active - lo) : 0;
-  if (lo >= incl - mine && lo < incl) {  // the range starts in this thread's sequences
-    long long at = lo - (incl - mine);
-    for (int s = s_lo; s < s_hi; ++s) {
-      const long long w = tree_seq<G, TILES>(p, s).total(p.kv_heads);
-      if (at < w) {
-        *start_seq = s;
-        *start_off = at;
-        break;
-      }
-      at -= w;
-    }
-  }
-  if (count > 0 && warp == 0) {
+  // ---- set-up that reads no input, beside the previous kernel's end
+  griddep_launch_dependents();  // the merge waits for this grid before it reads
+  if (warp == 0) {
     tmem_alloc(smem_u32(tmem_slot), kTrTmemCols);
     tmem_relinquish();
   }
   if (threadIdx.x == kTrKWarp * 32) {
     mbar_init(bars + 8 * kTrQFull, 1);
     mbar_init(bars + 8 * kTrQEmpty, 1);
+#pragma unroll 1
     for (int s = 0; s < kTrMaxStages; ++s) {
       mbar_init(bars + 8 * (kTrKFull + s), 1);
       mbar_init(bars + 8 * (kTrKEmpty + s), 1);
@@ -296,23 +255,69 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     mbar_init(bars + 8 * kTrEpi, 8);
     mbar_init(bars + 8 * kTrDrain, 1);
     fence_barrier_init();
+    *abort_flag = 0;
+    nonfinite[0] = nonfinite[1] = 0;
   }
+  if (threadIdx.x == kTrVWarp * 32) tma_prefetch_desc(&tmap_v);
+  if (threadIdx.x == kTrQWarp * 32) {
+    tma_prefetch_desc(&tmap_k);
+    tma_prefetch_desc(&tmap_q);
+  }
+  griddep_wait();  // inputs may have been written by the previous kernel in the stream
+
+  // ---- this CTA's range of the key tiles of all items
+  const int per_thread = (p.num_seqs + kTrThreads - 1) / kTrThreads;
+  const int s_lo = min(int(threadIdx.x) * per_thread, p.num_seqs);
+  const int s_hi = min(s_lo + per_thread, p.num_seqs);
+  long long mine = 0;
+  TreeSeq q{};
+  for (int s = s_lo; s < s_hi; ++s) {
+    q = tree_seq<G, TILES>(p, s);
+    if (q.bad && blockIdx.x == 0) atomicOr(&g_tree_error, kErrBadQueryRange);
+    mine += q.total(p.kv_heads);
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  if (lane == 31) scan[warp] = incl;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (threadIdx.x == 0) {
-    TreeStart st{-1, 0, 0, 0};
-    if (count > 0) {
-      const int tiles = tree_seq<G, TILES>(p, *start_seq).tiles;
-      st.seq = *start_seq;
-      st.item = int(*start_off / tiles);
-      st.tile = int(*start_off % tiles);
-    }
-    p.start[blockIdx.x] = st;
-  }
-  if (count == 0) return;  // uniform over the CTA; no tensor memory held
   const uint32_t tmem = *tmem_slot;
-  TreeWalk<G, TILES> walk(p, *start_seq, *start_off, count);
+  long long all = 0;
+#pragma unroll
+  for (int w = 0; w < kTrThreads / 32; ++w) {
+    if (w == warp) incl += all;
+    all += scan[w];
+  }
+  // with fewer tiles than CTAs the last CTAs have none, so that a cut item's
+  // pieces lie in consecutive CTAs
+  const long long active = min((long long)gridDim.x, all), c = blockIdx.x;
+  const long long lo = c < active ? all * c / active : all;
+  const int count = c < active ? int(all * (c + 1) / active - lo) : 0;
+  if (lo >= incl - mine && lo < incl) {  // the range starts in this thread's sequences
+    long long at = lo - (incl - mine);
+    int s = s_lo;
+    if (per_thread > 1)
+      for (;; ++s) {
+        q = tree_seq<G, TILES>(p, s);
+        const long long w = q.total(p.kv_heads);
+        if (at < w) break;
+        at -= w;
+      }
+    *begin = Begin{at, q, s};
+    const int item = int(at / q.tiles);
+    p.start[c] = TreeStart{count > 0 ? s : -1, item, int(at - (long long)item * q.tiles), q.qs,
+                           q.n, q.groups, {0, 0}};
+  } else if (lo >= all && threadIdx.x == 0) {
+    p.start[c].seq = -1;
+  }
+  __syncthreads();
+  if (count > 0) {
+  TreeWalk<G, TILES> walk(p, begin->seq, begin->s, begin->off, count);
 
   if (warp == kTrKWarp || warp == kTrVWarp) {
     // ================= K and V rings =================
@@ -323,7 +328,6 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     const uint32_t empty = bars + 8 * (is_v ? kTrVEmpty : kTrKEmpty);
     const CUtensorMap* map = is_v ? &tmap_v : &tmap_k;
     constexpr int kLoads = 8 * (D / 64);  // pages x column halves
-    if (lane == 0) tma_prefetch_desc(map);
     int i = 0;
     bool ok = true;
     while (ok && walk.next()) {
@@ -373,7 +377,6 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
   } else if (warp == kTrQWarp) {
     // ================= Q =================
     if (lane == 0) {
-      tma_prefetch_desc(&tmap_q);
       int k = 0;
       bool ok = true;
       for (; walk.next(); ++k) {
@@ -544,35 +547,38 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (!ok) break;
         tc_fence_after();
         if (warp_valid) {
-          uint32_t bits[4];
+          if (masked) {
+            // hidden keys' scores become what weighs nothing: -inf after scaling
+            const float hide = neg ? INFINITY : -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < kTrKeys; c += 32) {
+              const uint32_t bits = key_bits(mask, key0 + c - base);
+              float x[32];
+              tmem_ld32(lane_base + s_col + c, x);
+              tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) bits[c] = masked ? key_bits(mask, key0 + 32 * c - base) : ~0u;
-          // the tile's max over the keys this row sees
-          float ex[8];
-#pragma unroll
-          for (int a = 0; a < 8; ++a) ex[a] = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; c += 2) {
+              for (int u = 0; u < 32; ++u) x[u] = (bits >> u) & 1u ? x[u] : hide;
+              tmem_st32(lane_base + s_col + c, x);
+            }
+            tmem_wait_st();
+          }
+          // the tile's max
+          float ex[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c = 0; c < kTrKeys; c += 64) {
             float va[32], vb[32];
-            tmem_ld32(lane_base + s_col + c * 32, va);
-            tmem_ld32(lane_base + s_col + c * 32 + 32, vb);
+            tmem_ld32(lane_base + s_col + c, va);
+            tmem_ld32(lane_base + s_col + c + 32, vb);
             tmem_wait_ld();
             if (neg) {
 #pragma unroll
-              for (int u = 0; u < 32; ++u) va[u] = -va[u], vb[u] = -vb[u];
-            }
-            if (masked) {
+              for (int u = 0; u < 32; ++u) ex[u & 3] = max3f(ex[u & 3], -va[u], -vb[u]);
+            } else {
 #pragma unroll
-              for (int u = 0; u < 32; ++u) {
-                va[u] = (bits[c] >> u) & 1u ? va[u] : -INFINITY;
-                vb[u] = (bits[c + 1] >> u) & 1u ? vb[u] : -INFINITY;
-              }
+              for (int u = 0; u < 32; ++u) ex[u & 3] = max3f(ex[u & 3], va[u], vb[u]);
             }
-#pragma unroll
-            for (int u = 0; u < 32; ++u) ex[u & 7] = max3f(ex[u & 7], va[u], vb[u]);
           }
-          const float top = fmaxf(fmaxf(fmaxf(ex[0], ex[1]), fmaxf(ex[2], ex[3])),
-                                  fmaxf(fmaxf(ex[4], ex[5]), fmaxf(ex[6], ex[7])));
+          const float top = fmaxf(fmaxf(ex[0], ex[1]), fmaxf(ex[2], ex[3]));
           const float mx = top == -INFINITY ? -INFINITY : top * mag;
           const bool move = mx > m + kTrRescale || (m == -INFINITY && mx > m);
           if (__any_sync(0xffffffffu, move)) {
@@ -584,15 +590,15 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
               if (!ok) break;
               tc_fence_after();
               const uint64_t a2 = f2_pack(alpha, alpha);
-#pragma unroll
-              for (int c = 0; c < D / 32; ++c) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
                 float o[32];
-                tmem_ld32(lane_base + o_col + c * 32, o);
+                tmem_ld32(lane_base + o_col + c, o);
                 tmem_wait_ld();
 #pragma unroll
                 for (int u = 0; u < 32; u += 2)
                   f2_unpack(f2_mul(f2_pack(o[u], o[u + 1]), a2), o[u], o[u + 1]);
-                tmem_st32(lane_base + o_col + c * 32, o);
+                tmem_st32(lane_base + o_col + c, o);
               }
             }
             l *= alpha;
@@ -604,11 +610,11 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
           const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
           const uint64_t nm2 = f2_pack(-mref, -mref);
           uint64_t ls[2] = {0ull, 0ull};
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
+#pragma unroll 1
+          for (int c = 0; c < kTrKeys; c += 64) {
             float va[32], vb[32];
-            tmem_ld32(lane_base + s_col + 64 * g, va);
-            tmem_ld32(lane_base + s_col + 64 * g + 32, vb);
+            tmem_ld32(lane_base + s_col + c, va);
+            tmem_ld32(lane_base + s_col + c + 32, vb);
             tmem_wait_ld();
             uint32_t hi[32], lo[32];
 #pragma unroll
@@ -618,21 +624,16 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
               const float s1 = kk < 32 ? va[kk + 1] : vb[kk - 31];
               float x0, x1;
               f2_unpack(f2_fma(f2_pack(s0, s1), sc2, nm2), x0, x1);
-              float e0 = ex2(x0), e1 = ex2(x1);
-              if (masked) {
-                const uint32_t b = bits[2 * g + (kk >> 5)];
-                e0 = (b >> (kk & 31)) & 1u ? e0 : 0.f;
-                e1 = (b >> ((kk & 31) + 1)) & 1u ? e1 : 0.f;
-              }
-              const uint64_t e = f2_pack(e0, e1);
+              const uint64_t e = f2_pack(ex2(x0), ex2(x1));
               ls[u & 1] = f2_add(ls[u & 1], e);
+              float e0, e1, r0, r1;
+              f2_unpack(e, e0, e1);
               hi[u] = pack_bf16x2(e0, e1);
-              float r0, r1;
               f2_unpack(f2_sub(e, f2_pack(bf16_lo_to_f32(hi[u]), bf16_hi_to_f32(hi[u]))), r0, r1);
               lo[u] = pack_bf16x2(r0, r1);
             }
-            tmem_st32u(lane_base + s_col + 64 * g, hi);
-            tmem_st32u(lane_base + s_col + 64 * g + 32, lo);
+            tmem_st32u(lane_base + s_col + c, hi);
+            tmem_st32u(lane_base + s_col + c + 32, lo);
           }
           float a0, a1, b0, b1;
           f2_unpack(ls[0], a0, a1);
@@ -649,9 +650,9 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
           if (key >= base) {
             const uint32_t row = sbase + T::kVOff + (it % T::kVStages) * T::kTileBytes + r * 128;
             uint32_t any = 0;
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < D / 64; ++h)
-#pragma unroll
+#pragma unroll 4
               for (int c = 0; c < 8; ++c) {
                 const uint32_t at = row + h * T::kHalf + (((c + r) & 7) << 4);
                 const uint4 v = ld_shared_u4(at);
@@ -795,6 +796,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
     if (!ok && lane == 0) tr_abort(abort_flag);
   }
+  }  // count > 0
 
   tc_fence_before();
   __syncthreads();
@@ -816,28 +818,32 @@ __global__ void __launch_bounds__(kTrMergeWarps * 32)
 tree_merge_kernel(const TreeParams p, int ctas) {
   griddep_wait();
   const int b = blockIdx.x + 1;
-  const TreeStart here = p.start[b];
-  if (here.seq < 0 || here.tile == 0) return;
-  const TreeStart before = p.start[b - 1];
-  const bool same = before.seq == here.seq && before.item == here.item;
-  if (same && before.tile > 0) return;
-  const TreeSeq q = tree_seq<G, TILES>(p, here.seq);
-  const int kvh = here.item / q.groups, group = here.item % q.groups;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // lane i: CTA b - 1 + i; the CTAs b, b + 1, ... whose ranges start in the item
+  TreeStart at{-1, 0, 0, 0, 0, 0, {0, 0}};
+  if (b - 1 + lane < ctas) at = p.start[b - 1 + lane];
+  const int seq = __shfl_sync(0xffffffffu, at.seq, 1);
+  const int item = __shfl_sync(0xffffffffu, at.item, 1);
+  if (seq < 0 || __shfl_sync(0xffffffffu, at.tile, 1) == 0) return;
+  const bool mine = at.seq == seq && at.item == item;
+  unsigned vote = __ballot_sync(0xffffffffu, mine);
+  const bool same = vote & 1u;  // CTA b - 1's range starts in the item, too
+  if (same && __shfl_sync(0xffffffffu, at.tile, 0) > 0) return;
+  const int qs = __shfl_sync(0xffffffffu, at.qs, 1);
+  const int nodes = __shfl_sync(0xffffffffu, at.n, 1);
+  const int groups = __shfl_sync(0xffffffffu, at.groups, 1);
+  const int kvh = item / groups, group = item - kvh * groups;
   const int r = blockIdx.y * kTrMergeWarps + warp;  // row of the group
   const int node = group * TILES * (kTrRows / G) + r / G;
-  if (node >= q.n) return;
-  // CTAs b, b + 1, ... whose ranges start in the item, 32 looked at at a time
-  int parts = 1;
-  for (int c = b;; c += 32) {
-    bool mine = false;
-    if (c + lane < ctas) {
-      const TreeStart s = p.start[c + lane];
-      mine = s.seq == here.seq && s.item == here.item;
-    }
-    const unsigned vote = __ballot_sync(0xffffffffu, mine);
+  if (node >= nodes) return;
+  vote |= 1u;
+  int parts = vote == 0xffffffffu ? 32 : __ffs(~vote) - 1;
+  while (parts % 32 == 0) {  // more than the lanes look at at a time
+    const int c = b - 1 + parts + lane;
+    const bool more = c < ctas && p.start[c].seq == seq && p.start[c].item == item;
+    vote = __ballot_sync(0xffffffffu, more);
+    if (vote == 0) break;
     parts += vote == 0xffffffffu ? 32 : __ffs(~vote) - 1;
-    if (vote != 0xffffffffu) break;
   }
   auto row_of = [&](int i) {  // piece i's row in the workspace
     const size_t slot = i == 0 ? size_t(b - 1) * 2 + (same ? 0 : 1) : size_t(b + i - 1) * 2;
@@ -880,14 +886,14 @@ tree_merge_kernel(const TreeParams p, int ctas) {
     }
   }
   const float inv = tot != 0.f ? 1.f / tot : 0.f;
-  const size_t at = ((size_t(q.qs) + node) * p.q_heads + size_t(kvh) * G + r % G) * D + lane * V;
+  const size_t to = ((size_t(qs) + node) * p.q_heads + size_t(kvh) * G + r % G) * D + lane * V;
 #pragma unroll
   for (int u = 0; u < V; u += 2) {
     if (p.out_bf16)
-      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at + u) =
+      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + to + u) =
           pack_bf16x2(acc[u] * inv, acc[u + 1] * inv);
     else
-      *reinterpret_cast<float2*>(static_cast<float*>(p.out) + at + u) =
+      *reinterpret_cast<float2*>(static_cast<float*>(p.out) + to + u) =
           make_float2(acc[u] * inv, acc[u + 1] * inv);
   }
 }

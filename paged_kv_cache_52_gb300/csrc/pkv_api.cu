@@ -1888,7 +1888,7 @@ int tree_layout(int max_q_len, int q_heads, int kv_heads, int d_head, TreeLayout
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t rows = size_t(w->ctas) * 2 * size_t(pkv::tree_tile_rows()) *
                       size_t(pkv::tree_tiles(q_heads / kv_heads, max_q_len));
-  w->lse_off = up(size_t(w->ctas) * 16);
+  w->lse_off = up(size_t(w->ctas) * 32);
   w->o_off = w->lse_off + up(rows * 4);
   w->total = w->o_off + rows * size_t(d_head) * 4;
   return PKV_OK;
@@ -1938,7 +1938,9 @@ int tree_attention(const void* q, const int32_t* q_start, int num_seqs, int tota
   a.num_blocks = cache.num_blocks;
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.ctas = w.ctas;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  // a scale of 0 weighs every visible key alike: so does one too small to
+  // tell scores apart, which keeps a hidden key's -inf out of 0 * inf
+  a.scale_log2 = scale == 0.f ? 1e-30f : scale * 1.4426950408889634f;
   const cudaError_t e =
       pkv::launch_paged_tree(a, &tq, &tk, &tv, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKV_OK : PKV_ECUDA;

@@ -288,7 +288,7 @@ struct TreeArgs {
   void* out;
   bool out_bf16;
   float *part_o, *part_lse;  // 2 slots per CTA of tree_tiles() * tree_tile_rows() rows
-  void* start;               // 16 bytes per CTA
+  void* start;               // 32 bytes per CTA
   int num_seqs, total_q, max_q_len, q_heads, kv_heads, d_head, num_blocks, max_blocks_per_seq;
   int ctas;
   float scale_log2;

@@ -10,6 +10,7 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -956,62 +957,115 @@ def describe_device_error(word: int) -> list[str]:
 # --------------------------------------------------------------------------
 # The speculative step with trees of drafted tokens.
 # --------------------------------------------------------------------------
-def _same_device(first: torch.Tensor, *others: Optional[torch.Tensor]):
-    """Every tensor on ``first``'s GPU; returns a context that makes it the
-    current device for the call (a launch goes to the current device)."""
-    for t in others:
-        _need(t is None or t.device == first.device, "all tensors must be on one GPU")
-    return torch.cuda.device(first.device)
+# These calls take a few microseconds on the GPU for one user's step, less than
+# a slow argument check: the checks below read each tensor's device, type and
+# layout once, and build their messages only to raise.
+_BF16, _F32, _I32, _I64, _U8 = (torch.bfloat16, torch.float32, torch.int32, torch.int64,
+                                torch.uint8)
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _need_i32(t: torch.Tensor, name: str, *shape):
-    _need(t.is_cuda and t.dtype == torch.int32 and t.is_contiguous() and
-          tuple(t.shape) == shape, f"{name} must be a contiguous int32 CUDA tensor {list(shape)}")
+@functools.lru_cache(maxsize=256)
+def _desc(num_blocks: int, block_size: int, kv_heads: int, d_head: int) -> CacheDesc:
+    return CacheDesc(num_blocks, block_size, kv_heads, d_head)
 
 
-def _tree_batch(q_start: torch.Tensor, context_lens: torch.Tensor,
-                max_q_len: Optional[int]) -> tuple[int, int]:
-    _need(context_lens.dim() == 1, "context_lens must be [S]")
+def _refuse(name: str, what: str):
+    raise ValueError(f"{name} must be {what}")
+
+
+def _check_packed(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int, *shape: int):
+    """A contiguous tensor of this type and shape on GPU ``dev``."""
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
+        _refuse(name, f"a contiguous {dtype} tensor {list(shape)} on one GPU with the others")
+
+
+def _pools(k_cache: torch.Tensor, v_cache: torch.Tensor, *dtypes: torch.dtype) -> int:
+    """The GPU of two pools of one of these types, alike in shape."""
+    dev = k_cache.get_device()
+    if dev < 0 or v_cache.get_device() != dev:
+        _refuse("k_cache and v_cache", "CUDA tensors on one GPU")
+    if k_cache.dtype not in dtypes or v_cache.dtype is not k_cache.dtype:
+        _refuse("k_cache and v_cache", f"of one type, {' or '.join(map(str, dtypes))}")
+    if v_cache.shape != k_cache.shape:
+        _refuse("k_cache and v_cache", "of one shape")
+    return dev
+
+
+def _launch(dev: int, fn, *args):
+    """``fn(*args, stream)`` on GPU ``dev``'s current stream; a launch goes to
+    the current device, so that is switched when it is another."""
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(dev))
+    if st:
+        _check(fn.__name__, st)
+
+
+def _tree_batch(q_start: torch.Tensor, context_lens: torch.Tensor, dev: int,
+                max_q_len: Optional[int] = None) -> tuple[int, int]:
+    if context_lens.dim() != 1:
+        _refuse("context_lens", "[S]")
     S = context_lens.shape[0]
-    _need_i32(context_lens, "context_lens", S)
-    _need_i32(q_start, "q_start", S + 1)
+    _check_packed(context_lens, "context_lens", _I32, dev, S)
+    _check_packed(q_start, "q_start", _I32, dev, S + 1)
     if max_q_len is None:
-        max_q_len = int((q_start[1:] - q_start[:-1]).max().item()) if S else 0
+        max_q_len = int((q_start[1:] - q_start[:-1]).max()) if S else 0
     return S, int(max_q_len)
 
 
-def _rope_append(fn, name, pools, q, k, v, positions, rope_table, slot_mapping, k_cache, v_cache,
+def _tables(block_tables: torch.Tensor, dev: int, S: int) -> int:
+    if block_tables.dim() != 2:
+        _refuse("block_tables", "[S, max_blocks]")
+    width = block_tables.shape[1]
+    _check_packed(block_tables, "block_tables", _I32, dev, S, width)
+    return width
+
+
+def _token_rows(x: torch.Tensor, name: str, dev: int, T: int, heads: int, d: int) -> int:
+    """The token stride of ``x [T, heads, d]`` bf16 with contiguous rows."""
+    if x.dtype is not _BF16 or x.get_device() != dev or x.shape != (T, heads, d):
+        _refuse(name, f"a bfloat16 tensor [{T}, {heads}, {d}] on one GPU with the pools")
+    st, sh, sd = x.stride()
+    if T and (sd != 1 or (heads > 1 and sh != d)):
+        _refuse(name, "contiguous within each token's row")
+    return st if T > 1 else heads * d  # the stride of a single token is not used
+
+
+def _rope_append(fn, pool_dtype, q, k, v, positions, rope_table, slot_mapping, k_cache, v_cache,
                  scales, q_weight, k_weight, eps, interleaved, out):
-    pools(k_cache, v_cache)
-    hkv, d = k_cache.shape[2:]
-    _need(q.dim() == 3, "q must be [T, Hq, d]")
-    T, hq = q.shape[:2]
-    for x, n, heads in ((q, "q", hq), (k, "k", hkv), (v, "v", hkv)):
-        _need(x.is_cuda and x.dtype == torch.bfloat16 and tuple(x.shape) == (T, heads, d),
-              f"{n} must be a [T, heads, d] bf16 CUDA tensor")
-        _need(T == 0 or (x.stride(2) == 1 and (heads == 1 or x.stride(1) == d)),
-              f"each token row of {n} must be contiguous")
-    for x, n in ((positions, "positions"), (slot_mapping, "slot_mapping")):
-        _need(x.is_cuda and x.dtype == torch.int64 and x.is_contiguous() and x.shape == (T,),
-              f"{n} must be contiguous int64 [T] on the GPU")
-    _need(rope_table.is_cuda and rope_table.dtype == torch.float32 and rope_table.dim() == 2 and
-          rope_table.is_contiguous(), "rope_table must be contiguous float32 [positions, rot]")
-    for x, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        _need(x is None or (x.is_cuda and x.dtype == torch.bfloat16 and x.shape == (d,) and
-                            x.is_contiguous()), f"{n} must be contiguous bf16 [d]")
-    with _same_device(k_cache, q, k, v, v_cache, positions, rope_table, slot_mapping, q_weight,
-                      k_weight, out):
-        if out is None:
-            out = torch.empty(T, hq, d, dtype=torch.bfloat16, device=q.device)
-        _need(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == (T, hq, d),
-              "out must be contiguous bfloat16 [T, Hq, d]")
-        # a single token's stride is not used, but is checked: give its row
-        sq, sk, sv = (x.stride(0) if T > 1 else x.shape[1] * d for x in (q, k, v))
-        st = fn(_ptr(q), sq, _ptr(k), sk, _ptr(v), sv, T, hq, _ptr(positions), _ptr(rope_table),
-                rope_table.shape[0], rope_table.shape[1], int(bool(interleaved)), _ptr(q_weight),
-                _ptr(k_weight), float(eps), _ptr(slot_mapping), _ptr(out), _ptr(k_cache),
-                _ptr(v_cache), cache_desc(k_cache), *scales, _stream(k_cache))
-    _check(name, st)
+    dev = _pools(k_cache, v_cache, pool_dtype)
+    if k_cache.dim() != 4 or q.dim() != 3 or rope_table.dim() != 2:
+        _refuse("pools, q and rope_table",
+                "[NB, 16, Hkv, d], [T, Hq, d] and [positions, rot]")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        _refuse("pools", "contiguous")
+    nb, bs, hkv, d = k_cache.shape
+    T, hq = q.shape[0], q.shape[1]
+    sq = _token_rows(q, "q", dev, T, hq, d)
+    sk = _token_rows(k, "k", dev, T, hkv, d)
+    sv = _token_rows(v, "v", dev, T, hkv, d)
+    _check_packed(positions, "positions", _I64, dev, T)
+    _check_packed(slot_mapping, "slot_mapping", _I64, dev, T)
+    rows, rot = rope_table.shape
+    _check_packed(rope_table, "rope_table", _F32, dev, rows, rot)
+    qw = kw = None
+    if q_weight is not None:
+        _check_packed(q_weight, "q_weight", _BF16, dev, d)
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        _check_packed(k_weight, "k_weight", _BF16, dev, d)
+        kw = k_weight.data_ptr()
+    if out is None:
+        out = q.new_empty((T, hq, d))
+    else:
+        _check_packed(out, "out", _BF16, dev, T, hq, d)
+    _launch(dev, fn, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, T, hq,
+            positions.data_ptr(), rope_table.data_ptr(), rows, rot, 1 if interleaved else 0, qw,
+            kw, eps, slot_mapping.data_ptr(), out.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), _desc(nb, bs, hkv, d), *scales)
     return out
 
 
@@ -1029,9 +1083,9 @@ def qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     rot/2)``, or ``(2i, 2i+1)`` when ``interleaved``.  Token rows may be
     strided (views of a fused projection).  Returns the rotated queries, bf16
     ``[T, Hq, d]``."""
-    return _rope_append(lib.pkv_qk_norm_rope_append, "pkv_qk_norm_rope_append", _check_cache, q, k,
-                        v, positions, rope_table, slot_mapping, k_cache, v_cache, (), q_weight,
-                        k_weight, eps, interleaved, out)
+    return _rope_append(lib.pkv_qk_norm_rope_append, _BF16, q, k, v, positions, rope_table,
+                        slot_mapping, k_cache, v_cache, (), q_weight, k_weight, eps, interleaved,
+                        out)
 
 
 def qk_norm_rope_append_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -1044,10 +1098,9 @@ def qk_norm_rope_append_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                             out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """``qk_norm_rope_append`` into FP8 (e4m3) pools with per-pool scales: the
     float32 keys and values are rounded once, to their codes."""
-    return _rope_append(lib.pkv_qk_norm_rope_append_fp8, "pkv_qk_norm_rope_append_fp8",
-                        _check_fp8_cache, q, k, v, positions, rope_table, slot_mapping, k_cache,
-                        v_cache, (float(k_scale), float(v_scale)), q_weight, k_weight, eps,
-                        interleaved, out)
+    return _rope_append(lib.pkv_qk_norm_rope_append_fp8, _U8, q, k, v, positions, rope_table,
+                        slot_mapping, k_cache, v_cache, (k_scale, v_scale), q_weight, k_weight,
+                        eps, interleaved, out)
 
 
 def draft_tree_layout(parents: torch.Tensor, q_start: torch.Tensor, context_lens: torch.Tensor,
@@ -1060,22 +1113,22 @@ def draft_tree_layout(parents: torch.Tensor, q_start: torch.Tensor, context_lens
     node u as itself or an ancestor; its position is the committed length plus
     its depth.  ``max_q_len`` (host int) bounds a tree's nodes; when omitted it
     is read from ``q_start`` (a device sync)."""
-    _need(parents.dim() == 1, "parents must be [total]")
+    dev = parents.get_device()
+    if dev < 0 or parents.dim() != 1:
+        _refuse("parents", "a CUDA tensor [total]")
     total = parents.shape[0]
-    _need_i32(parents, "parents", total)
-    S, max_q_len = _tree_batch(q_start, context_lens, max_q_len)
-    with _same_device(parents, q_start, context_lens, tree_mask, positions):
-        if tree_mask is None:
-            tree_mask = torch.empty(total, dtype=torch.int64, device=parents.device)
-        if positions is None:
-            positions = torch.empty(total, dtype=torch.int64, device=parents.device)
-        for t, n in ((tree_mask, "tree_mask"), (positions, "positions")):
-            _need(t.dtype == torch.int64 and t.is_contiguous() and t.shape == (total,),
-                  f"{n} must be contiguous int64 [total]")
-        st = lib.pkv_draft_tree_layout(_ptr(parents), _ptr(q_start), S, total, max_q_len,
-                                       _ptr(context_lens), _ptr(tree_mask), _ptr(positions),
-                                       _stream(parents))
-    _check("pkv_draft_tree_layout", st)
+    _check_packed(parents, "parents", _I32, dev, total)
+    S, max_q_len = _tree_batch(q_start, context_lens, dev, max_q_len)
+    if tree_mask is None:
+        tree_mask = parents.new_empty((total,), dtype=_I64)
+    else:
+        _check_packed(tree_mask, "tree_mask", _I64, dev, total)
+    if positions is None:
+        positions = parents.new_empty((total,), dtype=_I64)
+    else:
+        _check_packed(positions, "positions", _I64, dev, total)
+    _launch(dev, lib.pkv_draft_tree_layout, parents.data_ptr(), q_start.data_ptr(), S, total,
+            max_q_len, context_lens.data_ptr(), tree_mask.data_ptr(), positions.data_ptr())
     return tree_mask, positions
 
 
@@ -1104,34 +1157,31 @@ def paged_tree_attention(q: torch.Tensor, q_start: torch.Tensor, tree_mask: torc
     float32 unless ``out_dtype`` (or a given ``out``) is bfloat16.
     ``max_q_len`` (host int) bounds a tree's nodes; when omitted it is read
     from ``q_start`` (a device sync)."""
-    _check_cache(k_cache, v_cache)
-    _need(q.is_cuda and q.dtype == torch.bfloat16 and q.dim() == 3 and q.is_contiguous(),
-          "q must be a contiguous [total, Hq, d] bf16 CUDA tensor")
-    total, hq, d = q.shape
-    _need(d == k_cache.shape[3], "q and cache head dims differ")
-    S, max_q_len = _tree_batch(q_start, context_lens, max_q_len)
-    _need(tree_mask.is_cuda and tree_mask.dtype == torch.int64 and tree_mask.is_contiguous() and
-          tree_mask.shape == (total,), "tree_mask must be contiguous int64 [total] on the GPU")
-    _need(block_tables.dim() == 2, "block_tables must be [S, max_blocks]")
-    _need_i32(block_tables, "block_tables", S, block_tables.shape[1])
+    dev = _pools(k_cache, v_cache, _BF16)
+    if k_cache.dim() != 4 or q.dim() != 3:
+        _refuse("pools and q", "[NB, 16, Hkv, d] and [total, Hq, d]")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        _refuse("pools", "contiguous")
+    nb, bs, hkv, d = k_cache.shape
+    total, hq = q.shape[0], q.shape[1]
+    _check_packed(q, "q", _BF16, dev, total, hq, d)
+    S, max_q_len = _tree_batch(q_start, context_lens, dev, max_q_len)
+    _check_packed(tree_mask, "tree_mask", _I64, dev, total)
+    width = _tables(block_tables, dev, S)
     odt = _out_dtype(out, out_dtype)
-    with _same_device(q, q_start, tree_mask, k_cache, v_cache, block_tables, context_lens, out,
-                      workspace):
-        if out is None:
-            out = torch.empty(total, hq, d, dtype=odt, device=q.device)
-        _need(out.dtype == odt and out.is_contiguous() and out.shape == (total, hq, d),
-              "out must be contiguous float32 or bfloat16 [total, Hq, d]")
-        if workspace is None:
-            workspace = tree_attention_workspace(S, max_q_len, hq, k_cache.shape[2], d, q.device)
-        _need(workspace.is_cuda and workspace.dtype == torch.uint8 and workspace.is_contiguous(),
-              "workspace must be a contiguous uint8 CUDA tensor")
-        fn = (lib.pkv_paged_tree_attention_bf16out if odt == torch.bfloat16
-              else lib.pkv_paged_tree_attention)
-        st = fn(_ptr(q), _ptr(q_start), S, total, max_q_len, hq, _ptr(tree_mask), _ptr(k_cache),
-                _ptr(v_cache), cache_desc(k_cache), _ptr(block_tables), block_tables.shape[1],
-                _ptr(context_lens), float(scale), _ptr(out), _ptr(workspace), workspace.numel(),
-                _stream(q))
-    _check(fn.__name__, st)
+    if out is None:
+        out = q.new_empty((total, hq, d), dtype=odt)
+    else:
+        _check_packed(out, "out", odt, dev, total, hq, d)
+    if workspace is None:
+        workspace = tree_attention_workspace(S, max_q_len, hq, hkv, d, q.device)
+    else:
+        _check_packed(workspace, "workspace", _U8, dev, workspace.numel())
+    _launch(dev, lib.pkv_paged_tree_attention_bf16out if odt is _BF16
+            else lib.pkv_paged_tree_attention, q.data_ptr(), q_start.data_ptr(), S, total,
+            max_q_len, hq, tree_mask.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            _desc(nb, bs, hkv, d), block_tables.data_ptr(), width, context_lens.data_ptr(), scale,
+            out.data_ptr(), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -1145,34 +1195,31 @@ def kv_accept_rows(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: t
     nodes.  The pools are one layer's ``[NB, 16, Hkv, d]`` or all layers'
     ``[layers, NB, 16, Hkv, d]`` (bf16, or uint8 FP8 codes; each layer
     contiguous).  Returns the new context lengths, int32 ``[S]``."""
-    for c in (k_cache, v_cache):
-        _need(c.is_cuda and c.dtype in (torch.bfloat16, torch.uint8) and c.dim() in (4, 5),
-              "pools must be [NB, 16, Hkv, d] or [layers, NB, 16, Hkv, d] bf16 or uint8 CUDA "
-              "tensors")
-    _need(k_cache.shape == v_cache.shape and k_cache.dtype == v_cache.dtype,
-          "k_cache and v_cache differ")
-    k5, v5 = ((c if c.dim() == 5 else c.unsqueeze(0)) for c in (k_cache, v_cache))
-    layers = k5.shape[0]
-    for c in (k5, v5):
-        _need(layers == 0 or c[0].is_contiguous(), "each layer's pool must be contiguous")
-    S, _ = _tree_batch(q_start, context_lens, 0)
-    _need(block_tables.dim() == 2, "block_tables must be [S, max_blocks]")
-    _need_i32(block_tables, "block_tables", S, block_tables.shape[1])
-    _need(accepted.dim() == 2, "accepted must be [S, max_accepted]")
-    _need_i32(accepted, "accepted", S, accepted.shape[1])
-    _need_i32(num_accepted, "num_accepted", S)
-    with _same_device(k_cache, v_cache, block_tables, context_lens, q_start, accepted,
-                      num_accepted, new_context_lens):
-        if new_context_lens is None:
-            new_context_lens = torch.empty(S, dtype=torch.int32, device=k_cache.device)
-        _need_i32(new_context_lens, "new_context_lens", S)
-        desc = CacheDesc(*k5.shape[1:])
-        st = lib.pkv_kv_accept_rows(_ptr(k_cache), k5.stride(0), _ptr(v_cache), v5.stride(0),
-                                    layers, desc, k_cache.element_size(), _ptr(block_tables),
-                                    block_tables.shape[1], _ptr(context_lens), _ptr(q_start), S,
-                                    _ptr(accepted), accepted.shape[1], _ptr(num_accepted),
-                                    _ptr(new_context_lens), _stream(k_cache))
-    _check("pkv_kv_accept_rows", st)
+    dev = _pools(k_cache, v_cache, _BF16, _U8)
+    dims = k_cache.dim()
+    if dims not in (4, 5):
+        _refuse("pools", "[NB, 16, Hkv, d] or [layers, NB, 16, Hkv, d]")
+    nb, bs, hkv, d = k_cache.shape[-4:]
+    row = (bs * hkv * d, hkv * d, d, 1)
+    sk, sv = k_cache.stride(), v_cache.stride()
+    if sk[-4:] != row or sv[-4:] != row:
+        _refuse("each layer's pool", "contiguous")
+    layers, lk, lv = (k_cache.shape[0], sk[0], sv[0]) if dims == 5 else (1, 0, 0)
+    S, _ = _tree_batch(q_start, context_lens, dev, 0)
+    width = _tables(block_tables, dev, S)
+    if accepted.dim() != 2:
+        _refuse("accepted", "[S, max_accepted]")
+    most = accepted.shape[1]
+    _check_packed(accepted, "accepted", _I32, dev, S, most)
+    _check_packed(num_accepted, "num_accepted", _I32, dev, S)
+    if new_context_lens is None:
+        new_context_lens = context_lens.new_empty((S,))
+    else:
+        _check_packed(new_context_lens, "new_context_lens", _I32, dev, S)
+    _launch(dev, lib.pkv_kv_accept_rows, k_cache.data_ptr(), lk, v_cache.data_ptr(), lv, layers,
+            _desc(nb, bs, hkv, d), k_cache.element_size(), block_tables.data_ptr(), width,
+            context_lens.data_ptr(), q_start.data_ptr(), S, accepted.data_ptr(), most,
+            num_accepted.data_ptr(), new_context_lens.data_ptr())
     return new_context_lens
 
 

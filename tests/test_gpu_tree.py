@@ -152,6 +152,8 @@ def test_large_scores_move_the_running_maximum(pk):
     check(b, b.run(pk), "large scores")
     b.scale = -b.scale
     check(b, b.run(pk), "negative scale")
+    b.scale = 0.0
+    check(b, b.run(pk), "scale 0: the mean of the visible rows")
 
 
 @pytest.mark.parametrize("hq", [2, 16])
