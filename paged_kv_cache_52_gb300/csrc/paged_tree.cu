@@ -28,9 +28,9 @@
 //    each).  TILES = 2: bound by the tensor cores; warpgroup t owns row tile
 //    t and K/V tiles serve both.
 //  * warps 0-3 and 4-7 softmax, correction and epilogue (thread = row =
-//    tensor-memory lane), warp 8 loads K, 9 issues the MMAs, 10 loads V, 11
-//    loads Q.  The rings run on across items; only Q and the accumulators
-//    change hands at an item's end.
+//    tensor-memory lane), warp 8 loads K, 9 loads Q and issues Q K^T, 10 loads
+//    V, 11 issues P V.  The rings run on across items; only Q and the
+//    accumulators change hands at an item's end.
 //  * S = Q K^T lands in tensor memory, the softmax overwrites it with P as
 //    bf16 hi + lo (two MMAs a step, error ~2^-17: a row may see very few
 //    keys, where P rounded to one bf16 would move the output by 2^-9), and
@@ -55,7 +55,7 @@ static __device__ unsigned g_tree_error = 0;
 constexpr int kTrRows = 128;     // rows (node x head) per tile
 constexpr int kTrKeys = 128;     // keys per K/V tile (8 pages)
 constexpr int kTrThreads = 384;
-constexpr int kTrKWarp = 8, kTrMmaWarp = 9, kTrVWarp = 10, kTrQWarp = 11;
+constexpr int kTrKWarp = 8, kTrSWarp = 9, kTrVWarp = 10, kTrPvWarp = 11;
 constexpr uint32_t kTrTmemCols = 512;  // warpgroup w: S/P at 256 w, O at 256 w + 128
 constexpr float kTrRescale = 8.0f;     // log2 units: move the running max when it grows by > x256
 constexpr int kTrMaxStages = 8;
@@ -65,13 +65,14 @@ struct TreeSmem {
   static constexpr int kHalf = 128 * 128;  // 128 rows x 64 bf16
   static constexpr int kTileBytes = (D / 64) * kHalf;
   static constexpr int kQBytes = TILES * kTileBytes;
-  // ring stages: what 227 KB hold beside Q.  A V tile waits for its softmax, a
-  // K tile only for its product, so V gets the odd stage only if K has three.
-  static constexpr int kKStages = D == 64 ? 5 : 3;
-  static constexpr int kVStages = D == 64 ? 5 : (TILES == 1 ? 3 : 2);
+  // ring stages: what 227 KB hold beside Q and the staging of the epilogue.
+  // A V tile also waits for its softmax, a K tile only for its product.
+  static constexpr int kKStages = D == 64 ? 4 : 2;
+  static constexpr int kVStages = D == 64 ? 4 : (TILES == 1 ? 3 : 2);
   static constexpr int kKOff = kQBytes;
   static constexpr int kVOff = kKOff + kKStages * kTileBytes;
-  static constexpr int kXchOff = kVOff + kVStages * kTileBytes;  // [2][128] (max, sum)
+  static constexpr int kStageOff = kVOff + kVStages * kTileBytes;  // 32 rows x 128 bytes a warp
+  static constexpr int kXchOff = kStageOff + 8 * 4096;             // [2][128] (max, sum)
   static constexpr int kBarOff = kXchOff + 2 * kTrRows * 8;
   static constexpr int kNumBars = 2 + 4 * kTrMaxStages + 6 + 3;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
@@ -253,13 +254,13 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
     mbar_init(bars + 8 * kTrXch, 8);
     mbar_init(bars + 8 * kTrEpi, 8);
-    mbar_init(bars + 8 * kTrDrain, 1);
+    mbar_init(bars + 8 * kTrDrain, 2);
     fence_barrier_init();
     *abort_flag = 0;
     nonfinite[0] = nonfinite[1] = 0;
   }
   if (threadIdx.x == kTrVWarp * 32) tma_prefetch_desc(&tmap_v);
-  if (threadIdx.x == kTrQWarp * 32) {
+  if (threadIdx.x == kTrSWarp * 32) {
     tma_prefetch_desc(&tmap_k);
     tma_prefetch_desc(&tmap_q);
   }
@@ -374,16 +375,20 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
     }
     __syncwarp();
-  } else if (warp == kTrQWarp) {
-    // ================= Q =================
+  } else if (warp == kTrSWarp) {
+    // ================= Q, and the products S = Q K^T (one thread) =================
+    // S and P V are issued by two threads, so that one's waits and the other's
+    // MMAs overlap: a thread's MMAs are taken at the tensor core's pace.
     if (lane == 0) {
-      int k = 0;
+      constexpr uint32_t kIdesc = idesc_bf16_f32(128, kTrKeys, 0, 0);
+      auto wait = [&](int bar, uint32_t parity) {
+        return tr_wait(bars + 8 * bar, parity, abort_flag);
+      };
+      int i = 0, k = 0;
       bool ok = true;
-      for (; walk.next(); ++k) {
-        if (k > 0) {
-          ok = tr_wait(bars + 8 * kTrQEmpty, (k - 1) & 1, abort_flag);
-          if (!ok) break;
-        }
+      for (; ok && walk.next(); ++k) {
+        ok = k == 0 || wait(kTrQEmpty, (k - 1) & 1);
+        if (!ok) break;
         mbar_arrive_expect_tx(bars + 8 * kTrQFull, T::kQBytes);
         const int tok = walk.seq.qs + walk.group() * TILES * TPT;
 #pragma unroll
@@ -392,120 +397,74 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
           for (int h = 0; h < D / 64; ++h)
             tma_load_3d(sbase + t * T::kTileBytes + h * T::kHalf, &tmap_q, bars + 8 * kTrQFull,
                         h * 64, walk.kv_head() * G, tok + t * TPT);
+        ok = wait(kTrQFull, k & 1);
+#pragma unroll 1
+        for (int j = 0; ok && j < walk.tiles; ++j, ++i) {
+          ok = wait(kTrKFull + i % T::kKStages, (i / T::kKStages) & 1);
+#pragma unroll 1
+          for (int t = 0; ok && t < TILES; ++t) {
+            const int w = TILES == 1 ? i & 1 : t;
+            // the scores' columns are free once the products that read P there are done
+            const int before = TILES == 1 ? (i >> 1) - 1 : i - 1;
+            ok = before < 0 || wait(kTrODone + w, before & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t q_smem = sbase + t * T::kTileBytes;
+            const uint32_t k_smem = sbase + T::kKOff + (i % T::kKStages) * T::kTileBytes;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              const uint32_t off = (c >> 2) * T::kHalf + (c & 3) * 32;
+              umma_bf16(tmem + w * 256, smem_desc_sw128(q_smem + off, 16, 1024),
+                        smem_desc_sw128(k_smem + off, 16, 1024), kIdesc, c > 0);
+            }
+            umma_commit(bars + 8 * (kTrSFull + w));
+          }
+          umma_commit(bars + 8 * (kTrKEmpty + i % T::kKStages));
+          if (j + 1 == walk.tiles) umma_commit(bars + 8 * kTrQEmpty);
+        }
       }
       if (!ok) tr_abort(abort_flag);
-      if (k > 0 && !tr_wait(bars + 8 * kTrQEmpty, (k - 1) & 1, abort_flag))
-        (void)mbar_wait_bounded(bars + 8 * kTrQFull, (k - 1) & 1);
+      // every MMA issued has completed, and Q has landed, before the CTA exits
+      umma_commit(bars + 8 * kTrDrain);
+      (void)mbar_wait_bounded(bars + 8 * kTrDrain, 0);
+      if (!ok && k > 0) (void)mbar_wait_bounded(bars + 8 * kTrQFull, (k - 1) & 1);
     }
     __syncwarp();
-  } else if (warp == kTrMmaWarp) {
-    // ================= MMA issuer (one thread) =================
+  } else if (warp == kTrPvWarp) {
+    // ================= the products O += P V (one thread) =================
     if (lane == 0) {
-      constexpr uint32_t kIdescS = idesc_bf16_f32(128, kTrKeys, 0, 0);
-      constexpr uint32_t kIdescPV = idesc_bf16_f32(128, D, 0, 1);
-      auto mma_s = [&](int w, int t, int i) {  // S_w = Q_t K_i^T
-        const uint32_t q_smem = sbase + t * T::kTileBytes;
-        const uint32_t k_smem = sbase + T::kKOff + (i % T::kKStages) * T::kTileBytes;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = (k >> 2) * T::kHalf + (k & 3) * 32;
-          umma_bf16(tmem + w * 256, smem_desc_sw128(q_smem + off, 16, 1024),
-                    smem_desc_sw128(k_smem + off, 16, 1024), kIdescS, k > 0);
-        }
-        umma_commit(bars + 8 * (kTrSFull + w));
-      };
-      auto mma_pv = [&](int w, int i, bool fresh) {  // O_w (+)= P_w V_i
-        const uint32_t v_smem = sbase + T::kVOff + (i % T::kVStages) * T::kTileBytes;
-#pragma unroll
-        for (int k = 0; k < kTrKeys / 16; ++k) {
-          const uint64_t vdesc = smem_desc_sw128(v_smem + k * 2048, T::kHalf, 1024);
-          const uint32_t a_hi = tmem + w * 256 + 64 * (k >> 2) + 8 * (k & 3);
-          umma_bf16_ts(tmem + w * 256 + 128, a_hi, vdesc, kIdescPV, (!fresh || k > 0) ? 1u : 0u);
-          umma_bf16_ts(tmem + w * 256 + 128, a_hi + 32, vdesc, kIdescPV, 1u);
-        }
-        umma_commit(bars + 8 * (kTrODone + w));
-      };
+      constexpr uint32_t kIdesc = idesc_bf16_f32(128, D, 0, 1);
       auto wait = [&](int bar, uint32_t parity) {
-        const bool r = tr_wait(bars + 8 * bar, parity, abort_flag);
-        if (r) tc_fence_after();
-        return r;
+        return tr_wait(bars + 8 * bar, parity, abort_flag);
       };
-      // the piece of the next S product (runs ahead) and of the next P V
-      TreeWalk<G, TILES> ahead = walk;
-      int sk = -1, s_end = 0;  // pieces begun by S, and the stream tile the current one ends at
-      auto ready_s = [&](int i) {  // operands of S(i) are in shared memory
-        if (i == s_end) {
-          if (!ahead.next()) return false;
-          s_end += ahead.tiles;
-          ++sk;
-          if (!wait(kTrQFull, sk & 1)) return false;
-        }
-        return wait(kTrKFull + i % T::kKStages, (i / T::kKStages) & 1);
-      };
-      auto done_s = [&](int i) {
-        umma_commit(bars + 8 * (kTrKEmpty + i % T::kKStages));
-        if (i + 1 == s_end) umma_commit(bars + 8 * kTrQEmpty);
-      };
+      int i = 0;
       bool ok = true;
-      int pk = -1, p_begin = 0, p_end = 0;
-      auto piece_of = [&](int i) {
-        if (i == p_end) {
-          (void)walk.next();
-          p_begin = p_end;
-          p_end += walk.tiles;
-          ++pk;
-        }
-      };
-      if constexpr (TILES == 1) {
-        for (int i = 0; ok && i < 2 && i < count; ++i) {
-          ok = ready_s(i);
-          if (ok) mma_s(i & 1, 0, i), done_s(i);
-        }
-        for (int i = 0; ok && i < count; ++i) {
-          const int w = i & 1;
-          piece_of(i);
-          const bool fresh = i - p_begin < 2;  // first tile of this accumulator in the piece
-          ok = wait(kTrPFull + w, (i >> 1) & 1) &&
-               wait(kTrVFull + i % T::kVStages, (i / T::kVStages) & 1) &&
-               (!fresh || pk == 0 || wait(kTrEpi, (pk - 1) & 1));
-          if (!ok) break;
-          mma_pv(w, i, fresh);
-          umma_commit(bars + 8 * (kTrVEmpty + i % T::kVStages));
-          if (i + 2 < count) {
-            ok = ready_s(i + 2);
-            if (ok) mma_s(w, 0, i + 2), done_s(i + 2);
-          }
-        }
-      } else {
-        ok = ready_s(0);
-        if (ok) {
-          mma_s(0, 0, 0);
-          mma_s(1, 1, 0);
-          done_s(0);
-        }
-        for (int i = 0; ok && i < count; ++i) {
-          piece_of(i);
-          const bool fresh = i == p_begin;
-          ok = wait(kTrPFull + 0, i & 1) &&
-               wait(kTrVFull + i % T::kVStages, (i / T::kVStages) & 1) &&
-               (!fresh || pk == 0 || wait(kTrEpi, (pk - 1) & 1));
-          if (!ok) break;
-          mma_pv(0, i, fresh);
-          const bool more = i + 1 < count;
-          if (more) {
-            ok = ready_s(i + 1);
+      for (int k = 0; ok && walk.next(); ++k) {
+#pragma unroll 1
+        for (int j = 0; ok && j < walk.tiles; ++j, ++i) {
+          const bool fresh = j < (TILES == 1 ? 2 : 1);  // the accumulator's first tile of the piece
+          ok = wait(kTrVFull + i % T::kVStages, (i / T::kVStages) & 1) &&
+               (!fresh || k == 0 || wait(kTrEpi, (k - 1) & 1));
+          const uint32_t v_smem = sbase + T::kVOff + (i % T::kVStages) * T::kTileBytes;
+#pragma unroll 1
+          for (int t = 0; ok && t < TILES; ++t) {
+            const int w = TILES == 1 ? i & 1 : t;
+            ok = wait(kTrPFull + w, (TILES == 1 ? i >> 1 : i) & 1);
             if (!ok) break;
-            mma_s(0, 0, i + 1);
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < kTrKeys / 16; ++c) {
+              const uint64_t vdesc = smem_desc_sw128(v_smem + c * 2048, T::kHalf, 1024);
+              const uint32_t a_hi = tmem + w * 256 + 64 * (c >> 2) + 8 * (c & 3);
+              umma_bf16_ts(tmem + w * 256 + 128, a_hi, vdesc, kIdesc, (!fresh || c > 0) ? 1u : 0u);
+              umma_bf16_ts(tmem + w * 256 + 128, a_hi + 32, vdesc, kIdesc, 1u);
+            }
+            umma_commit(bars + 8 * (kTrODone + w));
           }
-          ok = wait(kTrPFull + 1, i & 1);
-          if (!ok) break;
-          mma_pv(1, i, fresh);
           umma_commit(bars + 8 * (kTrVEmpty + i % T::kVStages));
-          if (more) mma_s(1, 1, i + 1), done_s(i + 1);
         }
       }
       if (!ok) tr_abort(abort_flag);
-      // every MMA issued has completed before tensor memory is released
       umma_commit(bars + 8 * kTrDrain);
       (void)mbar_wait_bounded(bars + 8 * kTrDrain, 0);
     }
@@ -514,7 +473,6 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     // ================= softmax, correction, epilogue =================
     const int w = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // row of the tile = tensor-memory lane
-    const int node_in_tile = r / G, head = r - (r / G) * G;
     const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t s_col = w * 256, o_col = w * 256 + 128;
     float2* xch = reinterpret_cast<float2*>(smem + T::kXchOff);
@@ -524,7 +482,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     bool ok = true;
     for (int k = 0; ok && walk.next(); ++k) {
       const TreeSeq& q = walk.seq;
-      const int node = (walk.group() * TILES + (TILES == 2 ? w : 0)) * TPT + node_in_tile;
+      const int node0 = (walk.group() * TILES + (TILES == 2 ? w : 0)) * TPT;  // of the tile
+      const int node = node0 + r / G;
       const bool valid = node < q.n;
       const bool warp_valid = __any_sync(0xffffffffu, valid);
       const int base = q.ctx - q.n;  // committed keys
@@ -723,11 +682,12 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       if (warp_valid) {
         const unsigned long long hit = mask & nonfinite[k & 1];
         const int kvh = walk.kv_head();
-        const size_t orow = (size_t(q.qs) + node) * p.q_heads + size_t(kvh) * G + head;
         const bool whole = walk.whole();
         // slot 2c: the piece the CTA's range starts with, 2c + 1: the one it ends with
         const size_t slot = size_t(blockIdx.x) * 2 + (k == 0 ? 0 : 1);
-        const size_t prow = (slot * TILES + (TILES == 2 ? w : 0)) * kTrRows + r;
+        const size_t prow0 = (slot * TILES + (TILES == 2 ? w : 0)) * kTrRows + (warp & 3) * 32;
+        const uint32_t stage = sbase + T::kStageOff + warp * 4096;
+        const unsigned rows_valid = __ballot_sync(0xffffffffu, valid);
         // TILES 1: this warpgroup's half of the columns of both accumulators
         constexpr int kCols = TILES == 1 ? D / 2 : D;
         const int col0 = TILES == 1 ? w * kCols : 0;
@@ -766,29 +726,37 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
               }
             }
           }
-          if (!valid) continue;
-          if (!whole) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + prow * D + col0 + c);
+          // Through shared memory, so that a store covers whole rows of the
+          // 32 x 32 block instead of 16 bytes of each of 32 rows: 32 rows of
+          // 128 bytes, the 16-byte chunks of row r rotated by r.
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-          } else if (p.out_bf16) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow * D +
-                                                  col0 + c);
+          for (int u = 0; u < 8; ++u)
+            st_shared_f4(stage + lane * 128 + (((u + lane) & 7) << 4), o[4 * u], o[4 * u + 1],
+                         o[4 * u + 2], o[4 * u + 3]);
+          __syncwarp();
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              dst[u] = make_uint4(pack_bf16x2(o[8 * u], o[8 * u + 1]),
-                                  pack_bf16x2(o[8 * u + 2], o[8 * u + 3]),
-                                  pack_bf16x2(o[8 * u + 4], o[8 * u + 5]),
-                                  pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
-          } else {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + orow * D + col0 + c);
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              dst[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          for (int u = 0; u < 8; ++u) {
+            const int row = 4 * u + (lane >> 3), chunk = lane & 7;
+            const uint4 x = ld_shared_u4(stage + row * 128 + (((chunk + row) & 7) << 4));
+            if (!((rows_valid >> row) & 1u)) continue;
+            const size_t cols = col0 + c + 4 * chunk;
+            if (!whole) {
+              *reinterpret_cast<uint4*>(p.part_o + (prow0 + row) * D + cols) = x;
+              continue;
+            }
+            const int tr = (warp & 3) * 32 + row;  // row of the tile
+            const size_t at = ((size_t(q.qs) + node0 + tr / G) * p.q_heads + size_t(kvh) * G +
+                               tr % G) * D + cols;
+            if (p.out_bf16)
+              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+                  make_uint2(pack_bf16x2(__uint_as_float(x.x), __uint_as_float(x.y)),
+                             pack_bf16x2(__uint_as_float(x.z), __uint_as_float(x.w)));
+            else
+              *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + at) = x;
           }
+          __syncwarp();
         }
-        if (valid && !whole && col0 == 0) p.part_lse[prow] = lse;
+        if (valid && !whole && col0 == 0) p.part_lse[prow0 + lane] = lse;
       }
       tc_fence_before();
       __syncwarp();
