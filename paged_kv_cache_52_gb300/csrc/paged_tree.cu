@@ -65,20 +65,23 @@ struct TreeSmem {
   static constexpr int kHalf = 128 * 128;  // 128 rows x 64 bf16
   static constexpr int kTileBytes = (D / 64) * kHalf;
   static constexpr int kQBytes = TILES * kTileBytes;
-  // ring stages: what 227 KB hold beside Q and the staging of the epilogue.
-  // A V tile also waits for its softmax, a K tile only for its product.
-  static constexpr int kKStages = D == 64 ? 4 : 2;
+  // Ring stages: what 227 KB hold beside Q.  A V tile also waits for its
+  // softmax, a K tile only for its product.
+  static constexpr int kKStages = D == 64 ? 4 : 3;
   static constexpr int kVStages = D == 64 ? 4 : (TILES == 1 ? 3 : 2);
   static constexpr int kKOff = kQBytes;
   static constexpr int kVOff = kKOff + kKStages * kTileBytes;
-  static constexpr int kStageOff = kVOff + kVStages * kTileBytes;  // 32 rows x 128 bytes a warp
-  static constexpr int kXchOff = kStageOff + 8 * 4096;             // [2][128] (max, sum)
+  // The epilogue stages 32 rows x 128 bytes a warp: heads of 128 in the V slot
+  // of the piece's last tile (which goes back to the ring after it), of 64 in
+  // shared memory of its own.
+  static constexpr int kStageOff = kVOff + kVStages * kTileBytes;
+  static constexpr int kXchOff = kStageOff + (D == 64 ? 8 * 4096 : 0);  // [2][128] (max, sum)
   static constexpr int kBarOff = kXchOff + 2 * kTrRows * 8;
   static constexpr int kNumBars = 2 + 4 * kTrMaxStages + 6 + 3;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
-  // tensor-memory base, abort flag; non-finite nodes [2] (64 bit); scan [12]
-  // (64 bit); the start of the range
-  static constexpr int kSmemBytes = kMiscOff + 16 + 16 + 96 + 48;
+  // tensor-memory base, abort flag; non-finite nodes [2] (64 bit); scan [12];
+  // the start of the range
+  static constexpr int kSmemBytes = kMiscOff + 16 + 16 + 48 + 32;
   static_assert(kSmemBytes <= 232448, "tree tile does not fit in shared memory");
   static_assert(kKStages <= kTrMaxStages && kVStages <= kTrMaxStages, "ring stages");
 };
@@ -117,9 +120,7 @@ struct TreeParams {
 struct TreeSeq {
   int qs, n, ctx, groups, tiles;
   bool bad;
-  __device__ __forceinline__ long long total(int kv_heads) const {
-    return (long long)groups * tiles * kv_heads;
-  }
+  __device__ __forceinline__ int total(int kv_heads) const { return groups * tiles * kv_heads; }
 };
 
 template <int G, int TILES>
@@ -142,12 +143,12 @@ template <int G, int TILES>
 struct TreeWalk {
   const TreeParams& p;
   int s;
-  long long off;   // tiles of sequence s before the next piece
+  int off;         // tiles of sequence s before the next piece
   int left;        // tiles of the range after the current piece
   TreeSeq seq;
   int item, first, tiles;  // current piece
   __device__ __forceinline__ TreeWalk(const TreeParams& pp, const TreeSeq& q0, int s0,
-                                      long long off0, int count)
+                                      int off0, int count)
       : p(pp), s(s0), off(off0), left(count), seq(q0) {}
   __device__ __forceinline__ bool next() {
     if (left <= 0) return false;
@@ -156,8 +157,8 @@ struct TreeWalk {
       off = 0;
       seq = tree_seq<G, TILES>(p, s);
     }
-    item = int(off / seq.tiles);
-    first = int(off - (long long)item * seq.tiles);
+    item = off / seq.tiles;
+    first = off - item * seq.tiles;
     tiles = min(seq.tiles - first, left);
     off += tiles;
     left -= tiles;
@@ -221,14 +222,13 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + T::kMiscOff);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + T::kMiscOff + 4);
   unsigned long long* nonfinite = reinterpret_cast<unsigned long long*>(smem + T::kMiscOff + 16);
-  long long* scan = reinterpret_cast<long long*>(smem + T::kMiscOff + 32);
+  int* scan = reinterpret_cast<int*>(smem + T::kMiscOff + 32);
   struct Begin {
-    long long off;
     TreeSeq seq;
-    int s;
+    int s, off;
   };
-  static_assert(sizeof(Begin) <= 48, "start of the range");
-  Begin* begin = reinterpret_cast<Begin*>(smem + T::kMiscOff + 128);
+  static_assert(sizeof(Begin) <= 32, "start of the range");
+  Begin* begin = reinterpret_cast<Begin*>(smem + T::kMiscOff + 80);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // ---- set-up that reads no input, beside the previous kernel's end
@@ -270,17 +270,17 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
   const int per_thread = (p.num_seqs + kTrThreads - 1) / kTrThreads;
   const int s_lo = min(int(threadIdx.x) * per_thread, p.num_seqs);
   const int s_hi = min(s_lo + per_thread, p.num_seqs);
-  long long mine = 0;
+  int mine = 0;
   TreeSeq q{};
   for (int s = s_lo; s < s_hi; ++s) {
     q = tree_seq<G, TILES>(p, s);
     if (q.bad && blockIdx.x == 0) atomicOr(&g_tree_error, kErrBadQueryRange);
     mine += q.total(p.kv_heads);
   }
-  long long incl = mine;
+  int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+    const int up = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += up;
   }
   if (lane == 31) scan[warp] = incl;
@@ -288,31 +288,32 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  long long all = 0;
+  int all = 0;
 #pragma unroll
   for (int w = 0; w < kTrThreads / 32; ++w) {
     if (w == warp) incl += all;
     all += scan[w];
   }
   // with fewer tiles than CTAs the last CTAs have none, so that a cut item's
-  // pieces lie in consecutive CTAs
-  const long long active = min((long long)gridDim.x, all), c = blockIdx.x;
-  const long long lo = c < active ? all * c / active : all;
-  const int count = c < active ? int(all * (c + 1) / active - lo) : 0;
+  // pieces lie in consecutive CTAs; CTA c starts at floor(c all / active)
+  const int active = min(int(gridDim.x), all), c = blockIdx.x;
+  const int each = active > 0 ? all / active : 0, rest = all - each * active;
+  const int lo = c < active ? c * each + c * rest / active : all;
+  const int count = c < active ? (c + 1) * each + (c + 1) * rest / active - lo : 0;
   if (lo >= incl - mine && lo < incl) {  // the range starts in this thread's sequences
-    long long at = lo - (incl - mine);
+    int at = lo - (incl - mine);
     int s = s_lo;
     if (per_thread > 1)
       for (;; ++s) {
         q = tree_seq<G, TILES>(p, s);
-        const long long w = q.total(p.kv_heads);
+        const int w = q.total(p.kv_heads);
         if (at < w) break;
         at -= w;
       }
-    *begin = Begin{at, q, s};
-    const int item = int(at / q.tiles);
-    p.start[c] = TreeStart{count > 0 ? s : -1, item, int(at - (long long)item * q.tiles), q.qs,
-                           q.n, q.groups, {0, 0}};
+    *begin = Begin{q, s, at};
+    const int item = at / q.tiles;
+    p.start[c] = TreeStart{count > 0 ? s : -1, item, at - item * q.tiles, q.qs, q.n, q.groups,
+                           {0, 0}};
   } else if (lo >= all && threadIdx.x == 0) {
     p.start[c].seq = -1;
   }
@@ -439,12 +440,20 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       };
       int i = 0;
       bool ok = true;
-      for (int k = 0; ok && walk.next(); ++k) {
+      // the epilogue of piece k - 1 has read the accumulators and the V slot
+      // it staged its rows in, which goes back to the ring
+      auto after_epilogue = [&](int k) {
+        if (!wait(kTrEpi, (k - 1) & 1)) return false;
+        mbar_arrive(bars + 8 * (kTrVEmpty + (i - 1) % T::kVStages));
+        return true;
+      };
+      int k = 0;
+      for (; ok && walk.next(); ++k) {
+        if (k > 0) ok = after_epilogue(k);
 #pragma unroll 1
         for (int j = 0; ok && j < walk.tiles; ++j, ++i) {
           const bool fresh = j < (TILES == 1 ? 2 : 1);  // the accumulator's first tile of the piece
-          ok = wait(kTrVFull + i % T::kVStages, (i / T::kVStages) & 1) &&
-               (!fresh || k == 0 || wait(kTrEpi, (k - 1) & 1));
+          ok = wait(kTrVFull + i % T::kVStages, (i / T::kVStages) & 1);
           const uint32_t v_smem = sbase + T::kVOff + (i % T::kVStages) * T::kTileBytes;
 #pragma unroll 1
           for (int t = 0; ok && t < TILES; ++t) {
@@ -461,9 +470,10 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
             }
             umma_commit(bars + 8 * (kTrODone + w));
           }
-          umma_commit(bars + 8 * (kTrVEmpty + i % T::kVStages));
+          if (j + 1 < walk.tiles) umma_commit(bars + 8 * (kTrVEmpty + i % T::kVStages));
         }
       }
+      if (ok) ok = after_epilogue(k);
       if (!ok) tr_abort(abort_flag);
       umma_commit(bars + 8 * kTrDrain);
       (void)mbar_wait_bounded(bars + 8 * kTrDrain, 0);
@@ -494,12 +504,10 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
       float m = -INFINITY, l = 0.f;
       int seen = 0;  // tiles of the piece this warpgroup has taken
-      int last = -1;
       for (int j = 0; j < walk.tiles; ++j) {
         const int it = i + j;
         if (TILES == 1 && (it & 1) != w) continue;
         const int ph = TILES == 1 ? it >> 1 : it;
-        last = ph;
         const int key0 = (walk.first + j) * kTrKeys;
         const bool masked = key0 + kTrKeys > base;
         ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * (kTrSFull + w), ph & 1, abort_flag));
@@ -521,59 +529,86 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
             }
             tmem_wait_st();
           }
-          // the tile's max
-          float ex[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          // The running max m is a reference only: any value near the scores'
+          // serves.  So the tile is weighed against the m it has, 64 keys at a
+          // time and without looking for their max, and that stands while
+          // each row's sum over the 64 is at most 2^64 (bf16 hi + lo has
+          // float32's range).  Where no key has been seen yet, or a sum is
+          // larger, the max of what is left of the tile is taken first, and m
+          // moves when it is more than 8 behind (a factor 256).
+          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+          bool raise = !__all_sync(0xffffffffu, m != -INFINITY), settled = false;
 #pragma unroll 1
-          for (int c = 0; c < kTrKeys; c += 64) {
+          for (int c = 0; c < kTrKeys;) {
             float va[32], vb[32];
-            tmem_ld32(lane_base + s_col + c, va);
-            tmem_ld32(lane_base + s_col + c + 32, vb);
-            tmem_wait_ld();
-            if (neg) {
-#pragma unroll
-              for (int u = 0; u < 32; ++u) ex[u & 3] = max3f(ex[u & 3], -va[u], -vb[u]);
-            } else {
-#pragma unroll
-              for (int u = 0; u < 32; ++u) ex[u & 3] = max3f(ex[u & 3], va[u], vb[u]);
-            }
-          }
-          const float top = fmaxf(fmaxf(ex[0], ex[1]), fmaxf(ex[2], ex[3]));
-          const float mx = top == -INFINITY ? -INFINITY : top * mag;
-          const bool move = mx > m + kTrRescale || (m == -INFINITY && mx > m);
-          if (__any_sync(0xffffffffu, move)) {
-            const float alpha = move ? ex2(m - mx) : 1.f;  // 0 when m is -inf
-            if (seen > 0) {
-              // the accumulator's last product must be done before it is scaled
-              ok = __all_sync(0xffffffffu,
-                              tr_wait(bars + 8 * (kTrODone + w), (ph - 1) & 1, abort_flag));
-              if (!ok) break;
-              tc_fence_after();
-              const uint64_t a2 = f2_pack(alpha, alpha);
+            if (raise) {
+              float ex[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-              for (int c = 0; c < D; c += 32) {
-                float o[32];
-                tmem_ld32(lane_base + o_col + c, o);
+              for (int cc = c; cc < kTrKeys; cc += 64) {
+                tmem_ld32(lane_base + s_col + cc, va);
+                tmem_ld32(lane_base + s_col + cc + 32, vb);
                 tmem_wait_ld();
 #pragma unroll
-                for (int u = 0; u < 32; u += 2)
-                  f2_unpack(f2_mul(f2_pack(o[u], o[u + 1]), a2), o[u], o[u + 1]);
-                tmem_st32(lane_base + o_col + c, o);
+                for (int u = 0; u < 32; ++u)
+                  ex[u & 3] = max3f(ex[u & 3], neg ? -va[u] : va[u], neg ? -vb[u] : vb[u]);
               }
-            }
-            l *= alpha;
-            if (move) m = mx;
-          }
-          // P = 2^(x - m) as bf16 hi + lo over the columns of the scores:
-          // keys [64 g, 64 g + 64): hi at 64 g, lo at 64 g + 32, two keys a column
-          const float mref = m == -INFINITY ? 0.f : m;  // nothing seen yet: all P are 0
-          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
-          const uint64_t nm2 = f2_pack(-mref, -mref);
-          uint64_t ls[2] = {0ull, 0ull};
+              const float top = fmaxf(fmaxf(ex[0], ex[1]), fmaxf(ex[2], ex[3]));
+              const float mx = top == -INFINITY ? -INFINITY : top * mag;
+              const bool move = mx > m + kTrRescale || (m == -INFINITY && mx > m);
+              if (__any_sync(0xffffffffu, move)) {
+                const float alpha = move ? ex2(m - mx) : 1.f;  // 0 when m is -inf
+                if (seen > 0) {
+                  // the accumulator's last product must be done before it is scaled
+                  ok = __all_sync(0xffffffffu,
+                                  tr_wait(bars + 8 * (kTrODone + w), (ph - 1) & 1, abort_flag));
+                  if (!ok) break;
+                  tc_fence_after();
+                  const uint64_t a2 = f2_pack(alpha, alpha);
 #pragma unroll 1
-          for (int c = 0; c < kTrKeys; c += 64) {
-            float va[32], vb[32];
+                  for (int cc = 0; cc < D; cc += 32) {
+                    tmem_ld32(lane_base + o_col + cc, va);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int u = 0; u < 32; u += 2)
+                      f2_unpack(f2_mul(f2_pack(va[u], va[u + 1]), a2), va[u], va[u + 1]);
+                    tmem_st32(lane_base + o_col + cc, va);
+                  }
+                }
+                if (c > 0) {
+                  // so is the P of the tile's first keys, already stored
+                  tmem_wait_st();
+#pragma unroll 1
+                  for (int cc = 0; cc < 32; cc += 16) {
+                    float ph16[16], pl16[16];
+                    tmem_ld16(lane_base + s_col + cc, ph16);
+                    tmem_ld16(lane_base + s_col + 32 + cc, pl16);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int u = 0; u < 16; ++u) {
+                      const uint32_t h = __float_as_uint(ph16[u]), lw = __float_as_uint(pl16[u]);
+                      const float e0 = (bf16_lo_to_f32(h) + bf16_lo_to_f32(lw)) * alpha;
+                      const float e1 = (bf16_hi_to_f32(h) + bf16_hi_to_f32(lw)) * alpha;
+                      const uint32_t n = pack_bf16x2(e0, e1);
+                      ph16[u] = __uint_as_float(n);
+                      pl16[u] = __uint_as_float(
+                          pack_bf16x2(e0 - bf16_lo_to_f32(n), e1 - bf16_hi_to_f32(n)));
+                    }
+                    tmem_st16(lane_base + s_col + cc, ph16);
+                    tmem_st16(lane_base + s_col + 32 + cc, pl16);
+                  }
+                }
+                l *= alpha;
+                if (move) m = mx;
+              }
+              raise = false;
+              settled = true;
+            }
+            // P = 2^(x - m) as bf16 hi + lo
             tmem_ld32(lane_base + s_col + c, va);
             tmem_ld32(lane_base + s_col + c + 32, vb);
+            const float mref = m == -INFINITY ? 0.f : m;  // nothing seen yet: all P are 0
+            const uint64_t nm2 = f2_pack(-mref, -mref);
+            uint64_t ls[2] = {0ull, 0ull};
             tmem_wait_ld();
             uint32_t hi[32], lo[32];
 #pragma unroll
@@ -591,13 +626,22 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
               f2_unpack(f2_sub(e, f2_pack(bf16_lo_to_f32(hi[u]), bf16_hi_to_f32(hi[u]))), r0, r1);
               lo[u] = pack_bf16x2(r0, r1);
             }
+            float a0, a1, b0, b1;
+            f2_unpack(ls[0], a0, a1);
+            f2_unpack(ls[1], b0, b1);
+            const float sum = (a0 + a1) + (b0 + b1);
+            if (!settled && !__all_sync(0xffffffffu, sum <= 18446744073709551616.f)) {
+              raise = true;  // NaN, too; the scores from c on are still there
+              continue;
+            }
+            l += sum;
+            // over the columns of the scores: keys [64 g, 64 g + 64) have hi at
+            // 64 g and lo at 64 g + 32, two keys a column
             tmem_st32u(lane_base + s_col + c, hi);
             tmem_st32u(lane_base + s_col + c + 32, lo);
+            c += 64;
           }
-          float a0, a1, b0, b1;
-          f2_unpack(ls[0], a0, a1);
-          f2_unpack(ls[1], b0, b1);
-          l += (a0 + a1) + (b0 + b1);
+          if (!ok) break;
         }
         if (masked && (TILES == 1 || w == 0)) {
           // thread r looks at key row r of V; the chunk order differs from
@@ -648,12 +692,19 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       if (lane == 0) mbar_arrive(bars + 8 * kTrXch);
       ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * kTrXch, k & 1, abort_flag));
       if (!ok) break;
-      if (last >= 0) {
-        ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * (kTrODone + w), last & 1, abort_flag));
+      // both accumulators' last products of the piece are done: each may be
+      // read, and nobody reads the last V tile any more
+      const int begin_tile = i;
+      i += walk.tiles;
+#pragma unroll 1
+      for (int a = 0; a < 2; ++a) {
+        const int lt = TILES == 2 || ((i - 1) & 1) == a ? i - 1 : i - 2;  // its last tile
+        if (lt < begin_tile) continue;
+        ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * (kTrODone + a),
+                                             (TILES == 1 ? lt >> 1 : lt) & 1, abort_flag));
         if (!ok) break;
       }
-      const int begin = i, end = i + walk.tiles;  // stream tiles of the piece
-      i = end;
+      if (!ok) break;
       float fa = 0.f, fb = 0.f, lse = -INFINITY;  // factors of O_w and of the other O
       if constexpr (TILES == 1) {
         const float2 other = xch[(1 - w) * kTrRows + r];
@@ -664,15 +715,6 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (l != 0.f) fa = wa / tot;  // NaN scores included
         if (other.y != 0.f) fb = wb / tot;
         if (tot != 0.f) lse = ref + __log2f(tot);
-        // the other warpgroup's last tile of the piece, if it had one
-        const int ot = ((end - 1) & 1) != w ? end - 1 : end - 2;
-        if (ot >= begin) {
-          ok = __all_sync(0xffffffffu,
-                          tr_wait(bars + 8 * (kTrODone + 1 - w), (ot >> 1) & 1, abort_flag));
-          if (!ok) break;
-        } else {
-          fb = 0.f;
-        }
       } else if (l != 0.f) {
         fa = 1.f / l;
         lse = (m == -INFINITY ? 0.f : m) + __log2f(l);
@@ -686,11 +728,16 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // slot 2c: the piece the CTA's range starts with, 2c + 1: the one it ends with
         const size_t slot = size_t(blockIdx.x) * 2 + (k == 0 ? 0 : 1);
         const size_t prow0 = (slot * TILES + (TILES == 2 ? w : 0)) * kTrRows + (warp & 3) * 32;
-        const uint32_t stage = sbase + T::kStageOff + warp * 4096;
-        const unsigned rows_valid = __ballot_sync(0xffffffffu, valid);
+        const uint32_t stage = sbase + warp * 4096 +
+            (D == 64 ? T::kStageOff : T::kVOff + ((i - 1) % T::kVStages) * T::kTileBytes);
         // TILES 1: this warpgroup's half of the columns of both accumulators
         constexpr int kCols = TILES == 1 ? D / 2 : D;
         const int col0 = TILES == 1 ? w * kCols : 0;
+        const unsigned rows_valid = __ballot_sync(0xffffffffu, valid);
+        const int chunk0 = col0 + 4 * (lane & 7);
+        float* part = p.part_o + prow0 * D + chunk0;
+        const size_t out0 =
+            ((size_t(q.qs) + node0) * p.q_heads + size_t(kvh) * G) * D + chunk0;
         const bool use_a = __any_sync(0xffffffffu, fa != 0.f);
         const bool use_b = TILES == 1 && __any_sync(0xffffffffu, fb != 0.f);
 #pragma unroll 1
@@ -734,30 +781,30 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
             st_shared_f4(stage + lane * 128 + (((u + lane) & 7) << 4), o[4 * u], o[4 * u + 1],
                          o[4 * u + 2], o[4 * u + 3]);
           __syncwarp();
+          // this lane's chunk of rows lane / 8 + 4 u
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            const int row = 4 * u + (lane >> 3), chunk = lane & 7;
-            const uint4 x = ld_shared_u4(stage + row * 128 + (((chunk + row) & 7) << 4));
+            const int row = 4 * u + (lane >> 3);
+            const uint4 x = ld_shared_u4(stage + row * 128 + (((lane + row) & 7) << 4));
             if (!((rows_valid >> row) & 1u)) continue;
-            const size_t cols = col0 + c + 4 * chunk;
             if (!whole) {
-              *reinterpret_cast<uint4*>(p.part_o + (prow0 + row) * D + cols) = x;
+              *reinterpret_cast<uint4*>(part + row * D + c) = x;
               continue;
             }
             const int tr = (warp & 3) * 32 + row;  // row of the tile
-            const size_t at = ((size_t(q.qs) + node0 + tr / G) * p.q_heads + size_t(kvh) * G +
-                               tr % G) * D + cols;
+            const size_t at = size_t(tr / G) * (p.q_heads * D) + (tr % G) * D + c;
             if (p.out_bf16)
-              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + out0 + at) =
                   make_uint2(pack_bf16x2(__uint_as_float(x.x), __uint_as_float(x.y)),
                              pack_bf16x2(__uint_as_float(x.z), __uint_as_float(x.w)));
             else
-              *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + at) = x;
+              *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + out0 + at) = x;
           }
           __syncwarp();
         }
         if (valid && !whole && col0 == 0) p.part_lse[prow0 + lane] = lse;
       }
+      fence_proxy_async_smem();  // the staging block is a V slot again
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * kTrEpi);

@@ -1908,6 +1908,11 @@ int tree_attention(const void* q, const int32_t* q_start, int num_seqs, int tota
   if (num_seqs == 0 || total_q == 0 || max_q_len == 0) return PKV_OK;
   if (!tree_mask || !aligned(tree_mask, 8)) return PKV_EINVAL;
   if (max_blocks_per_seq > INT32_MAX / kBlockSize) return PKV_EUNSUPPORTED;
+  // key tiles of all items are counted in 32 bits
+  const long long groups = ((long long)max_q_len * (q_heads / cache.kv_heads) - 1) /
+                               pkv::tree_tile_rows() + 1;
+  if (groups * num_seqs * cache.kv_heads > INT32_MAX / (max_blocks_per_seq / 8 + 1))
+    return PKV_EUNSUPPORTED;
   if (!workspace || ws_bytes < w.total) return PKV_ENOMEM;
   if (!aligned(workspace, 256)) return PKV_EINVAL;
   if (current_device_sms() <= 0) return PKV_ECUDA;
