@@ -55,10 +55,11 @@ static __device__ unsigned g_tree_error = 0;
 constexpr int kTrRows = 128;     // rows (node x head) per tile
 constexpr int kTrKeys = 128;     // keys per K/V tile (8 pages)
 constexpr int kTrThreads = 384;
-constexpr int kTrKWarp = 8, kTrSWarp = 9, kTrVWarp = 10, kTrPvWarp = 11;
+constexpr int kTrKWarp = 8, kTrSWarp = 9, kTrVWarp = 10;  // 11 issues P V
 constexpr uint32_t kTrTmemCols = 512;  // warpgroup w: S/P at 256 w, O at 256 w + 128
 constexpr float kTrRescale = 8.0f;     // log2 units: move the running max when it grows by > x256
-constexpr int kTrMaxStages = 8;
+constexpr int kTrMaxStages = 5;
+constexpr int kTrPieces = 4;  // piece descriptions in shared memory
 
 template <int D, int TILES>
 struct TreeSmem {
@@ -77,11 +78,12 @@ struct TreeSmem {
   static constexpr int kStageOff = kVOff + kVStages * kTileBytes;
   static constexpr int kXchOff = kStageOff + (D == 64 ? 8 * 4096 : 0);  // [2][128] (max, sum)
   static constexpr int kBarOff = kXchOff + 2 * kTrRows * 8;
-  static constexpr int kNumBars = 2 + 4 * kTrMaxStages + 6 + 3;
+  static constexpr int kNumBars = 2 + 4 * kTrMaxStages + 6 + 3 + 4;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   // tensor-memory base, abort flag; non-finite nodes [2] (64 bit); scan [12];
-  // the start of the range
-  static constexpr int kSmemBytes = kMiscOff + 16 + 16 + 48 + 32;
+  // the start of the range; the pieces
+  static constexpr int kPieceOff = kMiscOff + 16 + 16 + 48 + 32;
+  static constexpr int kSmemBytes = kPieceOff + kTrPieces * 32;
   static_assert(kSmemBytes <= 232448, "tree tile does not fit in shared memory");
   static_assert(kKStages <= kTrMaxStages && kVStages <= kTrMaxStages, "ring stages");
 };
@@ -91,7 +93,7 @@ enum TrBar {
   kTrKFull = 2, kTrKEmpty = kTrKFull + kTrMaxStages,
   kTrVFull = kTrKEmpty + kTrMaxStages, kTrVEmpty = kTrVFull + kTrMaxStages,
   kTrSFull = kTrVEmpty + kTrMaxStages, kTrPFull = kTrSFull + 2, kTrODone = kTrPFull + 2,
-  kTrXch = kTrODone + 2, kTrEpi = kTrXch + 1, kTrDrain = kTrEpi + 1
+  kTrXch = kTrODone + 2, kTrEpi = kTrXch + 1, kTrDrain = kTrEpi + 1, kTrPiece0 = kTrDrain + 1
 };
 
 // Where a CTA's range starts, for the merge: sequence (-1: no work), item of
@@ -137,6 +139,12 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int s) {
   r.tiles = (r.ctx + kTrKeys - 1) / kTrKeys;
   return r;
 }
+
+// A piece of an item in a CTA's range, as the softmax and P V warps take it
+// (tiles 0: no more).
+struct TreePiece {
+  int qs, n, ctx, seq, kvh, node0, first, tiles;  // tiles < 0: the whole item
+};
 
 // The pieces of items in one CTA's range, in order.
 template <int G, int TILES>
@@ -209,6 +217,48 @@ __device__ __forceinline__ uint32_t keep_finite(uint32_t w) {
   return w & ~((nonfinite_bf16x2(w) >> 15) * 0xffffu);
 }
 
+// 32 columns of this thread's tensor-memory lane; the registers hold them after
+// the next tmem_wait_ld, which may be many instructions later.
+__device__ __forceinline__ void tmem_ld32u(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+        "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+        "=r"(r[31])
+      : "r"(taddr));
+}
+
+// 32 scores to weights 2^(x sc - m) as bf16 hi + lo pairs, in place: of each
+// 16 scores hi in the first 8 registers, lo in the others.  Adds the weights
+// to ls.
+__device__ __forceinline__ void tree_weigh(uint32_t (&v)[32], uint64_t sc2, uint64_t nm2,
+                                           uint64_t (&ls)[2]) {
+#pragma unroll
+  for (int b = 0; b < 32; b += 16) {
+    uint32_t lo[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      float x0, x1, e0, e1, r0, r1;
+      f2_unpack(f2_fma(f2_pack(__uint_as_float(v[b + 2 * u]), __uint_as_float(v[b + 2 * u + 1])),
+                       sc2, nm2), x0, x1);
+      const uint64_t e = f2_pack(ex2(x0), ex2(x1));
+      ls[u & 1] = f2_add(ls[u & 1], e);
+      f2_unpack(e, e0, e1);
+      const uint32_t h = pack_bf16x2(e0, e1);
+      f2_unpack(f2_sub(e, f2_pack(bf16_lo_to_f32(h), bf16_hi_to_f32(h))), r0, r1);
+      v[b + u] = h;
+      lo[u] = pack_bf16x2(r0, r1);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[b + 8 + u] = lo[u];
+  }
+}
+
 template <int D, int G, int TILES>
 __global__ void __launch_bounds__(kTrThreads, 1)
 paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
@@ -228,6 +278,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     int s, off;
   };
   static_assert(sizeof(Begin) <= 32, "start of the range");
+  volatile TreePiece* pieces = reinterpret_cast<volatile TreePiece*>(smem + T::kPieceOff);
   Begin* begin = reinterpret_cast<Begin*>(smem + T::kMiscOff + 80);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -255,6 +306,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     mbar_init(bars + 8 * kTrXch, 8);
     mbar_init(bars + 8 * kTrEpi, 8);
     mbar_init(bars + 8 * kTrDrain, 2);
+    for (int s = 0; s < kTrPieces; ++s) mbar_init(bars + 8 * (kTrPiece0 + s), 1);
     fence_barrier_init();
     *abort_flag = 0;
     nonfinite[0] = nonfinite[1] = 0;
@@ -321,6 +373,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
   if (count > 0) {
   TreeWalk<G, TILES> walk(p, begin->seq, begin->s, begin->off, count);
 
+  if (warp >= 8) {
   if (warp == kTrKWarp || warp == kTrVWarp) {
     // ================= K and V rings =================
     const bool is_v = warp == kTrVWarp;
@@ -387,7 +440,27 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       };
       int i = 0, k = 0;
       bool ok = true;
-      for (; ok && walk.next(); ++k) {
+      // The pieces are worked out here, ahead of those who need them.  Slot k
+      // is free: the last S product needed a P V of piece k - 3 or later, whose
+      // first one needed everybody to be through with piece k - 4.
+      auto publish = [&](bool some) {
+        volatile TreePiece* t = pieces + k % kTrPieces;
+        if (some) {
+          t->qs = walk.seq.qs;
+          t->n = walk.seq.n;
+          t->ctx = walk.seq.ctx;
+          t->seq = walk.s;
+          t->kvh = walk.kv_head();
+          t->node0 = walk.group() * TILES * TPT;
+          t->first = walk.first;
+        }
+        t->tiles = some ? (walk.whole() ? -walk.tiles : walk.tiles) : 0;
+        mbar_arrive(bars + 8 * (kTrPiece0 + k % kTrPieces));
+      };
+      for (; ok; ++k) {
+        const bool some = walk.next();
+        publish(some);
+        if (!some) break;
         ok = k == 0 || wait(kTrQEmpty, (k - 1) & 1);
         if (!ok) break;
         mbar_arrive_expect_tx(bars + 8 * kTrQFull, T::kQBytes);
@@ -431,7 +504,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       if (!ok && k > 0) (void)mbar_wait_bounded(bars + 8 * kTrQFull, (k - 1) & 1);
     }
     __syncwarp();
-  } else if (warp == kTrPvWarp) {
+  } else {
     // ================= the products O += P V (one thread) =================
     if (lane == 0) {
       constexpr uint32_t kIdesc = idesc_bf16_f32(128, D, 0, 1);
@@ -448,10 +521,13 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
         return true;
       };
       int k = 0;
-      for (; ok && walk.next(); ++k) {
+      for (; ok; ++k) {
+        ok = wait(kTrPiece0 + k % kTrPieces, (k / kTrPieces) & 1);
+        const int tiles = ok ? abs(pieces[k % kTrPieces].tiles) : 0;
+        if (tiles == 0) break;
         if (k > 0) ok = after_epilogue(k);
 #pragma unroll 1
-        for (int j = 0; ok && j < walk.tiles; ++j, ++i) {
+        for (int j = 0; ok && j < tiles; ++j, ++i) {
           const bool fresh = j < (TILES == 1 ? 2 : 1);  // the accumulator's first tile of the piece
           ok = wait(kTrVFull + i % T::kVStages, (i / T::kVStages) & 1);
           const uint32_t v_smem = sbase + T::kVOff + (i % T::kVStages) * T::kTileBytes;
@@ -464,13 +540,13 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
             for (int c = 0; c < kTrKeys / 16; ++c) {
               const uint64_t vdesc = smem_desc_sw128(v_smem + c * 2048, T::kHalf, 1024);
-              const uint32_t a_hi = tmem + w * 256 + 64 * (c >> 2) + 8 * (c & 3);
+              const uint32_t a_hi = tmem + w * 256 + 16 * c;  // hi, and lo 8 columns on
               umma_bf16_ts(tmem + w * 256 + 128, a_hi, vdesc, kIdesc, (!fresh || c > 0) ? 1u : 0u);
-              umma_bf16_ts(tmem + w * 256 + 128, a_hi + 32, vdesc, kIdesc, 1u);
+              umma_bf16_ts(tmem + w * 256 + 128, a_hi + 8, vdesc, kIdesc, 1u);
             }
             umma_commit(bars + 8 * (kTrODone + w));
           }
-          if (j + 1 < walk.tiles) umma_commit(bars + 8 * (kTrVEmpty + i % T::kVStages));
+          if (j + 1 < tiles) umma_commit(bars + 8 * (kTrVEmpty + i % T::kVStages));
         }
       }
       if (ok) ok = after_epilogue(k);
@@ -479,6 +555,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       (void)mbar_wait_bounded(bars + 8 * kTrDrain, 0);
     }
     __syncwarp();
+  }
   } else {
     // ================= softmax, correction, epilogue =================
     const int w = warp >> 2;
@@ -490,25 +567,30 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     const float mag = fabsf(p.scale_log2);
     int i = 0;  // stream tile the current piece begins at
     bool ok = true;
-    for (int k = 0; ok && walk.next(); ++k) {
-      const TreeSeq& q = walk.seq;
-      const int node0 = (walk.group() * TILES + (TILES == 2 ? w : 0)) * TPT;  // of the tile
+    for (int k = 0;; ++k) {
+      ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * (kTrPiece0 + k % kTrPieces),
+                                           (k / kTrPieces) & 1, abort_flag));
+      if (!ok) break;
+      const volatile TreePiece* piece = pieces + k % kTrPieces;
+      const int n = piece->n, ctx = piece->ctx, first = piece->first, tiles = abs(piece->tiles);
+      if (tiles == 0) break;
+      const int node0 = piece->node0 + (TILES == 2 ? w : 0) * TPT;  // of the tile
       const int node = node0 + r / G;
-      const bool valid = node < q.n;
+      const bool valid = node < n;
       const bool warp_valid = __any_sync(0xffffffffu, valid);
-      const int base = q.ctx - q.n;  // committed keys
+      const int base = ctx - n;  // committed keys
       unsigned long long mask = 0;
       if (valid) {
-        mask = __ldg(p.tree_mask + q.qs + node);
-        if (q.n < 64) mask &= (1ull << q.n) - 1ull;
+        mask = __ldg(p.tree_mask + piece->qs + node);
+        if (n < 64) mask &= (1ull << n) - 1ull;
       }
       float m = -INFINITY, l = 0.f;
       int seen = 0;  // tiles of the piece this warpgroup has taken
-      for (int j = 0; j < walk.tiles; ++j) {
+      for (int j = 0; j < tiles; ++j) {
         const int it = i + j;
         if (TILES == 1 && (it & 1) != w) continue;
         const int ph = TILES == 1 ? it >> 1 : it;
-        const int key0 = (walk.first + j) * kTrKeys;
+        const int key0 = (first + j) * kTrKeys;
         const bool masked = key0 + kTrKeys > base;
         ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * (kTrSFull + w), ph & 1, abort_flag));
         if (!ok) break;
@@ -520,12 +602,12 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll 1
             for (int c = 0; c < kTrKeys; c += 32) {
               const uint32_t bits = key_bits(mask, key0 + c - base);
-              float x[32];
-              tmem_ld32(lane_base + s_col + c, x);
+              uint32_t x[32];
+              tmem_ld32u(lane_base + s_col + c, x);
               tmem_wait_ld();
 #pragma unroll
-              for (int u = 0; u < 32; ++u) x[u] = (bits >> u) & 1u ? x[u] : hide;
-              tmem_st32(lane_base + s_col + c, x);
+              for (int u = 0; u < 32; ++u) x[u] = (bits >> u) & 1u ? x[u] : __float_as_uint(hide);
+              tmem_st32u(lane_base + s_col + c, x);
             }
             tmem_wait_st();
           }
@@ -540,17 +622,19 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
           bool raise = !__all_sync(0xffffffffu, m != -INFINITY), settled = false;
 #pragma unroll 1
           for (int c = 0; c < kTrKeys;) {
-            float va[32], vb[32];
+            uint32_t va[32], vb[32];
             if (raise) {
               float ex[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+              const uint32_t flip = neg ? 0x80000000u : 0u;
 #pragma unroll 1
               for (int cc = c; cc < kTrKeys; cc += 64) {
-                tmem_ld32(lane_base + s_col + cc, va);
-                tmem_ld32(lane_base + s_col + cc + 32, vb);
+                tmem_ld32u(lane_base + s_col + cc, va);
+                tmem_ld32u(lane_base + s_col + cc + 32, vb);
                 tmem_wait_ld();
 #pragma unroll
                 for (int u = 0; u < 32; ++u)
-                  ex[u & 3] = max3f(ex[u & 3], neg ? -va[u] : va[u], neg ? -vb[u] : vb[u]);
+                  ex[u & 3] = max3f(ex[u & 3], __uint_as_float(va[u] ^ flip),
+                                    __uint_as_float(vb[u] ^ flip));
               }
               const float top = fmaxf(fmaxf(ex[0], ex[1]), fmaxf(ex[2], ex[3]));
               const float mx = top == -INFINITY ? -INFINITY : top * mag;
@@ -566,35 +650,35 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
                   const uint64_t a2 = f2_pack(alpha, alpha);
 #pragma unroll 1
                   for (int cc = 0; cc < D; cc += 32) {
-                    tmem_ld32(lane_base + o_col + cc, va);
+                    tmem_ld32u(lane_base + o_col + cc, va);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int u = 0; u < 32; u += 2)
-                      f2_unpack(f2_mul(f2_pack(va[u], va[u + 1]), a2), va[u], va[u + 1]);
-                    tmem_st32(lane_base + o_col + cc, va);
+                    for (int u = 0; u < 32; u += 2) {
+                      float y0, y1;
+                      f2_unpack(f2_mul(f2_pack(__uint_as_float(va[u]), __uint_as_float(va[u + 1])),
+                                       a2), y0, y1);
+                      va[u] = __float_as_uint(y0), va[u + 1] = __float_as_uint(y1);
+                    }
+                    tmem_st32u(lane_base + o_col + cc, va);
                   }
                 }
                 if (c > 0) {
                   // so is the P of the tile's first keys, already stored
                   tmem_wait_st();
 #pragma unroll 1
-                  for (int cc = 0; cc < 32; cc += 16) {
-                    float ph16[16], pl16[16];
-                    tmem_ld16(lane_base + s_col + cc, ph16);
-                    tmem_ld16(lane_base + s_col + 32 + cc, pl16);
+                  for (int cc = 0; cc < c; cc += 32) {
+                    tmem_ld32u(lane_base + s_col + cc, va);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int u = 0; u < 16; ++u) {
-                      const uint32_t h = __float_as_uint(ph16[u]), lw = __float_as_uint(pl16[u]);
+                    for (int u = 0; u < 32; u += u % 8 == 7 ? 9 : 1) {
+                      const uint32_t h = va[u], lw = va[u + 8];
                       const float e0 = (bf16_lo_to_f32(h) + bf16_lo_to_f32(lw)) * alpha;
                       const float e1 = (bf16_hi_to_f32(h) + bf16_hi_to_f32(lw)) * alpha;
-                      const uint32_t n = pack_bf16x2(e0, e1);
-                      ph16[u] = __uint_as_float(n);
-                      pl16[u] = __uint_as_float(
-                          pack_bf16x2(e0 - bf16_lo_to_f32(n), e1 - bf16_hi_to_f32(n)));
+                      va[u] = pack_bf16x2(e0, e1);
+                      va[u + 8] =
+                          pack_bf16x2(e0 - bf16_lo_to_f32(va[u]), e1 - bf16_hi_to_f32(va[u]));
                     }
-                    tmem_st16(lane_base + s_col + cc, ph16);
-                    tmem_st16(lane_base + s_col + 32 + cc, pl16);
+                    tmem_st32u(lane_base + s_col + cc, va);
                   }
                 }
                 l *= alpha;
@@ -603,29 +687,16 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
               raise = false;
               settled = true;
             }
-            // P = 2^(x - m) as bf16 hi + lo
-            tmem_ld32(lane_base + s_col + c, va);
-            tmem_ld32(lane_base + s_col + c + 32, vb);
+            // P = 2^(x - m) as bf16 hi + lo in the scores' place: of each 16 keys
+            // hi in the first 8 columns, lo in the others, two keys a column
+            tmem_ld32u(lane_base + s_col + c, va);
+            tmem_ld32u(lane_base + s_col + c + 32, vb);
             const float mref = m == -INFINITY ? 0.f : m;  // nothing seen yet: all P are 0
             const uint64_t nm2 = f2_pack(-mref, -mref);
             uint64_t ls[2] = {0ull, 0ull};
             tmem_wait_ld();
-            uint32_t hi[32], lo[32];
-#pragma unroll
-            for (int u = 0; u < 32; ++u) {
-              const int kk = 2 * u;
-              const float s0 = kk < 32 ? va[kk] : vb[kk - 32];
-              const float s1 = kk < 32 ? va[kk + 1] : vb[kk - 31];
-              float x0, x1;
-              f2_unpack(f2_fma(f2_pack(s0, s1), sc2, nm2), x0, x1);
-              const uint64_t e = f2_pack(ex2(x0), ex2(x1));
-              ls[u & 1] = f2_add(ls[u & 1], e);
-              float e0, e1, r0, r1;
-              f2_unpack(e, e0, e1);
-              hi[u] = pack_bf16x2(e0, e1);
-              f2_unpack(f2_sub(e, f2_pack(bf16_lo_to_f32(hi[u]), bf16_hi_to_f32(hi[u]))), r0, r1);
-              lo[u] = pack_bf16x2(r0, r1);
-            }
+            tree_weigh(va, sc2, nm2, ls);
+            tree_weigh(vb, sc2, nm2, ls);
             float a0, a1, b0, b1;
             f2_unpack(ls[0], a0, a1);
             f2_unpack(ls[1], b0, b1);
@@ -635,10 +706,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
               continue;
             }
             l += sum;
-            // over the columns of the scores: keys [64 g, 64 g + 64) have hi at
-            // 64 g and lo at 64 g + 32, two keys a column
-            tmem_st32u(lane_base + s_col + c, hi);
-            tmem_st32u(lane_base + s_col + c + 32, lo);
+            tmem_st32u(lane_base + s_col + c, va);
+            tmem_st32u(lane_base + s_col + c + 32, vb);
             c += 64;
           }
           if (!ok) break;
@@ -668,7 +737,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 }
               }
             if (any) {
-              if (key < q.ctx) atomicOr(nonfinite + (k & 1), 1ull << (key - base));
+              if (key < ctx) atomicOr(nonfinite + (k & 1), 1ull << (key - base));
               fence_proxy_async_smem();
             }
           }
@@ -695,7 +764,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       // both accumulators' last products of the piece are done: each may be
       // read, and nobody reads the last V tile any more
       const int begin_tile = i;
-      i += walk.tiles;
+      i += tiles;
 #pragma unroll 1
       for (int a = 0; a < 2; ++a) {
         const int lt = TILES == 2 || ((i - 1) & 1) == a ? i - 1 : i - 2;  // its last tile
@@ -722,9 +791,9 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       tc_fence_after();
 
       if (warp_valid) {
+        const int qs = piece->qs, seq = piece->seq, kvh = piece->kvh;
+        const bool whole = piece->tiles < 0;
         const unsigned long long hit = mask & nonfinite[k & 1];
-        const int kvh = walk.kv_head();
-        const bool whole = walk.whole();
         // slot 2c: the piece the CTA's range starts with, 2c + 1: the one it ends with
         const size_t slot = size_t(blockIdx.x) * 2 + (k == 0 ? 0 : 1);
         const size_t prow0 = (slot * TILES + (TILES == 2 ? w : 0)) * kTrRows + (warp & 3) * 32;
@@ -737,68 +806,68 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const int chunk0 = col0 + 4 * (lane & 7);
         float* part = p.part_o + prow0 * D + chunk0;
         const size_t out0 =
-            ((size_t(q.qs) + node0) * p.q_heads + size_t(kvh) * G) * D + chunk0;
+            ((size_t(qs) + node0) * p.q_heads + size_t(kvh) * G) * D + chunk0;
         const bool use_a = __any_sync(0xffffffffu, fa != 0.f);
         const bool use_b = TILES == 1 && __any_sync(0xffffffffu, fb != 0.f);
 #pragma unroll 1
         for (int c = 0; c < kCols; c += 32) {
-          float o[32];
+          uint32_t o[32], x[32];
+          if (use_a) tmem_ld32u(lane_base + o_col + col0 + c, o);
+          if (use_b) tmem_ld32u(lane_base + (256 - s_col) + 128 + col0 + c, x);
+          tmem_wait_ld();
+          // an accumulator that no tile of the piece went to holds anything
+          const uint64_t a2 = f2_pack(fa, fa), b2 = f2_pack(fb, fb);
 #pragma unroll
-          for (int u = 0; u < 32; ++u) o[u] = 0.f;
-          if (use_a) {
-            float a[32];
-            tmem_ld32(lane_base + o_col + col0 + c, a);
-            tmem_wait_ld();
-#pragma unroll
-            for (int u = 0; u < 32; ++u) o[u] = fa != 0.f ? a[u] * fa : 0.f;
-          }
-          if (use_b) {
-            float b[32];
-            tmem_ld32(lane_base + (256 - s_col) + 128 + col0 + c, b);
-            tmem_wait_ld();
-#pragma unroll
-            for (int u = 0; u < 32; ++u) o[u] += fb != 0.f ? b[u] * fb : 0.f;
-          }
-          // non-finite V elements of nodes this row sees (rare)
-          for (unsigned long long h = hit; h; h &= h - 1) {
-            const int at = base + __ffsll(h) - 1;
-            const int id = __ldg(p.block_tables + size_t(walk.s) * p.max_blocks_per_seq + at / 16);
-            const int64_t row = (int64_t(id) * 16 + at % 16) * p.kv_heads + kvh;
-            for (int u = 0; u < 32; ++u) {
-              const uint32_t x = reinterpret_cast<const uint16_t*>(p.v_pool)[row * D + col0 + c + u];
-              if ((x & 0x7f80u) == 0x7f80u) {
-                const float add = __uint_as_float(x << 16);
-#pragma unroll
-                for (int z = 0; z < 32; ++z) o[z] += z == u ? add : 0.f;
-              }
-            }
+          for (int u = 0; u < 32; u += 2) {
+            uint64_t y = use_a ? f2_mul(f2_pack(__uint_as_float(o[u]), __uint_as_float(o[u + 1])), a2)
+                               : 0ull;
+            if (use_b)
+              y = f2_fma(f2_pack(__uint_as_float(x[u]), __uint_as_float(x[u + 1])), b2, y);
+            float y0, y1;
+            f2_unpack(y, y0, y1);
+            o[u] = __float_as_uint(y0), o[u + 1] = __float_as_uint(y1);
           }
           // Through shared memory, so that a store covers whole rows of the
           // 32 x 32 block instead of 16 bytes of each of 32 rows: 32 rows of
           // 128 bytes, the 16-byte chunks of row r rotated by r.
 #pragma unroll
           for (int u = 0; u < 8; ++u)
-            st_shared_f4(stage + lane * 128 + (((u + lane) & 7) << 4), o[4 * u], o[4 * u + 1],
-                         o[4 * u + 2], o[4 * u + 3]);
+            st_shared_u4(stage + lane * 128 + (((u + lane) & 7) << 4),
+                         make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]));
+          // non-finite V elements of nodes this row sees (rare)
+          for (unsigned long long h = hit; h; h &= h - 1) {
+            const int at = base + __ffsll(h) - 1;
+            const int id = __ldg(p.block_tables + size_t(seq) * p.max_blocks_per_seq + at / 16);
+            const uint16_t* row = static_cast<const uint16_t*>(p.v_pool) + col0 + c +
+                                  ((int64_t(id) * 16 + at % 16) * p.kv_heads + kvh) * D;
+#pragma unroll 1
+            for (int u = 0; u < 32; ++u) {
+              const uint32_t v = row[u];
+              if ((v & 0x7f80u) != 0x7f80u) continue;
+              float* y = reinterpret_cast<float*>(
+                  smem + (stage - sbase) + lane * 128 + ((((u >> 2) + lane) & 7) << 4) + (u & 3) * 4);
+              *y += __uint_as_float(v << 16);
+            }
+          }
           __syncwarp();
           // this lane's chunk of rows lane / 8 + 4 u
-#pragma unroll
+#pragma unroll 2
           for (int u = 0; u < 8; ++u) {
             const int row = 4 * u + (lane >> 3);
-            const uint4 x = ld_shared_u4(stage + row * 128 + (((lane + row) & 7) << 4));
+            const uint4 y = ld_shared_u4(stage + row * 128 + (((lane + row) & 7) << 4));
             if (!((rows_valid >> row) & 1u)) continue;
             if (!whole) {
-              *reinterpret_cast<uint4*>(part + row * D + c) = x;
+              *reinterpret_cast<uint4*>(part + row * D + c) = y;
               continue;
             }
             const int tr = (warp & 3) * 32 + row;  // row of the tile
             const size_t at = size_t(tr / G) * (p.q_heads * D) + (tr % G) * D + c;
             if (p.out_bf16)
               *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + out0 + at) =
-                  make_uint2(pack_bf16x2(__uint_as_float(x.x), __uint_as_float(x.y)),
-                             pack_bf16x2(__uint_as_float(x.z), __uint_as_float(x.w)));
+                  make_uint2(pack_bf16x2(__uint_as_float(y.x), __uint_as_float(y.y)),
+                             pack_bf16x2(__uint_as_float(y.z), __uint_as_float(y.w)));
             else
-              *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + out0 + at) = x;
+              *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + out0 + at) = y;
           }
           __syncwarp();
         }
