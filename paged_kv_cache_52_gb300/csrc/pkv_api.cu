@@ -1841,23 +1841,23 @@ int rope_append(const void* q, int64_t q_tok_stride, const void* k, int64_t k_to
   const int sms = current_device_sms();
   if (sms <= 0) return PKV_ECUDA;
   pkv::QkRopeArgs a;
-  a.q = static_cast<const uint4*>(q);
-  a.k = static_cast<const uint4*>(k);
-  a.v = static_cast<const uint4*>(v);
-  a.q_stride_vec = q_tok_stride / 8;
-  a.k_stride_vec = k_tok_stride / 8;
-  a.v_stride_vec = v_tok_stride / 8;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.q_stride = q_tok_stride;
+  a.k_stride = k_tok_stride;
+  a.v_stride = v_tok_stride;
   a.positions = positions;
   a.table = rope_table;
   a.max_positions = max_positions;
   a.rot_dim = rot_dim;
-  a.q_weight = static_cast<const uint4*>(q_weight);
-  a.k_weight = static_cast<const uint4*>(k_weight);
+  a.q_weight = static_cast<const __nv_bfloat16*>(q_weight);
+  a.k_weight = static_cast<const __nv_bfloat16*>(k_weight);
   a.eps = eps;
   a.slot_mapping = slot_mapping;
   a.num_tokens = num_tokens;
   a.num_slots = int64_t(cache.num_blocks) * cache.block_size;
-  a.q_out = static_cast<uint4*>(q_out);
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
   a.k_cache = k_cache;
   a.v_cache = v_cache;
   a.q_heads = q_heads;

@@ -5,6 +5,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 namespace pkv {
@@ -241,17 +242,17 @@ unsigned read_mixed_error(bool clear);
 
 // ---- qk_rope_append.cu: norm and rotation of queries and keys, and the append
 struct QkRopeArgs {
-  const uint4 *q, *k, *v;                       // 16-byte vectors of 8 bf16
-  int64_t q_stride_vec, k_stride_vec, v_stride_vec;  // per token
+  const __nv_bfloat16 *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;         // elements per token
   const int64_t* positions;
   const float* table;                           // [max_positions][rot_dim]: cosines, sines
   int64_t max_positions;
   int rot_dim;
-  const uint4 *q_weight, *k_weight;             // [d_head] bf16, or null: no norm
+  const __nv_bfloat16 *q_weight, *k_weight;     // [d_head], or null: no norm
   float eps;
   const int64_t* slot_mapping;
   int64_t num_tokens, num_slots;
-  uint4* q_out;
+  __nv_bfloat16* q_out;
   void *k_cache, *v_cache;
   int q_heads, kv_heads;
   float k_inv, v_inv;                           // FP8 pools: 1 / scale

@@ -12,17 +12,19 @@
 // Everything is float32 from the bf16 inputs on; q', k' are rounded once, to
 // bf16 or (keys and values of FP8 pools) to e4m3.
 //
-// Bound by memory: each q, k, v element is read once and written once, ~8
-// flops each.  A lane holds 8 consecutive elements (one 16-byte load), d / 8
-// lanes a head, so a norm is log2(d / 8) shuffles and a rotation partner sits
-// in the same lane (interleaved) or rot / 16 lanes away (one packed shuffle of
-// the raw bf16 values; the partner's weight is loaded instead of its product).
-// A warp takes kRows row slots of one token's q, k and v heads laid end to
-// end, so the token's angles and the weights are loaded once for all of them.
+// Bound by memory: each q, k, v element is read once and written once; what
+// has to be kept low beside that are the instructions per element.  A lane
+// holds two runs of 4 elements that are each other's partners (i, i + rot/2),
+// so a pair never leaves its lane; d / 8 lanes make a head, and a norm is
+// log2(d / 8) shuffles.  A warp takes kRows x (256 / d) heads of one token and
+// one kind (q, k or v): the products of the weights with the cosines and
+// sines are made once for all of them, and a rotation is then two packed
+// multiply-adds for two elements.
 #include <cuda_fp8.h>
 
 #include "pkv_device.cuh"
 #include "pkv_internal.h"
+#include "pkv_tcgen05.cuh"
 
 namespace pkv {
 
@@ -30,160 +32,190 @@ static __device__ unsigned g_rope_error = 0;
 
 constexpr int kRopeThreads = 128;
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  f[0] = bf16_lo_to_f32(v.x), f[1] = bf16_hi_to_f32(v.x);
-  f[2] = bf16_lo_to_f32(v.y), f[3] = bf16_hi_to_f32(v.y);
-  f[4] = bf16_lo_to_f32(v.z), f[5] = bf16_hi_to_f32(v.z);
-  f[6] = bf16_lo_to_f32(v.w), f[7] = bf16_hi_to_f32(v.w);
+// Two packed bf16 as two packed floats.
+__device__ __forceinline__ uint64_t f2_of_bf16x2(uint32_t v) {
+  return f2_pack(bf16_lo_to_f32(v), bf16_hi_to_f32(v));
 }
 
-__device__ __forceinline__ uint4 pack8_bf16(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ uint32_t bf16x2_of_f2(uint64_t v) {
+  float a, b;
+  f2_unpack(v, a, b);
+  return pack_bf16x2(a, b);
 }
 
-__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+__device__ __forceinline__ uint32_t e4m3x4_of_f2(uint64_t v, uint64_t w) {
+  float a, b, c, d;
+  f2_unpack(v, a, b);
+  f2_unpack(w, c, d);
   const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
   const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
   return (lo & 0xffffu) | (hi << 16);
 }
 
-__device__ __forceinline__ uint2 pack8_e4m3(const float (&f)[8], float inv) {
-  return make_uint2(e4m3x4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv),
-                    e4m3x4(f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv));
-}
-
-// ROWS: row slots in flight per lane.
+// ROWS: heads in flight per lane.
 template <int D, bool INTERLEAVED, bool FP8, int ROWS>
 __global__ void __launch_bounds__(kRopeThreads)
 qk_rope_append_kernel(const QkRopeArgs p) {
   griddep_wait();  // inputs may have been written by the previous kernel in the stream
   constexpr int LPH = D / 8;       // lanes per head
-  constexpr int HPR = 32 / LPH;    // heads per row slot
+  constexpr int HPR = 32 / LPH;    // heads a warp holds side by side
   constexpr int HPU = ROWS * HPR;  // heads per warp
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t(blockIdx.x) * kRopeThreads + threadIdx.x) >> 5;
-  const int heads = p.q_heads + 2 * p.kv_heads;
-  const int units = (heads + HPU - 1) / HPU;  // warps per token
+  const int q_units = (p.q_heads + HPU - 1) / HPU, kv_units = (p.kv_heads + HPU - 1) / HPU;
+  const int units = q_units + 2 * kv_units;  // warps per token
   const int64_t t = unit / units;
   if (t >= p.num_tokens) return;
-  const int h0 = int(unit - t * units) * HPU + lane / LPH;
-  const int hl = lane % LPH;  // this lane's 8 elements: 8 hl ..
+  const int u = int(unit - t * units);
+  const bool is_q = u < q_units, is_v = u >= q_units + kv_units;
+  const int h0 = (is_q ? u : (is_v ? u - q_units - kv_units : u - q_units)) * HPU + lane / LPH;
+  const int heads = is_q ? p.q_heads : p.kv_heads;
+  const int hl = lane % LPH;
+  // this lane's two runs of 4 elements: partners, or (interleaved, and beyond
+  // the rotated elements) neighbours
+  const bool turns = 8 * hl < p.rot_dim;
+  const bool apart = !INTERLEAVED && turns;
+  const int ea = apart ? 4 * hl : 8 * hl;
+  const int eb = apart ? ea + p.rot_dim / 2 : ea + 4;
 
   const int64_t pos = __ldg(p.positions + t);
   const int64_t slot = __ldg(p.slot_mapping + t);
-  uint4 x[ROWS];
+  const __nv_bfloat16* src = is_q ? p.q + t * p.q_stride : (is_v ? p.v + t * p.v_stride
+                                                                 : p.k + t * p.k_stride);
+  uint2 xa[ROWS], xb[ROWS];
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     const int h = h0 + i * HPR;
-    const uint4* src = nullptr;
-    if (h < p.q_heads)
-      src = p.q + t * p.q_stride_vec + int64_t(h) * LPH;
-    else if (h < p.q_heads + p.kv_heads)
-      src = p.k + t * p.k_stride_vec + int64_t(h - p.q_heads) * LPH;
-    else if (h < heads)
-      src = p.v + t * p.v_stride_vec + int64_t(h - p.q_heads - p.kv_heads) * LPH;
-    x[i] = src ? __ldg(src + hl) : make_uint4(0u, 0u, 0u, 0u);
+    xa[i] = xb[i] = make_uint2(0u, 0u);
+    if (h < heads) {
+      xa[i] = __ldg(reinterpret_cast<const uint2*>(src + h * D + ea));
+      xb[i] = __ldg(reinterpret_cast<const uint2*>(src + h * D + eb));
+    }
   }
   const bool bad_pos = pos < 0 || pos >= p.max_positions;
   const bool bad_slot = slot < -1 || slot >= p.num_slots;
   if ((bad_pos || bad_slot) && lane == 0)
     atomicOr(&g_rope_error, (bad_pos ? kErrBadPosition : 0u) | (bad_slot ? kErrBadSlot : 0u));
-  if (bad_pos) return;  // the whole token is skipped
+  if (bad_pos) return;                              // the whole token is skipped
+  if (!is_q && (slot == -1 || bad_slot)) return;
 
-  // angles of this lane's elements (or pairs)
-  const int half = p.rot_dim / 2;
-  const bool turns = 8 * hl < p.rot_dim;
-  const bool second = !INTERLEAVED && 8 * hl >= half;
-  constexpr int NC = INTERLEAVED ? 4 : 8;
-  float c[NC], s[NC];
+  // where head h's elements go: q_out, or the slot's row of a pool
+  const int64_t row0 = is_q ? t * p.q_heads : slot * p.kv_heads;
+  if (is_v) {
 #pragma unroll
-  for (int i = 0; i < NC; ++i) c[i] = 1.f, s[i] = 0.f;
+    for (int i = 0; i < ROWS; ++i) {
+      const int h = h0 + i * HPR;
+      if (h >= heads) continue;
+      const int64_t at = (row0 + h) * D;
+      if constexpr (FP8) {
+        const uint64_t inv = f2_pack(p.v_inv, p.v_inv);
+        uint8_t* dst = static_cast<uint8_t*>(p.v_cache) + at;
+        *reinterpret_cast<uint32_t*>(dst + ea) =
+            e4m3x4_of_f2(f2_mul(f2_of_bf16x2(xa[i].x), inv), f2_mul(f2_of_bf16x2(xa[i].y), inv));
+        *reinterpret_cast<uint32_t*>(dst + eb) =
+            e4m3x4_of_f2(f2_mul(f2_of_bf16x2(xb[i].x), inv), f2_mul(f2_of_bf16x2(xb[i].y), inv));
+      } else {
+        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.v_cache) + at;
+        *reinterpret_cast<uint2*>(dst + ea) = xa[i];
+        *reinterpret_cast<uint2*>(dst + eb) = xb[i];
+      }
+    }
+    return;
+  }
+
+  const __nv_bfloat16* weight = is_q ? p.q_weight : p.k_weight;
+  uint64_t wa[2], wb[2];  // weights of the two runs, two elements each
+  wa[0] = wa[1] = wb[0] = wb[1] = f2_pack(1.f, 1.f);
+  if (weight) {
+    const uint2 a = __ldg(reinterpret_cast<const uint2*>(weight + ea));
+    const uint2 b = __ldg(reinterpret_cast<const uint2*>(weight + eb));
+    wa[0] = f2_of_bf16x2(a.x), wa[1] = f2_of_bf16x2(a.y);
+    wb[0] = f2_of_bf16x2(b.x), wb[1] = f2_of_bf16x2(b.y);
+  }
+  // cosines and sines of pairs 4 hl .. 4 hl + 3
+  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (turns) {
-    const float* row = p.table + pos * p.rot_dim +
-                       (INTERLEAVED ? 4 * hl : (second ? 8 * hl - half : 8 * hl));
+    const float* row = p.table + pos * p.rot_dim + 4 * hl;
+    c = __ldg(reinterpret_cast<const float4*>(row));
+    s = __ldg(reinterpret_cast<const float4*>(row + p.rot_dim / 2));
+  }
+  // apart:       y_a = x_a (w_a c) + x_b (-w_b s),  y_b = x_b (w_b c) + x_a (w_a s)
+  // interleaved: y = x (w c) + swap(x) (swap(w) (-s, s)), pairs side by side
+  uint64_t same_a[2], same_b[2], cross_a[2], cross_b[2];
+  if constexpr (INTERLEAVED) {
+    const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-    for (int i = 0; i < NC; i += 4) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(row + i));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(row + half + i));
-      c[i] = a.x, c[i + 1] = a.y, c[i + 2] = a.z, c[i + 3] = a.w;
-      s[i] = b.x, s[i + 1] = b.y, s[i + 2] = b.z, s[i + 3] = b.w;
+    for (int i = 0; i < 2; ++i) {
+      float lo, hi;
+      same_a[i] = f2_mul(wa[i], f2_pack(cs[i], cs[i]));
+      same_b[i] = f2_mul(wb[i], f2_pack(cs[2 + i], cs[2 + i]));
+      f2_unpack(wa[i], lo, hi);
+      cross_a[i] = f2_mul(f2_pack(hi, lo), f2_pack(-sn[i], sn[i]));
+      f2_unpack(wb[i], lo, hi);
+      cross_b[i] = f2_mul(f2_pack(hi, lo), f2_pack(-sn[2 + i], sn[2 + i]));
+    }
+  } else {
+    const uint64_t cc[2] = {f2_pack(c.x, c.y), f2_pack(c.z, c.w)};
+    const uint64_t ss[2] = {f2_pack(s.x, s.y), f2_pack(s.z, s.w)};
+    const uint64_t neg = f2_pack(-1.f, -1.f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      same_a[i] = f2_mul(wa[i], cc[i]);
+      same_b[i] = f2_mul(wb[i], cc[i]);
+      cross_a[i] = f2_mul(f2_mul(wb[i], ss[i]), neg);
+      cross_b[i] = f2_mul(wa[i], ss[i]);
     }
   }
-  const int reach = half / 8;  // lanes between the halves of a pair
-  const int partner = (turns && !INTERLEAVED) ? (second ? lane - reach : lane + reach) : lane;
-  const int pl = partner % LPH;
-  const uint4 one = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-  uint4 qw = one, kw = one, qwp = one, kwp = one;
-  if (p.q_weight) qw = __ldg(p.q_weight + hl), qwp = __ldg(p.q_weight + pl);
-  if (p.k_weight) kw = __ldg(p.k_weight + hl), kwp = __ldg(p.k_weight + pl);
 
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     const int h = h0 + i * HPR;
-    const bool is_q = h < p.q_heads;
-    const bool is_k = !is_q && h < p.q_heads + p.kv_heads;
-    float f[8];
-    unpack8(x[i], f);
-    float inv = 1.f;
-    float ss = 0.f;
+    const uint64_t fa[2] = {f2_of_bf16x2(xa[i].x), f2_of_bf16x2(xa[i].y)};
+    const uint64_t fb[2] = {f2_of_bf16x2(xb[i].x), f2_of_bf16x2(xb[i].y)};
+    float inv = is_q || !FP8 ? 1.f : p.k_inv;
+    if (weight) {  // uniform over the warp
+      const uint64_t sq = f2_add(f2_fma(fa[0], fa[0], f2_mul(fa[1], fa[1])),
+                                 f2_fma(fb[0], fb[0], f2_mul(fb[1], fb[1])));
+      float lo, hi;
+      f2_unpack(sq, lo, hi);
+      float sum = lo + hi;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(f[e], f[e], ss);
-#pragma unroll
-    for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (is_q ? p.q_weight != nullptr : (is_k && p.k_weight != nullptr))
-      inv = rsqrtf(ss * (1.f / D) + p.eps);
-    uint4 other = x[i];
-    if constexpr (!INTERLEAVED) {
-      other.x = __shfl_sync(0xffffffffu, x[i].x, partner);
-      other.y = __shfl_sync(0xffffffffu, x[i].y, partner);
-      other.z = __shfl_sync(0xffffffffu, x[i].z, partner);
-      other.w = __shfl_sync(0xffffffffu, x[i].w, partner);
+      for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      inv *= rsqrtf(sum * (1.f / D) + p.eps);
     }
-    float y[8];
-    if (is_q || is_k) {
-      float w[8];
-      unpack8(is_q ? qw : kw, w);
+    const uint64_t inv2 = f2_pack(inv, inv);
+    uint64_t ya[2], yb[2];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = f[e] * inv * w[e];
+    for (int z = 0; z < 2; ++z) {
+      uint64_t oa = fb[z], ob = fa[z];  // what the sines multiply
       if constexpr (INTERLEAVED) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[2 * e] = f[2 * e] * c[e] - f[2 * e + 1] * s[e];
-          y[2 * e + 1] = f[2 * e + 1] * c[e] + f[2 * e] * s[e];
-        }
-      } else {
-        float g[8];
-        unpack8(other, g);
-        unpack8(is_q ? qwp : kwp, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          g[e] = g[e] * inv * w[e];
-          y[e] = f[e] * c[e] + (second ? g[e] : -g[e]) * s[e];
-        }
-        if (!turns) {  // g is the element itself: keep an infinity out of 0 * inf
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = f[e];
-        }
+        float lo, hi;
+        f2_unpack(fa[z], lo, hi);
+        oa = f2_pack(hi, lo);
+        f2_unpack(fb[z], lo, hi);
+        ob = f2_pack(hi, lo);
       }
-      if (INTERLEAVED && !turns) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = f[e];
+      // elements beyond the rotated ones have no partner: an infinity there
+      // must not meet a sine of 0
+      ya[z] = f2_mul(fa[z], same_a[z]);
+      yb[z] = f2_mul(fb[z], same_b[z]);
+      if (turns) {
+        ya[z] = f2_fma(oa, cross_a[z], ya[z]);
+        yb[z] = f2_fma(ob, cross_b[z], yb[z]);
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = f[e];
+      ya[z] = f2_mul(ya[z], inv2);
+      yb[z] = f2_mul(yb[z], inv2);
     }
-    if (is_q) {
-      p.q_out[(t * p.q_heads + h) * LPH + hl] = pack8_bf16(y);
-    } else if (h < heads && slot != -1 && !bad_slot) {
-      const int kvh = is_k ? h - p.q_heads : h - p.q_heads - p.kv_heads;
-      void* pool = is_k ? p.k_cache : p.v_cache;
-      const int64_t at = (slot * p.kv_heads + kvh) * LPH + hl;
-      if constexpr (FP8)
-        static_cast<uint2*>(pool)[at] = pack8_e4m3(y, is_k ? p.k_inv : p.v_inv);
-      else
-        static_cast<uint4*>(pool)[at] = is_k ? pack8_bf16(y) : x[i];
+    if (h >= heads) continue;
+    const int64_t at = (row0 + h) * D;
+    if (FP8 && !is_q) {
+      uint8_t* dst = static_cast<uint8_t*>(p.k_cache) + at;
+      *reinterpret_cast<uint32_t*>(dst + ea) = e4m3x4_of_f2(ya[0], ya[1]);
+      *reinterpret_cast<uint32_t*>(dst + eb) = e4m3x4_of_f2(yb[0], yb[1]);
+    } else {
+      __nv_bfloat16* dst = (is_q ? p.q_out : static_cast<__nv_bfloat16*>(p.k_cache)) + at;
+      *reinterpret_cast<uint2*>(dst + ea) = make_uint2(bf16x2_of_f2(ya[0]), bf16x2_of_f2(ya[1]));
+      *reinterpret_cast<uint2*>(dst + eb) = make_uint2(bf16x2_of_f2(yb[0]), bf16x2_of_f2(yb[1]));
     }
   }
 }
@@ -205,7 +237,7 @@ unsigned read_rope_error(bool clear) {
 template <int D, bool INTERLEAVED, bool FP8, int ROWS>
 static cudaError_t launch_rope_t(const QkRopeArgs& a, cudaStream_t stream) {
   constexpr int HPU = ROWS * (32 / (D / 8));
-  const int64_t units = (a.q_heads + 2 * a.kv_heads + HPU - 1) / HPU;
+  const int64_t units = (a.q_heads + HPU - 1) / HPU + 2 * ((a.kv_heads + HPU - 1) / HPU);
   const int64_t blocks = (a.num_tokens * units * 32 + kRopeThreads - 1) / kRopeThreads;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
   return launch_after_previous(qk_rope_append_kernel<D, INTERLEAVED, FP8, ROWS>,
