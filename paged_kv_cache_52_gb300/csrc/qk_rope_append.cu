@@ -52,9 +52,11 @@ __device__ __forceinline__ uint32_t e4m3x4_of_f2(uint64_t v, uint64_t w) {
   return (lo & 0xffffu) | (hi << 16);
 }
 
-// ROWS: heads in flight per lane.
+// ROWS: heads in flight per lane.  Nine CTAs an SM (56 registers) measured best
+// with ROWS 4: 16384 tokens into FP8 pools 104.5 us (6.2 TB/s, 0.91 of the
+// measured copy rate), 109 with 8 CTAs, 108 with 10, 110 with 12.
 template <int D, bool INTERLEAVED, bool FP8, int ROWS>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 9)
 qk_rope_append_kernel(const QkRopeArgs p) {
   griddep_wait();  // inputs may have been written by the previous kernel in the stream
   constexpr int LPH = D / 8;       // lanes per head
@@ -167,23 +169,53 @@ qk_rope_append_kernel(const QkRopeArgs p) {
     }
   }
 
+  // the heads' factors: 1 / rms, and 1 / scale for codes
+  float inv[ROWS];
+  const float unit_scale = is_q || !FP8 ? 1.f : p.k_inv;
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) inv[i] = unit_scale;
+  if (weight) {  // uniform over the warp
+    float sum[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const uint64_t a0 = f2_of_bf16x2(xa[i].x), a1 = f2_of_bf16x2(xa[i].y);
+      const uint64_t b0 = f2_of_bf16x2(xb[i].x), b1 = f2_of_bf16x2(xb[i].y);
+      float lo, hi;
+      f2_unpack(f2_fma(a0, a0, f2_fma(a1, a1, f2_fma(b0, b0, f2_mul(b1, b1)))), lo, hi);
+      sum[i] = lo + hi;
+    }
+    if constexpr (ROWS == 4) {
+      // four sums over LPH lanes at once: the lanes' halves, then quarters,
+      // take over a part of the heads each, so that 9 shuffles do for 16
+      const bool up = lane & (LPH / 2), side = lane & (LPH / 4);
+      float k0 = up ? sum[2] : sum[0], k1 = up ? sum[3] : sum[1];
+      k0 += __shfl_xor_sync(0xffffffffu, up ? sum[0] : sum[2], LPH / 2);
+      k1 += __shfl_xor_sync(0xffffffffu, up ? sum[1] : sum[3], LPH / 2);
+      float k = side ? k1 : k0;
+      k += __shfl_xor_sync(0xffffffffu, side ? k0 : k1, LPH / 4);
+#pragma unroll
+      for (int o = LPH / 8; o > 0; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+      k = unit_scale * rsqrtf(k * (1.f / D) + p.eps);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        inv[i] = __shfl_sync(0xffffffffu, k, (lane & ~(LPH - 1)) + (i >> 1) * (LPH / 2) +
+                                                 (i & 1) * (LPH / 4));
+    } else {
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+#pragma unroll
+        for (int o = LPH / 2; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+        inv[i] *= rsqrtf(sum[i] * (1.f / D) + p.eps);
+      }
+    }
+  }
+
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     const int h = h0 + i * HPR;
     const uint64_t fa[2] = {f2_of_bf16x2(xa[i].x), f2_of_bf16x2(xa[i].y)};
     const uint64_t fb[2] = {f2_of_bf16x2(xb[i].x), f2_of_bf16x2(xb[i].y)};
-    float inv = is_q || !FP8 ? 1.f : p.k_inv;
-    if (weight) {  // uniform over the warp
-      const uint64_t sq = f2_add(f2_fma(fa[0], fa[0], f2_mul(fa[1], fa[1])),
-                                 f2_fma(fb[0], fb[0], f2_mul(fb[1], fb[1])));
-      float lo, hi;
-      f2_unpack(sq, lo, hi);
-      float sum = lo + hi;
-#pragma unroll
-      for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      inv *= rsqrtf(sum * (1.f / D) + p.eps);
-    }
-    const uint64_t inv2 = f2_pack(inv, inv);
+    const uint64_t inv2 = f2_pack(inv[i], inv[i]);
     uint64_t ya[2], yb[2];
 #pragma unroll
     for (int z = 0; z < 2; ++z) {
@@ -246,10 +278,13 @@ static cudaError_t launch_rope_t(const QkRopeArgs& a, cudaStream_t stream) {
 
 template <int D, bool INTERLEAVED, bool FP8>
 static cudaError_t launch_rope_r(const QkRopeArgs& a, int num_sms, cudaStream_t stream) {
-  // one row slot per warp spreads a few tokens over the SMs; four share the
-  // angles once there are warps enough to fill them
+  // One head (two of 64) per warp spreads a few tokens over the SMs; four share
+  // the angles, the weights and the shuffles once there is work enough.  Measured
+  // on GB300, one / four, us: 64 q + 2 x 8 kv heads of 128: 1 token 1.48 / 1.74, 64
+  // 1.93 / 1.95, 128 2.65 / 2.25, 2048 22.98 / 12.46; 16 + 2 x 4 heads of 64: 512
+  // tokens 1.95 / 2.20, 1024 2.89 / 2.69.
   const int64_t rows = a.num_tokens * (a.q_heads + 2 * a.kv_heads) / (32 / (D / 8));
-  return rows >= int64_t(num_sms) * 64 ? launch_rope_t<D, INTERLEAVED, FP8, 4>(a, stream)
+  return rows >= int64_t(num_sms) * 24 ? launch_rope_t<D, INTERLEAVED, FP8, 4>(a, stream)
                                        : launch_rope_t<D, INTERLEAVED, FP8, 1>(a, stream);
 }
 
