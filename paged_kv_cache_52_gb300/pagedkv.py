@@ -963,6 +963,7 @@ def describe_device_error(word: int) -> list[str]:
 _BF16, _F32, _I32, _I64, _U8 = (torch.bfloat16, torch.float32, torch.int32, torch.int64,
                                 torch.uint8)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
 @functools.lru_cache(maxsize=256)
@@ -974,10 +975,11 @@ def _refuse(name: str, what: str):
     raise ValueError(f"{name} must be {what}")
 
 
-def _check_packed(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int, *shape: int):
-    """A contiguous tensor of this type and shape on GPU ``dev``."""
+def _check_packed(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int, shape: tuple) -> int:
+    """The address of a contiguous tensor of this type and shape on GPU ``dev``."""
     if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
         _refuse(name, f"a contiguous {dtype} tensor {list(shape)} on one GPU with the others")
+    return t.data_ptr()
 
 
 def _pools(k_cache: torch.Tensor, v_cache: torch.Tensor, *dtypes: torch.dtype) -> int:
@@ -995,7 +997,7 @@ def _pools(k_cache: torch.Tensor, v_cache: torch.Tensor, *dtypes: torch.dtype) -
 def _launch(dev: int, fn, *args):
     """``fn(*args, stream)`` on GPU ``dev``'s current stream; a launch goes to
     the current device, so that is switched when it is another."""
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         st = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -1009,8 +1011,8 @@ def _tree_batch(q_start: torch.Tensor, context_lens: torch.Tensor, dev: int,
     if context_lens.dim() != 1:
         _refuse("context_lens", "[S]")
     S = context_lens.shape[0]
-    _check_packed(context_lens, "context_lens", _I32, dev, S)
-    _check_packed(q_start, "q_start", _I32, dev, S + 1)
+    _check_packed(context_lens, "context_lens", _I32, dev, (S,))
+    _check_packed(q_start, "q_start", _I32, dev, (S + 1,))
     if max_q_len is None:
         max_q_len = int((q_start[1:] - q_start[:-1]).max()) if S else 0
     return S, int(max_q_len)
@@ -1020,7 +1022,7 @@ def _tables(block_tables: torch.Tensor, dev: int, S: int) -> int:
     if block_tables.dim() != 2:
         _refuse("block_tables", "[S, max_blocks]")
     width = block_tables.shape[1]
-    _check_packed(block_tables, "block_tables", _I32, dev, S, width)
+    _check_packed(block_tables, "block_tables", _I32, dev, (S, width))
     return width
 
 
@@ -1047,21 +1049,16 @@ def _rope_append(fn, pool_dtype, q, k, v, positions, rope_table, slot_mapping, k
     sq = _token_rows(q, "q", dev, T, hq, d)
     sk = _token_rows(k, "k", dev, T, hkv, d)
     sv = _token_rows(v, "v", dev, T, hkv, d)
-    _check_packed(positions, "positions", _I64, dev, T)
-    _check_packed(slot_mapping, "slot_mapping", _I64, dev, T)
+    _check_packed(positions, "positions", _I64, dev, (T,))
+    _check_packed(slot_mapping, "slot_mapping", _I64, dev, (T,))
     rows, rot = rope_table.shape
-    _check_packed(rope_table, "rope_table", _F32, dev, rows, rot)
-    qw = kw = None
-    if q_weight is not None:
-        _check_packed(q_weight, "q_weight", _BF16, dev, d)
-        qw = q_weight.data_ptr()
-    if k_weight is not None:
-        _check_packed(k_weight, "k_weight", _BF16, dev, d)
-        kw = k_weight.data_ptr()
+    _check_packed(rope_table, "rope_table", _F32, dev, (rows, rot))
+    qw = None if q_weight is None else _check_packed(q_weight, "q_weight", _BF16, dev, (d,))
+    kw = None if k_weight is None else _check_packed(k_weight, "k_weight", _BF16, dev, (d,))
     if out is None:
-        out = q.new_empty((T, hq, d))
+        out = torch.empty((T, hq, d), dtype=_BF16, device=q.device)
     else:
-        _check_packed(out, "out", _BF16, dev, T, hq, d)
+        _check_packed(out, "out", _BF16, dev, (T, hq, d))
     _launch(dev, fn, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, T, hq,
             positions.data_ptr(), rope_table.data_ptr(), rows, rot, 1 if interleaved else 0, qw,
             kw, eps, slot_mapping.data_ptr(), out.data_ptr(), k_cache.data_ptr(),
@@ -1117,16 +1114,16 @@ def draft_tree_layout(parents: torch.Tensor, q_start: torch.Tensor, context_lens
     if dev < 0 or parents.dim() != 1:
         _refuse("parents", "a CUDA tensor [total]")
     total = parents.shape[0]
-    _check_packed(parents, "parents", _I32, dev, total)
+    _check_packed(parents, "parents", _I32, dev, (total,))
     S, max_q_len = _tree_batch(q_start, context_lens, dev, max_q_len)
     if tree_mask is None:
-        tree_mask = parents.new_empty((total,), dtype=_I64)
+        tree_mask = torch.empty(total, dtype=_I64, device=parents.device)
     else:
-        _check_packed(tree_mask, "tree_mask", _I64, dev, total)
+        _check_packed(tree_mask, "tree_mask", _I64, dev, (total,))
     if positions is None:
-        positions = parents.new_empty((total,), dtype=_I64)
+        positions = torch.empty(total, dtype=_I64, device=parents.device)
     else:
-        _check_packed(positions, "positions", _I64, dev, total)
+        _check_packed(positions, "positions", _I64, dev, (total,))
     _launch(dev, lib.pkv_draft_tree_layout, parents.data_ptr(), q_start.data_ptr(), S, total,
             max_q_len, context_lens.data_ptr(), tree_mask.data_ptr(), positions.data_ptr())
     return tree_mask, positions
@@ -1164,19 +1161,19 @@ def paged_tree_attention(q: torch.Tensor, q_start: torch.Tensor, tree_mask: torc
         _refuse("pools", "contiguous")
     nb, bs, hkv, d = k_cache.shape
     total, hq = q.shape[0], q.shape[1]
-    _check_packed(q, "q", _BF16, dev, total, hq, d)
+    _check_packed(q, "q", _BF16, dev, (total, hq, d))
     S, max_q_len = _tree_batch(q_start, context_lens, dev, max_q_len)
-    _check_packed(tree_mask, "tree_mask", _I64, dev, total)
+    _check_packed(tree_mask, "tree_mask", _I64, dev, (total,))
     width = _tables(block_tables, dev, S)
     odt = _out_dtype(out, out_dtype)
     if out is None:
-        out = q.new_empty((total, hq, d), dtype=odt)
+        out = torch.empty((total, hq, d), dtype=odt, device=q.device)
     else:
-        _check_packed(out, "out", odt, dev, total, hq, d)
+        _check_packed(out, "out", odt, dev, (total, hq, d))
     if workspace is None:
         workspace = tree_attention_workspace(S, max_q_len, hq, hkv, d, q.device)
     else:
-        _check_packed(workspace, "workspace", _U8, dev, workspace.numel())
+        _check_packed(workspace, "workspace", _U8, dev, (workspace.numel(),))
     _launch(dev, lib.pkv_paged_tree_attention_bf16out if odt is _BF16
             else lib.pkv_paged_tree_attention, q.data_ptr(), q_start.data_ptr(), S, total,
             max_q_len, hq, tree_mask.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
@@ -1210,12 +1207,12 @@ def kv_accept_rows(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: t
     if accepted.dim() != 2:
         _refuse("accepted", "[S, max_accepted]")
     most = accepted.shape[1]
-    _check_packed(accepted, "accepted", _I32, dev, S, most)
-    _check_packed(num_accepted, "num_accepted", _I32, dev, S)
+    _check_packed(accepted, "accepted", _I32, dev, (S, most))
+    _check_packed(num_accepted, "num_accepted", _I32, dev, (S,))
     if new_context_lens is None:
-        new_context_lens = context_lens.new_empty((S,))
+        new_context_lens = torch.empty(S, dtype=_I32, device=context_lens.device)
     else:
-        _check_packed(new_context_lens, "new_context_lens", _I32, dev, S)
+        _check_packed(new_context_lens, "new_context_lens", _I32, dev, (S,))
     _launch(dev, lib.pkv_kv_accept_rows, k_cache.data_ptr(), lk, v_cache.data_ptr(), lv, layers,
             _desc(nb, bs, hkv, d), k_cache.element_size(), block_tables.data_ptr(), width,
             context_lens.data_ptr(), q_start.data_ptr(), S, accepted.data_ptr(), most,
