@@ -111,7 +111,7 @@ struct TreeParams {
   const void* v_pool;
   void* out;
   int out_bf16;
-  float* part_o;    // [2 CTAs][TILES * 128][D], normalised
+  float* part_o;    // [2 CTAs][TILES][D / 4][128 rows][4], normalised
   float* part_lse;  // [2 CTAs][TILES * 128], log2
   TreeStart* start; // [CTAs]
   int num_seqs, total_q, max_q_len, q_heads, kv_heads, num_blocks, max_blocks_per_seq;
@@ -804,7 +804,6 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const int col0 = TILES == 1 ? w * kCols : 0;
         const unsigned rows_valid = __ballot_sync(0xffffffffu, valid);
         const int chunk0 = col0 + 4 * (lane & 7);
-        float* part = p.part_o + prow0 * D + chunk0;
         const size_t out0 =
             ((size_t(qs) + node0) * p.q_heads + size_t(kvh) * G) * D + chunk0;
         const bool use_a = __any_sync(0xffffffffu, fa != 0.f);
@@ -827,13 +826,23 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
             f2_unpack(y, y0, y1);
             o[u] = __float_as_uint(y0), o[u + 1] = __float_as_uint(y1);
           }
-          // Through shared memory, so that a store covers whole rows of the
-          // 32 x 32 block instead of 16 bytes of each of 32 rows: 32 rows of
-          // 128 bytes, the 16-byte chunks of row r rotated by r.
+          // A cut item's rows go to the workspace as rows of 4 columns, 512
+          // contiguous bytes a store; a whole item's through shared memory, so
+          // that a store covers whole rows of the 32 x 32 block instead of 16
+          // bytes of each of 32 rows: 32 rows of 128 bytes, the 16-byte chunks of
+          // row r rotated by r.
+          uint4* part = reinterpret_cast<uint4*>(p.part_o) +
+                        (prow0 / kTrRows * (D / 4) + (col0 + c) / 4) * kTrRows + r;
+          if (whole) {
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            st_shared_u4(stage + lane * 128 + (((u + lane) & 7) << 4),
-                         make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]));
+            for (int u = 0; u < 8; ++u)
+              st_shared_u4(stage + lane * 128 + (((u + lane) & 7) << 4),
+                           make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]));
+          } else if (valid) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              part[u * kTrRows] = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+          }
           // non-finite V elements of nodes this row sees (rare)
           for (unsigned long long h = hit; h; h &= h - 1) {
             const int at = base + __ffsll(h) - 1;
@@ -844,11 +853,13 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
             for (int u = 0; u < 32; ++u) {
               const uint32_t v = row[u];
               if ((v & 0x7f80u) != 0x7f80u) continue;
-              float* y = reinterpret_cast<float*>(
-                  smem + (stage - sbase) + lane * 128 + ((((u >> 2) + lane) & 7) << 4) + (u & 3) * 4);
-              *y += __uint_as_float(v << 16);
+              float* y = whole ? reinterpret_cast<float*>(smem + (stage - sbase) + lane * 128 +
+                                                          ((((u >> 2) + lane) & 7) << 4))
+                               : reinterpret_cast<float*>(part + (u >> 2) * kTrRows);
+              y[u & 3] += __uint_as_float(v << 16);
             }
           }
+          if (!whole) continue;
           __syncwarp();
           // this lane's chunk of rows lane / 8 + 4 u
 #pragma unroll 2
@@ -856,10 +867,6 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const int row = 4 * u + (lane >> 3);
             const uint4 y = ld_shared_u4(stage + row * 128 + (((lane + row) & 7) << 4));
             if (!((rows_valid >> row) & 1u)) continue;
-            if (!whole) {
-              *reinterpret_cast<uint4*>(part + row * D + c) = y;
-              continue;
-            }
             const int tr = (warp & 3) * 32 + row;  // row of the tile
             const size_t at = size_t(tr / G) * (p.q_heads * D) + (tr % G) * D + c;
             if (p.out_bf16)
@@ -891,18 +898,22 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
 }
 
 // Joins the pieces of the items that were cut between CTAs.  Block (b, y):
-// the item in which CTA b's range starts, if the range of an earlier CTA does
-// not start inside the same item (each cut item then has one b); its pieces
-// are CTA b - 1's last one and the first ones of b, b + 1, ... while they are
-// of the item.  A warp takes a row; out = sum 2^(lse_i - lse) o_i.
-constexpr int kTrMergeWarps = 4;
+// rows 32 y .. of the item in which CTA b + 1's range starts, if the range of
+// an earlier CTA does not start inside the same item (each cut item then has
+// one b); its pieces are CTA b's last one and the first ones of b + 1, b + 2,
+// ... while they are of the item.  out = sum 2^(lse_i - lse) o_i; lane = row,
+// a warp takes an eighth of the quads of columns, as the pieces are laid out,
+// and the rows leave through shared memory.
+constexpr int kTrMergeThreads = 256;
 
 template <int D, int G, int TILES>
-__global__ void __launch_bounds__(kTrMergeWarps * 32)
+__global__ void __launch_bounds__(kTrMergeThreads)
 tree_merge_kernel(const TreeParams p, int ctas) {
-  griddep_wait();
+  constexpr int kQuads = D / 4 / 8;  // per warp
+  __shared__ __align__(16) float rows_out[32][D + 4];
   const int b = blockIdx.x + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  griddep_wait();
   // lane i: CTA b - 1 + i; the CTAs b, b + 1, ... whose ranges start in the item
   TreeStart at{-1, 0, 0, 0, 0, 0, {0, 0}};
   if (b - 1 + lane < ctas) at = p.start[b - 1 + lane];
@@ -917,9 +928,9 @@ tree_merge_kernel(const TreeParams p, int ctas) {
   const int nodes = __shfl_sync(0xffffffffu, at.n, 1);
   const int groups = __shfl_sync(0xffffffffu, at.groups, 1);
   const int kvh = item / groups, group = item - kvh * groups;
-  const int r = blockIdx.y * kTrMergeWarps + warp;  // row of the group
-  const int node = group * TILES * (kTrRows / G) + r / G;
-  if (node >= nodes) return;
+  const int node0 = group * TILES * (kTrRows / G);
+  const int rows = min((nodes - node0) * G, TILES * kTrRows) - int(blockIdx.y) * 32;
+  if (rows <= 0) return;  // uniform over the block, as all returns are
   vote |= 1u;
   int parts = vote == 0xffffffffu ? 32 : __ffs(~vote) - 1;
   while (parts % 32 == 0) {  // more than the lanes look at at a time
@@ -929,56 +940,58 @@ tree_merge_kernel(const TreeParams p, int ctas) {
     if (vote == 0) break;
     parts += vote == 0xffffffffu ? 32 : __ffs(~vote) - 1;
   }
-  auto row_of = [&](int i) {  // piece i's row in the workspace
+  // piece i's tile of 128 rows in the workspace, and this lane's row of it
+  const int tile = blockIdx.y / 4, r = (blockIdx.y % 4) * 32 + lane;
+  auto tile_of = [&](int i) {
     const size_t slot = i == 0 ? size_t(b - 1) * 2 + (same ? 0 : 1) : size_t(b + i - 1) * 2;
-    return slot * (TILES * kTrRows) + r;
+    return slot * TILES + tile;
   };
-  constexpr int V = D / 32;  // columns per lane
-  float acc[V];
+  float4 acc[kQuads];
 #pragma unroll
-  for (int u = 0; u < V; ++u) acc[u] = 0.f;
+  for (int z = 0; z < kQuads; ++z) acc[z] = make_float4(0.f, 0.f, 0.f, 0.f);
   float big = -INFINITY, tot = 0.f;
-  for (int i0 = 0; i0 < parts; i0 += 32) {  // lane i weighs piece i0 + i
-    const float lse = i0 + lane < parts ? __ldg(p.part_lse + row_of(i0 + lane)) : -INFINITY;
-    float top = lse;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float now = fmaxf(big, top);
-    const float ref = now == -INFINITY ? 0.f : now;
-    const float fade = ex2(big - ref);
-    big = now;
-    const float wgt = ex2(lse - ref);
-    tot *= fade;
-#pragma unroll
-    for (int u = 0; u < V; ++u) acc[u] *= fade;
-    const int n = min(32, parts - i0);
+  if (lane < rows) {
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float g = __shfl_sync(0xffffffffu, wgt, i);
-      const float* o = p.part_o + row_of(i0 + i) * D + lane * V;
-      float x[V];
-      if constexpr (V == 4) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(o));
-        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-      } else {
-        const float2 v = __ldg(reinterpret_cast<const float2*>(o));
-        x[0] = v.x, x[1] = v.y;
-      }
-      tot += g;
+    for (int i = 0; i < parts; ++i) {
+      const size_t t = tile_of(i);
+      const float lse = __ldg(p.part_lse + t * kTrRows + r);
+      const float4* o = reinterpret_cast<const float4*>(p.part_o) +
+                        (t * (D / 4) + warp * kQuads) * kTrRows + r;
+      float4 x[kQuads];
 #pragma unroll
-      for (int u = 0; u < V; ++u) acc[u] = fmaf(x[u], g, acc[u]);
+      for (int z = 0; z < kQuads; ++z) x[z] = __ldg(o + z * kTrRows);
+      const float now = fmaxf(big, lse);
+      const float ref = now == -INFINITY ? 0.f : now;
+      const float fade = ex2(big - ref), wgt = ex2(lse - ref);
+      big = now;
+      tot = tot * fade + wgt;  // a piece in which the row saw nothing weighs 0 (its row is zeros)
+#pragma unroll
+      for (int z = 0; z < kQuads; ++z) {
+        acc[z].x = acc[z].x * fade + x[z].x * wgt;
+        acc[z].y = acc[z].y * fade + x[z].y * wgt;
+        acc[z].z = acc[z].z * fade + x[z].z * wgt;
+        acc[z].w = acc[z].w * fade + x[z].w * wgt;
+      }
     }
   }
   const float inv = tot != 0.f ? 1.f / tot : 0.f;
-  const size_t to = ((size_t(qs) + node) * p.q_heads + size_t(kvh) * G + r % G) * D + lane * V;
 #pragma unroll
-  for (int u = 0; u < V; u += 2) {
+  for (int z = 0; z < kQuads; ++z)
+    *reinterpret_cast<float4*>(&rows_out[lane][(warp * kQuads + z) * 4]) =
+        make_float4(acc[z].x * inv, acc[z].y * inv, acc[z].z * inv, acc[z].w * inv);
+  __syncthreads();
+  for (int k = threadIdx.x; k < 32 * (D / 4); k += kTrMergeThreads) {
+    const int row = k / (D / 4), col = (k % (D / 4)) * 4;
+    if (row >= rows) break;
+    const float4 y = *reinterpret_cast<const float4*>(&rows_out[row][col]);
+    const int rr = int(blockIdx.y) * 32 + row;
+    const size_t to =
+        ((size_t(qs) + node0 + rr / G) * p.q_heads + size_t(kvh) * G + rr % G) * D + col;
     if (p.out_bf16)
-      *reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + to + u) =
-          pack_bf16x2(acc[u] * inv, acc[u + 1] * inv);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + to) =
+          make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
     else
-      *reinterpret_cast<float2*>(static_cast<float*>(p.out) + to + u) =
-          make_float2(acc[u] * inv, acc[u + 1] * inv);
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + to) = y;
   }
 }
 
@@ -1011,8 +1024,8 @@ static cudaError_t launch_tree_t(const TreeParams& p, int ctas, const CUtensorMa
   if (e != cudaSuccess || ctas < 2) return e;
   const int rows = std::min(p.max_q_len * G, TILES * kTrRows);
   return launch_after_previous(tree_merge_kernel<D, G, TILES>,
-                               dim3(ctas - 1, (rows + kTrMergeWarps - 1) / kTrMergeWarps),
-                               dim3(kTrMergeWarps * 32), 0, stream, p, ctas);
+                               dim3(ctas - 1, (rows + 31) / 32), dim3(kTrMergeThreads), 0, stream,
+                               p, ctas);
 }
 
 template <int D, int TILES>
