@@ -1,4 +1,5 @@
-"""Thin ctypes binding over ``libpagedkv.so`` (argument marshalling only).
+"""Thin binding over ``libpagedkv.so`` (argument marshalling only): ctypes, and
+for the speculative step's calls the compiled checks of ``_marshal``.
 
 Every function here checks tensor dtypes/shapes/devices, takes raw device
 pointers and the current CUDA stream from torch, and calls the C entry point
@@ -10,7 +11,6 @@ fallback path.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 from typing import Optional
 
@@ -222,6 +222,11 @@ def _load():
 
 
 lib = _load()
+try:
+    from . import _marshal
+except ImportError as e:
+    raise RuntimeError("_marshal.so is not built for this Python and PyTorch; run "
+                       "`python -m paged_kv_cache_52_gb300.build`") from e
 
 
 def status_string(status: int) -> str:
@@ -957,113 +962,17 @@ def describe_device_error(word: int) -> list[str]:
 # --------------------------------------------------------------------------
 # The speculative step with trees of drafted tokens.
 # --------------------------------------------------------------------------
-# These calls take a few microseconds on the GPU for one user's step, less than
-# a slow argument check: the checks below read each tensor's device, type and
-# layout once, and build their messages only to raise.
-_BF16, _F32, _I32, _I64, _U8 = (torch.bfloat16, torch.float32, torch.int32, torch.int64,
-                                torch.uint8)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# These calls take a few microseconds on the GPU for one user's step: the module
+# ``_marshal`` (binding/marshal.cpp) checks their tensors (ValueError) and calls
+# the C entry of the same name; it returns a status only when that refuses.
+def _done(name: str, result):
+    if type(result) is int:
+        _check(name, result)
+    return result
 
 
-@functools.lru_cache(maxsize=256)
-def _desc(num_blocks: int, block_size: int, kv_heads: int, d_head: int) -> CacheDesc:
-    return CacheDesc(num_blocks, block_size, kv_heads, d_head)
-
-
-def _refuse(name: str, what: str):
-    raise ValueError(f"{name} must be {what}")
-
-
-def _check_packed(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int, shape: tuple) -> int:
-    """The address of a contiguous tensor of this type and shape on GPU ``dev``."""
-    if t.dtype is not dtype or t.get_device() != dev or t.shape != shape or not t.is_contiguous():
-        _refuse(name, f"a contiguous {dtype} tensor {list(shape)} on one GPU with the others")
-    return t.data_ptr()
-
-
-def _pools(k_cache: torch.Tensor, v_cache: torch.Tensor, *dtypes: torch.dtype) -> int:
-    """The GPU of two pools of one of these types, alike in shape."""
-    dev = k_cache.get_device()
-    if dev < 0 or v_cache.get_device() != dev:
-        _refuse("k_cache and v_cache", "CUDA tensors on one GPU")
-    if k_cache.dtype not in dtypes or v_cache.dtype is not k_cache.dtype:
-        _refuse("k_cache and v_cache", f"of one type, {' or '.join(map(str, dtypes))}")
-    if v_cache.shape != k_cache.shape:
-        _refuse("k_cache and v_cache", "of one shape")
-    return dev
-
-
-def _launch(dev: int, fn, *args):
-    """``fn(*args, stream)`` on GPU ``dev``'s current stream; a launch goes to
-    the current device, so that is switched when it is another."""
-    if _current_device() == dev:
-        st = fn(*args, _raw_stream(dev))
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, _raw_stream(dev))
-    if st:
-        _check(fn.__name__, st)
-
-
-def _tree_batch(q_start: torch.Tensor, context_lens: torch.Tensor, dev: int,
-                max_q_len: Optional[int] = None) -> tuple[int, int]:
-    if context_lens.dim() != 1:
-        _refuse("context_lens", "[S]")
-    S = context_lens.shape[0]
-    _check_packed(context_lens, "context_lens", _I32, dev, (S,))
-    _check_packed(q_start, "q_start", _I32, dev, (S + 1,))
-    if max_q_len is None:
-        max_q_len = int((q_start[1:] - q_start[:-1]).max()) if S else 0
-    return S, int(max_q_len)
-
-
-def _tables(block_tables: torch.Tensor, dev: int, S: int) -> int:
-    if block_tables.dim() != 2:
-        _refuse("block_tables", "[S, max_blocks]")
-    width = block_tables.shape[1]
-    _check_packed(block_tables, "block_tables", _I32, dev, (S, width))
-    return width
-
-
-def _token_rows(x: torch.Tensor, name: str, dev: int, T: int, heads: int, d: int) -> int:
-    """The token stride of ``x [T, heads, d]`` bf16 with contiguous rows."""
-    if x.dtype is not _BF16 or x.get_device() != dev or x.shape != (T, heads, d):
-        _refuse(name, f"a bfloat16 tensor [{T}, {heads}, {d}] on one GPU with the pools")
-    st, sh, sd = x.stride()
-    if T and (sd != 1 or (heads > 1 and sh != d)):
-        _refuse(name, "contiguous within each token's row")
-    return st if T > 1 else heads * d  # the stride of a single token is not used
-
-
-def _rope_append(fn, pool_dtype, q, k, v, positions, rope_table, slot_mapping, k_cache, v_cache,
-                 scales, q_weight, k_weight, eps, interleaved, out):
-    dev = _pools(k_cache, v_cache, pool_dtype)
-    if k_cache.dim() != 4 or q.dim() != 3 or rope_table.dim() != 2:
-        _refuse("pools, q and rope_table",
-                "[NB, 16, Hkv, d], [T, Hq, d] and [positions, rot]")
-    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
-        _refuse("pools", "contiguous")
-    nb, bs, hkv, d = k_cache.shape
-    T, hq = q.shape[0], q.shape[1]
-    sq = _token_rows(q, "q", dev, T, hq, d)
-    sk = _token_rows(k, "k", dev, T, hkv, d)
-    sv = _token_rows(v, "v", dev, T, hkv, d)
-    _check_packed(positions, "positions", _I64, dev, (T,))
-    _check_packed(slot_mapping, "slot_mapping", _I64, dev, (T,))
-    rows, rot = rope_table.shape
-    _check_packed(rope_table, "rope_table", _F32, dev, (rows, rot))
-    qw = None if q_weight is None else _check_packed(q_weight, "q_weight", _BF16, dev, (d,))
-    kw = None if k_weight is None else _check_packed(k_weight, "k_weight", _BF16, dev, (d,))
-    if out is None:
-        out = torch.empty((T, hq, d), dtype=_BF16, device=q.device)
-    else:
-        _check_packed(out, "out", _BF16, dev, (T, hq, d))
-    _launch(dev, fn, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, T, hq,
-            positions.data_ptr(), rope_table.data_ptr(), rows, rot, 1 if interleaved else 0, qw,
-            kw, eps, slot_mapping.data_ptr(), out.data_ptr(), k_cache.data_ptr(),
-            v_cache.data_ptr(), _desc(nb, bs, hkv, d), *scales)
-    return out
+def _longest(q_start: torch.Tensor) -> int:
+    return int((q_start[1:] - q_start[:-1]).max()) if q_start.numel() > 1 else 0
 
 
 def qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -1080,9 +989,9 @@ def qk_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     rot/2)``, or ``(2i, 2i+1)`` when ``interleaved``.  Token rows may be
     strided (views of a fused projection).  Returns the rotated queries, bf16
     ``[T, Hq, d]``."""
-    return _rope_append(lib.pkv_qk_norm_rope_append, _BF16, q, k, v, positions, rope_table,
-                        slot_mapping, k_cache, v_cache, (), q_weight, k_weight, eps, interleaved,
-                        out)
+    return _done("pkv_qk_norm_rope_append", _marshal.rope_append(
+        q, k, v, positions, rope_table, slot_mapping, k_cache, v_cache, None, q_weight, k_weight,
+        eps, interleaved, out))
 
 
 def qk_norm_rope_append_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -1095,9 +1004,9 @@ def qk_norm_rope_append_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
                             out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """``qk_norm_rope_append`` into FP8 (e4m3) pools with per-pool scales: the
     float32 keys and values are rounded once, to their codes."""
-    return _rope_append(lib.pkv_qk_norm_rope_append_fp8, _U8, q, k, v, positions, rope_table,
-                        slot_mapping, k_cache, v_cache, (k_scale, v_scale), q_weight, k_weight,
-                        eps, interleaved, out)
+    return _done("pkv_qk_norm_rope_append_fp8", _marshal.rope_append(
+        q, k, v, positions, rope_table, slot_mapping, k_cache, v_cache, (k_scale, v_scale),
+        q_weight, k_weight, eps, interleaved, out))
 
 
 def draft_tree_layout(parents: torch.Tensor, q_start: torch.Tensor, context_lens: torch.Tensor,
@@ -1110,23 +1019,10 @@ def draft_tree_layout(parents: torch.Tensor, q_start: torch.Tensor, context_lens
     node u as itself or an ancestor; its position is the committed length plus
     its depth.  ``max_q_len`` (host int) bounds a tree's nodes; when omitted it
     is read from ``q_start`` (a device sync)."""
-    dev = parents.get_device()
-    if dev < 0 or parents.dim() != 1:
-        _refuse("parents", "a CUDA tensor [total]")
-    total = parents.shape[0]
-    _check_packed(parents, "parents", _I32, dev, (total,))
-    S, max_q_len = _tree_batch(q_start, context_lens, dev, max_q_len)
-    if tree_mask is None:
-        tree_mask = torch.empty(total, dtype=_I64, device=parents.device)
-    else:
-        _check_packed(tree_mask, "tree_mask", _I64, dev, (total,))
-    if positions is None:
-        positions = torch.empty(total, dtype=_I64, device=parents.device)
-    else:
-        _check_packed(positions, "positions", _I64, dev, (total,))
-    _launch(dev, lib.pkv_draft_tree_layout, parents.data_ptr(), q_start.data_ptr(), S, total,
-            max_q_len, context_lens.data_ptr(), tree_mask.data_ptr(), positions.data_ptr())
-    return tree_mask, positions
+    if max_q_len is None:
+        max_q_len = _longest(q_start)
+    return _done("pkv_draft_tree_layout", _marshal.tree_layout(
+        parents, q_start, context_lens, max_q_len, tree_mask, positions))
 
 
 def tree_attention_workspace(num_seqs: int, max_q_len: int, q_heads: int, kv_heads: int,
@@ -1154,32 +1050,17 @@ def paged_tree_attention(q: torch.Tensor, q_start: torch.Tensor, tree_mask: torc
     float32 unless ``out_dtype`` (or a given ``out``) is bfloat16.
     ``max_q_len`` (host int) bounds a tree's nodes; when omitted it is read
     from ``q_start`` (a device sync)."""
-    dev = _pools(k_cache, v_cache, _BF16)
-    if k_cache.dim() != 4 or q.dim() != 3:
-        _refuse("pools and q", "[NB, 16, Hkv, d] and [total, Hq, d]")
-    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
-        _refuse("pools", "contiguous")
-    nb, bs, hkv, d = k_cache.shape
-    total, hq = q.shape[0], q.shape[1]
-    _check_packed(q, "q", _BF16, dev, (total, hq, d))
-    S, max_q_len = _tree_batch(q_start, context_lens, dev, max_q_len)
-    _check_packed(tree_mask, "tree_mask", _I64, dev, (total,))
-    width = _tables(block_tables, dev, S)
     odt = _out_dtype(out, out_dtype)
-    if out is None:
-        out = torch.empty((total, hq, d), dtype=odt, device=q.device)
-    else:
-        _check_packed(out, "out", odt, dev, (total, hq, d))
+    if max_q_len is None:
+        max_q_len = _longest(q_start)
     if workspace is None:
-        workspace = tree_attention_workspace(S, max_q_len, hq, hkv, d, q.device)
-    else:
-        _check_packed(workspace, "workspace", _U8, dev, (workspace.numel(),))
-    _launch(dev, lib.pkv_paged_tree_attention_bf16out if odt is _BF16
-            else lib.pkv_paged_tree_attention, q.data_ptr(), q_start.data_ptr(), S, total,
-            max_q_len, hq, tree_mask.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-            _desc(nb, bs, hkv, d), block_tables.data_ptr(), width, context_lens.data_ptr(), scale,
-            out.data_ptr(), workspace.data_ptr(), workspace.numel())
-    return out
+        _need(q.dim() == 3 and k_cache.dim() == 4, "q must be [total, Hq, d], pools [NB, 16, Hkv, d]")
+        workspace = tree_attention_workspace(context_lens.shape[0], max_q_len, q.shape[1],
+                                             k_cache.shape[2], q.shape[2], q.device)
+    bf16 = odt is torch.bfloat16
+    return _done("pkv_paged_tree_attention_bf16out" if bf16 else "pkv_paged_tree_attention",
+                 _marshal.tree_attention(q, q_start, tree_mask, k_cache, v_cache, block_tables,
+                                         context_lens, scale, out, max_q_len, workspace, bf16))
 
 
 def kv_accept_rows(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: torch.Tensor,
@@ -1192,32 +1073,9 @@ def kv_accept_rows(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: t
     nodes.  The pools are one layer's ``[NB, 16, Hkv, d]`` or all layers'
     ``[layers, NB, 16, Hkv, d]`` (bf16, or uint8 FP8 codes; each layer
     contiguous).  Returns the new context lengths, int32 ``[S]``."""
-    dev = _pools(k_cache, v_cache, _BF16, _U8)
-    dims = k_cache.dim()
-    if dims not in (4, 5):
-        _refuse("pools", "[NB, 16, Hkv, d] or [layers, NB, 16, Hkv, d]")
-    nb, bs, hkv, d = k_cache.shape[-4:]
-    row = (bs * hkv * d, hkv * d, d, 1)
-    sk, sv = k_cache.stride(), v_cache.stride()
-    if sk[-4:] != row or sv[-4:] != row:
-        _refuse("each layer's pool", "contiguous")
-    layers, lk, lv = (k_cache.shape[0], sk[0], sv[0]) if dims == 5 else (1, 0, 0)
-    S, _ = _tree_batch(q_start, context_lens, dev, 0)
-    width = _tables(block_tables, dev, S)
-    if accepted.dim() != 2:
-        _refuse("accepted", "[S, max_accepted]")
-    most = accepted.shape[1]
-    _check_packed(accepted, "accepted", _I32, dev, (S, most))
-    _check_packed(num_accepted, "num_accepted", _I32, dev, (S,))
-    if new_context_lens is None:
-        new_context_lens = torch.empty(S, dtype=_I32, device=context_lens.device)
-    else:
-        _check_packed(new_context_lens, "new_context_lens", _I32, dev, (S,))
-    _launch(dev, lib.pkv_kv_accept_rows, k_cache.data_ptr(), lk, v_cache.data_ptr(), lv, layers,
-            _desc(nb, bs, hkv, d), k_cache.element_size(), block_tables.data_ptr(), width,
-            context_lens.data_ptr(), q_start.data_ptr(), S, accepted.data_ptr(), most,
-            num_accepted.data_ptr(), new_context_lens.data_ptr())
-    return new_context_lens
+    return _done("pkv_kv_accept_rows", _marshal.accept_rows(
+        k_cache, v_cache, block_tables, context_lens, q_start, accepted, num_accepted,
+        new_context_lens))
 
 
 # --------------------------------------------------------------------------
