@@ -55,10 +55,13 @@ static __device__ unsigned g_tree_error = 0;
 constexpr int kTrRows = 128;     // rows (node x head) per tile
 constexpr int kTrKeys = 128;     // keys per K/V tile (8 pages)
 constexpr int kTrThreads = 384;
+constexpr int kTrRegsSoftmax = 192, kTrRegsIssue = 120;
 constexpr int kTrKWarp = 8, kTrSWarp = 9, kTrVWarp = 10;  // 11 issues P V
 constexpr uint32_t kTrTmemCols = 512;  // warpgroup w: S/P at 256 w, O at 256 w + 128
 constexpr float kTrRescale = 8.0f;     // log2 units: move the running max when it grows by > x256
 constexpr int kTrMaxStages = 5;
+constexpr int kTrMinTiles = 2;  // one for each softmax warpgroup
+constexpr int kTrSlack = 2;     // key tiles that a second piece costs a CTA
 constexpr int kTrPieces = 4;  // piece descriptions in shared memory
 
 template <int D, int TILES>
@@ -82,7 +85,7 @@ struct TreeSmem {
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   // tensor-memory base, abort flag; non-finite nodes [2] (64 bit); scan [12];
   // the start of the range; the pieces
-  static constexpr int kPieceOff = kMiscOff + 16 + 16 + 48 + 32;
+  static constexpr int kPieceOff = kMiscOff + 16 + 16 + 48 + 48;
   static constexpr int kSmemBytes = kPieceOff + kTrPieces * 32;
   static_assert(kSmemBytes <= 232448, "tree tile does not fit in shared memory");
   static_assert(kKStages <= kTrMaxStages && kVStages <= kTrMaxStages, "ring stages");
@@ -277,7 +280,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     TreeSeq seq;
     int s, off;
   };
-  static_assert(sizeof(Begin) <= 32, "start of the range");
+  static_assert(sizeof(Begin) <= 48, "start of the range");
   volatile TreePiece* pieces = reinterpret_cast<volatile TreePiece*>(smem + T::kPieceOff);
   Begin* begin = reinterpret_cast<Begin*>(smem + T::kMiscOff + 80);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -316,64 +319,122 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     tma_prefetch_desc(&tmap_k);
     tma_prefetch_desc(&tmap_q);
   }
-  griddep_wait();  // inputs may have been written by the previous kernel in the stream
-
-  // ---- this CTA's range of the key tiles of all items
-  const int per_thread = (p.num_seqs + kTrThreads - 1) / kTrThreads;
-  const int s_lo = min(int(threadIdx.x) * per_thread, p.num_seqs);
-  const int s_hi = min(s_lo + per_thread, p.num_seqs);
-  int mine = 0;
-  TreeSeq q{};
-  for (int s = s_lo; s < s_hi; ++s) {
-    q = tree_seq<G, TILES>(p, s);
-    if (q.bad && blockIdx.x == 0) atomicOr(&g_tree_error, kErrBadQueryRange);
-    mine += q.total(p.kv_heads);
-  }
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += up;
-  }
-  if (lane == 31) scan[warp] = incl;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  int all = 0;
-#pragma unroll
-  for (int w = 0; w < kTrThreads / 32; ++w) {
-    if (w == warp) incl += all;
-    all += scan[w];
-  }
-  // with fewer tiles than CTAs the last CTAs have none, so that a cut item's
-  // pieces lie in consecutive CTAs; CTA c starts at floor(c all / active)
-  const int active = min(int(gridDim.x), all), c = blockIdx.x;
-  const int each = active > 0 ? all / active : 0, rest = all - each * active;
-  const int lo = c < active ? c * each + c * rest / active : all;
-  const int count = c < active ? (c + 1) * each + (c + 1) * rest / active - lo : 0;
-  if (lo >= incl - mine && lo < incl) {  // the range starts in this thread's sequences
-    int at = lo - (incl - mine);
-    int s = s_lo;
-    if (per_thread > 1)
-      for (;; ++s) {
-        q = tree_seq<G, TILES>(p, s);
-        const int w = q.total(p.kv_heads);
-        if (at < w) break;
-        at -= w;
-      }
-    *begin = Begin{q, s, at};
-    const int item = at / q.tiles;
-    p.start[c] = TreeStart{count > 0 ? s : -1, item, at - item * q.tiles, q.qs, q.n, q.groups,
-                           {0, 0}};
-  } else if (lo >= all && threadIdx.x == 0) {
-    p.start[c].seq = -1;
-  }
-  __syncthreads();
-  if (count > 0) {
-  TreeWalk<G, TILES> walk(p, begin->seq, begin->s, begin->off, count);
+  griddep_wait();  // inputs may have been written by the previous kernel in the stream
 
+  // ---- this CTA's range of the key tiles of all items
+  const int ctas = gridDim.x, c = blockIdx.x;
+  TreeSeq q{};               // the sequence it starts in,
+  int s0 = -1, off0 = 0;     // its number, and the tiles of it before the range
+  int count = 0;
+  auto warp_scan = [&](int x) {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += up;
+    }
+    return x;
+  };
+  // Else the tiles are laid end to end, CTA c starting at floor(c all / active).  With few
+  // tiles the last CTAs have none, so that a cut item's pieces lie in
+  // consecutive CTAs.
+  auto even_share = [&](int all, int& lo, int& n) {
+    const int active = min(ctas, (all + kTrMinTiles - 1) / kTrMinTiles);
+    const int each = active > 0 ? all / active : 0, rest = all - each * active;
+    lo = c < active ? c * each + c * rest / active : all;
+    n = c < active ? (c + 1) * each + (c + 1) * rest / active - lo : 0;
+  };
+  if (p.num_seqs <= 32) {
+    // every warp for itself, lane = sequence: no barrier before the first load
+    if (lane < p.num_seqs) q = tree_seq<G, TILES>(p, lane);
+    if (q.bad && c == 0 && warp == 0) atomicOr(&g_tree_error, kErrBadQueryRange);
+    const int items = q.groups * p.kv_heads, mine = q.total(p.kv_heads);
+    const int all = __reduce_add_sync(0xffffffffu, mine);
+    // A CTA with parts of two items spends about kTrSlack tiles' time between
+    // them.  So with no more items than CTAs each item is cut into equal pieces
+    // of at most kTrSlack tiles above the even share, one piece a CTA, if there
+    // are CTAs enough.
+    const int longest = max(kTrMinTiles, all / ctas + kTrSlack);
+    const int cuts = items ? (q.tiles + longest - 1) / longest : 0;
+    const bool alone = __reduce_add_sync(0xffffffffu, items * cuts) <= ctas;
+    int lo = c;
+    if (!alone) even_share(all, lo, count);
+    const int width = alone ? items * cuts : mine;
+    const int end = warp_scan(width), at = lo - (end - width);
+    const unsigned here = __ballot_sync(0xffffffffu, at >= 0 && at < width);
+    if (here) {
+      const int src = __ffs(here) - 1;
+      if (alone && lane == src) {
+        const int item = at / cuts, j = at - item * cuts, first = j * q.tiles / cuts;
+        off0 = item * q.tiles + first;
+        count = (j + 1) * q.tiles / cuts - first;
+      } else {
+        off0 = at;
+      }
+      s0 = src;
+      off0 = __shfl_sync(0xffffffffu, off0, src);
+      count = __shfl_sync(0xffffffffu, count, src);
+      q.qs = __shfl_sync(0xffffffffu, q.qs, src);
+      q.n = __shfl_sync(0xffffffffu, q.n, src);
+      q.ctx = __shfl_sync(0xffffffffu, q.ctx, src);
+      q.groups = __shfl_sync(0xffffffffu, q.groups, src);
+      q.tiles = __shfl_sync(0xffffffffu, q.tiles, src);
+    } else {
+      count = 0;
+    }
+  } else {
+    const int per_thread = (p.num_seqs + kTrThreads - 1) / kTrThreads;
+    const int s_lo = min(int(threadIdx.x) * per_thread, p.num_seqs);
+    const int s_hi = min(s_lo + per_thread, p.num_seqs);
+    int mine = 0;
+    for (int s = s_lo; s < s_hi; ++s) {
+      q = tree_seq<G, TILES>(p, s);
+      if (q.bad && c == 0) atomicOr(&g_tree_error, kErrBadQueryRange);
+      mine += q.total(p.kv_heads);
+    }
+    int incl = warp_scan(mine), all = 0, lo;
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kTrThreads / 32; ++w) {
+      if (w == warp) incl += all;
+      all += scan[w];
+    }
+    even_share(all, lo, count);
+    if (lo >= incl - mine && lo < incl) {  // the range starts in this thread's sequences
+      int at = lo - (incl - mine), s = s_lo;
+      if (per_thread > 1)
+        for (;; ++s) {
+          q = tree_seq<G, TILES>(p, s);
+          const int w = q.total(p.kv_heads);
+          if (at < w) break;
+          at -= w;
+        }
+      *begin = Begin{q, s, at};
+    }
+    __syncthreads();
+    if (count > 0) {
+      q = begin->seq;
+      s0 = begin->s;
+      off0 = begin->off;
+    }
+  }
+  if (threadIdx.x == 0) {
+    const int item = count > 0 ? off0 / q.tiles : 0;
+    p.start[c] = TreeStart{count > 0 ? s0 : -1, item, off0 - item * q.tiles, q.qs, q.n, q.groups,
+                           {0, 0}};
+  }
+  if (count > 0) {
+  TreeWalk<G, TILES> walk(p, q, s0, off0, count);
+
+  // The launch gives every warp 168 registers; the four loading and issuing
+  // warps hand some of theirs to the softmax warps.  8 x 192 + 4 x 120 <= 12 x 168
+  // (checked at the launch).
   if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTrRegsIssue));
   if (warp == kTrKWarp || warp == kTrVWarp) {
     // ================= K and V rings =================
     const bool is_v = warp == kTrVWarp;
@@ -557,6 +618,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     __syncwarp();
   }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTrRegsSoftmax));
     // ================= softmax, correction, epilogue =================
     const int w = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // row of the tile = tensor-memory lane
@@ -1017,8 +1079,20 @@ static cudaError_t launch_tree_t(const TreeParams& p, int ctas, const CUtensorMa
                                  cudaStream_t stream) {
   using T = TreeSmem<D, TILES>;
   static std::atomic<int> attr_done[kAttrMaxDevices];
-  cudaError_t e = set_smem_limit_once(paged_tree_kernel<D, G, TILES>, T::kSmemBytes, attr_done);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= kAttrMaxDevices || !attr_done[dev].load(std::memory_order_acquire)) {
+    // the split of the registers draws on what the launch allots: an increase
+    // beyond it would wait forever
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, paged_tree_kernel<D, G, TILES>);
+    if (e != cudaSuccess) return e;
+    if (fa.numRegs * kTrThreads < 256 * kTrRegsSoftmax + (kTrThreads - 256) * kTrRegsIssue)
+      return cudaErrorInvalidConfiguration;
+    e = set_smem_limit_once(paged_tree_kernel<D, G, TILES>, T::kSmemBytes, attr_done);
+    if (e != cudaSuccess) return e;
+  }
   e = launch_after_previous(paged_tree_kernel<D, G, TILES>, dim3(ctas), dim3(kTrThreads),
                             T::kSmemBytes, stream, *tq, *tk, *tv, p);
   if (e != cudaSuccess || ctas < 2) return e;
