@@ -66,6 +66,14 @@ constexpr int kTrPieces = 4;  // piece descriptions in shared memory
 
 template <int D, int TILES>
 struct TreeSmem {
+  // Whether S, P and P V of a tile go in halves of 64 keys, so that a warpgroup
+  // weighs one half while the other's products and next scores run.  Pays
+  // where the tensor core waits for the softmax (one row tile, heads of 128),
+  // and costs where it does not: 64-key MMAs take more than half the time.
+  // Measured in halves / whole, us: 16 x 4096, 16 nodes 52.4 / 53.5, 64 x 700, 4
+  // nodes 56.3 / 61.6; 64 x 8192, 64 nodes (two row tiles) 926 / 865; 2 x 131072,
+  // 27 nodes, heads of 64 145 / 138.
+  static constexpr bool kHalves = D == 128 && TILES == 1;
   static constexpr int kHalf = 128 * 128;  // 128 rows x 64 bf16
   static constexpr int kTileBytes = (D / 64) * kHalf;
   static constexpr int kQBytes = TILES * kTileBytes;
@@ -81,7 +89,7 @@ struct TreeSmem {
   static constexpr int kStageOff = kVOff + kVStages * kTileBytes;
   static constexpr int kXchOff = kStageOff + (D == 64 ? 8 * 4096 : 0);  // [2][128] (max, sum)
   static constexpr int kBarOff = kXchOff + 2 * kTrRows * 8;
-  static constexpr int kNumBars = 2 + 4 * kTrMaxStages + 6 + 3 + 4;
+  static constexpr int kNumBars = 2 + 4 * kTrMaxStages + 12 + 3 + kTrPieces;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   // tensor-memory base, abort flag; non-finite nodes [2] (64 bit); scan [12];
   // the start of the range; the pieces
@@ -95,8 +103,9 @@ enum TrBar {
   kTrQFull = 0, kTrQEmpty = 1,
   kTrKFull = 2, kTrKEmpty = kTrKFull + kTrMaxStages,
   kTrVFull = kTrKEmpty + kTrMaxStages, kTrVEmpty = kTrVFull + kTrMaxStages,
-  kTrSFull = kTrVEmpty + kTrMaxStages, kTrPFull = kTrSFull + 2, kTrODone = kTrPFull + 2,
-  kTrXch = kTrODone + 2, kTrEpi = kTrXch + 1, kTrDrain = kTrEpi + 1, kTrPiece0 = kTrDrain + 1
+  // by half 2 h + w: first and second 64 keys of warpgroup w's tile
+  kTrSFull = kTrVEmpty + kTrMaxStages, kTrPFull = kTrSFull + 4, kTrDone = kTrPFull + 4,
+  kTrXch = kTrDone + 4, kTrEpi = kTrXch + 1, kTrDrain = kTrEpi + 1, kTrPiece0 = kTrDrain + 1
 };
 
 // Where a CTA's range starts, for the merge: sequence (-1: no work), item of
@@ -269,6 +278,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
                   const __grid_constant__ CUtensorMap tmap_v, const TreeParams p) {
   using T = TreeSmem<D, TILES>;
   constexpr int TPT = kTrRows / G;  // tree nodes per row tile
+  constexpr int kParts = T::kHalves ? 2 : 1;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + T::kBarOff;
@@ -301,10 +311,10 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       mbar_init(bars + 8 * (kTrVFull + s), 1);
       mbar_init(bars + 8 * (kTrVEmpty + s), 1);
     }
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(bars + 8 * (kTrSFull + w), 1);
-      mbar_init(bars + 8 * (kTrPFull + w), 4);
-      mbar_init(bars + 8 * (kTrODone + w), 1);
+    for (int h = 0; h < 4; ++h) {
+      mbar_init(bars + 8 * (kTrSFull + h), 1);
+      mbar_init(bars + 8 * (kTrPFull + h), 4);
+      mbar_init(bars + 8 * (kTrDone + h), 1);
     }
     mbar_init(bars + 8 * kTrXch, 8);
     mbar_init(bars + 8 * kTrEpi, 8);
@@ -495,7 +505,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     // S and P V are issued by two threads, so that one's waits and the other's
     // MMAs overlap: a thread's MMAs are taken at the tensor core's pace.
     if (lane == 0) {
-      constexpr uint32_t kIdesc = idesc_bf16_f32(128, kTrKeys, 0, 0);
+      constexpr uint32_t kIdesc = idesc_bf16_f32(128, kTrKeys / kParts, 0, 0);
       auto wait = [&](int bar, uint32_t parity) {
         return tr_wait(bars + 8 * bar, parity, abort_flag);
       };
@@ -536,23 +546,24 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll 1
         for (int j = 0; ok && j < walk.tiles; ++j, ++i) {
           ok = wait(kTrKFull + i % T::kKStages, (i / T::kKStages) & 1);
+          // a part's columns are free once the products that read its P are done
 #pragma unroll 1
-          for (int t = 0; ok && t < TILES; ++t) {
-            const int w = TILES == 1 ? i & 1 : t;
-            // the scores' columns are free once the products that read P there are done
+          for (int th = 0; ok && th < kParts * TILES; ++th) {
+            const int t = th / kParts, h = th % kParts, w = TILES == 1 ? i & 1 : t;
             const int before = TILES == 1 ? (i >> 1) - 1 : i - 1;
-            ok = before < 0 || wait(kTrODone + w, before & 1);
+            ok = before < 0 || wait(kTrDone + 2 * h + w, before & 1);
             if (!ok) break;
             tc_fence_after();
             const uint32_t q_smem = sbase + t * T::kTileBytes;
-            const uint32_t k_smem = sbase + T::kKOff + (i % T::kKStages) * T::kTileBytes;
+            const uint32_t k_smem =
+                sbase + T::kKOff + (i % T::kKStages) * T::kTileBytes + h * 64 * 128;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               const uint32_t off = (c >> 2) * T::kHalf + (c & 3) * 32;
-              umma_bf16(tmem + w * 256, smem_desc_sw128(q_smem + off, 16, 1024),
+              umma_bf16(tmem + w * 256 + h * 64, smem_desc_sw128(q_smem + off, 16, 1024),
                         smem_desc_sw128(k_smem + off, 16, 1024), kIdesc, c > 0);
             }
-            umma_commit(bars + 8 * (kTrSFull + w));
+            umma_commit(bars + 8 * (kTrSFull + 2 * h + w));
           }
           umma_commit(bars + 8 * (kTrKEmpty + i % T::kKStages));
           if (j + 1 == walk.tiles) umma_commit(bars + 8 * kTrQEmpty);
@@ -593,20 +604,22 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
           ok = wait(kTrVFull + i % T::kVStages, (i / T::kVStages) & 1);
           const uint32_t v_smem = sbase + T::kVOff + (i % T::kVStages) * T::kTileBytes;
 #pragma unroll 1
-          for (int t = 0; ok && t < TILES; ++t) {
-            const int w = TILES == 1 ? i & 1 : t;
-            ok = wait(kTrPFull + w, (TILES == 1 ? i >> 1 : i) & 1);
+          for (int th = 0; ok && th < kParts * TILES; ++th) {
+            const int t = th / kParts, h = th % kParts, w = TILES == 1 ? i & 1 : t;
+            ok = wait(kTrPFull + 2 * h + w, (TILES == 1 ? i >> 1 : i) & 1);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < kTrKeys / 16; ++c) {
-              const uint64_t vdesc = smem_desc_sw128(v_smem + c * 2048, T::kHalf, 1024);
-              const uint32_t a_hi = tmem + w * 256 + 16 * c;  // hi, and lo 8 columns on
-              umma_bf16_ts(tmem + w * 256 + 128, a_hi, vdesc, kIdesc, (!fresh || c > 0) ? 1u : 0u);
+            for (int c = 0; c < kTrKeys / 16 / kParts; ++c) {
+              const uint64_t vdesc = smem_desc_sw128(v_smem + (4 * h + c) * 2048, T::kHalf, 1024);
+              const uint32_t a_hi = tmem + w * 256 + 64 * h + 16 * c;  // hi, and lo 8 columns on
+              umma_bf16_ts(tmem + w * 256 + 128, a_hi, vdesc, kIdesc,
+                           (!fresh || h > 0 || c > 0) ? 1u : 0u);
               umma_bf16_ts(tmem + w * 256 + 128, a_hi + 8, vdesc, kIdesc, 1u);
             }
-            umma_commit(bars + 8 * (kTrODone + w));
+            umma_commit(bars + 8 * (kTrDone + 2 * h + w));
           }
+          if (!ok) break;
           if (j + 1 < tiles) umma_commit(bars + 8 * (kTrVEmpty + i % T::kVStages));
         }
       }
@@ -654,126 +667,6 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const int ph = TILES == 1 ? it >> 1 : it;
         const int key0 = (first + j) * kTrKeys;
         const bool masked = key0 + kTrKeys > base;
-        ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * (kTrSFull + w), ph & 1, abort_flag));
-        if (!ok) break;
-        tc_fence_after();
-        if (warp_valid) {
-          if (masked) {
-            // hidden keys' scores become what weighs nothing: -inf after scaling
-            const float hide = neg ? INFINITY : -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < kTrKeys; c += 32) {
-              const uint32_t bits = key_bits(mask, key0 + c - base);
-              uint32_t x[32];
-              tmem_ld32u(lane_base + s_col + c, x);
-              tmem_wait_ld();
-#pragma unroll
-              for (int u = 0; u < 32; ++u) x[u] = (bits >> u) & 1u ? x[u] : __float_as_uint(hide);
-              tmem_st32u(lane_base + s_col + c, x);
-            }
-            tmem_wait_st();
-          }
-          // The running max m is a reference only: any value near the scores'
-          // serves.  So the tile is weighed against the m it has, 64 keys at a
-          // time and without looking for their max, and that stands while
-          // each row's sum over the 64 is at most 2^64 (bf16 hi + lo has
-          // float32's range).  Where no key has been seen yet, or a sum is
-          // larger, the max of what is left of the tile is taken first, and m
-          // moves when it is more than 8 behind (a factor 256).
-          const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
-          bool raise = !__all_sync(0xffffffffu, m != -INFINITY), settled = false;
-#pragma unroll 1
-          for (int c = 0; c < kTrKeys;) {
-            uint32_t va[32], vb[32];
-            if (raise) {
-              float ex[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-              const uint32_t flip = neg ? 0x80000000u : 0u;
-#pragma unroll 1
-              for (int cc = c; cc < kTrKeys; cc += 64) {
-                tmem_ld32u(lane_base + s_col + cc, va);
-                tmem_ld32u(lane_base + s_col + cc + 32, vb);
-                tmem_wait_ld();
-#pragma unroll
-                for (int u = 0; u < 32; ++u)
-                  ex[u & 3] = max3f(ex[u & 3], __uint_as_float(va[u] ^ flip),
-                                    __uint_as_float(vb[u] ^ flip));
-              }
-              const float top = fmaxf(fmaxf(ex[0], ex[1]), fmaxf(ex[2], ex[3]));
-              const float mx = top == -INFINITY ? -INFINITY : top * mag;
-              const bool move = mx > m + kTrRescale || (m == -INFINITY && mx > m);
-              if (__any_sync(0xffffffffu, move)) {
-                const float alpha = move ? ex2(m - mx) : 1.f;  // 0 when m is -inf
-                if (seen > 0) {
-                  // the accumulator's last product must be done before it is scaled
-                  ok = __all_sync(0xffffffffu,
-                                  tr_wait(bars + 8 * (kTrODone + w), (ph - 1) & 1, abort_flag));
-                  if (!ok) break;
-                  tc_fence_after();
-                  const uint64_t a2 = f2_pack(alpha, alpha);
-#pragma unroll 1
-                  for (int cc = 0; cc < D; cc += 32) {
-                    tmem_ld32u(lane_base + o_col + cc, va);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int u = 0; u < 32; u += 2) {
-                      float y0, y1;
-                      f2_unpack(f2_mul(f2_pack(__uint_as_float(va[u]), __uint_as_float(va[u + 1])),
-                                       a2), y0, y1);
-                      va[u] = __float_as_uint(y0), va[u + 1] = __float_as_uint(y1);
-                    }
-                    tmem_st32u(lane_base + o_col + cc, va);
-                  }
-                }
-                if (c > 0) {
-                  // so is the P of the tile's first keys, already stored
-                  tmem_wait_st();
-#pragma unroll 1
-                  for (int cc = 0; cc < c; cc += 32) {
-                    tmem_ld32u(lane_base + s_col + cc, va);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int u = 0; u < 32; u += u % 8 == 7 ? 9 : 1) {
-                      const uint32_t h = va[u], lw = va[u + 8];
-                      const float e0 = (bf16_lo_to_f32(h) + bf16_lo_to_f32(lw)) * alpha;
-                      const float e1 = (bf16_hi_to_f32(h) + bf16_hi_to_f32(lw)) * alpha;
-                      va[u] = pack_bf16x2(e0, e1);
-                      va[u + 8] =
-                          pack_bf16x2(e0 - bf16_lo_to_f32(va[u]), e1 - bf16_hi_to_f32(va[u]));
-                    }
-                    tmem_st32u(lane_base + s_col + cc, va);
-                  }
-                }
-                l *= alpha;
-                if (move) m = mx;
-              }
-              raise = false;
-              settled = true;
-            }
-            // P = 2^(x - m) as bf16 hi + lo in the scores' place: of each 16 keys
-            // hi in the first 8 columns, lo in the others, two keys a column
-            tmem_ld32u(lane_base + s_col + c, va);
-            tmem_ld32u(lane_base + s_col + c + 32, vb);
-            const float mref = m == -INFINITY ? 0.f : m;  // nothing seen yet: all P are 0
-            const uint64_t nm2 = f2_pack(-mref, -mref);
-            uint64_t ls[2] = {0ull, 0ull};
-            tmem_wait_ld();
-            tree_weigh(va, sc2, nm2, ls);
-            tree_weigh(vb, sc2, nm2, ls);
-            float a0, a1, b0, b1;
-            f2_unpack(ls[0], a0, a1);
-            f2_unpack(ls[1], b0, b1);
-            const float sum = (a0 + a1) + (b0 + b1);
-            if (!settled && !__all_sync(0xffffffffu, sum <= 18446744073709551616.f)) {
-              raise = true;  // NaN, too; the scores from c on are still there
-              continue;
-            }
-            l += sum;
-            tmem_st32u(lane_base + s_col + c, va);
-            tmem_st32u(lane_base + s_col + c + 32, vb);
-            c += 64;
-          }
-          if (!ok) break;
-        }
         if (masked && (TILES == 1 || w == 0)) {
           // thread r looks at key row r of V; the chunk order differs from
           // row to row, so that a warp's reads spread over the banks
@@ -804,10 +697,133 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
             }
           }
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars + 8 * (kTrPFull + w));
+#pragma unroll 1
+        for (int c = 0; c < kTrKeys; c += 64) {  // the halves of the tile
+          const int part = T::kHalves ? (c >> 5) + w : w;
+          if (T::kHalves || c == 0) {
+            ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * (kTrSFull + part), ph & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+          }
+          if (warp_valid) {
+            uint32_t va[32], vb[32];
+            if (masked) {
+              // hidden keys' scores become what weighs nothing: -inf after scaling
+              const uint32_t hide = __float_as_uint(neg ? INFINITY : -INFINITY);
+#pragma unroll 1
+              for (int cc = c; cc < c + 64; cc += 32) {
+                const uint32_t bits = key_bits(mask, key0 + cc - base);
+                tmem_ld32u(lane_base + s_col + cc, va);
+                tmem_wait_ld();
+#pragma unroll
+                for (int u = 0; u < 32; ++u) va[u] = (bits >> u) & 1u ? va[u] : hide;
+                tmem_st32u(lane_base + s_col + cc, va);
+              }
+              tmem_wait_st();
+            }
+            // The running max m is a reference only: any value near the scores'
+            // serves.  So the keys are weighed against the m it has, without
+            // looking for their max, and that stands while each row's sum is at
+            // most 2^64 (bf16 hi + lo has float32's range).  Where no key has
+            // been seen yet, or a sum is larger, the max is taken first, and m
+            // moves when it is more than 8 behind (a factor 256).
+            const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
+            bool raise = !__all_sync(0xffffffffu, m != -INFINITY);
+#pragma unroll 1
+            for (;;) {
+              tmem_ld32u(lane_base + s_col + c, va);
+              tmem_ld32u(lane_base + s_col + c + 32, vb);
+              tmem_wait_ld();
+              if (raise) {
+                float ex[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                const uint32_t flip = neg ? 0x80000000u : 0u;
+#pragma unroll
+                for (int u = 0; u < 32; ++u)
+                  ex[u & 3] = max3f(ex[u & 3], __uint_as_float(va[u] ^ flip),
+                                    __uint_as_float(vb[u] ^ flip));
+                const float top = fmaxf(fmaxf(ex[0], ex[1]), fmaxf(ex[2], ex[3]));
+                const float mx = top == -INFINITY ? -INFINITY : top * mag;
+                const bool move = mx > m + kTrRescale || (m == -INFINITY && mx > m);
+                if (__any_sync(0xffffffffu, move)) {
+                  const float alpha = move ? ex2(m - mx) : 1.f;  // 0 when m is -inf
+                  if (seen > 0 || (T::kHalves && c > 0)) {
+                    // the accumulator's last products must be done before it is scaled
+                    ok = __all_sync(0xffffffffu,
+                                    T::kHalves
+                                        ? tr_wait(bars + 8 * (kTrDone + 2 * (c == 0) + w),
+                                                  (c == 0 ? ph - 1 : ph) & 1, abort_flag)
+                                        : tr_wait(bars + 8 * (kTrDone + w), (ph - 1) & 1,
+                                                  abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll 1
+                    for (int cc = 0; cc < D; cc += 32) {
+                      tmem_ld32u(lane_base + o_col + cc, va);
+                      tmem_wait_ld();
+#pragma unroll
+                      for (int u = 0; u < 32; u += 2) {
+                        float y0, y1;
+                        f2_unpack(f2_mul(f2_pack(__uint_as_float(va[u]),
+                                                 __uint_as_float(va[u + 1])), a2), y0, y1);
+                        va[u] = __float_as_uint(y0), va[u + 1] = __float_as_uint(y1);
+                      }
+                      tmem_st32u(lane_base + o_col + cc, va);
+                    }
+                  }
+                  if (!T::kHalves && c > 0) {  // so is the P of the first half, still unused
+                    tmem_wait_st();
+#pragma unroll 1
+                    for (int cc = 0; cc < 64; cc += 32) {
+                      tmem_ld32u(lane_base + s_col + cc, va);
+                      tmem_wait_ld();
+#pragma unroll
+                      for (int u = 0; u < 32; u += u % 8 == 7 ? 9 : 1) {
+                        const uint32_t h = va[u], lw = va[u + 8];
+                        const float e0 = (bf16_lo_to_f32(h) + bf16_lo_to_f32(lw)) * alpha;
+                        const float e1 = (bf16_hi_to_f32(h) + bf16_hi_to_f32(lw)) * alpha;
+                        va[u] = pack_bf16x2(e0, e1);
+                        va[u + 8] =
+                            pack_bf16x2(e0 - bf16_lo_to_f32(va[u]), e1 - bf16_hi_to_f32(va[u]));
+                      }
+                      tmem_st32u(lane_base + s_col + cc, va);
+                    }
+                  }
+                  tmem_ld32u(lane_base + s_col + c, va);
+                  tmem_wait_ld();
+                  l *= alpha;
+                  if (move) m = mx;
+                }
+              }
+              // P = 2^(x - m) as bf16 hi + lo in the scores' place: of each 16 keys
+              // hi in the first 8 columns, lo in the others, two keys a column
+              const float mref = m == -INFINITY ? 0.f : m;  // nothing seen yet: all P are 0
+              const uint64_t nm2 = f2_pack(-mref, -mref);
+              uint64_t ls[2] = {0ull, 0ull};
+              tree_weigh(va, sc2, nm2, ls);
+              tree_weigh(vb, sc2, nm2, ls);
+              float a0, a1, b0, b1;
+              f2_unpack(ls[0], a0, a1);
+              f2_unpack(ls[1], b0, b1);
+              const float sum = (a0 + a1) + (b0 + b1);
+              if (raise || __all_sync(0xffffffffu, sum <= 18446744073709551616.f)) {
+                l += sum;
+                break;
+              }
+              raise = true;  // NaN, too; the scores are still there
+            }
+            if (!ok) break;
+            tmem_st32u(lane_base + s_col + c, va);
+            tmem_st32u(lane_base + s_col + c + 32, vb);
+          }
+          if (T::kHalves || c > 0) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + 8 * (kTrPFull + part));
+          }
+        }
+        if (!ok) break;
         ++seen;
       }
       if (!ok) break;
@@ -831,7 +847,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       for (int a = 0; a < 2; ++a) {
         const int lt = TILES == 2 || ((i - 1) & 1) == a ? i - 1 : i - 2;  // its last tile
         if (lt < begin_tile) continue;
-        ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * (kTrODone + a),
+        ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * (kTrDone + 2 * (kParts - 1) + a),
                                              (TILES == 1 ? lt >> 1 : lt) & 1, abort_flag));
         if (!ok) break;
       }
