@@ -81,6 +81,11 @@ accept_rows_kernel(const AcceptArgs a) {
   const int cb = int(blockIdx.x - item * per_seq);
   const int layer = int(item / a.num_seqs);
   const int seq = int(item - int64_t(layer) * a.num_seqs);
+  const int i = threadIdx.x;
+  // the path is read beside the sizes that say how much of it counts
+  const int32_t* path = a.accepted + int64_t(seq) * a.max_accepted;
+  const int node = i < a.max_accepted ? __ldg(path + i) : 0;
+  const int before = i > 0 && i < a.max_accepted ? __ldg(path + i - 1) : -1;
   const int qs = __ldg(a.q_start + seq), qe = __ldg(a.q_start + seq + 1);
   const int ctx = __ldg(a.context_lens + seq);
   const int count = __ldg(a.num_accepted + seq);
@@ -89,13 +94,7 @@ accept_rows_kernel(const AcceptArgs a) {
   bool ok = n >= 0 && n <= kTreeMaxNodes && n <= ctx &&
             (int64_t(ctx) + kPageTokens - 1) / kPageTokens <= a.max_blocks_per_seq && count >= 0 &&
             count <= n && count <= a.max_accepted;
-  const int32_t* path = a.accepted + int64_t(seq) * a.max_accepted;
-  const int i = threadIdx.x;
-  if (ok && i < count) {
-    const int node = __ldg(path + i);
-    const int before = i > 0 ? __ldg(path + i - 1) : -1;
-    if (node <= before || node >= n) ok = false;
-  }
+  if (ok && i < count && (node <= before || node >= n)) ok = false;
   ok = __syncthreads_and(ok);
   if (!ok) {
     if (first && threadIdx.x == 0) {
@@ -108,7 +107,7 @@ accept_rows_kernel(const AcceptArgs a) {
   if (first && threadIdx.x == 0) a.new_context_lens[seq] = base + count;
   if (i < count) {
     const int32_t* table = a.block_tables + int64_t(seq) * a.max_blocks_per_seq;
-    const int from = base + __ldg(path + i), to = base + i;
+    const int from = base + node, to = base + i;
     const int bf = __ldg(table + from / kPageTokens), bt = __ldg(table + to / kPageTokens);
     const bool known = bf >= 0 && bf < a.num_blocks && bt >= 0 && bt < a.num_blocks;
     if (!known && first) atomicOr(&g_draft_error, kErrBadBlockId);
