@@ -293,7 +293,11 @@ int pkv_bm_commit_draft(pkv_block_manager* bm, int64_t seq_id, const int32_t* to
   for (int64_t j = L / bs; j < (L + num_tokens) / bs; ++j) {
     const int32_t* chunk = s.tokens.data() + size_t(j) * bs;
     s.last_hash = chain_hash(s.last_hash, chunk, bs);
-    bm->register_block(s.blocks[size_t(j)], s.last_hash, chunk);
+    try {
+      bm->register_block(s.blocks[size_t(j)], s.last_hash, chunk);
+    } catch (const std::bad_alloc&) {
+      bm->hashed[size_t(s.blocks[size_t(j)])] = 0;  // committed, only not shareable
+    }
   }
   return PKV_OK;
 }
