@@ -57,12 +57,12 @@ constexpr int kTrKeys = 128;     // keys per K/V tile (8 pages)
 constexpr int kTrThreads = 384;
 constexpr int kTrRegsSoftmax = 192, kTrRegsIssue = 120;
 constexpr int kTrKWarp = 8, kTrSWarp = 9, kTrVWarp = 10;  // 11 issues P V
-constexpr uint32_t kTrTmemCols = 512;  // warpgroup w: S/P at 256 w, O at 256 w + 128
+constexpr uint32_t kTrTmemCols = 512;
 constexpr float kTrRescale = 8.0f;     // log2 units: move the running max when it grows by > x256
 constexpr int kTrMaxStages = 5;
 constexpr int kTrMinTiles = 2;  // one for each softmax warpgroup
 constexpr int kTrSlack = 2;     // key tiles that a second piece costs a CTA
-constexpr int kTrPieces = 4;  // piece descriptions in shared memory
+constexpr int kTrPieces = 5;  // piece descriptions in shared memory
 
 template <int D, int TILES>
 struct TreeSmem {
@@ -74,6 +74,15 @@ struct TreeSmem {
   // nodes 56.3 / 61.6; 64 x 8192, 64 nodes (two row tiles) 926 / 865; 2 x 131072,
   // 27 nodes, heads of 64 145 / 138.
   static constexpr bool kHalves = D == 128 && TILES == 1;
+  // Tensor memory: S/P buffers that the products take in turn, and the
+  // warpgroups' accumulators.  Heads of 128: a buffer and an accumulator of 128
+  // columns a warpgroup.  Heads of 64 leave room for a third buffer, so that a
+  // warpgroup's next scores are made while its last P is still being multiplied.
+  static constexpr int kBufs = D == 64 ? 3 : 2;
+  static __device__ __forceinline__ uint32_t buf_col(int b) { return (D == 64 ? 128 : 256) * b; }
+  static __device__ __forceinline__ uint32_t out_col(int w) {
+    return D == 64 ? 384 + 64 * w : 256 * w + 128;
+  }
   static constexpr int kHalf = 128 * 128;  // 128 rows x 64 bf16
   static constexpr int kTileBytes = (D / 64) * kHalf;
   static constexpr int kQBytes = TILES * kTileBytes;
@@ -103,7 +112,7 @@ enum TrBar {
   kTrQFull = 0, kTrQEmpty = 1,
   kTrKFull = 2, kTrKEmpty = kTrKFull + kTrMaxStages,
   kTrVFull = kTrKEmpty + kTrMaxStages, kTrVEmpty = kTrVFull + kTrMaxStages,
-  // by half 2 h + w: first and second 64 keys of warpgroup w's tile
+  // by buffer, or by half 2 h + w: first and second 64 keys of warpgroup w's tile
   kTrSFull = kTrVEmpty + kTrMaxStages, kTrPFull = kTrSFull + 4, kTrDone = kTrPFull + 4,
   kTrXch = kTrDone + 4, kTrEpi = kTrXch + 1, kTrDrain = kTrEpi + 1, kTrPiece0 = kTrDrain + 1
 };
@@ -512,8 +521,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       int i = 0, k = 0;
       bool ok = true;
       // The pieces are worked out here, ahead of those who need them.  Slot k
-      // is free: the last S product needed a P V of piece k - 3 or later, whose
-      // first one needed everybody to be through with piece k - 4.
+      // is free: the last S product needed a P V of piece k - 4 or later, whose
+      // first one needed everybody to be through with piece k - 5.
       auto publish = [&](bool some) {
         volatile TreePiece* t = pieces + k % kTrPieces;
         if (some) {
@@ -549,9 +558,9 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
           // a part's columns are free once the products that read its P are done
 #pragma unroll 1
           for (int th = 0; ok && th < kParts * TILES; ++th) {
-            const int t = th / kParts, h = th % kParts, w = TILES == 1 ? i & 1 : t;
-            const int before = TILES == 1 ? (i >> 1) - 1 : i - 1;
-            ok = before < 0 || wait(kTrDone + 2 * h + w, before & 1);
+            const int t = th / kParts, h = th % kParts, job = i * TILES + t;
+            const int b = job % T::kBufs, before = job / T::kBufs - 1;
+            ok = before < 0 || wait(kTrDone + 2 * h + b, before & 1);
             if (!ok) break;
             tc_fence_after();
             const uint32_t q_smem = sbase + t * T::kTileBytes;
@@ -560,10 +569,10 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               const uint32_t off = (c >> 2) * T::kHalf + (c & 3) * 32;
-              umma_bf16(tmem + w * 256 + h * 64, smem_desc_sw128(q_smem + off, 16, 1024),
+              umma_bf16(tmem + T::buf_col(b) + h * 64, smem_desc_sw128(q_smem + off, 16, 1024),
                         smem_desc_sw128(k_smem + off, 16, 1024), kIdesc, c > 0);
             }
-            umma_commit(bars + 8 * (kTrSFull + 2 * h + w));
+            umma_commit(bars + 8 * (kTrSFull + 2 * h + b));
           }
           umma_commit(bars + 8 * (kTrKEmpty + i % T::kKStages));
           if (j + 1 == walk.tiles) umma_commit(bars + 8 * kTrQEmpty);
@@ -605,19 +614,20 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
           const uint32_t v_smem = sbase + T::kVOff + (i % T::kVStages) * T::kTileBytes;
 #pragma unroll 1
           for (int th = 0; ok && th < kParts * TILES; ++th) {
-            const int t = th / kParts, h = th % kParts, w = TILES == 1 ? i & 1 : t;
-            ok = wait(kTrPFull + 2 * h + w, (TILES == 1 ? i >> 1 : i) & 1);
+            const int t = th / kParts, h = th % kParts, job = i * TILES + t;
+            const int b = job % T::kBufs;
+            ok = wait(kTrPFull + 2 * h + b, (job / T::kBufs) & 1);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < kTrKeys / 16 / kParts; ++c) {
               const uint64_t vdesc = smem_desc_sw128(v_smem + (4 * h + c) * 2048, T::kHalf, 1024);
-              const uint32_t a_hi = tmem + w * 256 + 64 * h + 16 * c;  // hi, and lo 8 columns on
-              umma_bf16_ts(tmem + w * 256 + 128, a_hi, vdesc, kIdesc,
+              const uint32_t a_hi = tmem + T::buf_col(b) + 64 * h + 16 * c;  // hi, and lo 8 columns on
+              umma_bf16_ts(tmem + T::out_col(job & 1), a_hi, vdesc, kIdesc,
                            (!fresh || h > 0 || c > 0) ? 1u : 0u);
-              umma_bf16_ts(tmem + w * 256 + 128, a_hi + 8, vdesc, kIdesc, 1u);
+              umma_bf16_ts(tmem + T::out_col(job & 1), a_hi + 8, vdesc, kIdesc, 1u);
             }
-            umma_commit(bars + 8 * (kTrDone + 2 * h + w));
+            umma_commit(bars + 8 * (kTrDone + 2 * h + b));
           }
           if (!ok) break;
           if (j + 1 < tiles) umma_commit(bars + 8 * (kTrVEmpty + i % T::kVStages));
@@ -636,7 +646,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     const int w = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // row of the tile = tensor-memory lane
     const uint32_t lane_base = tmem + (uint32_t((warp & 3) * 32) << 16);
-    const uint32_t s_col = w * 256, o_col = w * 256 + 128;
+    const uint32_t o_col = T::out_col(w);
     float2* xch = reinterpret_cast<float2*>(smem + T::kXchOff);
     const bool neg = p.scale_log2 < 0.f;  // uniform
     const float mag = fabsf(p.scale_log2);
@@ -664,7 +674,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       for (int j = 0; j < tiles; ++j) {
         const int it = i + j;
         if (TILES == 1 && (it & 1) != w) continue;
-        const int ph = TILES == 1 ? it >> 1 : it;
+        const int job = TILES == 1 ? it : 2 * it + w, b = job % T::kBufs, ph = job / T::kBufs;
+        const uint32_t s_col = T::buf_col(b);
         const int key0 = (first + j) * kTrKeys;
         const bool masked = key0 + kTrKeys > base;
         if (masked && (TILES == 1 || w == 0)) {
@@ -699,7 +710,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
 #pragma unroll 1
         for (int c = 0; c < kTrKeys; c += 64) {  // the halves of the tile
-          const int part = T::kHalves ? (c >> 5) + w : w;
+          const int part = T::kHalves ? (c >> 5) + b : b;
           if (T::kHalves || c == 0) {
             ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * (kTrSFull + part), ph & 1, abort_flag));
             if (!ok) break;
@@ -752,8 +763,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
                                     T::kHalves
                                         ? tr_wait(bars + 8 * (kTrDone + 2 * (c == 0) + w),
                                                   (c == 0 ? ph - 1 : ph) & 1, abort_flag)
-                                        : tr_wait(bars + 8 * (kTrDone + w), (ph - 1) & 1,
-                                                  abort_flag));
+                                        : tr_wait(bars + 8 * (kTrDone + (job - 2) % T::kBufs),
+                                                  ((job - 2) / T::kBufs) & 1, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t a2 = f2_pack(alpha, alpha);
@@ -847,8 +858,10 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       for (int a = 0; a < 2; ++a) {
         const int lt = TILES == 2 || ((i - 1) & 1) == a ? i - 1 : i - 2;  // its last tile
         if (lt < begin_tile) continue;
-        ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * (kTrDone + 2 * (kParts - 1) + a),
-                                             (TILES == 1 ? lt >> 1 : lt) & 1, abort_flag));
+        const int job = TILES == 1 ? lt : 2 * lt + a;
+        ok = __all_sync(0xffffffffu,
+                        tr_wait(bars + 8 * (kTrDone + 2 * (kParts - 1) + job % T::kBufs),
+                                (job / T::kBufs) & 1, abort_flag));
         if (!ok) break;
       }
       if (!ok) break;
@@ -890,7 +903,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
         for (int c = 0; c < kCols; c += 32) {
           uint32_t o[32], x[32];
           if (use_a) tmem_ld32u(lane_base + o_col + col0 + c, o);
-          if (use_b) tmem_ld32u(lane_base + (256 - s_col) + 128 + col0 + c, x);
+          if (use_b) tmem_ld32u(lane_base + T::out_col(1 - w) + col0 + c, x);
           tmem_wait_ld();
           // an accumulator that no tile of the piece went to holds anything
           const uint64_t a2 = f2_pack(fa, fa), b2 = f2_pack(fb, fb);
