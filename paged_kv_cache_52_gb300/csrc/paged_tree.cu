@@ -59,7 +59,7 @@ constexpr int kTrRegsSoftmax = 192, kTrRegsIssue = 120;
 constexpr int kTrKWarp = 8, kTrSWarp = 9, kTrVWarp = 10;  // 11 issues P V
 constexpr uint32_t kTrTmemCols = 512;
 constexpr float kTrRescale = 8.0f;     // log2 units: move the running max when it grows by > x256
-constexpr int kTrMaxStages = 5;
+constexpr int kTrMaxStages = 4;
 constexpr int kTrMinTiles = 2;  // one for each softmax warpgroup
 constexpr int kTrSlack = 2;     // key tiles that a second piece costs a CTA
 constexpr int kTrPieces = 5;  // piece descriptions in shared memory
@@ -144,6 +144,16 @@ struct TreeSeq {
   int qs, n, ctx, groups, tiles;
   bool bad;
   __device__ __forceinline__ int total(int kv_heads) const { return groups * tiles * kv_heads; }
+  // With kTrSlack places before each item for what its start costs: places, and
+  // the key tiles among the first x of them.
+  __device__ __forceinline__ int places(int kv_heads) const {
+    return groups * (tiles + kTrSlack) * kv_heads;
+  }
+  __device__ __forceinline__ int tiles_in(int x, int kv_heads) const {
+    x = min(max(x, 0), places(kv_heads));
+    const int item = x / (tiles + kTrSlack);
+    return item * tiles + max(x - item * (tiles + kTrSlack) - kTrSlack, 0);
+  }
 };
 
 template <int G, int TILES>
@@ -157,7 +167,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int s) {
           r.ctx > p.max_blocks_per_seq * 16;
   constexpr int kTokens = TILES * kTrRows / G;
   r.groups = r.bad ? 0 : (r.n + kTokens - 1) / kTokens;
-  r.tiles = (r.ctx + kTrKeys - 1) / kTrKeys;
+  r.tiles = r.bad ? 0 : (r.ctx + kTrKeys - 1) / kTrKeys;
   return r;
 }
 
@@ -297,7 +307,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
   int* scan = reinterpret_cast<int*>(smem + T::kMiscOff + 32);
   struct Begin {
     TreeSeq seq;
-    int s, off;
+    int s, off, count;
   };
   static_assert(sizeof(Begin) <= 48, "start of the range");
   volatile TreePiece* pieces = reinterpret_cast<volatile TreePiece*>(smem + T::kPieceOff);
@@ -332,6 +342,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     fence_barrier_init();
     *abort_flag = 0;
     nonfinite[0] = nonfinite[1] = 0;
+    begin->count = 0;
   }
   if (threadIdx.x == kTrVWarp * 32) tma_prefetch_desc(&tmap_v);
   if (threadIdx.x == kTrSWarp * 32) {
@@ -357,11 +368,12 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
     return x;
   };
-  // Else the tiles are laid end to end, CTA c starting at floor(c all / active).  With few
-  // tiles the last CTAs have none, so that a cut item's pieces lie in
-  // consecutive CTAs.
+  // The items' places laid end to end, CTA c starting at floor(c all / active).
+  // With few the last CTAs have none.  A CTA whose places hold no tile has no
+  // work; a cut item's pieces lie in consecutive CTAs all the same.
   auto even_share = [&](int all, int& lo, int& n) {
-    const int active = min(ctas, (all + kTrMinTiles - 1) / kTrMinTiles);
+    constexpr int kLeast = kTrMinTiles + kTrSlack;
+    const int active = min(ctas, (all + kLeast - 1) / kLeast);
     const int each = active > 0 ? all / active : 0, rest = all - each * active;
     lo = c < active ? c * each + c * rest / active : all;
     n = c < active ? (c + 1) * each + (c + 1) * rest / active - lo : 0;
@@ -370,19 +382,22 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     // every warp for itself, lane = sequence: no barrier before the first load
     if (lane < p.num_seqs) q = tree_seq<G, TILES>(p, lane);
     if (q.bad && c == 0 && warp == 0) atomicOr(&g_tree_error, kErrBadQueryRange);
-    const int items = q.groups * p.kv_heads, mine = q.total(p.kv_heads);
-    const int all = __reduce_add_sync(0xffffffffu, mine);
-    // A CTA with parts of two items spends about kTrSlack tiles' time between
-    // them.  So with no more items than CTAs each item is cut into equal pieces
-    // of at most kTrSlack tiles above the even share, one piece a CTA, if there
-    // are CTAs enough.
-    const int longest = max(kTrMinTiles, all / ctas + kTrSlack);
+    const int items = q.groups * p.kv_heads;
+    const int tiles = __reduce_add_sync(0xffffffffu, q.total(p.kv_heads));
+    // With no more items than CTAs each item is cut into equal pieces of at most
+    // kTrSlack tiles above the even share, one piece a CTA, if there are CTAs
+    // enough.
+    const int longest = max(kTrMinTiles, tiles / ctas + kTrSlack);
     const int cuts = items ? (q.tiles + longest - 1) / longest : 0;
     const bool alone = __reduce_add_sync(0xffffffffu, items * cuts) <= ctas;
-    int lo = c;
-    if (!alone) even_share(all, lo, count);
-    const int width = alone ? items * cuts : mine;
-    const int end = warp_scan(width), at = lo - (end - width);
+    const int width = alone ? items * cuts : q.places(p.kv_heads);
+    const int end = warp_scan(width);
+    int lo = c, n = 0;
+    if (!alone) even_share(__shfl_sync(0xffffffffu, end, 31), lo, n);
+    const int at = lo - (end - width);
+    if (!alone)
+      count = __reduce_add_sync(0xffffffffu, q.tiles_in(at + n, p.kv_heads) -
+                                                 q.tiles_in(at, p.kv_heads));
     const unsigned here = __ballot_sync(0xffffffffu, at >= 0 && at < width);
     if (here) {
       const int src = __ffs(here) - 1;
@@ -391,11 +406,11 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
         off0 = item * q.tiles + first;
         count = (j + 1) * q.tiles / cuts - first;
       } else {
-        off0 = at;
+        off0 = q.tiles_in(at, p.kv_heads);
       }
       s0 = src;
       off0 = __shfl_sync(0xffffffffu, off0, src);
-      count = __shfl_sync(0xffffffffu, count, src);
+      count = __shfl_sync(0xffffffffu, count, src);  // the same in all lanes if not alone
       q.qs = __shfl_sync(0xffffffffu, q.qs, src);
       q.n = __shfl_sync(0xffffffffu, q.n, src);
       q.ctx = __shfl_sync(0xffffffffu, q.ctx, src);
@@ -412,9 +427,9 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     for (int s = s_lo; s < s_hi; ++s) {
       q = tree_seq<G, TILES>(p, s);
       if (q.bad && c == 0) atomicOr(&g_tree_error, kErrBadQueryRange);
-      mine += q.total(p.kv_heads);
+      mine += q.places(p.kv_heads);
     }
-    int incl = warp_scan(mine), all = 0, lo;
+    int incl = warp_scan(mine), all = 0, lo, n;
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
 #pragma unroll
@@ -422,19 +437,23 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       if (w == warp) incl += all;
       all += scan[w];
     }
-    even_share(all, lo, count);
-    if (lo >= incl - mine && lo < incl) {  // the range starts in this thread's sequences
-      int at = lo - (incl - mine), s = s_lo;
-      if (per_thread > 1)
-        for (;; ++s) {
-          q = tree_seq<G, TILES>(p, s);
-          const int w = q.total(p.kv_heads);
-          if (at < w) break;
-          at -= w;
+    even_share(all, lo, n);
+    if (lo < incl && lo + n > incl - mine) {  // some of the range is this thread's
+      int at = lo - (incl - mine);
+      for (int s = s_lo; s < s_hi; ++s) {
+        if (per_thread > 1) q = tree_seq<G, TILES>(p, s);
+        const int tiles = q.tiles_in(at + n, p.kv_heads) - q.tiles_in(at, p.kv_heads);
+        if (tiles > 0) atomicAdd(&begin->count, tiles);
+        if (at >= 0 && at < q.places(p.kv_heads)) {  // it starts here
+          begin->seq = q;
+          begin->s = s;
+          begin->off = q.tiles_in(at, p.kv_heads);
         }
-      *begin = Begin{q, s, at};
+        at -= q.places(p.kv_heads);
+      }
     }
     __syncthreads();
+    count = begin->count;
     if (count > 0) {
       q = begin->seq;
       s0 = begin->s;
@@ -471,8 +490,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const int nblk = (walk.seq.ctx + 15) / 16;
       for (int j = 0; j < walk.tiles; ++j, ++i) {
         const int st = i % stages;
+        const int blk0 = (walk.first + j) * 8, blk = blk0 + lane / (D / 64);
         int id = -1;  // pages past the context: the box is out of bounds and reads zeros
-        const int blk = (walk.first + j) * 8 + lane / (D / 64);
         if (lane < kLoads && blk < nblk) {
           id = __ldg(table + blk);
           if (id < 0 || id >= p.num_blocks) {
@@ -480,6 +499,11 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
             id = -1;
           }
         }
+        // The table's next entries come into L2 four tiles before they are
+        // read: without it a read of a new line took 4000-5700 cycles behind
+        // the queued pages, every fourth tile.
+        if (lane == 0 && !is_v && blk0 % 32 == 0 && blk0 + 32 < nblk)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(table + blk0 + 32));
         if (i >= stages) {
           ok = __all_sync(0xffffffffu, tr_wait(empty + 8 * st, (i / stages - 1) & 1, abort_flag));
           if (!ok) break;
@@ -893,29 +917,42 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // TILES 1: this warpgroup's half of the columns of both accumulators
         constexpr int kCols = TILES == 1 ? D / 2 : D;
         const int col0 = TILES == 1 ? w * kCols : 0;
-        const unsigned rows_valid = __ballot_sync(0xffffffffu, valid);
-        const int chunk0 = col0 + 4 * (lane & 7);
-        const size_t out0 =
-            ((size_t(qs) + node0) * p.q_heads + size_t(kvh) * G) * D + chunk0;
+        // A whole item's rows leave as rows 4 u + lane / 8 of the warp's 32, 4 columns
+        // a lane: where this lane's first one goes, how many are valid.
+        const int row8 = lane >> 3, warp_rows = (n - node0) * G - (warp & 3) * 32;
+        const int stores = (warp_rows - row8 + 3) >> 2;
+        const size_t node_stride = size_t(p.q_heads) * D;
+        const size_t out0 = (size_t(qs) + node0 + (warp & 3) * (32 / G) + row8 / G) * node_stride +
+                            size_t(kvh * G + row8 % G) * D + col0 + 4 * (lane & 7);
+        const uint32_t from = stage + row8 * 128 + (((lane + row8) & 7) << 4);
         const bool use_a = __any_sync(0xffffffffu, fa != 0.f);
         const bool use_b = TILES == 1 && __any_sync(0xffffffffu, fb != 0.f);
 #pragma unroll 1
         for (int c = 0; c < kCols; c += 32) {
           uint32_t o[32], x[32];
+          // an accumulator that no tile of the piece went to holds anything
           if (use_a) tmem_ld32u(lane_base + o_col + col0 + c, o);
           if (use_b) tmem_ld32u(lane_base + T::out_col(1 - w) + col0 + c, x);
           tmem_wait_ld();
-          // an accumulator that no tile of the piece went to holds anything
           const uint64_t a2 = f2_pack(fa, fa), b2 = f2_pack(fb, fb);
+          if (!use_a) {
+#pragma unroll
+            for (int u = 0; u < 32; ++u) o[u] = 0;
+          }
 #pragma unroll
           for (int u = 0; u < 32; u += 2) {
-            uint64_t y = use_a ? f2_mul(f2_pack(__uint_as_float(o[u]), __uint_as_float(o[u + 1])), a2)
-                               : 0ull;
-            if (use_b)
-              y = f2_fma(f2_pack(__uint_as_float(x[u]), __uint_as_float(x[u + 1])), b2, y);
             float y0, y1;
-            f2_unpack(y, y0, y1);
+            f2_unpack(f2_mul(f2_pack(__uint_as_float(o[u]), __uint_as_float(o[u + 1])), a2), y0, y1);
             o[u] = __float_as_uint(y0), o[u + 1] = __float_as_uint(y1);
+          }
+          if (use_b) {
+#pragma unroll
+            for (int u = 0; u < 32; u += 2) {
+              float y0, y1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[u]), __uint_as_float(x[u + 1])), b2,
+                               f2_pack(__uint_as_float(o[u]), __uint_as_float(o[u + 1]))), y0, y1);
+              o[u] = __float_as_uint(y0), o[u + 1] = __float_as_uint(y1);
+            }
           }
           // A cut item's rows go to the workspace as rows of 4 columns, 512
           // contiguous bytes a store; a whole item's through shared memory, so
@@ -952,21 +989,23 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
           }
           if (!whole) continue;
           __syncwarp();
-          // this lane's chunk of rows lane / 8 + 4 u
-#pragma unroll 2
-          for (int u = 0; u < 8; ++u) {
-            const int row = 4 * u + (lane >> 3);
-            const uint4 y = ld_shared_u4(stage + row * 128 + (((lane + row) & 7) << 4));
-            if (!((rows_valid >> row) & 1u)) continue;
-            const int tr = (warp & 3) * 32 + row;  // row of the tile
-            const size_t at = size_t(tr / G) * (p.q_heads * D) + (tr % G) * D + c;
-            if (p.out_bf16)
-              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + out0 + at) =
+          auto each = [&](auto store) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              if (u < stores)
+                store(ld_shared_u4((from ^ ((u & 1) << 6)) + u * 512),
+                      out0 + c + (4 * u / G) * node_stride + (4 * u % G) * D);
+          };
+          if (p.out_bf16)
+            each([&](const uint4& y, size_t at) {
+              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
                   make_uint2(pack_bf16x2(__uint_as_float(y.x), __uint_as_float(y.y)),
                              pack_bf16x2(__uint_as_float(y.z), __uint_as_float(y.w)));
-            else
-              *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + out0 + at) = y;
-          }
+            });
+          else
+            each([&](const uint4& y, size_t at) {
+              *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + at) = y;
+            });
           __syncwarp();
         }
         if (valid && !whole && col0 == 0) p.part_lse[prow0 + lane] = lse;
