@@ -136,6 +136,7 @@ struct TreeParams {
   float* part_lse;  // [2 CTAs][TILES * 128], log2
   TreeStart* start; // [CTAs]
   int num_seqs, total_q, max_q_len, q_heads, kv_heads, num_blocks, max_blocks_per_seq;
+  int lanes;  // parts of the grid that take the KV heads side by side
   float scale_log2;
 };
 
@@ -143,14 +144,14 @@ struct TreeParams {
 struct TreeSeq {
   int qs, n, ctx, groups, tiles;
   bool bad;
-  __device__ __forceinline__ int total(int kv_heads) const { return groups * tiles * kv_heads; }
+  __device__ __forceinline__ int total(int heads) const { return groups * tiles * heads; }
   // With kTrSlack places before each item for what its start costs: places, and
   // the key tiles among the first x of them.
-  __device__ __forceinline__ int places(int kv_heads) const {
-    return groups * (tiles + kTrSlack) * kv_heads;
+  __device__ __forceinline__ int places(int heads) const {
+    return groups * (tiles + kTrSlack) * heads;
   }
-  __device__ __forceinline__ int tiles_in(int x, int kv_heads) const {
-    x = min(max(x, 0), places(kv_heads));
+  __device__ __forceinline__ int tiles_in(int x, int heads) const {
+    x = min(max(x, 0), places(heads));
     const int item = x / (tiles + kTrSlack);
     return item * tiles + max(x - item * (tiles + kTrSlack) - kTrSlack, 0);
   }
@@ -183,15 +184,16 @@ struct TreeWalk {
   const TreeParams& p;
   int s;
   int off;         // tiles of sequence s before the next piece
+  int lane, heads; // part of the grid and its KV heads: lane, lane + lanes, ...
   int left;        // tiles of the range after the current piece
   TreeSeq seq;
   int item, first, tiles;  // current piece
   __device__ __forceinline__ TreeWalk(const TreeParams& pp, const TreeSeq& q0, int s0,
-                                      int off0, int count)
-      : p(pp), s(s0), off(off0), left(count), seq(q0) {}
+                                      int off0, int count, int lane0, int heads0)
+      : p(pp), s(s0), off(off0), lane(lane0), heads(heads0), left(count), seq(q0) {}
   __device__ __forceinline__ bool next() {
     if (left <= 0) return false;
-    while (off >= seq.total(p.kv_heads)) {
+    while (off >= seq.total(heads)) {
       if (++s >= p.num_seqs) return false;
       off = 0;
       seq = tree_seq<G, TILES>(p, s);
@@ -203,7 +205,9 @@ struct TreeWalk {
     left -= tiles;
     return true;
   }
-  __device__ __forceinline__ int kv_head() const { return item / seq.groups; }
+  __device__ __forceinline__ int kv_head() const {
+    return lane + item / seq.groups * p.lanes;
+  }
   __device__ __forceinline__ int group() const { return item % seq.groups; }
   __device__ __forceinline__ bool whole() const { return first == 0 && tiles == seq.tiles; }
 };
@@ -356,7 +360,13 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
   griddep_wait();  // inputs may have been written by the previous kernel in the stream
 
   // ---- this CTA's range of the key tiles of all items
-  const int ctas = gridDim.x, c = blockIdx.x;
+  // The grid's `lanes` equal parts take a share of the KV heads each.  Where there
+  // is work for some CTAs only, they then lie all over the GPU (us, against one
+  // part: 1 x 500 12.3 / 12.9, 1 x 2000 17.5 / 18.0, 4 x 1000 17.0 / 17.5; 16 x 4096
+  // and larger the same).  CTAs that the division leaves over have no work.
+  const int ctas = gridDim.x / p.lanes, heads = p.kv_heads / p.lanes;
+  const int part = blockIdx.x / ctas;
+  const int c = part < p.lanes ? blockIdx.x - part * ctas : ctas;
   TreeSeq q{};               // the sequence it starts in,
   int s0 = -1, off0 = 0;     // its number, and the tiles of it before the range
   int count = 0;
@@ -381,23 +391,23 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
   if (p.num_seqs <= 32) {
     // every warp for itself, lane = sequence: no barrier before the first load
     if (lane < p.num_seqs) q = tree_seq<G, TILES>(p, lane);
-    if (q.bad && c == 0 && warp == 0) atomicOr(&g_tree_error, kErrBadQueryRange);
-    const int items = q.groups * p.kv_heads;
-    const int tiles = __reduce_add_sync(0xffffffffu, q.total(p.kv_heads));
+    if (q.bad && blockIdx.x == 0 && warp == 0) atomicOr(&g_tree_error, kErrBadQueryRange);
+    const int items = q.groups * heads;
+    const int tiles = __reduce_add_sync(0xffffffffu, q.total(heads));
     // With no more items than CTAs each item is cut into equal pieces of at most
     // kTrSlack tiles above the even share, one piece a CTA, if there are CTAs
     // enough.
     const int longest = max(kTrMinTiles, tiles / ctas + kTrSlack);
     const int cuts = items ? (q.tiles + longest - 1) / longest : 0;
     const bool alone = __reduce_add_sync(0xffffffffu, items * cuts) <= ctas;
-    const int width = alone ? items * cuts : q.places(p.kv_heads);
+    const int width = alone ? items * cuts : q.places(heads);
     const int end = warp_scan(width);
     int lo = c, n = 0;
     if (!alone) even_share(__shfl_sync(0xffffffffu, end, 31), lo, n);
     const int at = lo - (end - width);
     if (!alone)
-      count = __reduce_add_sync(0xffffffffu, q.tiles_in(at + n, p.kv_heads) -
-                                                 q.tiles_in(at, p.kv_heads));
+      count = __reduce_add_sync(0xffffffffu, q.tiles_in(at + n, heads) -
+                                                 q.tiles_in(at, heads));
     const unsigned here = __ballot_sync(0xffffffffu, at >= 0 && at < width);
     if (here) {
       const int src = __ffs(here) - 1;
@@ -406,7 +416,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
         off0 = item * q.tiles + first;
         count = (j + 1) * q.tiles / cuts - first;
       } else {
-        off0 = q.tiles_in(at, p.kv_heads);
+        off0 = q.tiles_in(at, heads);
       }
       s0 = src;
       off0 = __shfl_sync(0xffffffffu, off0, src);
@@ -426,8 +436,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     int mine = 0;
     for (int s = s_lo; s < s_hi; ++s) {
       q = tree_seq<G, TILES>(p, s);
-      if (q.bad && c == 0) atomicOr(&g_tree_error, kErrBadQueryRange);
-      mine += q.places(p.kv_heads);
+      if (q.bad && blockIdx.x == 0) atomicOr(&g_tree_error, kErrBadQueryRange);
+      mine += q.places(heads);
     }
     int incl = warp_scan(mine), all = 0, lo, n;
     if (lane == 31) scan[warp] = incl;
@@ -442,14 +452,14 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       int at = lo - (incl - mine);
       for (int s = s_lo; s < s_hi; ++s) {
         if (per_thread > 1) q = tree_seq<G, TILES>(p, s);
-        const int tiles = q.tiles_in(at + n, p.kv_heads) - q.tiles_in(at, p.kv_heads);
+        const int tiles = q.tiles_in(at + n, heads) - q.tiles_in(at, heads);
         if (tiles > 0) atomicAdd(&begin->count, tiles);
-        if (at >= 0 && at < q.places(p.kv_heads)) {  // it starts here
+        if (at >= 0 && at < q.places(heads)) {  // it starts here
           begin->seq = q;
           begin->s = s;
-          begin->off = q.tiles_in(at, p.kv_heads);
+          begin->off = q.tiles_in(at, heads);
         }
-        at -= q.places(p.kv_heads);
+        at -= q.places(heads);
       }
     }
     __syncthreads();
@@ -461,12 +471,16 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
   }
   if (threadIdx.x == 0) {
-    const int item = count > 0 ? off0 / q.tiles : 0;
-    p.start[c] = TreeStart{count > 0 ? s0 : -1, item, off0 - item * q.tiles, q.qs, q.n, q.groups,
-                           {0, 0}};
+    TreeStart at{-1, 0, 0, 0, 0, 0, {0, 0}};
+    if (count > 0) {
+      const int item = off0 / q.tiles, kvh = part + item / q.groups * p.lanes;
+      at = TreeStart{s0, kvh * q.groups + item % q.groups, off0 - item * q.tiles, q.qs, q.n,
+                     q.groups, {0, 0}};
+    }
+    p.start[blockIdx.x] = at;
   }
   if (count > 0) {
-  TreeWalk<G, TILES> walk(p, q, s0, off0, count);
+  TreeWalk<G, TILES> walk(p, q, s0, off0, count, part, heads);
 
   // The launch gives every warp 168 registers; the four loading and issuing
   // warps hand some of theirs to the softmax warps.  8 x 192 + 4 x 120 <= 12 x 168
@@ -1204,6 +1218,9 @@ cudaError_t launch_paged_tree(const TreeArgs& a, const CUtensorMap* tq, const CU
   p.max_q_len = a.max_q_len;
   p.q_heads = a.q_heads;
   p.kv_heads = a.kv_heads;
+  // the most parts that divide the KV heads and leave at most a 20th of the CTAs over
+  p.lanes = a.kv_heads;
+  while (p.lanes > 1 && (a.kv_heads % p.lanes != 0 || a.ctas % p.lanes * 20 > a.ctas)) --p.lanes;
   p.num_blocks = a.num_blocks;
   p.max_blocks_per_seq = a.max_blocks_per_seq;
   p.scale_log2 = a.scale_log2;
