@@ -92,11 +92,7 @@ struct TreeSmem {
   static constexpr int kVStages = D == 64 ? 4 : (TILES == 1 ? 3 : 2);
   static constexpr int kKOff = kQBytes;
   static constexpr int kVOff = kKOff + kKStages * kTileBytes;
-  // The epilogue stages 32 rows x 128 bytes a warp: heads of 128 in the V slot
-  // of the piece's last tile (which goes back to the ring after it), of 64 in
-  // shared memory of its own.
-  static constexpr int kStageOff = kVOff + kVStages * kTileBytes;
-  static constexpr int kXchOff = kStageOff + (D == 64 ? 8 * 4096 : 0);  // [2][128] (max, sum)
+  static constexpr int kXchOff = kVOff + kVStages * kTileBytes;  // [2][128] (max, sum)
   static constexpr int kBarOff = kXchOff + 2 * kTrRows * 8;
   static constexpr int kNumBars = 2 + 4 * kTrMaxStages + 12 + 3 + kTrPieces;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
@@ -132,6 +128,7 @@ struct TreeParams {
   const void* v_pool;
   void* out;
   int out_bf16;
+  int out_wide;     // out lies at a multiple of 32 bytes
   float* part_o;    // [2 CTAs][TILES][D / 4][128 rows][4], normalised
   float* part_lse;  // [2 CTAs][TILES * 128], log2
   TreeStart* start; // [CTAs]
@@ -231,6 +228,18 @@ __device__ __forceinline__ uint32_t key_bits(unsigned long long mask, int off) {
   if (off >= 64 || off <= -32) return off < 0 ? 0xffffffffu : 0u;
   if (off >= 0) return uint32_t(mask >> off);
   return ((1u << -off) - 1u) | uint32_t(mask << -off);
+}
+
+// 32 bytes to a multiple of 16, in one piece where it is one of 32.
+__device__ __forceinline__ void store_sector(void* to, const uint32_t (&y)[8], bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(y[0]),
+                 "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(y[4]), "r"(y[5]), "r"(y[6]), "r"(y[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(to)[0] = make_uint4(y[0], y[1], y[2], y[3]);
+    static_cast<uint4*>(to)[1] = make_uint4(y[4], y[5], y[6], y[7]);
+  }
 }
 
 __device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
@@ -632,19 +641,12 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       };
       int i = 0;
       bool ok = true;
-      // the epilogue of piece k - 1 has read the accumulators and the V slot
-      // it staged its rows in, which goes back to the ring
-      auto after_epilogue = [&](int k) {
-        if (!wait(kTrEpi, (k - 1) & 1)) return false;
-        mbar_arrive(bars + 8 * (kTrVEmpty + (i - 1) % T::kVStages));
-        return true;
-      };
       int k = 0;
       for (; ok; ++k) {
         ok = wait(kTrPiece0 + k % kTrPieces, (k / kTrPieces) & 1);
         const int tiles = ok ? abs(pieces[k % kTrPieces].tiles) : 0;
         if (tiles == 0) break;
-        if (k > 0) ok = after_epilogue(k);
+        if (k > 0) ok = wait(kTrEpi, (k - 1) & 1);  // the accumulators have been read
 #pragma unroll 1
         for (int j = 0; ok && j < tiles; ++j, ++i) {
           const bool fresh = j < (TILES == 1 ? 2 : 1);  // the accumulator's first tile of the piece
@@ -668,10 +670,9 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
             umma_commit(bars + 8 * (kTrDone + 2 * h + b));
           }
           if (!ok) break;
-          if (j + 1 < tiles) umma_commit(bars + 8 * (kTrVEmpty + i % T::kVStages));
+          umma_commit(bars + 8 * (kTrVEmpty + i % T::kVStages));
         }
       }
-      if (ok) ok = after_epilogue(k);
       if (!ok) tr_abort(abort_flag);
       umma_commit(bars + 8 * kTrDrain);
       (void)mbar_wait_bounded(bars + 8 * kTrDrain, 0);
@@ -919,115 +920,129 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
       tc_fence_after();
 
-      if (warp_valid) {
-        const int qs = piece->qs, seq = piece->seq, kvh = piece->kvh;
-        const bool whole = piece->tiles < 0;
-        const unsigned long long hit = mask & nonfinite[k & 1];
-        // slot 2c: the piece the CTA's range starts with, 2c + 1: the one it ends with
-        const size_t slot = size_t(blockIdx.x) * 2 + (k == 0 ? 0 : 1);
-        const size_t prow0 = (slot * TILES + (TILES == 2 ? w : 0)) * kTrRows + (warp & 3) * 32;
-        const uint32_t stage = sbase + warp * 4096 +
-            (D == 64 ? T::kStageOff : T::kVOff + ((i - 1) % T::kVStages) * T::kTileBytes);
-        // TILES 1: this warpgroup's half of the columns of both accumulators
-        constexpr int kCols = TILES == 1 ? D / 2 : D;
-        const int col0 = TILES == 1 ? w * kCols : 0;
-        // A whole item's rows leave as rows 4 u + lane / 8 of the warp's 32, 4 columns
-        // a lane: where this lane's first one goes, how many are valid.
-        const int row8 = lane >> 3, warp_rows = (n - node0) * G - (warp & 3) * 32;
-        const int stores = (warp_rows - row8 + 3) >> 2;
-        const size_t node_stride = size_t(p.q_heads) * D;
-        const size_t out0 = (size_t(qs) + node0 + (warp & 3) * (32 / G) + row8 / G) * node_stride +
-                            size_t(kvh * G + row8 % G) * D + col0 + 4 * (lane & 7);
-        const uint32_t from = stage + row8 * 128 + (((lane + row8) & 7) << 4);
-        const bool use_a = __any_sync(0xffffffffu, fa != 0.f);
-        const bool use_b = TILES == 1 && __any_sync(0xffffffffu, fb != 0.f);
+      // TILES 1: this warpgroup's half of the columns of both accumulators.  They
+      // are read in groups of up to 64, as many as the registers hold; with the
+      // last group read, before it is stored, the accumulators are free for the
+      // next piece's products.
+      constexpr int kAll = TILES == 1 ? D / 2 : D, kCols = kAll < 64 ? kAll : 64;
+      const int qs = piece->qs, seq = piece->seq, kvh = piece->kvh;
+      const bool whole = piece->tiles < 0;
+      const unsigned long long hit = mask & nonfinite[k & 1];
+      const bool use_a = __any_sync(0xffffffffu, fa != 0.f);
+      const bool use_b = TILES == 1 && __any_sync(0xffffffffu, fb != 0.f);
 #pragma unroll 1
-        for (int c = 0; c < kCols; c += 32) {
-          uint32_t o[32], x[32];
+      for (int g = 0; g < kAll; g += kCols) {
+        const int col0 = (TILES == 1 ? w * kAll : 0) + g;
+        uint32_t o[kCols / 32][32];
+        if (warp_valid) {
           // an accumulator that no tile of the piece went to holds anything
-          if (use_a) tmem_ld32u(lane_base + o_col + col0 + c, o);
-          if (use_b) tmem_ld32u(lane_base + T::out_col(1 - w) + col0 + c, x);
-          tmem_wait_ld();
+          if (use_a) {
+#pragma unroll
+            for (int c = 0; c < kCols / 32; ++c) tmem_ld32u(lane_base + o_col + col0 + 32 * c, o[c]);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int c = 0; c < kCols / 32; ++c)
+#pragma unroll
+              for (int u = 0; u < 32; ++u) o[c][u] = 0;
+          }
           const uint64_t a2 = f2_pack(fa, fa), b2 = f2_pack(fb, fb);
-          if (!use_a) {
 #pragma unroll
-            for (int u = 0; u < 32; ++u) o[u] = 0;
-          }
-#pragma unroll
-          for (int u = 0; u < 32; u += 2) {
-            float y0, y1;
-            f2_unpack(f2_mul(f2_pack(__uint_as_float(o[u]), __uint_as_float(o[u + 1])), a2), y0, y1);
-            o[u] = __float_as_uint(y0), o[u + 1] = __float_as_uint(y1);
-          }
-          if (use_b) {
+          for (int c = 0; c < kCols / 32; ++c)
 #pragma unroll
             for (int u = 0; u < 32; u += 2) {
               float y0, y1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(x[u]), __uint_as_float(x[u + 1])), b2,
-                               f2_pack(__uint_as_float(o[u]), __uint_as_float(o[u + 1]))), y0, y1);
-              o[u] = __float_as_uint(y0), o[u + 1] = __float_as_uint(y1);
+              f2_unpack(f2_mul(f2_pack(__uint_as_float(o[c][u]), __uint_as_float(o[c][u + 1])), a2),
+                        y0, y1);
+              o[c][u] = __float_as_uint(y0), o[c][u + 1] = __float_as_uint(y1);
+            }
+          if (use_b) {
+#pragma unroll
+            for (int c = 0; c < kCols / 32; ++c) {
+              uint32_t x[32];
+              tmem_ld32u(lane_base + T::out_col(1 - w) + col0 + 32 * c, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int u = 0; u < 32; u += 2) {
+                float y0, y1;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(x[u]), __uint_as_float(x[u + 1])), b2,
+                                 f2_pack(__uint_as_float(o[c][u]), __uint_as_float(o[c][u + 1]))),
+                          y0, y1);
+                o[c][u] = __float_as_uint(y0), o[c][u + 1] = __float_as_uint(y1);
+              }
             }
           }
-          // A cut item's rows go to the workspace as rows of 4 columns, 512
-          // contiguous bytes a store; a whole item's through shared memory, so
-          // that a store covers whole rows of the 32 x 32 block instead of 16
-          // bytes of each of 32 rows: 32 rows of 128 bytes, the 16-byte chunks of
-          // row r rotated by r.
-          uint4* part = reinterpret_cast<uint4*>(p.part_o) +
-                        (prow0 / kTrRows * (D / 4) + (col0 + c) / 4) * kTrRows + r;
-          if (whole) {
+        }
+        if (g + kCols == kAll) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bars + 8 * kTrEpi);
+        }
+        if (valid) {
+          if (!whole) {
+            // A cut item's rows go to the workspace in quads of columns, 512 contiguous
+            // bytes a store.  Slot 2c: the piece the CTA's range starts with, 2c + 1: the
+            // one it ends with.
+            const size_t tile = (size_t(blockIdx.x) * 2 + (k == 0 ? 0 : 1)) * TILES +
+                                (TILES == 2 ? w : 0);
+            uint4* to = reinterpret_cast<uint4*>(p.part_o) + (tile * (D / 4) + col0 / 4) * kTrRows + r;
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-              st_shared_u4(stage + lane * 128 + (((u + lane) & 7) << 4),
-                           make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]));
-          } else if (valid) {
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              part[u * kTrRows] = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+            for (int u = 0; u < kCols; u += 4)
+              to[u / 4 * kTrRows] = make_uint4(o[u / 32][u % 32], o[u / 32][u % 32 + 1],
+                                               o[u / 32][u % 32 + 2], o[u / 32][u % 32 + 3]);
+            if (col0 == 0) p.part_lse[tile * kTrRows + r] = lse;
           }
-          // non-finite V elements of nodes this row sees (rare)
+          // A whole item's rows go out as sectors of 32 bytes.
+          const size_t out0 = ((size_t(qs) + node) * p.q_heads + size_t(kvh) * G + r % G) * D + col0;
+          if (whole && p.out_bf16) {
+            __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + out0;
+#pragma unroll
+            for (int u = 0; u < kCols; u += 16) {
+              uint32_t y[8];
+#pragma unroll
+              for (int v = 0; v < 8; ++v)
+                y[v] = pack_bf16x2(__uint_as_float(o[u / 32][u % 32 + 2 * v]),
+                                   __uint_as_float(o[u / 32][u % 32 + 2 * v + 1]));
+              store_sector(to + u, y, p.out_wide);
+            }
+          } else if (whole) {
+            float* to = static_cast<float*>(p.out) + out0;
+#pragma unroll
+            for (int u = 0; u < kCols; u += 8) {
+              uint32_t y[8];
+#pragma unroll
+              for (int v = 0; v < 8; ++v) y[v] = o[u / 32][u % 32 + v];
+              store_sector(to + u, y, p.out_wide);
+            }
+          }
+          // Non-finite V elements of nodes this row sees (rare) are added to what was
+          // stored: the sum of a finite number and one of them is the same after its
+          // rounding to bf16.
           for (unsigned long long h = hit; h; h &= h - 1) {
             const int at = base + __ffsll(h) - 1;
             const int id = __ldg(p.block_tables + size_t(seq) * p.max_blocks_per_seq + at / 16);
-            const uint16_t* row = static_cast<const uint16_t*>(p.v_pool) + col0 + c +
+            const uint16_t* row = static_cast<const uint16_t*>(p.v_pool) + col0 +
                                   ((int64_t(id) * 16 + at % 16) * p.kv_heads + kvh) * D;
 #pragma unroll 1
-            for (int u = 0; u < 32; ++u) {
+            for (int u = 0; u < kCols; ++u) {
               const uint32_t v = row[u];
               if ((v & 0x7f80u) != 0x7f80u) continue;
-              float* y = whole ? reinterpret_cast<float*>(smem + (stage - sbase) + lane * 128 +
-                                                          ((((u >> 2) + lane) & 7) << 4))
-                               : reinterpret_cast<float*>(part + (u >> 2) * kTrRows);
-              y[u & 3] += __uint_as_float(v << 16);
+              const float add = __uint_as_float(v << 16);
+              if (!whole) {
+                const size_t tile = (size_t(blockIdx.x) * 2 + (k == 0 ? 0 : 1)) * TILES +
+                                    (TILES == 2 ? w : 0);
+                p.part_o[((tile * (D / 4) + (col0 + u) / 4) * kTrRows + r) * 4 + u % 4] += add;
+              } else if (p.out_bf16) {
+                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.out) + out0 + u;
+                *y = __float2bfloat16(__bfloat162float(*y) + add);
+              } else {
+                static_cast<float*>(p.out)[out0 + u] += add;
+              }
             }
           }
-          if (!whole) continue;
-          __syncwarp();
-          auto each = [&](auto store) {
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              if (u < stores)
-                store(ld_shared_u4((from ^ ((u & 1) << 6)) + u * 512),
-                      out0 + c + (4 * u / G) * node_stride + (4 * u % G) * D);
-          };
-          if (p.out_bf16)
-            each([&](const uint4& y, size_t at) {
-              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
-                  make_uint2(pack_bf16x2(__uint_as_float(y.x), __uint_as_float(y.y)),
-                             pack_bf16x2(__uint_as_float(y.z), __uint_as_float(y.w)));
-            });
-          else
-            each([&](const uint4& y, size_t at) {
-              *reinterpret_cast<uint4*>(static_cast<float*>(p.out) + at) = y;
-            });
-          __syncwarp();
         }
-        if (valid && !whole && col0 == 0) p.part_lse[prow0 + lane] = lse;
+        __syncwarp();
       }
-      fence_proxy_async_smem();  // the staging block is a V slot again
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * kTrEpi);
     }
     if (!ok && lane == 0) tr_abort(abort_flag);
   }
@@ -1210,6 +1225,7 @@ cudaError_t launch_paged_tree(const TreeArgs& a, const CUtensorMap* tq, const CU
   p.v_pool = a.v_cache;
   p.out = a.out;
   p.out_bf16 = a.out_bf16 ? 1 : 0;
+  p.out_wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
   p.part_o = a.part_o;
   p.part_lse = a.part_lse;
   p.start = static_cast<TreeStart*>(a.start);
