@@ -66,14 +66,12 @@ constexpr int kTrPieces = 5;  // piece descriptions in shared memory
 
 template <int D, int TILES>
 struct TreeSmem {
-  // Whether S, P and P V of a tile go in halves of 64 keys, so that a warpgroup
-  // weighs one half while the other's products and next scores run.  Pays
-  // where the tensor core waits for the softmax (one row tile, heads of 128),
-  // and costs where it does not: 64-key MMAs take more than half the time.
-  // Measured in halves / whole, us: 16 x 4096, 16 nodes 52.4 / 53.5, 64 x 700, 4
-  // nodes 56.3 / 61.6; 64 x 8192, 64 nodes (two row tiles) 926 / 865; 2 x 131072,
-  // 27 nodes, heads of 64 145 / 138.
-  static constexpr bool kHalves = D == 128 && TILES == 1;
+  // S, P and P V of a tile of heads of 128 go in two halves of 64 keys, so that
+  // the products of one half and the next scores run while the other half is
+  // weighed; heads of 64, with a third buffer, keep them whole.  Measured in
+  // halves / whole, us: 64 x 8192, 64 nodes 860 / 923, 16 x 4096, 16 nodes 50.8 / 52.2,
+  // 64 x 700, 4 nodes 48.5 / 52.5; heads of 64, 2 x 131072, 27 nodes 117 / 109.
+  static constexpr int kParts = D == 128 ? 2 : 1;
   // Tensor memory: S/P buffers that the products take in turn, and the
   // warpgroups' accumulators.  Heads of 128: a buffer and an accumulator of 128
   // columns a warpgroup.  Heads of 64 leave room for a third buffer, so that a
@@ -94,7 +92,7 @@ struct TreeSmem {
   static constexpr int kVOff = kKOff + kKStages * kTileBytes;
   static constexpr int kXchOff = kVOff + kVStages * kTileBytes;  // [2][128] (max, sum)
   static constexpr int kBarOff = kXchOff + 2 * kTrRows * 8;
-  static constexpr int kNumBars = 2 + 4 * kTrMaxStages + 12 + 3 + kTrPieces;
+  static constexpr int kNumBars = 2 + 4 * kTrMaxStages + 18 + 3 + kTrPieces;
   static constexpr int kMiscOff = kBarOff + kNumBars * 8;
   // tensor-memory base, abort flag; non-finite nodes [2] (64 bit); scan [12];
   // the start of the range; the pieces
@@ -108,9 +106,9 @@ enum TrBar {
   kTrQFull = 0, kTrQEmpty = 1,
   kTrKFull = 2, kTrKEmpty = kTrKFull + kTrMaxStages,
   kTrVFull = kTrKEmpty + kTrMaxStages, kTrVEmpty = kTrVFull + kTrMaxStages,
-  // by buffer, or by half 2 h + w: first and second 64 keys of warpgroup w's tile
-  kTrSFull = kTrVEmpty + kTrMaxStages, kTrPFull = kTrSFull + 4, kTrDone = kTrPFull + 4,
-  kTrXch = kTrDone + 4, kTrEpi = kTrXch + 1, kTrDrain = kTrEpi + 1, kTrPiece0 = kTrDrain + 1
+  // by half of the tile's keys and buffer: 3 h + b
+  kTrSFull = kTrVEmpty + kTrMaxStages, kTrPFull = kTrSFull + 6, kTrDone = kTrPFull + 6,
+  kTrXch = kTrDone + 6, kTrEpi = kTrXch + 1, kTrDrain = kTrEpi + 1, kTrPiece0 = kTrDrain + 1
 };
 
 // Where a CTA's range starts, for the merge: sequence (-1: no work), item of
@@ -253,6 +251,17 @@ __device__ __forceinline__ void st_shared_u4(uint32_t addr, const uint4& v) {
                "r"(v.z), "r"(v.w) : "memory");
 }
 
+// The lane of a converged warp that issues its MMAs (always the same one).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
 // The bits 15 and 31 of the halves of a bf16 pair that are NaN or infinite.
 __device__ __forceinline__ uint32_t nonfinite_bf16x2(uint32_t w) {
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
@@ -310,7 +319,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
                   const __grid_constant__ CUtensorMap tmap_v, const TreeParams p) {
   using T = TreeSmem<D, TILES>;
   constexpr int TPT = kTrRows / G;  // tree nodes per row tile
-  constexpr int kParts = T::kHalves ? 2 : 1;
+  constexpr int kParts = T::kParts;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + T::kBarOff;
@@ -343,7 +352,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       mbar_init(bars + 8 * (kTrVFull + s), 1);
       mbar_init(bars + 8 * (kTrVEmpty + s), 1);
     }
-    for (int h = 0; h < 4; ++h) {
+    for (int h = 0; h < 6; ++h) {
       mbar_init(bars + 8 * (kTrSFull + h), 1);
       mbar_init(bars + 8 * (kTrPFull + h), 4);
       mbar_init(bars + 8 * (kTrDone + h), 1);
@@ -557,39 +566,45 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
     __syncwarp();
   } else if (warp == kTrSWarp) {
-    // ================= Q, and the products S = Q K^T (one thread) =================
-    // S and P V are issued by two threads, so that one's waits and the other's
-    // MMAs overlap: a thread's MMAs are taken at the tensor core's pace.
-    if (lane == 0) {
-      constexpr uint32_t kIdesc = idesc_bf16_f32(128, kTrKeys / kParts, 0, 0);
-      auto wait = [&](int bar, uint32_t parity) {
-        return tr_wait(bars + 8 * bar, parity, abort_flag);
-      };
-      int i = 0, k = 0;
-      bool ok = true;
-      // The pieces are worked out here, ahead of those who need them.  Slot k
-      // is free: the last S product needed a P V of piece k - 4 or later, whose
-      // first one needed everybody to be through with piece k - 5.
-      auto publish = [&](bool some) {
-        volatile TreePiece* t = pieces + k % kTrPieces;
-        if (some) {
-          t->qs = walk.seq.qs;
-          t->n = walk.seq.n;
-          t->ctx = walk.seq.ctx;
-          t->seq = walk.s;
-          t->kvh = walk.kv_head();
-          t->node0 = walk.group() * TILES * TPT;
-          t->first = walk.first;
-        }
+    // ================= Q, and the products S = Q K^T =================
+    // S and P V are issued by two warps, so that one's waits and the other's
+    // MMAs overlap.  Each runs as a whole warp and elects a lane for the MMAs:
+    // descriptors are then values of the warp.  From a branch on the lane number
+    // an MMA took 75-90 cycles to issue, more than it runs for with heads of 64
+    // (2 x 131072, 27 nodes: 128 us against 110).
+    constexpr uint32_t kIdesc = idesc_bf16_f32(128, kTrKeys / kParts, 0, 0);
+    auto wait = [&](int bar, uint32_t parity) {
+      return bool(__all_sync(0xffffffffu, tr_wait(bars + 8 * bar, parity, abort_flag)));
+    };
+    int i = 0, k = 0;
+    bool ok = true;
+    // The pieces are worked out here, ahead of those who need them.  Slot k
+    // is free: the last S product needed a P V of piece k - 4 or later, whose
+    // first one needed everybody to be through with piece k - 5.
+    auto publish = [&](bool some) {
+      volatile TreePiece* t = pieces + k % kTrPieces;
+      if (some && lane == 0) {
+        t->qs = walk.seq.qs;
+        t->n = walk.seq.n;
+        t->ctx = walk.seq.ctx;
+        t->seq = walk.s;
+        t->kvh = walk.kv_head();
+        t->node0 = walk.group() * TILES * TPT;
+        t->first = walk.first;
+      }
+      if (lane == 0) {
         t->tiles = some ? (walk.whole() ? -walk.tiles : walk.tiles) : 0;
         mbar_arrive(bars + 8 * (kTrPiece0 + k % kTrPieces));
-      };
-      for (; ok; ++k) {
-        const bool some = walk.next();
-        publish(some);
-        if (!some) break;
-        ok = k == 0 || wait(kTrQEmpty, (k - 1) & 1);
-        if (!ok) break;
+      }
+      __syncwarp();
+    };
+    for (; ok; ++k) {
+      const bool some = walk.next();
+      publish(some);
+      if (!some) break;
+      ok = k == 0 || wait(kTrQEmpty, (k - 1) & 1);
+      if (!ok) break;
+      if (lane == 0) {
         mbar_arrive_expect_tx(bars + 8 * kTrQFull, T::kQBytes);
         const int tok = walk.seq.qs + walk.group() * TILES * TPT;
 #pragma unroll
@@ -598,85 +613,91 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
           for (int h = 0; h < D / 64; ++h)
             tma_load_3d(sbase + t * T::kTileBytes + h * T::kHalf, &tmap_q, bars + 8 * kTrQFull,
                         h * 64, walk.kv_head() * G, tok + t * TPT);
-        ok = wait(kTrQFull, k & 1);
+      }
+      __syncwarp();
+      ok = wait(kTrQFull, k & 1);
 #pragma unroll 1
-        for (int j = 0; ok && j < walk.tiles; ++j, ++i) {
-          ok = wait(kTrKFull + i % T::kKStages, (i / T::kKStages) & 1);
-          // a part's columns are free once the products that read its P are done
+      for (int j = 0; ok && j < walk.tiles; ++j, ++i) {
+        ok = wait(kTrKFull + i % T::kKStages, (i / T::kKStages) & 1);
+        // a part's columns are free once the products that read its P are done
 #pragma unroll 1
-          for (int th = 0; ok && th < kParts * TILES; ++th) {
-            const int t = th / kParts, h = th % kParts, job = i * TILES + t;
-            const int b = job % T::kBufs, before = job / T::kBufs - 1;
-            ok = before < 0 || wait(kTrDone + 2 * h + b, before & 1);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t q_smem = sbase + t * T::kTileBytes;
-            const uint32_t k_smem =
-                sbase + T::kKOff + (i % T::kKStages) * T::kTileBytes + h * 64 * 128;
+        for (int th = 0; ok && th < kParts * TILES; ++th) {
+          const int t = th / kParts, h = th % kParts, job = i * TILES + t;
+          const int b = job % T::kBufs, before = job / T::kBufs - 1;
+          ok = before < 0 || wait(kTrDone + 3 * h + b, before & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t q_smem = sbase + t * T::kTileBytes;
+          const uint32_t k_smem =
+              sbase + T::kKOff + (i % T::kKStages) * T::kTileBytes + h * 64 * 128;
+          if (elect_lane()) {
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
               const uint32_t off = (c >> 2) * T::kHalf + (c & 3) * 32;
               umma_bf16(tmem + T::buf_col(b) + h * 64, smem_desc_sw128(q_smem + off, 16, 1024),
                         smem_desc_sw128(k_smem + off, 16, 1024), kIdesc, c > 0);
             }
-            umma_commit(bars + 8 * (kTrSFull + 2 * h + b));
+            umma_commit(bars + 8 * (kTrSFull + 3 * h + b));
           }
+        }
+        if (elect_lane()) {
           umma_commit(bars + 8 * (kTrKEmpty + i % T::kKStages));
           if (j + 1 == walk.tiles) umma_commit(bars + 8 * kTrQEmpty);
         }
       }
-      if (!ok) tr_abort(abort_flag);
-      // every MMA issued has completed, and Q has landed, before the CTA exits
-      umma_commit(bars + 8 * kTrDrain);
-      (void)mbar_wait_bounded(bars + 8 * kTrDrain, 0);
-      if (!ok && k > 0) (void)mbar_wait_bounded(bars + 8 * kTrQFull, (k - 1) & 1);
     }
+    if (!ok && lane == 0) tr_abort(abort_flag);
+    // every MMA issued has completed, and Q has landed, before the CTA exits
+    if (elect_lane()) umma_commit(bars + 8 * kTrDrain);
+    (void)mbar_wait_bounded(bars + 8 * kTrDrain, 0);
+    if (!ok && k > 0) (void)mbar_wait_bounded(bars + 8 * kTrQFull, (k - 1) & 1);
     __syncwarp();
   } else {
-    // ================= the products O += P V (one thread) =================
-    if (lane == 0) {
-      constexpr uint32_t kIdesc = idesc_bf16_f32(128, D, 0, 1);
-      auto wait = [&](int bar, uint32_t parity) {
-        return tr_wait(bars + 8 * bar, parity, abort_flag);
-      };
-      int i = 0;
-      bool ok = true;
-      int k = 0;
-      for (; ok; ++k) {
-        ok = wait(kTrPiece0 + k % kTrPieces, (k / kTrPieces) & 1);
-        const int tiles = ok ? abs(pieces[k % kTrPieces].tiles) : 0;
-        if (tiles == 0) break;
-        if (k > 0) ok = wait(kTrEpi, (k - 1) & 1);  // the accumulators have been read
+    // ================= the products O += P V =================
+    constexpr uint32_t kIdesc = idesc_bf16_f32(128, D, 0, 1);
+    auto wait = [&](int bar, uint32_t parity) {
+      return bool(__all_sync(0xffffffffu, tr_wait(bars + 8 * bar, parity, abort_flag)));
+    };
+    int i = 0;
+    bool ok = true;
+    int k = 0;
+    for (; ok; ++k) {
+      ok = wait(kTrPiece0 + k % kTrPieces, (k / kTrPieces) & 1);
+      const int tiles = ok ? abs(pieces[k % kTrPieces].tiles) : 0;
+      if (tiles == 0) break;
+      if (k > 0) ok = wait(kTrEpi, (k - 1) & 1);  // the accumulators have been read
 #pragma unroll 1
-        for (int j = 0; ok && j < tiles; ++j, ++i) {
-          const bool fresh = j < (TILES == 1 ? 2 : 1);  // the accumulator's first tile of the piece
-          ok = wait(kTrVFull + i % T::kVStages, (i / T::kVStages) & 1);
-          const uint32_t v_smem = sbase + T::kVOff + (i % T::kVStages) * T::kTileBytes;
+      for (int j = 0; ok && j < tiles; ++j, ++i) {
+        const bool fresh = j < (TILES == 1 ? 2 : 1);  // the accumulator's first tile of the piece
+        ok = wait(kTrVFull + i % T::kVStages, (i / T::kVStages) & 1);
+        const uint32_t v_smem = sbase + T::kVOff + (i % T::kVStages) * T::kTileBytes;
 #pragma unroll 1
-          for (int th = 0; ok && th < kParts * TILES; ++th) {
-            const int t = th / kParts, h = th % kParts, job = i * TILES + t;
-            const int b = job % T::kBufs;
-            ok = wait(kTrPFull + 2 * h + b, (job / T::kBufs) & 1);
-            if (!ok) break;
-            tc_fence_after();
+        for (int th = 0; ok && th < kParts * TILES; ++th) {
+          const int t = th / kParts, h = th % kParts, job = i * TILES + t;
+          const int b = job % T::kBufs;
+          ok = wait(kTrPFull + 3 * h + b, (job / T::kBufs) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_lane()) {
 #pragma unroll
             for (int c = 0; c < kTrKeys / 16 / kParts; ++c) {
               const uint64_t vdesc = smem_desc_sw128(v_smem + (4 * h + c) * 2048, T::kHalf, 1024);
-              const uint32_t a_hi = tmem + T::buf_col(b) + 64 * h + 16 * c;  // hi, and lo 8 columns on
+              // hi, and lo 8 columns on
+              const uint32_t a_hi = tmem + T::buf_col(b) + 64 * h + 16 * c;
               umma_bf16_ts(tmem + T::out_col(job & 1), a_hi, vdesc, kIdesc,
                            (!fresh || h > 0 || c > 0) ? 1u : 0u);
               umma_bf16_ts(tmem + T::out_col(job & 1), a_hi + 8, vdesc, kIdesc, 1u);
             }
-            umma_commit(bars + 8 * (kTrDone + 2 * h + b));
+            umma_commit(bars + 8 * (kTrDone + 3 * h + b));
           }
-          if (!ok) break;
-          umma_commit(bars + 8 * (kTrVEmpty + i % T::kVStages));
         }
+        if (!ok) break;
+        if (elect_lane()) umma_commit(bars + 8 * (kTrVEmpty + i % T::kVStages));
       }
-      if (!ok) tr_abort(abort_flag);
-      umma_commit(bars + 8 * kTrDrain);
-      (void)mbar_wait_bounded(bars + 8 * kTrDrain, 0);
     }
+    if (!ok && lane == 0) tr_abort(abort_flag);
+    if (elect_lane()) umma_commit(bars + 8 * kTrDrain);
+    (void)mbar_wait_bounded(bars + 8 * kTrDrain, 0);
     __syncwarp();
   }
   } else {
@@ -749,9 +770,10 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
 #pragma unroll 1
         for (int c = 0; c < kTrKeys; c += 64) {  // the halves of the tile
-          const int part = T::kHalves ? (c >> 5) + b : b;
-          if (T::kHalves || c == 0) {
-            ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * (kTrSFull + part), ph & 1, abort_flag));
+          const int h = c >> 6;
+          if (kParts == 2 || h == 0) {
+            ok = __all_sync(0xffffffffu,
+                            tr_wait(bars + 8 * (kTrSFull + 3 * h + b), ph & 1, abort_flag));
             if (!ok) break;
             tc_fence_after();
           }
@@ -796,14 +818,14 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 const bool move = mx > m + kTrRescale || (m == -INFINITY && mx > m);
                 if (__any_sync(0xffffffffu, move)) {
                   const float alpha = move ? ex2(m - mx) : 1.f;  // 0 when m is -inf
-                  if (seen > 0 || (T::kHalves && c > 0)) {
+                  if (seen > 0 || (kParts == 2 && h > 0)) {
                     // the accumulator's last products must be done before it is scaled
+                    const bool own = kParts == 2 && h > 0;  // of the tile's first half
+                    const int of = own ? job : job - 2;
                     ok = __all_sync(0xffffffffu,
-                                    T::kHalves
-                                        ? tr_wait(bars + 8 * (kTrDone + 2 * (c == 0) + w),
-                                                  (c == 0 ? ph - 1 : ph) & 1, abort_flag)
-                                        : tr_wait(bars + 8 * (kTrDone + (job - 2) % T::kBufs),
-                                                  ((job - 2) / T::kBufs) & 1, abort_flag));
+                                    tr_wait(bars + 8 * (kTrDone + (own ? 0 : 3 * (kParts - 1)) +
+                                                        of % T::kBufs),
+                                            (of / T::kBufs) & 1, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t a2 = f2_pack(alpha, alpha);
@@ -821,7 +843,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
                       tmem_st32u(lane_base + o_col + cc, va);
                     }
                   }
-                  if (!T::kHalves && c > 0) {  // so is the P of the first half, still unused
+                  if (kParts == 1 && h > 0) {  // so is the P of the first half, still unused
                     tmem_wait_st();
 #pragma unroll 1
                     for (int cc = 0; cc < 64; cc += 32) {
@@ -866,11 +888,11 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
             tmem_st32u(lane_base + s_col + c, va);
             tmem_st32u(lane_base + s_col + c + 32, vb);
           }
-          if (T::kHalves || c > 0) {
+          if (kParts == 2 || h > 0) {
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars + 8 * (kTrPFull + part));
+            if (lane == 0) mbar_arrive(bars + 8 * (kTrPFull + 3 * (kParts - 1 ? h : 0) + b));
           }
         }
         if (!ok) break;
@@ -899,7 +921,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (lt < begin_tile) continue;
         const int job = TILES == 1 ? lt : 2 * lt + a;
         ok = __all_sync(0xffffffffu,
-                        tr_wait(bars + 8 * (kTrDone + 2 * (kParts - 1) + job % T::kBufs),
+                        tr_wait(bars + 8 * (kTrDone + 3 * (kParts - 1) + job % T::kBufs),
                                 (job / T::kBufs) & 1, abort_flag));
         if (!ok) break;
       }
@@ -938,7 +960,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
           // an accumulator that no tile of the piece went to holds anything
           if (use_a) {
 #pragma unroll
-            for (int c = 0; c < kCols / 32; ++c) tmem_ld32u(lane_base + o_col + col0 + 32 * c, o[c]);
+            for (int c = 0; c < kCols / 32; ++c)
+              tmem_ld32u(lane_base + o_col + col0 + 32 * c, o[c]);
             tmem_wait_ld();
           } else {
 #pragma unroll
@@ -985,7 +1008,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
             // one it ends with.
             const size_t tile = (size_t(blockIdx.x) * 2 + (k == 0 ? 0 : 1)) * TILES +
                                 (TILES == 2 ? w : 0);
-            uint4* to = reinterpret_cast<uint4*>(p.part_o) + (tile * (D / 4) + col0 / 4) * kTrRows + r;
+            uint4* to =
+                reinterpret_cast<uint4*>(p.part_o) + (tile * (D / 4) + col0 / 4) * kTrRows + r;
 #pragma unroll
             for (int u = 0; u < kCols; u += 4)
               to[u / 4 * kTrRows] = make_uint4(o[u / 32][u % 32], o[u / 32][u % 32 + 1],
@@ -993,7 +1017,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
             if (col0 == 0) p.part_lse[tile * kTrRows + r] = lse;
           }
           // A whole item's rows go out as sectors of 32 bytes.
-          const size_t out0 = ((size_t(qs) + node) * p.q_heads + size_t(kvh) * G + r % G) * D + col0;
+          const size_t out0 =
+              ((size_t(qs) + node) * p.q_heads + size_t(kvh) * G + r % G) * D + col0;
           if (whole && p.out_bf16) {
             __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + out0;
 #pragma unroll
