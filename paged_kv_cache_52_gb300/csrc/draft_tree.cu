@@ -17,7 +17,8 @@ constexpr int kPageTokens = 16;
 
 // mask[t] = bit t | mask[parent], position = L - n + depth, depth = bits - 1.
 // One CTA per sequence, one thread per node; six doublings of the ancestor
-// pointers reach 64 nodes up.  20 bytes a node: bound by the launch.
+// pointers reach 64 nodes up.  20 bytes a node: bound by the launch (256 trees of
+// 16 nodes: 1.6 us in a graph).
 __global__ void __launch_bounds__(kTreeMaxNodes)
 tree_layout_kernel(const int32_t* __restrict__ parents, const int32_t* __restrict__ q_start,
                    int total_q, int max_q_len, const int32_t* __restrict__ context_lens,
@@ -68,7 +69,8 @@ tree_layout_kernel(const int32_t* __restrict__ parents, const int32_t* __restric
 // column of the rows and moves it in order of i, kMoveBatch loads ahead of
 // their stores.  Row i is a source only of moves j <= i, so each column is
 // read before it is overwritten.  A move of a row onto itself is skipped.
-// Bound by memory for a batch over all layers, by the launch for one layer.
+// Bound by memory for a batch over all layers (64 sequences x 32 layers, FP8:
+// 5.9 us in a graph, the bytes' 4.4), by the launch for few sequences (2.4 us).
 constexpr int kMoveThreads = 128;
 constexpr int kMoveBatch = 8;
 

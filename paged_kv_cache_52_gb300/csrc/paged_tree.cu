@@ -17,20 +17,18 @@
 //  * the work is cut by key tiles, not by sequences: the tiles of all items
 //    (pair, row group) laid end to end are divided evenly over one CTA per
 //    SM, so a batch of ragged contexts, or one long one, loads every SM
-//    alike.  A CTA's range covers parts of one or more items; an item that
-//    lies in one CTA is finished there, the pieces of a cut item (at most two
-//    per CTA) go through the workspace and a merge kernel by log-sum-exp.
-//  * TILES = 1 (at most 128 rows a pair): bound by HBM.  The two softmax
-//    warpgroups take the key tiles in turn, each with its own running max,
-//    sum and tensor-memory accumulator, so one works on its scores while the
-//    other's products run; at the end of an item each row's two halves are
-//    combined, both warpgroups reading both accumulators (half the columns
-//    each).  TILES = 2: bound by the tensor cores; warpgroup t owns row tile
-//    t and K/V tiles serve both.
+//    alike.  An item that lies in one CTA is finished there, the pieces of a
+//    cut item (at most two per CTA) go through the workspace and a merge
+//    kernel by log-sum-exp.
+//  * TILES = 1 (at most 128 rows a pair): the two softmax warpgroups take the
+//    key tiles in turn, each with its own running max, sum and tensor-memory
+//    accumulator; at the end of an item each row's two halves are combined,
+//    both warpgroups reading both accumulators (half the columns each).
+//    TILES = 2: warpgroup t owns row tile t and K/V tiles serve both.
 //  * warps 0-3 and 4-7 softmax, correction and epilogue (thread = row =
-//    tensor-memory lane), warp 8 loads K, 9 loads Q and issues Q K^T, 10 loads
-//    V, 11 issues P V.  The rings run on across items; only Q and the
-//    accumulators change hands at an item's end.
+//    tensor-memory lane), warp 8 loads K, 9 loads Q, works out the pieces and
+//    issues Q K^T, 10 loads V, 11 issues P V.  The rings run on across items;
+//    only Q and the accumulators change hands at an item's end.
 //  * S = Q K^T lands in tensor memory, the softmax overwrites it with P as
 //    bf16 hi + lo (two MMAs a step, error ~2^-17: a row may see very few
 //    keys, where P rounded to one bf16 would move the output by 2^-9), and
@@ -42,6 +40,23 @@
 //    so a sibling's (or a stale row's) NaN or infinity reaches nobody else.
 //  * every wait is bounded; a timeout sets the error word and an abort flag,
 //    copies and MMAs in flight are drained and tensor memory is freed.
+//
+// What bounds it (us in a graph, 64 query and 8 KV heads of 128 unless said):
+//  * 16 x 4096, 16 nodes: 51.  HBM in the middle (64 KB per SM in 2730 cycles =
+//    7 TB/s); 31 of them are the bytes.  The rest are the ends: 2.3 until the
+//    first pages are asked for, 3 until they are there, pieces that meet in a CTA
+//    (2-3 each), 4.5 for the merge.
+//  * 64 x 8192, 64 nodes (two row tiles): 870, the tensor cores' 585 with P as
+//    hi + lo.  A row tile's chain of scores, softmax and products, 4300 cycles a
+//    key tile for both against 3072 of MMAs at full rate: the softmax's two
+//    halves (1300 cycles each), and MMAs that run at 48-75 cycles where N = 64
+//    would need 32.
+//  * 2 x 131072, 27 nodes, 32 query heads of 64: 110 of 79 for the bytes; 16 MMAs of
+//    P V a tile with P from tensor memory take about as long with heads of 64
+//    as with 128.
+//  * 1 x 500, 8 nodes: 12, all latency: 1.3 for the split, 1.7 to the first page,
+//    2.7 for one tile of each warpgroup, 2.5 for its end, 0.8 + 2.8 for the
+//    merge.
 #include <algorithm>
 
 #include "pkv_device.cuh"
@@ -60,8 +75,14 @@ constexpr int kTrKWarp = 8, kTrSWarp = 9, kTrVWarp = 10;  // 11 issues P V
 constexpr uint32_t kTrTmemCols = 512;
 constexpr float kTrRescale = 8.0f;     // log2 units: move the running max when it grows by > x256
 constexpr int kTrMaxStages = 4;
-constexpr int kTrMinTiles = 2;  // one for each softmax warpgroup
-constexpr int kTrSlack = 2;     // key tiles that a second piece costs a CTA
+// The fewest key tiles worth a piece: one for each softmax warpgroup (1 x 2000,
+// 16 nodes: 18.1 us, with 1 tile 22.1).
+constexpr int kTrMinTiles = 2;
+// Key tiles' time that a second piece costs a CTA: the first one's end and the
+// next one's start.  us with 2 / 1 / 4: 8 x 2000, 8 nodes 25.6 / 26.9 / 25.7, 64 x 700,
+// 4 nodes 58.1 / 58.7 / 58.0, 64 x 8192, 64 nodes 880 / 890 / 882 (without: 894),
+// 1 x 500 13.5 / 13.5 / 14.2.
+constexpr int kTrSlack = 2;
 constexpr int kTrPieces = 5;  // piece descriptions in shared memory
 
 template <int D, int TILES>

@@ -196,3 +196,49 @@ def test_refusals(pk):
     empty = call(q=a["q"][:0], k=a["k"][:0], v=a["v"][:0], positions=a["positions"][:0],
                  slot_mapping=a["slots"][:0])
     assert empty.shape == (0, 4, 64)
+
+
+def test_replay_side_stream_and_two_calls_at_once(pk):
+    # two appends on two streams into their own pools, and one captured and
+    # replayed with other tokens, give what plain calls give
+    calls = []
+    for seed in (1, 2):
+        a = _inputs(150, 8, 2, 128, 64, seed=seed)
+        pools = [torch.zeros(a["blocks"], 16, 2, 128, dtype=torch.bfloat16, device=DEV)
+                 for _ in range(2)]
+        calls.append((a, pools))
+
+    def run(a, pools):
+        return pk.qk_norm_rope_append(a["q"], a["k"], a["v"], a["positions"], a["table"],
+                                      a["slots"], *pools, a["qw"], a["kw"], 1e-6)
+
+    want = []
+    for a, pools in calls:
+        out = run(a, pools)
+        torch.cuda.synchronize()
+        want.append([out.clone()] + [p.clone() for p in pools])
+        for p in pools:
+            p.zero_()
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = []
+    for (a, pools), s in zip(calls, streams):
+        with torch.cuda.stream(s):
+            got.append([run(a, pools)] + pools)
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(g, w))
+    # captured with the first call's tensors, replayed with the second's contents
+    a, pools = calls[0]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(a, pools)
+    b = calls[1][0]
+    for name in ("q", "k", "v", "positions", "table", "slots", "qw", "kw"):
+        a[name].copy_(b[name])
+    for p in pools:
+        p.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip([out] + pools, want[1]))
+    assert pk.get_device_error(clear=True) == 0

@@ -341,3 +341,54 @@ def test_layout_flags_bad_parents_and_ranges(pk):
     torch.cuda.synchronize()
     assert pk.get_device_error(clear=True) == 0x410
     assert masks.tolist() == [1, 2, 5, 8, 55, 55] and pos.tolist() == [5, 5, 6, 5, 55, 55]
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(6, 3, 64), (5, 5, 128), (12, 6, 128), (28, 7, 64),
+                                      (32, 32, 128), (48, 3, 64)])
+def test_head_counts_that_share_the_grid_unevenly(pk, hq, hkv, d):
+    b = Batch(hq, hkv, d, [33, 1, 64], [2100, 5000, 700], seed=hkv)
+    check(b, b.run(pk), f"{hq}/{hkv}")
+    assert pk.get_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(16, 2, 128), (8, 1, 64), (4, 4, 128)])
+def test_many_sequences_with_little_and_with_uneven_work(pk, hq, hkv, d):
+    # more sequences than the short split takes: empty ones, single tiles, and
+    # two long ones between them that are cut over many SMs
+    n = [i % 3 for i in range(45)]
+    lens = [max(m, (i * 37) % 100) for i, m in enumerate(n)]
+    few = Batch(hq, hkv, d, n, lens, seed=hq)
+    check(few, few.run(pk), "little")
+    n[20], lens[20], n[31], lens[31] = 64, 9000, 17, 4001
+    uneven = Batch(hq, hkv, d, n, lens, seed=hq)
+    check(uneven, uneven.run(pk), "uneven")
+    assert pk.get_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("hq,nodes,lens", [(8, [9, 3], [100, 60]), (32, [64, 20], [300, 5000])])
+def test_output_that_starts_between_32_byte_borders(pk, dtype, hq, nodes, lens):
+    b = Batch(hq, 2, 128, nodes, lens, seed=20)
+    want = b.run(pk, out_dtype=dtype)
+    shift = 16 // want.element_size()
+    flat = torch.full((want.numel() + 2 * shift,), 7.0, dtype=dtype, device=DEV)
+    out = flat[shift:-shift].view(want.shape)
+    assert out.data_ptr() % 32 == 16
+    pk.paged_tree_attention(**b.dev(), max_q_len=max(nodes), out=out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    assert (flat[:shift] == 7).all() and (flat[-shift:] == 7).all()
+
+
+@pytest.mark.parametrize("lens", [[300, 40], [9000, 5000]])
+def test_rounded_output_with_visible_infinities_and_nan(pk, lens):
+    # whole and cut items: what a non-finite V element makes of a row rounds to itself
+    b = Batch(16, 2, 128, [40, 20], lens, seed=21)
+    for s, node, col, value in [(0, 0, 3, np.inf), (0, 7, 3, -np.inf), (0, 7, 90, -np.inf),
+                                (0, 30, 127, np.nan), (1, 0, 64, np.inf)]:
+        blk, row = b.slot(s, b.lens[s] - b.n[s] + node)
+        b.v[blk, row, 1, col] = value
+    full, rounded = b.run(pk), b.run(pk, out_dtype=torch.bfloat16)
+    assert not full.isfinite().all()
+    assert torch.equal(full.bfloat16().nan_to_num(3e38), rounded.nan_to_num(3e38))
+    assert torch.equal(full.isnan(), rounded.isnan())
