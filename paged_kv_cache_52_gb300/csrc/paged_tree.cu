@@ -48,9 +48,9 @@
 //    (2-3 each), 4.5 for the merge.
 //  * 64 x 8192, 64 nodes (two row tiles): 870, the tensor cores' 585 with P as
 //    hi + lo.  A row tile's chain of scores, softmax and products, 4300 cycles a
-//    key tile for both against 3072 of MMAs at full rate: the softmax's two
-//    halves (1300 cycles each), and MMAs that run at 48-75 cycles where N = 64
-//    would need 32.
+//    key tile for both, 1.4 times the MMAs at their full rate: the softmax's
+//    two halves (1300 cycles each), and MMAs that run at 48-75 cycles where
+//    N = 64 would need 32.
 //  * 2 x 131072, 27 nodes, 32 query heads of 64: 110 of 79 for the bytes; 16 MMAs of
 //    P V a tile with P from tensor memory take about as long with heads of 64
 //    as with 128.
