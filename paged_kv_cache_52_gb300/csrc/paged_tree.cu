@@ -75,8 +75,8 @@ constexpr int kTrKWarp = 8, kTrSWarp = 9, kTrVWarp = 10;  // 11 issues P V
 constexpr uint32_t kTrTmemCols = 512;
 constexpr float kTrRescale = 8.0f;     // log2 units: move the running max when it grows by > x256
 constexpr int kTrMaxStages = 4;
-// The fewest key tiles worth a piece: one for each softmax warpgroup (1 x 2000,
-// 16 nodes: 18.1 us, with 1 tile 22.1).
+// The fewest key tiles worth a piece: one for each softmax warpgroup (us with 2 / 1:
+// 1 x 2000, 16 nodes 18.1 / 22.1; three tiles whole / cut 11.45 / 11.9).
 constexpr int kTrMinTiles = 2;
 // Key tiles' time that a second piece costs a CTA: the first one's end and the
 // next one's start.  us with 2 / 1 / 4: 8 x 2000, 8 nodes 25.6 / 26.9 / 25.7, 64 x 700,
@@ -437,7 +437,8 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
     // kTrSlack tiles above the even share, one piece a CTA, if there are CTAs
     // enough.
     const int longest = max(kTrMinTiles, tiles / ctas + kTrSlack);
-    const int cuts = items ? (q.tiles + longest - 1) / longest : 0;
+    const int cuts =
+        items ? max(1, min((q.tiles + longest - 1) / longest, q.tiles / kTrMinTiles)) : 0;
     const bool alone = __reduce_add_sync(0xffffffffu, items * cuts) <= ctas;
     const int width = alone ? items * cuts : q.places(heads);
     const int end = warp_scan(width);
