@@ -79,9 +79,10 @@ constexpr int kTrMaxStages = 4;
 // 1 x 2000, 16 nodes 18.1 / 22.1; three tiles whole / cut 11.45 / 11.9).
 constexpr int kTrMinTiles = 2;
 // Key tiles' time that a second piece costs a CTA: the first one's end and the
-// next one's start.  us with 2 / 1 / 4: 8 x 2000, 8 nodes 25.6 / 26.9 / 25.7, 64 x 700,
-// 4 nodes 58.1 / 58.7 / 58.0, 64 x 8192, 64 nodes 880 / 890 / 882 (without: 894),
-// 1 x 500 13.5 / 13.5 / 14.2.
+// next one's start.  us with 1 / 2 / 3: 8 x 2000, 8 nodes 25.6 / 24.1 / 24.1, 64 x 700,
+// 4 nodes 49.2 / 48.6 / 49.7, 32 x 1000, 16 nodes 41.4 / 41.5 / 42.3, 16 x 4096, 16
+// nodes 50.4 / 50.9 / 49.5, 64 x 8192, 64 nodes 844 / 845 / 840 (without places for it
+// in the even split 1.6% more).
 constexpr int kTrSlack = 2;
 constexpr int kTrPieces = 5;  // piece descriptions in shared memory
 
