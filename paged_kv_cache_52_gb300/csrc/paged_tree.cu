@@ -747,11 +747,11 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const bool valid = node < n;
       const bool warp_valid = __any_sync(0xffffffffu, valid);
       const int base = ctx - n;  // committed keys
-      unsigned long long mask = 0;
-      if (valid) {
-        mask = __ldg(p.tree_mask + piece->qs + node);
-        if (n < 64) mask &= (1ull << n) - 1ull;
-      }
+      // as loaded: cut to the nodes where it is used, so that nobody waits for it here
+      const unsigned long long raw_mask =
+          __ldg(p.tree_mask + piece->qs + (valid ? node : n - 1));
+      const unsigned long long nodes =
+          !valid ? 0ull : n < 64 ? (1ull << n) - 1ull : ~0ull;
       float m = -INFINITY, l = 0.f;
       int seen = 0;  // tiles of the piece this warpgroup has taken
       for (int j = 0; j < tiles; ++j) {
@@ -807,7 +807,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
               const uint32_t hide = __float_as_uint(neg ? INFINITY : -INFINITY);
 #pragma unroll 1
               for (int cc = c; cc < c + 64; cc += 32) {
-                const uint32_t bits = key_bits(mask, key0 + cc - base);
+                const uint32_t bits = key_bits(raw_mask & nodes, key0 + cc - base);
                 tmem_ld32u(lane_base + s_col + cc, va);
                 tmem_wait_ld();
 #pragma unroll
@@ -972,7 +972,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
       constexpr int kAll = TILES == 1 ? D / 2 : D, kCols = kAll < 64 ? kAll : 64;
       const int qs = piece->qs, seq = piece->seq, kvh = piece->kvh;
       const bool whole = piece->tiles < 0;
-      const unsigned long long hit = mask & nonfinite[k & 1];
+      const unsigned long long hit = raw_mask & nodes & nonfinite[k & 1];
       const bool use_a = __any_sync(0xffffffffu, fa != 0.f);
       const bool use_b = TILES == 1 && __any_sync(0xffffffffu, fb != 0.f);
 #pragma unroll 1
