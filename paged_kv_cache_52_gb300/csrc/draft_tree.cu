@@ -70,7 +70,7 @@ tree_layout_kernel(const int32_t* __restrict__ parents, const int32_t* __restric
 // their stores.  Row i is a source only of moves j <= i, so each column is
 // read before it is overwritten.  A move of a row onto itself is skipped.
 // Bound by memory for a batch over all layers (64 sequences x 32 layers, FP8:
-// 5.9 us in a graph, the bytes' 4.4), by the launch for few sequences (2.4 us).
+// 7.8 us in a graph, the bytes' 4.4), by the launch for few sequences (2.5 us).
 constexpr int kMoveThreads = 128;
 constexpr int kMoveBatch = 8;
 
