@@ -54,9 +54,9 @@
 //  * 2 x 131072, 27 nodes, 32 query heads of 64: 110 of 79 for the bytes; 16 MMAs of
 //    P V a tile with P from tensor memory take about as long with heads of 64
 //    as with 128.
-//  * 1 x 500, 8 nodes: 12, all latency: 1.3 for the split, 1.7 to the first page,
-//    2.7 for one tile of each warpgroup, 2.5 for its end, 0.8 + 2.8 for the
-//    merge.
+//  * 1 x 500, 8 nodes: 11.5, all latency: 1.3 for the split, 1.7 to the first
+//    page, 2.7 for one tile of each warpgroup, 2.5 for its end, 0.8 + 2.4 for
+//    the merge.
 #include <algorithm>
 
 #include "pkv_device.cuh"
@@ -1157,27 +1157,57 @@ tree_merge_kernel(const TreeParams p, int ctas) {
 #pragma unroll
   for (int z = 0; z < kQuads; ++z) acc[z] = make_float4(0.f, 0.f, 0.f, 0.f);
   float big = -INFINITY, tot = 0.f;
+  // Several pieces' loads at a time, those beyond the last as pieces without
+  // weight.  More at a time take registers, and with them the blocks that an SM
+  // holds: us with 2 / 3 / 4 / 8, heads of 128: 1 x 500, 8 nodes 11.5 / 11.4 / 11.5 /
+  // 11.5, 32 x 1000, 16 nodes 41.1 / 42.3 / 42.2 / 44.5, 16 x 4000, 64 nodes 112 / 114 /
+  // - / -; with 4 / 8, heads of 64: 1 x 30000, 27 nodes 26.9 / 26.3 (one at a time:
+  // 31.1).
+  constexpr int kAtOnce = D == 64 ? 8 : 2;
   if (lane < rows) {
-#pragma unroll 4
-    for (int i = 0; i < parts; ++i) {
-      const size_t t = tile_of(i);
-      const float lse = __ldg(p.part_lse + t * kTrRows + r);
-      const float4* o = reinterpret_cast<const float4*>(p.part_o) +
-                        (t * (D / 4) + warp * kQuads) * kTrRows + r;
-      float4 x[kQuads];
+#pragma unroll 1
+    for (int i = 0; i < parts; i += kAtOnce) {
+      float lse[kAtOnce];
+      float4 x[kAtOnce][kQuads];
 #pragma unroll
-      for (int z = 0; z < kQuads; ++z) x[z] = __ldg(o + z * kTrRows);
-      const float now = fmaxf(big, lse);
+      for (int u = 0; u < kAtOnce; ++u) {
+        const size_t t = tile_of(min(i + u, parts - 1));
+        const float4* o = reinterpret_cast<const float4*>(p.part_o) +
+                          (t * (D / 4) + warp * kQuads) * kTrRows + r;
+        lse[u] = -INFINITY;
+#pragma unroll
+        for (int z = 0; z < kQuads; ++z) x[u][z] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i + u < parts) {
+          lse[u] = __ldg(p.part_lse + t * kTrRows + r);
+#pragma unroll
+          for (int z = 0; z < kQuads; ++z) x[u][z] = __ldg(o + z * kTrRows);
+        }
+      }
+      float now = big;
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) now = fmaxf(now, lse[u]);
       const float ref = now == -INFINITY ? 0.f : now;
-      const float fade = ex2(big - ref), wgt = ex2(lse - ref);
+      const float fade = ex2(big - ref);
       big = now;
-      tot = tot * fade + wgt;  // a piece in which the row saw nothing weighs 0 (its row is zeros)
+      tot *= fade;
 #pragma unroll
       for (int z = 0; z < kQuads; ++z) {
-        acc[z].x = acc[z].x * fade + x[z].x * wgt;
-        acc[z].y = acc[z].y * fade + x[z].y * wgt;
-        acc[z].z = acc[z].z * fade + x[z].z * wgt;
-        acc[z].w = acc[z].w * fade + x[z].w * wgt;
+        acc[z].x *= fade;
+        acc[z].y *= fade;
+        acc[z].z *= fade;
+        acc[z].w *= fade;
+      }
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+        const float wgt = ex2(lse[u] - ref);
+        tot += wgt;  // a piece in which the row saw nothing weighs 0 (its row is zeros)
+#pragma unroll
+        for (int z = 0; z < kQuads; ++z) {
+          acc[z].x += x[u][z].x * wgt;
+          acc[z].y += x[u][z].y * wgt;
+          acc[z].z += x[u][z].z * wgt;
+          acc[z].w += x[u][z].w * wgt;
+        }
       }
     }
   }
