@@ -122,6 +122,8 @@ struct TreeSmem {
   static constexpr int kSmemBytes = kPieceOff + kTrPieces * 32;
   static_assert(kSmemBytes <= 232448, "tree tile does not fit in shared memory");
   static_assert(kKStages <= kTrMaxStages && kVStages <= kTrMaxStages, "ring stages");
+  // a V slot's tile before is of a job at least kBufs back (the softmax's wait for V)
+  static_assert(kVStages * TILES >= kBufs, "V stages");
 };
 
 enum TrBar {
@@ -763,7 +765,14 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const bool masked = key0 + kTrKeys > base;
         if (masked && (TILES == 1 || w == 0)) {
           // thread r looks at key row r of V; the chunk order differs from
-          // row to row, so that a warp's reads spread over the banks
+          // row to row, so that a warp's reads spread over the banks.
+          // S comes first: a wait on a parity says something only once the phase before is
+          // over, here the copy of tile it - kVStages into the same slot.  S of this job
+          // was issued after the products of job - kBufs, and those, in their order, after
+          // that tile's.
+          ok = __all_sync(0xffffffffu,
+                          tr_wait(bars + 8 * (kTrSFull + b), ph & 1, abort_flag));
+          if (!ok) break;
           ok = __all_sync(0xffffffffu, tr_wait(bars + 8 * (kTrVFull + it % T::kVStages),
                                                (it / T::kVStages) & 1, abort_flag));
           if (!ok) break;

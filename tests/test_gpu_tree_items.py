@@ -1,0 +1,124 @@
+"""Attention of drafted trees over many items of several key tiles each, so that
+the rings of tiles run on across the items of a CTA: rows that nobody sees may
+hold anything wherever in the stream their tile comes.
+
+The reference is the definition in float64 on the GPU.  Tolerance of a float32
+output element, from the arithmetic alone: a score is off by at most
+e = (d + 4) 2^-24 * 2 |scale| |q| |k| (float32 accumulation of d products,
+Cauchy-Schwarz on the magnitudes), a weight and the sum so by a factor
+exp(2 e); P as bf16 hi + lo adds 2^-16, the base-2 exponential 2^-21, the
+accumulation of L / 16 + 8 partial products and the join (L / 16 + 40) 2^-23;
+all of it times max|V|.
+"""
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+BS = 16
+
+
+@pytest.fixture(scope="module")
+def pk():
+    from paged_kv_cache_52_gb300 import pagedkv
+    pagedkv.get_device_error(clear=True)
+    return pagedkv
+
+
+class Batch:
+    """Trees of any mask over a shuffled pool on the GPU."""
+
+    def __init__(self, hq, hkv, d, nodes, lens, seed):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        rng = np.random.default_rng(seed)
+        self.n, self.lens = np.array(nodes), np.array(lens)
+        self.start = np.concatenate([[0], np.cumsum(self.n)])
+        total = int(self.start[-1])
+        need = -(-self.lens // BS)
+        blocks = int(need.sum()) + 3
+        perm = rng.permutation(blocks)
+        tables = np.full((len(nodes), int(need.max())), -1, dtype=np.int32)
+        at = 0
+        for s, b in enumerate(need):
+            tables[s, :b] = perm[at:at + b]
+            at += b
+        self.tables = torch.from_numpy(tables).to(DEV)
+        self.k = torch.randn(blocks, BS, hkv, d, device=DEV, generator=g).bfloat16()
+        self.v = torch.randn(blocks, BS, hkv, d, device=DEV, generator=g).bfloat16()
+        self.q = torch.randn(total, hq, d, device=DEV, generator=g).bfloat16()
+        self.mask = rng.integers(0, 2 ** 64, total, dtype=np.uint64)
+        self.scale = d ** -0.5
+
+    def row(self, s, pos):
+        return int(self.tables[s, pos // BS]), pos % BS
+
+    def run(self, pk, **kw):
+        i32 = lambda x: torch.from_numpy(x.astype(np.int32)).to(DEV)  # noqa: E731
+        kw = dict(max_q_len=int(self.n.max())) | kw
+        return pk.paged_tree_attention(
+            self.q, i32(self.start), torch.from_numpy(self.mask.view(np.int64)).to(DEV), self.k,
+            self.v, self.tables, i32(self.lens), self.scale, **kw)
+
+    def ref(self, s):
+        """Sequence s's rows in float64, from its visible keys."""
+        n, L = int(self.n[s]), int(self.lens[s])
+        pages = self.tables[s, :-(-L // BS)].long()
+        k, v = (x[pages].flatten(0, 1)[:L].double() for x in (self.k, self.v))
+        q = self.q[self.start[s]:self.start[s + 1]].double()
+        q = q.view(n, k.shape[1], -1, q.shape[2])
+        word = torch.from_numpy(self.mask[self.start[s]:self.start[s + 1]].view(np.int64)).to(DEV)
+        seen = torch.ones(n, L, dtype=torch.bool, device=DEV)
+        seen[:, L - n:] = (word[:, None] >> torch.arange(n, device=DEV)) & 1 == 1
+        x = torch.einsum("thgd,lhd->thgl", q, k) * float(np.float32(self.scale))
+        p = x.masked_fill(~seen[:, None, None, :], -math.inf).softmax(-1).nan_to_num(0.0)
+        return torch.einsum("thgl,lhd->thgd", p, v).flatten(1, 2)
+
+    def tolerance(self):
+        d, L = self.q.shape[2], int(self.lens.max())
+        q, k = (float(x.float().norm(dim=-1).max()) for x in (self.q, self.k))
+        e = (d + 4) * 2.0 ** -23 * abs(self.scale) * q * k
+        return float(self.v.float().abs().max()) * (
+            math.expm1(2 * e) + 2.0 ** -16 + 2.0 ** -21 + (L / 16 + 40) * 2.0 ** -23)
+
+    def check(self, out, what=""):
+        tol = self.tolerance()
+        for s in range(len(self.n)):
+            diff = (out[self.start[s]:self.start[s + 1]].double() - self.ref(s)).abs()
+            assert not self.n[s] or bool((diff <= tol).all()), (what, s, float(diff.max()), tol)
+
+
+# (query heads, KV heads, d, nodes): one row tile, and two
+SHAPES = [(8, 4, 128, 8), (8, 4, 64, 8), (4, 4, 64, 33), (32, 4, 128, 16), (32, 4, 128, 40),
+          (16, 4, 64, 64)]
+
+
+@pytest.mark.parametrize("hq,hkv,d,n", SHAPES)
+@pytest.mark.parametrize("seqs", [31, 40])
+def test_unseen_rows_may_hold_anything_wherever_in_the_stream(pk, hq, hkv, d, n, seqs):
+    # contexts of 9 to 17 key tiles whose last page is never full, items enough
+    # for every SM to take several pieces in turn
+    rng = np.random.default_rng(seqs + d + n)
+    lens = [int(x) * BS + 5 for x in rng.integers(70, 132, seqs)]
+    b = Batch(hq, hkv, d, [n] * seqs, lens, seed=n)
+    hidden = np.array([rng.integers(0, n) for _ in range(seqs)])
+    for s in range(seqs):  # one node of each tree that no row sees, itself included
+        b.mask[b.start[s]:b.start[s + 1]] &= ~np.uint64(1 << int(hidden[s]))
+    clean = b.run(pk)
+    b.check(clean)
+    for value in (float("nan"), float("inf"), -float("inf")):
+        for s in range(seqs):
+            blk, off = b.row(s, lens[s] - 1)
+            b.k[blk, off + 1:] = value
+            b.v[blk, off + 1:] = value
+            blk, off = b.row(s, lens[s] - n + int(hidden[s]))
+            b.k[blk, off] = value
+            b.v[blk, off] = value
+        for _ in range(4):
+            out = b.run(pk)
+            assert torch.equal(out, clean), value
+    assert pk.get_device_error(clear=True) == 0
