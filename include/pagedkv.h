@@ -714,6 +714,9 @@ PKV_API int pkv_draft_tree_layout(const int32_t* parents, const int32_t* q_start
  * n on are ignored, and a row that sees no key is zero.  A node that a row
  * does not see never reaches it, whatever its K and V rows hold (NaN and
  * infinities included).
+ * Finite elements of V may be as large as 2^110 / (context_len + 64): weights
+ * times V are accumulated in float32, the weights of a row up to 2^24 against
+ * its running maximum.
  *   q            : [total_q][q_heads][d_head] bf16, contiguous, 16-byte aligned.
  *   q_start, max_q_len, context_lens : as in pkv_draft_tree_layout; a sequence
  *                  outside those bounds, or with a context beyond the block

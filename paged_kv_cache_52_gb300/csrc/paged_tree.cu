@@ -74,6 +74,12 @@ constexpr int kTrRegsSoftmax = 192, kTrRegsIssue = 120;
 constexpr int kTrKWarp = 8, kTrSWarp = 9, kTrVWarp = 10;  // 11 issues P V
 constexpr uint32_t kTrTmemCols = 512;
 constexpr float kTrRescale = 8.0f;     // log2 units: move the running max when it grows by > x256
+// The most that a row's weights over 64 keys may add up to against the running max it
+// has.  The accumulator holds weights times V, at most (L / 64 + 1) 2^24 max|V|: finite V
+// up to 2^110 / (L + 64) cannot overflow it.  us with 2^16 / 2^24 / 2^64: 64 x 8192, 64
+// nodes 885 / 873 / 874, 6 x 9000, 64 nodes, heads of 64 48.7 / 46.1 / 46.1, 16 x 4096, 16
+// nodes 51.5 / 51.1 / 51.2.
+constexpr float kTrMaxSum = 16777216.f;
 constexpr int kTrMaxStages = 4;
 // The fewest key tiles worth a piece: one for each softmax warpgroup (us with 2 / 1:
 // 1 x 2000, 16 nodes 18.1 / 22.1; three tiles whole / cut 11.45 / 11.9).
@@ -828,9 +834,9 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
             // The running max m is a reference only: any value near the scores'
             // serves.  So the keys are weighed against the m it has, without
             // looking for their max, and that stands while each row's sum is at
-            // most 2^64 (bf16 hi + lo has float32's range).  Where no key has
-            // been seen yet, or a sum is larger, the max is taken first, and m
-            // moves when it is more than 8 behind (a factor 256).
+            // most kTrMaxSum.  Where no key has been seen yet, or a sum is larger,
+            // the max is taken first, and m moves when it is more than 8 behind (a
+            // factor 256).
             const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
             bool raise = !__all_sync(0xffffffffu, m != -INFINITY);
 #pragma unroll 1
@@ -910,7 +916,7 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
               f2_unpack(ls[0], a0, a1);
               f2_unpack(ls[1], b0, b1);
               const float sum = (a0 + a1) + (b0 + b1);
-              if (raise || __all_sync(0xffffffffu, sum <= 18446744073709551616.f)) {
+              if (raise || __all_sync(0xffffffffu, sum <= kTrMaxSum)) {
                 l += sum;
                 break;
               }

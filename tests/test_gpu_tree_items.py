@@ -122,3 +122,58 @@ def test_unseen_rows_may_hold_anything_wherever_in_the_stream(pk, hq, hkv, d, n,
             out = b.run(pk)
             assert torch.equal(out, clean), value
     assert pk.get_device_error(clear=True) == 0
+
+
+# Where a sequence's scores climb, (key, height): within the first tile, in each
+# half of a later one, several times, and in the tree.
+CLIMBS = [[(70, 30.0)], [(200, 15.0)], [(330, 20.0)], [(130, 14.0), (700, 50.0)],
+          [(64, 45.0), (128, 90.0)], [(400, 12.0), (460, 24.0), (900, 37.0), (970, 60.0)],
+          [(5, 60.0), (640, 70.0)], [(1297, 25.0)], [(1291, 100.0)], []]
+
+
+@pytest.mark.parametrize("hq,hkv,d,n", SHAPES)
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("big", [1.0, 2.0 ** 96])
+def test_climbing_scores(pk, hq, hkv, d, n, sign, big):
+    """Scores that are exact, a_row s_key: with q = a u, k = s u, u of d signs and
+    the scale 1 / d.  What is left of a score's error, in units of X, the largest
+    score times log2 e: the scale's product and constant, the multiply-add and up
+    to 12 differences of references and log-sum-exps, 2^-24 X each.  A weight is so
+    off by a factor E = exp(2 * 16 * 2^-24 X), by two roundings to hi + lo (2^-16
+    each) and up to eight exponentials of references (2^-21 each).  Every error
+    is relative to a key's weight or, from accumulating, to the sum of |p v|, so
+    an element is off by at most twice that part of sum p |v|; weights beyond
+    2^-126 of the largest are lost.  V up to 2^96 times 6.2: below 2^110 / (L + 64)."""
+    seqs, L = 40, 1301
+    b = Batch(hq, hkv, d, [n] * seqs, [L] * seqs, seed=d + n)
+    g = torch.Generator().manual_seed(3)
+    u = (torch.randint(0, 2, (d,), generator=g) * 2 - 1).float()
+    a = 2.0 ** -torch.randint(0, 3, b.q.shape[:2], generator=g).float()
+    b.q = (a[..., None] * u).bfloat16().to(DEV)
+    for s in range(seqs):
+        height = torch.randint(-2, 3, (L,), generator=g) / 2
+        for key, h in CLIMBS[s % len(CLIMBS)]:
+            height[key] += h
+        pages = b.tables[s].long()
+        rows = torch.zeros(len(pages) * BS, d)
+        rows[:L] = sign * height[:, None] * u
+        b.k[pages] = rows.bfloat16().to(DEV).view(-1, BS, 1, d).expand(-1, -1, hkv, -1)
+    b.v = (b.v.float() * big).bfloat16()
+    assert float(b.v.float().abs().max()) * (L + 64) < 2.0 ** 110
+    b.scale = sign / d
+    out = b.run(pk)
+    assert bool(out.isfinite().all())
+    X = 103 * 1.4427
+    part = (math.expm1(2 * 16 * 2.0 ** -24 * X) + 2 * 2.0 ** -16 + 8 * 2.0 ** -21
+            + (L / 16 + 40) * 2.0 ** -23)
+    values = b.v
+    for s in range(seqs):
+        got = out[b.start[s]:b.start[s + 1]].double()
+        want = b.ref(s)
+        b.v = values.abs()
+        tol = 2 * part * b.ref(s) + 2.0 ** -100 * big
+        b.v = values
+        bad = (got - want).abs() > tol
+        assert not bool(bad.any()), (s, CLIMBS[s % len(CLIMBS)], int(bad.sum()),
+                                     float(((got - want).abs() / tol).max()))
+    assert pk.get_device_error(clear=True) == 0
