@@ -717,6 +717,10 @@ PKV_API int pkv_draft_tree_layout(const int32_t* parents, const int32_t* q_start
  * Finite elements of V may be as large as 2^110 / (context_len + 64): weights
  * times V are accumulated in float32, the weights of a row up to 2^24 against
  * its running maximum.
+ * An infinity in V of a visible node comes through as itself; one in V of a
+ * committed key makes its element of every row infinite or NaN (it is
+ * multiplied by the two parts of a weight, the second of either sign or zero).
+ * NaN in V, K or q makes NaN of what it reaches.
  *   q            : [total_q][q_heads][d_head] bf16, contiguous, 16-byte aligned.
  *   q_start, max_q_len, context_lens : as in pkv_draft_tree_layout; a sequence
  *                  outside those bounds, or with a context beyond the block

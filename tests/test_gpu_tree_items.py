@@ -177,3 +177,22 @@ def test_climbing_scores(pk, hq, hkv, d, n, sign, big):
         assert not bool(bad.any()), (s, CLIMBS[s % len(CLIMBS)], int(bad.sum()),
                                      float(((got - want).abs() / tol).max()))
     assert pk.get_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,n", SHAPES)
+def test_non_finite_values_of_committed_keys_stay_in_their_element(pk, hq, hkv, d, n):
+    lens = [700 + 31 * s for s in range(40)]
+    b = Batch(hq, hkv, d, [n] * 40, lens, seed=n + 1)
+    clean = b.run(pk)
+    want = clean.isfinite()
+    assert bool(want.all())
+    group = hq // hkv
+    for s, (pos, head, col, value) in {0: (0, 0, 5, math.inf), 7: (300, 1, d - 1, -math.inf),
+                                       21: (lens[21] - n - 1, hkv - 1, 32, math.nan)}.items():
+        blk, off = b.row(s, pos)
+        b.v[blk, off, head, col] = value
+        want[b.start[s]:b.start[s + 1], head * group:(head + 1) * group, col] = False
+    out = b.run(pk)
+    assert torch.equal(out.isfinite(), want)
+    assert torch.equal(out[want], clean[want])
+    assert pk.get_device_error(clear=True) == 0
