@@ -733,6 +733,9 @@ PKV_API int pkv_draft_tree_layout(const int32_t* parents, const int32_t* q_start
  *                  need no initialisation; calls that share it must be ordered
  *                  on the GPU.  Its size depends on the current device.
  * Other arguments, shapes and errors are those of pkv_paged_prefill_attention.
+ * PKV_EUNSUPPORTED also for sizes whose key tiles pass 2^31: block tables of
+ * more than about 1.8e9 positions, or the tiles (and two more each) of all row
+ * groups of all KV heads of num_seqs such tables.
  * Context lengths are read on the device only: no host bound is needed, and a
  * captured call may be replayed with other lengths, trees and tables.
  * pkv_paged_tree_attention_bf16out rounds the float32 result once to bf16

@@ -1262,6 +1262,8 @@ unsigned read_tree_error(bool clear) {
 }
 
 int tree_tile_rows() { return kTrRows; }
+int tree_tile_keys() { return kTrKeys; }
+int tree_places(int tiles) { return tiles + kTrSlack; }
 
 template <int D, int G, int TILES>
 static cudaError_t launch_tree_t(const TreeParams& p, int ctas, const CUtensorMap* tq,

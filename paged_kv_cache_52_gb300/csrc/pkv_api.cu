@@ -1912,11 +1912,15 @@ int tree_attention(const void* q, const int32_t* q_start, int num_seqs, int tota
   if (st != PKV_OK) return st;
   if (num_seqs == 0 || total_q == 0 || max_q_len == 0) return PKV_OK;
   if (!tree_mask || !aligned(tree_mask, 8)) return PKV_EINVAL;
-  if (max_blocks_per_seq > INT32_MAX / kBlockSize) return PKV_EUNSUPPORTED;
-  // key tiles of all items are counted in 32 bits
+  // In 32 bits on the device: positions up to the end of the last key tile, a tile's
+  // number times that of CTAs (equal pieces of an item), and the places of all items,
+  // which are their tiles and a few more each.
+  const int tiles = max_blocks_per_seq / (pkv::tree_tile_keys() / kBlockSize) + 1;
+  if (tiles > INT32_MAX / pkv::tree_tile_keys() || tiles > INT32_MAX / w.ctas)
+    return PKV_EUNSUPPORTED;
   const long long groups = ((long long)max_q_len * (q_heads / cache.kv_heads) - 1) /
                                pkv::tree_tile_rows() + 1;
-  if (groups * num_seqs * cache.kv_heads > INT32_MAX / (max_blocks_per_seq / 8 + 1))
+  if (groups * num_seqs * cache.kv_heads > INT32_MAX / pkv::tree_places(tiles))
     return PKV_EUNSUPPORTED;
   if (!workspace || ws_bytes < w.total) return PKV_ENOMEM;
   if (!aligned(workspace, 256)) return PKV_EINVAL;

@@ -295,6 +295,8 @@ struct TreeArgs {
   float scale_log2;
 };
 int tree_tile_rows();
+int tree_tile_keys();
+int tree_places(int tiles);  // of an item of so many key tiles in the split
 int tree_tiles(int group, int max_q_len);  // row tiles per CTA for these sizes
 cudaError_t launch_paged_tree(const TreeArgs& a, const CUtensorMap* tmap_q,
                               const CUtensorMap* tmap_k, const CUtensorMap* tmap_v,

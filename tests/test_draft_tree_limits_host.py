@@ -1,0 +1,36 @@
+"""Refusals of the speculative step's calls that need no GPU: sizes whose index
+arithmetic would leave 32 bits, and arguments that lie over one another."""
+
+import ctypes
+
+import pytest
+
+NULL, DUMMY = ctypes.c_void_p(0), ctypes.c_void_p(1 << 20)  # DUMMY is never dereferenced
+
+
+@pytest.fixture(scope="module")
+def pk():
+    import os
+    from paged_kv_cache_52_gb300 import build as b
+    if not os.path.exists(b.LIB_PATH):
+        b.build()
+    from paged_kv_cache_52_gb300 import pagedkv
+    return pagedkv
+
+
+@pytest.mark.parametrize("seqs,blocks,heads,nodes,status", [
+    # the workspace is too small throughout: -4 where the sizes are taken
+    (1 << 28, 1, 2, 8, -4),             # 2^29 items of one tile: 3 places each
+    ((1 << 28) + (1 << 27), 1, 2, 8, -2),
+    (1 << 29, 7, 2, 8, -2),
+    (1 << 20, 8, 2, 64, -4),            # one row group a tree
+    (1 << 20, 16000, 2, 8, -2),
+    (2, 112_000_000, 2, 8, -4),         # positions up to 1.8e9
+    (2, (1 << 27) - 1, 2, 8, -2),       # their last tile's number times that of SMs
+    (1, (1 << 31) - 1, 1, 1, -2),
+])
+def test_tree_attention_refuses_sizes_beyond_32_bits(pk, seqs, blocks, heads, nodes, status):
+    desc = pk.CacheDesc(64, 16, heads, 64)
+    for fn in (pk.lib.pkv_paged_tree_attention, pk.lib.pkv_paged_tree_attention_bf16out):
+        assert fn(DUMMY, DUMMY, seqs, 9, nodes, 2 * heads, DUMMY, DUMMY, DUMMY, desc, DUMMY, blocks,
+                  DUMMY, 0.1, DUMMY, DUMMY, 1000, NULL) == status
