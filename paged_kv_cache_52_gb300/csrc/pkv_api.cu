@@ -92,14 +92,9 @@ bool encode_pool_map(CUtensorMap* map, const void* base, const pkv_cache_desc& c
                                  row * cuuint64_t(c.kv_heads) * cuuint64_t(c.block_size)};
   const cuuint32_t box[4] = {64, 1, cuuint32_t(c.block_size), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  // A token's row of a head is fetched as one piece: with heads of 64, 256 bytes
-  // would take the next head's row along (tree attention, 2 x 131072: 122 us
-  // against 134; decode of 64 x 4096 the same either way).
-  const CUtensorMapL2promotion piece =
-      row < 256 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
                    strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   CU_TENSOR_MAP_SWIZZLE_128B, piece,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
