@@ -5,7 +5,8 @@ compiled in parallel (one nvcc process each), then linked into a shared library 
 statically, so the library loads without a GPU driver present.  Objects go to
 ``_build/`` beside this file.  The host compiler builds ``binding/marshal.cpp``,
 the argument marshalling of the calls whose GPU time is a few microseconds, as
-the CPython module ``_marshal.so`` next to it.  Usage: ``python -m paged_kv_cache_52_gb300.build``.
+the CPython module ``_marshal.so`` next to it, against the installed PyTorch; only
+those calls need it.  Usage: ``python -m paged_kv_cache_52_gb300.build``.
 """
 
 from __future__ import annotations
@@ -69,7 +70,7 @@ def _compile_marshal(nvcc: str) -> str:
     obj = os.path.join(BUILD_DIR, "marshal.o")
     inc = os.path.join(_torch_dir(), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
-    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-w",
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall",
           f"-I{sysconfig.get_paths()['include']}", f"-isystem{inc}",
           f"-isystem{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}", f"-isystem{cuda}",
           "-c", MARSHAL_SRC, "-o", obj])
@@ -94,7 +95,6 @@ def build(verbose: bool = False) -> str:
     with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
         marshal = ex.submit(_compile_marshal, nvcc)
         results = list(ex.map(lambda s: _compile(nvcc, s), srcs))
-        marshal_obj = marshal.result()
     if verbose:
         for obj, log in results:
             sys.stderr.write(f"== {os.path.basename(obj)}\n{log}")
@@ -104,7 +104,11 @@ def build(verbose: bool = False) -> str:
     if proc.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{proc.stdout}{proc.stderr}")
     os.replace(tmp, LIB_PATH)
-    _link_marshal(marshal_obj)
+    try:
+        _link_marshal(marshal.result())
+    except RuntimeError as e:
+        raise RuntimeError("libpagedkv.so is built; _marshal.so, which the speculative step's "
+                           f"calls need, is not:\n{e}") from e
     return LIB_PATH
 
 

@@ -222,11 +222,24 @@ def _load():
 
 
 lib = _load()
-try:
-    from . import _marshal
-except ImportError as e:
-    raise RuntimeError("_marshal.so is not built for this Python and PyTorch; run "
-                       "`python -m paged_kv_cache_52_gb300.build`") from e
+
+
+class _Marshal:
+    """``_marshal.so``, imported at the first call that needs it: it is built for
+    one Python and one PyTorch, and nothing else here is."""
+
+    def __getattr__(self, name):  # only until a function is found the first time
+        try:
+            from . import _marshal as module
+        except ImportError as e:
+            raise RuntimeError("_marshal.so is not built for this Python and PyTorch; run "
+                               "`python -m paged_kv_cache_52_gb300.build`") from e
+        fn = getattr(module, name)
+        setattr(self, name, fn)
+        return fn
+
+
+_marshal = _Marshal()
 
 
 def status_string(status: int) -> str:
