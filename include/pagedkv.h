@@ -769,12 +769,13 @@ PKV_API int pkv_paged_tree_attention_bf16out(const void* q, const int32_t* q_sta
  * they held.
  *   k_cache, v_cache : the first layer's pools; layer l's start l *
  *                  k_layer_stride (v_layer_stride) elements on (ignored for
- *                  one layer; else at least a pool, a multiple of 16 bytes).
+ *                  one layer; else at least a pool, a multiple of 16 bytes). No
+ *                  K pool lies over a V pool (PKV_EINVAL).
  *   elem_bytes   : 2 (bf16 pools) or 1 (FP8).
  *   accepted     : [num_seqs][max_accepted] int32, strictly increasing node
  *                  numbers in [0, n) (a root-to-leaf path is).
  *   num_accepted : [num_seqs] int32 in [0, min(max_accepted, n)].
- *   new_context_lens : [num_seqs] int32 out; must not overlap an input.
+ *   new_context_lens : [num_seqs] int32 out; must not overlap an input (PKV_EINVAL).
  * The pages that hold a tree belong to its sequence alone (as after
  * pkv_bm_reserve_draft).  A path that breaks these rules, a tree of more than
  * 64 nodes or a context beyond the block table leaves its sequence's rows and

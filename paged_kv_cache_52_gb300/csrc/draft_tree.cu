@@ -157,11 +157,18 @@ cudaError_t launch_tree_layout(const int32_t* parents, const int32_t* q_start, i
                                reinterpret_cast<unsigned long long*>(tree_mask), positions);
 }
 
+static int accept_col_blocks(int row_vec) {
+  return (2 * row_vec + kMoveThreads - 1) / kMoveThreads;
+}
+
+int64_t accept_rows_blocks(int num_layers, int num_seqs, int row_vec) {
+  return int64_t(num_layers) * num_seqs * accept_col_blocks(row_vec);
+}
+
 cudaError_t launch_accept_rows(const AcceptArgs& args, int num_layers, cudaStream_t stream) {
   AcceptArgs a = args;
-  a.col_blocks = (2 * a.row_vec + kMoveThreads - 1) / kMoveThreads;
-  const int64_t blocks = int64_t(num_layers) * a.num_seqs * a.col_blocks;
-  if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+  a.col_blocks = accept_col_blocks(a.row_vec);
+  const int64_t blocks = accept_rows_blocks(num_layers, a.num_seqs, a.row_vec);
   return launch_after_previous(accept_rows_kernel, dim3(unsigned(blocks)), dim3(kMoveThreads), 0,
                                stream, a);
 }

@@ -1797,6 +1797,23 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   return x < y + nb && y < x + na;
 }
 
+// Whether a layer of one pool lies over a layer of the other: `layers` pieces of
+// `bytes` from each base, kstep and vstep bytes apart (at least `bytes`, or 0 for one
+// layer).  Where they do, K's thread of a column would read rows that V's has moved.
+bool layers_overlap(const void* k, int64_t kstep, const void* v, int64_t vstep, int layers,
+                    int64_t bytes) {
+  const int64_t apart = int64_t(reinterpret_cast<uintptr_t>(k) - reinterpret_cast<uintptr_t>(v));
+  if (apart >= (layers - 1) * vstep + bytes || -apart >= (layers - 1) * kstep + bytes) return false;
+  for (int l = 0; l < layers; ++l) {
+    const int64_t at = apart + l * kstep;  // from V's first layer
+    // V's last layer that starts at or before it, and the next one
+    const int64_t before = at < 0 || vstep == 0 ? 0 : std::min<int64_t>(at / vstep, layers - 1);
+    for (int64_t j = before; j <= std::min<int64_t>(before + 1, layers - 1); ++j)
+      if (at < j * vstep + bytes && j * vstep < at + bytes) return true;
+  }
+  return false;
+}
+
 int rope_append(const void* q, int64_t q_tok_stride, const void* k, int64_t k_tok_stride,
                 const void* v, int64_t v_tok_stride, int64_t num_tokens, int q_heads,
                 const int64_t* positions, const float* rope_table, int64_t max_positions,
@@ -2057,12 +2074,19 @@ int pkv_kv_accept_rows(void* k_cache, int64_t k_layer_stride, void* v_cache,
       !aligned(context_lens, 4) || !aligned(q_start, 4) || !aligned(accepted, 4) ||
       !aligned(num_accepted, 4) || !aligned(new_context_lens, 4))
     return PKV_EINVAL;
+  const int row_vec = int(row_bytes / 16);
+  if (pkv::accept_rows_blocks(num_layers, num_seqs, row_vec) > INT32_MAX)
+    return PKV_EUNSUPPORTED;
   // other CTAs of a sequence still read what one CTA would overwrite
   const size_t n = size_t(num_seqs) * 4;
   if (overlap(new_context_lens, n, context_lens, n) ||
       overlap(new_context_lens, n, num_accepted, n) ||
       overlap(new_context_lens, n, q_start, n + 4) ||
-      overlap(new_context_lens, n, accepted, n * size_t(max_accepted)))
+      overlap(new_context_lens, n, accepted, n * size_t(max_accepted)) ||
+      overlap(new_context_lens, n, block_tables, n * size_t(max_blocks_per_seq)))
+    return PKV_EINVAL;
+  if (layers_overlap(k_cache, num_layers > 1 ? k_layer_stride * elem_bytes : 0, v_cache,
+                     num_layers > 1 ? v_layer_stride * elem_bytes : 0, num_layers, pool_bytes))
     return PKV_EINVAL;
   pkv::AcceptArgs a;
   a.k_cache = static_cast<uint4*>(k_cache);
@@ -2079,11 +2103,11 @@ int pkv_kv_accept_rows(void* k_cache, int64_t k_layer_stride, void* v_cache,
   a.max_accepted = max_accepted;
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.num_blocks = cache.num_blocks;
-  a.row_vec = int(row_bytes / 16);
+  a.row_vec = row_vec;
   a.col_blocks = 0;
   const cudaError_t e =
       pkv::launch_accept_rows(a, num_layers, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? PKV_OK : (e == cudaErrorInvalidValue ? PKV_EUNSUPPORTED : PKV_ECUDA);
+  return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
 }  // extern "C"

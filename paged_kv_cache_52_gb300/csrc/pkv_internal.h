@@ -276,6 +276,7 @@ struct AcceptArgs {
   int row_vec;     // 16-byte vectors per token row
   int col_blocks;  // set by the launch
 };
+int64_t accept_rows_blocks(int num_layers, int num_seqs, int row_vec);  // at most INT32_MAX
 cudaError_t launch_accept_rows(const AcceptArgs& a, int num_layers, cudaStream_t stream);
 unsigned read_draft_error(bool clear);
 

@@ -34,3 +34,33 @@ def test_tree_attention_refuses_sizes_beyond_32_bits(pk, seqs, blocks, heads, no
     for fn in (pk.lib.pkv_paged_tree_attention, pk.lib.pkv_paged_tree_attention_bf16out):
         assert fn(DUMMY, DUMMY, seqs, 9, nodes, 2 * heads, DUMMY, DUMMY, DUMMY, desc, DUMMY, blocks,
                   DUMMY, 0.1, DUMMY, DUMMY, 1000, NULL) == status
+
+
+LAYER = 64 * 16 * 128 * 2  # bytes of a pool of the descriptor below
+
+
+def _accept(pk, layers, k, kstep, v, vstep, new=1 << 24, tables=1 << 26):
+    return pk.lib.pkv_kv_accept_rows(
+        ctypes.c_void_p((1 << 30) + k), kstep // 2, ctypes.c_void_p((1 << 30) + v), vstep // 2,
+        layers, pk.CacheDesc(64, 16, 2, 64), 2, ctypes.c_void_p(tables), 8, DUMMY, DUMMY, 2, DUMMY,
+        4, DUMMY, ctypes.c_void_p(new), NULL)
+
+
+# only layouts that are refused: the others would be launched
+@pytest.mark.parametrize("layers,k,kstep,v,vstep", [
+    (1, 0, 0, 0, 0),                              # one pool as both
+    (1, 0, 0, LAYER - 16, 0),
+    (1, LAYER - 16, 0, 0, 0),
+    (5, 0, 2 * LAYER, LAYER + 16, 2 * LAYER),     # K and V of a layer side by side, but
+    (5, 0, 2 * LAYER, LAYER - 16, 2 * LAYER),
+    (5, 0, LAYER, 4 * LAYER, LAYER),              # all K, then all V, but
+    (5, 8 * LAYER, LAYER, 0, 2 * LAYER),
+    (3, 0, 4 * LAYER, LAYER, 3 * LAYER),          # K at 0 4 8, V at 1 4 7
+])
+def test_accept_rows_refuses_pools_that_lie_over_one_another(pk, layers, k, kstep, v, vstep):
+    assert _accept(pk, layers, k, kstep, v, vstep) == -1
+
+
+def test_accept_rows_refuses_lengths_that_lie_over_the_block_table(pk):
+    for new in (1 << 24, (1 << 24) + 60):
+        assert _accept(pk, 1, 0, 0, LAYER, 0, new=new, tables=1 << 24) == -1
