@@ -97,7 +97,8 @@ Pools pools(PyObject* ko, PyObject* vo, bool allow_bf16, bool allow_fp8, bool al
   int64_t stride = 1;
   for (int64_t i = dims - 1; i >= first; --i) {
     if (k.size(i) > INT32_MAX) refuse("pools", "of sizes below 2^31");
-    if (k.stride(i) != stride || v.stride(i) != stride)
+    // a dimension of one element has no stride to speak of
+    if (k.size(i) != 1 && (k.stride(i) != stride || v.stride(i) != stride))
       refuse(allow_layers ? "each layer's pool" : "pools", "contiguous");
     stride *= k.size(i);
   }
