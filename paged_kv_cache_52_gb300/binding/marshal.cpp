@@ -102,6 +102,7 @@ Pools pools(PyObject* ko, PyObject* vo, bool allow_bf16, bool allow_fp8, bool al
       refuse(allow_layers ? "each layer's pool" : "pools", "contiguous");
     stride *= k.size(i);
   }
+  if (dims == 5 && (k.size(0) < 1 || k.size(0) > INT32_MAX)) refuse("pools", "of one layer or more");
   p.layers = dims == 5 ? int(k.size(0)) : 1;
   p.k_layer = dims == 5 ? k.stride(0) : 0;
   p.v_layer = dims == 5 ? v.stride(0) : 0;

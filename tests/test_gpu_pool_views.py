@@ -1,4 +1,5 @@
-"""The speculative step's calls take every view of a pool that is contiguous."""
+"""The speculative step's calls take every view of a pool that is contiguous, and
+refuse pools without layers."""
 
 import pytest
 import torch
@@ -51,10 +52,10 @@ def test_one_kv_head_in_any_contiguous_view(pk):
     assert pk.get_device_error(clear=True) == 0
 
 
-def test_strided_pools_are_refused(pk):
+def test_pools_without_layers_and_strided_ones_are_refused(pk):
     k = torch.zeros(2, 6, 16, 2, 64, dtype=torch.bfloat16, device=DEV)
     i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
     args = (i32([[0]]), i32([4]), i32([0, 2]), i32([[1]]), i32([1]))
-    for bad in (k[:, ::2], k[:, :, :, :1], k[..., :32]):
+    for bad in (k[:0], k[:, ::2], k[:, :, :, :1], k[..., :32]):
         with pytest.raises(ValueError):
             pk.kv_accept_rows(bad, bad.clone() if bad.is_contiguous() else bad, *args)
