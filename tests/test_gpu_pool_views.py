@@ -59,3 +59,32 @@ def test_pools_without_layers_and_strided_ones_are_refused(pk):
     for bad in (k[:0], k[:, ::2], k[:, :, :, :1], k[..., :32]):
         with pytest.raises(ValueError):
             pk.kv_accept_rows(bad, bad.clone() if bad.is_contiguous() else bad, *args)
+
+
+@pytest.mark.parametrize("T", [3, 700])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_norm_for_queries_or_keys_alone(pk, T, fp8):
+    # the side with a weight is as with both, the side without as with none
+    g = torch.Generator().manual_seed(T)
+    hq, hkv, d = 8, 4, 128
+    qkv = torch.randn(T, hq + 2 * hkv, d, generator=g).bfloat16().to(DEV)
+    q, k, v = qkv.split([hq, hkv, hkv], 1)
+    table = torch.randn(64, d, generator=g).to(DEV)
+    pos = torch.randint(0, 64, (T,), generator=g).to(DEV)
+    slots = torch.randperm(T, generator=g).to(DEV)
+    w = (torch.rand(d, generator=g) + 0.5).bfloat16().to(DEV)
+    blocks = -(-T // 16)
+
+    def run(qw, kw):
+        kc, vc = (torch.zeros(blocks, 16, hkv, d, device=DEV,
+                              dtype=torch.uint8 if fp8 else torch.bfloat16) for _ in range(2))
+        call = pk.qk_norm_rope_append_fp8 if fp8 else pk.qk_norm_rope_append
+        scales = (0.02, 0.03) if fp8 else ()
+        return call(q, k, v, pos, table, slots, kc, vc, *scales, q_weight=qw, k_weight=kw), kc, vc
+
+    both, none, q_only, k_only = run(w, w), run(None, None), run(w, None), run(None, w)
+    assert not torch.equal(both[0], none[0]) and not torch.equal(both[1], none[1])
+    for got, want_q, want_k in ((q_only, both, none), (k_only, none, both)):
+        assert torch.equal(got[0], want_q[0]) and torch.equal(got[1], want_k[1])
+        assert torch.equal(got[2], both[2])
+    assert pk.get_device_error(clear=True) == 0

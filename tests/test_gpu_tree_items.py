@@ -87,9 +87,9 @@ class Batch:
 
     def check(self, out, what=""):
         tol = self.tolerance()
-        for s in range(len(self.n)):
+        for s in np.flatnonzero(self.n):
             diff = (out[self.start[s]:self.start[s + 1]].double() - self.ref(s)).abs()
-            assert not self.n[s] or bool((diff <= tol).all()), (what, s, float(diff.max()), tol)
+            assert bool((diff <= tol).all()), (what, s, float(diff.max()), tol)
 
 
 # (query heads, KV heads, d, nodes): one row tile, and two
@@ -195,4 +195,68 @@ def test_non_finite_values_of_committed_keys_stay_in_their_element(pk, hq, hkv, 
     out = b.run(pk)
     assert torch.equal(out.isfinite(), want)
     assert torch.equal(out[want], clean[want])
+    assert pk.get_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(64, 8, 128), (32, 8, 64), (4, 4, 128), (16, 1, 64)])
+@pytest.mark.parametrize("seqs", [12, 40])
+def test_bound_above_the_trees(pk, hq, hkv, d, seqs):
+    # a bucket's bound instead of the largest tree's nodes: the second row tile has
+    # rows for some of the trees, for a part of its rows, or for none
+    for small in (True, False):
+        nodes = [1 + (5 * s) % 16 if small else (0, 1, 15, 17, 33, 40, 48, 64)[s % 8]
+                 for s in range(seqs)]
+        lens = [n + (97 * s) % 1500 for s, n in enumerate(nodes)]
+        b = Batch(hq, hkv, d, nodes, lens, seed=seqs + small)
+        out = torch.full((int(b.start[-1]), hq, d), float("nan"), device=DEV)
+        ws = pk.tree_attention_workspace(seqs, 64, hq, hkv, d, DEV)
+        b.run(pk, max_q_len=64, out=out, workspace=ws)
+        b.check(out, f"bound 64, small trees {small}")
+    assert pk.get_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(16, 2, 128), (8, 8, 128), (64, 4, 64), (3, 3, 64)])
+@pytest.mark.parametrize("seqs", [385, 900])
+def test_more_sequences_than_threads(pk, hq, hkv, d, seqs):
+    nodes = [(7 * s) % 12 for s in range(seqs)]
+    lens = [n + (53 * s) % 200 for s, n in enumerate(nodes)]
+    nodes[seqs // 2], lens[seqs // 2] = 64, 5000   # one of them long
+    b = Batch(hq, hkv, d, nodes, lens, seed=seqs)
+    b.check(b.run(pk))
+    assert pk.get_device_error(clear=True) == 0
+
+
+def test_pools_of_more_than_2_31_elements(pk):
+    # the step's calls on the last blocks of pools of 2.6e9 elements, against the same
+    # blocks in small pools
+    hq, hkv, d, n, L = 16, 8, 128, 20, 150
+    far, need = 160_000, -(-L // BS)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    qkv = torch.randn(n, hq + 2 * hkv, d, device=DEV, generator=g).bfloat16()
+    q, k, v = qkv.split([hq, hkv, hkv], 1)
+    small = [torch.randn(need, BS, hkv, d, device=DEV, generator=g).bfloat16() for _ in range(2)]
+    large = [torch.empty(far, BS, hkv, d, device=DEV, dtype=torch.bfloat16) for _ in range(2)]
+    assert large[0].numel() > 2 ** 31
+    for a, b in zip(large, small):
+        a[far - need:] = b
+    angles = torch.rand(L, d // 2, device=DEV, generator=g)
+    table = torch.cat([angles.cos(), angles.sin()], 1)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)  # noqa: E731
+    start, lens = i32([0, n]), i32([L])
+    parents = i32([-1] + [t // 2 for t in range(n - 1)])
+    mask, pos = pk.draft_tree_layout(parents, start, lens, max_q_len=n)
+    path, count = i32([[0, 2, 5, 12]]), i32([4])
+    got = []
+    for pools, first in ((small, 0), (large, far - need)):
+        slots = first * BS + torch.arange(L - n, L, device=DEV)
+        tables = torch.arange(first, first + need, device=DEV, dtype=torch.int32)[None].contiguous()
+        x = pk.qk_norm_rope_append(q, k, v, pos, table, slots, *pools)
+        out = pk.paged_tree_attention(x, start, mask, *pools, tables, lens, 0.09, max_q_len=n)
+        pools[1].view(-1, hkv, d)[slots[3], 2, 7] = float("inf")  # a visible node's V
+        inf = pk.paged_tree_attention(x, start, mask, *pools, tables, lens, 0.09, max_q_len=n)
+        new = pk.kv_accept_rows(*pools, tables, lens, start, path, count)
+        got.append([x, out, inf, new] + [p[first:first + need].clone() for p in pools])
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert not torch.equal(got[0][1], got[0][2])
     assert pk.get_device_error(clear=True) == 0
