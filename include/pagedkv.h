@@ -691,7 +691,8 @@ PKV_API int pkv_qk_norm_rope_append_fp8(const void* q, int64_t q_tok_stride, con
  *                  child of the last committed token).  Any other value counts
  *                  as -1 and sets PKV_DEVERR_BAD_TREE.
  *   context_lens : [num_seqs] int32, the tree included.
- *   max_q_len    : host bound on a tree's nodes, at most 64 (PKV_EUNSUPPORTED).
+ *   max_q_len    : host bound on a tree's nodes, at most 64 (PKV_EUNSUPPORTED);
+ *                  0 leaves every tree out, unflagged.
  *   tree_mask    : [total_q] uint64 out; bit u of node t's word: u is t or an
  *                  ancestor of t.
  *   positions    : [total_q] int64 out: context_len - n + depth, a root's depth
@@ -720,7 +721,8 @@ PKV_API int pkv_draft_tree_layout(const int32_t* parents, const int32_t* q_start
  * An infinity in V of a visible node comes through as itself; one in V of a
  * committed key makes its element of every row infinite or NaN (it is
  * multiplied by the two parts of a weight, the second of either sign or zero).
- * NaN in V, K or q makes NaN of what it reaches.
+ * NaN in V, K or q makes NaN of what it reaches.  The pools are bf16; there is
+ * no form over FP8 pools.
  *   q            : [total_q][q_heads][d_head] bf16, contiguous, 16-byte aligned.
  *   q_start, max_q_len, context_lens : as in pkv_draft_tree_layout; a sequence
  *                  outside those bounds, or with a context beyond the block
@@ -736,6 +738,9 @@ PKV_API int pkv_draft_tree_layout(const int32_t* parents, const int32_t* q_start
  * PKV_EUNSUPPORTED also for sizes whose key tiles pass 2^31: block tables of
  * more than about 1.8e9 positions, or the tiles (and two more each) of all row
  * groups of all KV heads of num_seqs such tables.
+ * max_q_len times the group (q_heads / kv_heads) above 128 selects a kernel for
+ * two tiles of 128 rows a pair, which trees of fewer rows pay for: give a
+ * captured call the bound of its bucket of tree sizes rather than 64.
  * Context lengths are read on the device only: no host bound is needed, and a
  * captured call may be replayed with other lengths, trees and tables.
  * pkv_paged_tree_attention_bf16out rounds the float32 result once to bf16

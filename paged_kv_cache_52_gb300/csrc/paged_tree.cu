@@ -30,8 +30,8 @@
 //    issues Q K^T, 10 loads V, 11 issues P V.  The rings run on across items;
 //    only Q and the accumulators change hands at an item's end.
 //  * S = Q K^T lands in tensor memory, the softmax overwrites it with P as
-//    bf16 hi + lo (two MMAs a step, error ~2^-17: a row may see very few
-//    keys, where P rounded to one bf16 would move the output by 2^-9), and
+//    bf16 hi + lo (two MMAs a step, an error of 2^-16 at most: a row may see very few
+//    keys, where P rounded to one bf16 would move the output by 2^-8), and
 //    P V reads P from tensor memory.
 //  * only tiles that reach the tree apply a mask: 128 bits a row, made from
 //    the 64-bit ancestor mask.  A masked key's P is 0, but 0 * NaN is not:
@@ -41,22 +41,26 @@
 //  * every wait is bounded; a timeout sets the error word and an abort flag,
 //    copies and MMAs in flight are drained and tensor memory is freed.
 //
-// What bounds it (us in a graph, 64 query and 8 KV heads of 128 unless said):
+// What bounds it (us in a graph at 2070 MHz, 64 query and 8 KV heads of 128 unless
+// said; shares from the profiler's counters):
 //  * 16 x 4096, 16 nodes: 51.  HBM in the middle (64 KB per SM in 2730 cycles =
-//    7 TB/s); 31 of them are the bytes.  The rest are the ends: 2.3 until the
-//    first pages are asked for, 3 until they are there, pieces that meet in a CTA
-//    (2-3 each), 4.5 for the merge.
-//  * 64 x 8192, 64 nodes (two row tiles): 870, the tensor cores' 585 with P as
-//    hi + lo.  A row tile's chain of scores, softmax and products, 4300 cycles a
-//    key tile for both, 1.4 times the MMAs at their full rate: the softmax's
-//    two halves (1300 cycles each), and MMAs that run at 48-75 cycles where
-//    N = 64 would need 32.
-//  * 2 x 131072, 27 nodes, 32 query heads of 64: 110 of 79 for the bytes; 16 MMAs of
-//    P V a tile with P from tensor memory take about as long with heads of 64
-//    as with 128.
-//  * 1 x 500, 8 nodes: 11.5, all latency: 1.3 for the split, 1.7 to the first
+//    7 TB/s), 58% of its peak over the kernel; 31 us are the bytes.  The rest are
+//    the ends: 2.3 until the first pages are asked for, 3 until they are there,
+//    pieces that meet in a CTA (2-3 each), 4.5 for the merge.
+//  * 64 x 8192, 64 nodes (two row tiles): 850-875, the tensor cores' 585 with P as
+//    hi + lo.  5500 cycles a key tile for both row tiles, of which the tensor
+//    pipe is busy for 56%: a row tile's chain of scores, softmax and products
+//    (the softmax's two halves 1300 cycles each).
+//  * 2 x 131072, 27 nodes, 32 query heads of 64: 107-111 (120 in some processes) of
+//    79 for the bytes.  HBM runs at 63% of its peak and the tensor pipe is busy for
+//    43% of the cycles, 770 of 1780 a tile: neither is full, and which wait of
+//    the chain fills the rest has not been shown.
+//  * 1 x 500, 8 nodes: 11.8, all latency: 1.3 for the split, 1.7 to the first
 //    page, 2.7 for one tile of each warpgroup, 2.5 for its end, 0.8 + 2.4 for
 //    the merge.
+//  * a bound above the trees: with max_q_len x group > 128 every tree takes two row
+//    tiles, also where the second has no rows.  max_q_len 64 instead of the trees' own:
+//    16 x 4096, 16 nodes 65.7 against 50.7, 64 x 700, 4 nodes 57.8 / 44.5, 2 x 131072 161 / 108.
 #include <algorithm>
 
 #include "pkv_device.cuh"
@@ -82,13 +86,13 @@ constexpr float kTrRescale = 8.0f;     // log2 units: move the running max when 
 constexpr float kTrMaxSum = 16777216.f;
 constexpr int kTrMaxStages = 4;
 // The fewest key tiles worth a piece: one for each softmax warpgroup (us with 2 / 1:
-// 1 x 2000, 16 nodes 18.1 / 22.1; three tiles whole / cut 11.45 / 11.9).
+// three tiles, 1 x 384, 8 nodes 11.6 / 11.8; 1 x 2000, 16 nodes 15.4 either way).
 constexpr int kTrMinTiles = 2;
 // Key tiles' time that a second piece costs a CTA: the first one's end and the
-// next one's start.  us with 1 / 2 / 3: 8 x 2000, 8 nodes 25.6 / 24.1 / 24.1, 64 x 700,
-// 4 nodes 49.2 / 48.6 / 49.7, 32 x 1000, 16 nodes 41.4 / 41.5 / 42.3, 16 x 4096, 16
-// nodes 50.4 / 50.9 / 49.5, 64 x 8192, 64 nodes 844 / 845 / 840 (without places for it
-// in the even split 1.6% more).
+// next one's start.  us with 1 / 2 / 3: 8 x 2000, 8 nodes 23.7 / 22.5 / 22.1, 64 x 700,
+// 4 nodes 44.8 / 44.5 / 44.0, 32 x 1000, 16 nodes 37.6 / 36.4 / 36.1, 16 x 4096, 16
+// nodes 50.8 / 50.7 / 49.8, 1 x 2000, 16 nodes 15.4 / 15.4 / 16.1, 2 x 131072, 27 nodes,
+// heads of 64 106.7 / 107.3 / 108.3.
 constexpr int kTrSlack = 2;
 constexpr int kTrPieces = 5;  // piece descriptions in shared memory
 
@@ -96,9 +100,9 @@ template <int D, int TILES>
 struct TreeSmem {
   // S, P and P V of a tile of heads of 128 go in two halves of 64 keys, so that
   // the products of one half and the next scores run while the other half is
-  // weighed; heads of 64, with a third buffer, keep them whole.  Measured in
-  // halves / whole, us: 64 x 8192, 64 nodes 860 / 923, 16 x 4096, 16 nodes 50.8 / 52.2,
-  // 64 x 700, 4 nodes 48.5 / 52.5; heads of 64, 2 x 131072, 27 nodes 117 / 109.
+  // weighed; heads of 64, with a third buffer, keep them whole.  us in halves / whole:
+  // 64 x 8192, 64 nodes 856 / 941, 16 x 4096, 16 nodes 50.7 / 52.1, 64 x 700, 4 nodes
+  // 44.5 / 47.6; heads of 64, 2 x 131072, 27 nodes 114.7 / 107.3.
   static constexpr int kParts = D == 128 ? 2 : 1;
   // Tensor memory: S/P buffers that the products take in turn, and the
   // warpgroups' accumulators.  Heads of 128: a buffer and an accumulator of 128
@@ -410,8 +414,9 @@ paged_tree_kernel(const __grid_constant__ CUtensorMap tmap_q,
   // ---- this CTA's range of the key tiles of all items
   // The grid's `lanes` equal parts take a share of the KV heads each.  Where there
   // is work for some CTAs only, they then lie all over the GPU (us, against one
-  // part: 1 x 500 12.3 / 12.9, 1 x 2000 17.5 / 18.0, 4 x 1000 17.0 / 17.5; 16 x 4096
-  // and larger the same).  CTAs that the division leaves over have no work.
+  // part: 1 x 500 11.8 / 12.4, 1 x 2000 15.4 / 16.8, 4 x 1000 16.7 / 17.4, 16 x 4096
+  // 50.7 / 51.8, 2 x 131072 with heads of 64 107 / 137; 64 x 8192 the same).  CTAs that
+  // the division leaves over have no work.
   const int ctas = gridDim.x / p.lanes, heads = p.kv_heads / p.lanes;
   const int part = blockIdx.x / ctas;
   const int c = part < p.lanes ? blockIdx.x - part * ctas : ctas;
@@ -1174,10 +1179,10 @@ tree_merge_kernel(const TreeParams p, int ctas) {
   float big = -INFINITY, tot = 0.f;
   // Several pieces' loads at a time, those beyond the last as pieces without
   // weight.  More at a time take registers, and with them the blocks that an SM
-  // holds: us with 2 / 3 / 4 / 8, heads of 128: 1 x 500, 8 nodes 11.5 / 11.4 / 11.5 /
-  // 11.5, 32 x 1000, 16 nodes 41.1 / 42.3 / 42.2 / 44.5, 16 x 4000, 64 nodes 112 / 114 /
-  // - / -; with 4 / 8, heads of 64: 1 x 30000, 27 nodes 26.9 / 26.3 (one at a time:
-  // 31.1).
+  // holds: us with 2 / 3 / 4 / 8, heads of 128: 1 x 500, 8 nodes 11.8 / 11.7 / 11.7 /
+  // 11.7, 64 x 700, 4 nodes 44.5 / 43.6 / 43.6 / 43.3, 32 x 1000, 16 nodes 36.4 / 37.3 /
+  // 37.4 / 39.4, 16 x 4000, 64 nodes 112.5 / 115.4 / 114.7 / 121.5; with 1 / 4 / 8, heads
+  // of 64: 1 x 30000, 27 nodes 34.7 / 28.9 / 28.8.
   constexpr int kAtOnce = D == 64 ? 8 : 2;
   if (lane < rows) {
 #pragma unroll 1
