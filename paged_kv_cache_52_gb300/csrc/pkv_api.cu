@@ -2068,7 +2068,8 @@ int pkv_kv_accept_rows(void* k_cache, int64_t k_layer_stride, void* v_cache,
   const int64_t pool_bytes = int64_t(cache.num_blocks) * cache.block_size * row_bytes;
   for (const int64_t s : {k_layer_stride, v_layer_stride})
     if (num_layers > 1 &&
-        (s < pool_bytes / elem_bytes || (s * elem_bytes) % 16 || s > (int64_t(1) << 60)))
+        (s < pool_bytes / elem_bytes || s > (int64_t(1) << 60) / num_layers ||
+         (s * elem_bytes) % 16))
       return PKV_EINVAL;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(block_tables, 4) ||
       !aligned(context_lens, 4) || !aligned(q_start, 4) || !aligned(accepted, 4) ||

@@ -64,3 +64,9 @@ def test_accept_rows_refuses_pools_that_lie_over_one_another(pk, layers, k, kste
 def test_accept_rows_refuses_lengths_that_lie_over_the_block_table(pk):
     for new in (1 << 24, (1 << 24) + 60):
         assert _accept(pk, 1, 0, 0, LAYER, 0, new=new, tables=1 << 24) == -1
+
+
+@pytest.mark.parametrize("kstep,vstep", [(1 << 60, 2 * LAYER), (2 * LAYER, 1 << 60)])
+def test_accept_rows_refuses_layers_that_no_address_reaches(pk, kstep, vstep):
+    # the last of 64 layers would lie 2^66 bytes on
+    assert _accept(pk, 64, 0, kstep, LAYER, vstep) == -1
