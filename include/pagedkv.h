@@ -898,6 +898,88 @@ PKV_API int pkv_paged_prefill_attention_fp8_limited(const void* q, const int32_t
                                                     size_t ws_bytes, pkv_stream_t stream);
 
 /*
+ * The block-scaled FP8 cache: pools of e4m3 codes as above, with a float32
+ * scale for each block of 16 tokens and KV head in place of one per pool
+ * (k_scales, v_scales: [num_blocks][kv_heads], contiguous).  A code c of block
+ * b and head h stands for e4m3(c) * scales[b][h], so a block of small values
+ * keeps its precision beside one of large values, and no calibration is
+ * needed: the append finds the scales.  d_head 64 or 128.
+ *
+ * pkv_kv_append_fp8_block_scaled -- quantizing append of each sequence's new
+ * rows.  Sequence s's new tokens are rows q_start[s] .. q_start[s+1]-1 of k and
+ * v and the last positions of its context (as the queries of
+ * pkv_paged_prefill_attention are).  For every block that receives rows, per
+ * head, K and V apart:
+ *   e     = the least whole number >= -126 with max |new element| <= 448 * 2^e
+ *   scale = max(old scale, 2^e); the old scale (and older rows) count only
+ *           where rows of the sequence lie before the new ones in the block
+ *   new rows stored as e4m3(x / scale); where the scale grew, the older rows
+ *           as e4m3(code * old scale / scale)  (nearest even, +-448 at most).
+ * Scales are powers of two, so a new code is its element rounded once, and
+ * code * scale is a bf16 value.  Infinities are left out of the maximum and
+ * stored as +-448; NaN is stored as NaN.
+ *   k, v : [num_tokens][kv_heads][d_head] bf16 rows, strides in elements, as in
+ *          pkv_kv_append.  Rows of no sequence (padding) are left out.
+ *   q_start : [num_seqs + 1] int32, non-decreasing, q_start[num_seqs] <=
+ *          num_tokens; a sequence may have no new rows.
+ *   context_lens : [num_seqs], the new rows included.
+ * Rows of a block behind the new ones keep what they held.  A block that
+ * receives rows belongs to one sequence (copy a shared one first:
+ * pkv_copy_blocks and pkv_copy_block_scales).  A sequence with more new rows
+ * than its context, with a context beyond the block table or with a q_start
+ * out of order is left out (PKV_DEVERR_BAD_QUERY_RANGE); a block id outside
+ * the pool skips its rows (PKV_DEVERR_BAD_BLOCK_ID).  The pools must not lie
+ * over one another, nor the scales (PKV_EINVAL).  No workspace.
+ *
+ * pkv_copy_block_scales -- the scales' part of pkv_copy_blocks: row pairs[i][1]
+ * of both arrays becomes a copy of row pairs[i][0].
+ */
+PKV_API int pkv_kv_append_fp8_block_scaled(const void* k, int64_t k_tok_stride, const void* v,
+                                           int64_t v_tok_stride, int64_t num_tokens,
+                                           const int32_t* q_start, int num_seqs,
+                                           const int32_t* block_tables, int max_blocks_per_seq,
+                                           const int32_t* context_lens, void* k_cache,
+                                           void* v_cache, float* k_scales, float* v_scales,
+                                           pkv_cache_desc cache, pkv_stream_t stream);
+PKV_API int pkv_copy_block_scales(float* k_scales, float* v_scales, pkv_cache_desc cache,
+                                  const int32_t* pairs, int32_t num_pairs, pkv_stream_t stream);
+
+/*
+ * pkv_paged_decode_attention_fp8_block_scaled -- pkv_paged_decode_attention
+ * over a block-scaled cache: the attention of the dequantized cache.  Any
+ * positive finite scales are taken.  Queries enter the product as f16, a row
+ * outside [2^-6, 2^15) brought into it by an exact power of two; the weights
+ * enter P V as f16, so an output element is off by at most 2^-10 * max|V| of
+ * the dequantized V.
+ *   max_context_len : host-side bound on context_lens.  Tokens of a longer
+ *               sequence are not attended and PKV_DEVERR_BAD_CONTEXT is set.
+ *   workspace : >= pkv_decode_fp8_block_scaled_workspace_bytes(...) device
+ *               bytes, 256-byte aligned (PKV_ENOMEM if NULL or smaller);
+ *               contents need no initialisation; calls that share it must be
+ *               ordered on the GPU.  Its size depends on the current device.
+ * Small batches (the pages of all pairs within a wave of CTAs) run in one
+ * launch, a cluster of CTAs for each (sequence, KV head) pair; others take the
+ * flat split.  Other arguments and errors are those of
+ * pkv_paged_decode_attention.
+ * pkv_paged_decode_attention_fp8_block_scaled_bf16out rounds the float32
+ * result once to bf16, bit for bit.
+ */
+PKV_API size_t pkv_decode_fp8_block_scaled_workspace_bytes(int num_seqs, int q_heads,
+                                                           int kv_heads, int d_head);
+PKV_API int pkv_paged_decode_attention_fp8_block_scaled(
+    const void* q, int num_seqs, int q_heads, const void* k_cache, const void* v_cache,
+    const float* k_scales, const float* v_scales, pkv_cache_desc cache,
+    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+    int max_context_len, float scale, float* out, void* workspace, size_t ws_bytes,
+    pkv_stream_t stream);
+PKV_API int pkv_paged_decode_attention_fp8_block_scaled_bf16out(
+    const void* q, int num_seqs, int q_heads, const void* k_cache, const void* v_cache,
+    const float* k_scales, const float* v_scales, pkv_cache_desc cache,
+    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+    int max_context_len, float scale, void* out, void* workspace, size_t ws_bytes,
+    pkv_stream_t stream);
+
+/*
  * Decode for callers that cannot allocate device memory.  The pages have no
  * counterpart to this entry point; it exists for callers that are handed
  * device buffers but may not call cudaMalloc (a fixed, pre-reserved memory

@@ -54,3 +54,10 @@ from .draft_tree import (  # noqa: F401,E402
     tree_attention,
     accept_rows,
 )
+
+from .block_scaled import (  # noqa: F401,E402
+    append_block_scaled,
+    attend,
+    block_scale,
+    dequantize_blocks,
+)

@@ -337,12 +337,79 @@ PyObject* accept_rows(PyObject* const* a) {
   return st == PKV_OK ? give(a[7], lens) : PyLong_FromLong(st);
 }
 
+// A block-scaled cache: pools of codes and their scales [NB, Hkv].
+struct BlockScaled : Pools {
+  float *ks, *vs;
+};
+
+BlockScaled block_scaled(PyObject* k, PyObject* v, PyObject* ks, PyObject* vs) {
+  BlockScaled p;
+  static_cast<Pools&>(p) = pools(k, v, false, true, false);
+  const int64_t nb = p.desc.num_blocks, hkv = p.desc.kv_heads;
+  p.ks = static_cast<float*>(packed(ks, "k_scales", at::kFloat, p.dev, {nb, hkv}));
+  p.vs = static_cast<float*>(packed(vs, "v_scales", at::kFloat, p.dev, {nb, hkv}));
+  return p;
+}
+
+// k, v, q_start, block_tables, context_lens, k_cache, v_cache, k_scales, v_scales
+PyObject* append_block_scaled(PyObject* const* a) {
+  const BlockScaled p = block_scaled(a[5], a[6], a[7], a[8]);
+  const Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
+  if (k.dim() != 3) refuse("k", "[T, Hkv, d]");
+  const int64_t T = k.size(0), hkv = p.desc.kv_heads, d = p.desc.d_head;
+  const int64_t sk = token_rows(k, "k", p.dev, T, hkv, d);
+  const int64_t sv = token_rows(v, "v", p.dev, T, hkv, d);
+  const TreeBatch b = tree_batch(a[2], a[4], p.dev);
+  int width;
+  const int32_t* tables = table(a[3], "block_tables", p.dev, b.S, &width);
+  const void *kp = k.data_ptr(), *vp = v.data_ptr();
+  const int st = launch(p.dev, [&](void* stream) {
+    return pkv_kv_append_fp8_block_scaled(kp, sk, vp, sv, T, b.q_start, b.S, tables, width, b.lens,
+                                          p.k, p.v, p.ks, p.vs, p.desc, stream);
+  });
+  if (st != PKV_OK) return PyLong_FromLong(st);
+  Py_RETURN_NONE;
+}
+
+// q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out,
+// max_context_len, workspace, bf16 out
+PyObject* decode_block_scaled(PyObject* const* a) {
+  const BlockScaled p = block_scaled(a[1], a[2], a[3], a[4]);
+  const Tensor& q = tensor(a[0], "q");
+  if (q.dim() != 3) refuse("q", "[S, Hq, d]");
+  const int64_t S = q.size(0), hq = q.size(1), d = p.desc.d_head;
+  const void* qp = packed(a[0], "q", at::kBFloat16, p.dev, {S, hq, d});
+  const auto* lens = static_cast<const int32_t*>(packed(a[6], "context_lens", at::kInt, p.dev, {S}));
+  int width;
+  const int32_t* tables = table(a[5], "block_tables", p.dev, S, &width);
+  const float scale = float(real(a[7]));
+  const int longest = int(whole(a[9], "max_context_len"));
+  const Tensor& ws = tensor(a[10], "workspace");
+  const int64_t ws_bytes = ws.numel();
+  void* wp = packed(a[10], "workspace", at::kByte, p.dev, {ws_bytes});
+  const int bf16 = PyObject_IsTrue(a[11]);
+  if (bf16 < 0) throw python_error();
+  const int ns = count(S, "q"), nq = count(hq, "q");
+  const Tensor out = result(a[8], "out", bf16 ? at::kBFloat16 : at::kFloat, p.dev, {S, hq, d});
+  void* op = out.data_ptr();
+  const int st = launch(p.dev, [&](void* stream) {
+    return bf16 ? pkv_paged_decode_attention_fp8_block_scaled_bf16out(
+                      qp, ns, nq, p.k, p.v, p.ks, p.vs, p.desc, tables, width, lens, longest, scale,
+                      op, wp, size_t(ws_bytes), stream)
+                : pkv_paged_decode_attention_fp8_block_scaled(
+                      qp, ns, nq, p.k, p.v, p.ks, p.vs, p.desc, tables, width, lens, longest, scale,
+                      static_cast<float*>(op), wp, size_t(ws_bytes), stream);
+  });
+  return st == PKV_OK ? give(a[8], out) : PyLong_FromLong(st);
+}
+
 #define PKV_METHOD(name, n) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<n, name>)), \
    METH_FASTCALL, nullptr}
 
 PyMethodDef methods[] = {PKV_METHOD(rope_append, 14), PKV_METHOD(tree_layout, 6),
                          PKV_METHOD(tree_attention, 12), PKV_METHOD(accept_rows, 8),
+                         PKV_METHOD(append_block_scaled, 9), PKV_METHOD(decode_block_scaled, 12),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,

@@ -1,0 +1,270 @@
+// The block-scaled FP8 cache: pools of e4m3 codes with one float32 scale for
+// each block of 16 tokens and KV head, [num_blocks][kv_heads].  Here: the
+// quantizing append, the widening of pages to bf16 rows for the prefill, and
+// the copy of scales that goes with a block copy.  (The decode is
+// paged_decode_block_scaled.cu.)
+//
+// The append.  For a block b and KV head h let x be the new rows that the call
+// writes into b.  Its scale becomes
+//   s = max(s_old, 2^e),  e = min{ e >= -126 : max |x| <= 448 2^e },
+// s_old counting only if older rows of the sequence lie before x in b; new
+// rows are stored as e4m3(x / s), older ones as e4m3(code s_old / s) when s
+// grew.  Powers of two: dividing by one rounds nothing, so a code is the
+// element rounded once; an older code moved to a larger scale only changes
+// where it falls among e4m3's subnormals; and a wider format holds code times
+// scale exactly.  A scale from the largest value itself would use up to one
+// bit more of e4m3's range, but none of its three fraction bits.
+//
+// One warp takes one (block, KV head, K or V): its up to 16 rows are in
+// registers between the maximum and the stores, so the inputs are read once.
+// Which rows form a block follows from q_start and the context lengths; the
+// CTA that holds a block's first new row takes the block.
+#include <algorithm>
+#include <climits>
+
+#include "pkv_device.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+
+static __device__ unsigned g_block_scaled_error = 0;
+
+constexpr int kBsTokens = 16;     // tokens per block
+constexpr int kBsThreads = 256;
+constexpr int kBsMaxRows = 16;    // new rows per CTA at most
+
+// The scale of values up to `amax` (bf16 bits of the largest finite
+// magnitude): 1.75 is 448's fraction, so a larger fraction needs one more.
+__device__ __forceinline__ float block_scale(uint32_t amax_bf16) {
+  const int e = int(((amax_bf16 << 16) + 0x1fffffu) >> 23) - 135;
+  return __uint_as_float(uint32_t(max(e, -126) + 127) << 23);
+}
+
+// The larger magnitudes of two bf16 pairs, infinities and NaN left out.
+__device__ __forceinline__ uint32_t finite_max2(uint32_t m, uint32_t w) {
+  const uint32_t a = w & 0x7fff7fffu;
+  return __vmaxu2(m, a & __vcmpltu2(a, 0x7f807f80u));
+}
+
+// Four floats -> four e4m3 codes (nearest even, finite overflow to +-448).
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
+// Four e4m3 codes -> floats (exact, through f16).
+__device__ __forceinline__ void e4m3x4_to_f32(uint32_t codes, float (&f)[4]) {
+  asm("{\n\t.reg .b16 c0, c1, h0, h1, h2, h3;\n\t.reg .b32 a, b;\n\t"
+      "mov.b32 {c0, c1}, %4;\n\t"
+      "cvt.rn.f16x2.e4m3x2 a, c0;\n\t"
+      "cvt.rn.f16x2.e4m3x2 b, c1;\n\t"
+      "mov.b32 {h0, h1}, a;\n\t"
+      "mov.b32 {h2, h3}, b;\n\t"
+      "cvt.f32.f16 %0, h0;\n\t"
+      "cvt.f32.f16 %1, h1;\n\t"
+      "cvt.f32.f16 %2, h2;\n\t"
+      "cvt.f32.f16 %3, h3;\n\t}"
+      : "=f"(f[0]), "=f"(f[1]), "=f"(f[2]), "=f"(f[3])
+      : "r"(codes));
+}
+
+__device__ __forceinline__ uint32_t rescaled(uint32_t codes, float ratio) {
+  float f[4];
+  e4m3x4_to_f32(codes, f);
+  return e4m3x4(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio);
+}
+
+// One (block, head) of one tensor, by one warp: `count` new rows from `src`
+// (stride elements apart) to the block's rows [first, first + count).
+template <int D>
+__device__ __forceinline__ void append_block(const __nv_bfloat16* __restrict__ src, int64_t stride,
+                                             uint8_t* __restrict__ block, int row_bytes,
+                                             float* __restrict__ scale, int first, int count) {
+  constexpr int kLanes = D / 8;           // lanes of a row, 8 elements each
+  constexpr int kRows = 32 / kLanes;      // rows of a step
+  constexpr int kSteps = kBsTokens / kRows;
+  const int lane = threadIdx.x & 31;
+  const int sub = lane / kLanes, col = (lane % kLanes) * 8;
+  const float old = first > 0 ? __ldcg(scale) : 0.f;
+  uint4 x[kSteps];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int r = i * kRows + sub;
+    x[i] = r < count ? __ldg(reinterpret_cast<const uint4*>(src + r * stride + col))
+                     : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i)
+    m = finite_max2(finite_max2(finite_max2(finite_max2(m, x[i].x), x[i].y), x[i].z), x[i].w);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float s = fmaxf(old, block_scale(max(m & 0xffffu, m >> 16)));
+  const float inv = 1.f / s;  // exact for a power of two
+  uint8_t* dst = block + size_t(first) * row_bytes + col;
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) {
+    const int r = i * kRows + sub;
+    if (r < count) {
+      const uint4 w = x[i];
+      *reinterpret_cast<uint2*>(dst + size_t(r) * row_bytes) = make_uint2(
+          e4m3x4(bf16_lo_to_f32(w.x) * inv, bf16_hi_to_f32(w.x) * inv, bf16_lo_to_f32(w.y) * inv,
+                 bf16_hi_to_f32(w.y) * inv),
+          e4m3x4(bf16_lo_to_f32(w.z) * inv, bf16_hi_to_f32(w.z) * inv, bf16_lo_to_f32(w.w) * inv,
+                 bf16_hi_to_f32(w.w) * inv));
+    }
+  }
+  if (s != old) {
+    if (first > 0) {  // the older rows move to the larger scale
+      const float ratio = old * inv;
+      for (int r = sub; r < first; r += kRows) {
+        uint2* at = reinterpret_cast<uint2*>(block + size_t(r) * row_bytes + col);
+        const uint2 w = *at;
+        *at = make_uint2(rescaled(w.x, ratio), rescaled(w.y, ratio));
+      }
+    }
+    if (lane == 0) *scale = s;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kBsThreads)
+append_block_scaled_kernel(const AppendBlockScaledArgs a, int rows_per_cta) {
+  griddep_wait();
+  griddep_launch_dependents();
+  __shared__ int seq_of[kBsMaxRows], hits[kBsMaxRows];
+  __shared__ int leaders, item_row[kBsMaxRows], item_first[kBsMaxRows], item_count[kBsMaxRows],
+      item_block[kBsMaxRows];
+  const int64_t r0 = int64_t(blockIdx.x) * rows_per_cta;
+  const int rows = int(min(int64_t(rows_per_cta), a.total - r0));
+  if (threadIdx.x < kBsMaxRows) hits[threadIdx.x] = 0;
+  if (threadIdx.x == 0) leaders = 0;
+  __syncthreads();
+  // whose rows these are: every sequence looks whether it holds some of them
+  bool bad = false;
+  for (int s = threadIdx.x; s < a.num_seqs; s += kBsThreads) {
+    const int qs = __ldg(a.q_start + s), qe = __ldg(a.q_start + s + 1);
+    bad |= qe < qs || qs < 0 || qe > a.total;
+    const int64_t lo = max(int64_t(qs), r0), hi = min(int64_t(qe), r0 + rows);
+    for (int64_t r = lo; r < hi; ++r) {
+      seq_of[r - r0] = s;
+      atomicAdd(&hits[r - r0], 1);
+    }
+  }
+  if (bad && blockIdx.x == 0) atomicOr(&g_block_scaled_error, kErrBadQueryRange);
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int i = threadIdx.x;
+    bool lead = false;
+    int first = 0, n_rows = 0, block = 0;
+    if (i < rows && hits[i] == 1) {  // a row of no sequence is left out
+      const int s = seq_of[i];
+      const int qs = __ldg(a.q_start + s), qe = __ldg(a.q_start + s + 1);
+      const int ctx = __ldg(a.context_lens + s);
+      const int r = int(r0) + i, n = qe - qs;
+      if (qs < 0 || qe > a.total || n > ctx || ctx > a.max_blocks_per_seq * kBsTokens) {
+        if (r == qs) atomicOr(&g_block_scaled_error, kErrBadQueryRange);
+      } else {
+        const int pos = ctx - n + (r - qs);
+        first = pos % kBsTokens;
+        if (first == 0 || r == qs) {
+          n_rows = min(kBsTokens - first, qe - r);
+          block = __ldg(a.block_tables + size_t(s) * a.max_blocks_per_seq + pos / kBsTokens);
+          lead = block >= 0 && block < a.num_blocks;
+          if (!lead) atomicOr(&g_block_scaled_error, kErrBadBlockId);
+        }
+      }
+    } else if (i < rows && hits[i] > 1) {
+      atomicOr(&g_block_scaled_error, kErrBadQueryRange);  // two sequences claim the row
+    }
+    const unsigned mask = __ballot_sync(0xffffffffu, lead);
+    if (lead) {
+      const int at = __popc(mask & ((1u << i) - 1));
+      item_row[at] = i;
+      item_first[at] = first;
+      item_count[at] = n_rows;
+      item_block[at] = block;
+    }
+    if (i == 0) leaders = __popc(mask);
+  }
+  __syncthreads();
+  const int row_bytes = a.kv_heads * D;
+  const int tasks = leaders * a.kv_heads * 2;
+  for (int t = threadIdx.x >> 5; t < tasks; t += kBsThreads / 32) {
+    const int item = t / (2 * a.kv_heads), rest = t - item * 2 * a.kv_heads;
+    const bool v = rest >= a.kv_heads;
+    const int h = v ? rest - a.kv_heads : rest;
+    const int64_t r = r0 + item_row[item];
+    const int block = item_block[item];
+    const int64_t stride = v ? a.v_stride : a.k_stride;
+    append_block<D>((v ? a.v : a.k) + r * stride + h * D, stride,
+                    (v ? a.v_cache : a.k_cache) + size_t(block) * kBsTokens * row_bytes + h * D,
+                    row_bytes, (v ? a.v_scales : a.k_scales) + size_t(block) * a.kv_heads + h,
+                    item_first[item], item_count[item]);
+  }
+}
+
+cudaError_t launch_append_block_scaled(const AppendBlockScaledArgs& a, int d_head,
+                                       cudaStream_t stream) {
+  // About one block's first row per CTA: a batch of single tokens gives every
+  // token a CTA, a prompt every block.
+  const int64_t firsts = std::min(a.total, a.total / kBsTokens + a.num_seqs);
+  int rows = 1;
+  while (rows < kBsMaxRows && int64_t(rows) * 2 * firsts <= a.total) rows *= 2;
+  const int64_t grid = (a.total + rows - 1) / rows;
+  if (grid > INT_MAX) return cudaErrorInvalidValue;
+  auto* kernel = d_head == 128 ? append_block_scaled_kernel<128> : append_block_scaled_kernel<64>;
+  return launch_after_previous(kernel, dim3(unsigned(grid)), dim3(kBsThreads), 0, stream, a, rows);
+}
+
+// The scales' part of a block copy: row dst of both arrays becomes row src.
+__global__ void __launch_bounds__(128)
+copy_block_scales_kernel(float* __restrict__ k_scales, float* __restrict__ v_scales,
+                         const int32_t* __restrict__ pairs, int num_pairs, int num_blocks,
+                         int kv_heads) {
+  const int64_t all = 2ll * num_pairs * kv_heads;
+  for (int64_t i = int64_t(blockIdx.x) * 128 + threadIdx.x; i < all; i += int64_t(gridDim.x) * 128) {
+    const int64_t p = i / (2 * kv_heads);
+    const int c = int(i - p * 2 * kv_heads);
+    const int32_t src = __ldg(pairs + 2 * p), dst = __ldg(pairs + 2 * p + 1);
+    if (src < 0 || src >= num_blocks || dst < 0 || dst >= num_blocks) {
+      if (c == 0) atomicOr(&g_block_scaled_error, kErrBadBlockId);
+      continue;
+    }
+    float* x = c < kv_heads ? k_scales + c : v_scales + (c - kv_heads);
+    x[size_t(dst) * kv_heads] = x[size_t(src) * kv_heads];
+  }
+}
+
+cudaError_t launch_copy_block_scales(float* k_scales, float* v_scales, const int32_t* pairs,
+                                     int num_pairs, int num_blocks, int kv_heads,
+                                     cudaStream_t stream, int num_sms) {
+  const int64_t want = (2ll * num_pairs * kv_heads + 127) / 128;
+  const int grid = int(std::min<int64_t>(want, int64_t(num_sms) * 8));
+  copy_block_scales_kernel<<<grid, 128, 0, stream>>>(k_scales, v_scales, pairs, num_pairs,
+                                                     num_blocks, kv_heads);
+  return cudaGetLastError();
+}
+
+// Device address of this unit's error word on the current device.
+cudaError_t block_scaled_error_word(unsigned** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_block_scaled_error);
+}
+
+unsigned read_block_scaled_error(bool clear) {
+  unsigned word = 0;
+  if (cudaMemcpyFromSymbol(&word, g_block_scaled_error, sizeof(word)) != cudaSuccess) return ~0u;
+  if (clear) {
+    const unsigned zero = 0;
+    if (cudaMemcpyToSymbol(g_block_scaled_error, &zero, sizeof(zero)) != cudaSuccess) return ~0u;
+  }
+  return word;
+}
+
+}  // namespace pkv

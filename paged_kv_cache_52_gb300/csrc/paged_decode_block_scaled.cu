@@ -1,0 +1,857 @@
+// Paged decode attention over the block-scaled FP8 cache: one query per
+// sequence, K = k_scales[block][head] * e4m3(code), V alike.
+//
+// Mathematics, per KV head with its group of G query heads, in log2 units:
+//   x_j = (q . code_j) * scale log2(e) * k_scale(block of j)
+//   m = max x,  l = sum 2^(x - m),  O = sum 2^(x - m) v_scale code_v / l
+// A block's scales are constants of 16 keys, so they join the arithmetic where
+// a whole block is one factor: K's in the factor that scores have anyway, V's
+// in the weights on their way to the second product.  The weights enter that
+// product as f16, at most 1 by construction: they are taken relative to the
+// largest V scale so far, vref, and O is kept in units of vref (rescaled when
+// vref grows, as when m grows), so a small scale costs no precision where a
+// larger one is about.  Queries are f16 after an exact power of two that
+// brings a row outside [2^-6, 2^15) into it.
+//
+// Bound by HBM: every code is read once, 4 flops for each byte and query head.
+// A warp owns a ring of pages (K and V of one KV head, fetched by TMA) and runs
+// the f16 warp MMAs on the converted codes; the page arithmetic is that of the
+// per-pool decode (pkv_decode_fp8_body.cuh), with the two factors.
+//
+// Two splits of the work:
+//  * cluster: a (sequence, KV head) pair belongs to a cluster of 1 to 8 CTAs
+//    of four warps, whose warps take the pair's pages in turn; the warps'
+//    results meet in shared memory and the CTAs' over distributed shared
+//    memory.  One launch, no workspace: for batches whose pages fit one wave.
+//  * flat: the pages of all sequences laid end to end are cut into equal
+//    ranges, one for each group of Hkv warps of a grid of one CTA per SM (as in
+//    paged_decode_flat.cu, whose merge joins the pieces).
+#include <cooperative_groups.h>
+
+#include <algorithm>
+#include <atomic>
+#include <climits>
+
+#include "pkv_decode_flat_body.cuh"
+#include "pkv_internal.h"
+
+namespace pkv {
+
+struct BsDecodeParams {
+  DecodeParams d;  // scale_log2 without the K scale; out_scale is not used
+  const float* k_scales;
+  const float* v_scales;
+  int max_blocks;  // pages attended per sequence at most
+};
+
+template <int D>
+struct BsPage {
+  static constexpr int kTileBytes = kBlockTokens * D;
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kStages = D == 128 ? 4 : 8;  // 16 KB a warp
+  static constexpr int kRingBytes = kStages * kStageBytes;
+  // byte address of 16-byte chunk c of row r: rows of 128 (64) bytes, written
+  // by TMA with the 128- (64-) byte swizzle
+  static __device__ __forceinline__ uint32_t at(int r, int c) {
+    return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  }
+};
+
+// Running state of one warp (layout of the accumulators as in F8Acc).
+template <int D, int G>
+struct BsAcc {
+  static constexpr int NH = (G + 7) / 8;
+  static constexpr int MT = D / 16;
+  float o[NH][MT][4];
+  float m[NH][2], l[NH][2];
+  float qmul[NH][2];  // what the queries were divided by
+  float vref, vinv;   // the largest V scale so far, and 1 / vref
+  uint32_t qf[NH][MT][2];
+
+  // The queries of rows row0 .. row0 + G - 1, in the order in which the K
+  // fragments arrive (see pkv_decode_fp8_body.cuh), and an empty state.
+  __device__ __forceinline__ void start(const __nv_bfloat16* q, size_t row0, int lane) {
+    const int gid = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+      const int head = 8 * nh + gid;
+      uint2 w[MT];
+      uint32_t top = 0;
+#pragma unroll
+      for (int kk = 0; kk < MT; ++kk) {
+        w[kk] = head < G ? __ldg(reinterpret_cast<const uint2*>(q + (row0 + head) * D + kk * 16 +
+                                                                4 * tig))
+                         : make_uint2(0, 0);
+        top = __vmaxu2(__vmaxu2(top, w[kk].x & 0x7fff7fffu), w[kk].y & 0x7fff7fffu);
+      }
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      // bf16 exponent of the largest element; 127 + [-6, 14] stays as it is
+      const int e = int(max(top & 0xffffu, top >> 16) >> 7);
+      const int shift = e < 121 || e > 141 ? min(max(e, 1), 254) - 127 : 0;
+      const float inv = __uint_as_float(uint32_t(127 - shift) << 23);  // 2^-shift, shift <= 127
+      const float mul = __uint_as_float(uint32_t(127 + shift) << 23);
+#pragma unroll
+      for (int kk = 0; kk < MT; ++kk) {
+        qf[nh][kk][0] = pack_f16x2(bf16_lo_to_f32(w[kk].x) * inv, bf16_hi_to_f32(w[kk].x) * inv);
+        qf[nh][kk][1] = pack_f16x2(bf16_lo_to_f32(w[kk].y) * inv, bf16_hi_to_f32(w[kk].y) * inv);
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        qmul[nh][c] = __shfl_sync(0xffffffffu, mul, (2 * tig + c) * 4);
+        m[nh][c] = -INFINITY;
+        l[nh][c] = 0.f;
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) o[nh][mt][0] = o[nh][mt][1] = o[nh][mt][2] = o[nh][mt][3] = 0.f;
+    }
+    vref = vinv = 0.f;
+  }
+
+  __device__ __forceinline__ void sum_l() {
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        l[nh][c] += __shfl_xor_sync(0xffffffffu, l[nh][c], 4);
+        l[nh][c] += __shfl_xor_sync(0xffffffffu, l[nh][c], 8);
+        l[nh][c] += __shfl_xor_sync(0xffffffffu, l[nh][c], 16);
+      }
+  }
+};
+
+// NP landed pages: page i at kbase[i], its first token tok0[i], its scales
+// ks[i] (times the softmax scale) and vs[i]; the sequence ends at `len`.
+template <int D, int G, int NP>
+__device__ __forceinline__ void bs_pages(BsAcc<D, G>& A, const uint32_t (&kbase)[NP],
+                                         const int (&tok0)[NP], const float (&ks)[NP],
+                                         const float (&vs)[NP], int len, int lane) {
+  using T = BsPage<D>;
+  constexpr int NH = BsAcc<D, G>::NH;
+  constexpr int MT = BsAcc<D, G>::MT;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int mi = lane >> 3, mr = lane & 7;
+  const int k_tok = (mi >> 1) * 8 + mr;
+  const int v_tok = (mi & 1) * 8 + mr;
+
+  // S^T = K Q^T, even and odd k-steps accumulated separately
+  float s[NP][NH][4], s_odd[NP][NH][4];
+#pragma unroll
+  for (int pg = 0; pg < NP; ++pg)
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[pg][nh][e] = s_odd[pg][nh][e] = 0.f;
+#pragma unroll
+  for (int kp = 0; kp < D / 32; ++kp) {
+#pragma unroll
+    for (int pg = 0; pg < NP; ++pg) {
+      uint32_t r0, r1, r2, r3;
+      ldsm_x4(kbase[pg] + T::at(k_tok, 2 * kp + (mi & 1)), r0, r1, r2, r3);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t a0, a1, a2, a3;
+        e4m3x4_to_f16x2x2(h ? r1 : r0, a0, a2);
+        e4m3x4_to_f16x2x2(h ? r3 : r2, a1, a3);
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+          mma_f16_16816(h ? s_odd[pg][nh] : s[pg][nh], a0, a1, a2, a3, A.qf[nh][2 * kp + h][0],
+                        A.qf[nh][2 * kp + h][1]);
+      }
+    }
+  }
+
+  // V's reference
+  float vtop = A.vref;
+#pragma unroll
+  for (int pg = 0; pg < NP; ++pg) vtop = fmaxf(vtop, vs[pg]);
+  bool all_same = vtop == A.vref;  // uniform over the warp
+  const float vold = A.vref;
+  if (!all_same) {
+    A.vref = vtop;
+    A.vinv = 1.f / vtop;
+  }
+  float vrel[NP];
+#pragma unroll
+  for (int pg = 0; pg < NP; ++pg) vrel[pg] = vs[pg] * A.vinv;
+
+  // online softmax per head column, in the log2 domain
+  bool k0_in[NP], k1_in[NP];
+#pragma unroll
+  for (int pg = 0; pg < NP; ++pg) {
+    k0_in[pg] = tok0[pg] + gid < len;
+    k1_in[pg] = tok0[pg] + gid + 8 < len;
+  }
+  uint32_t pb[NP][NH][2];
+  float alpha[NH][2];
+#pragma unroll
+  for (int nh = 0; nh < NH; ++nh) {
+    float pr[NP][4];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float x0[NP], x1[NP];
+      float mx = -INFINITY;
+#pragma unroll
+      for (int pg = 0; pg < NP; ++pg) {
+        const float f = ks[pg] * A.qmul[nh][c];
+        x0[pg] = k0_in[pg] ? (s[pg][nh][c] + s_odd[pg][nh][c]) * f : -INFINITY;
+        x1[pg] = k1_in[pg] ? (s[pg][nh][c + 2] + s_odd[pg][nh][c + 2]) * f : -INFINITY;
+        mx = fmaxf(mx, fmaxf(x0[pg], x1[pg]));
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      const float mn = fmaxf(A.m[nh][c], mx);
+      alpha[nh][c] = ex2(A.m[nh][c] - mn);
+      all_same = all_same && A.m[nh][c] == mn;
+      A.m[nh][c] = mn;
+      float add = 0.f;
+#pragma unroll
+      for (int pg = 0; pg < NP; ++pg) {
+        pr[pg][c] = ex2(x0[pg] - mn);
+        pr[pg][c + 2] = ex2(x1[pg] - mn);
+        add += pr[pg][c] + pr[pg][c + 2];
+      }
+      A.l[nh][c] = A.l[nh][c] * alpha[nh][c] + add;
+    }
+    // P^T as the B operand: (key, two heads) per lane -> (two keys, head)
+#pragma unroll
+    for (int pg = 0; pg < NP; ++pg) {
+      pb[pg][nh][0] = movmatrix_trans(pack_f16x2(pr[pg][0] * vrel[pg], pr[pg][1] * vrel[pg]));
+      pb[pg][nh][1] = movmatrix_trans(pack_f16x2(pr[pg][2] * vrel[pg], pr[pg][3] * vrel[pg]));
+    }
+  }
+  if (!__all_sync(0xffffffffu, all_same)) {
+    const float vmul = vold * A.vinv;  // 1 when vref stayed, 0 at first
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+      const float a0 = alpha[nh][0] * vmul, a1 = alpha[nh][1] * vmul;
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        A.o[nh][mt][0] *= a0;
+        A.o[nh][mt][1] *= a1;
+        A.o[nh][mt][2] *= a0;
+        A.o[nh][mt][3] *= a1;
+      }
+    }
+  }
+
+  // O^T += V^T P^T; codes of rows past the length may be NaN: zeroed
+  uint32_t vm0[NP], vm1[NP];
+#pragma unroll
+  for (int pg = 0; pg < NP; ++pg) {
+    vm0[pg] = vm1[pg] = 0xffffffffu;
+    if (tok0[pg] + kBlockTokens > len) {
+      const int k0 = tok0[pg] + 2 * tig;
+      vm0[pg] = (k0 < len ? 0x0000ffffu : 0u) | (k0 + 1 < len ? 0xffff0000u : 0u);
+      vm1[pg] = (k0 + 8 < len ? 0x0000ffffu : 0u) | (k0 + 9 < len ? 0xffff0000u : 0u);
+    }
+  }
+#pragma unroll
+  for (int cp = 0; cp < D / 32; ++cp) {
+#pragma unroll
+    for (int pg = 0; pg < NP; ++pg) {
+      uint32_t r0, r1, r2, r3;
+      ldsm_x4_trans(kbase[pg] + T::kTileBytes + T::at(v_tok, 2 * cp + (mi >> 1)), r0, r1, r2, r3);
+      r0 &= vm0[pg];
+      r1 &= vm1[pg];
+      r2 &= vm0[pg];
+      r3 &= vm1[pg];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t a0, a1, a2, a3;
+        e4m3x4_to_f16x2x2(__byte_perm(h ? r2 : r0, 0u, 0x3120), a0, a1);
+        e4m3x4_to_f16x2x2(__byte_perm(h ? r3 : r1, 0u, 0x3120), a2, a3);
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+          mma_f16_16816(A.o[nh][2 * cp + h], a0, a1, a2, a3, pb[pg][nh][0], pb[pg][nh][1]);
+      }
+    }
+  }
+}
+
+// One page's two boxes into a ring stage.
+template <int D>
+__device__ __forceinline__ void bs_issue(uint32_t dst, uint32_t bar, const CUtensorMap& tk,
+                                         const CUtensorMap& tv, int head, int id) {
+  mbar_arrive_expect_tx(bar, BsPage<D>::kStageBytes);
+  tma_load_4d(dst, &tk, bar, 0, head, 0, id);
+  tma_load_4d(dst + BsPage<D>::kTileBytes, &tv, bar, 0, head, 0, id);
+}
+
+// ------------------------------------------------------------ cluster split
+constexpr int kBsClWarps = 4;
+constexpr int kBsClMaxCtas = 8;    // per cluster: the portable limit
+constexpr int kBsClMaxPages = 32;  // per warp: one lane holds each page's id and scales
+
+template <int D, int G>
+struct BsCl {
+  static constexpr int kRings = kBsClWarps * BsPage<D>::kRingBytes;
+  static constexpr int kBarOff = kRings;
+  static constexpr int kOutOff = kBarOff + kBsClWarps * BsPage<D>::kStages * 8;
+  static constexpr int kRowFloats = G * D + 2 * G;  // O, then m and l
+  static constexpr int kSmemBytes = kOutOff + kRowFloats * 4 + 1024;
+  static_assert(kRowFloats * 4 <= BsPage<D>::kRingBytes, "a warp's result fits its ring");
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(kBsClWarps * 32, 3)
+decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                                   const __grid_constant__ CUtensorMap tmap_v,
+                                   const BsDecodeParams bp) {
+  griddep_wait();
+  griddep_launch_dependents();
+  using T = BsPage<D>;
+  using L = BsCl<D, G>;
+  constexpr int kStages = T::kStages;
+  constexpr unsigned kFull = 0xffffffffu;
+  const DecodeParams& p = bp.d;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = cluster.num_blocks(), rank = cluster.block_rank();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int pair = blockIdx.x / C;
+  const int seq = pair / p.kv_heads, kvh = pair - seq * p.kv_heads;
+  const uint32_t ring = smem_u32(smem + warp * T::kRingBytes);
+  const uint32_t bars = smem_u32(smem + L::kBarOff) + warp * kStages * 8;
+
+  // page i of this warp: the pair's page (i C + rank) W + warp
+  const int page0 = rank * kBsClWarps + warp, step = C * kBsClWarps;
+  int id = 0;
+  const int mine = page0 + lane * step;
+  if (mine < bp.max_blocks) id = __ldg(p.block_tables + size_t(seq) * p.max_blocks_per_seq + mine);
+  bool bad;
+  const int raw = __ldg(p.context_lens + seq);
+  const int nblk = flat_pages(raw, bp.max_blocks, bad);
+  if (bad && kvh == 0 && rank == 0 && threadIdx.x == 0) atomicOr(&g_decode_error, kErrBadContext);
+  const int len = raw < 0 ? 0 : min(raw, nblk * kBlockTokens);
+  const int cnt = nblk > page0 ? (nblk - page0 + step - 1) / step : 0;
+  float ks = 0.f, vs = 0.f;
+  if (lane < cnt) {
+    if (id >= 0 && id < p.num_blocks) {
+      ks = __ldg(bp.k_scales + size_t(id) * p.kv_heads + kvh) * p.scale_log2;
+      vs = __ldg(bp.v_scales + size_t(id) * p.kv_heads + kvh);
+    } else {
+      atomicOr(&g_decode_error, kErrBadBlockId);
+    }
+  }
+  if (lane == 0) {
+    for (int st = 0; st < kStages; ++st) mbar_init(bars + st * 8, 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  auto issue = [&](int i) {  // warp-wide; lane 0 issues
+    const int pid = __shfl_sync(kFull, id, i);
+    const int st = i % kStages;
+    if (lane == 0) bs_issue<D>(ring + st * T::kStageBytes, bars + st * 8, tmap_k, tmap_v, kvh, pid);
+  };
+  for (int i = 0; i < cnt && i < kStages; ++i) issue(i);
+  int issued = min(cnt, kStages);
+
+  const size_t row0 = size_t(seq) * p.q_heads + size_t(kvh) * G;
+  BsAcc<D, G> acc;
+  acc.start(p.q, row0, lane);
+  bool failed = false;
+  int i = 0;
+  while (i < cnt) {
+    const bool two = i + 1 < cnt;
+    bool landed = mbar_wait_bounded(bars + (i % kStages) * 8, (i / kStages) & 1);
+    if (two && landed)
+      landed = mbar_wait_bounded(bars + ((i + 1) % kStages) * 8, ((i + 1) / kStages) & 1);
+    if (!__all_sync(kFull, landed)) {
+      failed = true;
+      break;
+    }
+    const uint32_t b0 = ring + (i % kStages) * T::kStageBytes;
+    const int t0 = (page0 + i * step) * kBlockTokens;
+    const float ks0 = __shfl_sync(kFull, ks, i), vs0 = __shfl_sync(kFull, vs, i);
+    if (two) {
+      const uint32_t kb[2] = {b0, ring + ((i + 1) % kStages) * T::kStageBytes};
+      const int tk[2] = {t0, t0 + step * kBlockTokens};
+      const float k2[2] = {ks0, __shfl_sync(kFull, ks, i + 1)};
+      const float v2[2] = {vs0, __shfl_sync(kFull, vs, i + 1)};
+      bs_pages<D, G, 2>(acc, kb, tk, k2, v2, len, lane);
+    } else {
+      const uint32_t kb[1] = {b0};
+      const int tk[1] = {t0};
+      const float k1[1] = {ks0}, v1[1] = {vs0};
+      bs_pages<D, G, 1>(acc, kb, tk, k1, v1, len, lane);
+    }
+    __syncwarp();
+    const int n = two ? 2 : 1;
+    for (int j = i; j < i + n; ++j)
+      if (j + kStages < cnt) {
+        issue(j + kStages);
+        ++issued;
+      }
+    i += n;
+  }
+  if (failed) {
+    if (lane == 0) {
+      atomicOr(&g_decode_error, kErrWaitTimeout);
+      for (int k = i; k < issued; ++k)
+        (void)mbar_wait_bounded(bars + (k % kStages) * 8, (k / kStages) & 1);
+    }
+    __syncwarp();
+  }
+  acc.sum_l();
+
+  // the warp's result over its own ring: O in V's units, m, l
+  float* mo = reinterpret_cast<float*>(smem + warp * T::kRingBytes);
+#pragma unroll
+  for (int nh = 0; nh < BsAcc<D, G>::NH; ++nh)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int head = 8 * nh + 2 * tig + c;
+      if (head >= G) continue;
+#pragma unroll
+      for (int mt = 0; mt < BsAcc<D, G>::MT; ++mt)
+        *reinterpret_cast<float2*>(mo + head * D + 16 * mt + 2 * gid) =
+            make_float2(acc.o[nh][mt][c] * acc.vref, acc.o[nh][mt][c + 2] * acc.vref);
+      if (gid == 0) {
+        mo[G * D + head] = acc.m[nh][c];
+        mo[G * D + G + head] = acc.l[nh][c];
+      }
+    }
+  __syncthreads();
+  // the CTA's: normalised O, and its log2-sum-exp in place of m (-inf: no key)
+  float* part = reinterpret_cast<float*>(smem + L::kOutOff);
+  for (int x = threadIdx.x * 4; x < G * D; x += kBsClWarps * 32 * 4) {
+    const int row = x / D;
+    float big = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kBsClWarps; ++w)
+      big = fmaxf(big, reinterpret_cast<const float*>(smem + w * T::kRingBytes)[G * D + row]);
+    float tot = 0.f;
+    float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kBsClWarps; ++w) {
+      const float* wo = reinterpret_cast<const float*>(smem + w * T::kRingBytes);
+      const float m = wo[G * D + row];
+      const float wgt = m == -INFINITY ? 0.f : ex2(m - big);
+      const float4 o = *reinterpret_cast<const float4*>(wo + x);
+      tot += wo[G * D + G + row] * wgt;
+      val.x += o.x * wgt;
+      val.y += o.y * wgt;
+      val.z += o.z * wgt;
+      val.w += o.w * wgt;
+    }
+    const float inv = big == -INFINITY && tot == 0.f ? 0.f : 1.f / tot;
+    *reinterpret_cast<float4*>(part + x) =
+        make_float4(val.x * inv, val.y * inv, val.z * inv, val.w * inv);
+    if (x == row * D) part[G * D + row] = tot == 0.f ? -INFINITY : big + __log2f(tot);
+  }
+  if (C == 1) {
+    __syncthreads();
+    for (int x = threadIdx.x; x < G * D; x += kBsClWarps * 32) store_out(p, row0 * D + x, part[x]);
+    return;
+  }
+  cluster.sync();
+  // each CTA writes its share of the rows' elements
+  const int share = G * D / C;  // a multiple of 8: G D >= 64, C <= 8
+  for (int x = rank * share + int(threadIdx.x); x < (rank + 1) * share; x += kBsClWarps * 32) {
+    const int row = x / D;
+    float lse[kBsClMaxCtas], o[kBsClMaxCtas];
+#pragma unroll
+    for (int c = 0; c < kBsClMaxCtas; ++c) {
+      if (c < C) {
+        const float* other = cluster.map_shared_rank(part, c);
+        lse[c] = other[G * D + row];
+        o[c] = other[x];
+      } else {
+        lse[c] = -INFINITY;
+        o[c] = 0.f;
+      }
+    }
+    float big = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < kBsClMaxCtas; ++c) big = fmaxf(big, lse[c]);
+    float tot = 0.f, val = 0.f;
+#pragma unroll
+    for (int c = 0; c < kBsClMaxCtas; ++c) {
+      const float wgt = lse[c] == -INFINITY ? 0.f : ex2(lse[c] - big);
+      tot += wgt;
+      val += o[c] * wgt;
+    }
+    store_out(p, row0 * D + x, tot == 0.f ? 0.f : val / tot);
+  }
+  cluster.sync();  // no CTA leaves while another reads its shared memory
+}
+
+// --------------------------------------------------------------- flat split
+constexpr int kBsFlatMaxSeqs = 1024;
+constexpr int kBsFlatWarps = 12;
+
+template <int D>
+struct BsFlat {
+  static constexpr int kBarOff = kBsFlatWarps * BsPage<D>::kRingBytes;
+  static constexpr int kPreOff = kBarOff + kBsFlatWarps * BsPage<D>::kStages * 8;
+  static constexpr int kScanOff = kPreOff + (kBsFlatMaxSeqs + 1) * 4;
+  static constexpr int kSmemBytes = kScanOff + 32 * 4 + 1024;
+  static_assert(kSmemBytes <= 232448, "flat decode CTA does not fit in shared memory");
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(kBsFlatWarps * 32, 1)
+decode_block_scaled_flat_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                                const __grid_constant__ CUtensorMap tmap_v,
+                                const BsDecodeParams bp, const DecodeFlatParams fp) {
+  griddep_wait();
+  using T = BsPage<D>;
+  using L = BsFlat<D>;
+  constexpr int kStages = T::kStages;
+  constexpr int kThreads = kBsFlatWarps * 32;
+  constexpr unsigned kFull = 0xffffffffu;
+  const DecodeParams& p = bp.d;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  int32_t* pre = reinterpret_cast<int32_t*>(smem + L::kPreOff);
+  int32_t* scan = reinterpret_cast<int32_t*>(smem + L::kScanOff);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int S = fp.num_seqs;
+  const int Hkv = p.kv_heads;
+
+  // ---- pages per sequence and their prefix sum, alike in every CTA
+  const int per = (S + kThreads - 1) / kThreads;
+  const int s_begin = threadIdx.x * per;
+  int local = 0;
+  for (int k = 0; k < per; ++k) {
+    const int s = s_begin + k;
+    if (s < S) {
+      bool bad;
+      const int n = flat_pages(__ldg(p.context_lens + s), fp.max_blocks, bad);
+      if (bad && blockIdx.x == 0) atomicOr(&g_decode_error, kErrBadContext);
+      pre[s] = n;
+      local += n;
+    }
+  }
+  int incl = local;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) scan[warp] = incl;
+  const uint32_t ring = smem_u32(smem + warp * T::kRingBytes);
+  const uint32_t bars = smem_u32(smem + L::kBarOff) + warp * kStages * 8;
+  if (lane == 0) {
+    for (int st = 0; st < kStages; ++st) mbar_init(bars + st * 8, 1);
+    fence_barrier_init();
+  }
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tmap_k);
+    tma_prefetch_desc(&tmap_v);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int v = lane < kBsFlatWarps ? scan[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(kFull, v, o);
+      if (lane >= o) v += u;
+    }
+    if (lane < kBsFlatWarps) scan[lane] = v;
+  }
+  __syncthreads();
+  {
+    int base = (warp > 0 ? scan[warp - 1] : 0) + incl - local;
+    for (int k = 0; k < per; ++k) {
+      const int s = s_begin + k;
+      if (s < S) {
+        const int n = pre[s];
+        pre[s] = base;
+        base += n;
+      }
+    }
+    if (threadIdx.x == 0) pre[S] = scan[kBsFlatWarps - 1];
+  }
+  __syncthreads();
+  griddep_launch_dependents();
+  if (blockIdx.x == 0)
+    for (int s = threadIdx.x; s <= S; s += kThreads) fp.pre_out[s] = pre[s];
+
+  // ---- this warp's range [f0, f1) of the blocks laid end to end, head hw
+  const long long total = pre[S];
+  const long long groups = flat_groups((long long)gridDim.x * kBsFlatWarps, Hkv);
+  const long long gw = (long long)blockIdx.x * kBsFlatWarps + warp;
+  const long long g = gw / Hkv;
+  const int hw = int(gw - g * Hkv);
+  const long long c = flat_chunk(total, groups, fp.min_pages);
+  const long long f0 = g * c;
+  const long long f1 = g >= groups ? f0 : (f0 + c < total ? f0 + c : total);
+  const int cnt = f0 < f1 ? int(f1 - f0) : 0;
+  if (cnt == 0) return;  // no CTA-wide barrier follows
+
+  // Windows of 32 pages, lane k holding page 32 w + k: block id, sequence,
+  // block and scales.  Copies run at most kStages pages ahead, within the
+  // current window and the next; the one after is loaded a window ahead.
+  struct Window {
+    int id, seq, blk;
+    float ks, vs;
+  };
+  auto load_window = [&](int win) {
+    Window w = {0, -1, 0, 0.f, 0.f};
+    const long long f = f0 + (long long)win * 32 + lane;
+    if (f < f1) {
+      int lo = 0, hi = S - 1;  // the last sequence that starts at or before f
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= f) lo = mid;
+        else hi = mid - 1;
+      }
+      w.seq = lo;
+      w.blk = int(f - pre[lo]);
+      w.id = __ldg(p.block_tables + size_t(lo) * p.max_blocks_per_seq + w.blk);
+      if (w.id >= 0 && w.id < p.num_blocks) {
+        w.ks = __ldg(bp.k_scales + size_t(w.id) * Hkv + hw) * p.scale_log2;
+        w.vs = __ldg(bp.v_scales + size_t(w.id) * Hkv + hw);
+      } else if (hw == 0) {
+        atomicOr(&g_decode_error, kErrBadBlockId);
+      }
+    }
+    return w;
+  };
+  int wcur = 0;
+  Window wc = load_window(0), wn = load_window(1), wp = load_window(2);
+  auto issue = [&](int j) {
+    const int id = __shfl_sync(kFull, (j >> 5) == wcur ? wc.id : wn.id, j & 31);
+    const int st = j % kStages;
+    if (lane == 0) bs_issue<D>(ring + st * T::kStageBytes, bars + st * 8, tmap_k, tmap_v, hw, id);
+  };
+  for (int j = 0; j < cnt && j < kStages; ++j) issue(j);
+  int issued = min(cnt, kStages);
+
+  BsAcc<D, G> acc;
+  int cur_seq = -1, cur_first = 0, cur_last = 0, cur_len = 0, cur_end = 0;
+  // the finished piece: the output when it is the pair's whole context, else
+  // its normalised partial at slot (sequence + g) Hkv + head (for one head
+  // the pieces are ordered by sequence and range alike: no two share a slot)
+  auto flush = [&]() {
+    acc.sum_l();
+    const bool whole = cur_first == 0 && cur_last == cur_end - 1;
+    const size_t row0 = size_t(cur_seq) * p.q_heads + size_t(hw) * G;
+    const size_t slot = (size_t(cur_seq) + size_t(g)) * Hkv + hw;
+#pragma unroll
+    for (int nh = 0; nh < BsAcc<D, G>::NH; ++nh)
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        const int head = 8 * nh + 2 * tig + cc;
+        if (head >= G) continue;
+        const float inv = acc.vref / acc.l[nh][cc];
+#pragma unroll
+        for (int mt = 0; mt < BsAcc<D, G>::MT; ++mt) {
+          const int dim = 16 * mt + 2 * gid;
+          const float v0 = acc.o[nh][mt][cc] * inv, v1 = acc.o[nh][mt][cc + 2] * inv;
+          if (whole) {
+            store_out(p, (row0 + head) * D + dim, v0);
+            store_out(p, (row0 + head) * D + dim + 1, v1);
+          } else {
+            *reinterpret_cast<float2*>(p.part_o + (slot * G + head) * D + dim) = make_float2(v0, v1);
+          }
+        }
+        if (!whole && gid == 0) p.part_lse[slot * G + head] = acc.m[nh][cc] + __log2f(acc.l[nh][cc]);
+      }
+  };
+
+  bool failed = false;
+  int i = 0;
+  while (i < cnt) {
+    const bool in0 = (i >> 5) == wcur, in1 = ((i + 1) >> 5) == wcur;
+    const int seq0 = __shfl_sync(kFull, in0 ? wc.seq : wn.seq, i & 31);
+    const int blk0 = __shfl_sync(kFull, in0 ? wc.blk : wn.blk, i & 31);
+    const int seq1 = __shfl_sync(kFull, in1 ? wc.seq : wn.seq, (i + 1) & 31);
+    const bool two = i + 1 < cnt && seq1 == seq0;
+    if (seq0 != cur_seq) {
+      if (cur_seq >= 0) flush();
+      cur_seq = seq0;
+      cur_first = blk0;
+      cur_end = pre[seq0 + 1] - pre[seq0];
+      const int raw = __ldg(p.context_lens + seq0);
+      cur_len = raw < cur_end * kBlockTokens ? raw : cur_end * kBlockTokens;
+      acc.start(p.q, size_t(seq0) * p.q_heads + size_t(hw) * G, lane);
+    }
+    bool landed = mbar_wait_bounded(bars + (i % kStages) * 8, (i / kStages) & 1);
+    if (two && landed)
+      landed = mbar_wait_bounded(bars + ((i + 1) % kStages) * 8, ((i + 1) / kStages) & 1);
+    if (!__all_sync(kFull, landed)) {
+      failed = true;
+      break;
+    }
+    const uint32_t b0 = ring + (i % kStages) * T::kStageBytes;
+    const float ks0 = __shfl_sync(kFull, in0 ? wc.ks : wn.ks, i & 31);
+    const float vs0 = __shfl_sync(kFull, in0 ? wc.vs : wn.vs, i & 31);
+    if (two) {
+      const uint32_t kb[2] = {b0, ring + ((i + 1) % kStages) * T::kStageBytes};
+      const int tk[2] = {blk0 * kBlockTokens, (blk0 + 1) * kBlockTokens};
+      const float k2[2] = {ks0, __shfl_sync(kFull, in1 ? wc.ks : wn.ks, (i + 1) & 31)};
+      const float v2[2] = {vs0, __shfl_sync(kFull, in1 ? wc.vs : wn.vs, (i + 1) & 31)};
+      bs_pages<D, G, 2>(acc, kb, tk, k2, v2, cur_len, lane);
+    } else {
+      const uint32_t kb[1] = {b0};
+      const int tk[1] = {blk0 * kBlockTokens};
+      const float k1[1] = {ks0}, v1[1] = {vs0};
+      bs_pages<D, G, 1>(acc, kb, tk, k1, v1, cur_len, lane);
+    }
+    cur_last = blk0 + (two ? 1 : 0);
+    __syncwarp();
+    const int n = two ? 2 : 1;
+    for (int j = i; j < i + n; ++j)
+      if (j + kStages < cnt) {
+        issue(j + kStages);
+        ++issued;
+      }
+    i += n;
+    if ((i >> 5) != wcur && i < cnt) {
+      wcur = i >> 5;
+      wc = wn;
+      wn = wp;
+      wp = load_window(wcur + 2);
+    }
+  }
+  if (failed) {
+    if (lane == 0) {
+      atomicOr(&g_decode_error, kErrWaitTimeout);
+      for (int k = i; k < issued; ++k)
+        (void)mbar_wait_bounded(bars + (k % kStages) * 8, (k / kStages) & 1);
+    }
+    __syncwarp();
+    return;
+  }
+  flush();
+}
+
+// ------------------------------------------------------------------- launch
+namespace {
+
+template <int D, int G>
+cudaError_t launch_cluster(const BsDecodeParams& bp, int num_seqs, int ctas,
+                           const CUtensorMap* tk, const CUtensorMap* tv, cudaStream_t stream) {
+  using L = BsCl<D, G>;
+  static std::atomic<int> attr_done[kAttrMaxDevices];
+  cudaError_t e = set_smem_limit_once(decode_block_scaled_cluster_kernel<D, G>, L::kSmemBytes,
+                                      attr_done);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(num_seqs * bp.d.kv_heads * ctas));
+  cfg.blockDim = dim3(kBsClWarps * 32);
+  cfg.dynamicSmemBytes = L::kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = unsigned(ctas);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, decode_block_scaled_cluster_kernel<D, G>, *tk, *tv, bp);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <int D, int G>
+cudaError_t launch_flat(const BsDecodeParams& bp, const DecodeFlatParams& fp, int ctas,
+                        const CUtensorMap* tk, const CUtensorMap* tv, cudaStream_t stream) {
+  using L = BsFlat<D>;
+  static std::atomic<int> attr_done[kAttrMaxDevices];
+  cudaError_t e =
+      set_smem_limit_once(decode_block_scaled_flat_kernel<D, G>, L::kSmemBytes, attr_done);
+  if (e != cudaSuccess) return e;
+  e = launch_after_previous(decode_block_scaled_flat_kernel<D, G>, dim3(unsigned(ctas)),
+                            dim3(kBsFlatWarps * 32), L::kSmemBytes, stream, *tk, *tv, bp, fp);
+  if (e != cudaSuccess) return e;
+  return launch_decode_flat_merge(bp.d, fp, D, stream);
+}
+
+// CTAs of a pair's cluster, or 0 for the flat split.
+int cluster_ctas(long long pairs, int max_blocks, int num_sms) {
+  const long long slots = 3ll * num_sms;
+  int c = 1;
+  while (c < kBsClMaxCtas && pairs * c * 2 <= slots && max_blocks > c * kBsClWarps) c *= 2;
+  if (pairs * c > slots || max_blocks > c * kBsClWarps * kBsClMaxPages) return 0;
+  return c;
+}
+
+}  // namespace
+
+int decode_block_scaled_warps() { return kBsFlatWarps; }
+int decode_block_scaled_flat_seqs() { return kBsFlatMaxSeqs; }
+
+cudaError_t launch_decode_block_scaled(const DecodeBlockScaledArgs& a, const CUtensorMap* tk,
+                                       const CUtensorMap* tv, int num_sms, cudaStream_t stream) {
+  const int group = a.q_heads / a.kv_heads;
+  const size_t elem = a.out_bf16 ? 2 : 4;
+  const int max_blocks = std::min(a.max_blocks_per_seq, (a.max_context_len - 1) / kBlockTokens + 1);
+  BsDecodeParams bp = {};
+  DecodeParams& d = bp.d;
+  d.part_o = a.part_o;
+  d.part_lse = a.part_lse;
+  d.q_heads = a.q_heads;
+  d.kv_heads = a.kv_heads;
+  d.num_blocks = a.num_blocks;
+  d.max_blocks_per_seq = a.max_blocks_per_seq;
+  d.scale_log2 = a.scale_log2;
+  d.out_scale = 1.f;
+  d.out_bf16 = a.out_bf16 ? 1 : 0;
+  bp.k_scales = a.k_scales;
+  bp.v_scales = a.v_scales;
+  bp.max_blocks = max_blocks;
+  const long long all_pairs = (long long)a.num_seqs * a.kv_heads;
+  const int ctas = cluster_ctas(all_pairs, max_blocks, num_sms);
+  // the flat split's prefix sums hold 1024 sequences: more go in turn
+  const int chunk = ctas ? a.num_seqs : kBsFlatMaxSeqs;
+  for (int s = 0; s < a.num_seqs; s += chunk) {
+    const int n = std::min(chunk, a.num_seqs - s);
+    const size_t row = size_t(s) * a.q_heads * a.d_head;
+    d.q = static_cast<const __nv_bfloat16*>(a.q) + row;
+    d.out = reinterpret_cast<float*>(static_cast<char*>(a.out) + row * elem);
+    d.block_tables = a.block_tables + size_t(s) * a.max_blocks_per_seq;
+    d.context_lens = a.context_lens + s;
+    DecodeFlatParams fp;
+    fp.pre_out = a.pre;
+    fp.num_seqs = n;
+    fp.max_blocks = max_blocks;
+    fp.total_warps = num_sms * kBsFlatWarps;
+    fp.min_pages = kFlatMinPages;
+    cudaError_t e = cudaErrorInvalidValue;
+#define PKV_BS_CASE(DD, GG)                                                       \
+  if (a.d_head == DD && group == GG)                                              \
+    e = ctas ? launch_cluster<DD, GG>(bp, n, ctas, tk, tv, stream)                \
+             : launch_flat<DD, GG>(bp, fp, num_sms, tk, tv, stream)
+    PKV_BS_CASE(128, 1);
+    PKV_BS_CASE(128, 2);
+    PKV_BS_CASE(128, 4);
+    PKV_BS_CASE(128, 8);
+    PKV_BS_CASE(128, 16);
+    PKV_BS_CASE(64, 1);
+    PKV_BS_CASE(64, 2);
+    PKV_BS_CASE(64, 4);
+    PKV_BS_CASE(64, 8);
+    PKV_BS_CASE(64, 16);
+#undef PKV_BS_CASE
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+// Device address of this unit's error word on the current device.
+cudaError_t decode_block_scaled_error_word(unsigned** word) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(word), g_decode_error);
+}
+
+unsigned read_decode_block_scaled_error(bool clear) {
+  unsigned word = 0;
+  if (cudaMemcpyFromSymbol(&word, g_decode_error, sizeof(word)) != cudaSuccess) return ~0u;
+  if (clear) {
+    const unsigned zero = 0;
+    if (cudaMemcpyToSymbol(g_decode_error, &zero, sizeof(zero)) != cudaSuccess) return ~0u;
+  }
+  return word;
+}
+
+}  // namespace pkv

@@ -137,7 +137,8 @@ bool encode_out_map(CUtensorMap* map, void* out, int total_q, int q_heads, int d
 }
 
 // FP8 pool [num_blocks][16][kv_heads][d_head] of e4m3 codes (1 byte): one box
-// is a whole 128-byte row x 16 tokens of one head, 128-byte swizzled.
+// is a whole row (128 or 64 bytes) x 16 tokens of one head, swizzled over the
+// row's length.
 bool encode_pool_map_fp8(CUtensorMap* map, const void* base, const pkv_cache_desc& c) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
   if (!enc) return false;
@@ -149,7 +150,8 @@ bool encode_pool_map_fp8(CUtensorMap* map, const void* base, const pkv_cache_des
   const cuuint32_t box[4] = {cuuint32_t(c.d_head), 1, cuuint32_t(c.block_size), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides,
-                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   c.d_head == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
@@ -1697,7 +1699,7 @@ namespace {
 // atomic step, so a bit raised meanwhile by a kernel on another stream stays
 // for the next query instead of being lost -- and stores the OR.
 struct ErrorWordSet {
-  unsigned* word[12];
+  unsigned* word[16];
   int count;
   int clear;
 };
@@ -1715,14 +1717,17 @@ std::mutex g_collect_mutex;  // one collection in flight per process
 
 int collect_error_words(cudaStream_t stream, bool clear, unsigned* word) {
   ErrorWordSet s = {};
-  cudaError_t (*const getters[12])(unsigned**) = {
+  cudaError_t (*const getters[])(unsigned**) = {
       pkv::append_error_word, pkv::decode_error_word, pkv::decode_fp8_error_word,
       pkv::prefill_error_word, pkv::verify_error_word, pkv::probe_error_word,
       pkv::mixed_decode_error_word, pkv::mixed_prefill_error_word, pkv::decode_flat_error_word,
-      pkv::rope_error_word, pkv::draft_error_word, pkv::tree_error_word};
-  for (int i = 0; i < 12; ++i)
+      pkv::rope_error_word, pkv::draft_error_word, pkv::tree_error_word,
+      pkv::block_scaled_error_word, pkv::decode_block_scaled_error_word};
+  constexpr int kWords = int(sizeof(getters) / sizeof(getters[0]));
+  static_assert(kWords <= int(sizeof(s.word) / sizeof(s.word[0])), "room for every unit's word");
+  for (int i = 0; i < kWords; ++i)
     if (getters[i](&s.word[i]) != cudaSuccess) return PKV_ECUDA;
-  s.count = 12;
+  s.count = kWords;
   s.clear = clear ? 1 : 0;
   std::lock_guard<std::mutex> lock(g_collect_mutex);
   collect_error_words_kernel<<<1, 1, 0, stream>>>(s);
@@ -1767,10 +1772,13 @@ int pkv_get_device_error(unsigned int* word, int clear) {
   const unsigned r = pkv::read_rope_error(clear != 0);
   const unsigned dr = pkv::read_draft_error(clear != 0);
   const unsigned t = pkv::read_tree_error(clear != 0);
+  const unsigned bs = pkv::read_block_scaled_error(clear != 0);
+  const unsigned db = pkv::read_decode_block_scaled_error(clear != 0);
   if (a == ~0u || d == ~0u || f == ~0u || d8 == ~0u || v == ~0u || w == ~0u || m == ~0u ||
-      fl == ~0u || r == ~0u || dr == ~0u || t == ~0u)
+      fl == ~0u || r == ~0u || dr == ~0u || t == ~0u ||
+      bs == ~0u || db == ~0u)
     return PKV_ECUDA;
-  *word = a | d | f | d8 | v | w | m | fl | r | dr | t;
+  *word = a | d | f | d8 | v | w | m | fl | r | dr | t | bs | db;
   return PKV_OK;
 }
 
@@ -2108,6 +2116,200 @@ int pkv_kv_accept_rows(void* k_cache, int64_t k_layer_stride, void* v_cache,
   a.col_blocks = 0;
   const cudaError_t e =
       pkv::launch_accept_rows(a, num_layers, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The block-scaled FP8 cache: append, decode, copy of scales.
+// ---------------------------------------------------------------------------
+namespace {
+
+// The sizes that every call over a block-scaled cache takes.
+int check_block_scaled(const pkv_cache_desc& c) {
+  const int st = check_cache_desc(c);
+  if (st != PKV_OK) return st;
+  if (c.d_head != 64 && c.d_head != 128) return PKV_EUNSUPPORTED;
+  if (int64_t(c.kv_heads) * c.d_head > (1 << 24)) return PKV_EUNSUPPORTED;
+  return PKV_OK;
+}
+
+// Workspace of the flat split: partial rows, their log2-sum-exps, the prefix
+// sums of one launch's sequences.
+struct BlockScaledDecodeLayout {
+  int sms = 0;
+  size_t lse_off = 0, pre_off = 0, total = 0;
+};
+
+int block_scaled_decode_layout(int num_seqs, int q_heads, int kv_heads, int d_head,
+                               BlockScaledDecodeLayout* w) {
+  if (num_seqs < 0 || q_heads <= 0 || kv_heads <= 0) return PKV_EINVAL;
+  if (q_heads % kv_heads || !supported_group(q_heads / kv_heads)) return PKV_EUNSUPPORTED;
+  if (d_head != 64 && d_head != 128) return PKV_EUNSUPPORTED;
+  w->sms = current_device_sms();
+  if (w->sms <= 0) w->sms = 152;  // no device: the size for a GB300
+  const long long warps = (long long)w->sms * pkv::decode_block_scaled_warps();
+  if (kv_heads > warps) return PKV_EUNSUPPORTED;
+  const int seqs = std::min(num_seqs, pkv::decode_block_scaled_flat_seqs());
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t rows =
+      (size_t(seqs) * size_t(kv_heads) + size_t(warps)) * size_t(q_heads / kv_heads);
+  w->lse_off = up(rows * size_t(d_head) * 4);
+  w->pre_off = w->lse_off + up(rows * 4);
+  w->total = w->pre_off + up((size_t(seqs) + 1) * 4);
+  return PKV_OK;
+}
+
+int decode_block_scaled(const void* q, int num_seqs, int q_heads, const void* k_cache,
+                        const void* v_cache, const float* k_scales, const float* v_scales,
+                        const pkv_cache_desc& cache, const int32_t* block_tables,
+                        int max_blocks_per_seq, const int32_t* context_lens, int max_context_len,
+                        float scale, void* out, bool out_bf16, void* workspace, size_t ws_bytes,
+                        pkv_stream_t stream) {
+  int st = check_block_scaled(cache);
+  if (st != PKV_OK) return st;
+  if (max_context_len < 0) return PKV_EINVAL;
+  BlockScaledDecodeLayout w;
+  st = block_scaled_decode_layout(num_seqs, q_heads, cache.kv_heads, cache.d_head, &w);
+  if (st != PKV_OK) return st;
+  if (num_seqs == 0) return PKV_OK;
+  if (!q || !k_cache || !v_cache || !k_scales || !v_scales || !block_tables || !context_lens ||
+      !out || max_blocks_per_seq <= 0 || !std::isfinite(scale))
+    return PKV_EINVAL;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(block_tables, 4) ||
+      !aligned(context_lens, 4) || !aligned(out, out_bf16 ? 2 : 4))
+    return PKV_EINVAL;
+  // positions in 32 bits, the pairs and their clusters within a grid
+  if (max_blocks_per_seq > INT32_MAX / kBlockSize ||
+      (long long)num_seqs * cache.kv_heads > INT32_MAX / 8)
+    return PKV_EUNSUPPORTED;
+  if (!workspace || ws_bytes < w.total) return PKV_ENOMEM;
+  if (!aligned(workspace, 256)) return PKV_EINVAL;
+  if (current_device_sms() <= 0) return PKV_ECUDA;
+  CUtensorMap tk, tv;
+  if (!encode_pool_map_fp8(&tk, k_cache, cache) || !encode_pool_map_fp8(&tv, v_cache, cache))
+    return PKV_ECUDA;
+  char* ws = static_cast<char*>(workspace);
+  pkv::DecodeBlockScaledArgs a;
+  a.q = q;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.out = out;
+  a.out_bf16 = out_bf16;
+  a.part_o = reinterpret_cast<float*>(ws);
+  a.part_lse = reinterpret_cast<float*>(ws + w.lse_off);
+  a.pre = reinterpret_cast<int32_t*>(ws + w.pre_off);
+  a.num_seqs = num_seqs;
+  a.q_heads = q_heads;
+  a.kv_heads = cache.kv_heads;
+  a.d_head = cache.d_head;
+  a.num_blocks = cache.num_blocks;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.max_context_len = std::max(max_context_len, 1);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  const cudaError_t e = pkv::launch_decode_block_scaled(a, &tk, &tv, w.sms,
+                                                        static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pkv_kv_append_fp8_block_scaled(const void* k, int64_t k_tok_stride, const void* v,
+                                   int64_t v_tok_stride, int64_t num_tokens,
+                                   const int32_t* q_start, int num_seqs,
+                                   const int32_t* block_tables, int max_blocks_per_seq,
+                                   const int32_t* context_lens, void* k_cache, void* v_cache,
+                                   float* k_scales, float* v_scales, pkv_cache_desc cache,
+                                   pkv_stream_t stream) {
+  int st = check_block_scaled(cache);
+  if (st != PKV_OK) return st;
+  if (num_tokens < 0 || num_seqs < 0) return PKV_EINVAL;
+  if (num_tokens > INT32_MAX) return PKV_EUNSUPPORTED;
+  if (num_tokens == 0 || num_seqs == 0) return PKV_OK;
+  if (!k || !v || !q_start || !block_tables || !context_lens || !k_cache || !v_cache ||
+      !k_scales || !v_scales || max_blocks_per_seq <= 0)
+    return PKV_EINVAL;
+  const int64_t row = int64_t(cache.kv_heads) * cache.d_head;
+  if (k_tok_stride < row || v_tok_stride < row || k_tok_stride % 8 || v_tok_stride % 8)
+    return PKV_EINVAL;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(q_start, 4) ||
+      !aligned(block_tables, 4) || !aligned(context_lens, 4))
+    return PKV_EINVAL;
+  if (max_blocks_per_seq > INT32_MAX / kBlockSize) return PKV_EUNSUPPORTED;
+  // one warp stores what another reads if a pool or its scales lie over the other's
+  const size_t pool = size_t(cache.num_blocks) * kBlockSize * size_t(row);
+  const size_t scales = size_t(cache.num_blocks) * size_t(cache.kv_heads) * 4;
+  if (overlap(k_cache, pool, v_cache, pool) || overlap(k_scales, scales, v_scales, scales))
+    return PKV_EINVAL;
+  pkv::AppendBlockScaledArgs a;
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.k_stride = k_tok_stride;
+  a.v_stride = v_tok_stride;
+  a.q_start = q_start;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.k_cache = static_cast<uint8_t*>(k_cache);
+  a.v_cache = static_cast<uint8_t*>(v_cache);
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.total = num_tokens;
+  a.num_seqs = num_seqs;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_blocks = cache.num_blocks;
+  a.kv_heads = cache.kv_heads;
+  const cudaError_t e =
+      pkv::launch_append_block_scaled(a, cache.d_head, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
+}
+
+size_t pkv_decode_fp8_block_scaled_workspace_bytes(int num_seqs, int q_heads, int kv_heads,
+                                                   int d_head) {
+  BlockScaledDecodeLayout w;
+  return block_scaled_decode_layout(num_seqs, q_heads, kv_heads, d_head, &w) == PKV_OK ? w.total
+                                                                                       : 0;
+}
+
+int pkv_paged_decode_attention_fp8_block_scaled(
+    const void* q, int num_seqs, int q_heads, const void* k_cache, const void* v_cache,
+    const float* k_scales, const float* v_scales, pkv_cache_desc cache,
+    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+    int max_context_len, float scale, float* out, void* workspace, size_t ws_bytes,
+    pkv_stream_t stream) {
+  return decode_block_scaled(q, num_seqs, q_heads, k_cache, v_cache, k_scales, v_scales, cache,
+                             block_tables, max_blocks_per_seq, context_lens, max_context_len,
+                             scale, out, false, workspace, ws_bytes, stream);
+}
+
+int pkv_paged_decode_attention_fp8_block_scaled_bf16out(
+    const void* q, int num_seqs, int q_heads, const void* k_cache, const void* v_cache,
+    const float* k_scales, const float* v_scales, pkv_cache_desc cache,
+    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+    int max_context_len, float scale, void* out, void* workspace, size_t ws_bytes,
+    pkv_stream_t stream) {
+  return decode_block_scaled(q, num_seqs, q_heads, k_cache, v_cache, k_scales, v_scales, cache,
+                             block_tables, max_blocks_per_seq, context_lens, max_context_len,
+                             scale, out, true, workspace, ws_bytes, stream);
+}
+
+int pkv_copy_block_scales(float* k_scales, float* v_scales, pkv_cache_desc cache,
+                          const int32_t* pairs, int32_t num_pairs, pkv_stream_t stream) {
+  if (cache.num_blocks <= 0 || cache.kv_heads <= 0 || num_pairs < 0) return PKV_EINVAL;
+  if (num_pairs == 0) return PKV_OK;
+  if (!k_scales || !v_scales || !pairs) return PKV_EINVAL;
+  if (!aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(pairs, 4)) return PKV_EINVAL;
+  const int sms = current_device_sms();
+  if (sms <= 0) return PKV_ECUDA;
+  const cudaError_t e =
+      pkv::launch_copy_block_scales(k_scales, v_scales, pairs, num_pairs, cache.num_blocks,
+                                    cache.kv_heads, static_cast<cudaStream_t>(stream), sms);
   return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 

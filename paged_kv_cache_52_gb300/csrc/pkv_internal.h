@@ -25,6 +25,8 @@ cudaError_t decode_flat_error_word(unsigned** word);
 cudaError_t rope_error_word(unsigned** word);
 cudaError_t draft_error_word(unsigned** word);
 cudaError_t tree_error_word(unsigned** word);
+cudaError_t block_scaled_error_word(unsigned** word);
+cudaError_t decode_block_scaled_error_word(unsigned** word);
 
 // ---- kv_append.cu
 // reject (optional): a device flag set by launch_slot_duplicates; when it is
@@ -303,5 +305,41 @@ cudaError_t launch_paged_tree(const TreeArgs& a, const CUtensorMap* tmap_q,
                               const CUtensorMap* tmap_k, const CUtensorMap* tmap_v,
                               cudaStream_t stream);
 unsigned read_tree_error(bool clear);
+
+// ---- fp8_block_scaled.cu: the block-scaled FP8 cache
+struct AppendBlockScaledArgs {
+  const __nv_bfloat16 *k, *v;
+  int64_t k_stride, v_stride;  // elements per token
+  const int32_t *q_start, *block_tables, *context_lens;
+  uint8_t *k_cache, *v_cache;
+  float *k_scales, *v_scales;
+  int64_t total;  // rows of k and v
+  int num_seqs, max_blocks_per_seq, num_blocks, kv_heads;
+};
+cudaError_t launch_append_block_scaled(const AppendBlockScaledArgs& a, int d_head,
+                                       cudaStream_t stream);
+cudaError_t launch_copy_block_scales(float* k_scales, float* v_scales, const int32_t* pairs,
+                                     int num_pairs, int num_blocks, int kv_heads,
+                                     cudaStream_t stream, int num_sms);
+unsigned read_block_scaled_error(bool clear);
+
+// ---- paged_decode_block_scaled.cu
+struct DecodeBlockScaledArgs {
+  const void* q;
+  const int32_t *block_tables, *context_lens;
+  const float *k_scales, *v_scales;
+  void* out;
+  bool out_bf16;
+  float *part_o, *part_lse;  // a slot for every pair of one launch and every warp
+  int32_t* pre;              // [min(num_seqs, flat seqs) + 1]
+  int num_seqs, q_heads, kv_heads, d_head, num_blocks, max_blocks_per_seq, max_context_len;
+  float scale_log2;
+};
+int decode_block_scaled_warps();      // of a flat CTA
+int decode_block_scaled_flat_seqs();  // sequences of one flat launch
+cudaError_t launch_decode_block_scaled(const DecodeBlockScaledArgs& a, const CUtensorMap* tmap_k,
+                                       const CUtensorMap* tmap_v, int num_sms,
+                                       cudaStream_t stream);
+unsigned read_decode_block_scaled_error(bool clear);
 
 }  // namespace pkv

@@ -186,6 +186,17 @@ SIGNATURES = {
     "pkv_kv_accept_rows": ([_vp, _i64, _vp, _i64, ctypes.c_int, CacheDesc, _i32, _vp,
                             ctypes.c_int, _vp, _vp, ctypes.c_int, _vp, ctypes.c_int, _vp, _vp,
                             _vp], ctypes.c_int),
+    "pkv_kv_append_fp8_block_scaled": ([_vp, _i64, _vp, _i64, _i64, _vp, ctypes.c_int, _vp,
+                                        ctypes.c_int, _vp, _vp, _vp, _vp, _vp, CacheDesc, _vp],
+                                       ctypes.c_int),
+    "pkv_copy_block_scales": ([_vp, _vp, CacheDesc, _vp, _i32, _vp], ctypes.c_int),
+    "pkv_decode_fp8_block_scaled_workspace_bytes": ([ctypes.c_int] * 4, _sz),
+    "pkv_paged_decode_attention_fp8_block_scaled": (
+        [_vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, CacheDesc, _vp, ctypes.c_int, _vp,
+         ctypes.c_int, _f32, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "pkv_paged_decode_attention_fp8_block_scaled_bf16out": (
+        [_vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, CacheDesc, _vp, ctypes.c_int, _vp,
+         ctypes.c_int, _f32, _vp, _vp, _sz, _vp], ctypes.c_int),
     # host block manager (pagedkv_blocks.h); pointers are host memory
     "pkv_bm_create": ([_i32, _i32, ctypes.POINTER(_vp)], ctypes.c_int),
     "pkv_bm_destroy": ([_vp], None),
@@ -1092,6 +1103,61 @@ def kv_accept_rows(k_cache: torch.Tensor, v_cache: torch.Tensor, block_tables: t
 
 
 # --------------------------------------------------------------------------
+# The block-scaled FP8 cache: a scale for each block of 16 tokens and KV head.
+# --------------------------------------------------------------------------
+def kv_append_fp8_block_scaled(k: torch.Tensor, v: torch.Tensor, q_start: torch.Tensor,
+                               block_tables: torch.Tensor, context_lens: torch.Tensor,
+                               k_cache: torch.Tensor, v_cache: torch.Tensor,
+                               k_scales: torch.Tensor, v_scales: torch.Tensor) -> None:
+    """Quantize each sequence's new rows into a block-scaled FP8 cache: rows
+    ``q_start[s]:q_start[s+1]`` of ``k, v [T, Hkv, d]`` (bf16 views with
+    contiguous rows) are the last positions of sequence s's context.  The pools
+    hold e4m3 codes (uint8 ``[NB, 16, Hkv, d]``), the scales are float32 ``[NB,
+    Hkv]``; every block that receives rows gets the power of two its largest
+    value needs (never less than before, where older rows lie in it, which then
+    move to the new scale)."""
+    _done("pkv_kv_append_fp8_block_scaled", _marshal.append_block_scaled(
+        k, v, q_start, block_tables, context_lens, k_cache, v_cache, k_scales, v_scales))
+
+
+def decode_fp8_block_scaled_workspace(num_seqs: int, q_heads: int, kv_heads: int, d_head: int,
+                                      device) -> torch.Tensor:
+    """Workspace of ``paged_decode_attention_fp8_block_scaled`` for these sizes."""
+    with torch.cuda.device(device):
+        n = lib.pkv_decode_fp8_block_scaled_workspace_bytes(num_seqs, q_heads, kv_heads, d_head)
+    _need(n > 0, "unsupported sizes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def paged_decode_attention_fp8_block_scaled(q: torch.Tensor, k_cache: torch.Tensor,
+                                            v_cache: torch.Tensor, k_scales: torch.Tensor,
+                                            v_scales: torch.Tensor, block_tables: torch.Tensor,
+                                            context_lens: torch.Tensor, scale: float,
+                                            out: Optional[torch.Tensor] = None,
+                                            max_context_len: Optional[int] = None,
+                                            workspace: Optional[torch.Tensor] = None,
+                                            out_dtype: Optional[torch.dtype] = None
+                                            ) -> torch.Tensor:
+    """Decode attention over a block-scaled FP8 cache (see
+    ``kv_append_fp8_block_scaled``): ``q [S, Hq, d]`` bf16, one query per
+    sequence.  ``out`` is float32 unless ``out_dtype`` (or a given ``out``) is
+    bfloat16.  ``max_context_len`` (host int) bounds the context lengths; when
+    omitted it is read from ``context_lens`` (a device sync)."""
+    odt = _out_dtype(out, out_dtype)
+    if max_context_len is None:
+        max_context_len = int(context_lens.max().item()) if context_lens.numel() else 0
+    if workspace is None:
+        _need(q.dim() == 3 and k_cache.dim() == 4, "q must be [S, Hq, d], pools [NB, 16, Hkv, d]")
+        workspace = decode_fp8_block_scaled_workspace(q.shape[0], q.shape[1], k_cache.shape[2],
+                                                      q.shape[2], q.device)
+    bf16 = odt is torch.bfloat16
+    name = "pkv_paged_decode_attention_fp8_block_scaled"
+    return _done(name + "_bf16out" if bf16 else name, _marshal.decode_block_scaled(
+        q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out,
+        max_context_len, workspace, bf16))
+
+
+# --------------------------------------------------------------------------
 # Host block manager (pagedkv_blocks.h) and the copy-on-write block copy.
 # --------------------------------------------------------------------------
 def _i32_host(values) -> "ctypes.Array":
@@ -1219,10 +1285,18 @@ def blocks_for_budget(usable_bytes: int, model_bytes: int, activation_peak_bytes
     return n
 
 
-def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, pairs: torch.Tensor) -> None:
+def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, pairs: torch.Tensor,
+                k_scales: Optional[torch.Tensor] = None,
+                v_scales: Optional[torch.Tensor] = None) -> None:
     """Copy-on-write on the device: block ``pairs[i, 1]`` of both pools
     becomes a copy of block ``pairs[i, 0]`` (``pairs`` int32 [n, 2] on the
-    pools' device; bf16 or uint8 (FP8) pools)."""
+    pools' device; bf16 or uint8 (FP8) pools).  Of a block-scaled cache the
+    blocks' scales (float32 ``[NB, Hkv]``) are copied too."""
+    _need((k_scales is None) == (v_scales is None), "k_scales and v_scales go together")
+    for s in (k_scales, v_scales) if k_scales is not None else ():
+        _need(s.device == k_cache.device and s.dtype == torch.float32 and s.is_contiguous() and
+              k_cache.dim() == 4 and tuple(s.shape) == (k_cache.shape[0], k_cache.shape[2]),
+              "scales must be contiguous float32 [NB, Hkv] on the pools' device")
     for c in (k_cache, v_cache):
         _need(c.is_cuda and c.is_contiguous() and c.dim() == 4 and
               c.dtype in (torch.bfloat16, torch.uint8),
@@ -1236,3 +1310,7 @@ def copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, pairs: torch.Tenso
                              k_cache.element_size(), _ptr(pairs), pairs.shape[0],
                              _stream(k_cache))
     _check("pkv_copy_blocks", st)
+    if k_scales is not None:
+        st = lib.pkv_copy_block_scales(_ptr(k_scales), _ptr(v_scales), cache_desc(k_cache),
+                                       _ptr(pairs), pairs.shape[0], _stream(k_cache))
+        _check("pkv_copy_block_scales", st)
