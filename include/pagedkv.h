@@ -980,6 +980,62 @@ PKV_API int pkv_paged_decode_attention_fp8_block_scaled_bf16out(
     pkv_stream_t stream);
 
 /*
+ * pkv_paged_prefill_attention_fp8_block_scaled -- chunked prefill over a
+ * block-scaled cache: queries, q_start, context_lens and mask as in
+ * pkv_paged_prefill_attention (no host bound on a chunk is needed).  The pages
+ * of every sequence are first widened to bf16 rows in the workspace -- exact
+ * for the append's scales -- and attended by the kernel of
+ * pkv_prompt_attention, whose limits on V hold.
+ *   out : [total_q][q_heads][d_head] bf16, 32-byte aligned, not over q; rows
+ *         outside every chunk are not written.
+ *   workspace : >= pkv_prefill_fp8_block_scaled_workspace_bytes(...) device
+ *         bytes, 256-byte aligned (PKV_ENOMEM if NULL or smaller); contents
+ *         need no initialisation; calls that share it must be ordered on the
+ *         GPU.
+ * A chunk longer than its context (causal), a context beyond the block table,
+ * no context, or a q_start out of order rejects that sequence: none of its rows
+ * is written and PKV_DEVERR_BAD_QUERY_RANGE is set.
+ *
+ * pkv_prompt_attention -- attention of whole prompts over the keys and values
+ * just computed, before (or without) a cache: sequence s's tokens are rows
+ * q_start[s] .. q_start[s+1]-1 of q, k and v alike, packed behind one another.
+ *   out[i] = softmax(scale * q_i K^T) V over the sequence's tokens 0 .. i, or
+ *   all of them when causal is 0 ("Optimisation de l'inference", "Etape 2").
+ *   q    : [total_q][q_heads][d_head] bf16, row t at element t * q_tok_stride;
+ *          k, v : [total_q][kv_heads][d_head] likewise -- views of one fused
+ *          projection, or of a staging pool that pkv_qk_norm_rope_append filled
+ *          slot by slot, are accepted.  Bases 16-byte aligned, strides multiples
+ *          of 8 elements.
+ *   q_start : [num_seqs + 1] int32, non-decreasing, q_start[num_seqs] <=
+ *          total_q; sequences may be empty.
+ *   out  : [total_q][q_heads][d_head] bf16, contiguous, 32-byte aligned, not
+ *          over an input; rows of no sequence are not written.
+ * Scores, their maximum, the weights' sum and the output are accumulated in
+ * float32; the weights enter P V as bf16 (off by 2^-8 of themselves, as the
+ * output is), so there is no float32 output.  Weights stand up to 2^16 against
+ * the running maximum, so |V| may be as large as 2^110 / (tokens).  Rows of
+ * other sequences, and of none, never reach a row, whatever they hold; nor do
+ * NaN and infinities in V of later tokens of its own.  NaN in what a row sees
+ * makes NaN of it, an infinity in V an infinity or NaN.
+ * d_head 64 or 128, a group of 1, 2, 4, 8 or 16.  A q_start out of order or
+ * beyond total_q leaves that sequence out (PKV_DEVERR_BAD_QUERY_RANGE).  No
+ * workspace.
+ */
+PKV_API size_t pkv_prefill_fp8_block_scaled_workspace_bytes(int num_seqs, int max_blocks_per_seq,
+                                                            int kv_heads, int d_head);
+PKV_API int pkv_paged_prefill_attention_fp8_block_scaled(
+    const void* q, const int32_t* q_start, int num_seqs, int total_q, int q_heads,
+    const void* k_cache, const void* v_cache, const float* k_scales, const float* v_scales,
+    pkv_cache_desc cache, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int causal, float scale, void* out, void* workspace,
+    size_t ws_bytes, pkv_stream_t stream);
+PKV_API int pkv_prompt_attention(const void* q, int64_t q_tok_stride, const int32_t* q_start,
+                                 int num_seqs, int total_q, int q_heads, const void* k,
+                                 int64_t k_tok_stride, const void* v, int64_t v_tok_stride,
+                                 int kv_heads, int d_head, int causal, float scale, void* out,
+                                 pkv_stream_t stream);
+
+/*
  * Decode for callers that cannot allocate device memory.  The pages have no
  * counterpart to this entry point; it exists for callers that are handed
  * device buffers but may not call cudaMalloc (a fixed, pre-reserved memory

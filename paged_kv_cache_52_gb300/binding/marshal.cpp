@@ -1,4 +1,5 @@
-// Argument checks and marshalling of the speculative step's calls, as a CPython
+// Argument checks and marshalling of the speculative step's calls, of those over a
+// block-scaled cache and of prompt attention, as a CPython
 // module (`paged_kv_cache_52_gb300._marshal`).
 //
 // A step of one user keeps the GPU busy for 1.5 us in most of these calls; the
@@ -403,6 +404,63 @@ PyObject* decode_block_scaled(PyObject* const* a) {
   return st == PKV_OK ? give(a[8], out) : PyLong_FromLong(st);
 }
 
+// q, q_start, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, causal,
+// scale, out, workspace
+PyObject* prefill_block_scaled(PyObject* const* a) {
+  const BlockScaled p = block_scaled(a[2], a[3], a[4], a[5]);
+  const Tensor& q = tensor(a[0], "q");
+  if (q.dim() != 3) refuse("q", "[total, Hq, d]");
+  const int64_t total = q.size(0), hq = q.size(1), d = p.desc.d_head;
+  const void* qp = packed(a[0], "q", at::kBFloat16, p.dev, {total, hq, d});
+  const TreeBatch b = tree_batch(a[1], a[7], p.dev);
+  int width;
+  const int32_t* tables = table(a[6], "block_tables", p.dev, b.S, &width);
+  const int causal = PyObject_IsTrue(a[8]);
+  if (causal < 0) throw python_error();
+  const float scale = float(real(a[9]));
+  const Tensor& ws = tensor(a[11], "workspace");
+  const int64_t ws_bytes = ws.numel();
+  void* wp = packed(a[11], "workspace", at::kByte, p.dev, {ws_bytes});
+  const int nt = count(total, "q"), nq = count(hq, "q");
+  const Tensor out = result(a[10], "out", at::kBFloat16, p.dev, {total, hq, d});
+  void* op = out.data_ptr();
+  const int st = launch(p.dev, [&](void* stream) {
+    return pkv_paged_prefill_attention_fp8_block_scaled(qp, b.q_start, b.S, nt, nq, p.k, p.v, p.ks,
+                                                        p.vs, p.desc, tables, width, b.lens, causal,
+                                                        scale, op, wp, size_t(ws_bytes), stream);
+  });
+  return st == PKV_OK ? give(a[10], out) : PyLong_FromLong(st);
+}
+
+// q, q_start, k, v, causal, scale, out
+PyObject* prompt_attention(PyObject* const* a) {
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
+  const Tensor& start = tensor(a[1], "q_start");
+  if (!q.is_cuda() || q.dim() != 3) refuse("q", "a CUDA tensor [T, Hq, d]");
+  if (k.dim() != 3) refuse("k", "[T, Hkv, d]");
+  if (start.dim() != 1 || start.size(0) < 1) refuse("q_start", "[S + 1]");
+  const int dev = q.get_device();
+  const int64_t T = q.size(0), hq = q.size(1), d = q.size(2), hkv = k.size(1);
+  const int64_t S = start.size(0) - 1;
+  const int64_t sq = token_rows(q, "q", dev, T, hq, d);
+  const int64_t sk = token_rows(k, "k", dev, T, hkv, d);
+  const int64_t sv = token_rows(v, "v", dev, T, hkv, d);
+  const auto* sp = static_cast<const int32_t*>(packed(a[1], "q_start", at::kInt, dev, {S + 1}));
+  const int causal = PyObject_IsTrue(a[4]);
+  if (causal < 0) throw python_error();
+  const float scale = float(real(a[5]));
+  const int nt = count(T, "q"), nq = count(hq, "q"), nkv = count(hkv, "k"), nd = count(d, "q"),
+            ns = count(S, "q_start");
+  const Tensor out = result(a[6], "out", at::kBFloat16, dev, {T, hq, d});
+  const void *qp = q.data_ptr(), *kp = k.data_ptr(), *vp = v.data_ptr();
+  void* op = out.data_ptr();
+  const int st = launch(dev, [&](void* stream) {
+    return pkv_prompt_attention(qp, sq, sp, ns, nt, nq, kp, sk, vp, sv, nkv, nd, causal, scale, op,
+                                stream);
+  });
+  return st == PKV_OK ? give(a[6], out) : PyLong_FromLong(st);
+}
+
 #define PKV_METHOD(name, n) \
   {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&entry<n, name>)), \
    METH_FASTCALL, nullptr}
@@ -410,6 +468,7 @@ PyObject* decode_block_scaled(PyObject* const* a) {
 PyMethodDef methods[] = {PKV_METHOD(rope_append, 14), PKV_METHOD(tree_layout, 6),
                          PKV_METHOD(tree_attention, 12), PKV_METHOD(accept_rows, 8),
                          PKV_METHOD(append_block_scaled, 9), PKV_METHOD(decode_block_scaled, 12),
+                         PKV_METHOD(prefill_block_scaled, 12), PKV_METHOD(prompt_attention, 7),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods,

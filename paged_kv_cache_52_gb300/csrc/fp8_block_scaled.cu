@@ -17,8 +17,7 @@
 //
 // One warp takes one (block, KV head, K or V): its up to 16 rows are in
 // registers between the maximum and the stores, so the inputs are read once.
-// Which rows form a block follows from q_start and the context lengths; the
-// CTA that holds a block's first new row takes the block.
+// Which rows form a block follows from q_start and the context lengths.
 #include <algorithm>
 #include <climits>
 
@@ -32,6 +31,7 @@ static __device__ unsigned g_block_scaled_error = 0;
 constexpr int kBsTokens = 16;     // tokens per block
 constexpr int kBsThreads = 256;
 constexpr int kBsMaxRows = 16;    // new rows per CTA at most
+constexpr int kSplitPerSm = 3;    // CTAs per SM up to which a block's tasks are spread
 
 // The scale of values up to `amax` (bf16 bits of the largest finite
 // magnitude): 1.75 is 448's fraction, so a larger fraction needs one more.
@@ -133,70 +133,58 @@ __device__ __forceinline__ void append_block(const __nv_bfloat16* __restrict__ s
   }
 }
 
+// CTA (x, y): the blocks whose first new rows are among rows [x rows_per_cta,
+// ...), the y-th part of their (head, K or V) tasks.
 template <int D>
 __global__ void __launch_bounds__(kBsThreads)
 append_block_scaled_kernel(const AppendBlockScaledArgs a, int rows_per_cta) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ int seq_of[kBsMaxRows], hits[kBsMaxRows];
-  __shared__ int leaders, item_row[kBsMaxRows], item_first[kBsMaxRows], item_count[kBsMaxRows],
+  __shared__ int items, item_row[kBsMaxRows], item_first[kBsMaxRows], item_count[kBsMaxRows],
       item_block[kBsMaxRows];
-  const int64_t r0 = int64_t(blockIdx.x) * rows_per_cta;
-  const int rows = int(min(int64_t(rows_per_cta), a.total - r0));
-  if (threadIdx.x < kBsMaxRows) hits[threadIdx.x] = 0;
-  if (threadIdx.x == 0) leaders = 0;
+  if (threadIdx.x == 0) items = 0;
   __syncthreads();
-  // whose rows these are: every sequence looks whether it holds some of them
-  bool bad = false;
+  // every sequence looks for its blocks that start among these rows
+  const int64_t r0 = int64_t(blockIdx.x) * rows_per_cta;
+  const int64_t r1 = min(r0 + rows_per_cta, a.total);
+  const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
   for (int s = threadIdx.x; s < a.num_seqs; s += kBsThreads) {
     const int qs = __ldg(a.q_start + s), qe = __ldg(a.q_start + s + 1);
-    bad |= qe < qs || qs < 0 || qe > a.total;
-    const int64_t lo = max(int64_t(qs), r0), hi = min(int64_t(qe), r0 + rows);
-    for (int64_t r = lo; r < hi; ++r) {
-      seq_of[r - r0] = s;
-      atomicAdd(&hits[r - r0], 1);
+    const int ctx = __ldg(a.context_lens + s);
+    const int n = qe - qs;
+    if (qs < 0 || n < 0 || qe > a.total || n > ctx || ctx > a.max_blocks_per_seq * kBsTokens) {
+      if (n != 0 && first_cta) atomicOr(&g_block_scaled_error, kErrBadQueryRange);
+      continue;
     }
-  }
-  if (bad && blockIdx.x == 0) atomicOr(&g_block_scaled_error, kErrBadQueryRange);
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    const int i = threadIdx.x;
-    bool lead = false;
-    int first = 0, n_rows = 0, block = 0;
-    if (i < rows && hits[i] == 1) {  // a row of no sequence is left out
-      const int s = seq_of[i];
-      const int qs = __ldg(a.q_start + s), qe = __ldg(a.q_start + s + 1);
-      const int ctx = __ldg(a.context_lens + s);
-      const int r = int(r0) + i, n = qe - qs;
-      if (qs < 0 || qe > a.total || n > ctx || ctx > a.max_blocks_per_seq * kBsTokens) {
-        if (r == qs) atomicOr(&g_block_scaled_error, kErrBadQueryRange);
+    const int base = ctx - n - qs;  // position of row r: base + r
+    const int64_t hi = min(int64_t(qe), r1);
+    int64_t r = max(int64_t(qs), r0);
+    if (r > qs) r += (kBsTokens - (base + r) % kBsTokens) % kBsTokens;  // the next block's start
+    while (r < hi) {
+      const int pos = int(base + r), first = pos % kBsTokens;
+      const int block = __ldg(a.block_tables + size_t(s) * a.max_blocks_per_seq + pos / kBsTokens);
+      const int rows = min(kBsTokens - first, int(qe - r));
+      if (block < 0 || block >= a.num_blocks) {
+        atomicOr(&g_block_scaled_error, kErrBadBlockId);
       } else {
-        const int pos = ctx - n + (r - qs);
-        first = pos % kBsTokens;
-        if (first == 0 || r == qs) {
-          n_rows = min(kBsTokens - first, qe - r);
-          block = __ldg(a.block_tables + size_t(s) * a.max_blocks_per_seq + pos / kBsTokens);
-          lead = block >= 0 && block < a.num_blocks;
-          if (!lead) atomicOr(&g_block_scaled_error, kErrBadBlockId);
+        const int at = atomicAdd(&items, 1);
+        if (at < kBsMaxRows) {
+          item_row[at] = int(r - r0);
+          item_first[at] = first;
+          item_count[at] = rows;
+          item_block[at] = block;
+        } else {  // only where sequences claim the same rows
+          atomicOr(&g_block_scaled_error, kErrBadQueryRange);
         }
       }
-    } else if (i < rows && hits[i] > 1) {
-      atomicOr(&g_block_scaled_error, kErrBadQueryRange);  // two sequences claim the row
+      r += rows;
     }
-    const unsigned mask = __ballot_sync(0xffffffffu, lead);
-    if (lead) {
-      const int at = __popc(mask & ((1u << i) - 1));
-      item_row[at] = i;
-      item_first[at] = first;
-      item_count[at] = n_rows;
-      item_block[at] = block;
-    }
-    if (i == 0) leaders = __popc(mask);
   }
   __syncthreads();
   const int row_bytes = a.kv_heads * D;
-  const int tasks = leaders * a.kv_heads * 2;
-  for (int t = threadIdx.x >> 5; t < tasks; t += kBsThreads / 32) {
+  const int tasks = min(items, kBsMaxRows) * a.kv_heads * 2;
+  for (int t = int(blockIdx.y) * (kBsThreads / 32) + (threadIdx.x >> 5); t < tasks;
+       t += gridDim.y * (kBsThreads / 32)) {
     const int item = t / (2 * a.kv_heads), rest = t - item * 2 * a.kv_heads;
     const bool v = rest >= a.kv_heads;
     const int h = v ? rest - a.kv_heads : rest;
@@ -210,17 +198,23 @@ append_block_scaled_kernel(const AppendBlockScaledArgs a, int rows_per_cta) {
   }
 }
 
-cudaError_t launch_append_block_scaled(const AppendBlockScaledArgs& a, int d_head,
+cudaError_t launch_append_block_scaled(const AppendBlockScaledArgs& a, int d_head, int num_sms,
                                        cudaStream_t stream) {
   // About one block's first row per CTA: a batch of single tokens gives every
-  // token a CTA, a prompt every block.
+  // token a CTA, a prompt every block.  Few of them: a block's tasks are
+  // spread over several CTAs, down to one for each warp (one token of 32
+  // heads: 10.9 -> TBD us).
   const int64_t firsts = std::min(a.total, a.total / kBsTokens + a.num_seqs);
   int rows = 1;
   while (rows < kBsMaxRows && int64_t(rows) * 2 * firsts <= a.total) rows *= 2;
   const int64_t grid = (a.total + rows - 1) / rows;
   if (grid > INT_MAX) return cudaErrorInvalidValue;
+  const int parts = (2 * a.kv_heads + kBsThreads / 32 - 1) / (kBsThreads / 32);
+  int split = 1;
+  while (split < parts && split < 1024 && grid * split < kSplitPerSm * int64_t(num_sms)) split *= 2;
   auto* kernel = d_head == 128 ? append_block_scaled_kernel<128> : append_block_scaled_kernel<64>;
-  return launch_after_previous(kernel, dim3(unsigned(grid)), dim3(kBsThreads), 0, stream, a, rows);
+  return launch_after_previous(kernel, dim3(unsigned(grid), unsigned(split)), dim3(kBsThreads), 0,
+                               stream, a, rows);
 }
 
 // The scales' part of a block copy: row dst of both arrays becomes row src.
@@ -250,6 +244,62 @@ cudaError_t launch_copy_block_scales(float* k_scales, float* v_scales, const int
   copy_block_scales_kernel<<<grid, 128, 0, stream>>>(k_scales, v_scales, pairs, num_pairs,
                                                      num_blocks, kv_heads);
   return cudaGetLastError();
+}
+
+// Pages -> contiguous bf16 rows for the prefill: position t of sequence s to row
+// s * max_blocks * 16 + t of both outputs.  code * scale is a bf16 value for the
+// append's scales; other scales' products are rounded to one.  One CTA takes a
+// page of K and V; a thread 16 codes, which lie in one head, at a time.
+__global__ void __launch_bounds__(kBsThreads)
+widen_block_scaled_kernel(const WidenBlockScaledArgs a, int d_head) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t items = int64_t(a.num_seqs) * a.max_blocks_per_seq;
+  const int row_vec = a.kv_heads * d_head / 16;  // 16 codes each
+  const int page_vec = kBsTokens * row_vec;
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    const int s = int(item / a.max_blocks_per_seq);
+    const int j = int(item - int64_t(s) * a.max_blocks_per_seq);
+    const int live = __ldg(a.context_lens + s) - j * kBsTokens;  // rows of the page in use
+    if (live <= 0) continue;
+    const int id = __ldg(a.block_tables + item);
+    const bool good = id >= 0 && id < a.num_blocks;
+    if (!good && threadIdx.x == 0) atomicOr(&g_block_scaled_error, kErrBadBlockId);
+    for (int i = threadIdx.x; i < 2 * page_vec; i += kBsThreads) {
+      const bool v = i >= page_vec;
+      const int c = v ? i - page_vec : i;
+      const int row = c / row_vec;
+      if (row >= live) continue;
+      uint4 w = make_uint4(0, 0, 0, 0);
+      float f = 0.f;
+      if (good) {
+        w = __ldg(reinterpret_cast<const uint4*>(v ? a.v_cache : a.k_cache) +
+                  size_t(id) * page_vec + c);
+        f = __ldg((v ? a.v_scales : a.k_scales) + size_t(id) * a.kv_heads +
+                  (c - row * row_vec) * 16 / d_head);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(v ? a.v_out : a.k_out) + (item * page_vec + c) * 2;
+      const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+      uint32_t out[8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float x[4];
+        e4m3x4_to_f32(in[k], x);
+        out[2 * k] = pack_bf16x2(x[0] * f, x[1] * f);
+        out[2 * k + 1] = pack_bf16x2(x[2] * f, x[3] * f);
+      }
+      dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+      dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+    }
+  }
+}
+
+cudaError_t launch_widen_block_scaled(const WidenBlockScaledArgs& a, int d_head, int num_sms,
+                                      cudaStream_t stream) {
+  const int64_t items = int64_t(a.num_seqs) * a.max_blocks_per_seq;
+  const int grid = int(std::min<int64_t>(items, int64_t(num_sms) * 8));
+  return launch_after_previous(widen_block_scaled_kernel, dim3(unsigned(grid)), dim3(kBsThreads),
+                               0, stream, a, d_head);
 }
 
 // Device address of this unit's error word on the current device.

@@ -25,7 +25,8 @@
 //    memory.  One launch, no workspace: for batches whose pages fit one wave.
 //  * flat: the pages of all sequences laid end to end are cut into equal
 //    ranges, one for each group of Hkv warps of a grid of one CTA per SM (as in
-//    paged_decode_flat.cu, whose merge joins the pieces).
+//    paged_decode_flat.cu); a second kernel joins the pieces of the pairs that
+//    were cut.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -726,8 +727,94 @@ decode_block_scaled_flat_kernel(const __grid_constant__ CUtensorMap tmap_k,
   flush();
 }
 
+// Joins the pieces of a cut pair: row (sequence s, query head) of KV head h;
+// the pages [pre[s], pre[s] + n) lie in the ranges g0 = pre[s] / c .. g1 =
+// (pre[s] + n - 1) / c, range g's piece at slot (s + g) Hkv + h.  An empty
+// sequence gets zeros; a pair within one range is written already.  WPR warps
+// take a row's pieces in turn and meet in shared memory: with few rows every
+// row has a hundred pieces, and one warp would wait for each eight loads in
+// turn (2 x 131072 tokens: 39 us against 3.5), with many rows two or none.
+template <int D, int WPR>
+__global__ void __launch_bounds__(256)
+decode_block_scaled_merge_kernel(const DecodeParams p, const DecodeFlatParams fp,
+                                 long long total_rows) {
+  griddep_wait();
+  griddep_launch_dependents();
+  constexpr int kCols = D / 32;  // a lane's elements
+  __shared__ float part[WPR > 1 ? 8 : 1][WPR > 1 ? D : 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int w = warp % WPR;
+  const long long row = (long long)blockIdx.x * (8 / WPR) + warp / WPR;
+  if (row >= total_rows) return;  // WPR 8: the whole CTA
+  const int seq = int(row / p.q_heads);
+  const int hq = int(row - (long long)seq * p.q_heads);
+  const int G = p.q_heads / p.kv_heads;
+  const int h = hq / G, hg = hq - h * G;
+  const int start = __ldg(fp.pre_out + seq), n = __ldg(fp.pre_out + seq + 1) - start;
+  const long long c = flat_chunk(__ldg(fp.pre_out + fp.num_seqs),
+                                 flat_groups(fp.total_warps, p.kv_heads), fp.min_pages);
+  const int g0 = int(start / c), g1 = n > 0 ? int((start + n - 1) / c) : g0 - 1;
+  if (g1 == g0) return;
+  auto slot = [&](int g) { return (size_t(seq + g) * p.kv_heads + h) * G + hg; };
+  float big = -INFINITY;
+  for (int g = g0 + lane; g <= g1; g += 32) big = fmaxf(big, __ldg(p.part_lse + slot(g)));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+  float tot = 0.f;
+  for (int g = g0 + lane; g <= g1; g += 32) tot += ex2(__ldg(p.part_lse + slot(g)) - big);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+  float val[kCols];
+#pragma unroll
+  for (int i = 0; i < kCols; ++i) val[i] = 0.f;
+#pragma unroll 8
+  for (int g = g0 + w; g <= g1; g += WPR) {
+    const float wgt = ex2(__ldg(p.part_lse + slot(g)) - big);
+    const float* src = p.part_o + slot(g) * D + lane * kCols;
+    if constexpr (kCols == 4) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(src));
+      val[0] += wgt * x.x;
+      val[1] += wgt * x.y;
+      val[2] += wgt * x.z;
+      val[3] += wgt * x.w;
+    } else {
+      const float2 x = __ldg(reinterpret_cast<const float2*>(src));
+      val[0] += wgt * x.x;
+      val[1] += wgt * x.y;
+    }
+  }
+  const float inv = n > 0 ? 1.f / tot : 0.f;
+  if constexpr (WPR == 1) {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) store_out(p, size_t(row) * D + lane * kCols + i, val[i] * inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) part[w][lane * kCols + i] = val[i];
+    __syncthreads();
+    for (int x = threadIdx.x; x < D; x += 256) {
+      float sum = 0.f;
+#pragma unroll
+      for (int k = 0; k < WPR; ++k) sum += part[k][x];
+      store_out(p, size_t(row) * D + x, sum * inv);
+    }
+  }
+}
+
 // ------------------------------------------------------------------- launch
 namespace {
+
+template <int D>
+cudaError_t launch_merge(const DecodeParams& d, const DecodeFlatParams& fp, int ctas,
+                         cudaStream_t stream) {
+  const long long rows = (long long)fp.num_seqs * d.q_heads;
+  const bool few = rows <= 8ll * ctas;
+  const long long grid = few ? rows : (rows + 7) / 8;
+  if (grid > INT_MAX) return cudaErrorInvalidValue;
+  return few ? launch_after_previous(decode_block_scaled_merge_kernel<D, 8>,
+                                     dim3(unsigned(grid)), dim3(256), 0, stream, d, fp, rows)
+             : launch_after_previous(decode_block_scaled_merge_kernel<D, 1>,
+                                     dim3(unsigned(grid)), dim3(256), 0, stream, d, fp, rows);
+}
 
 template <int D, int G>
 cudaError_t launch_cluster(const BsDecodeParams& bp, int num_seqs, int ctas,
@@ -765,7 +852,7 @@ cudaError_t launch_flat(const BsDecodeParams& bp, const DecodeFlatParams& fp, in
   e = launch_after_previous(decode_block_scaled_flat_kernel<D, G>, dim3(unsigned(ctas)),
                             dim3(kBsFlatWarps * 32), L::kSmemBytes, stream, *tk, *tv, bp, fp);
   if (e != cudaSuccess) return e;
-  return launch_decode_flat_merge(bp.d, fp, D, stream);
+  return launch_merge<D>(bp.d, fp, ctas, stream);
 }
 
 // CTAs of a pair's cluster, or 0 for the flat split.

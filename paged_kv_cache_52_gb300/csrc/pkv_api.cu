@@ -1722,7 +1722,7 @@ int collect_error_words(cudaStream_t stream, bool clear, unsigned* word) {
       pkv::prefill_error_word, pkv::verify_error_word, pkv::probe_error_word,
       pkv::mixed_decode_error_word, pkv::mixed_prefill_error_word, pkv::decode_flat_error_word,
       pkv::rope_error_word, pkv::draft_error_word, pkv::tree_error_word,
-      pkv::block_scaled_error_word, pkv::decode_block_scaled_error_word};
+      pkv::block_scaled_error_word, pkv::decode_block_scaled_error_word, pkv::prompt_error_word};
   constexpr int kWords = int(sizeof(getters) / sizeof(getters[0]));
   static_assert(kWords <= int(sizeof(s.word) / sizeof(s.word[0])), "room for every unit's word");
   for (int i = 0; i < kWords; ++i)
@@ -1774,11 +1774,12 @@ int pkv_get_device_error(unsigned int* word, int clear) {
   const unsigned t = pkv::read_tree_error(clear != 0);
   const unsigned bs = pkv::read_block_scaled_error(clear != 0);
   const unsigned db = pkv::read_decode_block_scaled_error(clear != 0);
+  const unsigned pr = pkv::read_prompt_error(clear != 0);
   if (a == ~0u || d == ~0u || f == ~0u || d8 == ~0u || v == ~0u || w == ~0u || m == ~0u ||
       fl == ~0u || r == ~0u || dr == ~0u || t == ~0u ||
-      bs == ~0u || db == ~0u)
+      bs == ~0u || db == ~0u || pr == ~0u)
     return PKV_ECUDA;
-  *word = a | d | f | d8 | v | w | m | fl | r | dr | t | bs | db;
+  *word = a | d | f | d8 | v | w | m | fl | r | dr | t | bs | db | pr;
   return PKV_OK;
 }
 
@@ -2122,7 +2123,8 @@ int pkv_kv_accept_rows(void* k_cache, int64_t k_layer_stride, void* v_cache,
 }  // extern "C"
 
 // ---------------------------------------------------------------------------
-// The block-scaled FP8 cache: append, decode, copy of scales.
+// The block-scaled FP8 cache: append, decode, prefill, copy of scales; prompt
+// attention.
 // ---------------------------------------------------------------------------
 namespace {
 
@@ -2216,9 +2218,170 @@ int decode_block_scaled(const void* q, int num_seqs, int q_heads, const void* k_
   return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 
+// 3-D view of bf16 rows [rows][heads][d_head], `stride` elements apart: (d_head,
+// heads, rows).  One box is 64 columns x `box_heads` heads x `box_rows` rows,
+// 128-byte swizzled.
+bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int heads, int d_head,
+                     int64_t stride, int box_heads, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {cuuint64_t(d_head), cuuint64_t(heads), cuuint64_t(rows)};
+  const cuuint64_t strides[2] = {cuuint64_t(d_head) * 2, cuuint64_t(stride) * 2};
+  const cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_rows)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Queries over contiguous K and V rows.  kv_lens null: a sequence's keys are
+// its own rows; else kv_lens[s] rows from s * kv_stride on.
+int run_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+               int64_t v_stride, int64_t kv_rows, int total_q, const int32_t* q_start,
+               const int32_t* kv_lens, int kv_row_stride, int num_seqs, int q_heads, int kv_heads,
+               int d_head, int causal, float scale, void* out, cudaStream_t stream) {
+  const int group = q_heads / kv_heads;
+  CUtensorMap tq, tk, tv;
+  if (!encode_rows_map(&tq, q, total_q, q_heads, d_head, q_stride, group,
+                       pkv::prompt_tile_rows() / group) ||
+      !encode_rows_map(&tk, k, kv_rows, kv_heads, d_head, k_stride, 1,
+                       pkv::prompt_key_rows(d_head)) ||
+      !encode_rows_map(&tv, v, kv_rows, kv_heads, d_head, v_stride, 1, pkv::prompt_value_rows()))
+    return PKV_ECUDA;
+  pkv::PromptArgs a;
+  a.q_start = q_start;
+  a.kv_lens = kv_lens;
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.v_stride = v_stride;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.num_seqs = num_seqs;
+  a.total_q = total_q;
+  a.q_heads = q_heads;
+  a.kv_heads = kv_heads;
+  a.kv_stride = kv_row_stride;
+  a.causal = causal ? 1 : 0;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  const cudaError_t e = pkv::launch_prompt_attention(a, d_head, &tq, &tk, &tv, stream);
+  return e == cudaSuccess ? PKV_OK : (e == cudaErrorInvalidValue ? PKV_EUNSUPPORTED : PKV_ECUDA);
+}
+
+constexpr int kMaxPromptRows = INT32_MAX - 4096;  // a tile's end stays within 32 bits
+
+int check_prompt_heads(int q_heads, int kv_heads, int d_head) {
+  if (q_heads <= 0 || kv_heads <= 0) return PKV_EINVAL;
+  if (q_heads % kv_heads || !supported_group(q_heads / kv_heads)) return PKV_EUNSUPPORTED;
+  if (d_head != 64 && d_head != 128) return PKV_EUNSUPPORTED;
+  return q_heads > (1 << 20) ? PKV_EUNSUPPORTED : PKV_OK;
+}
+
+// Workspace of the block-scaled prefill: K rows, then V rows.
+bool block_scaled_prefill_layout(int num_seqs, int max_blocks, int kv_heads, int d_head,
+                                 size_t* v_off, size_t* total) {
+  if (num_seqs <= 0 || max_blocks <= 0 || kv_heads <= 0 || (d_head != 64 && d_head != 128))
+    return false;
+  const long long rows = (long long)num_seqs * max_blocks * kBlockSize;
+  if (rows > kMaxPromptRows || (long long)kv_heads * d_head > (1 << 24)) return false;
+  *v_off = (size_t(rows) * size_t(kv_heads) * size_t(d_head) * 2 + 255) / 256 * 256;
+  *total = 2 * *v_off;
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
+
+int pkv_prompt_attention(const void* q, int64_t q_tok_stride, const int32_t* q_start,
+                         int num_seqs, int total_q, int q_heads, const void* k,
+                         int64_t k_tok_stride, const void* v, int64_t v_tok_stride, int kv_heads,
+                         int d_head, int causal, float scale, void* out, pkv_stream_t stream) {
+  const int st = check_prompt_heads(q_heads, kv_heads, d_head);
+  if (st != PKV_OK) return st;
+  if (num_seqs < 0 || total_q < 0) return PKV_EINVAL;
+  if (total_q > kMaxPromptRows) return PKV_EUNSUPPORTED;
+  if (num_seqs == 0 || total_q == 0) return PKV_OK;
+  if (!q || !q_start || !k || !v || !out || !std::isfinite(scale)) return PKV_EINVAL;
+  const int64_t qrow = int64_t(q_heads) * d_head, row = int64_t(kv_heads) * d_head;
+  for (const int64_t s : {q_tok_stride, k_tok_stride, v_tok_stride}) {
+    if (s % 8) return PKV_EINVAL;
+    if (s >= (int64_t(1) << 39)) return PKV_EUNSUPPORTED;  // what a tensor map can hold
+  }
+  if (q_tok_stride < qrow || k_tok_stride < row || v_tok_stride < row) return PKV_EINVAL;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 32) ||
+      !aligned(q_start, 4))
+    return PKV_EINVAL;
+  auto span = [&](int64_t stride, int64_t r) { return size_t((total_q - 1) * stride + r) * 2; };
+  const size_t out_bytes = size_t(total_q) * size_t(qrow) * 2;
+  if (overlap(out, out_bytes, q, span(q_tok_stride, qrow)) ||
+      overlap(out, out_bytes, k, span(k_tok_stride, row)) ||
+      overlap(out, out_bytes, v, span(v_tok_stride, row)))
+    return PKV_EINVAL;
+  return run_prompt(q, q_tok_stride, k, k_tok_stride, v, v_tok_stride, total_q, total_q, q_start,
+                    nullptr, 0, num_seqs, q_heads, kv_heads, d_head, causal, scale, out,
+                    static_cast<cudaStream_t>(stream));
+}
+
+size_t pkv_prefill_fp8_block_scaled_workspace_bytes(int num_seqs, int max_blocks_per_seq,
+                                                    int kv_heads, int d_head) {
+  size_t v_off, total;
+  return block_scaled_prefill_layout(num_seqs, max_blocks_per_seq, kv_heads, d_head, &v_off,
+                                     &total)
+             ? total
+             : 0;
+}
+
+int pkv_paged_prefill_attention_fp8_block_scaled(
+    const void* q, const int32_t* q_start, int num_seqs, int total_q, int q_heads,
+    const void* k_cache, const void* v_cache, const float* k_scales, const float* v_scales,
+    pkv_cache_desc cache, const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* context_lens, int causal, float scale, void* out, void* workspace,
+    size_t ws_bytes, pkv_stream_t stream) {
+  int st = check_block_scaled(cache);
+  if (st == PKV_OK) st = check_prompt_heads(q_heads, cache.kv_heads, cache.d_head);
+  if (st != PKV_OK) return st;
+  if (num_seqs < 0 || total_q < 0) return PKV_EINVAL;
+  if (total_q > kMaxPromptRows) return PKV_EUNSUPPORTED;
+  if (num_seqs == 0 || total_q == 0) return PKV_OK;
+  if (!q || !q_start || !k_cache || !v_cache || !k_scales || !v_scales || !block_tables ||
+      !context_lens || !out || max_blocks_per_seq <= 0 || !std::isfinite(scale))
+    return PKV_EINVAL;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(out, 32) ||
+      !aligned(q_start, 4) || !aligned(block_tables, 4) || !aligned(context_lens, 4))
+    return PKV_EINVAL;
+  size_t v_off, total;
+  if (!block_scaled_prefill_layout(num_seqs, max_blocks_per_seq, cache.kv_heads, cache.d_head,
+                                   &v_off, &total))
+    return PKV_EUNSUPPORTED;
+  if (!workspace || ws_bytes < total) return PKV_ENOMEM;
+  if (!aligned(workspace, 256)) return PKV_EINVAL;
+  const int64_t qrow = int64_t(q_heads) * cache.d_head;
+  const size_t out_bytes = size_t(total_q) * size_t(qrow) * 2;
+  if (overlap(out, out_bytes, q, out_bytes)) return PKV_EINVAL;
+  const int sms = current_device_sms();
+  if (sms <= 0) return PKV_ECUDA;
+  char* ws = static_cast<char*>(workspace);
+  const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  pkv::WidenBlockScaledArgs w;
+  w.k_cache = static_cast<const uint8_t*>(k_cache);
+  w.v_cache = static_cast<const uint8_t*>(v_cache);
+  w.k_scales = k_scales;
+  w.v_scales = v_scales;
+  w.block_tables = block_tables;
+  w.context_lens = context_lens;
+  w.k_out = ws;
+  w.v_out = ws + v_off;
+  w.num_seqs = num_seqs;
+  w.max_blocks_per_seq = max_blocks_per_seq;
+  w.num_blocks = cache.num_blocks;
+  w.kv_heads = cache.kv_heads;
+  if (pkv::launch_widen_block_scaled(w, cache.d_head, sms, cs) != cudaSuccess) return PKV_ECUDA;
+  const int64_t row = int64_t(cache.kv_heads) * cache.d_head;
+  const int kv_stride = max_blocks_per_seq * kBlockSize;
+  return run_prompt(q, qrow, ws, row, ws + v_off, row, int64_t(num_seqs) * kv_stride, total_q,
+                    q_start, context_lens, kv_stride, num_seqs, q_heads, cache.kv_heads,
+                    cache.d_head, causal, scale, out, cs);
+}
 
 int pkv_kv_append_fp8_block_scaled(const void* k, int64_t k_tok_stride, const void* v,
                                    int64_t v_tok_stride, int64_t num_tokens,
@@ -2265,8 +2428,10 @@ int pkv_kv_append_fp8_block_scaled(const void* k, int64_t k_tok_stride, const vo
   a.max_blocks_per_seq = max_blocks_per_seq;
   a.num_blocks = cache.num_blocks;
   a.kv_heads = cache.kv_heads;
+  const int sms = current_device_sms();
+  if (sms <= 0) return PKV_ECUDA;
   const cudaError_t e =
-      pkv::launch_append_block_scaled(a, cache.d_head, static_cast<cudaStream_t>(stream));
+      pkv::launch_append_block_scaled(a, cache.d_head, sms, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKV_OK : PKV_ECUDA;
 }
 

@@ -27,6 +27,7 @@ cudaError_t draft_error_word(unsigned** word);
 cudaError_t tree_error_word(unsigned** word);
 cudaError_t block_scaled_error_word(unsigned** word);
 cudaError_t decode_block_scaled_error_word(unsigned** word);
+cudaError_t prompt_error_word(unsigned** word);
 
 // ---- kv_append.cu
 // reject (optional): a device flag set by launch_slot_duplicates; when it is
@@ -316,11 +317,20 @@ struct AppendBlockScaledArgs {
   int64_t total;  // rows of k and v
   int num_seqs, max_blocks_per_seq, num_blocks, kv_heads;
 };
-cudaError_t launch_append_block_scaled(const AppendBlockScaledArgs& a, int d_head,
+cudaError_t launch_append_block_scaled(const AppendBlockScaledArgs& a, int d_head, int num_sms,
                                        cudaStream_t stream);
 cudaError_t launch_copy_block_scales(float* k_scales, float* v_scales, const int32_t* pairs,
                                      int num_pairs, int num_blocks, int kv_heads,
                                      cudaStream_t stream, int num_sms);
+struct WidenBlockScaledArgs {
+  const uint8_t *k_cache, *v_cache;
+  const float *k_scales, *v_scales;
+  const int32_t *block_tables, *context_lens;
+  void *k_out, *v_out;  // bf16, num_seqs * max_blocks_per_seq * 16 rows
+  int num_seqs, max_blocks_per_seq, num_blocks, kv_heads;
+};
+cudaError_t launch_widen_block_scaled(const WidenBlockScaledArgs& a, int d_head, int num_sms,
+                                      cudaStream_t stream);
 unsigned read_block_scaled_error(bool clear);
 
 // ---- paged_decode_block_scaled.cu
@@ -341,5 +351,25 @@ cudaError_t launch_decode_block_scaled(const DecodeBlockScaledArgs& a, const CUt
                                        const CUtensorMap* tmap_v, int num_sms,
                                        cudaStream_t stream);
 unsigned read_decode_block_scaled_error(bool clear);
+
+// ---- prompt_attention.cu: queries over contiguous K and V rows
+struct PromptArgs {
+  const int32_t* q_start;
+  // null: a sequence's keys are the rows of its queries; else its keys, which
+  // start at row s * kv_stride
+  const int32_t* kv_lens;
+  const __nv_bfloat16* v;
+  int64_t v_stride;  // elements per row
+  __nv_bfloat16* out;
+  int num_seqs, total_q, q_heads, kv_heads, kv_stride, causal;
+  float scale_log2;
+};
+int prompt_tile_rows();           // query rows (tokens x heads) of a Q box
+int prompt_key_rows(int d_head);  // rows of a K box
+int prompt_value_rows();          // rows of a V box
+cudaError_t launch_prompt_attention(const PromptArgs& a, int d_head, const CUtensorMap* tmap_q,
+                                    const CUtensorMap* tmap_k, const CUtensorMap* tmap_v,
+                                    cudaStream_t stream);
+unsigned read_prompt_error(bool clear);
 
 }  // namespace pkv

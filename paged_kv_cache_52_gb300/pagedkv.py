@@ -197,6 +197,13 @@ SIGNATURES = {
     "pkv_paged_decode_attention_fp8_block_scaled_bf16out": (
         [_vp, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, CacheDesc, _vp, ctypes.c_int, _vp,
          ctypes.c_int, _f32, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "pkv_prefill_fp8_block_scaled_workspace_bytes": ([ctypes.c_int] * 4, _sz),
+    "pkv_paged_prefill_attention_fp8_block_scaled": (
+        [_vp, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp, CacheDesc, _vp,
+         ctypes.c_int, _vp, ctypes.c_int, _f32, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "pkv_prompt_attention": ([_vp, _i64, _vp, ctypes.c_int, ctypes.c_int, ctypes.c_int, _vp, _i64,
+                              _vp, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_int, _f32, _vp,
+                              _vp], ctypes.c_int),
     # host block manager (pagedkv_blocks.h); pointers are host memory
     "pkv_bm_create": ([_i32, _i32, ctypes.POINTER(_vp)], ctypes.c_int),
     "pkv_bm_destroy": ([_vp], None),
@@ -1155,6 +1162,52 @@ def paged_decode_attention_fp8_block_scaled(q: torch.Tensor, k_cache: torch.Tens
     return _done(name + "_bf16out" if bf16 else name, _marshal.decode_block_scaled(
         q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out,
         max_context_len, workspace, bf16))
+
+
+def prefill_fp8_block_scaled_workspace(num_seqs: int, max_blocks_per_seq: int, kv_heads: int,
+                                       d_head: int, device) -> torch.Tensor:
+    """Workspace of ``paged_prefill_attention_fp8_block_scaled``: every page that
+    the block tables can name, as bf16 rows of K and V."""
+    n = lib.pkv_prefill_fp8_block_scaled_workspace_bytes(num_seqs, max_blocks_per_seq, kv_heads,
+                                                         d_head)
+    _need(n > 0 or num_seqs == 0, "unsupported sizes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def paged_prefill_attention_fp8_block_scaled(q: torch.Tensor, q_start: torch.Tensor,
+                                             k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                             k_scales: torch.Tensor, v_scales: torch.Tensor,
+                                             block_tables: torch.Tensor,
+                                             context_lens: torch.Tensor, causal: bool,
+                                             scale: float, out: Optional[torch.Tensor] = None,
+                                             workspace: Optional[torch.Tensor] = None
+                                             ) -> torch.Tensor:
+    """Chunked prefill over a block-scaled FP8 cache: rows
+    ``q_start[s]:q_start[s+1]`` of ``q [total, Hq, d]`` are the last tokens of
+    sequence s (already appended).  Returns ``out`` bf16 ``[total, Hq, d]``."""
+    if workspace is None:
+        _need(k_cache.dim() == 4 and block_tables.dim() == 2,
+              "pools must be [NB, 16, Hkv, d], block_tables [S, max_blocks]")
+        workspace = prefill_fp8_block_scaled_workspace(context_lens.shape[0],
+                                                       block_tables.shape[1], k_cache.shape[2],
+                                                       k_cache.shape[3], q.device)
+    return _done("pkv_paged_prefill_attention_fp8_block_scaled", _marshal.prefill_block_scaled(
+        q, q_start, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, causal,
+        scale, out, workspace))
+
+
+# --------------------------------------------------------------------------
+# Attention of whole prompts, without a cache.
+# --------------------------------------------------------------------------
+def prompt_attention(q: torch.Tensor, q_start: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     causal: bool, scale: float,
+                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of packed prompts over their own keys and values: rows
+    ``q_start[s]:q_start[s+1]`` of ``q [T, Hq, d]`` and ``k, v [T, Hkv, d]`` (bf16
+    views with contiguous rows) are sequence s's tokens.  Returns ``out`` bf16
+    ``[T, Hq, d]``; rows of no sequence are not written."""
+    return _done("pkv_prompt_attention",
+                 _marshal.prompt_attention(q, q_start, k, v, causal, scale, out))
 
 
 # --------------------------------------------------------------------------
