@@ -2246,8 +2246,8 @@ int run_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
   if (!encode_rows_map(&tq, q, total_q, q_heads, d_head, q_stride, group,
                        pkv::prompt_tile_rows() / group) ||
       !encode_rows_map(&tk, k, kv_rows, kv_heads, d_head, k_stride, 1,
-                       pkv::prompt_key_rows(d_head)) ||
-      !encode_rows_map(&tv, v, kv_rows, kv_heads, d_head, v_stride, 1, pkv::prompt_value_rows()))
+                       pkv::prompt_tile_keys()) ||
+      !encode_rows_map(&tv, v, kv_rows, kv_heads, d_head, v_stride, 1, pkv::prompt_tile_keys()))
     return PKV_ECUDA;
   pkv::PromptArgs a;
   a.q_start = q_start;
@@ -2261,8 +2261,12 @@ int run_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
   a.kv_heads = kv_heads;
   a.kv_stride = kv_row_stride;
   a.causal = causal ? 1 : 0;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  const cudaError_t e = pkv::launch_prompt_attention(a, d_head, &tq, &tk, &tv, stream);
+  // a scale of 0 weighs every visible key alike: so does one too small to tell
+  // scores apart, which keeps a hidden key's -inf out of 0 * inf
+  a.scale_log2 = scale == 0.f ? 1e-30f : scale * 1.4426950408889634f;
+  const int sms = current_device_sms();
+  if (sms <= 0) return PKV_ECUDA;
+  const cudaError_t e = pkv::launch_prompt_attention(a, d_head, sms, &tq, &tk, &tv, stream);
   return e == cudaSuccess ? PKV_OK : (e == cudaErrorInvalidValue ? PKV_EUNSUPPORTED : PKV_ECUDA);
 }
 

@@ -364,12 +364,11 @@ struct PromptArgs {
   int num_seqs, total_q, q_heads, kv_heads, kv_stride, causal;
   float scale_log2;
 };
-int prompt_tile_rows();           // query rows (tokens x heads) of a Q box
-int prompt_key_rows(int d_head);  // rows of a K box
-int prompt_value_rows();          // rows of a V box
-cudaError_t launch_prompt_attention(const PromptArgs& a, int d_head, const CUtensorMap* tmap_q,
-                                    const CUtensorMap* tmap_k, const CUtensorMap* tmap_v,
-                                    cudaStream_t stream);
+int prompt_tile_rows();  // query rows (tokens x heads) of a Q box
+int prompt_tile_keys();  // rows of a K or V box
+cudaError_t launch_prompt_attention(const PromptArgs& a, int d_head, int num_sms,
+                                    const CUtensorMap* tmap_q, const CUtensorMap* tmap_k,
+                                    const CUtensorMap* tmap_v, cudaStream_t stream);
 unsigned read_prompt_error(bool clear);
 
 }  // namespace pkv

@@ -7,25 +7,22 @@
 //
 // Two matrix products of 2 n L d flops each per head, half of that under the
 // causal mask, over O((n + L) d) bytes: bound by the tensor cores.  Layout:
-//  * an item is TILES (times two in a pair) tiles of 128 rows -- 128 / G tokens
-//    times the G query heads of one KV head -- against the keys in tiles of
-//    128.  S and O of a tile stand in tensor memory, P (bf16) is written over
-//    S and read from there by the second product.
-//  * d_head 128: TILES 2, and two CTAs form a pair (cta_group::2): one MMA
-//    covers a row tile of each CTA, and each CTA holds half of the key tile's
-//    K rows and V columns.  One CTA alone reads 8 KB of operands per 64-cycle
-//    MMA from shared memory, all its bandwidth, while copies write there too.
-//  * d_head 64: TILES 1 and two CTAs per SM, whose softmax and MMA phases
-//    overlap, as do one's start and the other's work.
-//  * a thread owns a row in the softmax: no shuffles.  The running maximum is
-//    the ceiling of the largest score seen when it was last raised; a tile
-//    keeps it while every row's sum of weights over 64 keys is at most 2^16,
-//    so most tiles need no maximum.  It is a whole number, so raising it scales
-//    by a power of two, which rounds neither P nor O.
+//  * an item is two tiles of 128 rows -- 128 / G tokens times the G query heads
+//    of one KV head each -- against the keys in tiles of 128.  S and O of a row
+//    tile stand in tensor memory, P (bf16) is written over S and read from
+//    there by the second product.
+//  * one CTA per SM works through items for the whole launch: the copies run
+//    ahead into the next item, and its first products are issued while the
+//    last one's rows are written out.
+//  * a thread owns a row in the softmax, its 128 scores in registers: no
+//    shuffles, one trip to tensor memory.  P leaves in two halves, and the
+//    second product starts on the first.  O is rescaled only when the maximum
+//    rises by more than 8 (weights up to 2^8); a tile's S is complete only
+//    after the product before it, so O needs no barrier of its own.
 //  * P in bf16 is off by 2^-8 of each weight at most, as the bf16 output is of
 //    itself; S, O, the weights' sum and the maximum are float32.
-//  * items are taken longest first over all sequences (each CTA works its item
-//    out of q_start), heads side by side.
+//  * items are taken longest first over all sequences (worked out of q_start on
+//    the device), heads side by side.
 // Keys that no row sees: V rows past a sequence's end, which belong to the next
 // one or nobody, are zeroed in shared memory; NaN and infinities of V in the
 // tiles that the mask cuts are taken out of the product (0 times them is NaN)
@@ -41,172 +38,66 @@ namespace pkv {
 
 static __device__ unsigned g_prompt_error = 0;
 
-constexpr int kPrRows = 128;  // rows of a Q tile
-constexpr int kPrKeys = 128;  // keys of a K / V tile
-constexpr float kPrMaxSum = 65536.f;
+constexpr int kPrRows = 128;    // rows of a Q tile
+constexpr int kPrKeys = 128;    // keys of a K / V tile
+constexpr int kPrTiles = 2;     // Q tiles of an item, one softmax warpgroup each
+constexpr int kPrThreads = 352; // 2 softmax warpgroups, copies, MMA issue, V scrub
+constexpr int kPrLoadWarp = 8, kPrMmaWarp = 9, kPrScrubWarp = 10;
+constexpr float kPrRescale = 8.f;
+constexpr int kPrRegSeqs = 512;  // sequences whose items one warp holds in registers
+constexpr int kPrSlots = 4;      // items known ahead
 
-template <int D, bool PAIR>
+template <int D>
 struct PromptCfg {
-  static constexpr int kCtas = PAIR ? 2 : 1;
-  static constexpr int kTiles = D == 128 ? 2 : 1;  // Q tiles of a CTA
-  static constexpr int kSoftWarps = 4 * kTiles;
-  static constexpr int kThreads = kSoftWarps * 32 + 96;
-  static constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1,
-                       kScrubWarp = kSoftWarps + 2;
-  static constexpr int kQHalf = kPrRows * 128;             // 128 rows x 64 columns
-  static constexpr int kQTile = (D / 64) * kQHalf;
-  static constexpr int kKRows = kPrKeys / kCtas;           // K rows that this CTA holds
-  static constexpr int kKHalf = kKRows * 128;
-  static constexpr int kKTile = (D / 64) * kKHalf;
-  static constexpr int kVHalf = kPrKeys * 128;
-  static constexpr int kVCols = D / kCtas;                 // V columns that this CTA holds
-  static constexpr int kVTile = (kVCols / 64) * kVHalf;
-  static constexpr int kKStages = PAIR ? 5 : (D == 128 ? 2 : 3);
-  static constexpr int kVStages = PAIR ? 5 : 2;
+  static constexpr int kHalf = 128 * 128;             // 128 rows x 64 columns
+  static constexpr int kTile = (D / 64) * kHalf;      // of Q, K or V
+  static constexpr int kQBufs = D == 128 ? 1 : 2;     // items whose Q is there
+  static constexpr int kKStages = D == 128 ? 3 : 4;
+  static constexpr int kVStages = D == 128 ? 2 : 4;
   static constexpr int kQOff = 0;
-  static constexpr int kKOff = kQOff + kTiles * kQTile;
-  static constexpr int kVOff = kKOff + kKStages * kKTile;
-  static constexpr int kBarOff = kVOff + kVStages * kVTile;
-  // barriers
-  static constexpr int kQFull = 0, kKFull = 1, kKEmpty = kKFull + kKStages,
-                       kVFull = kKEmpty + kKStages, kVEmpty = kVFull + kVStages,
-                       kVLand = kVEmpty + kVStages, kVReady = kVLand + kVStages,
-                       kSFull = kVReady + kVStages, kPFull = kSFull + 2, kODone = kPFull + 2,
-                       kDrain = kODone + 2, kNumBars = kDrain + 1;
-  static constexpr int kMiscOff = kBarOff + kNumBars * 8;  // tmem, abort, non-finite, item (3)
-  static constexpr int kSmemBytes = kMiscOff + 32 + 1024;
-  static constexpr uint32_t kTmemCols = kTiles == 2 ? 512 : 256;
-  static constexpr uint32_t kTileCols = 256;               // S / P, then O at 128
-  static_assert(kTiles == 2 ? kSmemBytes <= 232448 : 2 * (kSmemBytes + 1024) <= 233472,
-                "one CTA of two tiles, two CTAs of one, to an SM's shared memory");
+  static constexpr int kKOff = kQOff + kQBufs * kPrTiles * kTile;
+  static constexpr int kVOff = kKOff + kKStages * kTile;
+  static constexpr int kBarOff = kVOff + kVStages * kTile;
+  // barriers: a tile's P in two halves; O read out; an item's data in its slot
+  static constexpr int kQFull = 0, kQEmpty = kQFull + kQBufs, kKFull = kQEmpty + kQBufs,
+                       kKEmpty = kKFull + kKStages, kVLand = kKEmpty + kKStages,
+                       kVReady = kVLand + kVStages, kVEmpty = kVReady + kVStages,
+                       kSFull = kVEmpty + kVStages, kPFull = kSFull + kPrTiles,
+                       kODone = kPFull + 2 * kPrTiles, kOFree = kODone + kPrTiles,
+                       kItem = kOFree + kPrTiles, kItemFree = kItem + kPrSlots,
+                       kDrain = kItemFree + kPrSlots,
+                       kNumBars = kDrain + 1;
+  static constexpr int kItemOff = kBarOff + kNumBars * 8;
+  static constexpr int kMiscOff = kItemOff + kPrSlots * 32;  // tensor memory's base, abort flag
+  static constexpr int kSmemBytes = kMiscOff + 16 + 1024;
+  static constexpr uint32_t kTmemCols = 512, kTileCols = 256;  // S / P, then O at 128
+  static_assert(kSmemBytes <= 232448, "shared memory");
 };
 
-// ---- cluster forms
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The address of this CTA's shared `addr` in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
-template <bool PAIR>
-struct Pr {
-  static __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
-    return PAIR ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity);
-  }
-  // Bounded; gives up as soon as another role of this CTA has aborted.
-  static __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity,
-                                              volatile int* abort_flag) {
-    for (uint32_t i = 0; i < kWaitPollLimit; ++i) {
-      if (try_wait(bar, parity)) return true;
-      if ((i & 255u) == 255u && *abort_flag) return false;
-    }
-    return false;
-  }
-  static __device__ __forceinline__ void wait_anyway(uint32_t bar, uint32_t parity) {
-    for (uint32_t i = 0; i < kWaitPollLimit; ++i)
-      if (try_wait(bar, parity)) return;
-  }
-  // One arrival on the leading CTA's barrier (`bar` as mapped there).
-  static __device__ __forceinline__ void arrive(uint32_t bar) {
-    if constexpr (PAIR) mbar_arrive_cluster(bar);
-    else mbar_arrive(bar);
-  }
-  static __device__ __forceinline__ void load(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                              int c0, int c1, int c2) {
-    if constexpr (PAIR)
-      asm volatile(
-          "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx"
-          "::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-          "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-          : "memory");
-    else
-      tma_load_3d(dst, map, bar, c0, c1, c2);
-  }
-  static __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                             uint32_t acc) {
-    if constexpr (PAIR)
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "setp.ne.b32 p, %4, 0;\n\t"
-          "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-          "l"(a), "l"(b), "r"(idesc), "r"(acc)
-          : "memory");
-    else
-      umma_bf16(d, a, b, idesc, acc);
-  }
-  static __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                                uint32_t acc) {
-    if constexpr (PAIR)
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "setp.ne.b32 p, %4, 0;\n\t"
-          "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-          "r"(a), "l"(b), "r"(idesc), "r"(acc)
-          : "memory");
-    else
-      umma_bf16_ts(d, a, b, idesc, acc);
-  }
-  // Arrives on `bar` in every CTA once the MMAs issued so far are done.
-  static __device__ __forceinline__ void commit(uint32_t bar) {
-    if constexpr (PAIR)
-      asm volatile(
-          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-          " [%0], %1;" ::"r"(bar),
-          "h"(uint16_t(3))
-          : "memory");
-    else
-      umma_commit(bar);
-  }
-  static __device__ __forceinline__ void alloc(uint32_t dst, uint32_t cols) {
-    if constexpr (PAIR) {
-      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst),
-                   "r"(cols)
-                   : "memory");
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    } else {
-      tmem_alloc(dst, cols);
-      tmem_relinquish();
-    }
-  }
-  static __device__ __forceinline__ void dealloc(uint32_t addr, uint32_t cols) {
-    if constexpr (PAIR)
-      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols)
-                   : "memory");
-    else
-      tmem_dealloc(addr, cols);
-  }
+// What the roles need of an item (32 bytes in a slot).
+struct PromptItem {
+  int seq;   // -1: no more
+  int kvh, qs, n, keys;
+  int t0;    // first query token
+  int row0;  // first K / V row
+  int odd;   // NaN or infinities were taken out of V
 };
+
+// Bounded wait that also gives up as soon as another role has aborted.
+__device__ __forceinline__ bool pr_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  for (uint32_t i = 0; i < kWaitPollLimit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 255u) == 255u && *abort_flag) return false;
+  }
+  return false;
+}
 
 __device__ __forceinline__ void pr_abort(volatile int* abort_flag) {
   *abort_flag = 1;
   atomicOr(&g_prompt_error, kErrWaitTimeout);
 }
 
-// A sequence's rows and keys.
+// A sequence's rows and keys; none where they are out of order.
 struct PromptSeq {
   int qs, n, keys;
   bool bad;
@@ -224,563 +115,609 @@ __device__ __forceinline__ PromptSeq prompt_seq(const PromptArgs& p, int s) {
   return q;
 }
 
-// Item `rank` of the launch, by one warp: items of `tpc` tokens, those with the
-// most keys first.  The level of an item is its last key over tpc (all keys'
-// when not causal); a sequence has one item of each of its levels, from
-// lo = (keys - n) / tpc on.  Finds the level by bisection over the counts of
-// items at or above one, then the sequence within it.  False: no such item.
-__device__ __forceinline__ bool prompt_item(const PromptArgs& p, int tpc, long long rank, int& seq,
-                                            int& tile) {
-  const int lane = threadIdx.x & 31;
-  constexpr unsigned kFull = 0xffffffffu;
-  // items of sequence s at `level` or above
-  auto above = [&](int s, int level) {
-    const PromptSeq q = prompt_seq(p, s);
-    const int items = (q.n + tpc - 1) / tpc;
-    if (!p.causal) return q.keys / tpc >= level ? items : 0;
-    const int lo = (q.keys - q.n) / tpc;
-    return min(items, max(0, lo + items - level));
-  };
-  auto count = [&](int level) {
-    long long c = 0;
-    for (int s = lane; s < p.num_seqs; s += 32) c += above(s, level);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(kFull, c, o);
-    return c;
-  };
-  int top = 0;
-  for (int s = lane; s < p.num_seqs; s += 32) {
-    const PromptSeq q = prompt_seq(p, s);
-    if (q.n > 0) top = max(top, p.causal ? (q.keys - q.n) / tpc + (q.n + tpc - 1) / tpc : q.keys / tpc + 1);
-  }
-  top = __reduce_max_sync(kFull, top);  // no item at this level
-  if (count(0) <= rank) return false;
-  int lo = 0, hi = top;  // count(lo) > rank >= count(hi) = 0 or so
-  while (hi - lo > 1) {
-    const int mid = lo + (hi - lo) / 2;
-    if (count(mid) > rank) lo = mid;
-    else hi = mid;
-  }
-  long long rest = rank - (hi >= top ? 0 : count(hi));
-  // the rest-th item of level lo, sequences in order
-  for (int s0 = 0; s0 < p.num_seqs; s0 += 32) {
-    const int s = s0 + lane;
-    const int mine = s < p.num_seqs ? above(s, lo) - above(s, lo + 1) : 0;
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(kFull, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const int all = __shfl_sync(kFull, incl, 31);
-    if (rest < all) {
-      const unsigned hit = __ballot_sync(kFull, incl > rest);
-      const int who = __ffs(hit) - 1;
-      const int before = __shfl_sync(kFull, incl - mine, who);
-      seq = s0 + who;
-      const PromptSeq q = prompt_seq(p, seq);
-      tile = p.causal ? lo - (q.keys - q.n) / tpc : int(rest) - before;
-      return true;
-    }
-    rest -= all;
-  }
-  return false;
+// The items of one sequence: `items` of tpc tokens, causal ones at levels lo,
+// lo + 1, ... (the last key over tpc), else all at level lo.
+struct PromptLevels {
+  int lo, items;
+};
+__device__ __forceinline__ PromptLevels prompt_levels(const PromptArgs& p, int s, int tpc) {
+  const PromptSeq q = prompt_seq(p, s);
+  PromptLevels v;
+  v.items = (q.n + tpc - 1) / tpc;
+  v.lo = v.items == 0 ? 0 : (p.causal ? q.keys - q.n : q.keys) / tpc;
+  return v;
 }
 
-template <int D, int G, bool PAIR>
-__global__ void __launch_bounds__(PromptCfg<D, PAIR>::kThreads, PromptCfg<D, PAIR>::kTiles == 2 ? 1 : 2)
+// Item `rank` of a KV head, by one warp, those with the most keys first: finds
+// the level by bisection over the counts of items at or above one, then the
+// sequence within it.  `own`: lane l's sequences l, l + 32, ... of the first
+// kPrRegSeqs; the others' are worked out again each time.
+struct PromptTable {
+  PromptLevels own[kPrRegSeqs / 32];
+
+  __device__ __forceinline__ void load(const PromptArgs& p, int tpc) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < kPrRegSeqs / 32; ++i) {
+      const int s = i * 32 + lane;
+      own[i] = s < p.num_seqs ? prompt_levels(p, s, tpc) : PromptLevels{0, 0};
+    }
+  }
+  // f(levels, sequence of lane 0) for every lane's sequences until it is false
+  template <typename F>
+  __device__ __forceinline__ void each(const PromptArgs& p, int tpc, F&& f) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < kPrRegSeqs / 32; ++i) {
+      if (i * 32 >= p.num_seqs) return;
+      if (!f(own[i], i * 32)) return;
+    }
+    for (int s0 = kPrRegSeqs; s0 < p.num_seqs; s0 += 32) {
+      const int s = s0 + lane;
+      if (!f(s < p.num_seqs ? prompt_levels(p, s, tpc) : PromptLevels{0, 0}, s0)) return;
+    }
+  }
+  __device__ __forceinline__ bool item(const PromptArgs& p, int tpc, long long rank, int& seq,
+                                       int& tile) const {
+    constexpr unsigned kFull = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    const bool causal = p.causal != 0;
+    auto above = [&](const PromptLevels& v, int level) {
+      if (!causal) return v.lo >= level ? v.items : 0;
+      return min(v.items, max(0, v.lo + v.items - level));
+    };
+    auto count = [&](int level) {
+      long long c = 0;
+      each(p, tpc, [&](const PromptLevels& v, int) {
+        c += above(v, level);
+        return true;
+      });
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(kFull, c, o);
+      return c;
+    };
+    int top = 0;  // no item at this level
+    each(p, tpc, [&](const PromptLevels& v, int) {
+      if (v.items > 0) top = max(top, v.lo + (causal ? v.items : 1));
+      return true;
+    });
+    top = __reduce_max_sync(kFull, top);
+    if (count(0) <= rank) return false;
+    int lo = 0, hi = top;  // count(lo) > rank >= count(hi)
+    while (hi - lo > 1) {
+      const int mid = lo + (hi - lo) / 2;
+      if (count(mid) > rank) lo = mid;
+      else hi = mid;
+    }
+    long long rest = rank - count(lo + 1);
+    // the rest-th item of level lo, sequences in order
+    each(p, tpc, [&](const PromptLevels& v, int s0) {
+      const int mine = above(v, lo) - above(v, lo + 1);
+      int incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += u;
+      }
+      const int all = __shfl_sync(kFull, incl, 31);
+      if (rest >= all) {
+        rest -= all;
+        return true;
+      }
+      const int who = __ffs(__ballot_sync(kFull, incl > rest)) - 1;
+      const int before = __shfl_sync(kFull, incl - mine, who);
+      const int at = __shfl_sync(kFull, v.lo, who);
+      seq = s0 + who;
+      tile = causal ? lo - at : int(rest) - before;
+      return false;
+    });
+    return true;
+  }
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(kPrThreads, 1)
 prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         const __grid_constant__ CUtensorMap tmap_k,
                         const __grid_constant__ CUtensorMap tmap_v, const PromptArgs p) {
-  using C = PromptCfg<D, PAIR>;
-  using X = Pr<PAIR>;
-  constexpr int kTiles = C::kTiles, kCtas = C::kCtas;
-  constexpr int kKStages = C::kKStages, kVStages = C::kVStages;
-  constexpr int TPT = kPrRows / G;              // tokens of a Q tile
-  constexpr int TPS = TPT * kCtas;              // tokens that one MMA covers
-  constexpr int TPC = TPS * kTiles;             // tokens of an item
+  using C = PromptCfg<D>;
+  constexpr int kKStages = C::kKStages, kVStages = C::kVStages, kQBufs = C::kQBufs;
+  constexpr int TPT = kPrRows / G;        // tokens of a Q tile
+  constexpr int TPC = TPT * kPrTiles;     // tokens of an item
   griddep_wait();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bars = sbase + C::kBarOff;
+  PromptItem* slots = reinterpret_cast<PromptItem*>(smem + C::kItemOff);
   volatile int* misc = reinterpret_cast<volatile int*>(smem + C::kMiscOff);
   volatile int* abort_flag = misc + 1;
-  volatile int* nonfinite = misc + 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = PAIR ? cluster_rank() : 0;
-  const long long work = blockIdx.x / kCtas;
-  const int kvh = int(work % p.kv_heads);
-  if (work == 0 && rank == 0)
-    for (int s = threadIdx.x; s < p.num_seqs; s += C::kThreads)
-      if (prompt_seq(p, s).bad) atomicOr(&g_prompt_error, kErrBadQueryRange);
 
-  // ---- this CTA's item, barriers, tensor memory
-  if (warp == 0) {
-    int seq = 0, tile = 0;
-    const bool some = prompt_item(p, TPC, work / p.kv_heads, seq, tile);
-    if (lane == 0) {
-      misc[3] = some ? seq : -1;
-      misc[4] = tile;
-      *abort_flag = 0;
-      *nonfinite = 0;
-    }
-  } else if (warp == C::kLoadWarp && lane == 0) {
-    auto init = [&](int b, int n) { mbar_init(bars + 8 * b, n); };
-    init(C::kQFull, 1);
-    for (int s = 0; s < kKStages; ++s) {
-      init(C::kKFull + s, 1);
-      init(C::kKEmpty + s, 1);
-    }
-    for (int s = 0; s < kVStages; ++s) {
-      init(C::kVFull + s, 1);
-      init(C::kVEmpty + s, 1);
-      init(C::kVLand + s, 1);
-      init(C::kVReady + s, kCtas);
-    }
-    for (int t = 0; t < 2; ++t) {
-      init(C::kSFull + t, 1);
-      init(C::kPFull + t, 4 * kCtas);
-      init(C::kODone + t, 1);
-    }
-    init(C::kDrain, 1);
+  if (blockIdx.x == 0)
+    for (int s = threadIdx.x; s < p.num_seqs; s += kPrThreads)
+      if (prompt_seq(p, s).bad) atomicOr(&g_prompt_error, kErrBadQueryRange);
+  if (warp == kPrLoadWarp && lane == 0) {
+    auto init = [&](int b, int count, int n) {
+      for (int i = 0; i < n; ++i) mbar_init(bars + 8 * (b + i), count);
+    };
+    init(C::kQFull, 1, kQBufs);
+    init(C::kQEmpty, 1, kQBufs);
+    init(C::kKFull, 1, kKStages);
+    init(C::kKEmpty, 1, kKStages);
+    init(C::kVLand, 1, kVStages);
+    init(C::kVReady, 1, kVStages);
+    init(C::kVEmpty, 1, kVStages);
+    init(C::kSFull, 1, kPrTiles);
+    init(C::kPFull, 4, 2 * kPrTiles);
+    init(C::kODone, 1, kPrTiles);
+    init(C::kOFree, 4, kPrTiles);
+    init(C::kItem, 1, kPrSlots);
+    init(C::kItemFree, 2 + 4 * kPrTiles, kPrSlots);  // copies, MMA, softmax warps
+    init(C::kDrain, 1, 1);
     fence_barrier_init();
+    *abort_flag = 0;
     tma_prefetch_desc(&tmap_q);
     tma_prefetch_desc(&tmap_k);
     tma_prefetch_desc(&tmap_v);
   }
-  __syncthreads();
-  const int seq = misc[3];
-  if (seq < 0) return;  // both CTAs of a pair alike
-  if (warp == C::kMmaWarp) X::alloc(sbase + C::kMiscOff, C::kTmemCols);
+  if (warp == kPrMmaWarp) {
+    tmem_alloc(sbase + C::kMiscOff, C::kTmemCols);
+    tmem_relinquish();
+  }
   tc_fence_before();
-  if constexpr (PAIR) cluster_sync_all();
-  else __syncthreads();
+  __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uint32_t(misc[0]);
-  const PromptSeq sq = prompt_seq(p, seq);
-  const int t0 = misc[4] * TPC;
-  const long long row0 = p.kv_lens ? (long long)seq * p.kv_stride : sq.qs;  // first K / V row
-  // key tiles that each MMA row tile needs (0: it has no rows), and the first
-  // key tile that some row does not see whole
-  int nt[kTiles];
-#pragma unroll
-  for (int t = 0; t < kTiles; ++t) {
-    const int first = t0 + t * TPS, last = min(sq.n, first + TPS);
-    const int end = p.causal ? sq.keys - sq.n + last : sq.keys;
-    nt[t] = first < sq.n ? (end + kPrKeys - 1) / kPrKeys : 0;
-  }
-  const int ntiles = kTiles == 2 ? max(nt[0], nt[kTiles - 1]) : nt[0];
-  const int cut = p.causal ? (sq.keys - sq.n + t0 + 1) / kPrKeys : sq.keys / kPrKeys;
-  const uint32_t lead = PAIR ? in_cta(bars, 0) : bars;  // the leading CTA's barriers
-  // the number of tile j among the cut tiles of its ring slot
-  auto cut_phase = [&](int j) {
-    const int st = j % kVStages;
-    const int j0 = cut + (st - cut % kVStages + kVStages) % kVStages;
-    return uint32_t((j - j0) / kVStages) & 1u;
-  };
 
-  if (warp == C::kLoadWarp) {
+  // Key tiles that row tile t needs (0: it has no rows), and the first key tile
+  // that some row does not see whole.
+  auto tiles_of = [&](const PromptItem& it, int t) {
+    const int first = it.t0 + t * TPT, last = min(it.n, first + TPT);
+    const int end = p.causal ? it.keys - it.n + last : it.keys;
+    return first < it.n ? (end + kPrKeys - 1) / kPrKeys : 0;
+  };
+  auto cut_of = [&](const PromptItem& it) {
+    return p.causal ? (it.keys - it.n + it.t0 + 1) / kPrKeys : it.keys / kPrKeys;
+  };
+  // A role's next item from its slot (i counts items).
+  auto take = [&](int i, PromptItem& it) {
+    const int sl = i % kPrSlots;
+    if (!pr_wait(bars + 8 * (C::kItem + sl), (i / kPrSlots) & 1, abort_flag)) return false;
+    it = slots[sl];
+    return true;
+  };
+  auto give_back = [&](int i) { mbar_arrive(bars + 8 * (C::kItemFree + i % kPrSlots)); };
+  // Whole-warp wait.
+  auto all_wait = [&](int bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, pr_wait(bars + 8 * bar, parity, abort_flag));
+  };
+  // Tiles are numbered through the launch: tile c of a ring of n is the
+  // (c / n)-th in slot c % n.
+
+  if (warp == kPrLoadWarp) {
     // ================= copies (one thread) =================
     if (lane == 0) {
-      int k_issued = 0, v_issued = 0;
+      uint32_t kc = 0, vc = 0;  // tiles issued
+      uint32_t qc = 0;
       bool ok = true;
-      if (rank == 0) mbar_arrive_expect_tx(bars + 8 * C::kQFull, kCtas * kTiles * C::kQTile);
+      for (int i = 0; ok; ++i) {
+        PromptItem it;
+        ok = take(i, it);
+        if (!ok || it.seq < 0) break;
+        give_back(i);
+        const int ntiles = max(tiles_of(it, 0), tiles_of(it, 1));
+        auto load_k = [&](int j) {
+          const uint32_t st = kc % kKStages;
+          if (kc >= kKStages && !pr_wait(bars + 8 * (C::kKEmpty + st), (kc / kKStages - 1) & 1, abort_flag))
+            return false;
+          const uint32_t bar = bars + 8 * (C::kKFull + st);
+          mbar_arrive_expect_tx(bar, C::kTile);
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t)
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(sbase + C::kKOff + st * C::kTile + h * C::kHalf, &tmap_k, bar, h * 64, it.kvh,
+                        it.row0 + j * kPrKeys);
+          ++kc;
+          return true;
+        };
+        auto load_v = [&](int j) {
+          const uint32_t st = vc % kVStages;
+          if (vc >= kVStages && !pr_wait(bars + 8 * (C::kVEmpty + st), (vc / kVStages - 1) & 1, abort_flag))
+            return false;
+          const uint32_t bar = bars + 8 * (C::kVLand + st);
+          mbar_arrive_expect_tx(bar, C::kTile);
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-          X::load(sbase + C::kQOff + t * C::kQTile + h * C::kQHalf, &tmap_q, lead + 8 * C::kQFull,
-                  h * 64, kvh * G, sq.qs + t0 + t * TPS + int(rank) * TPT);
-      auto load_k = [&](int j) {
-        const int st = j % kKStages;
-        if (j >= kKStages && !X::wait(bars + 8 * (C::kKEmpty + st), (j / kKStages - 1) & 1, abort_flag))
-          return false;
-        if (rank == 0) mbar_arrive_expect_tx(bars + 8 * (C::kKFull + st), kCtas * C::kKTile);
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(sbase + C::kVOff + st * C::kTile + h * C::kHalf, &tmap_v, bar, h * 64, it.kvh,
+                        it.row0 + j * kPrKeys);
+          ++vc;
+          return true;
+        };
+        const uint32_t qb = qc % kQBufs;
+        ok = qc < kQBufs || pr_wait(bars + 8 * (C::kQEmpty + qb), (qc / kQBufs - 1) & 1, abort_flag);
+        if (!ok) break;
+        mbar_arrive_expect_tx(bars + 8 * (C::kQFull + qb), kPrTiles * C::kTile);
 #pragma unroll
-        for (int h = 0; h < D / 64; ++h)
-          X::load(sbase + C::kKOff + st * C::kKTile + h * C::kKHalf, &tmap_k,
-                  lead + 8 * (C::kKFull + st), h * 64, kvh,
-                  int(row0) + j * kPrKeys + int(rank) * C::kKRows);
-        ++k_issued;
-        return true;
-      };
-      auto load_v = [&](int j) {
-        const int st = j % kVStages;
-        if (j >= kVStages && !X::wait(bars + 8 * (C::kVEmpty + st), (j / kVStages - 1) & 1, abort_flag))
-          return false;
-        // a cut tile lands on this CTA's own barrier, for the scrub warp
-        const bool own = j >= cut;
-        if (own) mbar_arrive_expect_tx(bars + 8 * (C::kVLand + st), C::kVTile);
-        else if (rank == 0) mbar_arrive_expect_tx(bars + 8 * (C::kVFull + st), kCtas * C::kVTile);
-        const uint32_t bar = own ? bars + 8 * (C::kVLand + st) : lead + 8 * (C::kVFull + st);
+        for (int t = 0; t < kPrTiles; ++t)
 #pragma unroll
-        for (int h = 0; h < C::kVCols / 64; ++h)
-          X::load(sbase + C::kVOff + st * C::kVTile + h * C::kVHalf, &tmap_v, bar,
-                  int(rank) * C::kVCols + h * 64, kvh, int(row0) + j * kPrKeys);
-        ++v_issued;
-        return true;
-      };
-      ok = load_k(0);
-      for (int j = 0; ok && j < ntiles; ++j) {
-        if (j + 1 < ntiles) ok = load_k(j + 1);
-        ok = ok && load_v(j);
+          for (int h = 0; h < D / 64; ++h)
+            tma_load_3d(sbase + C::kQOff + (qb * kPrTiles + t) * C::kTile + h * C::kHalf, &tmap_q,
+                        bars + 8 * (C::kQFull + qb), h * 64, it.kvh * G, it.qs + it.t0 + t * TPT);
+        ++qc;
+        ok = load_k(0);
+        for (int j = 0; ok && j < ntiles; ++j) {
+          if (j + 1 < ntiles) ok = load_k(j + 1);
+          ok = ok && load_v(j);
+        }
       }
       if (!ok) pr_abort(abort_flag);
-      // after an abort: what this CTA can see of its copies lands before it ends
-      if (*abort_flag) {
-        if (rank == 0) {
-          X::wait_anyway(bars + 8 * C::kQFull, 0);
-          for (int j = max(0, k_issued - kKStages); j < k_issued; ++j)
-            X::wait_anyway(bars + 8 * (C::kKFull + j % kKStages), (j / kKStages) & 1);
-          for (int j = max(0, v_issued - kVStages); j < v_issued && j < cut; ++j)
-            X::wait_anyway(bars + 8 * (C::kVFull + j % kVStages), (j / kVStages) & 1);
-        }
-        for (int j = max(cut, v_issued - kVStages); j < v_issued; ++j)
-          X::wait_anyway(bars + 8 * (C::kVLand + j % kVStages), cut_phase(j));
+      if (*abort_flag) {  // the copies in flight land before the CTA ends
+        for (uint32_t c = qc > kQBufs ? qc - kQBufs : 0; c < qc; ++c)
+          (void)mbar_wait_bounded(bars + 8 * (C::kQFull + c % kQBufs), (c / kQBufs) & 1);
+        for (uint32_t c = kc > kKStages ? kc - kKStages : 0; c < kc; ++c)
+          (void)mbar_wait_bounded(bars + 8 * (C::kKFull + c % kKStages), (c / kKStages) & 1);
+        for (uint32_t c = vc > kVStages ? vc - kVStages : 0; c < vc; ++c)
+          (void)mbar_wait_bounded(bars + 8 * (C::kVLand + c % kVStages), (c / kVStages) & 1);
       }
     }
     __syncwarp();
-  } else if (warp == C::kScrubWarp) {
-    // ===== V tiles that the mask cuts: rows past the end to zero, NaN and infinities out =====
-    for (int j = cut; j < ntiles; ++j) {
-      const int st = j % kVStages;
-      const bool ok = __all_sync(0xffffffffu,
-                                 X::wait(bars + 8 * (C::kVLand + st), cut_phase(j), abort_flag));
-      if (!ok) {
-        if (lane == 0) pr_abort(abort_flag);
-        break;
+  } else if (warp == kPrScrubWarp) {
+    // ===== the items, and V tiles: those that the mask cuts lose the rows past the
+    // sequence's end, NaN and infinities =====
+    PromptTable table;
+    table.load(p, TPC);
+    // Item k of this CTA: rounds of one per CTA, every other one from the far end
+    // (whoever has the longest of one round gets the shortest of the next).
+    auto publish = [&](int k) {
+      const long long g = gridDim.x;
+      const long long work =
+          k * g + ((k & 1) ? g - 1 - (long long)blockIdx.x : (long long)blockIdx.x);
+      PromptItem it = {-1, 0, 0, 0, 0, 0, 0, 0};
+      int seq = -1, tile = 0;
+      if (table.item(p, TPC, work / p.kv_heads, seq, tile)) {
+        const PromptSeq q = prompt_seq(p, seq);
+        it.seq = seq;
+        it.kvh = int(work % p.kv_heads);
+        it.qs = q.qs;
+        it.n = q.n;
+        it.keys = q.keys;
+        it.t0 = tile * TPC;
+        it.row0 = p.kv_lens ? seq * p.kv_stride : q.qs;
       }
-      const uint32_t v = sbase + C::kVOff + st * C::kVTile;
-      const int live = sq.keys - j * kPrKeys;  // rows of this tile that are the sequence's
-      bool found = false;
+      const int sl = k % kPrSlots;
+      if (k >= kPrSlots && !all_wait(C::kItemFree + sl, (k / kPrSlots - 1) & 1)) it.seq = -2;
+      if (lane == 0 && it.seq != -2) {
+        slots[sl] = it;
+        mbar_arrive(bars + 8 * (C::kItem + sl));
+      }
+      return it;
+    };
+    uint32_t vc = 0;
+    PromptItem next = publish(0);
+    bool ok = next.seq != -2;
+    for (int i = 0; ok && next.seq >= 0; ++i) {
+      const PromptItem it = next;
+      next = publish(i + 1);
+      ok = next.seq != -2;
+      const int ntiles = max(tiles_of(it, 0), tiles_of(it, 1)), cut = cut_of(it);
+      for (int j = 0; ok && j < ntiles; ++j, ++vc) {
+        const uint32_t st = vc % kVStages;
+        ok = all_wait(C::kVLand + st, (vc / kVStages) & 1);
+        if (!ok) break;
+        if (j >= cut) {
+          const uint32_t v = sbase + C::kVOff + st * C::kTile;
+          const int live = it.keys - j * kPrKeys;  // rows of this tile that are the sequence's
+          bool found = false;
 #pragma unroll 4
-      for (int i = lane; i < C::kVTile / 16; i += 32) {
-        const int row = (i >> 3) % kPrKeys;
-        uint32_t w[4];
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(v + i * 16)
-                     : "memory");
-        if (row >= live) {
-          st_shared_zero16(v + i * 16);
-          continue;
-        }
-        uint32_t odd = 0;
+          for (int x = lane; x < C::kTile / 16; x += 32) {
+            const int row = (x >> 3) % kPrKeys;
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(v + x * 16)
+                         : "memory");
+            if (row >= live) {
+              st_shared_zero16(v + x * 16);
+              continue;
+            }
+            uint32_t odd[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) odd |= __vcmpgeu2(w[c] & 0x7fff7fffu, 0x7f807f80u);
-        if (odd) {
-          found = true;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) w[c] &= ~__vcmpgeu2(w[c] & 0x7fff7fffu, 0x7f807f80u);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(v + i * 16), "r"(w[0]),
-                       "r"(w[1]), "r"(w[2]), "r"(w[3])
-                       : "memory");
+            for (int c = 0; c < 4; ++c) odd[c] = __vcmpgeu2(w[c] & 0x7fff7fffu, 0x7f807f80u);
+            if (odd[0] | odd[1] | odd[2] | odd[3]) {
+              found = true;
+              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(v + x * 16),
+                           "r"(w[0] & ~odd[0]), "r"(w[1] & ~odd[1]), "r"(w[2] & ~odd[2]),
+                           "r"(w[3] & ~odd[3])
+                           : "memory");
+            }
+          }
+          fence_proxy_async_smem();
+          if (__any_sync(0xffffffffu, found) && lane == 0)
+            *const_cast<volatile int*>(&slots[i % kPrSlots].odd) = 1;
+          __syncwarp();
         }
+        if (lane == 0) mbar_arrive(bars + 8 * (C::kVReady + st));
       }
-      fence_proxy_async_smem();
-      if (__any_sync(0xffffffffu, found) && lane == 0) {
-#pragma unroll
-        for (int c = 0; c < kCtas; ++c) {
-          const uint32_t at = sbase + C::kMiscOff + 8;
-          if constexpr (PAIR)
-            asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(in_cta(at, c)), "r"(1) : "memory");
-          else
-            *nonfinite = 1;
-        }
-      }
-      __syncwarp();
-      if (lane == 0) X::arrive(lead + 8 * (C::kVReady + st));
     }
-  } else if (warp == C::kMmaWarp) {
-    // ================= MMA issue (one thread of the leading CTA) =================
-    if (lane == 0 && rank == 0) {
-      constexpr uint32_t kIdescS = idesc_bf16_f32(kPrRows * kCtas, kPrKeys, 0, 0);
-      constexpr uint32_t kIdescPV = idesc_bf16_f32(kPrRows * kCtas, D, 0, 1);
-      auto issue_s = [&](int t, int j) {
-        const uint32_t q = sbase + C::kQOff + t * C::kQTile;
-        const uint32_t k = sbase + C::kKOff + (j % kKStages) * C::kKTile;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          X::mma(tmem + t * C::kTileCols,
-                 smem_desc_sw128(q + (i >> 2) * C::kQHalf + (i & 3) * 32, 16, 1024),
-                 smem_desc_sw128(k + (i >> 2) * C::kKHalf + (i & 3) * 32, 16, 1024), kIdescS, i > 0);
-        X::commit(bars + 8 * (C::kSFull + t));
-      };
-      auto issue_pv = [&](int t, int j) {
-        const uint32_t v = sbase + C::kVOff + (j % kVStages) * C::kVTile;
-        const uint32_t at = tmem + t * C::kTileCols;
-#pragma unroll
-        for (int i = 0; i < kPrKeys / 16; ++i)
-          X::mma_ts(at + 128, at + 64 * (i >> 2) + 8 * (i & 3),
-                    smem_desc_sw128(v + i * 2048, C::kVHalf, 1024), kIdescPV, j > 0 || i > 0);
-        X::commit(bars + 8 * (C::kODone + t));
-      };
+    if (!ok && lane == 0) pr_abort(abort_flag);
+  } else if (warp == kPrMmaWarp) {
+    // ================= MMA issue (one thread) =================
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = idesc_bf16_f32(kPrRows, kPrKeys, 0, 0);
+      constexpr uint32_t kIdescPV = idesc_bf16_f32(kPrRows, D, 0, 1);
       auto ready = [&](int bar, uint32_t parity) {
-        if (!X::wait(bars + 8 * bar, parity, abort_flag)) return false;
+        if (!pr_wait(bars + 8 * bar, parity, abort_flag)) return false;
         tc_fence_after();
         return true;
       };
-      auto k_ready = [&](int j) { return ready(C::kKFull + j % kKStages, (j / kKStages) & 1); };
-      auto v_ready = [&](int j) {
-        return j < cut ? ready(C::kVFull + j % kVStages, (j / kVStages) & 1)
-                       : ready(C::kVReady + j % kVStages, cut_phase(j));
-      };
-      bool ok = ready(C::kQFull, 0) && k_ready(0);
-      if (ok) {
+      uint32_t kc = 0, vc = 0;              // tiles consumed
+      uint32_t pc[kPrTiles] = {0, 0};       // P tiles of row tile t
+      uint32_t oc[kPrTiles] = {0, 0};       // items with rows in row tile t
+      bool ok = true;
+      for (int i = 0; ok; ++i) {
+        PromptItem it;
+        ok = take(i, it);
+        if (!ok || it.seq < 0) break;
+        give_back(i);
+        const int nt[kPrTiles] = {tiles_of(it, 0), tiles_of(it, 1)};
+        const int ntiles = max(nt[0], nt[1]);
+        const uint32_t qb = uint32_t(i) % kQBufs;
+        const uint32_t q_smem = sbase + C::kQOff + qb * kPrTiles * C::kTile;
+        auto issue_s = [&](int t, uint32_t c) {
+          const uint32_t q = q_smem + t * C::kTile;
+          const uint32_t k = sbase + C::kKOff + (c % kKStages) * C::kTile;
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-          if (nt[t] > 0) issue_s(t, 0);
-        X::commit(bars + 8 * C::kKEmpty);
-      }
-      for (int j = 0; ok && j < ntiles; ++j) {
-        ok = v_ready(j) && (j + 1 >= ntiles || k_ready(j + 1));
+          for (int x = 0; x < D / 16; ++x) {
+            const uint32_t off = (x >> 2) * C::kHalf + (x & 3) * 32;
+            umma_bf16(tmem + t * C::kTileCols, smem_desc_sw128(q + off, 16, 1024),
+                      smem_desc_sw128(k + off, 16, 1024), kIdescS, x > 0);
+          }
+          umma_commit(bars + 8 * (C::kSFull + t));
+        };
+        // keys [64 half, 64 half + 64) of a tile
+        auto issue_pv = [&](int t, uint32_t c, int half, bool first) {
+          const uint32_t v = sbase + C::kVOff + (c % kVStages) * C::kTile;
+          const uint32_t at = tmem + t * C::kTileCols;
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          if (!ok || j >= nt[t]) continue;
-          ok = ready(C::kPFull + t, j & 1);
-          if (!ok) continue;
-          issue_pv(t, j);
-          if (t == kTiles - 1) X::commit(bars + 8 * (C::kVEmpty + j % kVStages));
-          if (j + 1 < nt[t]) issue_s(t, j + 1);
-        }
+          for (int y = 0; y < 4; ++y) {
+            const int x = half * 4 + y;
+            umma_bf16_ts(at + 128, at + 8 * x, smem_desc_sw128(v + x * 2048, C::kHalf, 1024),
+                         kIdescPV, !first || x > 0);
+          }
+        };
+        ok = ready(C::kQFull + qb, (uint32_t(i) / kQBufs) & 1) &&
+             ready(C::kKFull + kc % kKStages, (kc / kKStages) & 1);
         if (!ok) break;
-        // the last row tile has none of this tile: its slot is free all the same
-        if (j >= nt[kTiles - 1]) X::commit(bars + 8 * (C::kVEmpty + j % kVStages));
-        if (j + 1 < ntiles) X::commit(bars + 8 * (C::kKEmpty + (j + 1) % kKStages));
+#pragma unroll
+        for (int t = 0; t < kPrTiles; ++t)
+          if (nt[t] > 0) issue_s(t, kc);
+        umma_commit(bars + 8 * (C::kKEmpty + kc % kKStages));
+        if (ntiles == 1) umma_commit(bars + 8 * (C::kQEmpty + qb));
+        ++kc;
+        for (int j = 0; ok && j < ntiles; ++j, ++vc) {
+          const bool more = j + 1 < ntiles;
+          ok = ready(C::kVReady + vc % kVStages, (vc / kVStages) & 1) &&
+               (!more || ready(C::kKFull + kc % kKStages, (kc / kKStages) & 1));
+#pragma unroll
+          for (int t = 0; t < kPrTiles; ++t) {
+            if (!ok || j >= nt[t]) continue;
+            if (j == 0) {  // O of the item before is read
+              ok = oc[t] == 0 || ready(C::kOFree + t, (oc[t] - 1) & 1);
+              ++oc[t];
+            }
+            ok = ok && ready(C::kPFull + 2 * t, pc[t] & 1);
+            if (!ok) continue;
+            issue_pv(t, vc, 0, j == 0);
+            ok = ready(C::kPFull + 2 * t + 1, pc[t] & 1);
+            if (!ok) continue;
+            ++pc[t];
+            issue_pv(t, vc, 1, false);
+            if (j + 1 == nt[t]) umma_commit(bars + 8 * (C::kODone + t));
+            if (t == kPrTiles - 1) umma_commit(bars + 8 * (C::kVEmpty + vc % kVStages));
+            if (j + 1 < nt[t]) issue_s(t, kc);
+          }
+          if (!ok) break;
+          // the second row tile has none of this tile: its slot is free all the same
+          if (j >= nt[kPrTiles - 1]) umma_commit(bars + 8 * (C::kVEmpty + vc % kVStages));
+          if (more) {
+            umma_commit(bars + 8 * (C::kKEmpty + kc % kKStages));
+            if (j + 2 == ntiles) umma_commit(bars + 8 * (C::kQEmpty + qb));
+            ++kc;
+          }
+        }
       }
       if (!ok) pr_abort(abort_flag);
       // every MMA is done before tensor memory is given back
-      X::commit(bars + 8 * C::kDrain);
-      X::wait_anyway(bars + 8 * C::kDrain, 0);
+      umma_commit(bars + 8 * C::kDrain);
+      (void)mbar_wait_bounded(bars + 8 * C::kDrain, 0);
     }
     __syncwarp();
   } else {
     // ================= softmax and output: warpgroup wg owns Q tile wg =================
     const int wg = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
-    const int tok = t0 + wg * TPS + int(rank) * TPT + r / G;
-    const bool valid = tok < sq.n;
-    // rows past the end see what the last row does, and are not stored
-    const int limit = p.causal ? sq.keys - sq.n + min(tok, sq.n - 1) : sq.keys - 1;
     const uint32_t at = tmem + wg * C::kTileCols + (uint32_t((warp & 3) * 32) << 16);
-    const uint32_t s_full = bars + 8 * (C::kSFull + wg), o_done = bars + 8 * (C::kODone + wg);
-    const uint32_t p_full = lead + 8 * (C::kPFull + wg);
-    const int tiles = nt[wg];
-    const uint64_t sc2 = f2_pack(p.scale_log2, p.scale_log2);
-    float m = -INFINITY, lsum = 0.f;
+    const uint32_t p_full = bars + 8 * (C::kPFull + 2 * wg);
+    const bool neg = p.scale_log2 < 0.f;
+    const float scale = fabsf(p.scale_log2);
+    const uint64_t sc2 = f2_pack(scale, scale);
+    uint32_t sc = 0, oc = 0;  // S tiles, items
     bool ok = true;
-    for (int j = 0; j < tiles; ++j) {
-      ok = __all_sync(0xffffffffu, X::wait(s_full, j & 1, abort_flag));
-      if (!ok) break;
-      tc_fence_after();
-      const int key0 = j * kPrKeys;
-      if (j == 0) {  // key 0 is visible to every row
-        float va[32];
-        tmem_ld32(at, va);
+    for (int i = 0; ok; ++i) {
+      PromptItem it;
+      ok = __all_sync(0xffffffffu, take(i, it));
+      if (!ok || it.seq < 0) break;
+      const int tok = it.t0 + wg * TPT + r / G;
+      const bool valid = tok < it.n;
+      // rows past the end see what the last row does, and are not stored
+      const int limit = p.causal ? it.keys - it.n + min(tok, it.n - 1) : it.keys - 1;
+      const int tiles = tiles_of(it, wg);
+      float m = -INFINITY, lsum = 0.f;
+      for (int j = 0; j < tiles; ++j, ++sc) {
+        ok = all_wait(C::kSFull + wg, sc & 1);
+        if (!ok) break;
+        tc_fence_after();
+        float s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(at + 32 * c, s[c]);
         tmem_wait_ld();
+        if (neg) {
+#pragma unroll
+          for (int x = 0; x < 128; ++x) s[x >> 5][x & 31] = -s[x >> 5][x & 31];
+        }
+        const int last = limit - j * kPrKeys;  // keys up to here are visible
+        if (last < kPrKeys - 1) {
+#pragma unroll
+          for (int x = 0; x < 128; ++x)
+            s[x >> 5][x & 31] = x <= last ? s[x >> 5][x & 31] : -INFINITY;
+        }
         float ex[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (i <= limit) ex[i & 3] = fmaxf(ex[i & 3], va[i] * p.scale_log2);
-        m = ceilf(fmaxf(fmaxf(ex[0], ex[1]), fmaxf(ex[2], ex[3])));
-      }
-#pragma unroll 1
-      for (int g = 0; g < 2; ++g) {  // 64 keys at a time
-        float va[32], vb[32];
-        tmem_ld32(at + 64 * g, va);
-        tmem_ld32(at + 64 * g + 32, vb);
-        tmem_wait_ld();
-        const int last = limit - key0 - 64 * g;  // keys of the group up to here are visible
-        for (int attempt = 0;; ++attempt) {
-          uint32_t pk[32];
-          const uint64_t nm2 = f2_pack(-m, -m);
-          uint64_t ls2[2] = {0ull, 0ull};
-          if (last >= 63) {
+        for (int x = 0; x < 128; x += 8)
 #pragma unroll
-            for (int u = 0; u < 32; ++u) {
-              const int kk = 2 * u;
-              float x0, x1;
-              f2_unpack(f2_fma(f2_pack(kk < 32 ? va[kk] : vb[kk - 32], kk < 32 ? va[kk + 1] : vb[kk - 31]),
-                               sc2, nm2), x0, x1);
-              const float e0 = ex2(x0), e1 = ex2(x1);
-              ls2[u & 1] = f2_add(ls2[u & 1], f2_pack(e0, e1));
-              pk[u] = pack_bf16x2(e0, e1);
-            }
-          } else {
-#pragma unroll
-            for (int u = 0; u < 32; ++u) {
-              const int kk = 2 * u;
-              float x0, x1;
-              f2_unpack(f2_fma(f2_pack(kk < 32 ? va[kk] : vb[kk - 32], kk < 32 ? va[kk + 1] : vb[kk - 31]),
-                               sc2, nm2), x0, x1);
-              const float e0 = kk <= last ? ex2(x0) : 0.f, e1 = kk + 1 <= last ? ex2(x1) : 0.f;
-              ls2[u & 1] = f2_add(ls2[u & 1], f2_pack(e0, e1));
-              pk[u] = pack_bf16x2(e0, e1);
-            }
-          }
-          float a0, a1, b0, b1;
-          f2_unpack(ls2[0], a0, a1);
-          f2_unpack(ls2[1], b0, b1);
-          const float sum = (a0 + a1) + (b0 + b1);
-          // no weight is above the sum; NaN and infinity fail the test
-          if (attempt > 0 || __all_sync(0xffffffffu, sum <= kPrMaxSum)) {
-            lsum += sum;
-            tmem_st32u(at + 64 * g, pk);
-            break;
-          }
-          // raise the maximum to this group's
-          float ex[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (i <= last) ex[i & 3] = fmaxf(ex[i & 3], va[i] * p.scale_log2);
-            if (i + 32 <= last) ex[i & 3] = fmaxf(ex[i & 3], vb[i] * p.scale_log2);
-          }
-          const float m_new =
-              fmaxf(m, ceilf(fmaxf(fmaxf(ex[0], ex[1]), fmaxf(ex[2], ex[3]))));
+          for (int y = 0; y < 4; ++y)
+            ex[y] = max3f(ex[y], s[x >> 5][(x & 31) + 2 * y], s[x >> 5][(x & 31) + 2 * y + 1]);
+        const float mx = max3f(fmaxf(ex[0], ex[1]), ex[2], ex[3]) * scale;
+        const bool raise = mx > m + kPrRescale;
+        if (j == 0) {
+          m = mx;
+        } else if (__any_sync(0xffffffffu, raise)) {
+          // S of this tile is there only once the product before it is done
+          const float m_new = raise ? mx : m;
           const float alpha = m_new == m ? 1.f : ex2(m - m_new);
-          if (j > 0) {  // after the product of the tile before
-            ok = __all_sync(0xffffffffu, X::wait(o_done, (j - 1) & 1, abort_flag));
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t al2 = f2_pack(alpha, alpha);
+          const uint64_t al2 = f2_pack(alpha, alpha);
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              float o[16];
-              tmem_ld16(at + 128 + c * 16, o);
-              tmem_wait_ld();
+          for (int c = 0; c < D / 16; ++c) {
+            float o[16];
+            tmem_ld16(at + 128 + c * 16, o);
+            tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; i += 2)
-                f2_unpack(f2_mul(f2_pack(o[i], o[i + 1]), al2), o[i], o[i + 1]);
-              tmem_st16(at + 128 + c * 16, o);
-            }
-          }
-          if (g == 1) {  // the first group's P, by an exact power of two
-            tmem_wait_st();
-#pragma unroll 1
-            for (int c = 0; c < 2; ++c) {
-              float ph[16];
-              tmem_ld16(at + 16 * c, ph);
-              tmem_wait_ld();
-#pragma unroll
-              for (int u = 0; u < 16; ++u) {
-                const uint32_t w = __float_as_uint(ph[u]);
-                ph[u] = __uint_as_float(
-                    pack_bf16x2(bf16_lo_to_f32(w) * alpha, bf16_hi_to_f32(w) * alpha));
-              }
-              tmem_st16(at + 16 * c, ph);
-            }
+            for (int x = 0; x < 16; x += 2)
+              f2_unpack(f2_mul(f2_pack(o[x], o[x + 1]), al2), o[x], o[x + 1]);
+            tmem_st16(at + 128 + c * 16, o);
           }
           lsum *= alpha;
           m = m_new;
         }
-        if (!ok) break;
+        const float shift = m == -INFINITY ? 0.f : -m;  // no score above -inf yet: weights of 0
+        const uint64_t nm2 = f2_pack(shift, shift);
+        uint64_t ls2[2] = {0ull, 0ull};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // P of 64 keys, 32 columns
+          uint32_t pk[32];
+#pragma unroll
+          for (int u = 0; u < 32; ++u) {
+            const int x = 64 * h + 2 * u;
+            float x0, x1;
+            f2_unpack(f2_fma(f2_pack(s[x >> 5][x & 31], s[x >> 5][(x & 31) + 1]), sc2, nm2), x0, x1);
+            const float e0 = ex2(x0), e1 = ex2(x1);
+            ls2[u & 1] = f2_add(ls2[u & 1], f2_pack(e0, e1));
+            pk[u] = pack_bf16x2(e0, e1);
+          }
+          tmem_st32u(at + 32 * h, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + 8 * h);
+        }
+        float a0, a1, b0, b1;
+        f2_unpack(ls2[0], a0, a1);
+        f2_unpack(ls2[1], b0, b1);
+        lsum += (a0 + a1) + (b0 + b1);
       }
       if (!ok) break;
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) X::arrive(p_full);
-    }
-    if (ok && tiles > 0) {
-      ok = __all_sync(0xffffffffu, X::wait(o_done, (tiles - 1) & 1, abort_flag));
-      if (ok) {
+      if (tiles > 0) {
+        ok = all_wait(C::kODone + wg, oc & 1);
+        if (!ok) break;
+        ++oc;
         tc_fence_after();
         const float inv = 1.f / lsum;
-        const size_t row = size_t(sq.qs + tok) * p.q_heads + size_t(kvh) * G + r % G;
+        const size_t row = size_t(it.qs + tok) * p.q_heads + size_t(it.kvh) * G + r % G;
         __nv_bfloat16* out = p.out + row * D;
-        const bool odd = *nonfinite != 0;
+        const bool odd = *const_cast<volatile int*>(&slots[i % kPrSlots].odd) != 0;
+        const int cut = cut_of(it);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           float o[32];
           tmem_ld32(at + 128 + c * 32, o);
           tmem_wait_ld();
+          if (c == D / 32 - 1) {  // the next item's product may overwrite O
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars + 8 * (C::kOFree + wg));
+          }
           if (odd && valid) {
             // what was taken out of the cut tiles: an infinity or NaN of a
             // visible key makes the element that
             const __nv_bfloat16* v =
-                p.v + (row0 + (long long)cut * kPrKeys) * p.v_stride + kvh * D + c * 32;
+                p.v + (it.row0 + (long long)cut * kPrKeys) * p.v_stride + it.kvh * D + c * 32;
             for (int key = cut * kPrKeys; key <= limit; ++key, v += p.v_stride) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float x = __bfloat162float(v[i]);
-                if (!isfinite(x)) o[i] += x;
+              for (int x = 0; x < 32; ++x) {
+                const float y = __bfloat162float(v[x]);
+                if (!isfinite(y)) o[x] += y;
               }
             }
           }
           if (valid) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 16)
+            for (int x = 0; x < 32; x += 16)
               asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                               out + c * 32 + i),
-                           "r"(pack_bf16x2(o[i] * inv, o[i + 1] * inv)),
-                           "r"(pack_bf16x2(o[i + 2] * inv, o[i + 3] * inv)),
-                           "r"(pack_bf16x2(o[i + 4] * inv, o[i + 5] * inv)),
-                           "r"(pack_bf16x2(o[i + 6] * inv, o[i + 7] * inv)),
-                           "r"(pack_bf16x2(o[i + 8] * inv, o[i + 9] * inv)),
-                           "r"(pack_bf16x2(o[i + 10] * inv, o[i + 11] * inv)),
-                           "r"(pack_bf16x2(o[i + 12] * inv, o[i + 13] * inv)),
-                           "r"(pack_bf16x2(o[i + 14] * inv, o[i + 15] * inv))
+                               out + c * 32 + x),
+                           "r"(pack_bf16x2(o[x] * inv, o[x + 1] * inv)),
+                           "r"(pack_bf16x2(o[x + 2] * inv, o[x + 3] * inv)),
+                           "r"(pack_bf16x2(o[x + 4] * inv, o[x + 5] * inv)),
+                           "r"(pack_bf16x2(o[x + 6] * inv, o[x + 7] * inv)),
+                           "r"(pack_bf16x2(o[x + 8] * inv, o[x + 9] * inv)),
+                           "r"(pack_bf16x2(o[x + 10] * inv, o[x + 11] * inv)),
+                           "r"(pack_bf16x2(o[x + 12] * inv, o[x + 13] * inv)),
+                           "r"(pack_bf16x2(o[x + 14] * inv, o[x + 15] * inv))
                            : "memory");
           }
         }
       }
+      __syncwarp();
+      if (lane == 0) give_back(i);
     }
     if (!ok && lane == 0) pr_abort(abort_flag);
   }
 
   tc_fence_before();
-  if constexpr (PAIR) cluster_sync_all();
-  else __syncthreads();
-  if (warp == C::kMmaWarp) X::dealloc(tmem, C::kTmemCols);
+  __syncthreads();
+  if (warp == kPrMmaWarp) tmem_dealloc(tmem, C::kTmemCols);
 }
 
 namespace {
 
-template <int D, int G, bool PAIR>
-cudaError_t launch_prompt_t(const PromptArgs& a, const CUtensorMap* tq, const CUtensorMap* tk,
-                            const CUtensorMap* tv, cudaStream_t stream) {
-  using C = PromptCfg<D, PAIR>;
+template <int D, int G>
+cudaError_t launch_prompt_t(const PromptArgs& a, int num_sms, const CUtensorMap* tq,
+                            const CUtensorMap* tk, const CUtensorMap* tv, cudaStream_t stream) {
+  using C = PromptCfg<D>;
   static std::atomic<int> attr_done[kAttrMaxDevices];
-  cudaError_t e = set_smem_limit_once(prompt_attention_kernel<D, G, PAIR>, C::kSmemBytes, attr_done);
+  const cudaError_t e =
+      set_smem_limit_once(prompt_attention_kernel<D, G>, C::kSmemBytes, attr_done);
   if (e != cudaSuccess) return e;
-  const int tpc = kPrRows / G * C::kCtas * C::kTiles;
-  const long long grid = (a.total_q / tpc + (long long)a.num_seqs) * a.kv_heads * C::kCtas;
-  if (grid > INT_MAX) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(grid));
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = C::kCtas;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = PAIR ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, prompt_attention_kernel<D, G, PAIR>, *tq, *tk, *tv, a);
-  return e == cudaSuccess ? cudaGetLastError() : e;
+  const int tpc = kPrRows / G * kPrTiles;
+  const long long items = (a.total_q / tpc + (long long)a.num_seqs) * a.kv_heads;  // at most
+  return launch_after_previous(prompt_attention_kernel<D, G>,
+                               dim3(unsigned(std::min<long long>(items, num_sms))),
+                               dim3(kPrThreads), C::kSmemBytes, stream, *tq, *tk, *tv, a);
 }
 
 }  // namespace
 
-int prompt_key_rows(int d_head) {
-  return d_head == 128 ? PromptCfg<128, true>::kKRows : PromptCfg<64, false>::kKRows;
-}
-int prompt_value_rows() { return kPrKeys; }
 int prompt_tile_rows() { return kPrRows; }
+int prompt_tile_keys() { return kPrKeys; }
 
-cudaError_t launch_prompt_attention(const PromptArgs& a, int d_head, const CUtensorMap* tq,
-                                    const CUtensorMap* tk, const CUtensorMap* tv,
-                                    cudaStream_t stream) {
+cudaError_t launch_prompt_attention(const PromptArgs& a, int d_head, int num_sms,
+                                    const CUtensorMap* tq, const CUtensorMap* tk,
+                                    const CUtensorMap* tv, cudaStream_t stream) {
   const int group = a.q_heads / a.kv_heads;
-#define PKV_PROMPT_CASE(GG)                                                        \
-  if (group == GG)                                                                 \
-    return d_head == 128 ? launch_prompt_t<128, GG, true>(a, tq, tk, tv, stream)   \
-                         : launch_prompt_t<64, GG, false>(a, tq, tk, tv, stream)
+#define PKV_PROMPT_CASE(GG)                                                         \
+  if (group == GG)                                                                  \
+    return d_head == 128 ? launch_prompt_t<128, GG>(a, num_sms, tq, tk, tv, stream) \
+                         : launch_prompt_t<64, GG>(a, num_sms, tq, tk, tv, stream)
   PKV_PROMPT_CASE(1);
   PKV_PROMPT_CASE(2);
   PKV_PROMPT_CASE(4);
