@@ -97,6 +97,17 @@ __device__ __forceinline__ void pr_abort(volatile int* abort_flag) {
   atomicOr(&g_prompt_error, kErrWaitTimeout);
 }
 
+// The lane of a converged warp that issues its MMAs (always the same one).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
 // A sequence's rows and keys; none where they are out of order.
 struct PromptSeq {
   int qs, n, keys;
@@ -442,31 +453,38 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
     if (!ok && lane == 0) pr_abort(abort_flag);
   } else if (warp == kPrMmaWarp) {
-    // ================= MMA issue (one thread) =================
-    if (lane == 0) {
-      constexpr uint32_t kIdescS = idesc_bf16_f32(kPrRows, kPrKeys, 0, 0);
-      constexpr uint32_t kIdescPV = idesc_bf16_f32(kPrRows, D, 0, 1);
-      auto ready = [&](int bar, uint32_t parity) {
-        if (!pr_wait(bars + 8 * bar, parity, abort_flag)) return false;
-        tc_fence_after();
-        return true;
-      };
-      uint32_t kc = 0, vc = 0;              // tiles consumed
-      uint32_t pc[kPrTiles] = {0, 0};       // P tiles of row tile t
-      uint32_t oc[kPrTiles] = {0, 0};       // items with rows in row tile t
-      bool ok = true;
-      for (int i = 0; ok; ++i) {
-        PromptItem it;
-        ok = take(i, it);
-        if (!ok || it.seq < 0) break;
-        give_back(i);
-        const int nt[kPrTiles] = {tiles_of(it, 0), tiles_of(it, 1)};
-        const int ntiles = max(nt[0], nt[1]);
-        const uint32_t qb = uint32_t(i) % kQBufs;
-        const uint32_t q_smem = sbase + C::kQOff + qb * kPrTiles * C::kTile;
-        auto issue_s = [&](int t, uint32_t c) {
-          const uint32_t q = q_smem + t * C::kTile;
-          const uint32_t k = sbase + C::kKOff + (c % kKStages) * C::kTile;
+    // ================= MMA issue =================
+    // The warp runs as a whole and elects a lane for the MMAs, whose descriptors
+    // are then values of the warp: from a branch on the lane number an MMA takes
+    // longer to issue than to run (1 x 16384 tokens: TBD us against 1784).
+    constexpr uint32_t kIdescS = idesc_bf16_f32(kPrRows, kPrKeys, 0, 0);
+    constexpr uint32_t kIdescPV = idesc_bf16_f32(kPrRows, D, 0, 1);
+    auto ready = [&](int bar, uint32_t parity) {
+      if (!all_wait(bar, parity)) return false;
+      tc_fence_after();
+      return true;
+    };
+    auto commit = [&](int bar) {
+      if (elect_lane()) umma_commit(bars + 8 * bar);
+    };
+    uint32_t kc = 0, vc = 0;         // tiles consumed
+    uint32_t pc[kPrTiles] = {0, 0};  // P tiles of row tile t
+    uint32_t oc[kPrTiles] = {0, 0};  // items with rows in row tile t
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      PromptItem it;
+      ok = __all_sync(0xffffffffu, take(i, it));
+      if (!ok || it.seq < 0) break;
+      if (lane == 0) give_back(i);
+      __syncwarp();
+      const int nt[kPrTiles] = {tiles_of(it, 0), tiles_of(it, 1)};
+      const int ntiles = max(nt[0], nt[1]);
+      const uint32_t qb = uint32_t(i) % kQBufs;
+      const uint32_t q_smem = sbase + C::kQOff + qb * kPrTiles * C::kTile;
+      auto issue_s = [&](int t, uint32_t c) {
+        const uint32_t q = q_smem + t * C::kTile;
+        const uint32_t k = sbase + C::kKOff + (c % kKStages) * C::kTile;
+        if (elect_lane()) {
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) {
             const uint32_t off = (x >> 2) * C::kHalf + (x & 3) * 32;
@@ -474,64 +492,68 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                       smem_desc_sw128(k + off, 16, 1024), kIdescS, x > 0);
           }
           umma_commit(bars + 8 * (C::kSFull + t));
-        };
-        // keys [64 half, 64 half + 64) of a tile
-        auto issue_pv = [&](int t, uint32_t c, int half, bool first) {
-          const uint32_t v = sbase + C::kVOff + (c % kVStages) * C::kTile;
-          const uint32_t at = tmem + t * C::kTileCols;
+        }
+      };
+      // keys [64 half, 64 half + 64) of a tile
+      auto issue_pv = [&](int t, uint32_t c, int half, bool first) {
+        const uint32_t v = sbase + C::kVOff + (c % kVStages) * C::kTile;
+        const uint32_t at = tmem + t * C::kTileCols;
+        if (elect_lane()) {
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const int x = half * 4 + y;
             umma_bf16_ts(at + 128, at + 8 * x, smem_desc_sw128(v + x * 2048, C::kHalf, 1024),
                          kIdescPV, !first || x > 0);
           }
-        };
-        ok = ready(C::kQFull + qb, (uint32_t(i) / kQBufs) & 1) &&
-             ready(C::kKFull + kc % kKStages, (kc / kKStages) & 1);
+        }
+      };
+      ok = ready(C::kQFull + qb, (uint32_t(i) / kQBufs) & 1) &&
+           ready(C::kKFull + kc % kKStages, (kc / kKStages) & 1);
+      if (!ok) break;
+#pragma unroll
+      for (int t = 0; t < kPrTiles; ++t)
+        if (nt[t] > 0) issue_s(t, kc);
+      commit(C::kKEmpty + kc % kKStages);
+      if (ntiles == 1) commit(C::kQEmpty + qb);
+      ++kc;
+#pragma unroll 1
+      for (int j = 0; ok && j < ntiles; ++j, ++vc) {
+        const bool more = j + 1 < ntiles;
+        ok = ready(C::kVReady + vc % kVStages, (vc / kVStages) & 1) &&
+             (!more || ready(C::kKFull + kc % kKStages, (kc / kKStages) & 1));
+#pragma unroll
+        for (int t = 0; t < kPrTiles; ++t) {
+          if (!ok || j >= nt[t]) continue;
+          if (j == 0) {  // O of the item before is read
+            ok = oc[t] == 0 || ready(C::kOFree + t, (oc[t] - 1) & 1);
+            ++oc[t];
+          }
+          ok = ok && ready(C::kPFull + 2 * t, pc[t] & 1);
+          if (!ok) continue;
+          issue_pv(t, vc, 0, j == 0);
+          ok = ready(C::kPFull + 2 * t + 1, pc[t] & 1);
+          if (!ok) continue;
+          ++pc[t];
+          issue_pv(t, vc, 1, false);
+          if (j + 1 == nt[t]) commit(C::kODone + t);
+          if (t == kPrTiles - 1) commit(C::kVEmpty + vc % kVStages);
+          if (j + 1 < nt[t]) issue_s(t, kc);
+        }
         if (!ok) break;
-#pragma unroll
-        for (int t = 0; t < kPrTiles; ++t)
-          if (nt[t] > 0) issue_s(t, kc);
-        umma_commit(bars + 8 * (C::kKEmpty + kc % kKStages));
-        if (ntiles == 1) umma_commit(bars + 8 * (C::kQEmpty + qb));
-        ++kc;
-        for (int j = 0; ok && j < ntiles; ++j, ++vc) {
-          const bool more = j + 1 < ntiles;
-          ok = ready(C::kVReady + vc % kVStages, (vc / kVStages) & 1) &&
-               (!more || ready(C::kKFull + kc % kKStages, (kc / kKStages) & 1));
-#pragma unroll
-          for (int t = 0; t < kPrTiles; ++t) {
-            if (!ok || j >= nt[t]) continue;
-            if (j == 0) {  // O of the item before is read
-              ok = oc[t] == 0 || ready(C::kOFree + t, (oc[t] - 1) & 1);
-              ++oc[t];
-            }
-            ok = ok && ready(C::kPFull + 2 * t, pc[t] & 1);
-            if (!ok) continue;
-            issue_pv(t, vc, 0, j == 0);
-            ok = ready(C::kPFull + 2 * t + 1, pc[t] & 1);
-            if (!ok) continue;
-            ++pc[t];
-            issue_pv(t, vc, 1, false);
-            if (j + 1 == nt[t]) umma_commit(bars + 8 * (C::kODone + t));
-            if (t == kPrTiles - 1) umma_commit(bars + 8 * (C::kVEmpty + vc % kVStages));
-            if (j + 1 < nt[t]) issue_s(t, kc);
-          }
-          if (!ok) break;
-          // the second row tile has none of this tile: its slot is free all the same
-          if (j >= nt[kPrTiles - 1]) umma_commit(bars + 8 * (C::kVEmpty + vc % kVStages));
-          if (more) {
-            umma_commit(bars + 8 * (C::kKEmpty + kc % kKStages));
-            if (j + 2 == ntiles) umma_commit(bars + 8 * (C::kQEmpty + qb));
-            ++kc;
-          }
+        // the second row tile has none of this tile: its slot is free all the same
+        if (j >= nt[kPrTiles - 1]) commit(C::kVEmpty + vc % kVStages);
+        if (more) {
+          commit(C::kKEmpty + kc % kKStages);
+          if (j + 2 == ntiles) commit(C::kQEmpty + qb);
+          ++kc;
         }
       }
-      if (!ok) pr_abort(abort_flag);
-      // every MMA is done before tensor memory is given back
-      umma_commit(bars + 8 * C::kDrain);
-      (void)mbar_wait_bounded(bars + 8 * C::kDrain, 0);
     }
+    if (!ok && lane == 0) pr_abort(abort_flag);
+    __syncwarp();
+    // every MMA is done before tensor memory is given back
+    commit(C::kDrain);
+    (void)mbar_wait_bounded(bars + 8 * C::kDrain, 0);
     __syncwarp();
   } else {
     // ================= softmax and output: warpgroup wg owns Q tile wg =================
