@@ -41,7 +41,11 @@ static __device__ unsigned g_prompt_error = 0;
 constexpr int kPrRows = 128;    // rows of a Q tile
 constexpr int kPrKeys = 128;    // keys of a K / V tile
 constexpr int kPrTiles = 2;     // Q tiles of an item, one softmax warpgroup each
-constexpr int kPrThreads = 352; // 2 softmax warpgroups, copies, MMA issue, V scrub
+constexpr int kPrThreads = 384; // 2 softmax warpgroups; copies, MMA issue, V scrub, one idle
+// The softmax holds a row's 128 scores: its warps take registers from the others
+// (of 384 x 168 that the block is launched with).
+constexpr int kPrRegsSoftmax = 200, kPrRegsOther = 104;
+static_assert(2 * 128 * kPrRegsSoftmax + 128 * kPrRegsOther <= kPrThreads * 168, "registers");
 constexpr int kPrLoadWarp = 8, kPrMmaWarp = 9, kPrScrubWarp = 10;
 constexpr float kPrRescale = 8.f;
 constexpr int kPrRegSeqs = 512;  // sequences whose items one warp holds in registers
@@ -106,6 +110,17 @@ __device__ __forceinline__ bool elect_lane() {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(e));
   return e != 0;
+}
+
+// smem_desc_sw128 (with a stride of 1024 bytes) of a shared address over 16:
+// only the low word depends on it, so an operand costs one addition.
+template <uint32_t kLbo>
+__device__ __forceinline__ uint64_t desc_at(uint32_t addr16) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};"
+      : "=l"(d)
+      : "r"(addr16 | ((kLbo >> 4) << 16)), "r"((1024u >> 4) | (1u << 14) | (2u << 29)));
+  return d;
 }
 
 // A sequence's rows and keys; none where they are out of order.
@@ -307,6 +322,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
   // Tiles are numbered through the launch: tile c of a ring of n is the
   // (c / n)-th in slot c % n.
 
+  if (warp >= kPrLoadWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrRegsOther));
   if (warp == kPrLoadWarp) {
     // ================= copies (one thread) =================
     if (lane == 0) {
@@ -454,6 +471,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     if (!ok && lane == 0) pr_abort(abort_flag);
   } else if (warp == kPrMmaWarp) {
     // ================= MMA issue =================
+    const uint32_t tmem = __shfl_sync(0xffffffffu, uint32_t(misc[0]), 0);
     // The warp runs as a whole and elects a lane for the MMAs, whose descriptors
     // are then values of the warp: from a branch on the lane number an MMA takes
     // longer to issue than to run (1 x 16384 tokens: TBD us against 1784).
@@ -474,10 +492,11 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     for (int i = 0; ok; ++i) {
       PromptItem it;
       ok = __all_sync(0xffffffffu, take(i, it));
-      if (!ok || it.seq < 0) break;
+      if (!ok || __shfl_sync(0xffffffffu, it.seq, 0) < 0) break;
       if (lane == 0) give_back(i);
       __syncwarp();
-      const int nt[kPrTiles] = {tiles_of(it, 0), tiles_of(it, 1)};
+      const int nt[kPrTiles] = {__shfl_sync(0xffffffffu, tiles_of(it, 0), 0),
+                                __shfl_sync(0xffffffffu, tiles_of(it, 1), 0)};
       const int ntiles = max(nt[0], nt[1]);
       const uint32_t qb = uint32_t(i) % kQBufs;
       const uint32_t q_smem = sbase + C::kQOff + qb * kPrTiles * C::kTile;
@@ -487,9 +506,9 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (elect_lane()) {
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) {
-            const uint32_t off = (x >> 2) * C::kHalf + (x & 3) * 32;
-            umma_bf16(tmem + t * C::kTileCols, smem_desc_sw128(q + off, 16, 1024),
-                      smem_desc_sw128(k + off, 16, 1024), kIdescS, x > 0);
+            const uint32_t off = ((x >> 2) * C::kHalf + (x & 3) * 32) >> 4;
+            umma_bf16(tmem + t * C::kTileCols, desc_at<16>((q >> 4) + off),
+                      desc_at<16>((k >> 4) + off), kIdescS, x > 0);
           }
           umma_commit(bars + 8 * (C::kSFull + t));
         }
@@ -502,7 +521,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const int x = half * 4 + y;
-            umma_bf16_ts(at + 128, at + 8 * x, smem_desc_sw128(v + x * 2048, C::kHalf, 1024),
+            umma_bf16_ts(at + 128, at + 8 * x, desc_at<C::kHalf>((v >> 4) + x * 128),
                          kIdescPV, !first || x > 0);
           }
         }
@@ -516,11 +535,15 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       commit(C::kKEmpty + kc % kKStages);
       if (ntiles == 1) commit(C::kQEmpty + qb);
       ++kc;
+      // K and V are waited for while MMAs are queued
+      auto operands = [&](int j) {
+        return ready(C::kVReady + vc % kVStages, (vc / kVStages) & 1) &&
+               (j + 1 >= ntiles || ready(C::kKFull + kc % kKStages, (kc / kKStages) & 1));
+      };
+      ok = operands(0);
 #pragma unroll 1
-      for (int j = 0; ok && j < ntiles; ++j, ++vc) {
+      for (int j = 0; ok && j < ntiles; ++j) {
         const bool more = j + 1 < ntiles;
-        ok = ready(C::kVReady + vc % kVStages, (vc / kVStages) & 1) &&
-             (!more || ready(C::kKFull + kc % kKStages, (kc / kKStages) & 1));
 #pragma unroll
         for (int t = 0; t < kPrTiles; ++t) {
           if (!ok || j >= nt[t]) continue;
@@ -547,6 +570,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           if (j + 2 == ntiles) commit(C::kQEmpty + qb);
           ++kc;
         }
+        ++vc;
+        if (more) ok = operands(j + 1);
       }
     }
     if (!ok && lane == 0) pr_abort(abort_flag);
@@ -555,7 +580,9 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     commit(C::kDrain);
     (void)mbar_wait_bounded(bars + 8 * C::kDrain, 0);
     __syncwarp();
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPrRegsSoftmax));
     // ================= softmax and output: warpgroup wg owns Q tile wg =================
     const int wg = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
