@@ -15,10 +15,17 @@
 //    ahead into the next item, and its first products are issued while the
 //    last one's rows are written out.
 //  * a thread owns a row in the softmax, its 128 scores in registers: no
-//    shuffles, one trip to tensor memory.  P leaves in two halves, and the
-//    second product starts on the first.  O is rescaled only when the maximum
-//    rises by more than 8 (weights up to 2^8); a tile's S is complete only
-//    after the product before it, so O needs no barrier of its own.
+//    shuffles, one trip to tensor memory.  The running maximum is looked for
+//    only where it has to move: a tile keeps it while every row's weights stay
+//    below 2^16 against it, seen from the sum of the first 64 keys' weights and
+//    the maximum of the others'.  P leaves in two halves, and the second product
+//    starts on the first.  A tile's S is complete only after the product before
+//    it, and a row's next P comes only after its O was read, so O needs no
+//    barriers of its own.
+//  * what waits costs: an mbarrier that is complete takes the MMA warp 135 cycles
+//    to see.  So it waits for P alone: the warp that looks after V (below) adds
+//    the arrival of the tile's operands to that barrier, V of a tile comes with
+//    K of the next, an item's Q with its first K.
 //  * P in bf16 is off by 2^-8 of each weight at most, as the bf16 output is of
 //    itself; S, O, the weights' sum and the maximum are float32.
 //  * items are taken longest first over all sequences (worked out of q_start on
@@ -47,7 +54,7 @@ constexpr int kPrThreads = 384; // 2 softmax warpgroups; copies, MMA issue, V sc
 constexpr int kPrRegsSoftmax = 200, kPrRegsOther = 104;
 static_assert(2 * 128 * kPrRegsSoftmax + 128 * kPrRegsOther <= kPrThreads * 168, "registers");
 constexpr int kPrLoadWarp = 8, kPrMmaWarp = 9, kPrScrubWarp = 10;
-constexpr float kPrRescale = 8.f;
+constexpr float kPrMost = 16.f;  // weights up to 2^16 against the running maximum
 constexpr int kPrRegSeqs = 512;  // sequences whose items one warp holds in registers
 constexpr int kPrSlots = 4;      // items known ahead
 
@@ -55,21 +62,19 @@ template <int D>
 struct PromptCfg {
   static constexpr int kHalf = 128 * 128;             // 128 rows x 64 columns
   static constexpr int kTile = (D / 64) * kHalf;      // of Q, K or V
-  static constexpr int kQBufs = D == 128 ? 1 : 2;     // items whose Q is there
-  static constexpr int kKStages = D == 128 ? 3 : 4;
-  static constexpr int kVStages = D == 128 ? 2 : 4;
-  static constexpr int kQOff = 0;
-  static constexpr int kKOff = kQOff + kQBufs * kPrTiles * kTile;
-  static constexpr int kVOff = kKOff + kKStages * kTile;
-  static constexpr int kBarOff = kVOff + kVStages * kTile;
-  // barriers: a tile's P in two halves; O read out; an item's data in its slot
-  static constexpr int kQFull = 0, kQEmpty = kQFull + kQBufs, kKFull = kQEmpty + kQBufs,
-                       kKEmpty = kKFull + kKStages, kVLand = kKEmpty + kKStages,
-                       kVReady = kVLand + kVStages, kVEmpty = kVReady + kVStages,
-                       kSFull = kVEmpty + kVStages, kPFull = kSFull + kPrTiles,
-                       kODone = kPFull + 2 * kPrTiles, kOFree = kODone + kPrTiles,
-                       kItem = kOFree + kPrTiles, kItemFree = kItem + kPrSlots,
-                       kDrain = kItemFree + kPrSlots,
+  // an item's Q and first K (its head), and pairs of a tile's V and the next K
+  static constexpr int kHeads = D == 128 ? 1 : 2;
+  static constexpr int kPairs = D == 128 ? 2 : 4;
+  static constexpr int kHeadTile = (kPrTiles + 1) * kTile, kPairTile = 2 * kTile;
+  static constexpr int kPairOff = kHeads * kHeadTile;
+  static constexpr int kBarOff = kPairOff + kPairs * kPairTile;
+  // barriers: a tile's P in two halves, the first with V and the next K; an
+  // item's data in its slot
+  static constexpr int kHeadFull = 0, kHeadFree = kHeadFull + kHeads,
+                       kPairLand = kHeadFree + kHeads, kPairFree = kPairLand + kPairs,
+                       kSFull = kPairFree + kPairs, kPFull = kSFull + kPrTiles,
+                       kODone = kPFull + 2 * kPrTiles, kItem = kODone + kPrTiles,
+                       kItemFree = kItem + kPrSlots, kDrain = kItemFree + kPrSlots,
                        kNumBars = kDrain + 1;
   static constexpr int kItemOff = kBarOff + kNumBars * 8;
   static constexpr int kMiscOff = kItemOff + kPrSlots * 32;  // tensor memory's base, abort flag
@@ -121,6 +126,21 @@ __device__ __forceinline__ uint64_t desc_at(uint32_t addr16) {
       : "=l"(d)
       : "r"(addr16 | ((kLbo >> 4) << 16)), "r"((1024u >> 4) | (1u << 14) | (2u << 29)));
   return d;
+}
+
+// Two scores' weights: added to `sum`, and packed as bf16.
+__device__ __forceinline__ void weights(float s0, float s1, uint64_t scale2, uint64_t shift2,
+                                        uint64_t& sum, uint32_t& packed) {
+  float x0, x1;
+  f2_unpack(f2_fma(f2_pack(s0, s1), scale2, shift2), x0, x1);
+  const float e0 = ex2(x0), e1 = ex2(x1);
+  sum = f2_add(sum, f2_pack(e0, e1));
+  packed = pack_bf16x2(e0, e1);
+}
+__device__ __forceinline__ float f2_sum(const uint64_t (&v)[2]) {
+  float a, b;
+  f2_unpack(f2_add(v[0], v[1]), a, b);
+  return a + b;
 }
 
 // A sequence's rows and keys; none where they are out of order.
@@ -247,7 +267,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
                         const __grid_constant__ CUtensorMap tmap_k,
                         const __grid_constant__ CUtensorMap tmap_v, const PromptArgs p) {
   using C = PromptCfg<D>;
-  constexpr int kKStages = C::kKStages, kVStages = C::kVStages, kQBufs = C::kQBufs;
+  constexpr int kHeads = C::kHeads, kPairs = C::kPairs;
   constexpr int TPT = kPrRows / G;        // tokens of a Q tile
   constexpr int TPC = TPT * kPrTiles;     // tokens of an item
   griddep_wait();
@@ -268,17 +288,16 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     auto init = [&](int b, int count, int n) {
       for (int i = 0; i < n; ++i) mbar_init(bars + 8 * (b + i), count);
     };
-    init(C::kQFull, 1, kQBufs);
-    init(C::kQEmpty, 1, kQBufs);
-    init(C::kKFull, 1, kKStages);
-    init(C::kKEmpty, 1, kKStages);
-    init(C::kVLand, 1, kVStages);
-    init(C::kVReady, 1, kVStages);
-    init(C::kVEmpty, 1, kVStages);
+    init(C::kHeadFull, 1, kHeads);
+    init(C::kHeadFree, 1, kHeads);
+    init(C::kPairLand, 1, kPairs);
+    init(C::kPairFree, 1, kPairs);
     init(C::kSFull, 1, kPrTiles);
-    init(C::kPFull, 4, 2 * kPrTiles);
+    for (int t = 0; t < kPrTiles; ++t) {
+      init(C::kPFull + 2 * t, 5, 1);      // softmax warps, and the operands
+      init(C::kPFull + 2 * t + 1, 4, 1);
+    }
     init(C::kODone, 1, kPrTiles);
-    init(C::kOFree, 4, kPrTiles);
     init(C::kItem, 1, kPrSlots);
     init(C::kItemFree, 2 + 4 * kPrTiles, kPrSlots);  // copies, MMA, softmax warps
     init(C::kDrain, 1, 1);
@@ -319,16 +338,15 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
   auto all_wait = [&](int bar, uint32_t parity) {
     return __all_sync(0xffffffffu, pr_wait(bars + 8 * bar, parity, abort_flag));
   };
-  // Tiles are numbered through the launch: tile c of a ring of n is the
-  // (c / n)-th in slot c % n.
+  // Heads and pairs are numbered through the launch: number c of a ring of n is
+  // the (c / n)-th in slot c % n.
 
   if (warp >= kPrLoadWarp) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPrRegsOther));
   if (warp == kPrLoadWarp) {
     // ================= copies (one thread) =================
     if (lane == 0) {
-      uint32_t kc = 0, vc = 0;  // tiles issued
-      uint32_t qc = 0;
+      uint32_t hc = 0, pc = 0;  // heads and pairs issued
       bool ok = true;
       for (int i = 0; ok; ++i) {
         PromptItem it;
@@ -336,63 +354,46 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (!ok || it.seq < 0) break;
         give_back(i);
         const int ntiles = max(tiles_of(it, 0), tiles_of(it, 1));
-        auto load_k = [&](int j) {
-          const uint32_t st = kc % kKStages;
-          if (kc >= kKStages && !pr_wait(bars + 8 * (C::kKEmpty + st), (kc / kKStages - 1) & 1, abort_flag))
-            return false;
-          const uint32_t bar = bars + 8 * (C::kKFull + st);
-          mbar_arrive_expect_tx(bar, C::kTile);
+        auto rows = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int head, int row) {
 #pragma unroll
           for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(sbase + C::kKOff + st * C::kTile + h * C::kHalf, &tmap_k, bar, h * 64, it.kvh,
-                        it.row0 + j * kPrKeys);
-          ++kc;
-          return true;
+            tma_load_3d(dst + h * C::kHalf, map, bar, h * 64, head, row);
         };
-        auto load_v = [&](int j) {
-          const uint32_t st = vc % kVStages;
-          if (vc >= kVStages && !pr_wait(bars + 8 * (C::kVEmpty + st), (vc / kVStages - 1) & 1, abort_flag))
-            return false;
-          const uint32_t bar = bars + 8 * (C::kVLand + st);
-          mbar_arrive_expect_tx(bar, C::kTile);
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(sbase + C::kVOff + st * C::kTile + h * C::kHalf, &tmap_v, bar, h * 64, it.kvh,
-                        it.row0 + j * kPrKeys);
-          ++vc;
-          return true;
-        };
-        const uint32_t qb = qc % kQBufs;
-        ok = qc < kQBufs || pr_wait(bars + 8 * (C::kQEmpty + qb), (qc / kQBufs - 1) & 1, abort_flag);
+        const uint32_t hb = hc % kHeads;
+        ok = hc < kHeads || pr_wait(bars + 8 * (C::kHeadFree + hb), (hc / kHeads - 1) & 1, abort_flag);
         if (!ok) break;
-        mbar_arrive_expect_tx(bars + 8 * (C::kQFull + qb), kPrTiles * C::kTile);
+        const uint32_t hfull = bars + 8 * (C::kHeadFull + hb), head = sbase + hb * C::kHeadTile;
+        mbar_arrive_expect_tx(hfull, C::kHeadTile);
 #pragma unroll
         for (int t = 0; t < kPrTiles; ++t)
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tma_load_3d(sbase + C::kQOff + (qb * kPrTiles + t) * C::kTile + h * C::kHalf, &tmap_q,
-                        bars + 8 * (C::kQFull + qb), h * 64, it.kvh * G, it.qs + it.t0 + t * TPT);
-        ++qc;
-        ok = load_k(0);
-        for (int j = 0; ok && j < ntiles; ++j) {
-          if (j + 1 < ntiles) ok = load_k(j + 1);
-          ok = ok && load_v(j);
+          rows(head + t * C::kTile, &tmap_q, hfull, it.kvh * G, it.qs + it.t0 + t * TPT);
+        rows(head + kPrTiles * C::kTile, &tmap_k, hfull, it.kvh, it.row0);
+        ++hc;
+        for (int j = 0; j < ntiles; ++j) {
+          const uint32_t st = pc % kPairs;
+          ok = pc < kPairs || pr_wait(bars + 8 * (C::kPairFree + st), (pc / kPairs - 1) & 1, abort_flag);
+          if (!ok) break;
+          const bool more = j + 1 < ntiles;
+          const uint32_t bar = bars + 8 * (C::kPairLand + st);
+          const uint32_t pair = sbase + C::kPairOff + st * C::kPairTile;
+          mbar_arrive_expect_tx(bar, more ? C::kPairTile : C::kTile);
+          rows(pair, &tmap_v, bar, it.kvh, it.row0 + j * kPrKeys);
+          if (more) rows(pair + C::kTile, &tmap_k, bar, it.kvh, it.row0 + (j + 1) * kPrKeys);
+          ++pc;
         }
       }
       if (!ok) pr_abort(abort_flag);
       if (*abort_flag) {  // the copies in flight land before the CTA ends
-        for (uint32_t c = qc > kQBufs ? qc - kQBufs : 0; c < qc; ++c)
-          (void)mbar_wait_bounded(bars + 8 * (C::kQFull + c % kQBufs), (c / kQBufs) & 1);
-        for (uint32_t c = kc > kKStages ? kc - kKStages : 0; c < kc; ++c)
-          (void)mbar_wait_bounded(bars + 8 * (C::kKFull + c % kKStages), (c / kKStages) & 1);
-        for (uint32_t c = vc > kVStages ? vc - kVStages : 0; c < vc; ++c)
-          (void)mbar_wait_bounded(bars + 8 * (C::kVLand + c % kVStages), (c / kVStages) & 1);
+        for (uint32_t c = hc > kHeads ? hc - kHeads : 0; c < hc; ++c)
+          (void)mbar_wait_bounded(bars + 8 * (C::kHeadFull + c % kHeads), (c / kHeads) & 1);
+        for (uint32_t c = pc > kPairs ? pc - kPairs : 0; c < pc; ++c)
+          (void)mbar_wait_bounded(bars + 8 * (C::kPairLand + c % kPairs), (c / kPairs) & 1);
       }
     }
     __syncwarp();
   } else if (warp == kPrScrubWarp) {
-    // ===== the items, and V tiles: those that the mask cuts lose the rows past the
-    // sequence's end, NaN and infinities =====
+    // ===== the items, and every tile's operands: V of those that the mask cuts loses
+    // the rows past the sequence's end, NaN and infinities =====
     PromptTable table;
     table.load(p, TPC);
     // Item k of this CTA: rounds of one per CTA, every other one from the far end
@@ -421,20 +422,21 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
       return it;
     };
-    uint32_t vc = 0;
+    uint32_t pc = 0, tc[kPrTiles] = {0, 0};  // pairs; P tiles of row tile t
     PromptItem next = publish(0);
     bool ok = next.seq != -2;
     for (int i = 0; ok && next.seq >= 0; ++i) {
       const PromptItem it = next;
       next = publish(i + 1);
       ok = next.seq != -2;
-      const int ntiles = max(tiles_of(it, 0), tiles_of(it, 1)), cut = cut_of(it);
-      for (int j = 0; ok && j < ntiles; ++j, ++vc) {
-        const uint32_t st = vc % kVStages;
-        ok = all_wait(C::kVLand + st, (vc / kVStages) & 1);
+      const int nt[kPrTiles] = {tiles_of(it, 0), tiles_of(it, 1)};
+      const int ntiles = max(nt[0], nt[1]), cut = cut_of(it);
+      for (int j = 0; ok && j < ntiles; ++j, ++pc) {
+        const uint32_t st = pc % kPairs;
+        ok = all_wait(C::kPairLand + st, (pc / kPairs) & 1);
         if (!ok) break;
         if (j >= cut) {
-          const uint32_t v = sbase + C::kVOff + st * C::kTile;
+          const uint32_t v = sbase + C::kPairOff + st * C::kPairTile;
           const int live = it.keys - j * kPrKeys;  // rows of this tile that are the sequence's
           bool found = false;
 #pragma unroll 4
@@ -465,7 +467,14 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             *const_cast<volatile int*>(&slots[i % kPrSlots].odd) = 1;
           __syncwarp();
         }
-        if (lane == 0) mbar_arrive(bars + 8 * (C::kVReady + st));
+        // one arrival in each phase of the tiles' P: not before the last one's end
+#pragma unroll
+        for (int t = 0; t < kPrTiles; ++t) {
+          if (j >= nt[t]) continue;
+          ok = ok && (tc[t] == 0 || all_wait(C::kPFull + 2 * t, (tc[t] - 1) & 1));
+          if (ok && lane == 0) mbar_arrive(bars + 8 * (C::kPFull + 2 * t));
+          ++tc[t];
+        }
       }
     }
     if (!ok && lane == 0) pr_abort(abort_flag);
@@ -485,9 +494,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     auto commit = [&](int bar) {
       if (elect_lane()) umma_commit(bars + 8 * bar);
     };
-    uint32_t kc = 0, vc = 0;         // tiles consumed
-    uint32_t pc[kPrTiles] = {0, 0};  // P tiles of row tile t
-    uint32_t oc[kPrTiles] = {0, 0};  // items with rows in row tile t
+    uint32_t pc = 0;                 // pairs consumed
+    uint32_t tc[kPrTiles] = {0, 0};  // P tiles of row tile t
     bool ok = true;
     for (int i = 0; ok; ++i) {
       PromptItem it;
@@ -498,11 +506,10 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const int nt[kPrTiles] = {__shfl_sync(0xffffffffu, tiles_of(it, 0), 0),
                                 __shfl_sync(0xffffffffu, tiles_of(it, 1), 0)};
       const int ntiles = max(nt[0], nt[1]);
-      const uint32_t qb = uint32_t(i) % kQBufs;
-      const uint32_t q_smem = sbase + C::kQOff + qb * kPrTiles * C::kTile;
-      auto issue_s = [&](int t, uint32_t c) {
-        const uint32_t q = q_smem + t * C::kTile;
-        const uint32_t k = sbase + C::kKOff + (c % kKStages) * C::kTile;
+      const uint32_t hb = uint32_t(i) % kHeads;
+      const uint32_t head = sbase + hb * C::kHeadTile;
+      auto issue_s = [&](int t, uint32_t k) {
+        const uint32_t q = head + t * C::kTile;
         if (elect_lane()) {
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) {
@@ -514,64 +521,42 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
       };
       // keys [64 half, 64 half + 64) of a tile
-      auto issue_pv = [&](int t, uint32_t c, int half, bool first) {
-        const uint32_t v = sbase + C::kVOff + (c % kVStages) * C::kTile;
+      auto issue_pv = [&](int t, uint32_t v, int half, bool first) {
         const uint32_t at = tmem + t * C::kTileCols;
         if (elect_lane()) {
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
             const int x = half * 4 + y;
-            umma_bf16_ts(at + 128, at + 8 * x, desc_at<C::kHalf>((v >> 4) + x * 128),
-                         kIdescPV, !first || x > 0);
+            umma_bf16_ts(at + 128, at + 8 * x, desc_at<C::kHalf>((v >> 4) + x * 128), kIdescPV,
+                         !first || x > 0);
           }
         }
       };
-      ok = ready(C::kQFull + qb, (uint32_t(i) / kQBufs) & 1) &&
-           ready(C::kKFull + kc % kKStages, (kc / kKStages) & 1);
+      ok = ready(C::kHeadFull + hb, (uint32_t(i) / kHeads) & 1);
       if (!ok) break;
 #pragma unroll
       for (int t = 0; t < kPrTiles; ++t)
-        if (nt[t] > 0) issue_s(t, kc);
-      commit(C::kKEmpty + kc % kKStages);
-      if (ntiles == 1) commit(C::kQEmpty + qb);
-      ++kc;
-      // K and V are waited for while MMAs are queued
-      auto operands = [&](int j) {
-        return ready(C::kVReady + vc % kVStages, (vc / kVStages) & 1) &&
-               (j + 1 >= ntiles || ready(C::kKFull + kc % kKStages, (kc / kKStages) & 1));
-      };
-      ok = operands(0);
+        if (nt[t] > 0) issue_s(t, head + kPrTiles * C::kTile);
+      if (ntiles == 1) commit(C::kHeadFree + hb);
 #pragma unroll 1
-      for (int j = 0; ok && j < ntiles; ++j) {
-        const bool more = j + 1 < ntiles;
+      for (int j = 0; ok && j < ntiles; ++j, ++pc) {
+        const uint32_t v = sbase + C::kPairOff + (pc % kPairs) * C::kPairTile;
 #pragma unroll
         for (int t = 0; t < kPrTiles; ++t) {
           if (!ok || j >= nt[t]) continue;
-          if (j == 0) {  // O of the item before is read
-            ok = oc[t] == 0 || ready(C::kOFree + t, (oc[t] - 1) & 1);
-            ++oc[t];
-          }
-          ok = ok && ready(C::kPFull + 2 * t, pc[t] & 1);
+          ok = ready(C::kPFull + 2 * t, tc[t] & 1);
           if (!ok) continue;
-          issue_pv(t, vc, 0, j == 0);
-          ok = ready(C::kPFull + 2 * t + 1, pc[t] & 1);
+          issue_pv(t, v, 0, j == 0);
+          ok = ready(C::kPFull + 2 * t + 1, tc[t] & 1);
           if (!ok) continue;
-          ++pc[t];
-          issue_pv(t, vc, 1, false);
-          if (j + 1 == nt[t]) commit(C::kODone + t);
-          if (t == kPrTiles - 1) commit(C::kVEmpty + vc % kVStages);
-          if (j + 1 < nt[t]) issue_s(t, kc);
+          ++tc[t];
+          issue_pv(t, v, 1, false);
+          if (j + 1 < nt[t]) issue_s(t, v + C::kTile);
+          else commit(C::kODone + t);
         }
         if (!ok) break;
-        // the second row tile has none of this tile: its slot is free all the same
-        if (j >= nt[kPrTiles - 1]) commit(C::kVEmpty + vc % kVStages);
-        if (more) {
-          commit(C::kKEmpty + kc % kKStages);
-          if (j + 2 == ntiles) commit(C::kQEmpty + qb);
-          ++kc;
-        }
-        ++vc;
-        if (more) ok = operands(j + 1);
+        commit(C::kPairFree + pc % kPairs);
+        if (j + 2 == ntiles) commit(C::kHeadFree + hb);
       }
     }
     if (!ok && lane == 0) pr_abort(abort_flag);
@@ -621,59 +606,69 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           for (int x = 0; x < 128; ++x)
             s[x >> 5][x & 31] = x <= last ? s[x >> 5][x & 31] : -INFINITY;
         }
-        float ex[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int x = 0; x < 128; x += 8)
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            ex[y] = max3f(ex[y], s[x >> 5][(x & 31) + 2 * y], s[x >> 5][(x & 31) + 2 * y + 1]);
-        const float mx = max3f(fmaxf(ex[0], ex[1]), ex[2], ex[3]) * scale;
-        const bool raise = mx > m + kPrRescale;
-        if (j == 0) {
-          m = mx;
-        } else if (__any_sync(0xffffffffu, raise)) {
-          // S of this tile is there only once the product before it is done
-          const float m_new = raise ? mx : m;
-          const float alpha = m_new == m ? 1.f : ex2(m - m_new);
-          const uint64_t al2 = f2_pack(alpha, alpha);
-#pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
-            float o[16];
-            tmem_ld16(at + 128 + c * 16, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 16; x += 2)
-              f2_unpack(f2_mul(f2_pack(o[x], o[x + 1]), al2), o[x], o[x + 1]);
-            tmem_st16(at + 128 + c * 16, o);
-          }
-          lsum *= alpha;
-          m = m_new;
-        }
-        const float shift = m == -INFINITY ? 0.f : -m;  // no score above -inf yet: weights of 0
-        const uint64_t nm2 = f2_pack(shift, shift);
-        uint64_t ls2[2] = {0ull, 0ull};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {  // P of 64 keys, 32 columns
-          uint32_t pk[32];
+        // P = 2^(x - m): the first 64 keys' with m as it is, and then m is
+        // looked at; where it has to rise (and for the first tile) all again.
+        // A row's m depends on its own scores alone.
+        bool settled = false, stays = false;
+        uint32_t pk[32];
+        uint64_t ls2[2], nm2;
+        if (j > 0) {
+          nm2 = f2_pack(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m);
+          ls2[0] = ls2[1] = 0ull;
+          float ex[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
           for (int u = 0; u < 32; ++u) {
-            const int x = 64 * h + 2 * u;
-            float x0, x1;
-            f2_unpack(f2_fma(f2_pack(s[x >> 5][x & 31], s[x >> 5][(x & 31) + 1]), sc2, nm2), x0, x1);
-            const float e0 = ex2(x0), e1 = ex2(x1);
-            ls2[u & 1] = f2_add(ls2[u & 1], f2_pack(e0, e1));
-            pk[u] = pack_bf16x2(e0, e1);
+            weights(s[u >> 4][(2 * u) & 31], s[u >> 4][((2 * u) & 31) + 1], sc2, nm2, ls2[u & 1], pk[u]);
+            ex[u & 3] = max3f(ex[u & 3], s[2 + (u >> 4)][(2 * u) & 31], s[2 + (u >> 4)][((2 * u) & 31) + 1]);
           }
-          tmem_st32u(at + 32 * h, pk);
+          const float mx = max3f(fmaxf(ex[0], ex[1]), ex[2], ex[3]) * scale;
+          stays = f2_sum(ls2) <= 65536.f && mx <= m + kPrMost;
+          settled = __all_sync(0xffffffffu, stays);
+        }
+        if (!settled) {
+          float ex[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int x = 0; x < 128; x += 2)
+            ex[(x >> 1) & 3] = max3f(ex[(x >> 1) & 3], s[x >> 5][x & 31], s[x >> 5][(x & 31) + 1]);
+          const float mx = max3f(fmaxf(ex[0], ex[1]), ex[2], ex[3]) * scale;
+          const float m_new = stays ? m : fmaxf(m, mx);
+          if (j > 0) {
+            const float alpha = m_new == m ? 1.f : ex2(m - m_new);
+            const uint64_t al2 = f2_pack(alpha, alpha);
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              float o[16];
+              tmem_ld16(at + 128 + c * 16, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 16; x += 2)
+                f2_unpack(f2_mul(f2_pack(o[x], o[x + 1]), al2), o[x], o[x + 1]);
+              tmem_st16(at + 128 + c * 16, o);
+            }
+            lsum *= alpha;
+          }
+          m = m_new;
+          // (no score above -inf yet: weights of 0)
+          nm2 = f2_pack(m == -INFINITY ? 0.f : -m, m == -INFINITY ? 0.f : -m);
+          ls2[0] = ls2[1] = 0ull;
+#pragma unroll
+          for (int u = 0; u < 32; ++u)
+            weights(s[u >> 4][(2 * u) & 31], s[u >> 4][((2 * u) & 31) + 1], sc2, nm2, ls2[u & 1], pk[u]);
+        }
+        auto leave = [&](int half) {  // P of 64 keys, 32 columns
+          tmem_st32u(at + 32 * half, pk);
           tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(p_full + 8 * h);
-        }
-        float a0, a1, b0, b1;
-        f2_unpack(ls2[0], a0, a1);
-        f2_unpack(ls2[1], b0, b1);
-        lsum += (a0 + a1) + (b0 + b1);
+          if (lane == 0) mbar_arrive(p_full + 8 * half);
+        };
+        leave(0);
+#pragma unroll
+        for (int u = 0; u < 32; ++u)
+          weights(s[2 + (u >> 4)][(2 * u) & 31], s[2 + (u >> 4)][((2 * u) & 31) + 1], sc2, nm2,
+                  ls2[u & 1], pk[u]);
+        leave(1);
+        lsum += f2_sum(ls2);
       }
       if (!ok) break;
       if (tiles > 0) {
@@ -691,11 +686,6 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           float o[32];
           tmem_ld32(at + 128 + c * 32, o);
           tmem_wait_ld();
-          if (c == D / 32 - 1) {  // the next item's product may overwrite O
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars + 8 * (C::kOFree + wg));
-          }
           if (odd && valid) {
             // what was taken out of the cut tiles: an infinity or NaN of a
             // visible key makes the element that
@@ -726,6 +716,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           }
         }
       }
+      tc_fence_before();  // the next item's P arrives after O was read
       __syncwarp();
       if (lane == 0) give_back(i);
     }
