@@ -24,7 +24,7 @@
 //    barriers of its own.
 //  * what waits costs: an mbarrier that is complete takes the MMA warp 135 cycles
 //    to see.  So it waits for P alone: the warp that looks after V (below) adds
-//    the arrival of the tile's operands to that barrier, V of a tile comes with
+//    the arrival of the tile's operands to that barrier; V of a tile comes with
 //    K of the next, an item's Q with its first K.
 //  * P in bf16 is off by 2^-8 of each weight at most, as the bf16 output is of
 //    itself; S, O, the weights' sum and the maximum are float32.
@@ -48,12 +48,12 @@ static __device__ unsigned g_prompt_error = 0;
 constexpr int kPrRows = 128;    // rows of a Q tile
 constexpr int kPrKeys = 128;    // keys of a K / V tile
 constexpr int kPrTiles = 2;     // Q tiles of an item, one softmax warpgroup each
-constexpr int kPrThreads = 384; // 2 softmax warpgroups; copies, MMA issue, V scrub, one idle
+constexpr int kPrThreads = 384; // 2 softmax warpgroups; copies, MMA issue, V scrub, items
 // The softmax holds a row's 128 scores: its warps take registers from the others
 // (of 384 x 168 that the block is launched with).
 constexpr int kPrRegsSoftmax = 200, kPrRegsOther = 104;
 static_assert(2 * 128 * kPrRegsSoftmax + 128 * kPrRegsOther <= kPrThreads * 168, "registers");
-constexpr int kPrLoadWarp = 8, kPrMmaWarp = 9, kPrScrubWarp = 10;
+constexpr int kPrLoadWarp = 8, kPrMmaWarp = 9, kPrScrubWarp = 10, kPrItemWarp = 11;
 constexpr float kPrMost = 16.f;  // weights up to 2^16 against the running maximum
 constexpr int kPrRegSeqs = 512;  // sequences whose items one warp holds in registers
 constexpr int kPrSlots = 4;      // items known ahead
@@ -299,7 +299,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
     init(C::kODone, 1, kPrTiles);
     init(C::kItem, 1, kPrSlots);
-    init(C::kItemFree, 2 + 4 * kPrTiles, kPrSlots);  // copies, MMA, softmax warps
+    init(C::kItemFree, 3 + 4 * kPrTiles, kPrSlots);  // copies, MMA, scrub, softmax warps
     init(C::kDrain, 1, 1);
     fence_barrier_init();
     *abort_flag = 0;
@@ -391,20 +391,20 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
     }
     __syncwarp();
-  } else if (warp == kPrScrubWarp) {
-    // ===== the items, and every tile's operands: V of those that the mask cuts loses
-    // the rows past the sequence's end, NaN and infinities =====
+  } else if (warp == kPrItemWarp) {
+    // ===== the CTA's items: rounds of one per CTA, every other one from the far end
+    // (whoever has the longest of one round gets the shortest of the next) =====
     PromptTable table;
     table.load(p, TPC);
-    // Item k of this CTA: rounds of one per CTA, every other one from the far end
-    // (whoever has the longest of one round gets the shortest of the next).
-    auto publish = [&](int k) {
+    bool ok = true, more = true;
+    for (int k = 0; ok && more; ++k) {
       const long long g = gridDim.x;
       const long long work =
           k * g + ((k & 1) ? g - 1 - (long long)blockIdx.x : (long long)blockIdx.x);
       PromptItem it = {-1, 0, 0, 0, 0, 0, 0, 0};
       int seq = -1, tile = 0;
-      if (table.item(p, TPC, work / p.kv_heads, seq, tile)) {
+      more = table.item(p, TPC, work / p.kv_heads, seq, tile);
+      if (more) {
         const PromptSeq q = prompt_seq(p, seq);
         it.seq = seq;
         it.kvh = int(work % p.kv_heads);
@@ -415,20 +415,22 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         it.row0 = p.kv_lens ? seq * p.kv_stride : q.qs;
       }
       const int sl = k % kPrSlots;
-      if (k >= kPrSlots && !all_wait(C::kItemFree + sl, (k / kPrSlots - 1) & 1)) it.seq = -2;
-      if (lane == 0 && it.seq != -2) {
+      ok = k < kPrSlots || all_wait(C::kItemFree + sl, (k / kPrSlots - 1) & 1);
+      if (ok && lane == 0) {
         slots[sl] = it;
         mbar_arrive(bars + 8 * (C::kItem + sl));
       }
-      return it;
-    };
+    }
+    if (!ok && lane == 0) pr_abort(abort_flag);
+  } else if (warp == kPrScrubWarp) {
+    // ===== every tile's operands: V of those that the mask cuts loses the rows past the
+    // sequence's end, NaN and infinities =====
     uint32_t pc = 0, tc[kPrTiles] = {0, 0};  // pairs; P tiles of row tile t
-    PromptItem next = publish(0);
-    bool ok = next.seq != -2;
-    for (int i = 0; ok && next.seq >= 0; ++i) {
-      const PromptItem it = next;
-      next = publish(i + 1);
-      ok = next.seq != -2;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      PromptItem it;
+      ok = __all_sync(0xffffffffu, take(i, it));
+      if (!ok || it.seq < 0) break;
       const int nt[kPrTiles] = {tiles_of(it, 0), tiles_of(it, 1)};
       const int ntiles = max(nt[0], nt[1]), cut = cut_of(it);
       for (int j = 0; ok && j < ntiles; ++j, ++pc) {
@@ -476,6 +478,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           ++tc[t];
         }
       }
+      __syncwarp();
+      if (lane == 0) give_back(i);
     }
     if (!ok && lane == 0) pr_abort(abort_flag);
   } else if (warp == kPrMmaWarp) {
