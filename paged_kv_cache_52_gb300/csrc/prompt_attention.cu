@@ -55,7 +55,7 @@ constexpr int kPrRegsSoftmax = 200, kPrRegsOther = 104;
 static_assert(2 * 128 * kPrRegsSoftmax + 128 * kPrRegsOther <= kPrThreads * 168, "registers");
 constexpr int kPrLoadWarp = 8, kPrMmaWarp = 9, kPrScrubWarp = 10, kPrItemWarp = 11;
 constexpr float kPrMost = 16.f;  // weights up to 2^16 against the running maximum
-constexpr int kPrRegSeqs = 512;  // sequences whose items one warp holds in registers
+constexpr int kPrRegSets = 16;   // times 32 sequences whose items one warp holds in registers
 constexpr int kPrSlots = 4;      // items known ahead
 
 template <int D>
@@ -128,6 +128,11 @@ __device__ __forceinline__ uint64_t desc_at(uint32_t addr16) {
   return d;
 }
 
+// Bits 15 and 31: which halves of a bf16 pair are NaN or infinite (other bits: anything).
+__device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
+  return (w & 0x7f807f80u) + 0x00800080u;
+}
+
 // Two scores' weights: added to `sum`, and packed as bf16.
 __device__ __forceinline__ void weights(float s0, float s1, uint64_t scale2, uint64_t shift2,
                                         uint64_t& sum, uint32_t& packed) {
@@ -177,14 +182,17 @@ __device__ __forceinline__ PromptLevels prompt_levels(const PromptArgs& p, int s
 // Item `rank` of a KV head, by one warp, those with the most keys first: finds
 // the level by bisection over the counts of items at or above one, then the
 // sequence within it.  `own`: lane l's sequences l, l + 32, ... of the first
-// kPrRegSeqs; the others' are worked out again each time.
+// 32 kSets; the others' are worked out again each time.
+// kSets 1 serves up to 32 sequences with little code, which a first item waits
+// for while it is fetched.
+template <int kSets>
 struct PromptTable {
-  PromptLevels own[kPrRegSeqs / 32];
+  PromptLevels own[kSets];
 
   __device__ __forceinline__ void load(const PromptArgs& p, int tpc) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < kPrRegSeqs / 32; ++i) {
+    for (int i = 0; i < kSets; ++i) {
       const int s = i * 32 + lane;
       own[i] = s < p.num_seqs ? prompt_levels(p, s, tpc) : PromptLevels{0, 0};
     }
@@ -194,16 +202,17 @@ struct PromptTable {
   __device__ __forceinline__ void each(const PromptArgs& p, int tpc, F&& f) const {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int i = 0; i < kPrRegSeqs / 32; ++i) {
-      if (i * 32 >= p.num_seqs) return;
+    for (int i = 0; i < kSets; ++i) {
+      if (kSets > 1 && i * 32 >= p.num_seqs) return;
       if (!f(own[i], i * 32)) return;
     }
-    for (int s0 = kPrRegSeqs; s0 < p.num_seqs; s0 += 32) {
-      const int s = s0 + lane;
-      if (!f(s < p.num_seqs ? prompt_levels(p, s, tpc) : PromptLevels{0, 0}, s0)) return;
-    }
+    if constexpr (kSets > 1)
+      for (int s0 = kSets * 32; s0 < p.num_seqs; s0 += 32) {
+        const int s = s0 + lane;
+        if (!f(s < p.num_seqs ? prompt_levels(p, s, tpc) : PromptLevels{0, 0}, s0)) return;
+      }
   }
-  __device__ __forceinline__ bool item(const PromptArgs& p, int tpc, long long rank, int& seq,
+  __device__ __forceinline__ bool item(const PromptArgs& p, int tpc, int rank, int& seq,
                                        int& tile) const {
     constexpr unsigned kFull = 0xffffffffu;
     const int lane = threadIdx.x & 31;
@@ -213,29 +222,29 @@ struct PromptTable {
       return min(v.items, max(0, v.lo + v.items - level));
     };
     auto count = [&](int level) {
-      long long c = 0;
+      int c = 0;  // (the launch's items are within 32 bits)
       each(p, tpc, [&](const PromptLevels& v, int) {
         c += above(v, level);
         return true;
       });
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(kFull, c, o);
-      return c;
+      return __reduce_add_sync(kFull, c);
     };
-    int top = 0;  // no item at this level
+    int top = 0, all = 0;  // no item at level top
     each(p, tpc, [&](const PromptLevels& v, int) {
       if (v.items > 0) top = max(top, v.lo + (causal ? v.items : 1));
+      all += v.items;
       return true;
     });
     top = __reduce_max_sync(kFull, top);
-    if (count(0) <= rank) return false;
+    if (__reduce_add_sync(kFull, all) <= rank) return false;
     int lo = 0, hi = top;  // count(lo) > rank >= count(hi)
+#pragma unroll 1
     while (hi - lo > 1) {
       const int mid = lo + (hi - lo) / 2;
       if (count(mid) > rank) lo = mid;
       else hi = mid;
     }
-    long long rest = rank - count(lo + 1);
+    int rest = rank - count(lo + 1);
     // the rest-th item of level lo, sequences in order
     each(p, tpc, [&](const PromptLevels& v, int s0) {
       const int mine = above(v, lo) - above(v, lo + 1);
@@ -245,16 +254,16 @@ struct PromptTable {
         const int u = __shfl_up_sync(kFull, incl, o);
         if (lane >= o) incl += u;
       }
-      const int all = __shfl_sync(kFull, incl, 31);
-      if (rest >= all) {
-        rest -= all;
+      const int sum = __shfl_sync(kFull, incl, 31);
+      if (rest >= sum) {
+        rest -= sum;
         return true;
       }
       const int who = __ffs(__ballot_sync(kFull, incl > rest)) - 1;
       const int before = __shfl_sync(kFull, incl - mine, who);
       const int at = __shfl_sync(kFull, v.lo, who);
       seq = s0 + who;
-      tile = causal ? lo - at : int(rest) - before;
+      tile = causal ? lo - at : rest - before;
       return false;
     });
     return true;
@@ -394,32 +403,44 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
   } else if (warp == kPrItemWarp) {
     // ===== the CTA's items: rounds of one per CTA, every other one from the far end
     // (whoever has the longest of one round gets the shortest of the next) =====
-    PromptTable table;
-    table.load(p, TPC);
-    bool ok = true, more = true;
-    for (int k = 0; ok && more; ++k) {
-      const long long g = gridDim.x;
-      const long long work =
-          k * g + ((k & 1) ? g - 1 - (long long)blockIdx.x : (long long)blockIdx.x);
-      PromptItem it = {-1, 0, 0, 0, 0, 0, 0, 0};
-      int seq = -1, tile = 0;
-      more = table.item(p, TPC, work / p.kv_heads, seq, tile);
-      if (more) {
-        const PromptSeq q = prompt_seq(p, seq);
-        it.seq = seq;
-        it.kvh = int(work % p.kv_heads);
-        it.qs = q.qs;
-        it.n = q.n;
-        it.keys = q.keys;
-        it.t0 = tile * TPC;
-        it.row0 = p.kv_lens ? seq * p.kv_stride : q.qs;
+    bool ok = true;
+    auto publish = [&](const auto& table) {
+      bool more = true;
+#pragma unroll 1
+      for (int k = 0; ok && more; ++k) {
+        const long long g = gridDim.x;
+        const long long work =
+            k * g + ((k & 1) ? g - 1 - (long long)blockIdx.x : (long long)blockIdx.x);
+        const long long rank = work / p.kv_heads;
+        PromptItem it = {-1, 0, 0, 0, 0, 0, 0, 0};
+        int seq = -1, tile = 0;
+        more = rank <= INT_MAX && table.item(p, TPC, int(rank), seq, tile);
+        if (more) {
+          const PromptSeq q = prompt_seq(p, seq);
+          it.seq = seq;
+          it.kvh = int(work - rank * p.kv_heads);
+          it.qs = q.qs;
+          it.n = q.n;
+          it.keys = q.keys;
+          it.t0 = tile * TPC;
+          it.row0 = p.kv_lens ? seq * p.kv_stride : q.qs;
+        }
+        const int sl = k % kPrSlots;
+        ok = k < kPrSlots || all_wait(C::kItemFree + sl, (k / kPrSlots - 1) & 1);
+        if (ok && lane == 0) {
+          slots[sl] = it;
+          mbar_arrive(bars + 8 * (C::kItem + sl));
+        }
       }
-      const int sl = k % kPrSlots;
-      ok = k < kPrSlots || all_wait(C::kItemFree + sl, (k / kPrSlots - 1) & 1);
-      if (ok && lane == 0) {
-        slots[sl] = it;
-        mbar_arrive(bars + 8 * (C::kItem + sl));
-      }
+    };
+    if (p.num_seqs <= 32) {
+      PromptTable<1> table;
+      table.load(p, TPC);
+      publish(table);
+    } else {
+      PromptTable<kPrRegSets> table;
+      table.load(p, TPC);
+      publish(table);
     }
     if (!ok && lane == 0) pr_abort(abort_flag);
   } else if (warp == kPrScrubWarp) {
@@ -438,30 +459,43 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         ok = all_wait(C::kPairLand + st, (pc / kPairs) & 1);
         if (!ok) break;
         if (j >= cut) {
-          const uint32_t v = sbase + C::kPairOff + st * C::kPairTile;
-          const int live = it.keys - j * kPrKeys;  // rows of this tile that are the sequence's
+          // 16-byte chunks of the rows that are the sequence's; eight loads at a
+          // time (one took 5300 cycles a tile, on short prompts' critical path)
+          const int live = min(it.keys - j * kPrKeys, kPrKeys) * 8;
           bool found = false;
-#pragma unroll 4
-          for (int x = lane; x < C::kTile / 16; x += 32) {
-            const int row = (x >> 3) % kPrKeys;
-            uint32_t w[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(v + x * 16)
-                         : "memory");
-            if (row >= live) {
-              st_shared_zero16(v + x * 16);
-              continue;
-            }
-            uint32_t odd[4];
+#pragma unroll 1
+          for (int h = 0; h < D / 64; ++h) {
+            const uint32_t v = sbase + C::kPairOff + st * C::kPairTile + h * C::kHalf;
+            for (int x = live + lane; x < kPrKeys * 8; x += 32) st_shared_zero16(v + x * 16);
+#pragma unroll 1
+            for (int x0 = lane; x0 < live; x0 += 256) {
+              uint32_t w[8][4], odd = 0;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) odd[c] = __vcmpgeu2(w[c] & 0x7fff7fffu, 0x7f807f80u);
-            if (odd[0] | odd[1] | odd[2] | odd[3]) {
-              found = true;
-              asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(v + x * 16),
-                           "r"(w[0] & ~odd[0]), "r"(w[1] & ~odd[1]), "r"(w[2] & ~odd[2]),
-                           "r"(w[3] & ~odd[3])
-                           : "memory");
+              for (int u = 0; u < 8; ++u) {
+                const int x = min(x0 + 32 * u, live - 1);
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[u][0]), "=r"(w[u][1]), "=r"(w[u][2]), "=r"(w[u][3])
+                             : "r"(v + x * 16)
+                             : "memory");
+              }
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) odd |= nonfinite2(w[u][c]);
+              if (odd & 0x80008000u) {
+                found = true;
+                for (int u = 0; u < 8; ++u) {
+                  const int x = min(x0 + 32 * u, live - 1);
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) {
+                    uint32_t y;
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(y) : "r"(v + x * 16 + c * 4) : "memory");
+                    const uint32_t bad = (nonfinite2(y) & 0x80008000u) >> 15;
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(v + x * 16 + c * 4), "r"(y & ~(bad * 0xffffu))
+                                 : "memory");
+                  }
+                }
+              }
             }
           }
           fence_proxy_async_smem();
