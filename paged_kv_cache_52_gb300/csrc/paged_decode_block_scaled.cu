@@ -38,6 +38,17 @@
 
 namespace pkv {
 
+// The lane of a converged warp that issues its copies (always the same one).
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t e;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e != 0;
+}
+
 struct BsDecodeParams {
   DecodeParams d;  // scale_log2 without the K scale; out_scale is not used
   const float* k_scales;
@@ -271,13 +282,17 @@ __device__ __forceinline__ void bs_pages(BsAcc<D, G>& A, const uint32_t (&kbase)
   }
 }
 
-// One page's two boxes into a ring stage.
+// One page's two boxes into a ring stage, by the warp as a whole: the copies'
+// operands are then values of the warp.  Issued from a branch on the lane number
+// they take TBD cycles a page, now TBD (24 x 2500 tokens, heads of 64: 10.0 us, TBD).
 template <int D>
 __device__ __forceinline__ void bs_issue(uint32_t dst, uint32_t bar, const CUtensorMap& tk,
                                          const CUtensorMap& tv, int head, int id) {
-  mbar_arrive_expect_tx(bar, BsPage<D>::kStageBytes);
-  tma_load_4d(dst, &tk, bar, 0, head, 0, id);
-  tma_load_4d(dst + BsPage<D>::kTileBytes, &tv, bar, 0, head, 0, id);
+  if (elect_lane()) {
+    mbar_arrive_expect_tx(bar, BsPage<D>::kStageBytes);
+    tma_load_4d(dst, &tk, bar, 0, head, 0, id);
+    tma_load_4d(dst + BsPage<D>::kTileBytes, &tv, bar, 0, head, 0, id);
+  }
 }
 
 // ------------------------------------------------------------ cluster split
@@ -313,7 +328,8 @@ decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = cluster.num_blocks(), rank = cluster.block_rank();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kFull, int(threadIdx.x >> 5), 0);  // a value of the warp
   const int gid = lane >> 2, tig = lane & 3;
   const int pair = blockIdx.x / C;
   const int seq = pair / p.kv_heads, kvh = pair - seq * p.kv_heads;
@@ -345,10 +361,10 @@ decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
     fence_barrier_init();
   }
   __syncwarp();
-  auto issue = [&](int i) {  // warp-wide; lane 0 issues
-    const int pid = __shfl_sync(kFull, id, i);
+  auto issue = [&](int i) {  // warp-wide
     const int st = i % kStages;
-    if (lane == 0) bs_issue<D>(ring + st * T::kStageBytes, bars + st * 8, tmap_k, tmap_v, kvh, pid);
+    bs_issue<D>(ring + st * T::kStageBytes, bars + st * 8, tmap_k, tmap_v, kvh,
+                __shfl_sync(kFull, id, i));
   };
   for (int i = 0; i < cnt && i < kStages; ++i) issue(i);
   int issued = min(cnt, kStages);
@@ -513,7 +529,8 @@ decode_block_scaled_flat_kernel(const __grid_constant__ CUtensorMap tmap_k,
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   int32_t* pre = reinterpret_cast<int32_t*>(smem + L::kPreOff);
   int32_t* scan = reinterpret_cast<int32_t*>(smem + L::kScanOff);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kFull, int(threadIdx.x >> 5), 0);  // a value of the warp
   const int gid = lane >> 2, tig = lane & 3;
   const int S = fp.num_seqs;
   const int Hkv = p.kv_heads;
@@ -623,7 +640,7 @@ decode_block_scaled_flat_kernel(const __grid_constant__ CUtensorMap tmap_k,
   auto issue = [&](int j) {
     const int id = __shfl_sync(kFull, (j >> 5) == wcur ? wc.id : wn.id, j & 31);
     const int st = j % kStages;
-    if (lane == 0) bs_issue<D>(ring + st * T::kStageBytes, bars + st * 8, tmap_k, tmap_v, hw, id);
+    bs_issue<D>(ring + st * T::kStageBytes, bars + st * 8, tmap_k, tmap_v, hw, id);
   };
   for (int j = 0; j < cnt && j < kStages; ++j) issue(j);
   int issued = min(cnt, kStages);
@@ -731,9 +748,11 @@ decode_block_scaled_flat_kernel(const __grid_constant__ CUtensorMap tmap_k,
 // the pages [pre[s], pre[s] + n) lie in the ranges g0 = pre[s] / c .. g1 =
 // (pre[s] + n - 1) / c, range g's piece at slot (s + g) Hkv + h.  An empty
 // sequence gets zeros; a pair within one range is written already.  WPR warps
-// take a row's pieces in turn and meet in shared memory: with few rows every
-// row has a hundred pieces, and one warp would wait for each eight loads in
-// turn (2 x 131072 tokens: 39 us against 3.5), with many rows two or none.
+// take a row's pieces, 16 (4) at a time each, with all their loads in flight at
+// once -- lane i reads piece i's log2-sum-exp -- and join their sums in shared
+// memory: with few rows each has a hundred pieces, and it is round trips that
+// count (2 x 131072 tokens, 114 pieces: 39 us for one warp and eight loads in
+// flight, TBD now); with many rows there are two or none.
 template <int D, int WPR>
 __global__ void __launch_bounds__(256)
 decode_block_scaled_merge_kernel(const DecodeParams p, const DecodeFlatParams fp,
@@ -741,7 +760,9 @@ decode_block_scaled_merge_kernel(const DecodeParams p, const DecodeFlatParams fp
   griddep_wait();
   griddep_launch_dependents();
   constexpr int kCols = D / 32;  // a lane's elements
-  __shared__ float part[WPR > 1 ? 8 : 1][WPR > 1 ? D : 1];
+  constexpr int kBatch = WPR > 1 ? 16 : 4;
+  constexpr unsigned kFull = 0xffffffffu;
+  __shared__ float part[WPR > 1 ? WPR : 1][WPR > 1 ? D + 2 : 1];  // O, then maximum and sum
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int w = warp % WPR;
   const long long row = (long long)blockIdx.x * (8 / WPR) + warp / WPR;
@@ -756,46 +777,74 @@ decode_block_scaled_merge_kernel(const DecodeParams p, const DecodeFlatParams fp
   const int g0 = int(start / c), g1 = n > 0 ? int((start + n - 1) / c) : g0 - 1;
   if (g1 == g0) return;
   auto slot = [&](int g) { return (size_t(seq + g) * p.kv_heads + h) * G + hg; };
-  float big = -INFINITY;
-  for (int g = g0 + lane; g <= g1; g += 32) big = fmaxf(big, __ldg(p.part_lse + slot(g)));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-  float tot = 0.f;
-  for (int g = g0 + lane; g <= g1; g += 32) tot += ex2(__ldg(p.part_lse + slot(g)) - big);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-  float val[kCols];
+  float big = -INFINITY, tot = 0.f, val[kCols];
 #pragma unroll
   for (int i = 0; i < kCols; ++i) val[i] = 0.f;
-#pragma unroll 8
-  for (int g = g0 + w; g <= g1; g += WPR) {
-    const float wgt = ex2(__ldg(p.part_lse + slot(g)) - big);
-    const float* src = p.part_o + slot(g) * D + lane * kCols;
-    if constexpr (kCols == 4) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(src));
-      val[0] += wgt * x.x;
-      val[1] += wgt * x.y;
-      val[2] += wgt * x.z;
-      val[3] += wgt * x.w;
-    } else {
-      const float2 x = __ldg(reinterpret_cast<const float2*>(src));
-      val[0] += wgt * x.x;
-      val[1] += wgt * x.y;
+  for (int b = g0 + w * kBatch; b <= g1; b += WPR * kBatch) {
+    const int cnt = min(kBatch, g1 - b + 1);
+    const float lse = lane < cnt ? __ldg(p.part_lse + slot(b + lane)) : -INFINITY;
+    float x[kBatch][kCols];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float* src = p.part_o + slot(b + min(i, cnt - 1)) * D + lane * kCols;
+      if constexpr (kCols == 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(src));
+        x[i][0] = v.x;
+        x[i][1] = v.y;
+        x[i][2] = v.z;
+        x[i][3] = v.w;
+      } else {
+        const float2 v = __ldg(reinterpret_cast<const float2*>(src));
+        x[i][0] = v.x;
+        x[i][1] = v.y;
+      }
+    }
+    float top = lse;
+#pragma unroll
+    for (int o = kBatch / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+    top = fmaxf(big, __shfl_sync(kFull, top, 0));
+    const float alpha = big == top ? 1.f : ex2(big - top);  // (-inf: 0, or nothing yet)
+    big = top;
+    const float mine = lane < cnt ? ex2(lse - top) : 0.f;
+    float sum = mine;
+#pragma unroll
+    for (int o = kBatch / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+    tot = tot * alpha + __shfl_sync(kFull, sum, 0);
+#pragma unroll
+    for (int k = 0; k < kCols; ++k) val[k] *= alpha;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const float f = __shfl_sync(kFull, mine, i);
+      if (i < cnt)
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) val[k] += f * x[i][k];
     }
   }
-  const float inv = n > 0 ? 1.f / tot : 0.f;
   if constexpr (WPR == 1) {
+    const float inv = n > 0 ? 1.f / tot : 0.f;
 #pragma unroll
     for (int i = 0; i < kCols; ++i) store_out(p, size_t(row) * D + lane * kCols + i, val[i] * inv);
   } else {
 #pragma unroll
     for (int i = 0; i < kCols; ++i) part[w][lane * kCols + i] = val[i];
+    if (lane == 0) {
+      part[w][D] = big;
+      part[w][D + 1] = tot;
+    }
     __syncthreads();
     for (int x = threadIdx.x; x < D; x += 256) {
-      float sum = 0.f;
+      float top = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < WPR; ++k) sum += part[k][x];
-      store_out(p, size_t(row) * D + x, sum * inv);
+      for (int k = 0; k < WPR; ++k) top = fmaxf(top, part[k][D]);
+      float sum = 0.f, all = 0.f;
+#pragma unroll
+      for (int k = 0; k < WPR; ++k) {
+        // a warp without pieces has a sum of 0 and no maximum
+        const float f = part[k][D + 1] == 0.f ? 0.f : ex2(part[k][D] - top);
+        sum += f * part[k][x];
+        all += f * part[k][D + 1];
+      }
+      store_out(p, size_t(row) * D + x, n > 0 ? sum / all : 0.f);
     }
   }
 }
