@@ -248,8 +248,10 @@ cudaError_t launch_copy_block_scales(float* k_scales, float* v_scales, const int
 
 // Pages -> contiguous bf16 rows for the prefill: position t of sequence s to row
 // s * max_blocks * 16 + t of both outputs.  code * scale is a bf16 value for the
-// append's scales; other scales' products are rounded to one.  One CTA takes a
-// page of K and V; a thread 16 codes, which lie in one head, at a time.
+// append's scales; other scales' products are rounded to one.  Bound by HBM (one
+// byte read, two written an element).  A CTA takes a page of K and V, a thread
+// four times 16 codes at once, which lie in one head each; the next page's
+// number is on its way meanwhile.
 __global__ void __launch_bounds__(kBsThreads)
 widen_block_scaled_kernel(const WidenBlockScaledArgs a, int d_head) {
   griddep_wait();
@@ -257,47 +259,75 @@ widen_block_scaled_kernel(const WidenBlockScaledArgs a, int d_head) {
   const int64_t items = int64_t(a.num_seqs) * a.max_blocks_per_seq;
   const int row_vec = a.kv_heads * d_head / 16;  // 16 codes each
   const int page_vec = kBsTokens * row_vec;
-  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+  const int head_vec = d_head / 16;
+  // the page's number and its rows in use; none: 0 rows
+  auto page_of = [&](int64_t item, int& id, int& live) {
+    live = 0;
+    if (item >= items) return;
     const int s = int(item / a.max_blocks_per_seq);
-    const int j = int(item - int64_t(s) * a.max_blocks_per_seq);
-    const int live = __ldg(a.context_lens + s) - j * kBsTokens;  // rows of the page in use
-    if (live <= 0) continue;
-    const int id = __ldg(a.block_tables + item);
-    const bool good = id >= 0 && id < a.num_blocks;
-    if (!good && threadIdx.x == 0) atomicOr(&g_block_scaled_error, kErrBadBlockId);
-    for (int i = threadIdx.x; i < 2 * page_vec; i += kBsThreads) {
-      const bool v = i >= page_vec;
-      const int c = v ? i - page_vec : i;
-      const int row = c / row_vec;
-      if (row >= live) continue;
-      uint4 w = make_uint4(0, 0, 0, 0);
-      float f = 0.f;
-      if (good) {
-        w = __ldg(reinterpret_cast<const uint4*>(v ? a.v_cache : a.k_cache) +
-                  size_t(id) * page_vec + c);
-        f = __ldg((v ? a.v_scales : a.k_scales) + size_t(id) * a.kv_heads +
-                  (c - row * row_vec) * 16 / d_head);
-      }
-      uint4* dst = reinterpret_cast<uint4*>(v ? a.v_out : a.k_out) + (item * page_vec + c) * 2;
-      const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-      uint32_t out[8];
+    live = __ldg(a.context_lens + s) - int(item - int64_t(s) * a.max_blocks_per_seq) * kBsTokens;
+    if (live > 0) id = __ldg(a.block_tables + item);
+  };
+  int id = 0, live;
+  page_of(blockIdx.x, id, live);
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x) {
+    int next_id = 0, next_live;
+    page_of(item + gridDim.x, next_id, next_live);
+    if (live > 0) {
+      const bool good = id >= 0 && id < a.num_blocks;
+      if (!good && threadIdx.x == 0) atomicOr(&g_block_scaled_error, kErrBadBlockId);
+      const int used = min(live, kBsTokens) * row_vec;  // of page_vec
+      constexpr int kBatch = 4;
+#pragma unroll 1
+      for (int i0 = threadIdx.x; i0 < 2 * used; i0 += kBatch * kBsThreads) {
+        uint4 w[kBatch];
+        float f[kBatch];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float x[4];
-        e4m3x4_to_f32(in[k], x);
-        out[2 * k] = pack_bf16x2(x[0] * f, x[1] * f);
-        out[2 * k + 1] = pack_bf16x2(x[2] * f, x[3] * f);
+        for (int u = 0; u < kBatch; ++u) {
+          const int i = i0 + u * kBsThreads;
+          const bool v = i >= used;
+          const int c = v ? i - used : i;
+          w[u] = make_uint4(0, 0, 0, 0);
+          f[u] = 0.f;
+          if (good && i < 2 * used) {
+            w[u] = __ldg(reinterpret_cast<const uint4*>(v ? a.v_cache : a.k_cache) +
+                         size_t(id) * page_vec + c);
+            f[u] = __ldg((v ? a.v_scales : a.k_scales) + size_t(id) * a.kv_heads +
+                         c % row_vec / head_vec);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int i = i0 + u * kBsThreads;
+          if (i >= 2 * used) break;
+          const bool v = i >= used;
+          const int c = v ? i - used : i;
+          const uint32_t in[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+          uint32_t out[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float x[4];
+            e4m3x4_to_f32(in[k], x);
+            out[2 * k] = pack_bf16x2(x[0] * f[u], x[1] * f[u]);
+            out[2 * k + 1] = pack_bf16x2(x[2] * f[u], x[3] * f[u]);
+          }
+          char* dst = static_cast<char*>(v ? a.v_out : a.k_out) + (item * page_vec + c) * 32;
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst),
+                       "r"(out[0]), "r"(out[1]), "r"(out[2]), "r"(out[3]), "r"(out[4]),
+                       "r"(out[5]), "r"(out[6]), "r"(out[7])
+                       : "memory");
+        }
       }
-      dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-      dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
     }
+    id = next_id;
+    live = next_live;
   }
 }
 
 cudaError_t launch_widen_block_scaled(const WidenBlockScaledArgs& a, int d_head, int num_sms,
                                       cudaStream_t stream) {
   const int64_t items = int64_t(a.num_seqs) * a.max_blocks_per_seq;
-  const int grid = int(std::min<int64_t>(items, int64_t(num_sms) * 8));
+  const int grid = int(std::min<int64_t>(items, int64_t(num_sms) * 6));
   return launch_after_previous(widen_block_scaled_kernel, dim3(unsigned(grid)), dim3(kBsThreads),
                                0, stream, a, d_head);
 }
