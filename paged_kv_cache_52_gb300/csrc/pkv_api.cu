@@ -1722,7 +1722,8 @@ int collect_error_words(cudaStream_t stream, bool clear, unsigned* word) {
       pkv::prefill_error_word, pkv::verify_error_word, pkv::probe_error_word,
       pkv::mixed_decode_error_word, pkv::mixed_prefill_error_word, pkv::decode_flat_error_word,
       pkv::rope_error_word, pkv::draft_error_word, pkv::tree_error_word,
-      pkv::block_scaled_error_word, pkv::decode_block_scaled_error_word, pkv::prompt_error_word};
+      pkv::block_scaled_error_word, pkv::decode_block_scaled_error_word, pkv::prompt_error_word,
+      pkv::prompt_shared_error_word};
   constexpr int kWords = int(sizeof(getters) / sizeof(getters[0]));
   static_assert(kWords <= int(sizeof(s.word) / sizeof(s.word[0])), "room for every unit's word");
   for (int i = 0; i < kWords; ++i)
@@ -1775,11 +1776,12 @@ int pkv_get_device_error(unsigned int* word, int clear) {
   const unsigned bs = pkv::read_block_scaled_error(clear != 0);
   const unsigned db = pkv::read_decode_block_scaled_error(clear != 0);
   const unsigned pr = pkv::read_prompt_error(clear != 0);
+  const unsigned ps = pkv::read_prompt_shared_error(clear != 0);
   if (a == ~0u || d == ~0u || f == ~0u || d8 == ~0u || v == ~0u || w == ~0u || m == ~0u ||
       fl == ~0u || r == ~0u || dr == ~0u || t == ~0u ||
-      bs == ~0u || db == ~0u || pr == ~0u)
+      bs == ~0u || db == ~0u || pr == ~0u || ps == ~0u)
     return PKV_ECUDA;
-  *word = a | d | f | d8 | v | w | m | fl | r | dr | t | bs | db | pr;
+  *word = a | d | f | d8 | v | w | m | fl | r | dr | t | bs | db | pr | ps;
   return PKV_OK;
 }
 
@@ -2260,6 +2262,8 @@ int run_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
   a.q_heads = q_heads;
   a.kv_heads = kv_heads;
   a.kv_stride = kv_row_stride;
+  a.max_keys = kv_lens ? kv_row_stride : total_q;
+  a.split = 1;
   a.causal = causal ? 1 : 0;
   // a scale of 0 weighs every visible key alike: so does one too small to tell
   // scores apart, which keeps a hidden key's -inf out of 0 * inf

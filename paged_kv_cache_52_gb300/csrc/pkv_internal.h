@@ -28,6 +28,7 @@ cudaError_t tree_error_word(unsigned** word);
 cudaError_t block_scaled_error_word(unsigned** word);
 cudaError_t decode_block_scaled_error_word(unsigned** word);
 cudaError_t prompt_error_word(unsigned** word);
+cudaError_t prompt_shared_error_word(unsigned** word);
 
 // ---- kv_append.cu
 // reject (optional): a device flag set by launch_slot_duplicates; when it is
@@ -362,13 +363,20 @@ struct PromptArgs {
   int64_t v_stride;  // elements per row
   __nv_bfloat16* out;
   int num_seqs, total_q, q_heads, kv_heads, kv_stride, causal;
+  int max_keys;  // of a sequence, at most
   float scale_log2;
+  int split;     // set by the launch: CTAs of an item
 };
 int prompt_tile_rows();  // query rows (tokens x heads) of a Q box
 int prompt_tile_keys();  // rows of a K or V box
-cudaError_t launch_prompt_attention(const PromptArgs& a, int d_head, int num_sms,
+cudaError_t launch_prompt_attention(PromptArgs a, int d_head, int num_sms,
                                     const CUtensorMap* tmap_q, const CUtensorMap* tmap_k,
                                     const CUtensorMap* tmap_v, cudaStream_t stream);
+// ... whose items a.split CTAs share each (prompt_attention_shared.cu)
+cudaError_t launch_prompt_shared(const PromptArgs& a, int d_head, long long ctas,
+                                 const CUtensorMap* tmap_q, const CUtensorMap* tmap_k,
+                                 const CUtensorMap* tmap_v, cudaStream_t stream);
 unsigned read_prompt_error(bool clear);
+unsigned read_prompt_shared_error(bool clear);
 
 }  // namespace pkv

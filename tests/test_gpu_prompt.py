@@ -247,6 +247,41 @@ def test_prefill_over_a_block_scaled_cache(pk, hq, hkv, d, causal, counts, lens)
     assert pk.get_device_error(clear=True) == 0
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(8, 1, 128), (2, 2, 64), (16, 1, 64)])
+@pytest.mark.parametrize("counts,lens", [([8], [5000]), ([1], [1025]), ([300], [2000]),
+                                         ([20, 1], [700, 3])])
+def test_items_shared_by_several_ctas(pk, hq, hkv, d, counts, lens):
+    """Few rows against many keys, so that CTAs share an item: some of them without a
+    key that a row sees, or without a tile of the second half of the rows."""
+    g = torch.Generator().manual_seed(hq)
+    c = dict(cache=_cached(lens, hkv, d, g), counts=counts, lens=lens, scale=0.03,
+             q=torch.randn(sum(counts), hq, d, generator=g).bfloat16())
+    got = _prefill(pk, c).double().cpu().numpy()
+    tables, (kc, vc), (ks, vs) = c["cache"]
+    kd, vd = (oracle.dequantize_blocks(a.numpy(), b.numpy()) for a, b in ((kc, ks), (vc, vs)))
+    start = _start(counts).tolist()
+    for s, (n, L) in enumerate(zip(counts, lens)):
+        pages = tables[s, :-(-L // BS)].tolist()
+        k, v = (x[pages].reshape(-1, hkv, d)[:L] for x in (kd, vd))
+        q = c["q"][start[s]:start[s + 1]].double().numpy()
+        for i in range(0, n, 37):
+            _check(got[start[s] + i:start[s] + i + 1], q[i:i + 1], k, v, 0.03, L - n + i)
+    assert pk.get_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_nonfinite_values_in_shared_items(pk, d):
+    lens = [1900]
+    qkv = _inputs(lens, 2, 1, d)
+    want = _run(pk, qkv, lens, 2, 1)
+    bad = qkv.clone()
+    bad[1850, 3, 7] = float("inf")
+    got = _run(pk, bad, lens, 2, 1)
+    assert torch.equal(got[:1850], want[:1850])
+    assert (got[1850:, :, 7] == float("inf")).all()
+    assert torch.equal(got[1850:, :, :7], want[1850:, :, :7])
+
+
 def test_prefill_rejects_bad_sequences(pk):
     g = torch.Generator().manual_seed(0)
     lens = [40, 100, 64, 32]
