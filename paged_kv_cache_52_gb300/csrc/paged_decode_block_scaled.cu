@@ -132,10 +132,11 @@ struct BsAcc {
   }
 };
 
+// FULL: every page lies within the sequence, and nothing is masked.
 // NP landed pages: page i at kbase[i], its first token tok0[i], its scales
 // ks[i] (times the softmax scale) and vs[i]; the sequence ends at `len`.
-template <int D, int G, int NP>
-__device__ __forceinline__ void bs_pages(BsAcc<D, G>& A, const uint32_t (&kbase)[NP],
+template <int D, int G, int NP, bool FULL>
+__device__ __forceinline__ void bs_pages_as(BsAcc<D, G>& A, const uint32_t (&kbase)[NP],
                                          const int (&tok0)[NP], const float (&ks)[NP],
                                          const float (&vs)[NP], int len, int lane) {
   using T = BsPage<D>;
@@ -206,8 +207,8 @@ __device__ __forceinline__ void bs_pages(BsAcc<D, G>& A, const uint32_t (&kbase)
 #pragma unroll
       for (int pg = 0; pg < NP; ++pg) {
         const float f = ks[pg] * A.qmul[nh][c];
-        x0[pg] = k0_in[pg] ? (s[pg][nh][c] + s_odd[pg][nh][c]) * f : -INFINITY;
-        x1[pg] = k1_in[pg] ? (s[pg][nh][c + 2] + s_odd[pg][nh][c + 2]) * f : -INFINITY;
+        x0[pg] = FULL || k0_in[pg] ? (s[pg][nh][c] + s_odd[pg][nh][c]) * f : -INFINITY;
+        x1[pg] = FULL || k1_in[pg] ? (s[pg][nh][c + 2] + s_odd[pg][nh][c + 2]) * f : -INFINITY;
         mx = fmaxf(mx, fmaxf(x0[pg], x1[pg]));
       }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
@@ -253,7 +254,7 @@ __device__ __forceinline__ void bs_pages(BsAcc<D, G>& A, const uint32_t (&kbase)
 #pragma unroll
   for (int pg = 0; pg < NP; ++pg) {
     vm0[pg] = vm1[pg] = 0xffffffffu;
-    if (tok0[pg] + kBlockTokens > len) {
+    if (!FULL && tok0[pg] + kBlockTokens > len) {
       const int k0 = tok0[pg] + 2 * tig;
       vm0[pg] = (k0 < len ? 0x0000ffffu : 0u) | (k0 + 1 < len ? 0xffff0000u : 0u);
       vm1[pg] = (k0 + 8 < len ? 0x0000ffffu : 0u) | (k0 + 9 < len ? 0xffff0000u : 0u);
@@ -265,10 +266,12 @@ __device__ __forceinline__ void bs_pages(BsAcc<D, G>& A, const uint32_t (&kbase)
     for (int pg = 0; pg < NP; ++pg) {
       uint32_t r0, r1, r2, r3;
       ldsm_x4_trans(kbase[pg] + T::kTileBytes + T::at(v_tok, 2 * cp + (mi >> 1)), r0, r1, r2, r3);
-      r0 &= vm0[pg];
-      r1 &= vm1[pg];
-      r2 &= vm0[pg];
-      r3 &= vm1[pg];
+      if constexpr (!FULL) {
+        r0 &= vm0[pg];
+        r1 &= vm1[pg];
+        r2 &= vm0[pg];
+        r3 &= vm1[pg];
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t a0, a1, a2, a3;
@@ -280,6 +283,16 @@ __device__ __forceinline__ void bs_pages(BsAcc<D, G>& A, const uint32_t (&kbase)
       }
     }
   }
+}
+
+template <int D, int G, int NP>
+__device__ __forceinline__ void bs_pages(BsAcc<D, G>& A, const uint32_t (&kbase)[NP],
+                                         const int (&tok0)[NP], const float (&ks)[NP],
+                                         const float (&vs)[NP], int len, int lane) {
+  if (NP == 2 && tok0[NP - 1] + kBlockTokens <= len)  // the last one is the furthest
+    bs_pages_as<D, G, NP, true>(A, kbase, tok0, ks, vs, len, lane);
+  else
+    bs_pages_as<D, G, NP, false>(A, kbase, tok0, ks, vs, len, lane);
 }
 
 // One page's two boxes into a ring stage, by the warp as a whole: the copies'
@@ -315,8 +328,6 @@ __global__ void __launch_bounds__(kBsClWarps * 32, 3)
 decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                    const __grid_constant__ CUtensorMap tmap_v,
                                    const BsDecodeParams bp) {
-  griddep_wait();
-  griddep_launch_dependents();
   using T = BsPage<D>;
   using L = BsCl<D, G>;
   constexpr int kStages = T::kStages;
@@ -335,6 +346,18 @@ decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
   const int seq = pair / p.kv_heads, kvh = pair - seq * p.kv_heads;
   const uint32_t ring = smem_u32(smem + warp * T::kRingBytes);
   const uint32_t bars = smem_u32(smem + L::kBarOff) + warp * kStages * 8;
+
+  if (lane == 0) {
+    for (int st = 0; st < kStages; ++st) mbar_init(bars + st * 8, 1);
+    fence_barrier_init();
+  }
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tmap_k);
+    tma_prefetch_desc(&tmap_v);
+  }
+  __syncwarp();
+  griddep_wait();
+  griddep_launch_dependents();
 
   // page i of this warp: the pair's page (i C + rank) W + warp
   const int page0 = rank * kBsClWarps + warp, step = C * kBsClWarps;
@@ -356,11 +379,6 @@ decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
       atomicOr(&g_decode_error, kErrBadBlockId);
     }
   }
-  if (lane == 0) {
-    for (int st = 0; st < kStages; ++st) mbar_init(bars + st * 8, 1);
-    fence_barrier_init();
-  }
-  __syncwarp();
   auto issue = [&](int i) {  // warp-wide
     const int st = i % kStages;
     bs_issue<D>(ring + st * T::kStageBytes, bars + st * 8, tmap_k, tmap_v, kvh,
@@ -517,7 +535,6 @@ __global__ void __launch_bounds__(kBsFlatWarps * 32, 1)
 decode_block_scaled_flat_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                 const __grid_constant__ CUtensorMap tmap_v,
                                 const BsDecodeParams bp, const DecodeFlatParams fp) {
-  griddep_wait();
   using T = BsPage<D>;
   using L = BsFlat<D>;
   constexpr int kStages = T::kStages;
@@ -534,6 +551,18 @@ decode_block_scaled_flat_kernel(const __grid_constant__ CUtensorMap tmap_k,
   const int gid = lane >> 2, tig = lane & 3;
   const int S = fp.num_seqs;
   const int Hkv = p.kv_heads;
+
+  const uint32_t ring = smem_u32(smem + warp * T::kRingBytes);
+  const uint32_t bars = smem_u32(smem + L::kBarOff) + warp * kStages * 8;
+  if (lane == 0) {
+    for (int st = 0; st < kStages; ++st) mbar_init(bars + st * 8, 1);
+    fence_barrier_init();
+  }
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tmap_k);
+    tma_prefetch_desc(&tmap_v);
+  }
+  griddep_wait();
 
   // ---- pages per sequence and their prefix sum, alike in every CTA
   const int per = (S + kThreads - 1) / kThreads;
@@ -556,16 +585,6 @@ decode_block_scaled_flat_kernel(const __grid_constant__ CUtensorMap tmap_k,
     if (lane >= o) incl += v;
   }
   if (lane == 31) scan[warp] = incl;
-  const uint32_t ring = smem_u32(smem + warp * T::kRingBytes);
-  const uint32_t bars = smem_u32(smem + L::kBarOff) + warp * kStages * 8;
-  if (lane == 0) {
-    for (int st = 0; st < kStages; ++st) mbar_init(bars + st * 8, 1);
-    fence_barrier_init();
-  }
-  if (threadIdx.x == 0) {
-    tma_prefetch_desc(&tmap_k);
-    tma_prefetch_desc(&tmap_v);
-  }
   __syncthreads();
   if (warp == 0) {
     int v = lane < kBsFlatWarps ? scan[lane] : 0;
@@ -908,7 +927,7 @@ cudaError_t launch_flat(const BsDecodeParams& bp, const DecodeFlatParams& fp, in
 int cluster_ctas(long long pairs, int max_blocks, int num_sms) {
   const long long slots = 3ll * num_sms;
   int c = 1;
-  while (c < kBsClMaxCtas && pairs * c * 2 <= slots && max_blocks > c * kBsClWarps) c *= 2;
+  while (c < kBsClMaxCtas && pairs * c * 2 <= slots && max_blocks > 2 * c * kBsClWarps) c *= 2;
   if (pairs * c > slots || max_blocks > c * kBsClWarps * kBsClMaxPages) return 0;
   return c;
 }

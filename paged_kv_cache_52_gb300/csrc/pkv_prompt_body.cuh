@@ -319,7 +319,6 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
   constexpr int kHeads = C::kHeads, kPairs = C::kPairs;
   constexpr int TPT = kPrRows / G;        // tokens of a Q tile
   constexpr int TPC = TPT * kPrTiles;     // tokens of an item
-  griddep_wait();
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -330,9 +329,6 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
   volatile int* abort_flag = misc + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (blockIdx.x == 0)
-    for (int s = threadIdx.x; s < p.num_seqs; s += kPrThreads)
-      if (prompt_seq(p, s).bad) atomicOr(&g_prompt_error, kErrBadQueryRange);
   if (warp == kPrLoadWarp && lane == 0) {
     auto init = [&](int b, int count, int n) {
       for (int i = 0; i < n; ++i) mbar_init(bars + 8 * (b + i), count);
@@ -364,6 +360,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = uint32_t(misc[0]);
+  griddep_wait();  // what follows reads what kernels before may have written
+  griddep_launch_dependents();
 
   // Key tiles of row tile t (0: it has no rows), those of them that are this
   // CTA's, and the first key tile that some row does not see whole.
@@ -449,6 +447,9 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
   } else if (warp == kPrItemWarp) {
     // ===== the CTA's (cluster's) items: rounds of one per CTA, every other one from the
     // far end (whoever has the longest of one round gets the shortest of the next) =====
+    if (blockIdx.x == 0)
+      for (int s = lane; s < p.num_seqs; s += 32)
+        if (prompt_seq(p, s).bad) atomicOr(&g_prompt_error, kErrBadQueryRange);
     bool ok = true;
     auto publish = [&](const auto& table) {
       bool more = true;
