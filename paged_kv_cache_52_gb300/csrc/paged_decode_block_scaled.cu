@@ -76,13 +76,14 @@ struct BsAcc {
   static constexpr int MT = D / 16;
   float o[NH][MT][4];
   float m[NH][2], l[NH][2];
-  float qmul[NH][2];  // what the queries were divided by
+  float qmul[NH][2];  // what the queries were divided by, times the softmax scale
   float vref, vinv;   // the largest V scale so far, and 1 / vref
   uint32_t qf[NH][MT][2];
 
   // The queries of rows row0 .. row0 + G - 1, in the order in which the K
   // fragments arrive (see pkv_decode_fp8_body.cuh), and an empty state.
-  __device__ __forceinline__ void start(const __nv_bfloat16* q, size_t row0, int lane) {
+  __device__ __forceinline__ void start(const __nv_bfloat16* q, size_t row0, float scale_log2,
+                                        int lane) {
     const int gid = lane >> 2, tig = lane & 3;
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
@@ -100,9 +101,9 @@ struct BsAcc {
       top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // bf16 exponent of the largest element; 127 + [-6, 14] stays as it is
       const int e = int(max(top & 0xffffu, top >> 16) >> 7);
-      const int shift = e < 121 || e > 141 ? min(max(e, 1), 254) - 127 : 0;
-      const float inv = __uint_as_float(uint32_t(127 - shift) << 23);  // 2^-shift, shift <= 127
-      const float mul = __uint_as_float(uint32_t(127 + shift) << 23);
+      const int shift = e < 121 || e > 141 ? min(max(e, 1), 253) - 127 : 0;
+      const float inv = __uint_as_float(uint32_t(127 - shift) << 23);  // 2^-shift, shift <= 126: normal
+      const float mul = __uint_as_float(uint32_t(127 + shift) << 23) * scale_log2;
 #pragma unroll
       for (int kk = 0; kk < MT; ++kk) {
         qf[nh][kk][0] = pack_f16x2(bf16_lo_to_f32(w[kk].x) * inv, bf16_hi_to_f32(w[kk].x) * inv);
@@ -134,7 +135,7 @@ struct BsAcc {
 
 // FULL: every page lies within the sequence, and nothing is masked.
 // NP landed pages: page i at kbase[i], its first token tok0[i], its scales
-// ks[i] (times the softmax scale) and vs[i]; the sequence ends at `len`.
+// ks[i] and vs[i]; the sequence ends at `len`.
 template <int D, int G, int NP, bool FULL>
 __device__ __forceinline__ void bs_pages_as(BsAcc<D, G>& A, const uint32_t (&kbase)[NP],
                                          const int (&tok0)[NP], const float (&ks)[NP],
@@ -373,7 +374,7 @@ decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
   float ks = 0.f, vs = 0.f;
   if (lane < cnt) {
     if (id >= 0 && id < p.num_blocks) {
-      ks = __ldg(bp.k_scales + size_t(id) * p.kv_heads + kvh) * p.scale_log2;
+      ks = __ldg(bp.k_scales + size_t(id) * p.kv_heads + kvh);
       vs = __ldg(bp.v_scales + size_t(id) * p.kv_heads + kvh);
     } else {
       atomicOr(&g_decode_error, kErrBadBlockId);
@@ -389,7 +390,7 @@ decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
 
   const size_t row0 = size_t(seq) * p.q_heads + size_t(kvh) * G;
   BsAcc<D, G> acc;
-  acc.start(p.q, row0, lane);
+  acc.start(p.q, row0, p.scale_log2, lane);
   bool failed = false;
   int i = 0;
   while (i < cnt) {
@@ -646,7 +647,7 @@ decode_block_scaled_flat_kernel(const __grid_constant__ CUtensorMap tmap_k,
       w.blk = int(f - pre[lo]);
       w.id = __ldg(p.block_tables + size_t(lo) * p.max_blocks_per_seq + w.blk);
       if (w.id >= 0 && w.id < p.num_blocks) {
-        w.ks = __ldg(bp.k_scales + size_t(w.id) * Hkv + hw) * p.scale_log2;
+        w.ks = __ldg(bp.k_scales + size_t(w.id) * Hkv + hw);
         w.vs = __ldg(bp.v_scales + size_t(w.id) * Hkv + hw);
       } else if (hw == 0) {
         atomicOr(&g_decode_error, kErrBadBlockId);
@@ -711,7 +712,7 @@ decode_block_scaled_flat_kernel(const __grid_constant__ CUtensorMap tmap_k,
       cur_end = pre[seq0 + 1] - pre[seq0];
       const int raw = __ldg(p.context_lens + seq0);
       cur_len = raw < cur_end * kBlockTokens ? raw : cur_end * kBlockTokens;
-      acc.start(p.q, size_t(seq0) * p.q_heads + size_t(hw) * G, lane);
+      acc.start(p.q, size_t(seq0) * p.q_heads + size_t(hw) * G, p.scale_log2, lane);
     }
     bool landed = mbar_wait_bounded(bars + (i % kStages) * 8, (i / kStages) & 1);
     if (two && landed)

@@ -258,6 +258,19 @@ def test_decode_of_queries_outside_the_range_of_f16(pk, lens, q_size):
 
 
 @pytest.mark.parametrize("lens", [[300, 90], [(29 * i) % 200 for i in range(260)]])
+def test_decode_of_queries_at_the_end_of_bf16(pk, lens):
+    """Rows whose largest element is 2^127 or more, against keys of small scales."""
+    c = _decode_case(lens, 8, 2, 128)
+    q = (c["q"].double() * 8e37).clamp(-3.3e38, 3.3e38)
+    q[..., 0] = 2.0 ** 127
+    c["q"] = q.bfloat16()
+    c["ks"] = c["ks"] * 2.0 ** -60
+    c["scale"] = 0.02 / 8e37 * 2.0 ** 60
+    _check_rows(_decode(pk, c).cpu().numpy(), c, range(0, len(lens), 9))
+    assert pk.get_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("lens", [[300, 90], [(29 * i) % 200 for i in range(260)]])
 def test_decode_of_scales_far_apart(pk, lens):
     """V scales over 60 powers of two, in rising and falling order, all small in
     another sequence."""
