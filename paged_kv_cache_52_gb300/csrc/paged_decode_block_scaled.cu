@@ -7,10 +7,12 @@
 // A block's scales are constants of 16 keys, so they join the arithmetic where
 // a whole block is one factor: K's in the factor that scores have anyway, V's
 // in the weights on their way to the second product.  The weights enter that
-// product as f16, at most 1 by construction: they are taken relative to the
-// largest V scale so far, vref, and O is kept in units of vref (rescaled when
-// vref grows, as when m grows), so a small scale costs no precision where a
-// larger one is about.  Queries are f16 after an exact power of two that
+// product as f16, so O has a running maximum of its own,
+//   mv = max (x + floor(log2 v_scale)),
+// and is kept in units of 2^mv: a weight v_scale 2^(x - mv) is below 2 for every
+// row, and a block counts by what it gives to the row, whatever scales blocks
+// have to which the row pays no heed.  What is below 2^-25 of a row's largest
+// is lost, the rest within 2^-11 of itself or 2^-25 of the largest.  Queries are f16 after an exact power of two that
 // brings a row outside [2^-6, 2^15) into it.
 //
 // Bound by HBM: every code is read once, 4 flops for each byte and query head.
@@ -76,8 +78,8 @@ struct BsAcc {
   static constexpr int MT = D / 16;
   float o[NH][MT][4];
   float m[NH][2], l[NH][2];
+  float mv[NH][2];    // O is in units of 2^mv
   float qmul[NH][2];  // what the queries were divided by, times the softmax scale
-  float vref, vinv;   // the largest V scale so far, and 1 / vref
   uint32_t qf[NH][MT][2];
 
   // The queries of rows row0 .. row0 + G - 1, in the order in which the K
@@ -112,13 +114,16 @@ struct BsAcc {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         qmul[nh][c] = __shfl_sync(0xffffffffu, mul, (2 * tig + c) * 4);
-        m[nh][c] = -INFINITY;
+        m[nh][c] = mv[nh][c] = -INFINITY;
         l[nh][c] = 0.f;
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) o[nh][mt][0] = o[nh][mt][1] = o[nh][mt][2] = o[nh][mt][3] = 0.f;
     }
-    vref = vinv = 0.f;
+  }
+  // O's unit over the weights' (an empty state's O is 0)
+  __device__ __forceinline__ float unit(int nh, int c) const {
+    return m[nh][c] == -INFINITY ? 0.f : ex2(mv[nh][c] - m[nh][c]);
   }
 
   __device__ __forceinline__ void sum_l() {
@@ -175,19 +180,9 @@ __device__ __forceinline__ void bs_pages_as(BsAcc<D, G>& A, const uint32_t (&kba
     }
   }
 
-  // V's reference
-  float vtop = A.vref;
+  float lv[NP];  // exponents of V's scales
 #pragma unroll
-  for (int pg = 0; pg < NP; ++pg) vtop = fmaxf(vtop, vs[pg]);
-  bool all_same = vtop == A.vref;  // uniform over the warp
-  const float vold = A.vref;
-  if (!all_same) {
-    A.vref = vtop;
-    A.vinv = 1.f / vtop;
-  }
-  float vrel[NP];
-#pragma unroll
-  for (int pg = 0; pg < NP; ++pg) vrel[pg] = vs[pg] * A.vinv;
+  for (int pg = 0; pg < NP; ++pg) lv[pg] = float(int(__float_as_uint(vs[pg]) >> 23) - 127);
 
   // online softmax per head column, in the log2 domain
   bool k0_in[NP], k1_in[NP];
@@ -197,28 +192,42 @@ __device__ __forceinline__ void bs_pages_as(BsAcc<D, G>& A, const uint32_t (&kba
     k1_in[pg] = tok0[pg] + gid + 8 < len;
   }
   uint32_t pb[NP][NH][2];
-  float alpha[NH][2];
+  float beta[NH][2];
+  bool all_same = true;
 #pragma unroll
   for (int nh = 0; nh < NH; ++nh) {
-    float pr[NP][4];
+    float pr[NP][4], w[NP][2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
       float x0[NP], x1[NP];
-      float mx = -INFINITY;
+      float mx = -INFINITY, mxv = -INFINITY;
 #pragma unroll
       for (int pg = 0; pg < NP; ++pg) {
         const float f = ks[pg] * A.qmul[nh][c];
         x0[pg] = FULL || k0_in[pg] ? (s[pg][nh][c] + s_odd[pg][nh][c]) * f : -INFINITY;
         x1[pg] = FULL || k1_in[pg] ? (s[pg][nh][c + 2] + s_odd[pg][nh][c + 2]) * f : -INFINITY;
-        mx = fmaxf(mx, fmaxf(x0[pg], x1[pg]));
+        const float top = fmaxf(x0[pg], x1[pg]);
+        mx = fmaxf(mx, top);
+        mxv = fmaxf(mxv, top + lv[pg]);
       }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-      const float mn = fmaxf(A.m[nh][c], mx);
-      alpha[nh][c] = ex2(A.m[nh][c] - mn);
-      all_same = all_same && A.m[nh][c] == mn;
+#pragma unroll
+      for (int o = 4; o <= 16; o <<= 1) {
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        mxv = fmaxf(mxv, __shfl_xor_sync(0xffffffffu, mxv, o));
+      }
+      const float mn = fmaxf(A.m[nh][c], mx), mvn = fmaxf(A.mv[nh][c], mxv);
+      const float alpha = ex2(A.m[nh][c] - mn);
+      beta[nh][c] = ex2(A.mv[nh][c] - mvn);
+      all_same = all_same && A.mv[nh][c] == mvn;
       A.m[nh][c] = mn;
+      A.mv[nh][c] = mvn;
+      // (bounded: where a weight is 0 its block's factor may be past float32)
+      const float unit = ex2(mn - mvn);
+#pragma unroll
+      for (int pg = 0; pg < NP; ++pg) {
+        const float f = vs[pg] * unit;
+        w[pg][c] = f > 0x1p126f ? 0x1p126f : f;
+      }
       float add = 0.f;
 #pragma unroll
       for (int pg = 0; pg < NP; ++pg) {
@@ -226,20 +235,19 @@ __device__ __forceinline__ void bs_pages_as(BsAcc<D, G>& A, const uint32_t (&kba
         pr[pg][c + 2] = ex2(x1[pg] - mn);
         add += pr[pg][c] + pr[pg][c + 2];
       }
-      A.l[nh][c] = A.l[nh][c] * alpha[nh][c] + add;
+      A.l[nh][c] = A.l[nh][c] * alpha + add;
     }
     // P^T as the B operand: (key, two heads) per lane -> (two keys, head)
 #pragma unroll
     for (int pg = 0; pg < NP; ++pg) {
-      pb[pg][nh][0] = movmatrix_trans(pack_f16x2(pr[pg][0] * vrel[pg], pr[pg][1] * vrel[pg]));
-      pb[pg][nh][1] = movmatrix_trans(pack_f16x2(pr[pg][2] * vrel[pg], pr[pg][3] * vrel[pg]));
+      pb[pg][nh][0] = movmatrix_trans(pack_f16x2(pr[pg][0] * w[pg][0], pr[pg][1] * w[pg][1]));
+      pb[pg][nh][1] = movmatrix_trans(pack_f16x2(pr[pg][2] * w[pg][0], pr[pg][3] * w[pg][1]));
     }
   }
   if (!__all_sync(0xffffffffu, all_same)) {
-    const float vmul = vold * A.vinv;  // 1 when vref stayed, 0 at first
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
-      const float a0 = alpha[nh][0] * vmul, a1 = alpha[nh][1] * vmul;
+      const float a0 = beta[nh][0], a1 = beta[nh][1];  // 0 at first
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         A.o[nh][mt][0] *= a0;
@@ -436,7 +444,7 @@ decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
   }
   acc.sum_l();
 
-  // the warp's result over its own ring: O in V's units, m, l
+  // the warp's result over its own ring: O in the weights' unit, m, l
   float* mo = reinterpret_cast<float*>(smem + warp * T::kRingBytes);
 #pragma unroll
   for (int nh = 0; nh < BsAcc<D, G>::NH; ++nh)
@@ -444,10 +452,11 @@ decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
     for (int c = 0; c < 2; ++c) {
       const int head = 8 * nh + 2 * tig + c;
       if (head >= G) continue;
+      const float unit = acc.unit(nh, c);
 #pragma unroll
       for (int mt = 0; mt < BsAcc<D, G>::MT; ++mt)
         *reinterpret_cast<float2*>(mo + head * D + 16 * mt + 2 * gid) =
-            make_float2(acc.o[nh][mt][c] * acc.vref, acc.o[nh][mt][c + 2] * acc.vref);
+            make_float2(acc.o[nh][mt][c] * unit, acc.o[nh][mt][c + 2] * unit);
       if (gid == 0) {
         mo[G * D + head] = acc.m[nh][c];
         mo[G * D + G + head] = acc.l[nh][c];
@@ -681,7 +690,7 @@ decode_block_scaled_flat_kernel(const __grid_constant__ CUtensorMap tmap_k,
       for (int cc = 0; cc < 2; ++cc) {
         const int head = 8 * nh + 2 * tig + cc;
         if (head >= G) continue;
-        const float inv = acc.vref / acc.l[nh][cc];
+        const float inv = acc.unit(nh, cc) / acc.l[nh][cc];
 #pragma unroll
         for (int mt = 0; mt < BsAcc<D, G>::MT; ++mt) {
           const int dim = 16 * mt + 2 * gid;

@@ -283,6 +283,50 @@ def test_decode_of_scales_far_apart(pk, lens):
     assert pk.get_device_error(clear=True) == 0
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("lens", [[300, 90], [(29 * i) % 200 for i in range(260)]])
+def test_decode_of_large_values_that_weigh_nothing(pk, lens, d):
+    """Every other block has V scales 2^40 times the others' and scores so low that
+    it gives the rows next to nothing: the others' values come out.  A weight times
+    its block's scale is off by half a step of f16 (2^-11), or 2^-25 of the row's
+    largest such product where that is more."""
+    c = _decode_case(lens, 8, 2, d, spread=0.5)
+    c["q"] = c["q"].abs() + 0.5
+    low = torch.arange(c["kc"].shape[0]) % 2 == 0
+    low[c["tables"][:, 0].long()] = False       # the first block of each is one of the others
+    sign = torch.where(low, 0x80, 0).to(torch.uint8)[:, None, None, None]
+    nan = (c["kc"] & 0x7f) == 0x7f
+    c["kc"] = torch.where(nan, c["kc"], (c["kc"] & 0x7f) | sign)
+    c["ks"] = torch.where(low, 2.0, 2.0 ** -9)[:, None].expand(-1, 2).contiguous()
+    c["vs"] = torch.where(low, 2.0 ** 30, 2.0 ** -10)[:, None].expand(-1, 2).contiguous()
+    got = _decode(pk, c).cpu().numpy()
+    assert pk.get_device_error(clear=True) == 0
+    kd, vd = (oracle.dequantize_blocks(c[x].numpy(), c[y].numpy())
+              for x, y in (("kc", "ks"), ("vc", "vs")))
+    q = c["q"].double().numpy()
+    for s in range(0, len(lens), 9):
+        n = lens[s]
+        if n == 0:
+            continue
+        pages = c["tables"][s, :-(-n // BS)].tolist()
+        k = kd[pages].reshape(-1, *kd.shape[2:])[:n]
+        v = vd[pages].reshape(-1, *vd.shape[2:])[:n]
+        vscale = np.repeat(c["vs"][pages].double().numpy(), BS, axis=0)[:n]
+        for h in range(8):
+            x = (k[:, h // 4] @ q[s, h]) * c["scale"]
+            w = np.exp(x - x.max())
+            l = w.sum()
+            want = w @ v[:, h // 4] / l
+            dots = (np.abs(k[:, h // 4]) @ np.abs(q[s, h]))
+            own = w > 1e-30
+            rel = 2.0 ** -11 + 2 * d * 2.0 ** -24 * dots[own].max() * c["scale"] + 2.0 ** -18
+            tol = rel * (w @ np.abs(v[:, h // 4]) / l)
+            tol = tol + n * 2.0 ** -25 * 448 * (w * vscale[:, h // 4]).max() / l
+            part = w * vscale[:, h // 4]
+            assert part[vscale[:, h // 4] > 1].max(initial=0) < 2.0 ** -10  # the others' largest
+            assert (np.abs(got[s, h] - want) <= tol).all(), (s, h, n)
+
+
 def test_decode_of_context_bounds_and_block_ids(pk):
     c = _decode_case([40, 100, 30], 8, 2, 64, width=7)
     want = _decode(pk, c)
