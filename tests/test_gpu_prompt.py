@@ -117,6 +117,22 @@ def test_many_prompts(pk):
     assert pk.get_device_error(clear=True) == 0
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_more_prompts_than_one_warp_holds(pk, causal):
+    """The items of the first 512 sequences are held, the others' found again."""
+    lens = [(i * i * 11) % 70 for i in range(1100)]
+    lens[700] = 400
+    qkv = _inputs(lens, 4, 2, 64)
+    got = _run(pk, qkv, lens, 4, 2, causal)
+    start = _start(lens).tolist()
+    for s in [0, 1, 31, 32, 33, 511, 512, 513, 700, 701, 1023, 1024, 1099]:
+        alone = _run(pk, qkv[start[s]:start[s + 1]], [lens[s]], 4, 2, causal)
+        assert torch.equal(alone, got[start[s]:start[s + 1]])
+    rows = list(range(0, sum(lens), 501))
+    _check_prompts(got, qkv, lens, 4, 2, causal, rows=rows)
+    assert pk.get_device_error(clear=True) == 0
+
+
 @pytest.mark.parametrize("d", [64, 128])
 def test_maxima_that_rise_late(pk, d):
     """Scores far above the first keys' in every tile: the running maximum moves
