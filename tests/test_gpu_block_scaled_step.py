@@ -245,3 +245,41 @@ def test_prompts_captured_beside_other_work(pk):
                 _check(out[a:b].double().cpu().numpy(), x[0][a:b], x[1][a:b], x[2][a:b], 0.1, 0)
         assert not out[s[3]:].any()
     assert pk.get_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("lens", [[40, 1, 333], [17] * 300])
+def test_pools_past_32_bits(pk, lens):
+    """Blocks at the far end of pools of 4.3 GB: as in small ones, bit for bit."""
+    hq, hkv, d = 16, 8, 128
+    g = torch.Generator().manual_seed(5)
+    need = [-(-n // BS) for n in lens]
+    near = torch.arange(sum(need) + 1, dtype=torch.int32)
+    tables = torch.zeros(len(lens), max(need), dtype=torch.int32)
+    at = 0
+    for s, n in enumerate(need):
+        tables[s, :n] = near[at:at + n]
+        at += n
+    blocks = (1 << 32) // (BS * hkv * d) + 512
+    kv = torch.randn(sum(lens), 2 * hkv, d, generator=g).bfloat16().to(DEV)
+    q = torch.randn(len(lens), hq, d, generator=g).bfloat16().to(DEV)
+    rows = torch.randn(sum(lens), hq, d, generator=g).bfloat16().to(DEV)
+    results = []
+    for count, shift in ((at + 1, 0), (blocks, blocks - at - 1)):
+        pools = [torch.empty(count, BS, hkv, d, dtype=torch.uint8, device=DEV) for _ in "kv"]
+        scales = [torch.empty(count, hkv, device=DEV) for _ in "kv"]
+        t = (tables + shift).to(DEV)
+        for x in pools:
+            x[shift:].zero_()
+        pk.kv_append_fp8_block_scaled(*kv.split([hkv] * 2, 1), _start(lens).to(DEV), t,
+                                      _i32(lens), *pools, *scales)
+        pairs = torch.tensor([[shift, shift + at]], dtype=torch.int32, device=DEV)
+        pk.copy_blocks(*pools, pairs, *scales)
+        results.append([x[shift:].clone() for x in pools + scales] + [
+            pk.paged_decode_attention_fp8_block_scaled(q, *pools, *scales, t, _i32(lens), 0.1),
+            pk.paged_prefill_attention_fp8_block_scaled(rows, _start(lens).to(DEV), *pools, *scales,
+                                                        t, _i32(lens), True, 0.1)])
+        assert pk.get_device_error(clear=True) == 0
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    for x in results[1][:4]:
+        assert torch.equal(x[at], x[0])
