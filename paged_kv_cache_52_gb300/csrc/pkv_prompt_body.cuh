@@ -348,6 +348,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     init(C::kDrain, 1, 1);
     fence_barrier_init();
     *abort_flag = 0;
+    slots[0].seq = -1;  // a shared item's end reads it even if a wait ran out
     tma_prefetch_desc(&tmap_q);
     tma_prefetch_desc(&tmap_k);
     tma_prefetch_desc(&tmap_v);
