@@ -947,10 +947,10 @@ PKV_API int pkv_copy_block_scales(float* k_scales, float* v_scales, pkv_cache_de
 /*
  * pkv_paged_decode_attention_fp8_block_scaled -- pkv_paged_decode_attention
  * over a block-scaled cache: the attention of the dequantized cache.  Any
- * positive finite scales are taken.  Queries enter the product as f16, a row
- * outside [2^-6, 2^15) brought into it by an exact power of two; the weights
- * enter P V as f16, so an output element is off by at most 2^-10 * max|V| of
- * the dequantized V.
+ * positive finite scales are taken, and scores are float32.  Queries enter the
+ * product as f16, a row outside [2^-6, 2^15) brought into it by an exact power
+ * of two; a weight times its block's V scale enters P V as f16, off by 2^-11 of
+ * itself, or by 2^-25 of the row's largest such product where that is more.
  *   max_context_len : host-side bound on context_lens.  Tokens of a longer
  *               sequence are not attended and PKV_DEVERR_BAD_CONTEXT is set.
  *   workspace : >= pkv_decode_fp8_block_scaled_workspace_bytes(...) device
