@@ -234,6 +234,17 @@ def test_decode_of_batches_over_one_wave(pk, hq, hkv, d):
     assert pk.get_device_error(clear=True) == 0
 
 
+@pytest.mark.parametrize("hq,hkv,d", [(32, 32, 128), (128, 8, 64)])
+@pytest.mark.parametrize("lens", [[1] * 227, [(5 * i) % 34 for i in range(254)]])
+def test_decode_of_many_short_contexts(pk, hq, hkv, d, lens):
+    """Fewer pages than warps: ranges of two pages, over several sequences and within one."""
+    c = _decode_case(lens, hq, hkv, d, seed=hq)
+    got = _decode(pk, c)
+    _check_rows(got.cpu().numpy(), c, range(0, len(lens), 11))
+    assert torch.equal(_decode(pk, c, out_dtype=torch.bfloat16), got.bfloat16())
+    assert pk.get_device_error(clear=True) == 0
+
+
 @pytest.mark.parametrize("hq,hkv,d", [(4, 1, 128), (2, 2, 64)])
 def test_decode_of_long_contexts(pk, hq, hkv, d):
     lens = [20000, 16, 17001]
