@@ -958,8 +958,9 @@ PKV_API int pkv_copy_block_scales(float* k_scales, float* v_scales, pkv_cache_de
  *               contents need no initialisation; calls that share it must be
  *               ordered on the GPU.  Its size depends on the current device.
  * Small batches (the pages of all pairs within a wave of CTAs) run in one
- * launch, a cluster of CTAs for each (sequence, KV head) pair; others take the
- * flat split.  Other arguments and errors are those of
+ * launch, a cluster of CTAs for each (sequence, KV head) pair; more pairs, if
+ * max_context_len and the table hold them to 32 pages, a warp each; others take
+ * the flat split.  The splits round differently.  Other arguments and errors are those of
  * pkv_paged_decode_attention.
  * pkv_paged_decode_attention_fp8_block_scaled_bf16out rounds the float32
  * result once to bf16, bit for bit.

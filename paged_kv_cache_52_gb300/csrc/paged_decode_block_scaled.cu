@@ -20,11 +20,13 @@
 // the f16 warp MMAs on the converted codes; the page arithmetic is that of the
 // per-pool decode (pkv_decode_fp8_body.cuh), with the two factors.
 //
-// Two splits of the work:
+// Three splits of the work:
 //  * cluster: a (sequence, KV head) pair belongs to a cluster of 1 to 8 CTAs
 //    of four warps, whose warps take the pair's pages in turn; the warps'
 //    results meet in shared memory and the CTAs' over distributed shared
 //    memory.  One launch, no workspace: for batches whose pages fit one wave.
+//  * pairs: each warp takes a (sequence, KV head) pair whole.  One launch: for
+//    more pairs than clusters of one CTA run at once, of up to 32 pages each.
 //  * flat: the pages of all sequences laid end to end are cut into equal
 //    ranges, one for each group of Hkv warps of a grid of one CTA per SM (as in
 //    paged_decode_flat.cu); a second kernel joins the pieces of the pairs that
@@ -317,6 +319,71 @@ __device__ __forceinline__ void bs_issue(uint32_t dst, uint32_t bar, const CUten
   }
 }
 
+// A warp's `cnt` pages, the i-th at block page0 + i step of the sequence, lane i
+// holding its id and scales: attended by the queries of rows row0 on.
+template <int D, int G>
+__device__ __forceinline__ void bs_walk(BsAcc<D, G>& acc, uint32_t ring, uint32_t bars,
+                                        const CUtensorMap& tmap_k, const CUtensorMap& tmap_v,
+                                        const DecodeParams& p, size_t row0, int kvh, int id,
+                                        float ks, float vs, int cnt, int page0, int step, int len,
+                                        int lane) {
+  using T = BsPage<D>;
+  constexpr int kStages = T::kStages;
+  constexpr unsigned kFull = 0xffffffffu;
+  auto issue = [&](int i) {  // warp-wide
+    const int st = i % kStages;
+    bs_issue<D>(ring + st * T::kStageBytes, bars + st * 8, tmap_k, tmap_v, kvh,
+                __shfl_sync(kFull, id, i));
+  };
+  for (int i = 0; i < cnt && i < kStages; ++i) issue(i);
+  int issued = min(cnt, kStages);
+
+  acc.start(p.q, row0, p.scale_log2, lane);
+  bool failed = false;
+  int i = 0;
+  while (i < cnt) {
+    const bool two = i + 1 < cnt;
+    bool landed = mbar_wait_bounded(bars + (i % kStages) * 8, (i / kStages) & 1);
+    if (two && landed)
+      landed = mbar_wait_bounded(bars + ((i + 1) % kStages) * 8, ((i + 1) / kStages) & 1);
+    if (!__all_sync(kFull, landed)) {
+      failed = true;
+      break;
+    }
+    const uint32_t b0 = ring + (i % kStages) * T::kStageBytes;
+    const int t0 = (page0 + i * step) * kBlockTokens;
+    const float ks0 = __shfl_sync(kFull, ks, i), vs0 = __shfl_sync(kFull, vs, i);
+    if (two) {
+      const uint32_t kb[2] = {b0, ring + ((i + 1) % kStages) * T::kStageBytes};
+      const int tk[2] = {t0, t0 + step * kBlockTokens};
+      const float k2[2] = {ks0, __shfl_sync(kFull, ks, i + 1)};
+      const float v2[2] = {vs0, __shfl_sync(kFull, vs, i + 1)};
+      bs_pages<D, G, 2>(acc, kb, tk, k2, v2, len, lane);
+    } else {
+      const uint32_t kb[1] = {b0};
+      const int tk[1] = {t0};
+      const float k1[1] = {ks0}, v1[1] = {vs0};
+      bs_pages<D, G, 1>(acc, kb, tk, k1, v1, len, lane);
+    }
+    __syncwarp();
+    const int n = two ? 2 : 1;
+    for (int j = i; j < i + n; ++j)
+      if (j + kStages < cnt) {
+        issue(j + kStages);
+        ++issued;
+      }
+    i += n;
+  }
+  if (failed) {
+    if (lane == 0) {
+      atomicOr(&g_decode_error, kErrWaitTimeout);
+      for (int k = i; k < issued; ++k)
+        (void)mbar_wait_bounded(bars + (k % kStages) * 8, (k / kStages) & 1);
+    }
+    __syncwarp();
+  }
+}
+
 // ------------------------------------------------------------ cluster split
 constexpr int kBsClWarps = 4;
 constexpr int kBsClMaxCtas = 8;    // per cluster: the portable limit
@@ -388,60 +455,10 @@ decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
       atomicOr(&g_decode_error, kErrBadBlockId);
     }
   }
-  auto issue = [&](int i) {  // warp-wide
-    const int st = i % kStages;
-    bs_issue<D>(ring + st * T::kStageBytes, bars + st * 8, tmap_k, tmap_v, kvh,
-                __shfl_sync(kFull, id, i));
-  };
-  for (int i = 0; i < cnt && i < kStages; ++i) issue(i);
-  int issued = min(cnt, kStages);
-
-  const size_t row0 = size_t(seq) * p.q_heads + size_t(kvh) * G;
   BsAcc<D, G> acc;
-  acc.start(p.q, row0, p.scale_log2, lane);
-  bool failed = false;
-  int i = 0;
-  while (i < cnt) {
-    const bool two = i + 1 < cnt;
-    bool landed = mbar_wait_bounded(bars + (i % kStages) * 8, (i / kStages) & 1);
-    if (two && landed)
-      landed = mbar_wait_bounded(bars + ((i + 1) % kStages) * 8, ((i + 1) / kStages) & 1);
-    if (!__all_sync(kFull, landed)) {
-      failed = true;
-      break;
-    }
-    const uint32_t b0 = ring + (i % kStages) * T::kStageBytes;
-    const int t0 = (page0 + i * step) * kBlockTokens;
-    const float ks0 = __shfl_sync(kFull, ks, i), vs0 = __shfl_sync(kFull, vs, i);
-    if (two) {
-      const uint32_t kb[2] = {b0, ring + ((i + 1) % kStages) * T::kStageBytes};
-      const int tk[2] = {t0, t0 + step * kBlockTokens};
-      const float k2[2] = {ks0, __shfl_sync(kFull, ks, i + 1)};
-      const float v2[2] = {vs0, __shfl_sync(kFull, vs, i + 1)};
-      bs_pages<D, G, 2>(acc, kb, tk, k2, v2, len, lane);
-    } else {
-      const uint32_t kb[1] = {b0};
-      const int tk[1] = {t0};
-      const float k1[1] = {ks0}, v1[1] = {vs0};
-      bs_pages<D, G, 1>(acc, kb, tk, k1, v1, len, lane);
-    }
-    __syncwarp();
-    const int n = two ? 2 : 1;
-    for (int j = i; j < i + n; ++j)
-      if (j + kStages < cnt) {
-        issue(j + kStages);
-        ++issued;
-      }
-    i += n;
-  }
-  if (failed) {
-    if (lane == 0) {
-      atomicOr(&g_decode_error, kErrWaitTimeout);
-      for (int k = i; k < issued; ++k)
-        (void)mbar_wait_bounded(bars + (k % kStages) * 8, (k / kStages) & 1);
-    }
-    __syncwarp();
-  }
+  const size_t row0 = size_t(seq) * p.q_heads + size_t(kvh) * G;
+  bs_walk<D, G>(acc, ring, bars, tmap_k, tmap_v, p, row0, kvh, id, ks, vs, cnt, page0, step, len,
+                lane);
   acc.sum_l();
 
   // the warp's result over its own ring: O in the weights' unit, m, l
@@ -527,12 +544,85 @@ decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
   cluster.sync();  // no CTA leaves while another reads its shared memory
 }
 
+// -------------------------------------------------------- a pair to each warp
+// The four warps of a CTA take four pairs, whole and by themselves: no join, no
+// second launch, and CTAs are handed out as others end (256 contexts of up to 200
+// tokens, 64 heads of 128 on 8: 15.3 us, 27.2 with the flat split; 254 of one token,
+// 128 / 8 of 64: 5.8, 16.9; 256 of 500, 64 / 8 of 128: 57, 62).  One long context
+// among short ones is what the flat split does better (15 of 30 tokens and one of
+// 500, 32 / 32 heads of 128: 9.5 against 13.0).
+template <int D, int G>
+__global__ void __launch_bounds__(kBsClWarps * 32, 3)
+decode_block_scaled_pairs_kernel(const __grid_constant__ CUtensorMap tmap_k,
+                                 const __grid_constant__ CUtensorMap tmap_v,
+                                 const BsDecodeParams bp, int pairs) {
+  using T = BsPage<D>;
+  using L = BsCl<D, G>;
+  const DecodeParams& p = bp.d;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0);  // a value of the warp
+  const int gid = lane >> 2, tig = lane & 3;
+  const uint32_t ring = smem_u32(smem + warp * T::kRingBytes);
+  const uint32_t bars = smem_u32(smem + L::kBarOff) + warp * T::kStages * 8;
+  if (lane == 0) {
+    for (int st = 0; st < T::kStages; ++st) mbar_init(bars + st * 8, 1);
+    fence_barrier_init();
+    tma_prefetch_desc(&tmap_k);
+    tma_prefetch_desc(&tmap_v);
+  }
+  __syncwarp();
+  griddep_wait();
+  griddep_launch_dependents();
+  const int pair = blockIdx.x * kBsClWarps + warp;
+  if (pair >= pairs) return;
+  const int seq = pair / p.kv_heads, kvh = pair - seq * p.kv_heads;
+
+  int id = 0;
+  if (lane < bp.max_blocks)
+    id = __ldg(p.block_tables + size_t(seq) * p.max_blocks_per_seq + lane);
+  bool bad;
+  const int raw = __ldg(p.context_lens + seq);
+  const int cnt = flat_pages(raw, bp.max_blocks, bad);
+  if (bad && kvh == 0 && lane == 0) atomicOr(&g_decode_error, kErrBadContext);
+  const int len = raw < 0 ? 0 : min(raw, cnt * kBlockTokens);
+  float ks = 0.f, vs = 0.f;
+  if (lane < cnt) {
+    if (id >= 0 && id < p.num_blocks) {
+      ks = __ldg(bp.k_scales + size_t(id) * p.kv_heads + kvh);
+      vs = __ldg(bp.v_scales + size_t(id) * p.kv_heads + kvh);
+    } else {
+      atomicOr(&g_decode_error, kErrBadBlockId);
+    }
+  }
+  BsAcc<D, G> acc;
+  const size_t row0 = size_t(seq) * p.q_heads + size_t(kvh) * G;
+  bs_walk<D, G>(acc, ring, bars, tmap_k, tmap_v, p, row0, kvh, id, ks, vs, cnt, 0, 1, len, lane);
+  acc.sum_l();
+#pragma unroll
+  for (int nh = 0; nh < BsAcc<D, G>::NH; ++nh)
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int head = 8 * nh + 2 * tig + c;
+      if (head >= G) continue;
+      const float inv = cnt == 0 ? 0.f : acc.unit(nh, c) / acc.l[nh][c];
+#pragma unroll
+      for (int mt = 0; mt < BsAcc<D, G>::MT; ++mt) {
+        const size_t at = (row0 + head) * D + 16 * mt + 2 * gid;
+        store_out(p, at, acc.o[nh][mt][c] * inv);
+        store_out(p, at + 1, acc.o[nh][mt][c + 2] * inv);
+      }
+    }
+}
+
 // --------------------------------------------------------------- flat split
 constexpr int kBsFlatMaxSeqs = 1024;
 constexpr int kBsFlatWarps = 12;
-// Pages of a range at least, the two that a step takes: only batches of short
-// contexts have fewer than warps to take them (254 contexts of a token, 128 heads of
-// 64 on 8: 17.0 us, 35.1 with eight pages at least; 227 of 32 / 32 of 128: 14.4, 21.7).
+// Pages of a range at least, the two that a step takes: only contexts far below the
+// bound on their lengths leave warps without work (254 contexts of a token, 128 heads
+// of 64 on 8: 17.0 us, 35.1 with eight pages at least; 227 of 32 / 32 of 128: 14.4, 21.7).
 constexpr int kBsFlatMinPages = 2;
 
 template <int D>
@@ -924,6 +1014,19 @@ cudaError_t launch_cluster(const BsDecodeParams& bp, int num_seqs, int ctas,
 }
 
 template <int D, int G>
+cudaError_t launch_pairs(const BsDecodeParams& bp, int num_seqs, const CUtensorMap* tk,
+                         const CUtensorMap* tv, cudaStream_t stream) {
+  constexpr int kSmem = BsCl<D, G>::kOutOff + 1024;  // rings and barriers
+  static std::atomic<int> attr_done[kAttrMaxDevices];
+  cudaError_t e = set_smem_limit_once(decode_block_scaled_pairs_kernel<D, G>, kSmem, attr_done);
+  if (e != cudaSuccess) return e;
+  const int pairs = num_seqs * bp.d.kv_heads;
+  return launch_after_previous(decode_block_scaled_pairs_kernel<D, G>,
+                               dim3(unsigned((pairs + kBsClWarps - 1) / kBsClWarps)),
+                               dim3(kBsClWarps * 32), kSmem, stream, *tk, *tv, bp, pairs);
+}
+
+template <int D, int G>
 cudaError_t launch_flat(const BsDecodeParams& bp, const DecodeFlatParams& fp, int ctas,
                         const CUtensorMap* tk, const CUtensorMap* tv, cudaStream_t stream) {
   using L = BsFlat<D>;
@@ -973,7 +1076,8 @@ cudaError_t launch_decode_block_scaled(const DecodeBlockScaledArgs& a, const CUt
   const long long all_pairs = (long long)a.num_seqs * a.kv_heads;
   const int ctas = cluster_ctas(all_pairs, max_blocks, num_sms);
   // the flat split's prefix sums hold 1024 sequences: more go in turn
-  const int chunk = ctas ? a.num_seqs : kBsFlatMaxSeqs;
+  const bool alone = ctas == 0 && max_blocks <= kBsClMaxPages;
+  const int chunk = ctas || alone ? a.num_seqs : kBsFlatMaxSeqs;
   for (int s = 0; s < a.num_seqs; s += chunk) {
     const int n = std::min(chunk, a.num_seqs - s);
     const size_t row = size_t(s) * a.q_heads * a.d_head;
@@ -990,8 +1094,9 @@ cudaError_t launch_decode_block_scaled(const DecodeBlockScaledArgs& a, const CUt
     cudaError_t e = cudaErrorInvalidValue;
 #define PKV_BS_CASE(DD, GG)                                                       \
   if (a.d_head == DD && group == GG)                                              \
-    e = ctas ? launch_cluster<DD, GG>(bp, n, ctas, tk, tv, stream)                \
-             : launch_flat<DD, GG>(bp, fp, num_sms, tk, tv, stream)
+    e = ctas    ? launch_cluster<DD, GG>(bp, n, ctas, tk, tv, stream)             \
+        : alone ? launch_pairs<DD, GG>(bp, n, tk, tv, stream)                     \
+                : launch_flat<DD, GG>(bp, fp, num_sms, tk, tv, stream)
     PKV_BS_CASE(128, 1);
     PKV_BS_CASE(128, 2);
     PKV_BS_CASE(128, 4);

@@ -236,13 +236,43 @@ def test_decode_of_batches_over_one_wave(pk, hq, hkv, d):
 
 @pytest.mark.parametrize("hq,hkv,d", [(32, 32, 128), (128, 8, 64)])
 @pytest.mark.parametrize("lens", [[1] * 227, [(5 * i) % 34 for i in range(254)]])
-def test_decode_of_many_short_contexts(pk, hq, hkv, d, lens):
-    """Fewer pages than warps: ranges of two pages, over several sequences and within one."""
-    c = _decode_case(lens, hq, hkv, d, seed=hq)
-    got = _decode(pk, c)
+@pytest.mark.parametrize("width", [None, 40])
+def test_decode_of_many_short_contexts(pk, hq, hkv, d, lens, width):
+    """A warp each; or, where contexts might be of 40 pages, fewer pages than warps:
+    ranges of two pages, over several sequences and within one."""
+    c = _decode_case(lens, hq, hkv, d, seed=hq, width=width)
+    bound = BS * c["tables"].shape[1]
+    got = _decode(pk, c, max_context_len=bound)
     _check_rows(got.cpu().numpy(), c, range(0, len(lens), 11))
-    assert torch.equal(_decode(pk, c, out_dtype=torch.bfloat16), got.bfloat16())
+    assert torch.equal(_decode(pk, c, max_context_len=bound, out_dtype=torch.bfloat16),
+                       got.bfloat16())
     assert pk.get_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(8, 8, 64), (16, 4, 128), (16, 16, 128), (128, 8, 128),
+                                      (4, 2, 64), (4, 2, 128), (16, 1, 64), (32, 4, 64)])
+@pytest.mark.parametrize("width", [32, 33])
+def test_decode_of_ranges_and_of_whole_pairs(pk, hq, hkv, d, width):
+    """Tables of up to 32 pages give a warp a whole pair, wider ones a range of pages;
+    one sequence fills its table, another's length is below 0."""
+    lens = [(41 * i * i) % 330 for i in range(460)]
+    lens[7] = BS * width
+    c = _decode_case(lens, hq, hkv, d, seed=hq, width=width)
+    got = _decode(pk, c, max_context_len=BS * width)
+    _check_rows(got.cpu().numpy(), c, list(range(0, 460, 23)) + [7])
+    assert torch.equal(_decode(pk, c, max_context_len=BS * width, out_dtype=torch.bfloat16),
+                       got.bfloat16())
+    assert pk.get_device_error(clear=True) == 0
+    bad = dict(c, lens=lens[:9] + [-1] + lens[10:])
+    bad["tables"] = c["tables"].clone()
+    bad["tables"][11, 0] = -5
+    lens_11 = lens[11]
+    other = _decode(pk, bad, max_context_len=BS * width)
+    assert pk.get_device_error(clear=True) == 0x4 | (0x2 if lens_11 else 0)
+    assert not other[9].any() and torch.isfinite(other).all()
+    rest = [s for s in range(460) if s not in (9, 11)]
+    if width == 32:  # (ranges move with the lengths before them)
+        assert torch.equal(other[rest], got[rest])
 
 
 @pytest.mark.parametrize("hq,hkv,d", [(4, 1, 128), (2, 2, 64)])
