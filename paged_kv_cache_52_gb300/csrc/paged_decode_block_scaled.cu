@@ -8,12 +8,15 @@
 // a whole block is one factor: K's in the factor that scores have anyway, V's
 // in the weights on their way to the second product.  The weights enter that
 // product as f16, so O has a running maximum of its own,
-//   mv = max (x + floor(log2 v_scale)),
-// and is kept in units of 2^mv: a weight v_scale 2^(x - mv) is below 2 for every
-// row, and a block counts by what it gives to the row, whatever scales blocks
+//   dv = max ((x - m) + floor(log2 v_scale)),
+// and is kept in units of 2^(m + dv): a weight v_scale 2^(x - m - dv) is below 2 for
+// every row, and a block counts by what it gives to the row, whatever scales blocks
 // have to which the row pays no heed.  What is below 2^-25 of a row's largest
-// is lost, the rest within 2^-11 of itself or 2^-25 of the largest.  Queries are f16 after an exact power of two that
-// brings a row outside [2^-6, 2^15) into it.
+// is lost, the rest within 2^-11 of itself or 2^-25 of the largest.  dv is kept beside
+// m and not added to it: a score of 2^31 would swallow it.  For the same reason the
+// pieces of a pair meet as (m, l) and not as m + log2 l: rows of equal scores are means
+// of their values however large the scores.  Queries are f16 after an exact power of
+// two that brings a row outside [2^-6, 2^15) into it.
 //
 // Bound by HBM: every code is read once, 4 flops for each byte and query head.
 // A warp owns a ring of pages (K and V of one KV head, fetched by TMA) and runs
@@ -57,7 +60,8 @@ struct BsDecodeParams {
   DecodeParams d;  // scale_log2 without the K scale; out_scale is not used
   const float* k_scales;
   const float* v_scales;
-  int max_blocks;  // pages attended per sequence at most
+  float2* part_ml;  // a piece's maximum and sum (d.part_o: its normalised rows)
+  int max_blocks;   // pages attended per sequence at most
 };
 
 template <int D>
@@ -80,7 +84,7 @@ struct BsAcc {
   static constexpr int MT = D / 16;
   float o[NH][MT][4];
   float m[NH][2], l[NH][2];
-  float mv[NH][2];    // O is in units of 2^mv
+  float dv[NH][2];    // O is in units of 2^(m + dv)
   float qmul[NH][2];  // what the queries were divided by, times the softmax scale
   uint32_t qf[NH][MT][2];
 
@@ -116,8 +120,8 @@ struct BsAcc {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         qmul[nh][c] = __shfl_sync(0xffffffffu, mul, (2 * tig + c) * 4);
-        m[nh][c] = mv[nh][c] = -INFINITY;
-        l[nh][c] = 0.f;
+        m[nh][c] = -INFINITY;
+        l[nh][c] = dv[nh][c] = 0.f;
       }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) o[nh][mt][0] = o[nh][mt][1] = o[nh][mt][2] = o[nh][mt][3] = 0.f;
@@ -125,7 +129,7 @@ struct BsAcc {
   }
   // O's unit over the weights' (an empty state's O is 0)
   __device__ __forceinline__ float unit(int nh, int c) const {
-    return m[nh][c] == -INFINITY ? 0.f : ex2(mv[nh][c] - m[nh][c]);
+    return m[nh][c] == -INFINITY ? 0.f : ex2(dv[nh][c]);
   }
 
   __device__ __forceinline__ void sum_l() {
@@ -201,30 +205,33 @@ __device__ __forceinline__ void bs_pages_as(BsAcc<D, G>& A, const uint32_t (&kba
     float pr[NP][4], w[NP][2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      float x0[NP], x1[NP];
-      float mx = -INFINITY, mxv = -INFINITY;
+      float x0[NP], x1[NP], top[NP];
 #pragma unroll
       for (int pg = 0; pg < NP; ++pg) {
         const float f = ks[pg] * A.qmul[nh][c];
         x0[pg] = FULL || k0_in[pg] ? (s[pg][nh][c] + s_odd[pg][nh][c]) * f : -INFINITY;
         x1[pg] = FULL || k1_in[pg] ? (s[pg][nh][c + 2] + s_odd[pg][nh][c + 2]) * f : -INFINITY;
-        const float top = fmaxf(x0[pg], x1[pg]);
-        mx = fmaxf(mx, top);
-        mxv = fmaxf(mxv, top + lv[pg]);
+        top[pg] = fmaxf(x0[pg], x1[pg]);
       }
 #pragma unroll
-      for (int o = 4; o <= 16; o <<= 1) {
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        mxv = fmaxf(mxv, __shfl_xor_sync(0xffffffffu, mxv, o));
-      }
-      const float mn = fmaxf(A.m[nh][c], mx), mvn = fmaxf(A.mv[nh][c], mxv);
-      const float alpha = ex2(A.m[nh][c] - mn);
-      beta[nh][c] = ex2(A.mv[nh][c] - mvn);
-      all_same = all_same && A.mv[nh][c] == mvn;
+      for (int o = 4; o <= 16; o <<= 1)
+#pragma unroll
+        for (int pg = 0; pg < NP; ++pg)
+          top[pg] = fmaxf(top[pg], __shfl_xor_sync(0xffffffffu, top[pg], o));
+      float mn = A.m[nh][c];
+#pragma unroll
+      for (int pg = 0; pg < NP; ++pg) mn = fmaxf(mn, top[pg]);
+      const float fall = A.m[nh][c] - mn, dv = A.dv[nh][c] + fall;  // (-inf at first)
+      float dvn = dv;
+#pragma unroll
+      for (int pg = 0; pg < NP; ++pg) dvn = fmaxf(dvn, (top[pg] - mn) + lv[pg]);
+      const float alpha = ex2(fall);
+      beta[nh][c] = ex2(dv - dvn);
+      all_same = all_same && dv == dvn;
       A.m[nh][c] = mn;
-      A.mv[nh][c] = mvn;
+      A.dv[nh][c] = dvn;
       // (bounded: where a weight is 0 its block's factor may be past float32)
-      const float unit = ex2(mn - mvn);
+      const float unit = ex2(-dvn);
 #pragma unroll
       for (int pg = 0; pg < NP; ++pg) {
         const float f = vs[pg] * unit;
@@ -394,7 +401,7 @@ struct BsCl {
   static constexpr int kRings = kBsClWarps * BsPage<D>::kRingBytes;
   static constexpr int kBarOff = kRings;
   static constexpr int kOutOff = kBarOff + kBsClWarps * BsPage<D>::kStages * 8;
-  static constexpr int kRowFloats = G * D + 2 * G;  // O, then m and l
+  static constexpr int kRowFloats = G * D + 2 * G;  // O, then each row's m and l
   static constexpr int kSmemBytes = kOutOff + kRowFloats * 4 + 1024;
   static_assert(kRowFloats * 4 <= BsPage<D>::kRingBytes, "a warp's result fits its ring");
 };
@@ -475,28 +482,27 @@ decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
         *reinterpret_cast<float2*>(mo + head * D + 16 * mt + 2 * gid) =
             make_float2(acc.o[nh][mt][c] * unit, acc.o[nh][mt][c + 2] * unit);
       if (gid == 0) {
-        mo[G * D + head] = acc.m[nh][c];
-        mo[G * D + G + head] = acc.l[nh][c];
+        reinterpret_cast<float2*>(mo + G * D)[head] = make_float2(acc.m[nh][c], acc.l[nh][c]);
       }
     }
   __syncthreads();
-  // the CTA's: normalised O, and its log2-sum-exp in place of m (-inf: no key)
+  // the CTA's: normalised O, m and l (0: no key)
   float* part = reinterpret_cast<float*>(smem + L::kOutOff);
   for (int x = threadIdx.x * 4; x < G * D; x += kBsClWarps * 32 * 4) {
     const int row = x / D;
     float big = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kBsClWarps; ++w)
-      big = fmaxf(big, reinterpret_cast<const float*>(smem + w * T::kRingBytes)[G * D + row]);
+      big = fmaxf(big, reinterpret_cast<const float2*>(smem + w * T::kRingBytes + G * D * 4)[row].x);
     float tot = 0.f;
     float4 val = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kBsClWarps; ++w) {
       const float* wo = reinterpret_cast<const float*>(smem + w * T::kRingBytes);
-      const float m = wo[G * D + row];
-      const float wgt = m == -INFINITY ? 0.f : ex2(m - big);
+      const float2 ml = reinterpret_cast<const float2*>(wo + G * D)[row];
+      const float wgt = ml.x == -INFINITY ? 0.f : ex2(ml.x - big);
       const float4 o = *reinterpret_cast<const float4*>(wo + x);
-      tot += wo[G * D + G + row] * wgt;
+      tot += ml.y * wgt;
       val.x += o.x * wgt;
       val.y += o.y * wgt;
       val.z += o.z * wgt;
@@ -505,7 +511,7 @@ decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
     const float inv = big == -INFINITY && tot == 0.f ? 0.f : 1.f / tot;
     *reinterpret_cast<float4*>(part + x) =
         make_float4(val.x * inv, val.y * inv, val.z * inv, val.w * inv);
-    if (x == row * D) part[G * D + row] = tot == 0.f ? -INFINITY : big + __log2f(tot);
+    if (x == row * D) reinterpret_cast<float2*>(part + G * D)[row] = make_float2(big, tot);
   }
   if (C == 1) {
     __syncthreads();
@@ -517,25 +523,26 @@ decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
   const int share = G * D / C;  // a multiple of 8: G D >= 64, C <= 8
   for (int x = rank * share + int(threadIdx.x); x < (rank + 1) * share; x += kBsClWarps * 32) {
     const int row = x / D;
-    float lse[kBsClMaxCtas], o[kBsClMaxCtas];
+    float2 ml[kBsClMaxCtas];
+    float o[kBsClMaxCtas];
 #pragma unroll
     for (int c = 0; c < kBsClMaxCtas; ++c) {
       if (c < C) {
         const float* other = cluster.map_shared_rank(part, c);
-        lse[c] = other[G * D + row];
+        ml[c] = reinterpret_cast<const float2*>(other + G * D)[row];
         o[c] = other[x];
       } else {
-        lse[c] = -INFINITY;
+        ml[c] = make_float2(-INFINITY, 0.f);
         o[c] = 0.f;
       }
     }
     float big = -INFINITY;
 #pragma unroll
-    for (int c = 0; c < kBsClMaxCtas; ++c) big = fmaxf(big, lse[c]);
+    for (int c = 0; c < kBsClMaxCtas; ++c) big = fmaxf(big, ml[c].x);
     float tot = 0.f, val = 0.f;
 #pragma unroll
     for (int c = 0; c < kBsClMaxCtas; ++c) {
-      const float wgt = lse[c] == -INFINITY ? 0.f : ex2(lse[c] - big);
+      const float wgt = ml[c].y == 0.f ? 0.f : ml[c].y * ex2(ml[c].x - big);
       tot += wgt;
       val += o[c] * wgt;
     }
@@ -771,8 +778,8 @@ decode_block_scaled_flat_kernel(const __grid_constant__ CUtensorMap tmap_k,
   BsAcc<D, G> acc;
   int cur_seq = -1, cur_first = 0, cur_last = 0, cur_len = 0, cur_end = 0;
   // the finished piece: the output when it is the pair's whole context, else
-  // its normalised partial at slot (sequence + g) Hkv + head (for one head
-  // the pieces are ordered by sequence and range alike: no two share a slot)
+  // its normalised partial, m and l at slot (sequence + g) Hkv + head (for one
+  // head the pieces are ordered by sequence and range alike: no two share a slot)
   auto flush = [&]() {
     acc.sum_l();
     const bool whole = cur_first == 0 && cur_last == cur_end - 1;
@@ -796,7 +803,8 @@ decode_block_scaled_flat_kernel(const __grid_constant__ CUtensorMap tmap_k,
             *reinterpret_cast<float2*>(p.part_o + (slot * G + head) * D + dim) = make_float2(v0, v1);
           }
         }
-        if (!whole && gid == 0) p.part_lse[slot * G + head] = acc.m[nh][cc] + __log2f(acc.l[nh][cc]);
+        if (!whole && gid == 0)
+          bp.part_ml[slot * G + head] = make_float2(acc.m[nh][cc], acc.l[nh][cc]);
       }
   };
 
@@ -872,14 +880,15 @@ decode_block_scaled_flat_kernel(const __grid_constant__ CUtensorMap tmap_k,
 // (pre[s] + n - 1) / c, range g's piece at slot (s + g) Hkv + h.  An empty
 // sequence gets zeros; a pair within one range is written already.  WPR warps
 // take a row's pieces, 16 (4) at a time each, with all their loads in flight at
-// once -- lane i reads piece i's log2-sum-exp -- and join their sums in shared
+// once -- lane i reads piece i's maximum and sum -- and join their sums in shared
 // memory: with few rows each has a hundred pieces, and it is round trips that
 // count (2 x 131072 tokens, 114 pieces: 39 us for one warp and eight loads in
 // flight, 5.0 now); with many rows there are two or none.
 template <int D, int WPR>
 __global__ void __launch_bounds__(256)
-decode_block_scaled_merge_kernel(const DecodeParams p, const DecodeFlatParams fp,
+decode_block_scaled_merge_kernel(const BsDecodeParams bp, const DecodeFlatParams fp,
                                  long long total_rows) {
+  const DecodeParams& p = bp.d;
   griddep_wait();
   griddep_launch_dependents();
   constexpr int kCols = D / 32;  // a lane's elements
@@ -905,7 +914,8 @@ decode_block_scaled_merge_kernel(const DecodeParams p, const DecodeFlatParams fp
   for (int i = 0; i < kCols; ++i) val[i] = 0.f;
   for (int b = g0 + w * kBatch; b <= g1; b += WPR * kBatch) {
     const int cnt = min(kBatch, g1 - b + 1);
-    const float lse = lane < cnt ? __ldg(p.part_lse + slot(b + lane)) : -INFINITY;
+    const float2 ml =
+        lane < cnt ? __ldg(bp.part_ml + slot(b + lane)) : make_float2(-INFINITY, 0.f);
     float x[kBatch][kCols];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
@@ -922,13 +932,13 @@ decode_block_scaled_merge_kernel(const DecodeParams p, const DecodeFlatParams fp
         x[i][1] = v.y;
       }
     }
-    float top = lse;
+    float top = ml.x;
 #pragma unroll
     for (int o = kBatch / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
     top = fmaxf(big, __shfl_sync(kFull, top, 0));
     const float alpha = big == top ? 1.f : ex2(big - top);  // (-inf: 0, or nothing yet)
     big = top;
-    const float mine = lane < cnt ? ex2(lse - top) : 0.f;
+    const float mine = lane < cnt ? ml.y * ex2(ml.x - top) : 0.f;
     float sum = mine;
 #pragma unroll
     for (int o = kBatch / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
@@ -976,16 +986,16 @@ decode_block_scaled_merge_kernel(const DecodeParams p, const DecodeFlatParams fp
 namespace {
 
 template <int D>
-cudaError_t launch_merge(const DecodeParams& d, const DecodeFlatParams& fp, int ctas,
+cudaError_t launch_merge(const BsDecodeParams& bp, const DecodeFlatParams& fp, int ctas,
                          cudaStream_t stream) {
-  const long long rows = (long long)fp.num_seqs * d.q_heads;
+  const long long rows = (long long)fp.num_seqs * bp.d.q_heads;
   const bool few = rows <= 8ll * ctas;
   const long long grid = few ? rows : (rows + 7) / 8;
   if (grid > INT_MAX) return cudaErrorInvalidValue;
   return few ? launch_after_previous(decode_block_scaled_merge_kernel<D, 8>,
-                                     dim3(unsigned(grid)), dim3(256), 0, stream, d, fp, rows)
+                                     dim3(unsigned(grid)), dim3(256), 0, stream, bp, fp, rows)
              : launch_after_previous(decode_block_scaled_merge_kernel<D, 1>,
-                                     dim3(unsigned(grid)), dim3(256), 0, stream, d, fp, rows);
+                                     dim3(unsigned(grid)), dim3(256), 0, stream, bp, fp, rows);
 }
 
 template <int D, int G>
@@ -1037,7 +1047,7 @@ cudaError_t launch_flat(const BsDecodeParams& bp, const DecodeFlatParams& fp, in
   e = launch_after_previous(decode_block_scaled_flat_kernel<D, G>, dim3(unsigned(ctas)),
                             dim3(kBsFlatWarps * 32), L::kSmemBytes, stream, *tk, *tv, bp, fp);
   if (e != cudaSuccess) return e;
-  return launch_merge<D>(bp.d, fp, ctas, stream);
+  return launch_merge<D>(bp, fp, ctas, stream);
 }
 
 // CTAs of a pair's cluster, or 0 for the flat split.
@@ -1062,7 +1072,6 @@ cudaError_t launch_decode_block_scaled(const DecodeBlockScaledArgs& a, const CUt
   BsDecodeParams bp = {};
   DecodeParams& d = bp.d;
   d.part_o = a.part_o;
-  d.part_lse = a.part_lse;
   d.q_heads = a.q_heads;
   d.kv_heads = a.kv_heads;
   d.num_blocks = a.num_blocks;
@@ -1072,6 +1081,7 @@ cudaError_t launch_decode_block_scaled(const DecodeBlockScaledArgs& a, const CUt
   d.out_bf16 = a.out_bf16 ? 1 : 0;
   bp.k_scales = a.k_scales;
   bp.v_scales = a.v_scales;
+  bp.part_ml = a.part_ml;
   bp.max_blocks = max_blocks;
   const long long all_pairs = (long long)a.num_seqs * a.kv_heads;
   const int ctas = cluster_ctas(all_pairs, max_blocks, num_sms);

@@ -2139,11 +2139,11 @@ int check_block_scaled(const pkv_cache_desc& c) {
   return PKV_OK;
 }
 
-// Workspace of the flat split: partial rows, their log2-sum-exps, the prefix
+// Workspace of the flat split: partial rows, their maxima and sums, the prefix
 // sums of one launch's sequences.
 struct BlockScaledDecodeLayout {
   int sms = 0;
-  size_t lse_off = 0, pre_off = 0, total = 0;
+  size_t ml_off = 0, pre_off = 0, total = 0;
 };
 
 int block_scaled_decode_layout(int num_seqs, int q_heads, int kv_heads, int d_head,
@@ -2159,8 +2159,8 @@ int block_scaled_decode_layout(int num_seqs, int q_heads, int kv_heads, int d_he
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t rows =
       (size_t(seqs) * size_t(kv_heads) + size_t(warps)) * size_t(q_heads / kv_heads);
-  w->lse_off = up(rows * size_t(d_head) * 4);
-  w->pre_off = w->lse_off + up(rows * 4);
+  w->ml_off = up(rows * size_t(d_head) * 4);
+  w->pre_off = w->ml_off + up(rows * 8);
   w->total = w->pre_off + up((size_t(seqs) + 1) * 4);
   return PKV_OK;
 }
@@ -2205,7 +2205,7 @@ int decode_block_scaled(const void* q, int num_seqs, int q_heads, const void* k_
   a.out = out;
   a.out_bf16 = out_bf16;
   a.part_o = reinterpret_cast<float*>(ws);
-  a.part_lse = reinterpret_cast<float*>(ws + w.lse_off);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.ml_off);
   a.pre = reinterpret_cast<int32_t*>(ws + w.pre_off);
   a.num_seqs = num_seqs;
   a.q_heads = q_heads;

@@ -341,8 +341,10 @@ struct DecodeBlockScaledArgs {
   const float *k_scales, *v_scales;
   void* out;
   bool out_bf16;
-  float *part_o, *part_lse;  // a slot for every pair of one launch and every warp
-  int32_t* pre;              // [min(num_seqs, flat seqs) + 1]
+  // a slot for every pair of one launch and every warp: rows, their maxima and sums
+  float* part_o;
+  float2* part_ml;
+  int32_t* pre;  // [min(num_seqs, flat seqs) + 1]
   int num_seqs, q_heads, kv_heads, d_head, num_blocks, max_blocks_per_seq, max_context_len;
   float scale_log2;
 };
