@@ -69,3 +69,68 @@ def test_equal_scores_of_any_size_give_the_mean(pk, way, d, size, power):
         want = np.repeat(v.mean(0), 4, axis=0)
         tol = np.repeat(np.abs(v).mean(0), 4, axis=0) * (n * 2.0 ** -23 + 2.0 ** -19)
         assert (np.abs(got[s] - want) <= tol).all(), (s, n, got[s, :, 0], want[:, 0])
+
+
+# ------------------------------------------------- the flat split's own paths
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (8, 4, 128)])
+def test_flat_decode_of_more_sequences_than_one_launch_holds(pk, hq, hkv, d):
+    """Three launches of up to 1024 sequences, each joining its own pieces over the
+    workspace of the one before."""
+    lens = [(13 * i) % 50 for i in range(2100)]
+    for s in (5, 1022, 1023, 1024, 1500, 2047, 2048, 2099):
+        lens[s] = 500 + s % 37
+    c = _decode_case(lens, hq, hkv, d, width=33)
+    got = _bounded(pk, c)
+    _check_rows(got.cpu().numpy(), c, list(range(0, 2100, 97)) +
+                [5, 1022, 1023, 1024, 1025, 1500, 2047, 2048, 2049, 2098, 2099])
+    assert torch.equal(_bounded(pk, c, out_dtype=torch.bfloat16), got.bfloat16())
+    assert not got[torch.tensor(lens) == 0].any()
+    assert pk.get_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("q_size", [1e-12, 2e-3, 3e4, 1e30])
+def test_flat_decode_of_queries_outside_the_range_of_f16(pk, q_size):
+    c = _decode_case(MANY, 8, 2, 128, q_size=q_size, width=40)
+    _check_rows(_bounded(pk, c).cpu().numpy(), c, range(0, len(MANY), 9))
+    assert pk.get_device_error(clear=True) == 0
+
+
+def test_flat_decode_of_scales_far_apart(pk):
+    c = _decode_case(MANY, 8, 2, 128, width=40)
+    order = torch.arange(c["vs"].shape[0]) % 61
+    c["vs"] = torch.exp2((order - 70).float())[:, None].expand(-1, 2).contiguous()
+    _check_rows(_bounded(pk, c).cpu().numpy(), c, range(0, len(MANY), 9))
+    assert pk.get_device_error(clear=True) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_flat_decode_of_large_values_that_weigh_nothing(pk, d):
+    """Every other block's values are 2^40 times the others' and its weights below
+    2^-1000: the others' values come out."""
+    c = _decode_case(MANY, 8, 2, d, spread=0.5, width=40)
+    c["q"] = c["q"].abs() + 0.5
+    low = torch.arange(c["kc"].shape[0]) % 2 == 0
+    low[c["tables"][:, 0].clamp(min=0).long()] = False
+    c["kc"] = torch.where(low[:, None, None, None], 0xf8, 0x38).to(torch.uint8).expand_as(
+        c["kc"]).contiguous()                                   # -256 or 1
+    c["ks"] = torch.where(low, 4.0, 2.0 ** -9)[:, None].repeat(1, 2)
+    c["vs"] = torch.where(low, 2.0 ** 30, 2.0 ** -10)[:, None].repeat(1, 2)
+    c["scale"] = 1.0                                            # scores of -d 1024 / 2 ln2 or less
+    got = _bounded(pk, c).double().cpu().numpy()
+    assert pk.get_device_error(clear=True) == 0
+    for s in range(0, len(MANY), 9):
+        if MANY[s]:
+            c1 = dict(c, vc=torch.where(low[:, None, None, None], 0, c["vc"]).to(torch.uint8))
+            k, v, kept = _values(c, s, "k"), _values(c1, s), _values(c, s, "k")[:, 0, 0] > 0
+            want = np.repeat(v[kept].mean(0), 4, axis=0)        # their scores are equal
+            tol = np.repeat(np.abs(v[kept]).mean(0), 4, axis=0) * (MANY[s] * 2.0 ** -23 + 2.0 ** -19)
+            assert k[~kept].max(initial=-1024) == -1024
+            assert (np.abs(got[s] - want) <= tol).all(), s
+
+
+def test_a_call_again_gives_the_same_bits(pk):
+    for lens, width in WAYS.values():
+        c = _decode_case(lens, 8, 2, 128, width=width)
+        first = _bounded(pk, c)
+        for _ in range(5):
+            assert torch.equal(_bounded(pk, c), first)
