@@ -950,7 +950,8 @@ PKV_API int pkv_copy_block_scales(float* k_scales, float* v_scales, pkv_cache_de
  * positive finite scales are taken, and scores are float32.  Queries enter the
  * product as f16, a row outside [2^-6, 2^15) brought into it by an exact power
  * of two; a weight times its block's V scale enters P V as f16, off by 2^-11 of
- * itself, or by 2^-25 of the row's largest such product where that is more.
+ * itself, or by 2^-39 of the row's largest such product where that is more (a
+ * weight below 2^-112 may count as less).
  *   max_context_len : host-side bound on context_lens.  Tokens of a longer
  *               sequence are not attended and PKV_DEVERR_BAD_CONTEXT is set.
  *   workspace : >= pkv_decode_fp8_block_scaled_workspace_bytes(...) device

@@ -9,10 +9,12 @@
 // in the weights on their way to the second product.  The weights enter that
 // product as f16, so O has a running maximum of its own,
 //   dv = max ((x - m) + floor(log2 v_scale)),
-// and is kept in units of 2^(m + dv): a weight v_scale 2^(x - m - dv) is below 2 for
-// every row, and a block counts by what it gives to the row, whatever scales blocks
-// have to which the row pays no heed.  What is below 2^-25 of a row's largest
-// is lost, the rest within 2^-11 of itself or 2^-25 of the largest.  dv is kept beside
+// and is kept in units of 2^(m + dv - 14): a weight v_scale 2^(x - m - dv + 14) is below
+// 2^15 for every row (f16 ends at 2^16), and a block counts by what it gives to the row,
+// whatever scales blocks have to which the row pays no heed.  What is below 2^-39 of a
+// row's largest is lost, the rest within 2^-11 of itself or 2^-39 of the largest:
+// with weights up to 2 the tail of a long context, 10^5 keys of weights below 2^-25,
+// was lost as a whole.  dv is kept beside
 // m and not added to it: a score of 2^31 would swallow it.  For the same reason the
 // pieces of a pair meet as (m, l) and not as m + log2 l: rows of equal scores are means
 // of their values however large the scores.  Queries are f16 after an exact power of
@@ -82,9 +84,10 @@ template <int D, int G>
 struct BsAcc {
   static constexpr int NH = (G + 7) / 8;
   static constexpr int MT = D / 16;
+  static constexpr float kUp = 0x1p14f;
   float o[NH][MT][4];
   float m[NH][2], l[NH][2];
-  float dv[NH][2];    // O is in units of 2^(m + dv)
+  float dv[NH][2];    // O is in units of 2^(m + dv) / kUp
   float qmul[NH][2];  // what the queries were divided by, times the softmax scale
   uint32_t qf[NH][MT][2];
 
@@ -127,7 +130,11 @@ struct BsAcc {
       for (int mt = 0; mt < MT; ++mt) o[nh][mt][0] = o[nh][mt][1] = o[nh][mt][2] = o[nh][mt][3] = 0.f;
     }
   }
-  // O's unit over the weights' (an empty state's O is 0)
+  // an element of O times `f` (kUp by itself: its factor and f's may be small both)
+  __device__ __forceinline__ float value(int nh, int mt, int e, float f) const {
+    return o[nh][mt][e] * (1.f / kUp) * f;
+  }
+  // O's unit, kUp aside, over the weights' (an empty state's O is 0)
   __device__ __forceinline__ float unit(int nh, int c) const {
     return m[nh][c] == -INFINITY ? 0.f : ex2(dv[nh][c]);
   }
@@ -230,12 +237,13 @@ __device__ __forceinline__ void bs_pages_as(BsAcc<D, G>& A, const uint32_t (&kba
       all_same = all_same && dv == dvn;
       A.m[nh][c] = mn;
       A.dv[nh][c] = dvn;
-      // (bounded: where a weight is 0 its block's factor may be past float32)
+      // (bounded: a block whose weights are below 2^-112 may have a larger factor, past
+      // float32 even)
       const float unit = ex2(-dvn);
 #pragma unroll
       for (int pg = 0; pg < NP; ++pg) {
         const float f = vs[pg] * unit;
-        w[pg][c] = f > 0x1p126f ? 0x1p126f : f;
+        w[pg][c] = (f > 0x1p112f ? 0x1p112f : f) * A.kUp;
       }
       float add = 0.f;
 #pragma unroll
@@ -480,7 +488,7 @@ decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
       for (int mt = 0; mt < BsAcc<D, G>::MT; ++mt)
         *reinterpret_cast<float2*>(mo + head * D + 16 * mt + 2 * gid) =
-            make_float2(acc.o[nh][mt][c] * unit, acc.o[nh][mt][c + 2] * unit);
+            make_float2(acc.value(nh, mt, c, unit), acc.value(nh, mt, c + 2, unit));
       if (gid == 0) {
         reinterpret_cast<float2*>(mo + G * D)[head] = make_float2(acc.m[nh][c], acc.l[nh][c]);
       }
@@ -618,8 +626,8 @@ decode_block_scaled_pairs_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
       for (int mt = 0; mt < BsAcc<D, G>::MT; ++mt) {
         const size_t at = (row0 + head) * D + 16 * mt + 2 * gid;
-        store_out(p, at, acc.o[nh][mt][c] * inv);
-        store_out(p, at + 1, acc.o[nh][mt][c + 2] * inv);
+        store_out(p, at, acc.value(nh, mt, c, inv));
+        store_out(p, at + 1, acc.value(nh, mt, c + 2, inv));
       }
     }
 }
@@ -795,7 +803,7 @@ decode_block_scaled_flat_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
         for (int mt = 0; mt < BsAcc<D, G>::MT; ++mt) {
           const int dim = 16 * mt + 2 * gid;
-          const float v0 = acc.o[nh][mt][cc] * inv, v1 = acc.o[nh][mt][cc + 2] * inv;
+          const float v0 = acc.value(nh, mt, cc, inv), v1 = acc.value(nh, mt, cc + 2, inv);
           if (whole) {
             store_out(p, (row0 + head) * D + dim, v0);
             store_out(p, (row0 + head) * D + dim + 1, v1);

@@ -71,6 +71,35 @@ def test_equal_scores_of_any_size_give_the_mean(pk, way, d, size, power):
         assert (np.abs(got[s] - want) <= tol).all(), (s, n, got[s, :, 0], want[:, 0])
 
 
+@pytest.mark.parametrize("S,n,width", [(1, 3000, None), (2, 60000, None), (300, 600, 40),
+                                       (300, 500, 32)])
+def test_many_small_weights_beside_a_large_one(pk, S, n, width):
+    """One key of weight 1 and value 0, and n - 1 of weight 2^-26 and value 1.  A weight
+    times its V scale is off by half a step of f16, 2^-11 of itself, or by 2^-39 of the
+    row's largest such product; the score -26 and its exponential by 2^-17, a piece's
+sum of 512 keys or fewer by 2^-14."""
+    hkv, d = 2, 64
+    lens = [n] * S
+    g = torch.Generator().manual_seed(n)
+    tables, blocks = _tables(lens, g, width)
+    kc = torch.zeros(blocks, BS, hkv, d, dtype=torch.uint8)
+    kc[..., 0] = 0xdd                                           # -26
+    vc = torch.full_like(kc, 0x38)                              # 1
+    first = tables[:, 0].long()
+    kc[first, 3] = 0
+    vc[first, 3] = 0
+    one = torch.ones(blocks, hkv)
+    q = torch.zeros(S, 4, d, dtype=torch.bfloat16)
+    q[..., 0] = 1
+    c = dict(q=q, kc=kc, vc=vc, ks=one, vs=one, tables=tables, lens=lens, scale=float(np.log(2.0)))
+    got = _bounded(pk, c).double().cpu().numpy()
+    assert oracle.dequantize_blocks(kc[:1].numpy(), one[:1].numpy()).min() == -26
+    part = (n - 1) * 2.0 ** -26
+    want = part / (1 + part)
+    tol = want * (2.0 ** -11 + 2.0 ** -14 + 2.0 ** -17) + n * 2.0 ** -39
+    assert np.abs(got - want).max() <= tol, (got.min(), got.max(), want)
+
+
 # ------------------------------------------------- the flat split's own paths
 @pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (8, 4, 128)])
 def test_flat_decode_of_more_sequences_than_one_launch_holds(pk, hq, hkv, d):
