@@ -994,9 +994,10 @@ PKV_API int pkv_paged_decode_attention_fp8_block_scaled_bf16out(
  *         bytes, 256-byte aligned (PKV_ENOMEM if NULL or smaller); contents
  *         need no initialisation; calls that share it must be ordered on the
  *         GPU.
- * A chunk longer than its context (causal), a context beyond the block table,
- * no context, or a q_start out of order rejects that sequence: none of its rows
- * is written and PKV_DEVERR_BAD_QUERY_RANGE is set.
+ * A chunk longer than its context (causal), a context beyond the block table, no
+ * context, or a q_start beyond total_q rejects that sequence, one that ends
+ * before it begins all from it on: none of their rows is written and
+ * PKV_DEVERR_BAD_QUERY_RANGE is set.
  *
  * pkv_prompt_attention -- attention of whole prompts over the keys and values
  * just computed, before (or without) a cache: sequence s's tokens are rows
@@ -1019,9 +1020,10 @@ PKV_API int pkv_paged_decode_attention_fp8_block_scaled_bf16out(
  * other sequences, and of none, never reach a row, whatever they hold; nor do
  * NaN and infinities in V of later tokens of its own.  NaN in what a row sees
  * makes NaN of it, an infinity in V an infinity or NaN.
- * d_head 64 or 128, a group of 1, 2, 4, 8 or 16.  A q_start out of order or
- * beyond total_q leaves that sequence out (PKV_DEVERR_BAD_QUERY_RANGE).  No
- * workspace.
+ * d_head 64 or 128, a group of 1, 2, 4, 8 or 16.  A q_start beyond total_q leaves
+ * that sequence out; where q_start falls, the sequence that ends before it begins
+ * and all behind it are left out, for they may lie over earlier ones.  Both set
+ * PKV_DEVERR_BAD_QUERY_RANGE.  No workspace.
  */
 PKV_API size_t pkv_prefill_fp8_block_scaled_workspace_bytes(int num_seqs, int max_blocks_per_seq,
                                                             int kv_heads, int d_head);

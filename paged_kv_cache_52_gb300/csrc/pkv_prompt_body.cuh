@@ -221,19 +221,20 @@ __device__ __forceinline__ PromptLevels prompt_levels(const PromptArgs& p, int s
 // Item `rank` of a KV head, by one warp, those with the most keys first: finds
 // the level by bisection over the counts of items at or above one, then the
 // sequence within it.  `own`: lane l's sequences l, l + 32, ... of the first
-// 32 kSets; the others' are worked out again each time.
+// 32 kSets; the others' are worked out again each time.  `seqs`: how many count.
 // kSets 1 serves up to 32 sequences with little code, which a first item waits
 // for while it is fetched.
 template <int kSets>
 struct PromptTable {
   PromptLevels own[kSets];
+  int seqs;
 
   __device__ __forceinline__ void load(const PromptArgs& p, int tpc) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < kSets; ++i) {
       const int s = i * 32 + lane;
-      own[i] = s < p.num_seqs ? prompt_levels(p, s, tpc) : PromptLevels{0, 0};
+      own[i] = s < seqs ? prompt_levels(p, s, tpc) : PromptLevels{0, 0};
     }
   }
   // f(levels, sequence of lane 0) for every lane's sequences until it is false
@@ -242,13 +243,13 @@ struct PromptTable {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int i = 0; i < kSets; ++i) {
-      if (kSets > 1 && i * 32 >= p.num_seqs) return;
+      if (kSets > 1 && i * 32 >= seqs) return;
       if (!f(own[i], i * 32)) return;
     }
     if constexpr (kSets > 1)
-      for (int s0 = kSets * 32; s0 < p.num_seqs; s0 += 32) {
+      for (int s0 = kSets * 32; s0 < seqs; s0 += 32) {
         const int s = s0 + lane;
-        if (!f(s < p.num_seqs ? prompt_levels(p, s, tpc) : PromptLevels{0, 0}, s0)) return;
+        if (!f(s < seqs ? prompt_levels(p, s, tpc) : PromptLevels{0, 0}, s0)) return;
       }
   }
   __device__ __forceinline__ bool item(const PromptArgs& p, int tpc, int rank, int& seq,
@@ -451,6 +452,14 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     if (blockIdx.x == 0)
       for (int s = lane; s < p.num_seqs; s += 32)
         if (prompt_seq(p, s).bad) atomicOr(&g_prompt_error, kErrBadQueryRange);
+    // Sequences from the first on that ends before it begins are left out: the others'
+    // rows lie behind one another, so that no two write one row, and their items are
+    // no more than the launch took for granted (a cluster has one item).
+    int seqs = p.num_seqs;
+#pragma unroll 1
+    for (int s = lane; s < p.num_seqs; s += 32)
+      if (__ldg(p.q_start + s + 1) < __ldg(p.q_start + s)) seqs = min(seqs, s);
+    seqs = __reduce_min_sync(0xffffffffu, seqs);
     bool ok = true;
     auto publish = [&](const auto& table) {
       bool more = true;
@@ -487,10 +496,12 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
     };
     if (p.num_seqs <= 32) {
       PromptTable<1> table;
+      table.seqs = seqs;
       table.load(p, TPC);
       publish(table);
     } else {
       PromptTable<kPrRegSets> table;
+      table.seqs = seqs;
       table.load(p, TPC);
       publish(table);
     }
