@@ -927,9 +927,10 @@ PKV_API int pkv_paged_prefill_attention_fp8_limited(const void* q, const int32_t
  * receives rows belongs to one sequence (copy a shared one first:
  * pkv_copy_blocks and pkv_copy_block_scales).  A sequence with more new rows
  * than its context, with a context beyond the block table or with a q_start
- * out of order is left out (PKV_DEVERR_BAD_QUERY_RANGE); a block id outside
- * the pool skips its rows (PKV_DEVERR_BAD_BLOCK_ID).  The pools must not lie
- * over one another, nor the scales (PKV_EINVAL).  No workspace.
+ * beyond num_tokens is left out, and where q_start falls the sequence that ends
+ * before it begins and all behind it (PKV_DEVERR_BAD_QUERY_RANGE); a block id
+ * outside the pool skips its rows (PKV_DEVERR_BAD_BLOCK_ID).  The pools must not
+ * lie over one another, nor the scales (PKV_EINVAL).  No workspace.
  *
  * pkv_copy_block_scales -- the scales' part of pkv_copy_blocks: row pairs[i][1]
  * of both arrays becomes a copy of row pairs[i][0].

@@ -161,49 +161,65 @@ __global__ void __launch_bounds__(kBsThreads, 4)
 append_block_scaled_kernel(const AppendBlockScaledArgs a, int rows_per_cta) {
   griddep_wait();
   griddep_launch_dependents();
-  __shared__ int items, item_row[kBsMaxRows], item_first[kBsMaxRows], item_count[kBsMaxRows],
-      item_block[kBsMaxRows];
-  if (threadIdx.x == 0) items = 0;
+  __shared__ int items, fall, item_row[kBsMaxRows], item_first[kBsMaxRows],
+      item_count[kBsMaxRows], item_block[kBsMaxRows];
+  if (threadIdx.x == 0) {
+    items = 0;
+    fall = a.num_seqs;
+  }
   __syncthreads();
   // every sequence looks for its blocks that start among these rows
   const int64_t r0 = int64_t(blockIdx.x) * rows_per_cta;
   const int64_t r1 = min(r0 + rows_per_cta, a.total);
   const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
-  for (int s = threadIdx.x; s < a.num_seqs; s += kBsThreads) {
-    const int qs = __ldg(a.q_start + s), qe = __ldg(a.q_start + s + 1);
-    const int ctx = __ldg(a.context_lens + s);
-    const int n = qe - qs;
-    if (qs < 0 || n < 0 || qe > a.total || n > ctx || ctx > a.max_blocks_per_seq * kBsTokens) {
-      if (n != 0 && first_cta) atomicOr(&g_block_scaled_error, kErrBadQueryRange);
-      continue;
-    }
-    const int base = ctx - n - qs;  // position of row r: base + r
-    const int64_t hi = min(int64_t(qe), r1);
-    int64_t r = max(int64_t(qs), r0);
-    if (r > qs) r += (kBsTokens - (base + r) % kBsTokens) % kBsTokens;  // the next block's start
-    while (r < hi) {
-      const int pos = int(base + r), first = pos % kBsTokens;
-      const int block = __ldg(a.block_tables + size_t(s) * a.max_blocks_per_seq + pos / kBsTokens);
-      const int rows = min(kBsTokens - first, int(qe - r));
-      if (block < 0 || block >= a.num_blocks) {
-        atomicOr(&g_block_scaled_error, kErrBadBlockId);
-      } else {
-        const int at = atomicAdd(&items, 1);
-        if (at < kBsMaxRows) {
-          item_row[at] = int(r - r0);
-          item_first[at] = first;
-          item_count[at] = rows;
-          item_block[at] = block;
-        } else {  // only where sequences claim the same rows
-          atomicOr(&g_block_scaled_error, kErrBadQueryRange);
+  auto find = [&](int seqs) {
+    bool falls = false;
+    for (int s = threadIdx.x; s < seqs; s += kBsThreads) {
+      const int qs = __ldg(a.q_start + s), qe = __ldg(a.q_start + s + 1);
+      const int ctx = __ldg(a.context_lens + s);
+      const int n = qe - qs;
+      if (qs < 0 || qe < qs || qe > a.total || n > ctx || ctx > a.max_blocks_per_seq * kBsTokens) {
+        if (n != 0 && first_cta) atomicOr(&g_block_scaled_error, kErrBadQueryRange);
+        if (qe < qs) {
+          falls = true;
+          atomicMin(&fall, s);
         }
+        continue;
       }
-      r += rows;
+      const int base = ctx - n - qs;  // position of row r: base + r
+      const int64_t hi = min(int64_t(qe), r1);
+      int64_t r = max(int64_t(qs), r0);
+      if (r > qs) r += (kBsTokens - (base + r) % kBsTokens) % kBsTokens;  // the next block's start
+      while (r < hi) {
+        const int pos = int(base + r), first = pos % kBsTokens;
+        const int block = __ldg(a.block_tables + size_t(s) * a.max_blocks_per_seq + pos / kBsTokens);
+        const int rows = min(kBsTokens - first, int(qe - r));
+        if (block < 0 || block >= a.num_blocks) {
+          atomicOr(&g_block_scaled_error, kErrBadBlockId);
+        } else {
+          const int at = atomicAdd(&items, 1);
+          if (at < kBsMaxRows) {  // (more only where sequences claim the same rows)
+            item_row[at] = int(r - r0);
+            item_first[at] = first;
+            item_count[at] = rows;
+            item_block[at] = block;
+          }
+        }
+        r += rows;
+      }
     }
+    return falls;
+  };
+  // Where starts fall, the sequence that ends before it begins and all behind it are
+  // left out: the others lie behind one another, a block's first row each.
+  if (__syncthreads_or(find(a.num_seqs))) {
+    if (threadIdx.x == 0) items = 0;
+    __syncthreads();
+    find(fall);
+    __syncthreads();
   }
-  __syncthreads();
   const int row_bytes = a.kv_heads * D;
-  const int tasks = min(items, kBsMaxRows) * a.kv_heads * 2;
+  const int tasks = items * a.kv_heads * 2;
   for (int t = int(blockIdx.y) * (kBsThreads / 32) + (threadIdx.x >> 5); t < tasks;
        t += gridDim.y * (kBsThreads / 32)) {
     const int item = t / (2 * a.kv_heads), rest = t - item * 2 * a.kv_heads;

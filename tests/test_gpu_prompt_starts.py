@@ -92,6 +92,32 @@ def test_prefill_of_chunks_that_begin_inside_another(pk, hkv, d):
     assert (got[2000:] == 3.0).all()
 
 
+@pytest.mark.parametrize("start,taken", [
+    ([0, 20] * 20, [0]),
+    ([0, 40, 30, 35, 41, 45, 60], [0]),
+    ([5, 5, 2, 9, 8, 9, 30], []),
+    ([10 * i if i != 301 else 2980 for i in range(700)], list(range(300))),
+])
+def test_append_of_sequences_that_begin_inside_another(pk, start, taken):
+    hkv, d, S = 2, 64, len(start) - 1
+    T = max(start) + 3
+    lens = [max(0, b - a) + (7 * s) % 40 for s, (a, b) in enumerate(zip(start, start[1:]))]
+    g = torch.Generator().manual_seed(S)
+    tables, codes, scales = _cached(lens, hkv, d, g)
+    k = torch.randn(T, hkv, d, generator=g).bfloat16()
+    host = [codes[0].numpy(), codes[1].numpy(), scales[0].numpy(), scales[1].numpy()]
+    bits = wl.bf16_bits(k)
+    for s in taken:
+        a, b = start[s], start[s + 1]
+        host = oracle.append_block_scaled(bits[a:b], bits[a:b], [0, b - a], tables[s:s + 1].tolist(),
+                                          lens[s:s + 1], *host)
+    got = [x.to(DEV) for x in codes + scales]
+    pk.kv_append_fp8_block_scaled(k.to(DEV), k.to(DEV), _i32(start), tables.to(DEV), _i32(lens), *got)
+    assert pk.get_device_error(clear=True) == 0x10
+    for a, b in zip(got, host):
+        assert np.array_equal(a.cpu().numpy(), b)
+
+
 def test_a_call_again_gives_the_same_bits(pk):
     for lens, hq, hkv, d in (([700, 3, 129], 8, 2, 128), ([4000], 2, 1, 128), ([90] * 60, 4, 4, 64)):
         qkv = _inputs(lens, hq, hkv, d)
