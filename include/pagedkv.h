@@ -986,8 +986,8 @@ PKV_API int pkv_paged_decode_attention_fp8_block_scaled_bf16out(
  * pkv_paged_prefill_attention_fp8_block_scaled -- chunked prefill over a
  * block-scaled cache: queries, q_start, context_lens and mask as in
  * pkv_paged_prefill_attention (no host bound on a chunk is needed).  The pages
- * of every sequence are first widened to bf16 rows in the workspace -- exact
- * for the append's scales -- and attended by the kernel of
+ * of every sequence with new rows are first widened to bf16 rows in the workspace
+ * -- exact for the append's scales -- and attended by the kernel of
  * pkv_prompt_attention, whose limits on V hold.
  *   out : [total_q][q_heads][d_head] bf16, 32-byte aligned, not over q; rows
  *         outside every chunk are not written.

@@ -288,7 +288,7 @@ cudaError_t launch_copy_block_scales(float* k_scales, float* v_scales, const int
 // append's scales; other scales' products are rounded to one.  Bound by HBM (one
 // byte read, two written an element).  A CTA takes a page of K and V, a thread
 // four times 16 codes at once, which lie in one head each; the next page's
-// number is on its way meanwhile.
+// number is on its way meanwhile.  Pages of sequences without new rows are nobody's.
 __global__ void __launch_bounds__(kBsThreads)
 widen_block_scaled_kernel(const WidenBlockScaledArgs a, int d_head) {
   griddep_wait();
@@ -302,7 +302,9 @@ widen_block_scaled_kernel(const WidenBlockScaledArgs a, int d_head) {
     live = 0;
     if (item >= items) return;
     const int s = int(item / a.max_blocks_per_seq);
+    const int new_rows = __ldg(a.q_start + s + 1) - __ldg(a.q_start + s);
     live = __ldg(a.context_lens + s) - int(item - int64_t(s) * a.max_blocks_per_seq) * kBsTokens;
+    if (new_rows <= 0) live = 0;
     if (live > 0) id = __ldg(a.block_tables + item);
   };
   int id = 0, live;

@@ -2375,6 +2375,7 @@ int pkv_paged_prefill_attention_fp8_block_scaled(
   w.v_cache = static_cast<const uint8_t*>(v_cache);
   w.k_scales = k_scales;
   w.v_scales = v_scales;
+  w.q_start = q_start;
   w.block_tables = block_tables;
   w.context_lens = context_lens;
   w.k_out = ws;

@@ -326,7 +326,7 @@ cudaError_t launch_copy_block_scales(float* k_scales, float* v_scales, const int
 struct WidenBlockScaledArgs {
   const uint8_t *k_cache, *v_cache;
   const float *k_scales, *v_scales;
-  const int32_t *block_tables, *context_lens;
+  const int32_t *q_start, *block_tables, *context_lens;
   void *k_out, *v_out;  // bf16, num_seqs * max_blocks_per_seq * 16 rows
   int num_seqs, max_blocks_per_seq, num_blocks, kv_heads;
 };

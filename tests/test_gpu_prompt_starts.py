@@ -118,6 +118,26 @@ def test_append_of_sequences_that_begin_inside_another(pk, start, taken):
         assert np.array_equal(a.cpu().numpy(), b)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefill_does_not_look_at_pages_of_sequences_without_rows(pk, d):
+    """Their block tables may name anything, and their part of the workspace stays."""
+    g = torch.Generator().manual_seed(d)
+    counts, lens = [5, 0, 9, 0], [60, 100, 33, 500]
+    c = dict(cache=_cached(lens, 2, d, g, width=32), counts=counts, lens=lens, scale=0.02,
+             q=torch.randn(14, 4, d, generator=g).bfloat16())
+    want = _prefill(pk, c)
+    assert pk.get_device_error(clear=True) == 0
+    c["cache"][0][1, :] = 10 ** 6
+    c["cache"][0][3, :] = -7
+    ws = pk.prefill_fp8_block_scaled_workspace(4, 32, 2, d, DEV)
+    ws.fill_(0xa5)
+    got = _prefill(pk, c, workspace=ws)
+    assert pk.get_device_error(clear=True) == 0
+    assert torch.equal(got, want)
+    rows = ws.view(2, 4, -1)
+    assert (rows[:, 1] == 0xa5).all() and (rows[:, 3] == 0xa5).all()
+
+
 def test_a_call_again_gives_the_same_bits(pk):
     for lens, hq, hkv, d in (([700, 3, 129], 8, 2, 128), ([4000], 2, 1, 128), ([90] * 60, 4, 4, 64)):
         qkv = _inputs(lens, hq, hkv, d)
