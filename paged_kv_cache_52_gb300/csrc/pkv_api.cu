@@ -8,6 +8,7 @@
 #include <atomic>
 #include <climits>
 #include <cmath>
+#include <limits>
 #include <mutex>
 
 #include "../../include/pagedkv.h"
@@ -2265,9 +2266,10 @@ int run_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
   a.max_keys = kv_lens ? kv_row_stride : total_q;
   a.split = 1;
   a.causal = causal ? 1 : 0;
-  // a scale of 0 weighs every visible key alike: so does one too small to tell
-  // scores apart, which keeps a hidden key's -inf out of 0 * inf
-  a.scale_log2 = scale == 0.f ? 1e-30f : scale * 1.4426950408889634f;
+  // a scale of 0 weighs every visible key alike: so does the least subnormal, which
+  // brings any score below 2^-21, and keeps a hidden key's -inf out of 0 * inf
+  a.scale_log2 = scale == 0.f ? std::numeric_limits<float>::denorm_min()
+                              : scale * 1.4426950408889634f;
   const int sms = current_device_sms();
   if (sms <= 0) return PKV_ECUDA;
   const cudaError_t e = pkv::launch_prompt_attention(a, d_head, sms, &tq, &tk, &tv, stream);

@@ -138,6 +138,22 @@ def test_prefill_does_not_look_at_pages_of_sequences_without_rows(pk, d):
     assert (rows[:, 1] == 0xa5).all() and (rows[:, 3] == 0xa5).all()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_scale_of_0_weighs_all_alike_whatever_the_scores(pk, d):
+    lens = [200, 1, 700]
+    qkv = _inputs(lens, 2, 1, d)
+    qkv[:, :3] *= 2.0 ** 55                     # q k up to 2^120
+    got = _run(pk, qkv, lens, 2, 1, scale=0.0).double().cpu().numpy()
+    x = qkv.double().numpy()
+    start = _start(lens).tolist()
+    for s, n in enumerate(lens):
+        for i in sorted({0, n // 3, n - 1}):
+            a = start[s]
+            _check(got[a + i:a + i + 1], x[a + i:a + i + 1, :2], x[a:a + n, 2:3], x[a:a + n, 3:],
+                   0.0, i)
+    assert pk.get_device_error(clear=True) == 0
+
+
 def test_a_call_again_gives_the_same_bits(pk):
     for lens, hq, hkv, d in (([700, 3, 129], 8, 2, 128), ([4000], 2, 1, 128), ([90] * 60, 4, 4, 64)):
         qkv = _inputs(lens, hq, hkv, d)
