@@ -2478,6 +2478,7 @@ int pkv_paged_decode_attention_fp8_block_scaled_bf16out(
 int pkv_copy_block_scales(float* k_scales, float* v_scales, pkv_cache_desc cache,
                           const int32_t* pairs, int32_t num_pairs, pkv_stream_t stream) {
   if (cache.num_blocks <= 0 || cache.kv_heads <= 0 || num_pairs < 0) return PKV_EINVAL;
+  if (cache.kv_heads > (1 << 24)) return PKV_EUNSUPPORTED;  // as the calls over such a cache
   if (num_pairs == 0) return PKV_OK;
   if (!k_scales || !v_scales || !pairs) return PKV_EINVAL;
   if (!aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(pairs, 4)) return PKV_EINVAL;
