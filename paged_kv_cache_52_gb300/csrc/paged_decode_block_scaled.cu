@@ -1093,9 +1093,9 @@ cudaError_t launch_decode_block_scaled(const DecodeBlockScaledArgs& a, const CUt
   bp.max_blocks = max_blocks;
   const long long all_pairs = (long long)a.num_seqs * a.kv_heads;
   const int ctas = cluster_ctas(all_pairs, max_blocks, num_sms);
-  // the flat split's prefix sums hold 1024 sequences: more go in turn
+  // the flat split's prefix sums hold 1024 sequences, and 2^31 pages: more go in turn
   const bool alone = ctas == 0 && max_blocks <= kBsClMaxPages;
-  const int chunk = ctas || alone ? a.num_seqs : kBsFlatMaxSeqs;
+  const int chunk = ctas || alone ? a.num_seqs : std::min(kBsFlatMaxSeqs, INT_MAX / max_blocks);
   for (int s = 0; s < a.num_seqs; s += chunk) {
     const int n = std::min(chunk, a.num_seqs - s);
     const size_t row = size_t(s) * a.q_heads * a.d_head;

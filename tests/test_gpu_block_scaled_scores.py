@@ -117,6 +117,24 @@ def test_flat_decode_of_more_sequences_than_one_launch_holds(pk, hq, hkv, d):
     assert pk.get_device_error(clear=True) == 0
 
 
+def test_flat_decode_of_tables_whose_pages_pass_32_bits(pk):
+    """17 sequences that might be of 2^27 - 1 pages each, 2^31 together and more: 16 to a
+    launch, for the page counts' sums are 32-bit numbers."""
+    lens = [300, 1, 0, 16, 17, 90] * 3
+    lens = lens[:17]
+    c = _decode_case(lens, 4, 2, 64)
+    want = _decode(pk, c, max_context_len=300)
+    wide = torch.empty(17, 2 ** 27 - 1, dtype=torch.int32, device=DEV)
+    wide[:, :c["tables"].shape[1]] = c["tables"].to(DEV)
+    got = pk.paged_decode_attention_fp8_block_scaled(
+        *(c[x].to(DEV) for x in ("q", "kc", "vc", "ks", "vs")), wide,
+        torch.tensor(lens, dtype=torch.int32, device=DEV), c["scale"],
+        max_context_len=2 ** 31 - 1)
+    _check_rows(got.cpu().numpy(), c, range(17))
+    _check_rows(want.cpu().numpy(), c, range(17))
+    assert pk.get_device_error(clear=True) == 0
+
+
 @pytest.mark.parametrize("q_size", [1e-12, 2e-3, 3e4, 1e30])
 def test_flat_decode_of_queries_outside_the_range_of_f16(pk, q_size):
     c = _decode_case(MANY, 8, 2, 128, q_size=q_size, width=40)
