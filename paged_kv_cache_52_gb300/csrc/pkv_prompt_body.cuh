@@ -64,6 +64,10 @@ constexpr int kPrRegsSoftmax = 200, kPrRegsOther = 104;
 static_assert(2 * 128 * kPrRegsSoftmax + 128 * kPrRegsOther <= kPrThreads * 168, "registers");
 constexpr int kPrLoadWarp = 8, kPrMmaWarp = 9, kPrScrubWarp = 10, kPrItemWarp = 11;
 constexpr float kPrMost = 16.f;  // weights up to 2^16 against the running maximum
+// Scores (in log2 units) from which on a row's are rounded as its maximum is before the
+// weights: their multiply-add does not share that rounding, half a step of 2^3 here and of
+// 2^8 at 2^31, by which all weights of a row would overflow or vanish.
+constexpr float kPrLarge = 0x1p26f;
 constexpr int kPrRegSets = 16;   // times 32 sequences whose items one warp holds in registers
 constexpr int kPrSlots = 4;      // items known ahead
 constexpr int kPrMaxSplit = 8;   // CTAs of an item: the portable cluster size
@@ -723,7 +727,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // A row's m depends on its own scores alone.
         bool settled = false, stays = false;
         uint32_t pk[32];
-        uint64_t ls2[2], nm2;
+        uint64_t ls2[2], nm2, ts2 = sc2;
         if (j > 0) {
           nm2 = f2_pack(-m, -m);
           ls2[0] = ls2[1] = 0ull;
@@ -734,7 +738,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             ex[u & 3] = max3f(ex[u & 3], s[2 + (u >> 4)][(2 * u) & 31], s[2 + (u >> 4)][((2 * u) & 31) + 1]);
           }
           const float mx = max3f(fmaxf(ex[0], ex[1]), ex[2], ex[3]) * scale;
-          stays = m > -INFINITY && f2_sum(ls2) <= 65536.f && mx <= m + kPrMost;
+          stays = fabsf(m) < kPrLarge && f2_sum(ls2) <= 65536.f && mx <= m + kPrMost;
           settled = __all_sync(0xffffffffu, stays);
         }
         if (!settled) {
@@ -744,6 +748,13 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
             ex[(x >> 1) & 3] = max3f(ex[(x >> 1) & 3], s[x >> 5][x & 31], s[x >> 5][(x & 31) + 1]);
           const float mx = max3f(fmaxf(ex[0], ex[1]), ex[2], ex[3]) * scale;
           const float m_new = stays ? m : fmaxf(m, mx);
+          if (fabsf(m_new) >= kPrLarge) {  // scores rounded as the maximum is
+#pragma unroll
+            for (int x = 0; x < 128; x += 2)
+              f2_unpack(f2_mul(f2_pack(s[x >> 5][x & 31], s[x >> 5][(x & 31) + 1]), sc2),
+                        s[x >> 5][x & 31], s[x >> 5][(x & 31) + 1]);
+            ts2 = f2_pack(1.f, 1.f);
+          }
           if (j > 0) {
             const float alpha = m_new == m ? 1.f : ex2(m - m_new);
             const uint64_t al2 = f2_pack(alpha, alpha);
@@ -765,7 +776,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
           ls2[0] = ls2[1] = 0ull;
 #pragma unroll
           for (int u = 0; u < 32; ++u)
-            weights(s[u >> 4][(2 * u) & 31], s[u >> 4][((2 * u) & 31) + 1], sc2, nm2, ls2[u & 1], pk[u]);
+            weights(s[u >> 4][(2 * u) & 31], s[u >> 4][((2 * u) & 31) + 1], ts2, nm2, ls2[u & 1], pk[u]);
         }
         auto leave = [&](int half) {  // P of 64 keys, 32 columns
           tmem_st32u(at + 32 * half, pk);
@@ -777,7 +788,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap tmap_q,
         leave(0);
 #pragma unroll
         for (int u = 0; u < 32; ++u)
-          weights(s[2 + (u >> 4)][(2 * u) & 31], s[2 + (u >> 4)][((2 * u) & 31) + 1], sc2, nm2,
+          weights(s[2 + (u >> 4)][(2 * u) & 31], s[2 + (u >> 4)][((2 * u) & 31) + 1], ts2, nm2,
                   ls2[u & 1], pk[u]);
         leave(1);
         lsum += f2_sum(ls2);
