@@ -130,9 +130,10 @@ struct BsAcc {
       for (int mt = 0; mt < MT; ++mt) o[nh][mt][0] = o[nh][mt][1] = o[nh][mt][2] = o[nh][mt][3] = 0.f;
     }
   }
-  // an element of O times `f` (kUp by itself: its factor and f's may be small both)
-  __device__ __forceinline__ float value(int nh, int mt, int e, float f) const {
-    return o[nh][mt][e] * (1.f / kUp) * f;
+  // an element of O over `l`, in the weights' units (factor by factor: their product may
+  // be a number of few bits where the result is not)
+  __device__ __forceinline__ float value(int nh, int mt, int e, float inv_l, float unit) const {
+    return o[nh][mt][e] * ((1.f / kUp) * inv_l) * unit;
   }
   // O's unit, kUp aside, over the weights' (an empty state's O is 0)
   __device__ __forceinline__ float unit(int nh, int c) const {
@@ -193,9 +194,10 @@ __device__ __forceinline__ void bs_pages_as(BsAcc<D, G>& A, const uint32_t (&kba
     }
   }
 
-  float lv[NP];  // exponents of V's scales
+  float lv[NP];  // exponents of V's scales, no less than a normal number's
 #pragma unroll
-  for (int pg = 0; pg < NP; ++pg) lv[pg] = float(int(__float_as_uint(vs[pg]) >> 23) - 127);
+  for (int pg = 0; pg < NP; ++pg)
+    lv[pg] = float(max(int(__float_as_uint(vs[pg]) >> 23), 1) - 127);
 
   // online softmax per head column, in the log2 domain
   bool k0_in[NP], k1_in[NP];
@@ -488,7 +490,7 @@ decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
 #pragma unroll
       for (int mt = 0; mt < BsAcc<D, G>::MT; ++mt)
         *reinterpret_cast<float2*>(mo + head * D + 16 * mt + 2 * gid) =
-            make_float2(acc.value(nh, mt, c, unit), acc.value(nh, mt, c + 2, unit));
+            make_float2(acc.value(nh, mt, c, 1.f, unit), acc.value(nh, mt, c + 2, 1.f, unit));
       if (gid == 0) {
         reinterpret_cast<float2*>(mo + G * D)[head] = make_float2(acc.m[nh][c], acc.l[nh][c]);
       }
@@ -622,12 +624,12 @@ decode_block_scaled_pairs_kernel(const __grid_constant__ CUtensorMap tmap_k,
     for (int c = 0; c < 2; ++c) {
       const int head = 8 * nh + 2 * tig + c;
       if (head >= G) continue;
-      const float inv = cnt == 0 ? 0.f : acc.unit(nh, c) / acc.l[nh][c];
+      const float inv = cnt == 0 ? 0.f : 1.f / acc.l[nh][c], unit = acc.unit(nh, c);
 #pragma unroll
       for (int mt = 0; mt < BsAcc<D, G>::MT; ++mt) {
         const size_t at = (row0 + head) * D + 16 * mt + 2 * gid;
-        store_out(p, at, acc.value(nh, mt, c, inv));
-        store_out(p, at + 1, acc.value(nh, mt, c + 2, inv));
+        store_out(p, at, acc.value(nh, mt, c, inv, unit));
+        store_out(p, at + 1, acc.value(nh, mt, c + 2, inv, unit));
       }
     }
 }
@@ -799,11 +801,12 @@ decode_block_scaled_flat_kernel(const __grid_constant__ CUtensorMap tmap_k,
       for (int cc = 0; cc < 2; ++cc) {
         const int head = 8 * nh + 2 * tig + cc;
         if (head >= G) continue;
-        const float inv = acc.unit(nh, cc) / acc.l[nh][cc];
+        const float inv = 1.f / acc.l[nh][cc], unit = acc.unit(nh, cc);
 #pragma unroll
         for (int mt = 0; mt < BsAcc<D, G>::MT; ++mt) {
           const int dim = 16 * mt + 2 * gid;
-          const float v0 = acc.value(nh, mt, cc, inv), v1 = acc.value(nh, mt, cc + 2, inv);
+          const float v0 = acc.value(nh, mt, cc, inv, unit),
+                      v1 = acc.value(nh, mt, cc + 2, inv, unit);
           if (whole) {
             store_out(p, (row0 + head) * D + dim, v0);
             store_out(p, (row0 + head) * D + dim + 1, v1);

@@ -71,6 +71,28 @@ def test_equal_scores_of_any_size_give_the_mean(pk, way, d, size, power):
         assert (np.abs(got[s] - want) <= tol).all(), (s, n, got[s, :, 0], want[:, 0])
 
 
+@pytest.mark.parametrize("way", WAYS)
+@pytest.mark.parametrize("power", [-126, -130, -140])
+def test_v_scales_down_to_subnormal_numbers(pk, way, power):
+    """Equal weights, V's scales of 2^power: the mean, in float32's steps of 2^-149 and
+    twice that for a piece's rounding before it is joined."""
+    lens, width = WAYS[way]
+    c = _decode_case(lens, 8, 2, 64, width=width)
+    c["kc"] = torch.zeros_like(c["kc"])
+    c["vs"] = torch.full_like(c["vs"], 2.0 ** power)
+    assert (c["vs"] > 0).all()
+    got = _bounded(pk, c).double().cpu().numpy()
+    assert pk.get_device_error(clear=True) == 0
+    for s in range(0, len(lens), 5 if len(lens) > 9 else 1):
+        n = lens[s]
+        if n:
+            v = _values(c, s)
+            want = np.repeat(v.mean(0), 4, axis=0)
+            tol = np.repeat(np.abs(v).mean(0), 4, axis=0) * (n * 2.0 ** -23 + 2.0 ** -19)
+            assert (np.abs(got[s] - want) <= tol + 3 * 2.0 ** -149).all(), (s, n)
+            assert np.abs(got[s]).max() > 0
+
+
 @pytest.mark.parametrize("S,n,width", [(1, 3000, None), (2, 60000, None), (300, 600, 40),
                                        (300, 500, 32)])
 def test_many_small_weights_beside_a_large_one(pk, S, n, width):
