@@ -916,8 +916,9 @@ PKV_API int pkv_paged_prefill_attention_fp8_limited(const void* q, const int32_t
  *   new rows stored as e4m3(x / scale); where the scale grew, the older rows
  *           as e4m3(code * old scale / scale)  (nearest even, +-448 at most).
  * Scales are powers of two, so a new code is its element rounded once, and
- * code * scale is a bf16 value.  Infinities are left out of the maximum and
- * stored as +-448; NaN is stored as NaN.
+ * code * scale is a bf16 value -- but for elements past 1.9375 * 2^127, whose
+ * nearest code stands for 2^128, an infinity.  Infinities are left out of the
+ * maximum and stored as +-448; NaN is stored as NaN.
  *   k, v : [num_tokens][kv_heads][d_head] bf16 rows, strides in elements, as in
  *          pkv_kv_append.  Rows of no sequence (padding) are left out.
  *   q_start : [num_seqs + 1] int32, non-decreasing, q_start[num_seqs] <=
@@ -953,8 +954,9 @@ PKV_API int pkv_copy_block_scales(float* k_scales, float* v_scales, pkv_cache_de
  * of two; a weight times its block's V scale enters P V as f16, off by 2^-11 of
  * itself, or by 2^-39 of the row's largest such product where that is more (a
  * weight below 2^-112 may count as less).
- *   max_context_len : host-side bound on context_lens.  Tokens of a longer
- *               sequence are not attended and PKV_DEVERR_BAD_CONTEXT is set.
+ *   max_context_len : host-side bound on context_lens.  Of a longer sequence the
+ *               pages behind the bound's last one are not attended, and
+ *               PKV_DEVERR_BAD_CONTEXT is set where there are any.
  *   workspace : >= pkv_decode_fp8_block_scaled_workspace_bytes(...) device
  *               bytes, 256-byte aligned (PKV_ENOMEM if NULL or smaller);
  *               contents need no initialisation; calls that share it must be
@@ -994,7 +996,9 @@ PKV_API int pkv_paged_decode_attention_fp8_block_scaled_bf16out(
  *   workspace : >= pkv_prefill_fp8_block_scaled_workspace_bytes(...) device
  *         bytes, 256-byte aligned (PKV_ENOMEM if NULL or smaller); contents
  *         need no initialisation; calls that share it must be ordered on the
- *         GPU.
+ *         GPU.  It has room for every page that the tables can name, 4 bytes an
+ *         element: pass tables no wider than the longest context of the call
+ *         needs (32 tables for 131072 tokens, 8 heads of 128: 17 GB).
  * A chunk longer than its context (causal), a context beyond the block table, no
  * context, or a q_start beyond total_q rejects that sequence, one that ends
  * before it begins all from it on: none of their rows is written and

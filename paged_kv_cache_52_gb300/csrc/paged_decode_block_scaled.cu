@@ -565,7 +565,11 @@ decode_block_scaled_cluster_kernel(const __grid_constant__ CUtensorMap tmap_k,
 // The four warps of a CTA take four pairs, whole and by themselves: no join, no
 // second launch, and CTAs are handed out as others end (256 contexts of up to 200
 // tokens, 64 heads of 128 on 8: 15.3 us, 27.2 with the flat split; 254 of one token,
-// 128 / 8 of 64: 5.8, 16.9; 256 of 500, 64 / 8 of 128: 57, 62).  One long context
+// 128 / 8 of 64: 5.8, 16.9; 256 of 500, 64 / 8 of 128: 57, 62).  From where it begins,
+// at 464 pairs, to 2432, of 2 to 32 pages, full and ragged, heads of 128 in groups of 8
+// and of 1 and of 64 in groups of 2, it takes 0.27 to 1.02 of the flat split's time (464
+// pairs of 32 pages, 64 / 8 of 128: 16.8 us, 21.1), but for heads of 64 with 32 pages
+// at some counts (1216 pairs 26.6 us, 25.2; 2432 43.3, 39.4).  One long context
 // among short ones is what the flat split does better (15 of 30 tokens and one of
 // 500, 32 / 32 heads of 128: 9.5 against 13.0).
 template <int D, int G>

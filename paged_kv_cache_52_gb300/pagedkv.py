@@ -1167,7 +1167,8 @@ def paged_decode_attention_fp8_block_scaled(q: torch.Tensor, k_cache: torch.Tens
 def prefill_fp8_block_scaled_workspace(num_seqs: int, max_blocks_per_seq: int, kv_heads: int,
                                        d_head: int, device) -> torch.Tensor:
     """Workspace of ``paged_prefill_attention_fp8_block_scaled``: every page that
-    the block tables can name, as bf16 rows of K and V."""
+    the block tables can name, as bf16 rows of K and V.  Tables no wider than the
+    longest context keep it small."""
     n = lib.pkv_prefill_fp8_block_scaled_workspace_bytes(num_seqs, max_blocks_per_seq, kv_heads,
                                                          d_head)
     _need(n > 0 or num_seqs == 0, "unsupported sizes")
