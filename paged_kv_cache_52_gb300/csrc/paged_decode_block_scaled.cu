@@ -12,13 +12,12 @@
 // and is kept in units of 2^(m + dv - 14): a weight v_scale 2^(x - m - dv + 14) is below
 // 2^15 for every row (f16 ends at 2^16), and a block counts by what it gives to the row,
 // whatever scales blocks have to which the row pays no heed.  What is below 2^-39 of a
-// row's largest is lost, the rest within 2^-11 of itself or 2^-39 of the largest:
-// with weights up to 2 the tail of a long context, 10^5 keys of weights below 2^-25,
-// was lost as a whole.  dv is kept beside
-// m and not added to it: a score of 2^31 would swallow it.  For the same reason the
-// pieces of a pair meet as (m, l) and not as m + log2 l: rows of equal scores are means
-// of their values however large the scores.  Queries are f16 after an exact power of
-// two that brings a row outside [2^-6, 2^15) into it.
+// row's largest is lost, the rest within 2^-11 of itself or 2^-39 of the largest (with
+// weights up to 2 the tail of a long context, 10^5 keys of weights below 2^-25, was lost
+// as a whole).  dv is kept beside m and not added to it: a score of 2^31 would swallow
+// it.  For the same reason the pieces of a pair meet as (m, l) and not as m + log2 l: rows
+// of equal scores are means of their values however large the scores.  Queries are f16
+// after an exact power of two that brings a row outside [2^-6, 2^15) into it.
 //
 // Bound by HBM: every code is read once, 4 flops for each byte and query head.
 // A warp owns a ring of pages (K and V of one KV head, fetched by TMA) and runs
